@@ -45,6 +45,13 @@
  *   extend_attn reads the codes and converts them on chip (head_dim 128), or gathers the set's
  *   context into a bf16 pool of the E4M3 values first (head_dim 64; see
  *   pkv_extend_fp8_workspace_size).
+ *   PKV_KV_FP8_E4M3_BLOCK: the same codes with a scale of their own for each block and KV head,
+ *   code c of head h in block b standing for e4m3(c) * k_scales[b, h] (V: v_scales). Scales are
+ *   positive and finite; any such values may be read. kv_append writes such a cache (with
+ *   powers of two), paged_decode_attn, paged_decode_attn_noalloc and extend_attn read it
+ *   (head_dim 128, block_size 16); the other calls return PKV_ERR_UNSUPPORTED. kv_block_pack
+ *   and kv_block_unpack move its codes when it is described as PKV_KV_FP8_E4M3; the scales of
+ *   the moved blocks are the caller's to move.
  *
  * The batch (arrival order, the layout vLLM's model runner gives its attention backend)
  *   R requests; cu_q int32 [R+1]: request r owns query rows cu_q[r] .. cu_q[r+1]-1 of the
@@ -110,6 +117,7 @@ typedef enum {
 
 #define PKV_KV_BF16 0
 #define PKV_KV_FP8_E4M3 1
+#define PKV_KV_FP8_E4M3_BLOCK 2 /* E4M3 codes with an fp32 scale for each (block, KV head) */
 
 typedef struct {
   void* k;              /* device, kv_dtype elements, see "The paged cache of one layer" */
@@ -119,9 +127,11 @@ typedef struct {
   int32_t num_kv_heads;
   int32_t head_dim;
   int64_t stride_block; /* elements between consecutive blocks */
-  int32_t kv_dtype;     /* PKV_KV_BF16 or PKV_KV_FP8_E4M3 */
+  int32_t kv_dtype;     /* PKV_KV_BF16, PKV_KV_FP8_E4M3 or PKV_KV_FP8_E4M3_BLOCK */
   float k_scale;        /* FP8: value of a K code = e4m3(code) * k_scale (> 0, finite) */
-  float v_scale;        /* FP8: value of a V code = e4m3(code) * v_scale; both ignored for bf16 */
+  float v_scale;        /* FP8: value of a V code = e4m3(code) * v_scale; both ignored otherwise */
+  float* k_scales;      /* FP8_E4M3_BLOCK: device fp32 [num_blocks, num_kv_heads], the scale of */
+  float* v_scales;      /* each block and head; written by kv_append, else read; ignored otherwise */
 } pkv_cache;
 
 typedef struct {
@@ -155,6 +165,62 @@ const char* pkv_status_string(pkv_status s);
  * ------------------------------------------------------------------------------------- */
 pkv_status pkv_kv_cache_write(const void* key, const void* value, const int64_t* slot_mapping,
                               int64_t num_tokens, pkv_cache cache, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * kv_append — rotate the new tokens' queries and keys by their positions and append keys and
+ * values to the paged cache, in one pass over them.
+ * Source: vLLM blog "rocm-attention-backend", section "Unified attention backends" (stage 1
+ * of every forward writes the new K/V into the cache); the rotation is the rotary position
+ * embedding that such a forward applies to q and k just before it. Stands beside
+ * kv_cache_write, which copies rows that are rotated already.
+ * For each token t < num_tokens with slot s = slot_mapping[t] and position p = positions[t]:
+ *   s < 0 -> skipped (a padding row: its rows of q_out and key_out are left as they were);
+ *   s >= num_blocks * block_size -> skipped, PKV_DEVERR_SLOT set;
+ *   p outside [0, rope.max_pos) (rope.dim > 0) -> skipped, PKV_DEVERR_LEN set;
+ *   otherwise q_out[t] = R_p q[t], key_out[t] = R_p key[t] (bf16, one rounding from fp32), and
+ *   the row R_p key[t] (rounded once from fp32 to the cache's type) and value[t] go to slot s.
+ * R_p turns dims rope.offset .. rope.offset + n - 1 of every head (n = rope.dim), the others
+ * pass through. With c_i = cos_sin[p][i], s_i = cos_sin[p][n/2 + i], i < n/2, and x those n dims:
+ *   interleaved == 0: y_i = x_i c_i - x_{n/2+i} s_i,  y_{n/2+i} = x_{n/2+i} c_i + x_i s_i;
+ *   interleaved != 0: y_2i = x_2i c_i - x_{2i+1} s_i, y_{2i+1} = x_{2i+1} c_i + x_2i s_i
+ * (fp32, each product and sum rounded by itself). rope.dim == 0: no rotation (cos_sin and
+ * positions may be NULL).
+ * Cache kinds:
+ *   bf16; PKV_KV_FP8_E4M3 (the codes of kv_cache_write: E4M3(x * (1.0f / scale)));
+ *   a latent cache (bf16, num_kv_heads 1, cache.v NULL or equal to cache.k): value must be NULL,
+ *     and only key rows are written (a 576-wide row of mla_decode_attn: 512 latent dims, then
+ *     64 dims to rotate: rope.offset 512);
+ *   PKV_KV_FP8_E4M3_BLOCK (block_size 16, head_dim 128): the tokens of one block must be
+ *     consecutive rows at consecutive slots (a sequence's new tokens are), a "run" of rows
+ *     a .. b-1 of the block. For each head, K and V alike, with amax the largest finite magnitude
+ *     of the run and need = 2^ceil(log2(amax / 448)), clamped to [2^-64, 2^120] (2^-64 for an
+ *     all-zero run):
+ *       a == 0: the block starts afresh, its scale becomes need (its old codes and scale are
+ *         not read);
+ *       a > 0:  its scale becomes max(scale, need); when that grows, the codes of rows
+ *         0 .. a-1 are rewritten for it (E4M3(e4m3(code) * (old / new)): exact for
+ *         power-of-two scales but for codes that fall below E4M3's smallest steps).
+ *     The run's codes are E4M3(x * (1.0f / scale)). Rows b and up are left as they were. Two runs
+ *     of one call in the same block race (undefined codes and scale within that block).
+ * q: bf16, q_stride elements between tokens, each [num_q_heads, head_dim]; key and value alike
+ * with num_kv_heads (so slices of one fused projection can be passed). q_out, key_out:
+ * contiguous. q may be NULL (with num_q_heads 0: append only), key_out may be NULL. q_out may
+ * equal q, and key_out key, when the input is contiguous. head_dim, rope.dim and rope.offset:
+ * multiples of 16, rope.offset + rope.dim <= head_dim <= 1024 (others PKV_ERR_UNSUPPORTED);
+ * pointers 16-byte aligned, strides multiples of 8. Two tokens with the same slot race.
+ * ------------------------------------------------------------------------------------- */
+typedef struct {
+  const float* cos_sin; /* device fp32 [max_pos, dim], 16-byte aligned: dim/2 cosines, then dim/2 sines */
+  int64_t max_pos;
+  int32_t dim;          /* rotated dims of a head; 0: no rotation */
+  int32_t offset;       /* first rotated dim */
+  int32_t interleaved;  /* pairs (2i, 2i+1) instead of (i, dim/2 + i) */
+} pkv_rope;
+pkv_status pkv_kv_append(const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+                         const void* value, int64_t value_stride, const int64_t* positions,
+                         const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                         pkv_rope rope, pkv_cache cache, void* q_out, void* key_out,
+                         pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * batch_classify_reorder — sort the batch's requests into [decode : extend : prefill].

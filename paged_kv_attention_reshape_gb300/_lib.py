@@ -19,17 +19,22 @@ DEVERR = {0x1: "slot", 0x2: "block", 0x4: "reqs", 0x8: "len", 0x10: "timeout"}
 CLASS_DECODE, CLASS_EXTEND, CLASS_PREFILL = 0, 1, 2
 
 
-KV_BF16, KV_FP8_E4M3 = 0, 1
+KV_BF16, KV_FP8_E4M3, KV_FP8_E4M3_BLOCK = 0, 1, 2
 
 
 class PkvCache(ctypes.Structure):
     _fields_ = [("k", P), ("v", P), ("num_blocks", i64), ("block_size", i32),
                 ("num_kv_heads", i32), ("head_dim", i32), ("stride_block", i64),
-                ("kv_dtype", i32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+                ("kv_dtype", i32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("k_scales", P), ("v_scales", P)]
 
 
 class PkvReqs(ctypes.Structure):
     _fields_ = [("order", P), ("bounds", P), ("cls", i32), ("max_reqs", i32), ("batch_reqs", i32)]
+
+
+class PkvRope(ctypes.Structure):
+    _fields_ = [("cos_sin", P), ("max_pos", i64), ("dim", i32), ("offset", i32), ("interleaved", i32)]
 
 
 # (name, restype, argtypes) of every exported entry point; the tests check this list against
@@ -37,6 +42,7 @@ class PkvReqs(ctypes.Structure):
 SIGNATURES = [
     ("pkv_status_string", ctypes.c_char_p, [i32]),
     ("pkv_kv_cache_write", i32, [P, P, P, i64, PkvCache, P]),
+    ("pkv_kv_append", i32, [P, i64, P, i64, P, i64, P, P, i64, i32, PkvRope, PkvCache, P, P, P]),
     ("pkv_batch_classify_reorder", i32, [P, P, i32, i32, P, P, P, P, i64, P]),
     ("pkv_paged_decode_workspace_size", sz, [i32, i32, i32, i32, i32]),
     ("pkv_paged_decode_attn", i32, [P, PkvCache, P, i32, P, P, PkvReqs, i32, i32, f32, P, P, P, sz, P]),

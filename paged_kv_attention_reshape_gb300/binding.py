@@ -49,11 +49,12 @@ def _need(t: torch.Tensor, dtype, name: str, contiguous: bool = True):
         raise PkvError(f"{name} must be contiguous")
 
 
-def make_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float = 1.0,
-               v_scale: float = 1.0) -> "_lib.PkvCache":
+def make_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale=1.0, v_scale=1.0) -> "_lib.PkvCache":
     """Describe one layer's paged cache: k_cache / v_cache [num_blocks, block_size, Hkv, D]
     with contiguous blocks (any stride between blocks). bf16 tensors are a bf16 cache; uint8
-    or float8_e4m3fn tensors are an FP8 (E4M3) cache whose codes stand for e4m3(code) * scale."""
+    or float8_e4m3fn tensors are an FP8 (E4M3) cache whose codes stand for e4m3(code) * scale.
+    k_scale and v_scale are numbers (one scale for the tensor) or fp32 tensors [num_blocks, Hkv]
+    (a scale for each block and KV head)."""
     fp8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
     want = k_cache.dtype if fp8 else torch.bfloat16
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
@@ -64,6 +65,19 @@ def make_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float = 1.
     if k_cache.shape != v_cache.shape or k_cache.stride(0) != v_cache.stride(0):
         raise PkvError("k_cache and v_cache must have the same shape and block stride")
     nb, bs, hkv, d = k_cache.shape
+    if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
+        if not fp8:
+            raise PkvError("block scales belong to an FP8 cache")
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not isinstance(t, torch.Tensor):
+                raise PkvError("k_scale and v_scale must both be numbers or both be tensors")
+            _need(t, torch.float32, n)
+            if tuple(t.shape) != (nb, hkv):
+                raise PkvError(f"{n} must be [num_blocks, Hkv] = [{nb}, {hkv}], got {list(t.shape)}")
+            if t.device != k_cache.device:
+                raise PkvError(f"{n} must be on the cache's device")
+        return _lib.PkvCache(k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, hkv, d, k_cache.stride(0),
+                             _lib.KV_FP8_E4M3_BLOCK, 1.0, 1.0, k_scale.data_ptr(), v_scale.data_ptr())
     return _lib.PkvCache(k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, hkv, d, k_cache.stride(0),
                          _lib.KV_FP8_E4M3 if fp8 else _lib.KV_BF16, float(k_scale), float(v_scale))
 
@@ -94,6 +108,81 @@ def kv_cache_write(key, value, slot_mapping, k_cache, v_cache, stream=None, k_sc
     cache = make_cache(k_cache, v_cache, k_scale, v_scale)
     _check(lib.pkv_kv_cache_write(_ptr(key), _ptr(value), _ptr(slot_mapping), slot_mapping.numel(),
                                   cache, _stream(stream)), "kv_cache_write")
+
+
+def _token_rows(t: torch.Tensor, name: str, heads: int, dim: int, device) -> int:
+    """Checks bf16 rows [T, heads, dim] whose tokens may lie apart (a slice of a fused projection);
+    returns the elements between tokens."""
+    _need(t, torch.bfloat16, name, contiguous=False)
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+        raise PkvError(f"{name} must be [T, {heads}, {dim}], got {list(t.shape)}")
+    if t.device != device:
+        raise PkvError(f"{name} must be on the cache's device")
+    if t.shape[0] <= 1:
+        inner_ok = t.is_contiguous()
+    else:
+        inner_ok = (dim == 1 or t.stride(2) == 1) and (heads == 1 or t.stride(1) == dim)
+    if not inner_ok:
+        raise PkvError(f"{name}: each token's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def kv_append(q, key, value, positions, slot_mapping, k_cache, v_cache, cos_sin=None, *, rope_offset=0,
+              interleaved=False, q_out=None, k_out=None, k_scale=1.0, v_scale=1.0, stream=None):
+    """Rotate q and key by their positions and append key and value to the cache slots.
+
+    q [T, Hq, D] (or None), key and value [T, Hkv, D] bf16, tokens any stride apart; positions and
+    slot_mapping int64 [T] (slot < 0: a padding row, skipped); cos_sin fp32 [max_pos, n]: n/2 cosines
+    then n/2 sines for dims rope_offset .. rope_offset + n - 1 of every head (None: no rotation). A
+    bf16 or FP8 cache; with k_scale / v_scale tensors [num_blocks, Hkv] the scales of the blocks
+    written are updated too. A latent cache: value and v_cache None. Returns (q_out, k_out): the
+    rotated rows, [T, H, D] contiguous, allocated here when not given (rows of skipped tokens are
+    left as they were)."""
+    lib = _lib.load()
+    if (value is None) != (v_cache is None):
+        raise PkvError("a latent cache has neither value nor v_cache; any other has both")
+    cache = make_cache(k_cache, k_cache if v_cache is None else v_cache, k_scale, v_scale)
+    dev, hkv, d = k_cache.device, k_cache.shape[2], k_cache.shape[3]
+    if dev.index != torch.cuda.current_device():
+        raise PkvError("the cache must be on the current device")
+    k_stride = _token_rows(key, "key", hkv, d, dev)
+    T = key.shape[0]
+    v_stride = hkv * d
+    if value is not None:
+        v_stride = _token_rows(value, "value", hkv, d, dev)
+    hq, q_stride = 0, 0
+    if q is not None:
+        hq = q.shape[1]
+        q_stride = _token_rows(q, "q", hq, d, dev)
+    for t, n in ((value, "value"), (q, "q")):
+        if t is not None and t.shape[0] != T:
+            raise PkvError(f"{n} must have key's {T} tokens, got {t.shape[0]}")
+    rope = _lib.PkvRope(None, 0, 0, 0, 0)
+    need = [(slot_mapping, torch.int64, "slot_mapping")]
+    if cos_sin is not None:
+        _need(cos_sin, torch.float32, "cos_sin")
+        if cos_sin.dim() != 2 or cos_sin.device != dev:
+            raise PkvError("cos_sin must be [max_pos, n] on the cache's device")
+        rope = _lib.PkvRope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(rope_offset),
+                            1 if interleaved else 0)
+        need.append((positions, torch.int64, "positions"))
+    for t, dtype, n in need:
+        _need(t, dtype, n)
+        if t.numel() != T or t.device != dev:
+            raise PkvError(f"{n} must have {T} entries on the cache's device")
+    if q is not None and q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
+    if k_out is None:
+        k_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=dev)
+    for t, h, n in ((q_out, hq, "q_out"), (k_out, hkv, "k_out")):
+        if t is not None:
+            _need(t, torch.bfloat16, n)
+            if tuple(t.shape) != (T, h, d) or t.device != dev:
+                raise PkvError(f"{n} must be [{T}, {h}, {d}] on the cache's device")
+    _check(lib.pkv_kv_append(_ptr(q), q_stride, _ptr(key), k_stride, _ptr(value), v_stride,
+                             _ptr(positions) if cos_sin is not None else None, _ptr(slot_mapping), T, hq, rope, cache,
+                             _ptr(q_out) if q is not None else None, _ptr(k_out), _stream(stream)), "kv_append")
+    return q_out, k_out
 
 
 def kv_block_pack(k_cache, v_cache, block_ids, dst=None, stream=None):
@@ -209,7 +298,8 @@ def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, 
                       reqs: Optional[Reqs] = None, scale=None, out=None, lse=None, workspace=None,
                       stream=None, k_scale=1.0, v_scale=1.0):
     """One query token per request against its paged context. q [T, Hq, D]. An FP8 cache is
-    dequantised with the per-tensor scales as it is read."""
+    dequantised as it is read, with the per-tensor scales or with the scale of each block and KV
+    head (k_scale, v_scale: fp32 tensors [num_blocks, Hkv])."""
     lib = _lib.load()
     _need(q, torch.bfloat16, "q")
     _need(block_tables, torch.int32, "block_tables")
@@ -290,7 +380,8 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
     """New tokens attend to their cached context (paged) and causally to themselves. An FP8
     cache (uint8 / float8 codes with per-tensor scales) is read as codes and converted in the
     kernel at head_dim 128; at head_dim 64 it is gathered into a bf16 workspace of the set's
-    context first (allocated here when not given)."""
+    context first (allocated here when not given). k_scale / v_scale may be fp32 tensors
+    [num_blocks, Hkv], a scale for each block and KV head (head_dim 128)."""
     lib = _lib.load()
     for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
         _need(t, torch.bfloat16, n)

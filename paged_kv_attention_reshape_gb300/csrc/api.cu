@@ -77,7 +77,7 @@ int32_t next_sched_slot() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int64_t elem_bytes(const pkv_cache& c) { return c.kv_dtype == PKV_KV_FP8_E4M3 ? 1 : 2; }
+int64_t elem_bytes(const pkv_cache& c) { return c.kv_dtype == PKV_KV_BF16 ? 2 : 1; }
 
 // TMA map over a token-major tensor [rows, heads, D] (bf16): dims (64, heads*D/64, rows),
 // box 64 x 1 x box_rows, 128-byte swizzle. One box = one 64-wide half of one head's rows.
@@ -99,7 +99,7 @@ bool encode_cache(CUtensorMap* m, const void* base, const pkv_cache& c) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   const int D = c.head_dim;
-  if (c.kv_dtype == PKV_KV_FP8_E4M3) {
+  if (c.kv_dtype != PKV_KV_BF16) {
     // one byte per element: dims (D, Hkv, block_size, num_blocks), box D x 1 x block_size x 1
     // (one head of one block; 128 bytes per row at D = 128), 128-byte swizzle
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(c.num_kv_heads),
@@ -130,11 +130,19 @@ bool group_ok(int Hq, int Hkv) {
 }
 
 // Common checks of a cache descriptor. attention: the stricter shape set of the attention calls.
-pkv_status check_cache(const pkv_cache& c, bool attention) {
+// scaled: the call knows a block-scaled cache (one head_dim and block size).
+pkv_status check_cache(const pkv_cache& c, bool attention, bool scaled = false) {
   if (c.k == nullptr || c.v == nullptr || c.num_blocks <= 0 || c.block_size <= 0 ||
       c.num_kv_heads <= 0 || c.head_dim <= 0)
     return PKV_ERR_INVALID_ARG;
-  if (c.kv_dtype != PKV_KV_BF16 && c.kv_dtype != PKV_KV_FP8_E4M3) return PKV_ERR_INVALID_ARG;
+  if (c.kv_dtype != PKV_KV_BF16 && c.kv_dtype != PKV_KV_FP8_E4M3 && c.kv_dtype != PKV_KV_FP8_E4M3_BLOCK)
+    return PKV_ERR_INVALID_ARG;
+  if (c.kv_dtype == PKV_KV_FP8_E4M3_BLOCK) {
+    if (!scaled || c.head_dim != 128 || c.block_size != 16) return PKV_ERR_UNSUPPORTED;
+    if (c.k_scales == nullptr || c.v_scales == nullptr || (reinterpret_cast<uintptr_t>(c.k_scales) & 3u) ||
+        (reinterpret_cast<uintptr_t>(c.v_scales) & 3u))
+      return PKV_ERR_INVALID_ARG;
+  }
   if (c.kv_dtype == PKV_KV_FP8_E4M3 &&
       !(std::isfinite(c.k_scale) && c.k_scale > 0.f && std::isfinite(c.v_scale) && c.v_scale > 0.f))
     return PKV_ERR_INVALID_ARG;
@@ -146,7 +154,7 @@ pkv_status check_cache(const pkv_cache& c, bool attention) {
   if (attention) {
     if (c.head_dim != 64 && c.head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (c.block_size != 16) return PKV_ERR_UNSUPPORTED;
-    if (c.kv_dtype == PKV_KV_FP8_E4M3 && c.head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (c.kv_dtype != PKV_KV_BF16 && c.head_dim != 128) return PKV_ERR_UNSUPPORTED;
   }
   return PKV_OK;
 }
@@ -279,6 +287,76 @@ pkv_status pkv_kv_cache_write(const void* key, const void* value, const int64_t*
   if (num_tokens > (int64_t(1) << 40)) return PKV_ERR_INVALID_ARG;
   st = cuda_status(launch_kv_cache_write(key, value, slot_mapping, num_tokens, cache, error_word(),
                                          reinterpret_cast<cudaStream_t>(stream)));
+  t_launches += 1;
+  return st;
+}
+
+pkv_status pkv_kv_append(const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+                         const void* value, int64_t value_stride, const int64_t* positions,
+                         const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                         pkv_rope rope, pkv_cache cache, void* q_out, void* key_out,
+                         pkv_stream_t stream) {
+  if (num_tokens < 0 || num_q_heads < 0) return PKV_ERR_INVALID_ARG;
+  const bool latent = cache.kv_dtype == PKV_KV_BF16 && cache.num_kv_heads == 1 &&
+                      (cache.v == nullptr || cache.v == cache.k);
+  if (cache.v == nullptr && latent) cache.v = cache.k;
+  pkv_status st = check_cache(cache, false, true);
+  if (st != PKV_OK) return st;
+  const int D = cache.head_dim;
+  if (rope.dim < 0 || rope.offset < 0) return PKV_ERR_INVALID_ARG;
+  if (D % 16 != 0 || D > 1024 || rope.dim % 16 != 0 || rope.offset % 16 != 0 ||
+      static_cast<int64_t>(rope.offset) + rope.dim > D)
+    return PKV_ERR_UNSUPPORTED;
+  // an item's flat row index and its offset in a row stay within 32 bits
+  const int64_t rows = num_q_heads + 2 * static_cast<int64_t>(cache.num_kv_heads);
+  if (rows * D > INT32_MAX || num_tokens > (int64_t(1) << 30)) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PKV_OK;
+  if (key == nullptr || slot_mapping == nullptr || (value == nullptr) != latent) return PKV_ERR_INVALID_ARG;
+  if ((q == nullptr) != (num_q_heads == 0) || (q != nullptr && q_out == nullptr)) return PKV_ERR_INVALID_ARG;
+  if (rope.dim > 0 && (rope.cos_sin == nullptr || rope.max_pos <= 0 || positions == nullptr || !aligned16(rope.cos_sin)))
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(key) || !aligned16(value) || !aligned16(q) || !aligned16(q_out) || !aligned16(key_out))
+    return PKV_ERR_INVALID_ARG;
+  const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * D, q_row = static_cast<int64_t>(num_q_heads) * D;
+  if (key_stride < kv_row || key_stride % 8 != 0 || (value != nullptr && (value_stride < kv_row || value_stride % 8 != 0)) ||
+      (q != nullptr && (q_stride < q_row || q_stride % 8 != 0)))
+    return PKV_ERR_INVALID_ARG;
+  // in place only when the input is contiguous, as the outputs are
+  if ((q != nullptr && q_out == q && q_stride != q_row) || (key_out == key && key_stride != kv_row))
+    return PKV_ERR_INVALID_ARG;
+  AppendParams p{};
+  p.err = error_word();
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(key);
+  p.v = static_cast<const __nv_bfloat16*>(value);
+  p.q_stride = q_stride;
+  p.k_stride = key_stride;
+  p.v_stride = value_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_out = static_cast<__nv_bfloat16*>(key_out);
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.num_tokens = num_tokens;
+  p.Hq = num_q_heads;
+  p.Hkv = cache.num_kv_heads;
+  p.D = D;
+  p.cos_sin = rope.cos_sin;
+  p.max_pos = rope.max_pos;
+  p.rot = rope.dim;
+  p.rot_off = rope.offset;
+  p.interleaved = rope.interleaved;
+  p.k_cache = cache.k;
+  p.v_cache = cache.v;
+  p.num_slots = cache.num_blocks * cache.block_size;
+  p.block_size = cache.block_size;
+  p.stride_block = cache.stride_block;
+  if (cache.kv_dtype == PKV_KV_FP8_E4M3) {
+    p.k_inv = 1.0f / cache.k_scale;
+    p.v_inv = 1.0f / cache.v_scale;
+  }
+  p.k_scales = cache.k_scales;
+  p.v_scales = cache.v_scales;
+  st = cuda_status(launch_kv_append(p, cache.kv_dtype, reinterpret_cast<cudaStream_t>(stream)));
   t_launches += 1;
   return st;
 }
@@ -444,12 +522,14 @@ size_t pkv_paged_decode_workspace_size(int32_t max_reqs, int32_t num_q_heads, in
   return decode_workspace_bytes(num_q_heads, num_kv_heads, head_dim);
 }
 
+static pkv_status run_decode_scaled(const DecodeParams& d, const pkv_cache& cache, pkv_stream_t stream);
+
 pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* block_tables,
                                  int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_q,
                                  pkv_reqs reqs, int32_t num_q_heads, int32_t max_seq_len,
                                  float scale, void* out, float* lse, void* workspace,
                                  size_t workspace_bytes, pkv_stream_t stream) {
-  pkv_status st = check_cache(cache, true);
+  pkv_status st = check_cache(cache, true, true);
   if (st != PKV_OK) return st;
   if ((st = check_reqs(reqs)) != PKV_OK) return st;
   if (!group_ok(num_q_heads, cache.num_kv_heads)) return PKV_ERR_UNSUPPORTED;
@@ -485,6 +565,7 @@ pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* 
   // into the output
   p.scale_log2 = scale * (fp8 ? cache.k_scale : 1.f) * 1.4426950408889634f;
   p.v_scale = fp8 ? cache.v_scale : 1.f;
+  if (cache.kv_dtype == PKV_KV_FP8_E4M3_BLOCK) return run_decode_scaled(p, cache, stream);
   const size_t need = decode_workspace_bytes(p.Hq, p.Hkv, cache.head_dim);
   if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_WORKSPACE;
   p.ws_part = static_cast<float*>(workspace);
@@ -501,6 +582,38 @@ pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* 
     st = cuda_status(launch_paged_decode(p, tk, tv, cache.head_dim, fp8,
                                          reinterpret_cast<cudaStream_t>(stream), &launches));
   }
+  t_launches += launches;
+  return st;
+}
+
+static pkv_status run_decode_scaled(const DecodeParams& d, const pkv_cache& cache, pkv_stream_t stream) {
+  ScaledDecodeParams p{};
+  p.err = d.err;
+  p.q = d.q;
+  p.out = d.out;
+  p.lse = d.lse;
+  p.block_tables = d.block_tables;
+  p.max_blocks = d.max_blocks;
+  p.seq_lens = d.seq_lens;
+  p.cu_q = d.cu_q;
+  p.order = d.order;
+  p.bounds = d.bounds;
+  p.cls = d.cls;
+  p.max_reqs = d.max_reqs;
+  p.batch_reqs = d.batch_reqs;
+  p.Hq = d.Hq;
+  p.Hkv = d.Hkv;
+  p.G = d.G;
+  p.k = static_cast<const uint8_t*>(cache.k);
+  p.v = static_cast<const uint8_t*>(cache.v);
+  p.k_scales = cache.k_scales;
+  p.v_scales = cache.v_scales;
+  p.num_blocks = cache.num_blocks;
+  p.stride_block = cache.stride_block;
+  p.max_seq_len = d.max_seq_len;
+  p.scale_log2 = d.scale_log2;
+  int launches = 0;
+  const pkv_status st = cuda_status(launch_decode_scaled(p, reinterpret_cast<cudaStream_t>(stream), &launches));
   t_launches += launches;
   return st;
 }
@@ -592,8 +705,10 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
                                 float ctx_k_scale = 1.f, float ctx_v_scale = 1.f) {
   pkv_status st = check_reqs(reqs);
   if (st != PKV_OK) return st;
-  if (cache != nullptr && (st = check_cache(*cache, true)) != PKV_OK) return st;
-  if (cache != nullptr && cache->kv_dtype != (ctx_kind == kAttnCtxFp8 ? PKV_KV_FP8_E4M3 : PKV_KV_BF16))
+  if (cache != nullptr && (st = check_cache(*cache, true, true)) != PKV_OK) return st;
+  if (cache != nullptr && cache->kv_dtype != (ctx_kind == kAttnCtxFp8     ? PKV_KV_FP8_E4M3
+                                              : ctx_kind == kAttnCtxBlock ? PKV_KV_FP8_E4M3_BLOCK
+                                                                          : PKV_KV_BF16))
     return PKV_ERR_UNSUPPORTED;
   if (D != 64 && D != 128) return PKV_ERR_UNSUPPORTED;
   if (!group_ok(Hq, Hkv)) return PKV_ERR_UNSUPPORTED;
@@ -630,6 +745,8 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   p.scale_log2 = scale * 1.4426950408889634f;
   p.ctx_scale_log2 = scale * ctx_k_scale * 1.4426950408889634f;
   p.ctx_v_scale = ctx_v_scale;
+  p.k_scales = cache ? cache->k_scales : nullptr;
+  p.v_scales = cache ? cache->v_scales : nullptr;
   CUtensorMap tq, tk, tv, tck, tcv, tqf;
   std::memset(&tck, 0, sizeof tck);
   std::memset(&tcv, 0, sizeof tcv);
@@ -687,6 +804,10 @@ pkv_status pkv_extend_attn(const void* q, const void* k_new, const void* v_new, 
                            int32_t chunk_budget_tokens, float scale, void* out, float* lse,
                            void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
   if (chunk_budget_tokens < 0) return PKV_ERR_INVALID_ARG;
+  if (cache.kv_dtype == PKV_KV_FP8_E4M3_BLOCK)
+    return run_attention(q, k_new, v_new, num_tokens, cu_q, seq_lens, &cache, block_tables, max_blocks, reqs,
+                         num_q_heads, cache.num_kv_heads, cache.head_dim, max_q_len, max_seq_len, scale, out, lse,
+                         stream, kAttnCtxBlock);
   if (cache.kv_dtype != PKV_KV_FP8_E4M3)
     return run_attention(q, k_new, v_new, num_tokens, cu_q, seq_lens, &cache, block_tables,
                          max_blocks, reqs, num_q_heads, cache.num_kv_heads, cache.head_dim,

@@ -21,7 +21,8 @@
 //   warp 8     TMA producer: takes the CTA's next work item and publishes it to the other
 //              roles, then loads its Q tiles and K and V tiles into a ring of NBUF tile buffers
 //   warp 9     MMA issuer (one thread): S_i = Q_i K^T (SS), O_i += P_i V (P read from TMEM)
-//   warps 10-11 (FP8 context only) convert E4M3 code tiles, Q and new-token tiles to fp16
+//   warps 10-11 (FP8 context only) convert E4M3 code tiles, Q and new-token tiles to fp16, or
+//              (block scales) E4M3 code tiles to the bf16 values they stand for
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; P_i (bf16 pairs) overwrites the first
 // half of S_i, which the next S_i = Q_i K^T only writes after the P_i V product that reads it
 // (tcgen05 MMAs issued by one thread run in order).
@@ -43,14 +44,18 @@ namespace pkv {
 // Kinds of cached context the kernel reads (the bf16 kernel is kind 0):
 //   kCtxBf16    a bf16 cache;
 //   kCtxPool    a bf16 pool holding the E4M3 values of an FP8 cache (gathered beforehand);
-//   kCtxFp8     the FP8 cache's E4M3 codes themselves, converted in shared memory as they land.
-constexpr int kCtxBf16 = kAttnCtxBf16, kCtxPool = kAttnCtxPool, kCtxFp8 = kAttnCtxFp8;
+//   kCtxFp8     the FP8 cache's E4M3 codes themselves, converted in shared memory as they land;
+//   kCtxBlock   the same for a cache with a scale for each block and head.
+constexpr int kCtxBf16 = kAttnCtxBf16, kCtxPool = kAttnCtxPool, kCtxFp8 = kAttnCtxFp8, kCtxBlock = kAttnCtxBlock;
 
 template <int D, int KIND = kCtxBf16>
 struct TcCfg {
   static constexpr int BM = 128, BN = 128, BS = 16;
-  static constexpr bool CONV = KIND == kCtxFp8;  // converter warps 10 and 11
-  static constexpr bool F16 = CONV;              // the products run on fp16 operands
+  static constexpr bool CONV = KIND == kCtxFp8 || KIND == kCtxBlock;  // converter warps 10 and 11
+  static constexpr bool F16 = KIND == kCtxFp8;   // the products run on fp16 operands
+  // kCtxBlock: the scales of a context tile's blocks travel with the tile, one 4-byte cp.async a
+  // block, each an arrival of its own on the tile's barrier
+  static constexpr int SCALE_ARRIVALS = KIND == kCtxBlock ? BN / BS : 0;
   static constexpr int HALVES = D / 64;
   static constexpr int HALF_BYTES = 128 * 128;           // 128 rows x 128 bytes
   static constexpr int TILE_BYTES = HALVES * HALF_BYTES;  // one 128-row tile of Q, K or V
@@ -74,7 +79,14 @@ struct TcCfg {
   static constexpr int STAGE_WARP_BYTES = 32 * 64;
   static constexpr int ITEM_RING = 4;  // claimed work items published to the consumer roles
   static constexpr int ITEM_OFF = STAGE_OFF + 8 * STAGE_WARP_BYTES;
-  static constexpr int BAR_OFF = ITEM_OFF + ITEM_RING * 8;
+  // kCtxBlock: the block scales of V by ring buffer (read by the converters before the buffer is
+  // handed on), then those of K by key tile, tile k of the CTA in slot k % KSCALE_RING (read by the
+  // softmax warps, which may still be at tile k when the producer is at k + 2, never when it is at
+  // k + 4: K of tile k + 4 is loaded once S of tile k + 2 is done, which needs P of tile k + 1)
+  static constexpr int KSCALE_RING = 4;
+  static constexpr int SCALE_OFF = (ITEM_OFF + ITEM_RING * 8 + 15) / 16 * 16;
+  static constexpr int KSCALE_OFF = SCALE_OFF + NBUF * SCALE_ARRIVALS * 4;
+  static constexpr int BAR_OFF = KSCALE_OFF + KSCALE_RING * SCALE_ARRIVALS * 4;
   // barriers: q_full, q_empty, kv_full[NBUF], kv_empty[NBUF], s_full[2], p_full[2], o_final[2],
   // item_full[ITEM_RING], item_empty[ITEM_RING], q_conv, conv_full[NBUF]
   static constexpr int NBAR = 2 + 2 * NBUF + 6 + 2 * ITEM_RING + 1 + NBUF;
@@ -268,6 +280,47 @@ __device__ __forceinline__ void conv_code_row(uint32_t tile, int R, bool keep) {
   }
 }
 
+// Code row R -> bf16: the E4M3 values (exactly), or (SCALE) the values times sc, rounded once (not at
+// all when sc is a power of two). Zeros when !keep.
+template <bool SCALE>
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t c, float sc) {
+  const uint32_t h = e4m3x2_to_f16x2(c);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return SCALE ? pack_bf16(f.x * sc, f.y * sc) : pack_bf16(f.x, f.y);
+}
+template <bool SCALE>
+__device__ __forceinline__ void conv_code_row_bf16(uint32_t tile, int R, float sc, bool keep) {
+  uint4 c[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) c[q] = ld_shared_v4(tile + 16384u + R * 128 + ((q ^ (R & 7)) << 4));
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
+    if (keep) {
+      a = make_uint4(e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].x), sc),
+                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].x >> 16), sc),
+                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].y), sc),
+                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].y >> 16), sc));
+      b = make_uint4(e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].z), sc),
+                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].z >> 16), sc),
+                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].w), sc),
+                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].w >> 16), sc));
+    }
+    const uint32_t base = tile + (q >> 2) * 16384u + R * 128;
+    const int ch = 2 * (q & 3);
+    st_shared_v4(base + ((ch ^ (R & 7)) << 4), a);
+    st_shared_v4(base + (((ch + 1) ^ (R & 7)) << 4), b);
+  }
+}
+// Row R of a [halves][128][128 B] tile set to zeros.
+template <int HALVES>
+__device__ __forceinline__ void zero_row(uint32_t tile, int R) {
+#pragma unroll
+  for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) st_shared_v4(tile + h * 16384u + R * 128 + (q << 4), make_uint4(0, 0, 0, 0));
+}
+
 // bf16 x 2 -> fp16 x 2, times sc
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2_scaled(uint32_t x, float sc) {
   return pack_f16(__uint_as_float(x << 16) * sc, __uint_as_float(x & 0xFFFF0000u) * sc);
@@ -291,7 +344,7 @@ __device__ __forceinline__ void conv_bf16_row(uint32_t tile, int R, float sc, bo
     }
 }
 
-// KIND != kCtxBf16 (SCALED): the cached context holds the E4M3 values of an FP8 cache. The key
+// kCtxPool and kCtxFp8 (SCALED): the cached context holds the E4M3 values of an FP8 cache. The key
 // scale goes with the softmax scale of context tiles. The value scale vs is taken out of the
 // sum instead of multiplied into every context tile's P, so that
 // O = vs * (sum_ctx p code + sum_new p v / vs) / l: for kCtxPool the few new-token tiles pack
@@ -305,6 +358,14 @@ __device__ __forceinline__ void conv_bf16_row(uint32_t tile, int R, float sc, bo
 // core multiplies fp16 operands (kind::f16), P is packed as fp16, and the MMA warp waits on
 // the converters' barriers (q_conv, conv_full) instead of the loads'. Queries, new keys and
 // new values divided by vs must lie within the fp16 range.
+//
+// kCtxBlock: the same pipeline with a scale for each 16-token block and head, and bf16 operands
+// (whose range is fp32's, so that no scale is out of range; the queries and new tokens stay as they
+// come). The converter warps write K as the E4M3 values themselves, exactly, and the softmax
+// multiplies each block's 16 columns of S by its scale in fp32: rounding code * scale to bf16
+// instead would put an error of up to 2^-8 of each product into the exponent. V is written as
+// code * scale, rounded once to bf16 (2^-8 of the value at most, like P's own rounding; not at all
+// for the powers of two that kv_append makes).
 template <int D, int KIND>
 __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kernel(
     const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
@@ -312,7 +373,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
     const __grid_constant__ CUtensorMap tm_ck, const __grid_constant__ CUtensorMap tm_cv,
     const __grid_constant__ CUtensorMap tm_qf) {
   using C = TcCfg<D, KIND>;
-  constexpr bool SCALED = KIND != kCtxBf16;
+  constexpr bool SCALED = KIND == kCtxPool || KIND == kCtxFp8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                  // [slot][half][128][128 B]
@@ -353,7 +414,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int b = 0; b < C::NBUF; ++b) {
-      mbar_init(&kv_full[b], 1);
+      mbar_init(&kv_full[b], 1 + C::SCALE_ARRIVALS);
       mbar_init(&kv_empty[b], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -473,6 +534,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
     const int t = tid & 127;  // row of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t sc = 0, oc = 0;
+    uint32_t tile0 = 0;  // kCtxBlock: the CTA's key tiles before this item
     const float lvs = SCALED ? log2f(p.ctx_v_scale) : 0.f;  // new-token tiles' extra shift
     int64_t w_static = blockIdx.x;
     int odd = 0;
@@ -486,7 +548,10 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       }
       if (w < 0) break;
       const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
-      if (slot >= it.nslot) continue;
+      if (slot >= it.nslot) {
+        if constexpr (KIND == kCtxBlock) tile0 += it.NT;
+        continue;
+      }
       // query index of this row within its request (a packed decode's rows are heads of its one
       // token)
       const int qi = it.dec ? 0 : it.qr0 + t;
@@ -509,6 +574,18 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         const bool vsc = KIND == kCtxPool && !ctx && p.ctx_v_scale != 1.f;
         float alpha = 1.f, rs = 0.f;
         if constexpr (C::ONE_READ) {
+        // scale of each block's 16 columns: with block scales the key scale goes with the softmax scale
+        float slg[KIND == kCtxBlock ? 8 : 1];
+        if constexpr (KIND == kCtxBlock) {
+          const float4* ks = reinterpret_cast<const float4*>(smem + C::KSCALE_OFF) + (tile0 + j) % C::KSCALE_RING * 2;
+          const float4 k0 = ctx ? ks[0] : make_float4(1.f, 1.f, 1.f, 1.f), k1 = ctx ? ks[1] : make_float4(1.f, 1.f, 1.f, 1.f);
+          slg[0] = k0.x * sl, slg[1] = k0.y * sl, slg[2] = k0.z * sl, slg[3] = k0.w * sl;
+          slg[4] = k1.x * sl, slg[5] = k1.y * sl, slg[6] = k1.z * sl, slg[7] = k1.w * sl;
+        } else {
+          slg[0] = sl;
+        }
+        // the factor of column c * 32 + e
+        auto slc = [&](int c, int e) { return KIND == kCtxBlock ? slg[2 * c + (e >> 4)] : slg[0]; };
         // the whole row of S into registers (four loads, one wait)
         uint32_t v[4][32];
 #pragma unroll
@@ -516,9 +593,23 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         tc::wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
-        // row max of the raw scores (the scale is positive, so it commutes with max)
+        // row max of the raw scores (the scale is positive, so it commutes with max; with block
+        // scales it does so within a block's columns)
         float mx = -CUDART_INF_F;
-        if (full) {
+        if constexpr (KIND == kCtxBlock) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            float mg = -CUDART_INF_F;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int c = g / 2, b = (g & 1) * 16 + e;
+              const float a0 = full || g * 16 + e < kv ? __uint_as_float(v[c][b]) : -CUDART_INF_F;
+              const float a1 = full || g * 16 + e + 1 < kv ? __uint_as_float(v[c][b + 1]) : -CUDART_INF_F;
+              mg = sm::max3(mg, a0, a1);
+            }
+            mx = fmaxf(mx, mg * slg[g]);
+          }
+        } else if (full) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -530,7 +621,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             for (int e = 0; e < 32; ++e)
               if (c * 32 + e < kv) mx = fmaxf(mx, __uint_as_float(v[c][e]));
         }
-        mx = mx * sl;  // -inf stays -inf
+        if constexpr (KIND != kCtxBlock) mx = mx * sl;  // -inf stays -inf
         if (mx > m + 8.f || m == -CUDART_INF_F) {  // lazy rescale: only when the max really grows
           const float m_new = fmaxf(m, mx);
           if (m_new != -CUDART_INF_F) {
@@ -543,14 +634,15 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         if (full) {
           // every column valid: pairs of columns in packed fp32 (one instruction per pair for
           // the scale-and-shift and the running sum)
-          const uint64_t sc2 = sm::f2(sl, sl), nm2 = sm::f2(neg_m, neg_m);
+          const uint64_t nm2 = sm::f2(neg_m, neg_m);
           uint64_t rs2 = sm::f2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
+              const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
+                                          sm::f2(slc(c, e), slc(c, e)), nm2);
               float x0, x1;
               sm::unf2(x, x0, x1);
               const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
@@ -568,8 +660,8 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              float p0 = ex2_approx(fmaf(__uint_as_float(v[c][e]), sl, neg_m));
-              float p1 = ex2_approx(fmaf(__uint_as_float(v[c][e + 1]), sl, neg_m));
+              float p0 = ex2_approx(fmaf(__uint_as_float(v[c][e]), slc(c, e), neg_m));
+              float p1 = ex2_approx(fmaf(__uint_as_float(v[c][e + 1]), slc(c, e + 1), neg_m));
               p0 = (c * 32 + e < kv) ? p0 : 0.f;
               p1 = (c * 32 + e + 1 < kv) ? p1 : 0.f;
               rs += p0 + p1;
@@ -681,6 +773,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         mbar_arrive(&p_full[slot]);
       }
       if (!ok) break;
+      if constexpr (KIND == kCtxBlock) tile0 += it.NT;
       if (!tc_wait_warp(&o_final[slot], oc & 1, &s_abort, p.err)) break;
       ++oc;
       tc::fence_after_sync();
@@ -828,6 +921,13 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             if constexpr (C::CONV) {
               // the block's 16 rows of E4M3 codes (128 bytes each) into the upper half of the
               // buffer: rows 16 lane .. 16 lane + 15 of a [128][128 B] code tile
+              if (C::SCALE_ARRIVALS > 0 && lane < 8) {
+                // kvc / 2 counts the CTA's key tiles
+                cp_async4(smem + (kvsel ? C::SCALE_OFF + (buf * 8 + lane) * 4
+                                        : C::KSCALE_OFF + (kvc / 2 % C::KSCALE_RING * 8 + lane) * 4),
+                          (kvsel ? p.v_scales : p.k_scales) + static_cast<int64_t>(blk) * p.Hkv + it.kh);
+                cp_async_arrive_noinc(&kv_full[buf]);
+              }
               if (lane < 8)
                 tma_load_4d(dst + C::TILE_BYTES / 2 + lane * 2048, kvsel ? &tm_cv : &tm_ck, &kv_full[buf], 0,
                             it.kh, 0, blk);
@@ -837,12 +937,15 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
                 tma_load_4d(dst + hf * C::HALF_BYTES + lane * 2048, kvsel ? &tm_cv : &tm_ck, &kv_full[buf], 0,
                             it.kh * C::HALVES + hf, 0, blk);
             }
-          } else if (lane == 0) {
-            const int row = static_cast<int>(it.row0) + (j - it.nct) * 128;
+          } else {
+            if (C::SCALE_ARRIVALS > 0 && lane < 8) mbar_arrive(&kv_full[buf]);  // a new-token tile has no scales
+            if (lane == 0) {
+              const int row = static_cast<int>(it.row0) + (j - it.nct) * 128;
 #pragma unroll
-            for (int hf = 0; hf < C::HALVES; ++hf)
-              tma_load_3d(dst + hf * C::HALF_BYTES, kvsel ? &tm_v : &tm_k, &kv_full[buf], 0,
-                          it.kh * C::HALVES + hf, row);
+              for (int hf = 0; hf < C::HALVES; ++hf)
+                tma_load_3d(dst + hf * C::HALF_BYTES, kvsel ? &tm_v : &tm_k, &kv_full[buf], 0,
+                            it.kh * C::HALVES + hf, row);
+            }
           }
           __syncwarp();
         }
@@ -882,7 +985,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       if (w < 0) break;
       const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
       const bool two = it.nslot == 2;
-      if (!tc_wait_warp(C::CONV ? q_conv : q_full, items & 1, &s_abort, p.err)) break;
+      if (!tc_wait_warp(C::F16 ? q_conv : q_full, items & 1, &s_abort, p.err)) break;
       int prev_vbuf = -1;
       for (int j = 0; j < it.NT; ++j) {
         const int kbuf = kvc % C::NBUF, vbuf = (kvc + 1) % C::NBUF;
@@ -976,13 +1079,15 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       }
       if (w < 0) break;
       const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
-      if (!tc_wait_warp(q_full, k & 1, &s_abort, p.err)) break;
-      for (int sl = 0; sl < it.nslot; ++sl)
+      if constexpr (C::F16) {
+        if (!tc_wait_warp(q_full, k & 1, &s_abort, p.err)) break;
+        for (int sl = 0; sl < it.nslot; ++sl)
 #pragma unroll
-        for (int rr = 0; rr < 2; ++rr) conv_bf16_row<C::HALVES>(q_base + sl * C::TILE_BYTES, ct + 64 * rr, 1.f, true);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_conv);
+          for (int rr = 0; rr < 2; ++rr) conv_bf16_row<C::HALVES>(q_base + sl * C::TILE_BYTES, ct + 64 * rr, 1.f, true);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_conv);
+      }
       for (int j = 0; j < it.NT && ok; ++j) {
         for (int kvsel = 0; kvsel < 2; ++kvsel, ++kvc) {
           const int buf = kvc % C::NBUF;
@@ -992,8 +1097,25 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
           if (j < it.nct) {
             // V rows past the context end become zeros (P = 0 there must not meet a NaN code)
             const int valid = kvsel ? it.C - j * 128 : 128;
+            if constexpr (KIND == kCtxBlock) {
+              const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + buf * 8;
 #pragma unroll
-            for (int rr = 0; rr < 2; ++rr) conv_code_row(tile, ct + 64 * rr, ct + 64 * rr < valid);
+              for (int rr = 0; rr < 2; ++rr) {
+                if (kvsel)
+                  conv_code_row_bf16<true>(tile, ct + 64 * rr, sc[(ct + 64 * rr) / 16], ct + 64 * rr < valid);
+                else
+                  conv_code_row_bf16<false>(tile, ct + 64 * rr, 1.f, true);
+              }
+            } else {
+#pragma unroll
+              for (int rr = 0; rr < 2; ++rr) conv_code_row(tile, ct + 64 * rr, ct + 64 * rr < valid);
+            }
+          } else if constexpr (KIND == kCtxBlock) {
+            // new tokens are bf16 as they came; V rows past the request's own tokens become zeros
+            const int valid = kvsel ? it.q_len - (j - it.nct) * 128 : 128;
+#pragma unroll
+            for (int rr = 0; rr < 2; ++rr)
+              if (ct + 64 * rr >= valid) zero_row<C::HALVES>(tile, ct + 64 * rr);
           } else {
             // new-token values are stored divided by vs; V rows past the request's own tokens
             // become zeros
@@ -1033,6 +1155,7 @@ static cudaError_t launch_attention_tc_impl(const AttnParams& p, const CUtensorM
                                             const CUtensorMap& tqf, cudaStream_t stream, int* launches) {
   using C = TcCfg<D, KIND>;
   const int slot = KIND == kCtxFp8 ? kAttrAttn128Fp8
+                   : KIND == kCtxBlock ? kAttrAttn128Block
                                    : (KIND == kCtxPool ? (D == 64 ? kAttrAttn64Scaled : kAttrAttn128Scaled)
                                                        : (D == 64 ? kAttrAttn64 : kAttrAttn128));
   cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attention_tc_kernel<D, KIND>), C::SMEM, slot);
@@ -1050,6 +1173,10 @@ cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_q, const
   if (ctx_kind == kAttnCtxFp8) {
     if (D != 128) return cudaErrorInvalidValue;
     return launch_attention_tc_impl<128, kCtxFp8>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
+  }
+  if (ctx_kind == kAttnCtxBlock) {
+    if (D != 128) return cudaErrorInvalidValue;
+    return launch_attention_tc_impl<128, kCtxBlock>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
   }
   if (ctx_kind == kAttnCtxPool)
     return D == 64 ? launch_attention_tc_impl<64, kCtxPool>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches)

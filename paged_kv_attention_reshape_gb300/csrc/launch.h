@@ -80,6 +80,8 @@ struct AttnParams {
   float scale_log2;
   float ctx_scale_log2;  // cached-context key tiles: softmax scale * key scale * log2(e)
   float ctx_v_scale;     // cached-context tiles: P is multiplied by the value scale for P V
+  const float* k_scales;  // block-scaled cache: [num_blocks][Hkv]
+  const float* v_scales;
   int32_t sched_slot;    // this launch's work-item counter slot (< kAttnSchedSlots)
 };
 
@@ -103,6 +105,59 @@ struct CtxDequantParams {
   __nv_bfloat16* v_pool;
   int32_t* table_out;    // [batch_reqs][max_blocks]
   int64_t pool_blocks;
+};
+
+// Decode over a block-scaled E4M3 cache.
+struct ScaledDecodeParams {
+  unsigned int* err;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;
+  const int32_t* block_tables;
+  int32_t max_blocks;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  const int32_t* order;
+  const int32_t* bounds;
+  int32_t cls;
+  int32_t max_reqs;
+  int32_t batch_reqs;
+  int32_t Hq, Hkv, G;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scales;
+  const float* v_scales;
+  int64_t num_blocks, stride_block;
+  int32_t max_seq_len;
+  float scale_log2;      // softmax scale * log2(e)
+};
+
+// kv_append: rotation of q and k, append of k and v.
+struct AppendParams {
+  unsigned int* err;
+  const __nv_bfloat16* q;  // [num_tokens][Hq][D], rows q_stride elements apart (k, v alike, Hkv heads)
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;  // NULL: a latent cache (key rows only)
+  int64_t q_stride, k_stride, v_stride;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;    // may be NULL
+  const int64_t* positions;
+  const int64_t* slots;
+  int64_t num_tokens;
+  int32_t Hq, Hkv, D;
+  const float* cos_sin;    // [max_pos][rot]
+  int64_t max_pos;
+  int32_t rot, rot_off, interleaved;
+  void* k_cache;
+  void* v_cache;
+  int64_t num_slots;
+  int32_t block_size;
+  int64_t stride_block;    // elements
+  float k_inv, v_inv;      // FP8 with tensor scales: 1 / scale
+  float* k_scales;         // FP8 with block scales
+  float* v_scales;
+  int32_t run_tokens;      // block scales: tokens whose runs one CTA appends (set by the launcher)
+  uint32_t run_groups;     // block scales: CTAs that append runs (set by the launcher)
 };
 
 // Launch with programmatic stream serialisation: the kernel may begin launching while the
@@ -133,6 +188,7 @@ enum AttrSlot {
   kAttrAttn64Scaled,
   kAttrAttn128Scaled,
   kAttrAttn128Fp8,
+  kAttrAttn128Block,
   kAttrMla,
   kAttrCount
 };
@@ -146,6 +202,8 @@ int max_smem_optin();   // opt-in shared memory per block of the current device,
 cudaError_t launch_kv_cache_write(const void* key, const void* value, const int64_t* slot_mapping,
                                   int64_t num_tokens, const pkv_cache& c, unsigned int* err,
                                   cudaStream_t stream);
+// kind: the cache's kv_dtype
+cudaError_t launch_kv_append(const AppendParams& p, int kind, cudaStream_t stream);
 cudaError_t launch_kv_block_pack(const pkv_cache& c, const int32_t* block_ids, int32_t num_ids,
                                  void* dst, unsigned int* err, cudaStream_t stream);
 cudaError_t launch_kv_block_unpack(const void* src, const int32_t* block_ids, int32_t num_ids,
@@ -156,6 +214,7 @@ cudaError_t launch_batch_classify_reorder(const int32_t* cu_q, const int32_t* se
                                           int64_t num_tokens, cudaStream_t stream, int* launches);
 cudaError_t launch_paged_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                 int D, bool fp8, cudaStream_t stream, int* launches);
+cudaError_t launch_decode_scaled(const ScaledDecodeParams& p, cudaStream_t stream, int* launches);
 int decode_smem_bytes(int D);
 size_t decode_workspace_bytes(int Hq, int Hkv, int D);
 size_t decode_workspace_ctr_offset(int Hq, int Hkv, int D);
@@ -165,8 +224,8 @@ cudaError_t launch_mla_decode(const DecodeParams& p, const CUtensorMap& tm, cuda
 size_t mla_workspace_bytes(int Hq);
 size_t mla_workspace_ctr_offset(int Hq);
 // Cached context of the extend kernel: a bf16 cache, a bf16 pool of an FP8 cache's E4M3 values,
-// or the FP8 cache's codes (head_dim 128), converted in the kernel.
-constexpr int kAttnCtxBf16 = 0, kAttnCtxPool = 1, kAttnCtxFp8 = 2;
+// or the FP8 cache's codes (head_dim 128), converted in the kernel, with tensor or block scales.
+constexpr int kAttnCtxBf16 = 0, kAttnCtxPool = 1, kAttnCtxFp8 = 2, kAttnCtxBlock = 3;
 // tm_q over q, tm_k/tm_v over the packed new keys/values, tm_ck/tm_cv over the paged cache
 // (ignored for prefill), tm_qf over q viewed as [T * Hq][D] (one-token requests' heads as rows).
 cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
