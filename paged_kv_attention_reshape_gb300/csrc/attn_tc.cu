@@ -21,8 +21,7 @@
 //   warp 8     TMA producer: takes the CTA's next work item and publishes it to the other
 //              roles, then loads its Q tiles and K and V tiles into a ring of NBUF tile buffers
 //   warp 9     MMA issuer (one thread): S_i = Q_i K^T (SS), O_i += P_i V (P read from TMEM)
-//   warps 10-11 (FP8 context only) convert E4M3 code tiles, Q and new-token tiles to fp16, or
-//              (block scales) E4M3 code tiles to the bf16 values they stand for
+//   warps 10-11 (FP8 context only) convert E4M3 code tiles, Q and new-token tiles to fp16
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; P_i (bf16 pairs) overwrites the first
 // half of S_i, which the next S_i = Q_i K^T only writes after the P_i V product that reads it
 // (tcgen05 MMAs issued by one thread run in order).
@@ -52,9 +51,9 @@ template <int D, int KIND = kCtxBf16>
 struct TcCfg {
   static constexpr int BM = 128, BN = 128, BS = 16;
   static constexpr bool CONV = KIND == kCtxFp8 || KIND == kCtxBlock;  // converter warps 10 and 11
-  static constexpr bool F16 = KIND == kCtxFp8;   // the products run on fp16 operands
-  // kCtxBlock: the scales of a context tile's blocks travel with the tile, one 4-byte cp.async a
-  // block, each an arrival of its own on the tile's barrier
+  static constexpr bool F16 = CONV;  // the products run on fp16 operands (kCtxBlock: but P V of new tokens)
+  // kCtxBlock: the K and V scales of a context tile's blocks travel with its K tile, two 4-byte
+  // cp.async a block, each block an arrival of its own on the tile's barrier
   static constexpr int SCALE_ARRIVALS = KIND == kCtxBlock ? BN / BS : 0;
   static constexpr int HALVES = D / 64;
   static constexpr int HALF_BYTES = 128 * 128;           // 128 rows x 128 bytes
@@ -79,14 +78,14 @@ struct TcCfg {
   static constexpr int STAGE_WARP_BYTES = 32 * 64;
   static constexpr int ITEM_RING = 4;  // claimed work items published to the consumer roles
   static constexpr int ITEM_OFF = STAGE_OFF + 8 * STAGE_WARP_BYTES;
-  // kCtxBlock: the block scales of V by ring buffer (read by the converters before the buffer is
-  // handed on), then those of K by key tile, tile k of the CTA in slot k % KSCALE_RING (read by the
-  // softmax warps, which may still be at tile k when the producer is at k + 2, never when it is at
-  // k + 4: K of tile k + 4 is loaded once S of tile k + 2 is done, which needs P of tile k + 1)
-  static constexpr int KSCALE_RING = 4;
+  // kCtxBlock, key tile k of the CTA in slot k % SCALE_RING: the blocks' scales as they land (8 of K,
+  // 8 of V), and what the softmax makes of them ({key scale * softmax scale, log2 of the value
+  // scale, its inverse, -} a block). Slot k is written again for tile k + 4, whose K is loaded once S of
+  // tile k + 2 is done, which needs P of tile k + 1: every reader is past tile k by then.
+  static constexpr int SCALE_RING = 4;
   static constexpr int SCALE_OFF = (ITEM_OFF + ITEM_RING * 8 + 15) / 16 * 16;
-  static constexpr int KSCALE_OFF = SCALE_OFF + NBUF * SCALE_ARRIVALS * 4;
-  static constexpr int BAR_OFF = KSCALE_OFF + KSCALE_RING * SCALE_ARRIVALS * 4;
+  static constexpr int FACTOR_OFF = SCALE_OFF + SCALE_RING * 2 * SCALE_ARRIVALS * 4;
+  static constexpr int BAR_OFF = FACTOR_OFF + SCALE_RING * SCALE_ARRIVALS * 16;
   // barriers: q_full, q_empty, kv_full[NBUF], kv_empty[NBUF], s_full[2], p_full[2], o_final[2],
   // item_full[ITEM_RING], item_empty[ITEM_RING], q_conv, conv_full[NBUF]
   static constexpr int NBAR = 2 + 2 * NBUF + 6 + 2 * ITEM_RING + 1 + NBUF;
@@ -280,47 +279,6 @@ __device__ __forceinline__ void conv_code_row(uint32_t tile, int R, bool keep) {
   }
 }
 
-// Code row R -> bf16: the E4M3 values (exactly), or (SCALE) the values times sc, rounded once (not at
-// all when sc is a power of two). Zeros when !keep.
-template <bool SCALE>
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t c, float sc) {
-  const uint32_t h = e4m3x2_to_f16x2(c);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return SCALE ? pack_bf16(f.x * sc, f.y * sc) : pack_bf16(f.x, f.y);
-}
-template <bool SCALE>
-__device__ __forceinline__ void conv_code_row_bf16(uint32_t tile, int R, float sc, bool keep) {
-  uint4 c[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) c[q] = ld_shared_v4(tile + 16384u + R * 128 + ((q ^ (R & 7)) << 4));
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
-    if (keep) {
-      a = make_uint4(e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].x), sc),
-                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].x >> 16), sc),
-                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].y), sc),
-                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].y >> 16), sc));
-      b = make_uint4(e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].z), sc),
-                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].z >> 16), sc),
-                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].w), sc),
-                     e4m3x2_to_bf16x2<SCALE>(static_cast<uint16_t>(c[q].w >> 16), sc));
-    }
-    const uint32_t base = tile + (q >> 2) * 16384u + R * 128;
-    const int ch = 2 * (q & 3);
-    st_shared_v4(base + ((ch ^ (R & 7)) << 4), a);
-    st_shared_v4(base + (((ch + 1) ^ (R & 7)) << 4), b);
-  }
-}
-// Row R of a [halves][128][128 B] tile set to zeros.
-template <int HALVES>
-__device__ __forceinline__ void zero_row(uint32_t tile, int R) {
-#pragma unroll
-  for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) st_shared_v4(tile + h * 16384u + R * 128 + (q << 4), make_uint4(0, 0, 0, 0));
-}
-
 // bf16 x 2 -> fp16 x 2, times sc
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2_scaled(uint32_t x, float sc) {
   return pack_f16(__uint_as_float(x << 16) * sc, __uint_as_float(x & 0xFFFF0000u) * sc);
@@ -344,6 +302,15 @@ __device__ __forceinline__ void conv_bf16_row(uint32_t tile, int R, float sc, bo
     }
 }
 
+// Row R of a [halves][128][128 B] tile set to zeros.
+template <int HALVES>
+__device__ __forceinline__ void zero_row(uint32_t tile, int R) {
+#pragma unroll
+  for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) st_shared_v4(tile + h * 16384u + R * 128 + (q << 4), make_uint4(0, 0, 0, 0));
+}
+
 // kCtxPool and kCtxFp8 (SCALED): the cached context holds the E4M3 values of an FP8 cache. The key
 // scale goes with the softmax scale of context tiles. The value scale vs is taken out of the
 // sum instead of multiplied into every context tile's P, so that
@@ -359,13 +326,18 @@ __device__ __forceinline__ void conv_bf16_row(uint32_t tile, int R, float sc, bo
 // the converters' barriers (q_conv, conv_full) instead of the loads'. Queries, new keys and
 // new values divided by vs must lie within the fp16 range.
 //
-// kCtxBlock: the same pipeline with a scale for each 16-token block and head, and bf16 operands
-// (whose range is fp32's, so that no scale is out of range; the queries and new tokens stay as they
-// come). The converter warps write K as the E4M3 values themselves, exactly, and the softmax
-// multiplies each block's 16 columns of S by its scale in fp32: rounding code * scale to bf16
-// instead would put an error of up to 2^-8 of each product into the exponent. V is written as
-// code * scale, rounded once to bf16 (2^-8 of the value at most, like P's own rounding; not at all
-// for the powers of two that kv_append makes).
+// kCtxBlock: the same pipeline for a cache with scales ks_b, vs_b for each 16-token block b and
+// head. The tensor core multiplies the E4M3 values themselves (exact in fp16) and the softmax
+// applies the scales to a block's 16 columns in fp32, where nothing is rounded to few bits: with
+//   u_j = log2(e) scale ks_b s_j + log2 vs_b,   m the running max of u,
+//   P_j = 2^(u_j - m)  (fp16; O = sum_j P_j v_j),   l = sum_j P_j / vs_b  (fp32),
+// out = O / l and lse = (m + log2 l) ln 2. Taking the max over u rather than over the scores keeps
+// P within [0, 2^8] whatever the scales, and costs nothing per column: the shift of the exponent
+// and the factor of the sum are the block's. (Rounding scale * code to 16 bits in the converters,
+// the first form, put 2^-8 of each product into the exponent or of each value into the sum, and
+// its conversions, 9 instructions for a pair of codes against 2, made the kernel 2.5 times
+// slower.) New tokens have vs = 1; their P and V stay bf16, so values of any size pass; queries
+// and new keys become fp16 and must lie within its range.
 template <int D, int KIND>
 __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kernel(
     const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
@@ -574,18 +546,6 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         const bool vsc = KIND == kCtxPool && !ctx && p.ctx_v_scale != 1.f;
         float alpha = 1.f, rs = 0.f;
         if constexpr (C::ONE_READ) {
-        // scale of each block's 16 columns: with block scales the key scale goes with the softmax scale
-        float slg[KIND == kCtxBlock ? 8 : 1];
-        if constexpr (KIND == kCtxBlock) {
-          const float4* ks = reinterpret_cast<const float4*>(smem + C::KSCALE_OFF) + (tile0 + j) % C::KSCALE_RING * 2;
-          const float4 k0 = ctx ? ks[0] : make_float4(1.f, 1.f, 1.f, 1.f), k1 = ctx ? ks[1] : make_float4(1.f, 1.f, 1.f, 1.f);
-          slg[0] = k0.x * sl, slg[1] = k0.y * sl, slg[2] = k0.z * sl, slg[3] = k0.w * sl;
-          slg[4] = k1.x * sl, slg[5] = k1.y * sl, slg[6] = k1.z * sl, slg[7] = k1.w * sl;
-        } else {
-          slg[0] = sl;
-        }
-        // the factor of column c * 32 + e
-        auto slc = [&](int c, int e) { return KIND == kCtxBlock ? slg[2 * c + (e >> 4)] : slg[0]; };
         // the whole row of S into registers (four loads, one wait)
         uint32_t v[4][32];
 #pragma unroll
@@ -593,23 +553,64 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         tc::wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
-        // row max of the raw scores (the scale is positive, so it commutes with max; with block
-        // scales it does so within a block's columns)
-        float mx = -CUDART_INF_F;
         if constexpr (KIND == kCtxBlock) {
+        // the factors of block g of the tile: {key scale * softmax scale, log2 vs, 1 / vs}
+        const float4* fac = reinterpret_cast<const float4*>(smem + C::FACTOR_OFF) + (tile0 + j) % C::SCALE_RING * 8;
+        // columns past kv become -inf (their p is 0); the max of a block's raw scores, then of the blocks' u
+        if (!full) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            float mg = -CUDART_INF_F;
+          for (int c = 0; c < 4; ++c) mask_cols(v[c], kv - c * 32);
+        }
+        float mx = -CUDART_INF_F;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const int c = g / 2, b = (g & 1) * 16 + e;
-              const float a0 = full || g * 16 + e < kv ? __uint_as_float(v[c][b]) : -CUDART_INF_F;
-              const float a1 = full || g * 16 + e + 1 < kv ? __uint_as_float(v[c][b + 1]) : -CUDART_INF_F;
-              mg = sm::max3(mg, a0, a1);
-            }
-            mx = fmaxf(mx, mg * slg[g]);
+        for (int g = 0; g < 8; ++g) {
+          float mg = -CUDART_INF_F;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            mg = sm::max3(mg, __uint_as_float(v[g / 2][(g & 1) * 16 + e]), __uint_as_float(v[g / 2][(g & 1) * 16 + e + 1]));
+          const float4 f = fac[g];
+          mx = fmaxf(mx, fmaf(mg, f.x, f.y));
+        }
+        if (mx > m + 8.f || m == -CUDART_INF_F) {  // lazy rescale: only when the max really grows
+          const float m_new = fmaxf(m, mx);
+          if (m_new != -CUDART_INF_F) {
+            alpha = (m == -CUDART_INF_F) ? 0.f : ex2_approx(m - m_new);
+            m = m_new;
           }
-        } else if (full) {
+        }
+        const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+        // P of the 16 columns of block g, packed over the first half of S: fp16 beside the context's
+        // codes, bf16 beside new values; the row sum takes each P over its block's vs
+        uint64_t rs2 = sm::f2(0.f, 0.f);
+        auto exp_pass = [&](auto f16) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int gg = 0; gg < 2; ++gg) {
+              const float4 f = fac[2 * c + gg];
+              const uint64_t sc2 = sm::f2(f.x, f.x), nm2 = sm::f2(neg_m + f.y, neg_m + f.y), iv2 = sm::f2(f.z, f.z);
+#pragma unroll
+              for (int e = 16 * gg; e < 16 * gg + 16; e += 2) {
+                const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
+                float x0, x1;
+                sm::unf2(x, x0, x1);
+                const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
+                rs2 = sm::fma2(pp, iv2, rs2);
+                pk[e / 2] = decltype(f16)::value ? sm::f16x2(pp) : sm::bf16x2(pp);
+              }
+            }
+            tc::st16(srow + c * 16, pk);
+          }
+        };
+        if (ctx) exp_pass(std::true_type{}); else exp_pass(std::false_type{});
+        float r0, r1;
+        sm::unf2(rs2, r0, r1);
+        rs = r0 + r1;
+        } else {
+        // row max of the raw scores (the scale is positive, so it commutes with max)
+        float mx = -CUDART_INF_F;
+        if (full) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             for (int e = 0; e < 32; ++e)
               if (c * 32 + e < kv) mx = fmaxf(mx, __uint_as_float(v[c][e]));
         }
-        if constexpr (KIND != kCtxBlock) mx = mx * sl;  // -inf stays -inf
+        mx = mx * sl;  // -inf stays -inf
         if (mx > m + 8.f || m == -CUDART_INF_F) {  // lazy rescale: only when the max really grows
           const float m_new = fmaxf(m, mx);
           if (m_new != -CUDART_INF_F) {
@@ -634,15 +635,14 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         if (full) {
           // every column valid: pairs of columns in packed fp32 (one instruction per pair for
           // the scale-and-shift and the running sum)
-          const uint64_t nm2 = sm::f2(neg_m, neg_m);
+          const uint64_t sc2 = sm::f2(sl, sl), nm2 = sm::f2(neg_m, neg_m);
           uint64_t rs2 = sm::f2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
-                                          sm::f2(slc(c, e), slc(c, e)), nm2);
+              const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
               float x0, x1;
               sm::unf2(x, x0, x1);
               const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
@@ -660,8 +660,8 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              float p0 = ex2_approx(fmaf(__uint_as_float(v[c][e]), slc(c, e), neg_m));
-              float p1 = ex2_approx(fmaf(__uint_as_float(v[c][e + 1]), slc(c, e + 1), neg_m));
+              float p0 = ex2_approx(fmaf(__uint_as_float(v[c][e]), sl, neg_m));
+              float p1 = ex2_approx(fmaf(__uint_as_float(v[c][e + 1]), sl, neg_m));
               p0 = (c * 32 + e < kv) ? p0 : 0.f;
               p1 = (c * 32 + e + 1 < kv) ? p1 : 0.f;
               rs += p0 + p1;
@@ -669,6 +669,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             }
             tc::st16(srow + c * 16, pk);
           }
+        }
         }
         } else {
         // pass 1: row max of the raw scores (the scale is positive, so it commutes with max)
@@ -922,11 +923,15 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
               // the block's 16 rows of E4M3 codes (128 bytes each) into the upper half of the
               // buffer: rows 16 lane .. 16 lane + 15 of a [128][128 B] code tile
               if (C::SCALE_ARRIVALS > 0 && lane < 8) {
-                // kvc / 2 counts the CTA's key tiles
-                cp_async4(smem + (kvsel ? C::SCALE_OFF + (buf * 8 + lane) * 4
-                                        : C::KSCALE_OFF + (kvc / 2 % C::KSCALE_RING * 8 + lane) * 4),
-                          (kvsel ? p.v_scales : p.k_scales) + static_cast<int64_t>(blk) * p.Hkv + it.kh);
-                cp_async_arrive_noinc(&kv_full[buf]);
+                if (kvsel == 0) {  // kvc / 2 counts the CTA's key tiles
+                  const int64_t at = static_cast<int64_t>(blk) * p.Hkv + it.kh;
+                  float* dst_sc = reinterpret_cast<float*>(smem + C::SCALE_OFF) + kvc / 2 % C::SCALE_RING * 16 + lane;
+                  cp_async4(dst_sc, p.k_scales + at);
+                  cp_async4(dst_sc + 8, p.v_scales + at);
+                  cp_async_arrive_noinc(&kv_full[buf]);
+                } else {
+                  mbar_arrive(&kv_full[buf]);
+                }
               }
               if (lane < 8)
                 tma_load_4d(dst + C::TILE_BYTES / 2 + lane * 2048, kvsel ? &tm_cv : &tm_ck, &kv_full[buf], 0,
@@ -965,12 +970,13 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
                    C::IDESC_QK, k > 0);
       }
     };
-    auto pv = [&](int slot, const uint8_t* vbuf, bool acc) {
+    auto pv = [&](int slot, const uint8_t* vbuf, bool acc, bool ctx) {
       const uint32_t vb = smem_u32(vbuf);
+      const uint32_t idesc = KIND == kCtxBlock && !ctx ? tc::idesc_bf16(128, D, 0, 1) : C::IDESC_PV;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         tc::mma_ts(tmem + ocol(slot), tmem + scol(slot) + k * 8,
-                   tc::smem_desc(vb + k * 2048, C::HALF_BYTES, 1024), C::IDESC_PV, (acc || k > 0) ? 1u : 0u);
+                   tc::smem_desc(vb + k * 2048, C::HALF_BYTES, 1024), idesc, (acc || k > 0) ? 1u : 0u);
     };
     int64_t w_static = blockIdx.x;
     int odd = 0;
@@ -985,7 +991,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       if (w < 0) break;
       const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
       const bool two = it.nslot == 2;
-      if (!tc_wait_warp(C::F16 ? q_conv : q_full, items & 1, &s_abort, p.err)) break;
+      if (!tc_wait_warp(C::CONV ? q_conv : q_full, items & 1, &s_abort, p.err)) break;
       int prev_vbuf = -1;
       for (int j = 0; j < it.NT; ++j) {
         const int kbuf = kvc % C::NBUF, vbuf = (kvc + 1) % C::NBUF;
@@ -1003,7 +1009,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
           ++pc1;
           tc::fence_after_sync();
           if (lane == 0) {
-            pv(1, ring + prev_vbuf * C::TILE_BYTES, j - 1 > 0);
+            pv(1, ring + prev_vbuf * C::TILE_BYTES, j - 1 > 0, j - 1 < it.nct);
             tc::commit(&kv_empty[prev_vbuf]);
           }
           __syncwarp();
@@ -1037,7 +1043,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         ++pc;
         tc::fence_after_sync();
         if (lane == 0) {
-          pv(0, ring + vbuf * C::TILE_BYTES, j > 0);
+          pv(0, ring + vbuf * C::TILE_BYTES, j > 0, j < it.nct);
           // slot 0's O is final once this product is done: its epilogue may overlap slot 1's
           // last softmax and P V
           if (j == it.NT - 1) tc::commit(&o_final[0]);
@@ -1050,7 +1056,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         if (!tc_wait_warp(&p_full[1], pc1 & 1, &s_abort, p.err)) break;
         ++pc1;
         tc::fence_after_sync();
-        if (lane == 0) pv(1, ring + prev_vbuf * C::TILE_BYTES, it.NT - 1 > 0);
+        if (lane == 0) pv(1, ring + prev_vbuf * C::TILE_BYTES, it.NT - 1 > 0, it.NT - 1 < it.nct);
       }
       if (lane == 0) {
         tc::commit(&kv_empty[prev_vbuf]);
@@ -1063,7 +1069,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
     // Thread ct converts rows ct and ct + 64 of every tile: Q (both head slots) once per item,
     // then each K and V tile as it lands, in the producer's order.
     const int ct = tid - 320;
-    const float inv_vs = 1.f / p.ctx_v_scale;
+    const float inv_vs = SCALED ? 1.f / p.ctx_v_scale : 1.f;
     const uint32_t q_base = smem_u32(sQ), ring_base = smem_u32(ring);
     uint32_t kvc = 0;
     bool ok = true;
@@ -1079,40 +1085,39 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       }
       if (w < 0) break;
       const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
-      if constexpr (C::F16) {
-        if (!tc_wait_warp(q_full, k & 1, &s_abort, p.err)) break;
-        for (int sl = 0; sl < it.nslot; ++sl)
+      if (!tc_wait_warp(q_full, k & 1, &s_abort, p.err)) break;
+      for (int sl = 0; sl < it.nslot; ++sl)
 #pragma unroll
-          for (int rr = 0; rr < 2; ++rr) conv_bf16_row<C::HALVES>(q_base + sl * C::TILE_BYTES, ct + 64 * rr, 1.f, true);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_conv);
-      }
+        for (int rr = 0; rr < 2; ++rr) conv_bf16_row<C::HALVES>(q_base + sl * C::TILE_BYTES, ct + 64 * rr, 1.f, true);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_conv);
       for (int j = 0; j < it.NT && ok; ++j) {
         for (int kvsel = 0; kvsel < 2; ++kvsel, ++kvc) {
           const int buf = kvc % C::NBUF;
           const uint32_t use = kvc / C::NBUF;
           if (!tc_wait_warp(&kv_full[buf], use & 1, &s_abort, p.err)) { ok = false; break; }
           const uint32_t tile = ring_base + buf * C::TILE_BYTES;
+          if (KIND == kCtxBlock && kvsel == 0 && ct < 8) {
+            // the tile's softmax factors of block ct
+            const uint32_t at = kvc / 2 % C::SCALE_RING;
+            float4 f = make_float4(p.scale_log2, 0.f, 1.f, 0.f);
+            if (j < it.nct) {
+              const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + at * 16;
+              // a zero scale counts as 2^-100: no logarithm of 0, no product of 0 and a masked -inf
+              const float ks = fmaxf(sc[ct], 0x1p-100f), vs = fmaxf(sc[8 + ct], 0x1p-100f);
+              f = make_float4(ks * p.scale_log2, __log2f(vs), 1.f / vs, 0.f);
+            }
+            reinterpret_cast<float4*>(smem + C::FACTOR_OFF)[at * 8 + ct] = f;
+          }
           if (j < it.nct) {
             // V rows past the context end become zeros (P = 0 there must not meet a NaN code)
             const int valid = kvsel ? it.C - j * 128 : 128;
-            if constexpr (KIND == kCtxBlock) {
-              const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + buf * 8;
 #pragma unroll
-              for (int rr = 0; rr < 2; ++rr) {
-                if (kvsel)
-                  conv_code_row_bf16<true>(tile, ct + 64 * rr, sc[(ct + 64 * rr) / 16], ct + 64 * rr < valid);
-                else
-                  conv_code_row_bf16<false>(tile, ct + 64 * rr, 1.f, true);
-              }
-            } else {
-#pragma unroll
-              for (int rr = 0; rr < 2; ++rr) conv_code_row(tile, ct + 64 * rr, ct + 64 * rr < valid);
-            }
-          } else if constexpr (KIND == kCtxBlock) {
-            // new tokens are bf16 as they came; V rows past the request's own tokens become zeros
-            const int valid = kvsel ? it.q_len - (j - it.nct) * 128 : 128;
+            for (int rr = 0; rr < 2; ++rr) conv_code_row(tile, ct + 64 * rr, ct + 64 * rr < valid);
+          } else if (KIND == kCtxBlock && kvsel) {
+            // new values stay as they come; V rows past the request's own tokens become zeros
+            const int valid = it.q_len - (j - it.nct) * 128;
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr)
               if (ct + 64 * rr >= valid) zero_row<C::HALVES>(tile, ct + 64 * rr);
@@ -1154,7 +1159,7 @@ static cudaError_t launch_attention_tc_impl(const AttnParams& p, const CUtensorM
                                             const CUtensorMap& tck, const CUtensorMap& tcv,
                                             const CUtensorMap& tqf, cudaStream_t stream, int* launches) {
   using C = TcCfg<D, KIND>;
-  const int slot = KIND == kCtxFp8 ? kAttrAttn128Fp8
+  const int slot = KIND == kCtxFp8     ? kAttrAttn128Fp8
                    : KIND == kCtxBlock ? kAttrAttn128Block
                                    : (KIND == kCtxPool ? (D == 64 ? kAttrAttn64Scaled : kAttrAttn128Scaled)
                                                        : (D == 64 ? kAttrAttn64 : kAttrAttn128));
