@@ -522,8 +522,6 @@ size_t pkv_paged_decode_workspace_size(int32_t max_reqs, int32_t num_q_heads, in
   return decode_workspace_bytes(num_q_heads, num_kv_heads, head_dim);
 }
 
-static pkv_status run_decode_scaled(const DecodeParams& d, const pkv_cache& cache, pkv_stream_t stream);
-
 pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* block_tables,
                                  int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_q,
                                  pkv_reqs reqs, int32_t num_q_heads, int32_t max_seq_len,
@@ -565,12 +563,16 @@ pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* 
   // into the output
   p.scale_log2 = scale * (fp8 ? cache.k_scale : 1.f) * 1.4426950408889634f;
   p.v_scale = fp8 ? cache.v_scale : 1.f;
-  if (cache.kv_dtype == PKV_KV_FP8_E4M3_BLOCK) return run_decode_scaled(p, cache, stream);
-  const size_t need = decode_workspace_bytes(p.Hq, p.Hkv, cache.head_dim);
+  const bool scaled = cache.kv_dtype == PKV_KV_FP8_E4M3_BLOCK;
+  if (scaled && !decode_scaled_supported(p.Hkv)) return PKV_ERR_UNSUPPORTED;
+  p.k_scales = cache.k_scales;
+  p.v_scales = cache.v_scales;
+  const size_t need = scaled ? decode_scaled_workspace_bytes(p.Hq, p.Hkv) : decode_workspace_bytes(p.Hq, p.Hkv, cache.head_dim);
   if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_WORKSPACE;
   p.ws_part = static_cast<float*>(workspace);
   p.ws_ctr = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) +
-                                                   decode_workspace_ctr_offset(p.Hq, p.Hkv, cache.head_dim));
+                                                   (scaled ? decode_scaled_ctr_offset(p.Hq, p.Hkv)
+                                                           : decode_workspace_ctr_offset(p.Hq, p.Hkv, cache.head_dim)));
   CUtensorMap tk, tv;
   if (!encode_cache(&tk, cache.k, cache) || !encode_cache(&tv, cache.v, cache)) return PKV_ERR_CUDA;
   // one launch per chunk of kSetChunk set positions, in stream order (each reuses the
@@ -579,41 +581,10 @@ pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* 
   for (int32_t off = 0; off < reqs.max_reqs && st == PKV_OK; off += kSetChunk) {
     p.set_offset = off;
     p.epoch = next_epoch();
-    st = cuda_status(launch_paged_decode(p, tk, tv, cache.head_dim, fp8,
-                                         reinterpret_cast<cudaStream_t>(stream), &launches));
+    st = cuda_status(scaled ? launch_decode_scaled(p, tk, tv, reinterpret_cast<cudaStream_t>(stream), &launches)
+                            : launch_paged_decode(p, tk, tv, cache.head_dim, fp8, reinterpret_cast<cudaStream_t>(stream),
+                                                  &launches));
   }
-  t_launches += launches;
-  return st;
-}
-
-static pkv_status run_decode_scaled(const DecodeParams& d, const pkv_cache& cache, pkv_stream_t stream) {
-  ScaledDecodeParams p{};
-  p.err = d.err;
-  p.q = d.q;
-  p.out = d.out;
-  p.lse = d.lse;
-  p.block_tables = d.block_tables;
-  p.max_blocks = d.max_blocks;
-  p.seq_lens = d.seq_lens;
-  p.cu_q = d.cu_q;
-  p.order = d.order;
-  p.bounds = d.bounds;
-  p.cls = d.cls;
-  p.max_reqs = d.max_reqs;
-  p.batch_reqs = d.batch_reqs;
-  p.Hq = d.Hq;
-  p.Hkv = d.Hkv;
-  p.G = d.G;
-  p.k = static_cast<const uint8_t*>(cache.k);
-  p.v = static_cast<const uint8_t*>(cache.v);
-  p.k_scales = cache.k_scales;
-  p.v_scales = cache.v_scales;
-  p.num_blocks = cache.num_blocks;
-  p.stride_block = cache.stride_block;
-  p.max_seq_len = d.max_seq_len;
-  p.scale_log2 = d.scale_log2;
-  int launches = 0;
-  const pkv_status st = cuda_status(launch_decode_scaled(p, reinterpret_cast<cudaStream_t>(stream), &launches));
   t_launches += launches;
   return st;
 }

@@ -54,6 +54,8 @@ struct DecodeParams {
   int32_t launch_shares;    // shares the launch's grid holds (CTAs x shares per CTA): the level stride of the merge counters
   const void* kv;           // MLA decode: the latent cache (blocks kv_block_bytes apart)
   int64_t kv_block_bytes;
+  const float* k_scales;    // block-scaled cache: [num_blocks][Hkv]
+  const float* v_scales;
 };
 
 // Extend and prefill share one kernel; prefill is the case without cached context.
@@ -105,31 +107,6 @@ struct CtxDequantParams {
   __nv_bfloat16* v_pool;
   int32_t* table_out;    // [batch_reqs][max_blocks]
   int64_t pool_blocks;
-};
-
-// Decode over a block-scaled E4M3 cache.
-struct ScaledDecodeParams {
-  unsigned int* err;
-  const __nv_bfloat16* q;
-  __nv_bfloat16* out;
-  float* lse;
-  const int32_t* block_tables;
-  int32_t max_blocks;
-  const int32_t* seq_lens;
-  const int32_t* cu_q;
-  const int32_t* order;
-  const int32_t* bounds;
-  int32_t cls;
-  int32_t max_reqs;
-  int32_t batch_reqs;
-  int32_t Hq, Hkv, G;
-  const uint8_t* k;
-  const uint8_t* v;
-  const float* k_scales;
-  const float* v_scales;
-  int64_t num_blocks, stride_block;
-  int32_t max_seq_len;
-  float scale_log2;      // softmax scale * log2(e)
 };
 
 // kv_append: rotation of q and k, append of k and v.
@@ -189,6 +166,8 @@ enum AttrSlot {
   kAttrAttn128Scaled,
   kAttrAttn128Fp8,
   kAttrAttn128Block,
+  kAttrDecodeScaled8,
+  kAttrDecodeScaled16,
   kAttrMla,
   kAttrCount
 };
@@ -214,7 +193,12 @@ cudaError_t launch_batch_classify_reorder(const int32_t* cu_q, const int32_t* se
                                           int64_t num_tokens, cudaStream_t stream, int* launches);
 cudaError_t launch_paged_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                 int D, bool fp8, cudaStream_t stream, int* launches);
-cudaError_t launch_decode_scaled(const ScaledDecodeParams& p, cudaStream_t stream, int* launches);
+// Decode over a block-scaled E4M3 cache (its workspace is never larger than paged_decode's).
+cudaError_t launch_decode_scaled(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream,
+                                 int* launches);
+bool decode_scaled_supported(int Hkv);
+size_t decode_scaled_workspace_bytes(int Hq, int Hkv);
+size_t decode_scaled_ctr_offset(int Hq, int Hkv);
 int decode_smem_bytes(int D);
 size_t decode_workspace_bytes(int Hq, int Hkv, int D);
 size_t decode_workspace_ctr_offset(int Hq, int Hkv, int D);

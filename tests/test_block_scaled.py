@@ -429,6 +429,23 @@ def test_decode_long_and_cut_sequences(lens, G, Hkv, qs):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,G", [([1500, 1, 1900, 130], 1), ([4003, 2500], 2), ([700, 650, 3001], 16)])
+def test_decode_many_tiles_a_share(lens, G):
+    """Many KV heads, so that each of them has few shares and a share holds tens of 128-token tiles."""
+    Hkv = 64
+    g = gen(len(lens))
+    t, nb = tables([(c + 15) // 16 for c in lens], g)
+    any_codes = lambda: torch.randint(0, 120, (nb, 16, Hkv, 128), generator=g, dtype=torch.uint8) + \
+        128 * torch.randint(0, 2, (nb, 16, Hkv, 128), generator=g, dtype=torch.uint8)  # noqa: E731
+    st = dict(lens=lens, table=t, kc=any_codes(), vc=any_codes(), gap=0, ks=0.01 * torch.rand((nb, Hkv), generator=g) + 0.001,
+              vs=0.01 * torch.rand((nb, Hkv), generator=g) + 0.001,
+              q=torch.randn((len(lens), G * Hkv, 128), generator=g).to(torch.bfloat16))
+    for _ in range(3):
+        out = gpu_decode(st)
+    check_decode(st, *out, SCALE)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("what", ["wide_v", "wide_k", "tiny", "sink", "zero", "scale"])
 def test_decode_extreme_scales_and_scores(what):
     """Values whose size changes from block to block by many powers of two, scores that one token dominates."""
