@@ -77,6 +77,8 @@ def lib_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libpkv.so (building it first when it is missing and nvcc is available)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

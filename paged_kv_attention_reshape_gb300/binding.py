@@ -32,8 +32,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a Stream object around it (a few microseconds a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
@@ -49,36 +55,51 @@ def _need(t: torch.Tensor, dtype, name: str, contiguous: bool = True):
         raise PkvError(f"{name} must be contiguous")
 
 
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _block_scales(k_scale, v_scale, nb: int, hkv: int, device_index: int):
+    """Checks scale tensors [num_blocks, Hkv]; returns their addresses."""
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if not isinstance(t, torch.Tensor):
+            raise PkvError("k_scale and v_scale must both be numbers or both be tensors")
+        _need(t, torch.float32, n)
+        if tuple(t.shape) != (nb, hkv):
+            raise PkvError(f"{n} must be [num_blocks, Hkv] = [{nb}, {hkv}], got {list(t.shape)}")
+        if t.get_device() != device_index:
+            raise PkvError(f"{n} must be on the cache's device")
+    return k_scale.data_ptr(), v_scale.data_ptr()
+
+
 def make_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale=1.0, v_scale=1.0) -> "_lib.PkvCache":
     """Describe one layer's paged cache: k_cache / v_cache [num_blocks, block_size, Hkv, D]
     with contiguous blocks (any stride between blocks). bf16 tensors are a bf16 cache; uint8
     or float8_e4m3fn tensors are an FP8 (E4M3) cache whose codes stand for e4m3(code) * scale.
     k_scale and v_scale are numbers (one scale for the tensor) or fp32 tensors [num_blocks, Hkv]
     (a scale for each block and KV head)."""
-    fp8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-    want = k_cache.dtype if fp8 else torch.bfloat16
+    dtype = k_cache.dtype
+    fp8 = dtype in _FP8
+    want = dtype if fp8 else torch.bfloat16
+    shape = k_cache.shape
+    nb, bs, hkv, d = shape
+    stride = 0
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, want, n, contiguous=False)
-        nb, bs, hkv, d = t.shape
-        if t.stride()[1:] != (hkv * d, d, 1):
+        st = t.stride()
+        if st[1:] != (hkv * d, d, 1):
             raise PkvError(f"{n}: each block must be contiguous [block_size, Hkv, D]")
-    if k_cache.shape != v_cache.shape or k_cache.stride(0) != v_cache.stride(0):
-        raise PkvError("k_cache and v_cache must have the same shape and block stride")
-    nb, bs, hkv, d = k_cache.shape
+        if t.shape != shape or (stride and st[0] != stride):
+            raise PkvError("k_cache and v_cache must have the same shape and block stride")
+        stride = st[0]
+        if v_cache is k_cache:
+            break
     if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
         if not fp8:
             raise PkvError("block scales belong to an FP8 cache")
-        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if not isinstance(t, torch.Tensor):
-                raise PkvError("k_scale and v_scale must both be numbers or both be tensors")
-            _need(t, torch.float32, n)
-            if tuple(t.shape) != (nb, hkv):
-                raise PkvError(f"{n} must be [num_blocks, Hkv] = [{nb}, {hkv}], got {list(t.shape)}")
-            if t.device != k_cache.device:
-                raise PkvError(f"{n} must be on the cache's device")
-        return _lib.PkvCache(k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, hkv, d, k_cache.stride(0),
-                             _lib.KV_FP8_E4M3_BLOCK, 1.0, 1.0, k_scale.data_ptr(), v_scale.data_ptr())
-    return _lib.PkvCache(k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, hkv, d, k_cache.stride(0),
+        ks, vs = _block_scales(k_scale, v_scale, nb, hkv, k_cache.get_device())
+        return _lib.PkvCache(k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, hkv, d, stride,
+                             _lib.KV_FP8_E4M3_BLOCK, 1.0, 1.0, ks, vs)
+    return _lib.PkvCache(k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, hkv, d, stride,
                          _lib.KV_FP8_E4M3 if fp8 else _lib.KV_BF16, float(k_scale), float(v_scale))
 
 
@@ -110,21 +131,36 @@ def kv_cache_write(key, value, slot_mapping, k_cache, v_cache, stream=None, k_sc
                                   cache, _stream(stream)), "kv_cache_write")
 
 
-def _token_rows(t: torch.Tensor, name: str, heads: int, dim: int, device) -> int:
-    """Checks bf16 rows [T, heads, dim] whose tokens may lie apart (a slice of a fused projection);
+def _token_rows(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, device_index: int) -> int:
+    """Checks bf16 rows [rows, heads, dim] whose tokens may lie apart (a slice of a fused projection);
     returns the elements between tokens."""
-    _need(t, torch.bfloat16, name, contiguous=False)
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
-        raise PkvError(f"{name} must be [T, {heads}, {dim}], got {list(t.shape)}")
-    if t.device != device:
+    if not t.is_cuda or t.get_device() != device_index:
         raise PkvError(f"{name} must be on the cache's device")
-    if t.shape[0] <= 1:
-        inner_ok = t.is_contiguous()
-    else:
-        inner_ok = (dim == 1 or t.stride(2) == 1) and (heads == 1 or t.stride(1) == dim)
-    if not inner_ok:
+    if t.dtype is not torch.bfloat16:
+        raise PkvError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != (rows, heads, dim):
+        raise PkvError(f"{name} must be [{rows}, {heads}, {dim}], got {list(t.shape)}")
+    if t.is_contiguous():
+        return heads * dim
+    st = t.stride()
+    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
         raise PkvError(f"{name}: each token's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return st[0] if rows > 1 else heads * dim
+
+
+def _token_index(t: torch.Tensor, name: str, rows: int, device_index: int) -> int:
+    if not t.is_cuda or t.get_device() != device_index or t.dtype is not torch.int64 or t.numel() != rows \
+            or not t.is_contiguous():
+        raise PkvError(f"{name} must be {rows} contiguous int64 entries on the cache's device")
+    return t.data_ptr()
+
+
+def _token_out(t: Optional[torch.Tensor], name: str, rows: int, heads: int, dim: int, like: torch.Tensor) -> torch.Tensor:
+    if t is None:
+        return torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=like.device)
+    if _token_rows(t, name, rows, heads, dim, like.get_device()) != heads * dim or not t.is_contiguous():
+        raise PkvError(f"{name} must be contiguous")
+    return t
 
 
 def kv_append(q, key, value, positions, slot_mapping, k_cache, v_cache, cos_sin=None, *, rope_offset=0,
@@ -142,46 +178,34 @@ def kv_append(q, key, value, positions, slot_mapping, k_cache, v_cache, cos_sin=
     if (value is None) != (v_cache is None):
         raise PkvError("a latent cache has neither value nor v_cache; any other has both")
     cache = make_cache(k_cache, k_cache if v_cache is None else v_cache, k_scale, v_scale)
-    dev, hkv, d = k_cache.device, k_cache.shape[2], k_cache.shape[3]
-    if dev.index != torch.cuda.current_device():
+    dev, hkv, d = k_cache.get_device(), cache.num_kv_heads, cache.head_dim
+    if dev != torch.cuda.current_device():
         raise PkvError("the cache must be on the current device")
-    k_stride = _token_rows(key, "key", hkv, d, dev)
     T = key.shape[0]
-    v_stride = hkv * d
+    k_stride = _token_rows(key, "key", T, hkv, d, dev)
+    v_ptr, v_stride = None, 0
     if value is not None:
-        v_stride = _token_rows(value, "value", hkv, d, dev)
-    hq, q_stride = 0, 0
+        v_ptr, v_stride = value.data_ptr(), _token_rows(value, "value", T, hkv, d, dev)
+    hq, q_ptr, q_stride, qo_ptr = 0, None, 0, None
     if q is not None:
         hq = q.shape[1]
-        q_stride = _token_rows(q, "q", hq, d, dev)
-    for t, n in ((value, "value"), (q, "q")):
-        if t is not None and t.shape[0] != T:
-            raise PkvError(f"{n} must have key's {T} tokens, got {t.shape[0]}")
-    rope = _lib.PkvRope(None, 0, 0, 0, 0)
-    need = [(slot_mapping, torch.int64, "slot_mapping")]
+        q_ptr, q_stride = q.data_ptr(), _token_rows(q, "q", T, hq, d, dev)
+        q_out = _token_out(q_out, "q_out", T, hq, d, k_cache)
+        qo_ptr = q_out.data_ptr()
+    k_out = _token_out(k_out, "k_out", T, hkv, d, k_cache)
+    pos_ptr = None
     if cos_sin is not None:
-        _need(cos_sin, torch.float32, "cos_sin")
-        if cos_sin.dim() != 2 or cos_sin.device != dev:
-            raise PkvError("cos_sin must be [max_pos, n] on the cache's device")
-        rope = _lib.PkvRope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(rope_offset),
-                            1 if interleaved else 0)
-        need.append((positions, torch.int64, "positions"))
-    for t, dtype, n in need:
-        _need(t, dtype, n)
-        if t.numel() != T or t.device != dev:
-            raise PkvError(f"{n} must have {T} entries on the cache's device")
-    if q is not None and q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
-    if k_out is None:
-        k_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=dev)
-    for t, h, n in ((q_out, hq, "q_out"), (k_out, hkv, "k_out")):
-        if t is not None:
-            _need(t, torch.bfloat16, n)
-            if tuple(t.shape) != (T, h, d) or t.device != dev:
-                raise PkvError(f"{n} must be [{T}, {h}, {d}] on the cache's device")
-    _check(lib.pkv_kv_append(_ptr(q), q_stride, _ptr(key), k_stride, _ptr(value), v_stride,
-                             _ptr(positions) if cos_sin is not None else None, _ptr(slot_mapping), T, hq, rope, cache,
-                             _ptr(q_out) if q is not None else None, _ptr(k_out), _stream(stream)), "kv_append")
+        if not cos_sin.is_cuda or cos_sin.get_device() != dev or cos_sin.dtype is not torch.float32 \
+                or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise PkvError("cos_sin must be contiguous fp32 [max_pos, n] on the cache's device")
+        rows, n = cos_sin.shape
+        rope = _lib.PkvRope(cos_sin.data_ptr(), rows, n, int(rope_offset), 1 if interleaved else 0)
+        pos_ptr = _token_index(positions, "positions", T, dev)
+    else:
+        rope = _lib.PkvRope(None, 0, 0, 0, 0)
+    slots = _token_index(slot_mapping, "slot_mapping", T, dev)
+    _check(lib.pkv_kv_append(q_ptr, q_stride, key.data_ptr(), k_stride, v_ptr, v_stride, pos_ptr, slots, T, hq, rope,
+                             cache, qo_ptr, k_out.data_ptr(), _stream(stream)), "kv_append")
     return q_out, k_out
 
 
