@@ -93,6 +93,20 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int heads, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// TMA map over q [rows, heads, D] (bf16) for packed query tiles: dims (64, D/64, heads, rows), box 64 x 1 x
+// group x 128/group, 128-byte swizzle. One box = one 64-wide half of the group's heads of 128 / group tokens.
+bool encode_packed_q(CUtensorMap* m, const void* base, int64_t rows, int heads, int group, int D) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(D / 64), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[3] = {128, static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(heads) * D * 2};
+  cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group)};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // TMA map over one paged cache tensor: dims (64, Hkv*D/64, block_size, num_blocks), box
 // 64 x 1 x block_size x 1 (one 64-wide half of one head of one block), 128-byte swizzle.
 bool encode_cache(CUtensorMap* m, const void* base, const pkv_cache& c) {
@@ -721,7 +735,9 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   CUtensorMap tq, tk, tv, tck, tcv, tqf;
   std::memset(&tck, 0, sizeof tck);
   std::memset(&tcv, 0, sizeof tcv);
-  if (!encode_rows(&tq, q, num_tokens, Hq, D, 128) || !encode_rows(&tk, k, num_tokens, Hkv, D, 128) ||
+  const bool packed = ctx_kind == kAttnCtxBlock;
+  if (!(packed ? encode_packed_q(&tq, q, num_tokens, Hq, p.G, D) : encode_rows(&tq, q, num_tokens, Hq, D, 128)) ||
+      !encode_rows(&tk, k, num_tokens, Hkv, D, 128) ||
       !encode_rows(&tv, v, num_tokens, Hkv, D, 128) || !encode_rows(&tqf, q, num_tokens * Hq, 1, D, 128))
     return PKV_ERR_CUDA;
   if (cache != nullptr &&
@@ -731,8 +747,9 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   for (int32_t off = 0; off < reqs.max_reqs && st == PKV_OK; off += kAttnSetChunk) {
     p.set_offset = off;
     p.sched_slot = next_sched_slot();
-    st = cuda_status(launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
-                                      reinterpret_cast<cudaStream_t>(stream), &launches));
+    st = cuda_status(packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, reinterpret_cast<cudaStream_t>(stream), &launches)
+                            : launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
+                                               reinterpret_cast<cudaStream_t>(stream), &launches));
   }
   t_launches += launches;
   return st;

@@ -1,0 +1,849 @@
+// attn_scaled.cu — extend_attn over a block-scaled E4M3 cache (an fp32 scale for each 16-token block
+// and KV head) on the tcgen05 tensor cores: several new tokens a request against their cached
+// context and causally against themselves (vLLM blog "rocm-attention-backend", "Processing
+// details: extend path").
+//
+// Mathematics. For a query row, context positions j of block b with E4M3 values k_j, v_j, and new
+// tokens i with bf16 k_i, v_i:
+//   u_j = log2(e) scale ks_b (q . k_j) + log2 vs_b,   u_i = log2(e) scale (q . k_i),
+//   m the running max of u,  P = 2^(u - m),
+//   O = sum_j P_j v_j + sum_i P_i v_i,   l = sum_j P_j / vs_b + sum_i P_i,
+//   out = O / l,   lse = (m + log2 l) ln 2.
+// The tensor core multiplies the E4M3 values themselves, exact in fp16, and the softmax applies both
+// scales in fp32, where nothing is rounded to few bits. Taking the max over u rather than over the
+// scores keeps P within [0, 2^8] whatever the scales, and costs nothing per column: the shift of the
+// exponent and the factor of the sum are the block's. (Rounding scale * code to bf16 in the
+// converter warps, the first form, put 2^-8 of each product into the exponent and of each value into
+// the sum, and its conversions, 9 instructions for a pair of codes against 2, took 2.5 times as long:
+// 5.7 ms against 2.3 on 8 x 512 tokens over contexts of 4K to 32K, Hq 64 / Hkv 8.)
+// Queries and new keys become fp16 and must lie within its range; new values and their P stay bf16,
+// so values of any size pass.
+//
+// Work items. The rows of a request for one KV head are its (token, query head of the group) pairs,
+// tokens outermost, in tiles of 128 (a box of Q is G heads x 128 / G tokens). An item is two such
+// tiles, one a head slot: a KV head's context is read once for 256 rows whatever G is, and a draft
+// of 4 tokens at G = 8 is one tile of 32 rows where items of a token tile and a head pair would be
+// four, with 4 rows used of 128 (32 x 4 tokens over 1K-4K: 385 us so, 95 packed). An item whose
+// rows fit one tile splits its key tiles between the slots instead (even ones to slot 0, odd ones to
+// slot 1, both on the one Q tile) and the two states are merged at the end, so both softmax
+// warpgroups work on a request of few tokens. Items are claimed from a counter, heaviest first: with
+// 256 rows an item they are few and long, and a static deal in snake order lost more to the spread
+// of the last round (8 x 512: 2.42 ms against 2.09; 2048 over 100K: 7.45 against 6.35).
+//
+// Roles (12 warps, one CTA per SM, persistent):
+//   warps 0-3, 4-7  softmax of slot 0, 1 (thread t owns row t = TMEM lane t) and the epilogue
+//   warp 8          TMA producer: claims the items, loads Q and the ring of K and V tiles (128 keys)
+//   warp 9          MMA issuer (one thread, which also does its waits: as a whole warp with votes
+//                   around each of them 2.30 ms against 2.18): S = Q K^T, O += P V (P read from
+//                   tensor memory)
+//   warps 10-11     converters: E4M3 code tiles, Q and new keys to fp16 in shared memory, two rows a
+//                   thread (four warps convert faster but slow the products, whose operands they
+//                   compete with for shared memory; and unrolled loops over the rows and over K and V
+//                   measured 2.18 ms against 2.02 on the 8 x 512 tokens)
+// Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; P_s overwrites the first half of S_s.
+#include <math_constants.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "launch.h"
+#include "softmax.cuh"
+#include "tc.cuh"
+
+namespace pkv {
+
+namespace {
+
+struct AsCfg {
+  static constexpr int D = 128, BN = 128, BS = 16, TBLK = BN / BS;
+  static constexpr int HALF_BYTES = 128 * 128;       // 128 rows x 128 bytes
+  static constexpr int TILE_BYTES = 2 * HALF_BYTES;  // one 128-row tile of Q, K or V in 16 bits
+  static constexpr int NBUF = 4;                     // K/V ring: one tile per buffer
+  static constexpr int MAXR = kAttnSetChunk;         // requests of the set one launch holds
+  static constexpr int W_LOAD = 8, W_MMA = 9, W_CONV = 10, NCONV = 2, WARPS = 12;
+  static constexpr int THREADS = WARPS * 32;
+  // launched at 168 registers a thread; the softmax warpgroups hold a whole row of S and take more,
+  // the third warpgroup gives them up
+  static constexpr int REGS_SOFTMAX = 192, REGS_OTHER = 120;
+  static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER == THREADS * 168, "register split");
+  static constexpr int RING_OFF = 2 * TILE_BYTES;
+  static constexpr int REQ_OFF = RING_OFF + NBUF * TILE_BYTES;  // int4 {r, row0, q_len, C}
+  static constexpr int START_OFF = REQ_OFF + MAXR * 16;
+  static constexpr int PERM_OFF = START_OFF + (MAXR + 2) * 4;   // set positions by cost, heaviest first
+  // output staging: per softmax warp, 32 rows x 32 bf16 columns (64-byte rows, 64-byte swizzle)
+  static constexpr int STAGE_OFF = (PERM_OFF + MAXR * 4 + 127) / 128 * 128;
+  static constexpr int STAGE_WARP_BYTES = 32 * 64;
+  static constexpr int ITEM_RING = 4;                // claimed items published to the other roles
+  static constexpr int ITEM_READERS = 1 + 8 + NCONV;
+  static constexpr int ITEM_OFF = STAGE_OFF + 8 * STAGE_WARP_BYTES;
+  // key tile k of the CTA in slot k % SCALE_RING: the blocks' scales as they land (8 of K, 8 of V), and
+  // what the softmax makes of them ({key scale * softmax scale, log2 of the value scale, its inverse,
+  // -} a block). Slot k is written again for tile k + 4, whose K is loaded once S of tile k + 2 is
+  // done, which needs P of tile k + 1 (of tile k, in a split item): every reader is past tile k.
+  static constexpr int SCALE_RING = 4;
+  static constexpr int SCALE_OFF = (ITEM_OFF + ITEM_RING * 8 + 15) / 16 * 16;
+  static constexpr int FACTOR_OFF = SCALE_OFF + SCALE_RING * 2 * TBLK * 4;
+  static constexpr int MERGE_OFF = FACTOR_OFF + SCALE_RING * TBLK * 16;  // slot 1's {m, l} by row (split items)
+  static constexpr int BAR_OFF = MERGE_OFF + 128 * 8;
+  static constexpr uint32_t IDESC_QK = tc::idesc_f16(128, 128, 0, 0);
+  static constexpr uint32_t IDESC_PV = tc::idesc_f16(128, D, 0, 1), IDESC_PV_NEW = tc::idesc_bf16(128, D, 0, 1);
+};
+struct AsBars {
+  uint64_t q_full, q_empty, q_conv;
+  uint64_t kv_full[AsCfg::NBUF], kv_empty[AsCfg::NBUF], conv_full[AsCfg::NBUF];
+  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t item_full[AsCfg::ITEM_RING], item_empty[AsCfg::ITEM_RING];
+  uint64_t drained;                 // the products in flight when a role gave up
+  uint64_t merge_full, merge_done;  // slot 1's m and l are in shared memory; slot 0 has read them and O_1
+};
+constexpr int kAsSmem = 1024 + AsCfg::BAR_OFF + static_cast<int>(sizeof(AsBars));
+static_assert(kAsSmem <= 226 * 1024, "shared memory");
+
+__device__ __forceinline__ constexpr uint32_t as_scol(int slot) { return slot * 128u; }
+__device__ __forceinline__ constexpr uint32_t as_ocol(int slot) { return 256u + slot * 128u; }
+
+struct AsItem {
+  int r, q_len, C;      // request, new tokens, cached tokens
+  int kh;               // KV head
+  int base;             // first of the item's rows (rows of the request: token * G + head of the group)
+  int split;            // 1: one tile of rows, key tiles dealt to the two slots
+  int nct, NT;          // context key tiles, all key tiles
+  int64_t row0;         // the request's first row of q
+};
+__device__ __forceinline__ int as_pairs(const int4& q, int G) { return (q.z * G + 255) / 256; }
+// Key tiles an item of the request walks at most: the schedule's order.
+__device__ __forceinline__ int as_cost(const int4& q) { return (q.w + 127) / 128 + (q.z + 127) / 128; }
+
+// Work item w: s_req holds {request id, first query row, q_len, cached tokens} of each request of the
+// set, s_perm the set positions by decreasing cost, s_start the prefix of items in that order.
+__device__ __forceinline__ AsItem as_item(const AttnParams& p, const int* s_start, const int4* s_req, const int* s_perm,
+                                          int n, int w) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_start[mid] <= w) lo = mid; else hi = mid - 1;
+  }
+  const int4 q = s_req[s_perm[lo]];
+  const int idx = w - s_start[lo];
+  AsItem it;
+  it.r = q.x;
+  it.row0 = q.y;
+  it.q_len = q.z;
+  it.C = q.w;
+  it.kh = idx % p.Hkv;
+  it.base = 256 * (as_pairs(q, p.G) - 1 - idx / p.Hkv);  // later (heavier) rows of a request first
+  const int rows = min(256, q.z * p.G - it.base);
+  it.split = rows <= 128;
+  it.nct = (it.C + 127) / 128;
+  it.NT = it.nct + (it.base + rows - 1) / p.G / 128 + 1;
+  return it;
+}
+
+// Counters of claimed items and of finished CTAs; launch k uses slot k % kAttnSchedSlots and its last
+// CTA to finish sets the slot back to zero.
+__device__ unsigned int g_as_next[kAttnSchedSlots];
+__device__ unsigned int g_as_done[kAttnSchedSlots];
+
+// Bounded wait that also gives up as soon as another role has given up; the same answer in all lanes.
+__device__ __forceinline__ bool as_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+      if ((ok = mbar_try_wait(bar, parity))) break;
+      if ((i & 63u) == 0) {
+        if (*abort_flag) break;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          flag_error(err, PKV_DEVERR_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The same by one thread.
+__device__ __forceinline__ bool as_wait1(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        flag_error(err, PKV_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// The k-th work item (-1: no more, or a wait gave up). Lane 0 reads the entry and frees it.
+__device__ __forceinline__ int as_take(const int* s_item, AsBars& bar, uint32_t k, volatile int* abort_flag,
+                                       unsigned int* err, int lane) {
+  const int e = static_cast<int>(k % AsCfg::ITEM_RING);
+  if (!as_wait(&bar.item_full[e], (k / AsCfg::ITEM_RING) & 1, abort_flag, err)) return -1;
+  int w = 0;
+  if (lane == 0) {
+    w = *reinterpret_cast<const volatile int*>(&s_item[e]);
+    mbar_arrive(&bar.item_empty[e]);
+  }
+  return __shfl_sync(0xffffffffu, w, 0);
+}
+
+__device__ __forceinline__ int as_take1(const int* s_item, AsBars& bar, uint32_t k, volatile int* abort_flag, unsigned int* err) {
+  const int e = static_cast<int>(k % AsCfg::ITEM_RING);
+  if (!as_wait1(&bar.item_full[e], (k / AsCfg::ITEM_RING) & 1, abort_flag, err)) return -1;
+  const int w = *reinterpret_cast<const volatile int*>(&s_item[e]);
+  mbar_arrive(&bar.item_empty[e]);
+  return w;
+}
+
+// ---- conversions ------------------------------------------------------------------------------------
+// A K or V tile buffer is [2 halves][128 rows][128 B] (64 16-bit values of a row per half, 128-byte
+// swizzle: 16-byte chunk q of row R at R * 128 + ((q ^ (R & 7)) << 4)). A context tile lands as
+// codes, [128 rows][128 B] with the same swizzle, in the buffer's upper half: code row R lies exactly
+// where fp16 row R of half 1 goes, and half 0 holds no codes, so a thread converts its own row in
+// place: dims 0..63 into half 0, then dims 64..127, all read first, over the codes.
+__device__ __forceinline__ void as_conv_codes(uint32_t tile, int R, bool keep) {
+  uint4 c[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) c[q] = ld_shared_v4(tile + 16384u + R * 128 + ((q ^ (R & 7)) << 4));
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {  // 16 codes: two 16-byte chunks of fp16
+    uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
+    if (keep) {
+      a = make_uint4(e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].x)), e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].x >> 16)),
+                     e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].y)), e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].y >> 16)));
+      b = make_uint4(e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].z)), e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].z >> 16)),
+                     e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].w)), e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].w >> 16)));
+    }
+    const uint32_t base = tile + (q >> 2) * 16384u + R * 128;
+    st_shared_v4(base + (((2 * (q & 3)) ^ (R & 7)) << 4), a);
+    st_shared_v4(base + (((2 * (q & 3) + 1) ^ (R & 7)) << 4), b);
+  }
+}
+// bf16 row R of a tile -> fp16 in place.
+__device__ __forceinline__ void as_conv_bf16(uint32_t tile, int R) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint32_t a = tile + h * 16384u + R * 128 + (q << 4);  // in place: any chunk order will do
+      const uint4 v = ld_shared_v4(a);
+      st_shared_v4(a, make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w)));
+    }
+}
+__device__ __forceinline__ void as_zero_row(uint32_t tile, int R) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) st_shared_v4(tile + h * 16384u + R * 128 + (q << 4), make_uint4(0, 0, 0, 0));
+}
+
+// Columns n .. 31 of a 32-column chunk of S (raw fp32 bits) become -inf, so that whatever the tensor
+// core wrote there never enters the arithmetic.
+__device__ __forceinline__ void as_mask(uint32_t (&v)[32], int n) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = e < n ? v[e] : 0xFF800000u;
+}
+
+__global__ void __launch_bounds__(AsCfg::THREADS, 1)
+    attn_scaled_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ck,
+                       const __grid_constant__ CUtensorMap tm_cv) {
+  using C = AsCfg;
+  constexpr int D = C::D;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                  // [slot][half][128][128 B]
+  uint8_t* ring = smem + C::RING_OFF;  // [NBUF][half][128][128 B]
+  int* s_start = reinterpret_cast<int*>(smem + C::START_OFF);
+  int* s_perm = reinterpret_cast<int*>(smem + C::PERM_OFF);
+  int4* s_req = reinterpret_cast<int4*>(smem + C::REQ_OFF);
+  int* s_item = reinterpret_cast<int*>(smem + C::ITEM_OFF);
+  AsBars& bar = *reinterpret_cast<AsBars*>(smem + C::BAR_OFF);
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ int s_scan[C::WARPS];
+
+  pdl_wait();
+  pdl_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // this launch's chunk of the request set
+  int begin = 0, n = p.max_reqs;
+  if (p.bounds != nullptr) {
+    begin = p.bounds[p.cls];
+    n = p.bounds[p.cls + 1] - begin;
+    if (n > p.max_reqs) {
+      if (blockIdx.x == 0 && tid == 0) flag_error(p.err, PKV_DEVERR_REQS);
+      n = p.max_reqs;
+    }
+    n = max(n, 0);
+  }
+  begin += p.set_offset;
+  n = max(0, min(n - p.set_offset, C::MAXR));
+
+  if (tid == 0) {
+    mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.q_empty, 1);
+    mbar_init(&bar.q_conv, C::NCONV);
+    for (int b = 0; b < C::NBUF; ++b) {
+      mbar_init(&bar.kv_full[b], 1 + C::TBLK);  // the producer's bytes, and each block's scales
+      mbar_init(&bar.kv_empty[b], 1);
+      mbar_init(&bar.conv_full[b], C::NCONV);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 128);
+      mbar_init(&bar.o_final[i], 1);
+    }
+    for (int i = 0; i < C::ITEM_RING; ++i) {
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_empty[i], C::ITEM_READERS);
+    }
+    mbar_init(&bar.drained, 1);
+    mbar_init(&bar.merge_full, 128);
+    mbar_init(&bar.merge_done, 128);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::W_MMA) tc::tmem_alloc(&s_tmem, 512);
+
+  // the set's requests
+  for (int i = tid; i < n; i += C::THREADS) {
+    const int r = p.order ? p.order[begin + i] : begin + i;
+    int4 q = make_int4(0, 0, 0, 0);
+    if (r >= 0 && r < p.batch_reqs) {
+      const int q_len = max(0, p.cu_q[r + 1] - p.cu_q[r]);
+      int c = max(0, p.seq_lens[r] - q_len);
+      if (c > static_cast<int64_t>(p.max_blocks) * C::BS) {
+        if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_LEN);
+        c = p.max_blocks * C::BS;
+      }
+      q = make_int4(r, p.cu_q[r], q_len, c);
+    } else if (blockIdx.x == 0) {
+      flag_error(p.err, PKV_DEVERR_REQS);
+    }
+    s_req[i] = q;
+  }
+  __syncthreads();
+  // rank by cost, heaviest first, ties in set order (a stable order every CTA computes alike)
+  for (int i = tid; i < n; i += C::THREADS) {
+    const int ki = as_cost(s_req[i]);
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const int kj = as_cost(s_req[j]);
+      rank += (kj > ki || (kj == ki && j < i)) ? 1 : 0;
+    }
+    s_perm[rank] = i;
+  }
+  __syncthreads();
+  // exclusive prefix of the requests' items in that order (n <= MAXR <= THREADS)
+  static_assert(C::MAXR <= C::THREADS, "one request a thread");
+  {
+    const int t = tid < n ? p.Hkv * as_pairs(s_req[s_perm[tid]], p.G) : 0;
+    int x = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) x += s_scan[w];
+    if (tid < n) s_start[tid] = x - t;
+    if (tid == C::THREADS - 1) s_start[n] = x;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  const int W = s_start[n];
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+    // ======================= softmax warpgroups =======================
+    const int slot = warp >> 2;
+    const int t = tid & 127;  // row of the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t sc = 0, oc = 0;  // S tiles of this slot; its O's
+    uint32_t tile0 = 0;       // the CTA's key tiles before this item
+    uint32_t par = 0;         // parities of the items whose slot 1 has an O (bit 0), of the merges (bit 1)
+    for (uint32_t k = 0;; ++k) {
+      const int w = as_take(s_item, bar, k, &s_abort, p.err, lane);
+      if (w < 0) break;
+      float m = -CUDART_INF_F, l = 0.f;
+      {
+        const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
+        if (slot == 1 && it.split && it.NT == 1) {  // its one key tile is slot 0's
+          tile0 += it.NT;
+          continue;
+        }
+        const int tok = (it.base + (it.split ? 0 : slot * 128) + t) / p.G;  // this row's token
+        bool ok = true;
+        // a split item's slot walks every other tile, from its own index on
+        for (int j = it.split ? slot : 0; j < it.NT; j += 1 + it.split) {
+          if (!as_wait(&bar.s_full[slot], sc & 1, &s_abort, p.err)) { ok = false; break; }
+          ++sc;
+          tc::fence_after_sync();
+          // valid keys of this row in tile j: columns [0, kv) (context) or causal (new)
+          const bool ctx = j < it.nct;
+          const int kv = ctx ? min(128, it.C - j * 128) : min(128, tok - (j - it.nct) * 128 + 1);
+          const bool full = __all_sync(0xffffffffu, kv >= 128);
+          const uint32_t srow = tmem + lane_off + as_scol(slot);
+          // the whole row of S into registers (four loads, one wait)
+          uint32_t v[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::ld32(srow + c * 32, v[c]);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
+          // the factors of block g of the tile: {key scale * softmax scale, log2 vs, 1 / vs}
+          const float4* fac = reinterpret_cast<const float4*>(smem + C::FACTOR_OFF) + (tile0 + j) % C::SCALE_RING * 8;
+          if (!full) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) as_mask(v[c], kv - c * 32);
+          }
+          // the max of a block's raw scores (its factor is positive), then of the blocks' u
+          float mx = -CUDART_INF_F;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            float mg = -CUDART_INF_F;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)
+              mg = sm::max3(mg, __uint_as_float(v[g / 2][(g & 1) * 16 + e]), __uint_as_float(v[g / 2][(g & 1) * 16 + e + 1]));
+            const float4 f = fac[g];
+            mx = fmaxf(mx, fmaf(mg, f.x, f.y));
+          }
+          float alpha = 1.f;
+          if (mx > m + 8.f || m == -CUDART_INF_F) {  // lazy rescale: only when the max really grows
+            const float m_new = fmaxf(m, mx);
+            if (m_new != -CUDART_INF_F) {
+              alpha = (m == -CUDART_INF_F) ? 0.f : ex2_approx(m - m_new);
+              m = m_new;
+            }
+          }
+          const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+          // P of the 16 columns of block g, packed over the first half of S: fp16 beside the context's
+          // codes, bf16 beside new values; the row sum takes each P over its block's vs
+          uint64_t rs2 = sm::f2(0.f, 0.f);
+          auto exp_pass = [&](auto f16) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int gg = 0; gg < 2; ++gg) {
+                const float4 f = fac[2 * c + gg];
+                const uint64_t sc2 = sm::f2(f.x, f.x), nm2 = sm::f2(neg_m + f.y, neg_m + f.y), iv2 = sm::f2(f.z, f.z);
+#pragma unroll
+                for (int e = 16 * gg; e < 16 * gg + 16; e += 2) {
+                  const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
+                  float x0, x1;
+                  sm::unf2(x, x0, x1);
+                  const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
+                  rs2 = sm::fma2(pp, iv2, rs2);
+                  pk[e / 2] = decltype(f16)::value ? sm::f16x2(pp) : sm::bf16x2(pp);
+                }
+              }
+              tc::st16(srow + c * 16, pk);
+            }
+          };
+          if (ctx) exp_pass(std::true_type{}); else exp_pass(std::false_type{});
+          float r0, r1;
+          sm::unf2(rs2, r0, r1);
+          l = l * alpha + (r0 + r1);
+          // The rescale decision is per row, but tcgen05.ld/st are warp-collective: the whole
+          // warp takes the branch when any of its rows needs it (alpha is 1 for the others).
+          if (j > (it.split ? slot : 0) && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // O of this row is quiescent: the previous P V product finished before S(j) did
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc::ld32(tmem + lane_off + as_ocol(slot) + c * 32, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tc::st32(tmem + lane_off + as_ocol(slot) + c * 32, o);
+            }
+          }
+          tc::wait_st();
+          tc::fence_before_sync();
+          mbar_arrive(&bar.p_full[slot]);
+        }
+        if (!ok) break;
+        tile0 += it.NT;
+      }
+      // ---- epilogue (the item found again, so that its fields need not stay in registers above) ----
+      const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
+      const bool both = it.split && it.NT > 1;  // two states of the same rows
+      float2* mrg = reinterpret_cast<float2*>(smem + C::MERGE_OFF);
+      if (both && slot == 1) {
+        // slot 0 merges the two states and writes the rows
+        mrg[t] = make_float2(m, l);
+        mbar_arrive(&bar.merge_full);
+        if (!as_wait(&bar.merge_done, (par >> 1) & 1, &s_abort, p.err)) break;
+        par ^= 2;
+        ++oc;
+        continue;
+      }
+      if (!as_wait(&bar.o_final[slot], oc & 1, &s_abort, p.err)) break;
+      ++oc;
+      float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and of slot 1's
+      if (both) {
+        if (!as_wait(&bar.o_final[1], par & 1, &s_abort, p.err) || !as_wait(&bar.merge_full, (par >> 1) & 1, &s_abort, p.err))
+          break;
+        par ^= 2;
+        const float2 o1 = mrg[t];
+        const float mm = fmaxf(m, o1.x);
+        w0 = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mm);
+        w1 = o1.x == -CUDART_INF_F ? 0.f : ex2_approx(o1.x - mm);
+        l = l * w0 + o1.y * w1;
+        m = mm;
+      }
+      if (both || !it.split) par ^= 1;
+      tc::fence_after_sync();
+      const int base = it.base + (it.split ? 0 : slot * 128);  // the tile's first row of the request
+      // flat row of [T * Hq] of tile row tr, or -1 for a row that is not there
+      auto flat_row = [&](int tr) -> int64_t {
+        const int rr = base + tr, tok = rr / p.G;
+        return tok < it.q_len && it.row0 + tok < p.num_tokens ? (it.row0 + tok) * p.Hq + it.kh * p.G + rr % p.G : -1;
+      };
+      const float inv = l > 0.f ? w0 / l : 0.f, inv1 = l > 0.f ? w1 / l : 0.f;
+      // O leaves through the warp's staging tile (32 rows x 32 columns at a time): each thread puts
+      // its row there, then every store instruction writes 8 rows x 64 contiguous bytes
+      uint32_t tid_now;
+      asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid_now));
+      const uint32_t stg = ((smem_u32(smem_raw) + 1023u) & ~1023u) + C::STAGE_OFF + (tid_now >> 5) * C::STAGE_WARP_BYTES;
+      const int wrow0 = static_cast<int>(tid_now & 96u);  // the warp's first row of the tile
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tc::ld32(tmem + lane_off + as_ocol(slot) + c * 32, o);
+        tc::wait_ld();
+        tc::touch32(o);
+        if (both) {
+          uint32_t o1[32];
+          tc::ld32(tmem + lane_off + as_ocol(1) + c * 32, o1);
+          tc::wait_ld();
+          tc::touch32(o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), inv1, __uint_as_float(o[e]) * inv));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+        }
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint4 x;
+          x.x = pack_bf16(__uint_as_float(o[q4 * 8 + 0]), __uint_as_float(o[q4 * 8 + 1]));
+          x.y = pack_bf16(__uint_as_float(o[q4 * 8 + 2]), __uint_as_float(o[q4 * 8 + 3]));
+          x.z = pack_bf16(__uint_as_float(o[q4 * 8 + 4]), __uint_as_float(o[q4 * 8 + 5]));
+          x.w = pack_bf16(__uint_as_float(o[q4 * 8 + 6]), __uint_as_float(o[q4 * 8 + 7]));
+          // 16-byte chunk q4 of row `lane`, 64-byte swizzle: conflict-free both ways
+          st_shared_v4(stg + lane * 64 + ((q4 ^ ((lane >> 1) & 3)) << 4), x);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 2), kk = lane & 3;  // row of the warp's 32, 16-byte chunk
+          const uint4 x = ld_shared_v4(stg + rr * 64 + ((kk ^ ((rr >> 1) & 3)) << 4));
+          const int64_t fr = flat_row(wrow0 + rr);
+          if (fr >= 0) *reinterpret_cast<uint4*>(p.out + fr * D + c * 32 + kk * 8) = x;
+        }
+        __syncwarp();
+      }
+      tc::fence_before_sync();
+      if (both) mbar_arrive(&bar.merge_done);
+      if (p.lse) {
+        const int64_t fr = flat_row(t);
+        if (fr >= 0) p.lse[fr] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+    if (warp == C::W_LOAD) {
+      // ======================= TMA producer =======================
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tm_ck);
+        tma_prefetch_desc(&tm_cv);
+      }
+      uint32_t kvc = 0;
+      bool ok = true;
+      for (uint32_t items = 0; ok; ++items) {
+        // take the next item once the Q buffer is free, and publish it to the other roles
+        if (items > 0 && !as_wait(&bar.q_empty, (items - 1) & 1, &s_abort, p.err)) break;
+        const int e = static_cast<int>(items % C::ITEM_RING);
+        if (items >= C::ITEM_RING && !as_wait(&bar.item_empty[e], (items / C::ITEM_RING - 1) & 1, &s_abort, p.err)) break;
+        int w = 0;
+        if (lane == 0) {
+          w = static_cast<int>(atomicAdd(&g_as_next[p.sched_slot], 1u));
+          if (w >= W) w = -1;
+          *reinterpret_cast<volatile int*>(&s_item[e]) = w;
+          mbar_arrive(&bar.item_full[e]);
+        }
+        w = __shfl_sync(0xffffffffu, w, 0);
+        if (w < 0) break;
+        const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
+        if (lane == 0) {
+          const int nq = it.split ? 1 : 2;
+          mbar_arrive_expect_tx(&bar.q_full, nq * C::TILE_BYTES);
+          for (int s = 0; s < nq; ++s)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+              tma_load_4d(sQ + s * C::TILE_BYTES + hf * C::HALF_BYTES, &tm_q, &bar.q_full, 0, hf, it.kh * p.G,
+                          static_cast<int>(it.row0) + (it.base + s * 128) / p.G);
+        }
+        const int32_t* table = p.block_tables + static_cast<int64_t>(it.r) * p.max_blocks;
+        const int ctx_blocks = (it.C + 15) / 16;
+        // a tile's table entries (lanes 0..7, a block each) are read a tile ahead: the loads are on a
+        // split item's critical path
+        auto entry = [&](int j) {
+          const int lb = j * 8 + lane;
+          return j < it.nct && lane < 8 ? table[lb < ctx_blocks ? lb : j * 8] : 0;
+        };
+        int next = entry(0);
+        for (int j = 0; j < it.NT && ok; ++j) {
+          const bool ctx = j < it.nct;
+          int blk = next;
+          if (blk < 0 || blk >= p.num_blocks) {
+            flag_error(p.err, PKV_DEVERR_BLOCK);
+            blk = 0;
+          }
+          next = entry(j + 1);
+#pragma unroll 1
+          for (int sel = 0; sel < 2; ++sel, ++kvc) {
+            const int b = kvc % C::NBUF;
+            if (kvc >= C::NBUF && !as_wait(&bar.kv_empty[b], (kvc / C::NBUF - 1) & 1, &s_abort, p.err)) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = ring + b * C::TILE_BYTES;
+            if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[b], ctx ? C::HALF_BYTES : C::TILE_BYTES);
+            __syncwarp();
+            if (lane < 8) {
+              if (ctx && sel == 0) {  // both scales come with K; kvc / 2 counts the CTA's key tiles
+                const int64_t at = static_cast<int64_t>(blk) * p.Hkv + it.kh;
+                float* dst_sc = reinterpret_cast<float*>(smem + C::SCALE_OFF) + kvc / 2 % C::SCALE_RING * 16 + lane;
+                cp_async4(dst_sc, p.k_scales + at);
+                cp_async4(dst_sc + 8, p.v_scales + at);
+                cp_async_arrive_noinc(&bar.kv_full[b]);
+              } else {
+                mbar_arrive(&bar.kv_full[b]);
+              }
+              // the block's 16 rows of codes into the upper half of the buffer
+              if (ctx) tma_load_4d(dst + C::HALF_BYTES + lane * 2048, sel ? &tm_cv : &tm_ck, &bar.kv_full[b], 0, it.kh, 0, blk);
+            }
+            if (!ctx && lane == 0) {
+              const int row = static_cast<int>(it.row0) + (j - it.nct) * 128;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                tma_load_3d(dst + hf * C::HALF_BYTES, sel ? &tm_v : &tm_k, &bar.kv_full[b], 0, it.kh * 2 + hf, row);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (*const_cast<volatile int*>(&s_abort)) {  // a role gave up: wait (bounded) for the copies still in flight
+        for (uint32_t i = kvc > C::NBUF ? kvc - C::NBUF : 0; i < kvc; ++i)
+          __all_sync(0xffffffffu, mbar_wait(&bar.kv_full[i % C::NBUF], (i / C::NBUF) & 1, p.err));
+        cp_async_wait_all();
+      }
+    } else if (warp == C::W_MMA) {
+      // ======================= MMA issuer =======================
+      if (lane == 0) {
+        uint32_t kvc = 0, pc0 = 0, pc1 = 0;  // K and V tiles before this item; P tiles consumed per slot
+        bool ok = true;
+        const uint64_t q_desc = tc::smem_desc(smem_u32(sQ), 16, 1024), k_desc = tc::smem_desc(smem_u32(ring), 16, 1024);
+        const uint64_t v_desc = tc::smem_desc(smem_u32(ring), C::HALF_BYTES, 1024);
+        auto qk = [&](int slot, int buf, int qtile) {
+          const uint64_t qd = q_desc + qtile * (C::TILE_BYTES >> 4), kd = k_desc + buf * (C::TILE_BYTES >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k / 4) * C::HALF_BYTES + (k % 4) * 32) >> 4;
+            tc::mma_ss(tmem + as_scol(slot), qd + off, kd + off, C::IDESC_QK, k > 0);
+          }
+        };
+        auto pv = [&](int slot, int buf, bool acc, bool ctx) {
+          const uint64_t vd = v_desc + buf * (C::TILE_BYTES >> 4);
+          const uint32_t idesc = ctx ? C::IDESC_PV : C::IDESC_PV_NEW;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc::mma_ts(tmem + as_ocol(slot), tmem + as_scol(slot) + k * 8, vd + ((k * 2048) >> 4), idesc,
+                       (acc || k > 0) ? 1u : 0u);
+        };
+        auto wait_kv = [&](uint32_t h) {
+          if (!as_wait1(&bar.conv_full[h % C::NBUF], (h / C::NBUF) & 1, &s_abort, p.err)) return false;
+          tc::fence_after_sync();
+          return true;
+        };
+        auto wait_p = [&](int slot) {
+          uint32_t& c = slot ? pc1 : pc0;
+          if (!as_wait1(&bar.p_full[slot], c & 1, &s_abort, p.err)) return false;
+          ++c;
+          tc::fence_after_sync();
+          return true;
+        };
+        for (uint32_t items = 0; ok; ++items) {
+          const int w = as_take1(s_item, bar, items, &s_abort, p.err);
+          if (w < 0) break;
+          const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
+          if (!as_wait1(&bar.q_conv, items & 1, &s_abort, p.err)) break;
+          if (it.split) {
+            // key tile j goes to slot j % 2: S(j) and the other slot's O += P V of tile j - 1, whichever has
+            // its operands first (S(j) overwrites P(j - 2), whose product was issued a step before)
+            auto do_s = [&](int j) {
+              const uint32_t kh = kvc + 2 * j;
+              if (!wait_kv(kh)) return false;
+              qk(j & 1, kh % C::NBUF, 0);
+              tc::commit(&bar.s_full[j & 1]);
+              tc::commit(&bar.kv_empty[kh % C::NBUF]);
+              if (j == it.NT - 1) tc::commit(&bar.q_empty);
+              return true;
+            };
+            for (int j = 0; j <= it.NT && ok; ++j) {
+              const uint32_t kh = kvc + 2 * j;
+              const bool now = j < it.NT && (j == 0 || mbar_test(&bar.conv_full[kh % C::NBUF], (kh / C::NBUF) & 1));
+              if (now) ok = do_s(j);
+              if (ok && j > 0) {
+                const int s = (j - 1) & 1;
+                const uint32_t vh = kvc + 2 * j - 1;
+                ok = as_wait1(&bar.conv_full[vh % C::NBUF], (vh / C::NBUF) & 1, &s_abort, p.err) && wait_p(s);
+                if (ok) {
+                  pv(s, vh % C::NBUF, j - 1 >= 2, j - 1 < it.nct);
+                  tc::commit(&bar.kv_empty[vh % C::NBUF]);
+                  if (j - 1 >= it.NT - 2) tc::commit(&bar.o_final[s]);
+                }
+              }
+              if (ok && !now && j < it.NT) ok = do_s(j);
+            }
+          } else {
+            // per key tile: S_0(j), O_1 += P_1 V (j - 1), S_1(j), O_0 += P_0 V (j), so that each softmax
+            // warpgroup works while the tensor core serves the other
+            for (int j = 0; j < it.NT; ++j) {
+              const uint32_t kh = kvc + 2 * j, vh = kh + 1;
+              if (!(ok = wait_kv(kh))) break;
+              qk(0, kh % C::NBUF, 0);
+              tc::commit(&bar.s_full[0]);
+              if (j > 0) {
+                if (!(ok = wait_p(1))) break;
+                pv(1, (vh - 2) % C::NBUF, j - 1 > 0, j - 1 < it.nct);
+                tc::commit(&bar.kv_empty[(vh - 2) % C::NBUF]);
+              }
+              qk(1, kh % C::NBUF, 1);
+              tc::commit(&bar.s_full[1]);
+              tc::commit(&bar.kv_empty[kh % C::NBUF]);
+              if (j == it.NT - 1) tc::commit(&bar.q_empty);
+              if (!(ok = as_wait1(&bar.conv_full[vh % C::NBUF], (vh / C::NBUF) & 1, &s_abort, p.err) && wait_p(0))) break;
+              pv(0, vh % C::NBUF, j > 0, j < it.nct);
+              // slot 0's O is final once this product is done: its epilogue may overlap slot 1's last
+              // softmax and P V
+              if (j == it.NT - 1) tc::commit(&bar.o_final[0]);
+            }
+            if (!ok || !(ok = wait_p(1))) break;
+            const uint32_t vh = kvc + 2 * it.NT - 1;
+            pv(1, vh % C::NBUF, it.NT > 1, it.NT - 1 < it.nct);
+            tc::commit(&bar.kv_empty[vh % C::NBUF]);
+            tc::commit(&bar.o_final[1]);
+          }
+          kvc += 2 * it.NT;
+        }
+        if (!ok) {  // a role gave up: wait (bounded) for the products in flight before the tensor memory goes
+          tc::commit(&bar.drained);
+          mbar_wait(&bar.drained, 0, p.err);
+        }
+      }
+      __syncwarp();
+    } else {
+      // ======================= converters =======================
+      // Thread ct converts rows ct and ct + 64 of every tile: Q once per item, then each K and V tile as it lands.
+      const int ct = tid - C::W_CONV * 32;
+      const uint32_t q_base = smem_u32(sQ), ring_base = smem_u32(ring);
+      uint32_t kvc = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok; ++k) {
+        const int w = as_take(s_item, bar, k, &s_abort, p.err, lane);
+        if (w < 0) break;
+        const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
+        if (!as_wait(&bar.q_full, k & 1, &s_abort, p.err)) break;
+        for (int s = 0; s < (it.split ? 1 : 2); ++s) {
+          as_conv_bf16(q_base + s * C::TILE_BYTES, ct);
+          as_conv_bf16(q_base + s * C::TILE_BYTES, ct + 64);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.q_conv);
+        for (int j = 0; j < it.NT && ok; ++j) {
+#pragma unroll 1
+          for (int sel = 0; sel < 2; ++sel, ++kvc) {
+            const int b = kvc % C::NBUF;
+            if (!as_wait(&bar.kv_full[b], (kvc / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
+            const uint32_t tile = ring_base + b * C::TILE_BYTES;
+            if (sel == 0 && ct < 8) {
+              // the tile's softmax factors of block ct
+              const uint32_t at = kvc / 2 % C::SCALE_RING;
+              float4 f = make_float4(p.scale_log2, 0.f, 1.f, 0.f);
+              if (j < it.nct) {
+                const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + at * 16;
+                // a zero scale counts as 2^-100: no logarithm of 0, no product of 0 and a masked -inf
+                const float ks = fmaxf(sc[ct], 0x1p-100f), vs = fmaxf(sc[8 + ct], 0x1p-100f);
+                f = make_float4(ks * p.scale_log2, __log2f(vs), 1.f / vs, 0.f);
+              }
+              reinterpret_cast<float4*>(smem + C::FACTOR_OFF)[at * 8 + ct] = f;
+            }
+#pragma unroll 1
+            for (int R = ct; R < 128; R += 64) {
+              if (j < it.nct) {
+                // V rows past the context's end become zeros (P = 0 there must not meet a NaN code)
+                as_conv_codes(tile, R, sel == 0 || R < it.C - j * 128);
+              } else if (sel == 0) {
+                as_conv_bf16(tile, R);
+              } else if (R >= it.q_len - (j - it.nct) * 128) {
+                // new values stay as they come, but for rows past the request's own tokens
+                as_zero_row(tile, R);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.conv_full[b]);
+          }
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == C::W_MMA) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+  // every role of this CTA is done, its producer's claims included: the launch's last CTA to get here
+  // sets the scheduler slot back to zero for the next launch that uses it
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(&g_as_done[p.sched_slot], 1u) == gridDim.x - 1) {
+      atomicExch(&g_as_next[p.sched_slot], 0u);
+      atomicExch(&g_as_done[p.sched_slot], 0u);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_scaled(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream, int* launches) {
+  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attn_scaled_kernel), kAsSmem, kAttrAttn128Block);
+  if (e != cudaSuccess) return e;
+  *launches += 1;
+  return launch_pdl(attn_scaled_kernel, dim3(num_sms()), dim3(AsCfg::THREADS), kAsSmem, stream, p, tq, tk, tv, tck, tcv);
+}
+
+}  // namespace pkv

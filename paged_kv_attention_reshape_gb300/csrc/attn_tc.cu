@@ -43,18 +43,14 @@ namespace pkv {
 // Kinds of cached context the kernel reads (the bf16 kernel is kind 0):
 //   kCtxBf16    a bf16 cache;
 //   kCtxPool    a bf16 pool holding the E4M3 values of an FP8 cache (gathered beforehand);
-//   kCtxFp8     the FP8 cache's E4M3 codes themselves, converted in shared memory as they land;
-//   kCtxBlock   the same for a cache with a scale for each block and head.
-constexpr int kCtxBf16 = kAttnCtxBf16, kCtxPool = kAttnCtxPool, kCtxFp8 = kAttnCtxFp8, kCtxBlock = kAttnCtxBlock;
+//   kCtxFp8     the FP8 cache's E4M3 codes themselves, converted in shared memory as they land.
+constexpr int kCtxBf16 = kAttnCtxBf16, kCtxPool = kAttnCtxPool, kCtxFp8 = kAttnCtxFp8;
 
 template <int D, int KIND = kCtxBf16>
 struct TcCfg {
   static constexpr int BM = 128, BN = 128, BS = 16;
-  static constexpr bool CONV = KIND == kCtxFp8 || KIND == kCtxBlock;  // converter warps 10 and 11
-  static constexpr bool F16 = CONV;  // the products run on fp16 operands (kCtxBlock: but P V of new tokens)
-  // kCtxBlock: the K and V scales of a context tile's blocks travel with its K tile, two 4-byte
-  // cp.async a block, each block an arrival of its own on the tile's barrier
-  static constexpr int SCALE_ARRIVALS = KIND == kCtxBlock ? BN / BS : 0;
+  static constexpr bool CONV = KIND == kCtxFp8;  // converter warps 10 and 11
+  static constexpr bool F16 = CONV;              // the products run on fp16 operands
   static constexpr int HALVES = D / 64;
   static constexpr int HALF_BYTES = 128 * 128;           // 128 rows x 128 bytes
   static constexpr int TILE_BYTES = HALVES * HALF_BYTES;  // one 128-row tile of Q, K or V
@@ -78,14 +74,7 @@ struct TcCfg {
   static constexpr int STAGE_WARP_BYTES = 32 * 64;
   static constexpr int ITEM_RING = 4;  // claimed work items published to the consumer roles
   static constexpr int ITEM_OFF = STAGE_OFF + 8 * STAGE_WARP_BYTES;
-  // kCtxBlock, key tile k of the CTA in slot k % SCALE_RING: the blocks' scales as they land (8 of K,
-  // 8 of V), and what the softmax makes of them ({key scale * softmax scale, log2 of the value
-  // scale, its inverse, -} a block). Slot k is written again for tile k + 4, whose K is loaded once S of
-  // tile k + 2 is done, which needs P of tile k + 1: every reader is past tile k by then.
-  static constexpr int SCALE_RING = 4;
-  static constexpr int SCALE_OFF = (ITEM_OFF + ITEM_RING * 8 + 15) / 16 * 16;
-  static constexpr int FACTOR_OFF = SCALE_OFF + SCALE_RING * 2 * SCALE_ARRIVALS * 4;
-  static constexpr int BAR_OFF = FACTOR_OFF + SCALE_RING * SCALE_ARRIVALS * 16;
+  static constexpr int BAR_OFF = ITEM_OFF + ITEM_RING * 8;
   // barriers: q_full, q_empty, kv_full[NBUF], kv_empty[NBUF], s_full[2], p_full[2], o_final[2],
   // item_full[ITEM_RING], item_empty[ITEM_RING], q_conv, conv_full[NBUF]
   static constexpr int NBAR = 2 + 2 * NBUF + 6 + 2 * ITEM_RING + 1 + NBUF;
@@ -302,16 +291,7 @@ __device__ __forceinline__ void conv_bf16_row(uint32_t tile, int R, float sc, bo
     }
 }
 
-// Row R of a [halves][128][128 B] tile set to zeros.
-template <int HALVES>
-__device__ __forceinline__ void zero_row(uint32_t tile, int R) {
-#pragma unroll
-  for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) st_shared_v4(tile + h * 16384u + R * 128 + (q << 4), make_uint4(0, 0, 0, 0));
-}
-
-// kCtxPool and kCtxFp8 (SCALED): the cached context holds the E4M3 values of an FP8 cache. The key
+// KIND != kCtxBf16 (SCALED): the cached context holds the E4M3 values of an FP8 cache. The key
 // scale goes with the softmax scale of context tiles. The value scale vs is taken out of the
 // sum instead of multiplied into every context tile's P, so that
 // O = vs * (sum_ctx p code + sum_new p v / vs) / l: for kCtxPool the few new-token tiles pack
@@ -325,19 +305,6 @@ __device__ __forceinline__ void zero_row(uint32_t tile, int R) {
 // core multiplies fp16 operands (kind::f16), P is packed as fp16, and the MMA warp waits on
 // the converters' barriers (q_conv, conv_full) instead of the loads'. Queries, new keys and
 // new values divided by vs must lie within the fp16 range.
-//
-// kCtxBlock: the same pipeline for a cache with scales ks_b, vs_b for each 16-token block b and
-// head. The tensor core multiplies the E4M3 values themselves (exact in fp16) and the softmax
-// applies the scales to a block's 16 columns in fp32, where nothing is rounded to few bits: with
-//   u_j = log2(e) scale ks_b s_j + log2 vs_b,   m the running max of u,
-//   P_j = 2^(u_j - m)  (fp16; O = sum_j P_j v_j),   l = sum_j P_j / vs_b  (fp32),
-// out = O / l and lse = (m + log2 l) ln 2. Taking the max over u rather than over the scores keeps
-// P within [0, 2^8] whatever the scales, and costs nothing per column: the shift of the exponent
-// and the factor of the sum are the block's. (Rounding scale * code to 16 bits in the converters,
-// the first form, put 2^-8 of each product into the exponent or of each value into the sum, and
-// its conversions, 9 instructions for a pair of codes against 2, made the kernel 2.5 times
-// slower.) New tokens have vs = 1; their P and V stay bf16, so values of any size pass; queries
-// and new keys become fp16 and must lie within its range.
 template <int D, int KIND>
 __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kernel(
     const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
@@ -345,7 +312,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
     const __grid_constant__ CUtensorMap tm_ck, const __grid_constant__ CUtensorMap tm_cv,
     const __grid_constant__ CUtensorMap tm_qf) {
   using C = TcCfg<D, KIND>;
-  constexpr bool SCALED = KIND == kCtxPool || KIND == kCtxFp8;
+  constexpr bool SCALED = KIND != kCtxBf16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                  // [slot][half][128][128 B]
@@ -386,7 +353,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int b = 0; b < C::NBUF; ++b) {
-      mbar_init(&kv_full[b], 1 + C::SCALE_ARRIVALS);
+      mbar_init(&kv_full[b], 1);
       mbar_init(&kv_empty[b], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -506,7 +473,6 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
     const int t = tid & 127;  // row of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t sc = 0, oc = 0;
-    uint32_t tile0 = 0;  // kCtxBlock: the CTA's key tiles before this item
     const float lvs = SCALED ? log2f(p.ctx_v_scale) : 0.f;  // new-token tiles' extra shift
     int64_t w_static = blockIdx.x;
     int odd = 0;
@@ -520,10 +486,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       }
       if (w < 0) break;
       const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
-      if (slot >= it.nslot) {
-        if constexpr (KIND == kCtxBlock) tile0 += it.NT;
-        continue;
-      }
+      if (slot >= it.nslot) continue;
       // query index of this row within its request (a packed decode's rows are heads of its one
       // token)
       const int qi = it.dec ? 0 : it.qr0 + t;
@@ -553,61 +516,6 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         tc::wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
-        if constexpr (KIND == kCtxBlock) {
-        // the factors of block g of the tile: {key scale * softmax scale, log2 vs, 1 / vs}
-        const float4* fac = reinterpret_cast<const float4*>(smem + C::FACTOR_OFF) + (tile0 + j) % C::SCALE_RING * 8;
-        // columns past kv become -inf (their p is 0); the max of a block's raw scores, then of the blocks' u
-        if (!full) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mask_cols(v[c], kv - c * 32);
-        }
-        float mx = -CUDART_INF_F;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float mg = -CUDART_INF_F;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            mg = sm::max3(mg, __uint_as_float(v[g / 2][(g & 1) * 16 + e]), __uint_as_float(v[g / 2][(g & 1) * 16 + e + 1]));
-          const float4 f = fac[g];
-          mx = fmaxf(mx, fmaf(mg, f.x, f.y));
-        }
-        if (mx > m + 8.f || m == -CUDART_INF_F) {  // lazy rescale: only when the max really grows
-          const float m_new = fmaxf(m, mx);
-          if (m_new != -CUDART_INF_F) {
-            alpha = (m == -CUDART_INF_F) ? 0.f : ex2_approx(m - m_new);
-            m = m_new;
-          }
-        }
-        const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
-        // P of the 16 columns of block g, packed over the first half of S: fp16 beside the context's
-        // codes, bf16 beside new values; the row sum takes each P over its block's vs
-        uint64_t rs2 = sm::f2(0.f, 0.f);
-        auto exp_pass = [&](auto f16) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int gg = 0; gg < 2; ++gg) {
-              const float4 f = fac[2 * c + gg];
-              const uint64_t sc2 = sm::f2(f.x, f.x), nm2 = sm::f2(neg_m + f.y, neg_m + f.y), iv2 = sm::f2(f.z, f.z);
-#pragma unroll
-              for (int e = 16 * gg; e < 16 * gg + 16; e += 2) {
-                const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
-                float x0, x1;
-                sm::unf2(x, x0, x1);
-                const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
-                rs2 = sm::fma2(pp, iv2, rs2);
-                pk[e / 2] = decltype(f16)::value ? sm::f16x2(pp) : sm::bf16x2(pp);
-              }
-            }
-            tc::st16(srow + c * 16, pk);
-          }
-        };
-        if (ctx) exp_pass(std::true_type{}); else exp_pass(std::false_type{});
-        float r0, r1;
-        sm::unf2(rs2, r0, r1);
-        rs = r0 + r1;
-        } else {
         // row max of the raw scores (the scale is positive, so it commutes with max)
         float mx = -CUDART_INF_F;
         if (full) {
@@ -669,7 +577,6 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             }
             tc::st16(srow + c * 16, pk);
           }
-        }
         }
         } else {
         // pass 1: row max of the raw scores (the scale is positive, so it commutes with max)
@@ -774,7 +681,6 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         mbar_arrive(&p_full[slot]);
       }
       if (!ok) break;
-      if constexpr (KIND == kCtxBlock) tile0 += it.NT;
       if (!tc_wait_warp(&o_final[slot], oc & 1, &s_abort, p.err)) break;
       ++oc;
       tc::fence_after_sync();
@@ -922,17 +828,6 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             if constexpr (C::CONV) {
               // the block's 16 rows of E4M3 codes (128 bytes each) into the upper half of the
               // buffer: rows 16 lane .. 16 lane + 15 of a [128][128 B] code tile
-              if (C::SCALE_ARRIVALS > 0 && lane < 8) {
-                if (kvsel == 0) {  // kvc / 2 counts the CTA's key tiles
-                  const int64_t at = static_cast<int64_t>(blk) * p.Hkv + it.kh;
-                  float* dst_sc = reinterpret_cast<float*>(smem + C::SCALE_OFF) + kvc / 2 % C::SCALE_RING * 16 + lane;
-                  cp_async4(dst_sc, p.k_scales + at);
-                  cp_async4(dst_sc + 8, p.v_scales + at);
-                  cp_async_arrive_noinc(&kv_full[buf]);
-                } else {
-                  mbar_arrive(&kv_full[buf]);
-                }
-              }
               if (lane < 8)
                 tma_load_4d(dst + C::TILE_BYTES / 2 + lane * 2048, kvsel ? &tm_cv : &tm_ck, &kv_full[buf], 0,
                             it.kh, 0, blk);
@@ -942,15 +837,12 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
                 tma_load_4d(dst + hf * C::HALF_BYTES + lane * 2048, kvsel ? &tm_cv : &tm_ck, &kv_full[buf], 0,
                             it.kh * C::HALVES + hf, 0, blk);
             }
-          } else {
-            if (C::SCALE_ARRIVALS > 0 && lane < 8) mbar_arrive(&kv_full[buf]);  // a new-token tile has no scales
-            if (lane == 0) {
-              const int row = static_cast<int>(it.row0) + (j - it.nct) * 128;
+          } else if (lane == 0) {
+            const int row = static_cast<int>(it.row0) + (j - it.nct) * 128;
 #pragma unroll
-              for (int hf = 0; hf < C::HALVES; ++hf)
-                tma_load_3d(dst + hf * C::HALF_BYTES, kvsel ? &tm_v : &tm_k, &kv_full[buf], 0,
-                            it.kh * C::HALVES + hf, row);
-            }
+            for (int hf = 0; hf < C::HALVES; ++hf)
+              tma_load_3d(dst + hf * C::HALF_BYTES, kvsel ? &tm_v : &tm_k, &kv_full[buf], 0,
+                          it.kh * C::HALVES + hf, row);
           }
           __syncwarp();
         }
@@ -970,13 +862,12 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
                    C::IDESC_QK, k > 0);
       }
     };
-    auto pv = [&](int slot, const uint8_t* vbuf, bool acc, bool ctx) {
+    auto pv = [&](int slot, const uint8_t* vbuf, bool acc) {
       const uint32_t vb = smem_u32(vbuf);
-      const uint32_t idesc = KIND == kCtxBlock && !ctx ? tc::idesc_bf16(128, D, 0, 1) : C::IDESC_PV;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         tc::mma_ts(tmem + ocol(slot), tmem + scol(slot) + k * 8,
-                   tc::smem_desc(vb + k * 2048, C::HALF_BYTES, 1024), idesc, (acc || k > 0) ? 1u : 0u);
+                   tc::smem_desc(vb + k * 2048, C::HALF_BYTES, 1024), C::IDESC_PV, (acc || k > 0) ? 1u : 0u);
     };
     int64_t w_static = blockIdx.x;
     int odd = 0;
@@ -1009,7 +900,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
           ++pc1;
           tc::fence_after_sync();
           if (lane == 0) {
-            pv(1, ring + prev_vbuf * C::TILE_BYTES, j - 1 > 0, j - 1 < it.nct);
+            pv(1, ring + prev_vbuf * C::TILE_BYTES, j - 1 > 0);
             tc::commit(&kv_empty[prev_vbuf]);
           }
           __syncwarp();
@@ -1043,7 +934,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         ++pc;
         tc::fence_after_sync();
         if (lane == 0) {
-          pv(0, ring + vbuf * C::TILE_BYTES, j > 0, j < it.nct);
+          pv(0, ring + vbuf * C::TILE_BYTES, j > 0);
           // slot 0's O is final once this product is done: its epilogue may overlap slot 1's
           // last softmax and P V
           if (j == it.NT - 1) tc::commit(&o_final[0]);
@@ -1056,7 +947,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         if (!tc_wait_warp(&p_full[1], pc1 & 1, &s_abort, p.err)) break;
         ++pc1;
         tc::fence_after_sync();
-        if (lane == 0) pv(1, ring + prev_vbuf * C::TILE_BYTES, it.NT - 1 > 0, it.NT - 1 < it.nct);
+        if (lane == 0) pv(1, ring + prev_vbuf * C::TILE_BYTES, it.NT - 1 > 0);
       }
       if (lane == 0) {
         tc::commit(&kv_empty[prev_vbuf]);
@@ -1069,7 +960,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
     // Thread ct converts rows ct and ct + 64 of every tile: Q (both head slots) once per item,
     // then each K and V tile as it lands, in the producer's order.
     const int ct = tid - 320;
-    const float inv_vs = SCALED ? 1.f / p.ctx_v_scale : 1.f;
+    const float inv_vs = 1.f / p.ctx_v_scale;
     const uint32_t q_base = smem_u32(sQ), ring_base = smem_u32(ring);
     uint32_t kvc = 0;
     bool ok = true;
@@ -1098,29 +989,11 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
           const uint32_t use = kvc / C::NBUF;
           if (!tc_wait_warp(&kv_full[buf], use & 1, &s_abort, p.err)) { ok = false; break; }
           const uint32_t tile = ring_base + buf * C::TILE_BYTES;
-          if (KIND == kCtxBlock && kvsel == 0 && ct < 8) {
-            // the tile's softmax factors of block ct
-            const uint32_t at = kvc / 2 % C::SCALE_RING;
-            float4 f = make_float4(p.scale_log2, 0.f, 1.f, 0.f);
-            if (j < it.nct) {
-              const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + at * 16;
-              // a zero scale counts as 2^-100: no logarithm of 0, no product of 0 and a masked -inf
-              const float ks = fmaxf(sc[ct], 0x1p-100f), vs = fmaxf(sc[8 + ct], 0x1p-100f);
-              f = make_float4(ks * p.scale_log2, __log2f(vs), 1.f / vs, 0.f);
-            }
-            reinterpret_cast<float4*>(smem + C::FACTOR_OFF)[at * 8 + ct] = f;
-          }
           if (j < it.nct) {
             // V rows past the context end become zeros (P = 0 there must not meet a NaN code)
             const int valid = kvsel ? it.C - j * 128 : 128;
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) conv_code_row(tile, ct + 64 * rr, ct + 64 * rr < valid);
-          } else if (KIND == kCtxBlock && kvsel) {
-            // new values stay as they come; V rows past the request's own tokens become zeros
-            const int valid = it.q_len - (j - it.nct) * 128;
-#pragma unroll
-            for (int rr = 0; rr < 2; ++rr)
-              if (ct + 64 * rr >= valid) zero_row<C::HALVES>(tile, ct + 64 * rr);
           } else {
             // new-token values are stored divided by vs; V rows past the request's own tokens
             // become zeros
@@ -1159,8 +1032,7 @@ static cudaError_t launch_attention_tc_impl(const AttnParams& p, const CUtensorM
                                             const CUtensorMap& tck, const CUtensorMap& tcv,
                                             const CUtensorMap& tqf, cudaStream_t stream, int* launches) {
   using C = TcCfg<D, KIND>;
-  const int slot = KIND == kCtxFp8     ? kAttrAttn128Fp8
-                   : KIND == kCtxBlock ? kAttrAttn128Block
+  const int slot = KIND == kCtxFp8 ? kAttrAttn128Fp8
                                    : (KIND == kCtxPool ? (D == 64 ? kAttrAttn64Scaled : kAttrAttn128Scaled)
                                                        : (D == 64 ? kAttrAttn64 : kAttrAttn128));
   cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attention_tc_kernel<D, KIND>), C::SMEM, slot);
@@ -1178,10 +1050,6 @@ cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_q, const
   if (ctx_kind == kAttnCtxFp8) {
     if (D != 128) return cudaErrorInvalidValue;
     return launch_attention_tc_impl<128, kCtxFp8>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
-  }
-  if (ctx_kind == kAttnCtxBlock) {
-    if (D != 128) return cudaErrorInvalidValue;
-    return launch_attention_tc_impl<128, kCtxBlock>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
   }
   if (ctx_kind == kAttnCtxPool)
     return D == 64 ? launch_attention_tc_impl<64, kCtxPool>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches)

@@ -208,13 +208,20 @@ cudaError_t launch_mla_decode(const DecodeParams& p, const CUtensorMap& tm, cuda
 size_t mla_workspace_bytes(int Hq);
 size_t mla_workspace_ctr_offset(int Hq);
 // Cached context of the extend kernel: a bf16 cache, a bf16 pool of an FP8 cache's E4M3 values,
-// or the FP8 cache's codes (head_dim 128), converted in the kernel, with tensor or block scales.
-constexpr int kAttnCtxBf16 = 0, kAttnCtxPool = 1, kAttnCtxFp8 = 2, kAttnCtxBlock = 3;
+// or the FP8 cache's codes (head_dim 128), converted in the kernel.
+constexpr int kAttnCtxBf16 = 0, kAttnCtxPool = 1, kAttnCtxFp8 = 2;
 // tm_q over q, tm_k/tm_v over the packed new keys/values, tm_ck/tm_cv over the paged cache
 // (ignored for prefill), tm_qf over q viewed as [T * Hq][D] (one-token requests' heads as rows).
 cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                              const CUtensorMap& tm_v, const CUtensorMap& tm_ck,
                              const CUtensorMap& tm_cv, const CUtensorMap& tm_qf, int D, int ctx_kind,
                              cudaStream_t stream, int* launches);
+
+// Extend over a block-scaled FP8 cache (head_dim 128): tm_q over q as (64, D/64, Hq, T) with boxes of a
+// group's heads (api.cu), the others as for launch_attention.
+constexpr int kAttnCtxBlock = 3;
+cudaError_t launch_attn_scaled(const AttnParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                               const CUtensorMap& tm_v, const CUtensorMap& tm_ck, const CUtensorMap& tm_cv,
+                               cudaStream_t stream, int* launches);
 
 }  // namespace pkv
