@@ -421,7 +421,7 @@ def test_decode_edge_lengths(G, Hkv):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("lens,G,Hkv,qs", [
-    ([5000], 8, 2, 1.0), ([20011], 16, 1, 3.0), ([3000, 1, 2500, 17, 2900] * 3, 4, 4, 1.0), ([777] * 40, 2, 2, 6.0),
+    ([5000], 8, 2, 1.0), ([20011], 16, 1, 3.0), ([40003], 2, 8, 1.0), ([100 + i % 37 for i in range(300)], 1, 8, 2.0), ([3000, 1, 2500, 17, 2900] * 3, 4, 4, 1.0), ([777] * 40, 2, 2, 6.0),
     ([9000, 40], 1, 3, 2.0)])
 def test_decode_long_and_cut_sequences(lens, G, Hkv, qs):
     st = decode_state(lens, G * Hkv, Hkv, seed=len(lens), qs=qs)
