@@ -190,18 +190,18 @@ pkv_status pkv_kv_cache_write(const void* key, const void* value, const int64_t*
  *   a latent cache (bf16, num_kv_heads 1, cache.v NULL or equal to cache.k): value must be NULL,
  *     and only key rows are written (a 576-wide row of mla_decode_attn: 512 latent dims, then
  *     64 dims to rotate: rope.offset 512);
- *   PKV_KV_FP8_E4M3_BLOCK (block_size 16, head_dim 128): the tokens of one block must be
- *     consecutive rows at consecutive slots (a sequence's new tokens are), a "run" of rows
- *     a .. b-1 of the block. For each head, K and V alike, with amax the largest finite magnitude
- *     of the run and need = 2^ceil(log2(amax / 448)), clamped to [2^-64, 2^120] (2^-64 for an
- *     all-zero run):
- *       a == 0: the block starts afresh, its scale becomes need (its old codes and scale are
- *         not read);
+ *   PKV_KV_FP8_E4M3_BLOCK (block_size 16, head_dim 128): the tokens of one block must lie within
+ *     16 consecutive rows of the call (a sequence's new tokens do; padding rows may lie between
+ *     them) and are a "run", of rows a and up of the block. For each head, K and V alike, with
+ *     amax the largest finite magnitude of the run and need = 2^ceil(log2(amax / 448)), clamped
+ *     to [2^-64, 2^120] (2^-64 for an all-zero run):
+ *       a == 0: the block starts afresh, its scale becomes need (its old codes and scale do
+ *         not count);
  *       a > 0:  its scale becomes max(scale, need); when that grows, the codes of rows
  *         0 .. a-1 are rewritten for it (E4M3(e4m3(code) * (old / new)): exact for
  *         power-of-two scales but for codes that fall below E4M3's smallest steps).
- *     The run's codes are E4M3(x * (1.0f / scale)). Rows b and up are left as they were. Two runs
- *     of one call in the same block race (undefined codes and scale within that block).
+ *     The run's codes are E4M3(x * (1.0f / scale)). The block's other rows are left as they were.
+ *     Tokens of one block that lie further apart leave that block's codes and scale undefined.
  * q: bf16, q_stride elements between tokens, each [num_q_heads, head_dim]; key and value alike
  * with num_kv_heads (so slices of one fused projection can be passed). q_out, key_out:
  * contiguous. q may be NULL (with num_q_heads 0: append only), key_out may be NULL. q_out may

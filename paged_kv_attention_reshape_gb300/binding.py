@@ -60,6 +60,12 @@ _FP8 = (torch.uint8, torch.float8_e4m3fn)
 
 def _block_scales(k_scale, v_scale, nb: int, hkv: int, device_index: int):
     """Checks scale tensors [num_blocks, Hkv]; returns their addresses."""
+    want = (nb, hkv)
+    if (isinstance(k_scale, torch.Tensor) and isinstance(v_scale, torch.Tensor) and k_scale.dtype is torch.float32
+            and v_scale.dtype is torch.float32 and k_scale.shape == want and v_scale.shape == want
+            and k_scale.get_device() == device_index == v_scale.get_device() and k_scale.is_contiguous()
+            and v_scale.is_contiguous()):
+        return k_scale.data_ptr(), v_scale.data_ptr()
     for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if not isinstance(t, torch.Tensor):
             raise PkvError("k_scale and v_scale must both be numbers or both be tensors")
@@ -79,20 +85,19 @@ def make_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale=1.0, v_scal
     (a scale for each block and KV head)."""
     dtype = k_cache.dtype
     fp8 = dtype in _FP8
-    want = dtype if fp8 else torch.bfloat16
     shape = k_cache.shape
     nb, bs, hkv, d = shape
-    stride = 0
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, want, n, contiguous=False)
-        st = t.stride()
-        if st[1:] != (hkv * d, d, 1):
-            raise PkvError(f"{n}: each block must be contiguous [block_size, Hkv, D]")
-        if t.shape != shape or (stride and st[0] != stride):
+    st = k_cache.stride()
+    stride = st[0]
+    if not (k_cache.is_cuda and v_cache.is_cuda and (fp8 or dtype is torch.bfloat16) and v_cache.dtype is dtype
+            and v_cache.shape == shape and v_cache.stride() == st and st[1] == hkv * d and st[2] == d and st[3] == 1):
+        want = dtype if fp8 else torch.bfloat16
+        for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, want, n, contiguous=False)
+            if t.stride()[1:] != (hkv * d, d, 1):
+                raise PkvError(f"{n}: each block must be contiguous [block_size, Hkv, D]")
+        if k_cache.shape != v_cache.shape or stride != v_cache.stride(0):
             raise PkvError("k_cache and v_cache must have the same shape and block stride")
-        stride = st[0]
-        if v_cache is k_cache:
-            break
     if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
         if not fp8:
             raise PkvError("block scales belong to an FP8 cache")
@@ -134,7 +139,7 @@ def kv_cache_write(key, value, slot_mapping, k_cache, v_cache, stream=None, k_sc
 def _token_rows(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, device_index: int) -> int:
     """Checks bf16 rows [rows, heads, dim] whose tokens may lie apart (a slice of a fused projection);
     returns the elements between tokens."""
-    if not t.is_cuda or t.get_device() != device_index:
+    if t.get_device() != device_index:  # -1 for a CPU tensor
         raise PkvError(f"{name} must be on the cache's device")
     if t.dtype is not torch.bfloat16:
         raise PkvError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
@@ -149,7 +154,7 @@ def _token_rows(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dev
 
 
 def _token_index(t: torch.Tensor, name: str, rows: int, device_index: int) -> int:
-    if not t.is_cuda or t.get_device() != device_index or t.dtype is not torch.int64 or t.numel() != rows \
+    if t.get_device() != device_index or t.dtype is not torch.int64 or t.numel() != rows \
             or not t.is_contiguous():
         raise PkvError(f"{name} must be {rows} contiguous int64 entries on the cache's device")
     return t.data_ptr()
@@ -195,7 +200,7 @@ def kv_append(q, key, value, positions, slot_mapping, k_cache, v_cache, cos_sin=
     k_out = _token_out(k_out, "k_out", T, hkv, d, k_cache)
     pos_ptr = None
     if cos_sin is not None:
-        if not cos_sin.is_cuda or cos_sin.get_device() != dev or cos_sin.dtype is not torch.float32 \
+        if cos_sin.get_device() != dev or cos_sin.dtype is not torch.float32 \
                 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise PkvError("cos_sin must be contiguous fp32 [max_pos, n] on the cache's device")
         rows, n = cos_sin.shape

@@ -370,8 +370,9 @@ pkv_status pkv_kv_append(const void* q, int64_t q_stride, const void* key, int64
   }
   p.k_scales = cache.k_scales;
   p.v_scales = cache.v_scales;
-  st = cuda_status(launch_kv_append(p, cache.kv_dtype, reinterpret_cast<cudaStream_t>(stream)));
-  t_launches += 1;
+  int launches = 0;
+  st = cuda_status(launch_kv_append(p, cache.kv_dtype, reinterpret_cast<cudaStream_t>(stream), &launches));
+  t_launches += launches;
   return st;
 }
 

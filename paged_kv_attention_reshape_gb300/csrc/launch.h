@@ -134,7 +134,7 @@ struct AppendParams {
   float* k_scales;         // FP8 with block scales
   float* v_scales;
   int32_t run_tokens;      // block scales: tokens whose runs one CTA appends (set by the launcher)
-  uint32_t run_groups;     // block scales: CTAs that append runs (set by the launcher)
+  uint32_t run_groups;     // block scales: groups of tokens whose runs a CTA appends (set by the launcher)
 };
 
 // Launch with programmatic stream serialisation: the kernel may begin launching while the
@@ -168,6 +168,8 @@ enum AttrSlot {
   kAttrAttn128Block,
   kAttrDecodeScaled8,
   kAttrDecodeScaled16,
+  kAttrAppend0,  // + the cache kind (three)
+  kAttrAppendLast = kAttrAppend0 + 2,
   kAttrMla,
   kAttrCount
 };
@@ -182,7 +184,7 @@ cudaError_t launch_kv_cache_write(const void* key, const void* value, const int6
                                   int64_t num_tokens, const pkv_cache& c, unsigned int* err,
                                   cudaStream_t stream);
 // kind: the cache's kv_dtype
-cudaError_t launch_kv_append(const AppendParams& p, int kind, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendParams& p, int kind, cudaStream_t stream, int* launches);
 cudaError_t launch_kv_block_pack(const pkv_cache& c, const int32_t* block_ids, int32_t num_ids,
                                  void* dst, unsigned int* err, cudaStream_t stream);
 cudaError_t launch_kv_block_unpack(const void* src, const int32_t* block_ids, int32_t num_ids,

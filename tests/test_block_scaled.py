@@ -346,6 +346,53 @@ def test_append_skips_and_flags_bad_slots_and_positions():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("kind,Hq,Hkv,d,rot,off,inter", [
+    ("bf16", 3, 1, 128, 64, 32, False), ("bf16", 0, 2, 64, 0, 0, False), ("bf16", 5, 2, 128, 0, 0, False),
+    ("tensor", 2, 1, 64, 64, 0, True), ("tensor", 9, 3, 128, 32, 96, False), ("latent", 4, 1, 576, 64, 512, True),
+    ("block", 5, 1, 128, 128, 0, False), ("block", 2, 3, 128, 16, 0, True),
+    # rows of which two CTAs do not hold enough in shared memory
+    ("bf16", 100, 8, 128, 128, 0, False), ("latent", 25, 1, 576, 64, 512, False), ("block", 150, 1, 128, 128, 0, False)])
+def test_append_of_many_tokens(kind, Hq, Hkv, d, rot, off, inter, fused):
+    """Long batches: a long chunk, short ones, padding, bad slots and positions in between. fused: q, k
+    and v are slices of one tensor, and the rotated q and k of contiguous ones replace them."""
+    ctx, new = [5, 0, 77, 300], [2011, 1, 16, 100]
+    st = append_state(kind, ctx, new, Hq, Hkv, d, rot, off, inter, pad=29, seed=Hq + d, max_pos=2100)
+    st["slot"][700], st["slot"][2050], want_err = -1, st["nb"] * 16 + 5, 1
+    if rot:
+        st["pos"][3], st["pos"][2100], want_err = 2100, -7, 1 | 8
+    want = plain_append(st)
+    T = len(st["slot"])
+    more = {}
+    if fused:
+        parts = [st[n].reshape(T, -1) for n in "qkv" if st[n] is not None]
+        one = torch.cat(parts, 1).cuda()
+        at = 0
+        for n in "qkv":
+            if st[n] is not None:
+                h = st[n].shape[1]
+                more[n] = one[:, at:at + h * d].view(T, h, d)
+                at += h * d
+    got, err = gpu_append(st, **more)
+    assert err == want_err
+    assert_append(got, want)
+    if fused:
+        qi, ki = on(st["q"]), on(st["k"])
+        skip = torch.ones(T, dtype=torch.bool)  # the tokens that are skipped keep what q and k held
+        skip[st["slot"] >= 0] = False
+        skip[2050] = True
+        if rot:
+            skip[[3, 2100]] = True
+        for n, x in (("q_out", st["q"]), ("k_out", st["k"])):
+            if x is not None:
+                i = 0 if n == "q_out" else 1
+                want = tuple(torch.where(skip[:, None, None], x, w) if j == i else w for j, w in enumerate(want))
+        got, err = gpu_append(st, q=qi, k=ki, q_out=qi, k_out=ki)
+        assert err == want_err
+        assert_append(got, want)
+
+
+@pytest.mark.gpu
 def test_append_twice_is_append_once():
     """Appending the same rows again changes nothing: the scales already hold them."""
     st = append_state("block", [3, 0, 50], [30, 2, 1], 2, 2, 128, 128, seed=8)
