@@ -30,14 +30,29 @@
 // 256 rows an item they are few and long, and a static deal in snake order lost more to the spread
 // of the last round (8 x 512: 2.42 ms against 2.09; 2048 over 100K: 7.45 against 6.35).
 //
-// Roles (12 warps, one CTA per SM, persistent):
+// Two launches of the one kernel. When the bound on new tokens leaves every request 128 rows at most
+// (FEW), all items are split, and a tile's rows are copied to fill it: up to 32 rows four times, up to
+// 64 twice, each copy with its own part of every key tile, so that the four warps of a slot share the
+// softmax, which one would else do for all (a slot's step 1050 clocks against 2000 to 2700). The
+// copies' states are joined with the slots' at the end. There are more converter warps, a fifth buffer in
+// place of the second Q tile, and S is read 32 columns at a time, for which no registers need to change
+// hands. 32 x 4 tokens over contexts of 1K to 4K, Hq 64 / Hkv 8: 66 us, 93 by the general launch.
+//
+// What bounds it. Many rows: tensor core and shared memory together (a key tile of 256 rows takes 4000
+// clocks; its products alone 2200, their operands' and the conversions' reads and writes of shared
+// memory 2500): 8 x 512 tokens over 4K to 32K 1.98 ms, 0.65 of the measured bf16 rate, 2048 tokens over
+// 100K 6.17 ms, 0.58. FEW: the same for a tile of which only every copy's part is new, 2500 clocks of
+// products and conversions a key tile; 0.38 of the measured HBM rate.
+//
+// Roles (12 warps, or 16 in FEW, one CTA per SM, persistent):
 //   warps 0-3, 4-7  softmax of slot 0, 1 (thread t owns row t = TMEM lane t) and the epilogue
 //   warp 8          TMA producer: claims the items, loads Q and the ring of K and V tiles (128 keys)
 //   warp 9          MMA issuer (one thread, which also does its waits: as a whole warp with votes
 //                   around each of them 2.30 ms against 2.18): S = Q K^T, O += P V (P read from
 //                   tensor memory)
 //   warps 10-11     converters: E4M3 code tiles, Q and new keys to fp16 in shared memory, two rows a
-//                   thread (four warps convert faster but slow the products, whose operands they
+//                   thread (FEW: warps 10-13 for K and Q, 14-15 for V, 66 us against 71 with two and two; in
+//                   the general launch four warps convert faster but slow the products, whose operands they
 //                   compete with for shared memory; and unrolled loops over the rows and over K and V
 //                   measured 2.18 ms against 2.02 on the 8 x 512 tokens)
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; P_s overwrites the first half of S_s.
@@ -54,50 +69,61 @@ namespace pkv {
 
 namespace {
 
-struct AsCfg {
+struct AsBase {
   static constexpr int D = 128, BN = 128, BS = 16, TBLK = BN / BS;
   static constexpr int HALF_BYTES = 128 * 128;       // 128 rows x 128 bytes
   static constexpr int TILE_BYTES = 2 * HALF_BYTES;  // one 128-row tile of Q, K or V in 16 bits
-  static constexpr int NBUF = 4;                     // K/V ring: one tile per buffer
   static constexpr int MAXR = kAttnSetChunk;         // requests of the set one launch holds
-  static constexpr int W_LOAD = 8, W_MMA = 9, W_CONV = 10, NCONV = 2, WARPS = 12;
-  static constexpr int THREADS = WARPS * 32;
-  // launched at 168 registers a thread; the softmax warpgroups hold a whole row of S and take more,
-  // the third warpgroup gives them up
-  static constexpr int REGS_SOFTMAX = 192, REGS_OTHER = 120;
-  static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER == THREADS * 168, "register split");
-  static constexpr int RING_OFF = 2 * TILE_BYTES;
-  static constexpr int REQ_OFF = RING_OFF + NBUF * TILE_BYTES;  // int4 {r, row0, q_len, C}
-  static constexpr int START_OFF = REQ_OFF + MAXR * 16;
-  static constexpr int PERM_OFF = START_OFF + (MAXR + 2) * 4;   // set positions by cost, heaviest first
-  // output staging: per softmax warp, 32 rows x 32 bf16 columns (64-byte rows, 64-byte swizzle)
-  static constexpr int STAGE_OFF = (PERM_OFF + MAXR * 4 + 127) / 128 * 128;
+  static constexpr int W_LOAD = 8, W_MMA = 9, W_CONV = 10;
+  static constexpr int MAXBUF = 5;
   static constexpr int STAGE_WARP_BYTES = 32 * 64;
   static constexpr int ITEM_RING = 4;                // claimed items published to the other roles
-  static constexpr int ITEM_READERS = 1 + 8 + NCONV;
-  static constexpr int ITEM_OFF = STAGE_OFF + 8 * STAGE_WARP_BYTES;
   // key tile k of the CTA in slot k % SCALE_RING: the blocks' scales as they land (8 of K, 8 of V), and
   // what the softmax makes of them ({key scale * softmax scale, log2 of the value scale, its inverse,
-  // -} a block). Slot k is written again for tile k + 4, whose K is loaded once S of tile k + 2 is
-  // done, which needs P of tile k + 1 (of tile k, in a split item): every reader is past tile k.
+  // -} a block). Slot k is written again for tile k + 4, whose K is loaded once S of tile k + 2 (with
+  // five buffers, P V of tile k + 1) is done, which needs P of tile k + 1 (of tile k, in a split item,
+  // where the products P V are issued in order): every reader is past tile k.
   static constexpr int SCALE_RING = 4;
-  static constexpr int SCALE_OFF = (ITEM_OFF + ITEM_RING * 8 + 15) / 16 * 16;
-  static constexpr int FACTOR_OFF = SCALE_OFF + SCALE_RING * 2 * TBLK * 4;
-  static constexpr int MERGE_OFF = FACTOR_OFF + SCALE_RING * TBLK * 16;  // slot 1's {m, l} by row (split items)
-  static constexpr int BAR_OFF = MERGE_OFF + 128 * 8;
   static constexpr uint32_t IDESC_QK = tc::idesc_f16(128, 128, 0, 0);
   static constexpr uint32_t IDESC_PV = tc::idesc_f16(128, D, 0, 1), IDESC_PV_NEW = tc::idesc_bf16(128, D, 0, 1);
 };
 struct AsBars {
   uint64_t q_full, q_empty, q_conv;
-  uint64_t kv_full[AsCfg::NBUF], kv_empty[AsCfg::NBUF], conv_full[AsCfg::NBUF];
+  uint64_t kv_full[AsBase::MAXBUF], kv_empty[AsBase::MAXBUF], conv_full[AsBase::MAXBUF];
   uint64_t s_full[2], p_full[2], o_final[2];
-  uint64_t item_full[AsCfg::ITEM_RING], item_empty[AsCfg::ITEM_RING];
+  uint64_t item_full[AsBase::ITEM_RING], item_empty[AsBase::ITEM_RING];
   uint64_t drained;                 // the products in flight when a role gave up
+  uint64_t rep_full;                // slot 0's copies of the rows are joined (FEW)
   uint64_t merge_full, merge_done;  // slot 1's m and l are in shared memory; slot 0 has read them and O_1
 };
-constexpr int kAsSmem = 1024 + AsCfg::BAR_OFF + static_cast<int>(sizeof(AsBars));
-static_assert(kAsSmem <= 226 * 1024, "shared memory");
+// FEW: the launch for sets in which every request's rows for a KV head fit one tile (all items are split).
+template <bool FEW>
+struct AsCfg : AsBase {
+  // converter warps: of K (Q and new keys too) and of V; the general launch's two convert both
+  static constexpr int NK = FEW ? 4 : 2, NV = FEW ? 2 : 0, NCONV = NK + NV;
+  static constexpr int WARPS = W_CONV + NCONV, THREADS = WARPS * 32;
+  // The general launch has 168 registers a thread; the softmax warpgroups hold a whole row of S and take
+  // more, the third warpgroup gives them up.
+  static constexpr int REGS_SOFTMAX = 192, REGS_OTHER = 120;
+  static_assert(FEW || 256 * REGS_SOFTMAX + 128 * REGS_OTHER == THREADS * 168, "register split");
+  static constexpr int NBUF = FEW ? 5 : 4;           // K/V ring: one tile per buffer
+  static constexpr int NQ = FEW ? 1 : 2;             // Q tiles of an item
+  static constexpr int RING_OFF = NQ * TILE_BYTES;
+  static constexpr int REQ_OFF = RING_OFF + NBUF * TILE_BYTES;  // int4 {r, row0, q_len, C}
+  static constexpr int START_OFF = REQ_OFF + MAXR * 16;
+  static constexpr int PERM_OFF = START_OFF + (MAXR + 2) * 4;   // set positions by cost, heaviest first
+  // output staging: per softmax warp, 32 rows x 32 bf16 columns (64-byte rows, 64-byte swizzle)
+  static constexpr int STAGE_OFF = (PERM_OFF + MAXR * 4 + 127) / 128 * 128;
+  static constexpr int ITEM_READERS = 1 + 8 + NCONV;
+  static constexpr int ITEM_OFF = STAGE_OFF + 8 * STAGE_WARP_BYTES;
+  static constexpr int SCALE_OFF = (ITEM_OFF + ITEM_RING * 8 + 15) / 16 * 16;
+  static constexpr int FACTOR_OFF = SCALE_OFF + SCALE_RING * 2 * TBLK * 4;
+  static constexpr int MERGE_OFF = FACTOR_OFF + SCALE_RING * TBLK * 16;  // slot 1's {m, l} by row (split items)
+  static constexpr int REP_OFF = MERGE_OFF + 128 * 8;            // slot 0's {m, l} by row (FEW)
+  static constexpr int BAR_OFF = REP_OFF + (FEW ? 128 * 8 : 0);
+  static constexpr int SMEM = 1024 + BAR_OFF + static_cast<int>(sizeof(AsBars));
+  static_assert(SMEM <= 226 * 1024, "shared memory");
+};
 
 __device__ __forceinline__ constexpr uint32_t as_scol(int slot) { return slot * 128u; }
 __device__ __forceinline__ constexpr uint32_t as_ocol(int slot) { return 256u + slot * 128u; }
@@ -111,11 +137,15 @@ struct AsItem {
   int64_t row0;         // the request's first row of q
 };
 __device__ __forceinline__ int as_pairs(const int4& q, int G) { return (q.z * G + 255) / 256; }
+// FEW: rows of a copy. A tile of up to 32 (64) rows holds four (two) copies of them, each of which takes
+// its own quarter (half) of every key tile, so that all four warps have the same part of the softmax.
+__device__ __forceinline__ int as_span(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 // Key tiles an item of the request walks at most: the schedule's order.
 __device__ __forceinline__ int as_cost(const int4& q) { return (q.w + 127) / 128 + (q.z + 127) / 128; }
 
 // Work item w: s_req holds {request id, first query row, q_len, cached tokens} of each request of the
 // set, s_perm the set positions by decreasing cost, s_start the prefix of items in that order.
+template <bool FEW>
 __device__ __forceinline__ AsItem as_item(const AttnParams& p, const int* s_start, const int4* s_req, const int* s_perm,
                                           int n, int w) {
   int lo = 0, hi = n - 1;
@@ -133,7 +163,7 @@ __device__ __forceinline__ AsItem as_item(const AttnParams& p, const int* s_star
   it.kh = idx % p.Hkv;
   it.base = 256 * (as_pairs(q, p.G) - 1 - idx / p.Hkv);  // later (heavier) rows of a request first
   const int rows = min(256, q.z * p.G - it.base);
-  it.split = rows <= 128;
+  it.split = FEW || rows <= 128;
   it.nct = (it.C + 127) / 128;
   it.NT = it.nct + (it.base + rows - 1) / p.G / 128 + 1;
   return it;
@@ -184,8 +214,8 @@ __device__ __forceinline__ bool as_wait1(uint64_t* bar, uint32_t parity, volatil
 // The k-th work item (-1: no more, or a wait gave up). Lane 0 reads the entry and frees it.
 __device__ __forceinline__ int as_take(const int* s_item, AsBars& bar, uint32_t k, volatile int* abort_flag,
                                        unsigned int* err, int lane) {
-  const int e = static_cast<int>(k % AsCfg::ITEM_RING);
-  if (!as_wait(&bar.item_full[e], (k / AsCfg::ITEM_RING) & 1, abort_flag, err)) return -1;
+  const int e = static_cast<int>(k % AsBase::ITEM_RING);
+  if (!as_wait(&bar.item_full[e], (k / AsBase::ITEM_RING) & 1, abort_flag, err)) return -1;
   int w = 0;
   if (lane == 0) {
     w = *reinterpret_cast<const volatile int*>(&s_item[e]);
@@ -195,8 +225,8 @@ __device__ __forceinline__ int as_take(const int* s_item, AsBars& bar, uint32_t 
 }
 
 __device__ __forceinline__ int as_take1(const int* s_item, AsBars& bar, uint32_t k, volatile int* abort_flag, unsigned int* err) {
-  const int e = static_cast<int>(k % AsCfg::ITEM_RING);
-  if (!as_wait1(&bar.item_full[e], (k / AsCfg::ITEM_RING) & 1, abort_flag, err)) return -1;
+  const int e = static_cast<int>(k % AsBase::ITEM_RING);
+  if (!as_wait1(&bar.item_full[e], (k / AsBase::ITEM_RING) & 1, abort_flag, err)) return -1;
   const int w = *reinterpret_cast<const volatile int*>(&s_item[e]);
   mbar_arrive(&bar.item_empty[e]);
   return w;
@@ -232,16 +262,28 @@ __device__ __forceinline__ void as_conv_bf16(uint32_t tile, int R) {
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const uint32_t a = tile + h * 16384u + R * 128 + (q << 4);  // in place: any chunk order will do
+      const uint32_t a = tile + h * 16384u + R * 128 + ((q ^ (R & 7)) << 4);  // 8 rows: 8 different bank groups
       const uint4 v = ld_shared_v4(a);
       st_shared_v4(a, make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w)));
+    }
+}
+// The same, and again every `span` rows below.
+__device__ __forceinline__ void as_conv_copies(uint32_t tile, int R, int span) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint32_t a = tile + h * 16384u + R * 128 + ((q ^ (R & 7)) << 4);
+      const uint4 v = ld_shared_v4(a);
+      const uint4 f = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+      for (int r = 0; r < 128 - R; r += span) st_shared_v4(a + r * 128, f);
     }
 }
 __device__ __forceinline__ void as_zero_row(uint32_t tile, int R) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) st_shared_v4(tile + h * 16384u + R * 128 + (q << 4), make_uint4(0, 0, 0, 0));
+    for (int q = 0; q < 8; ++q) st_shared_v4(tile + h * 16384u + R * 128 + ((q ^ (R & 7)) << 4), make_uint4(0, 0, 0, 0));
 }
 
 // Columns n .. 31 of a 32-column chunk of S (raw fp32 bits) become -inf, so that whatever the tensor
@@ -251,11 +293,12 @@ __device__ __forceinline__ void as_mask(uint32_t (&v)[32], int n) {
   for (int e = 0; e < 32; ++e) v[e] = e < n ? v[e] : 0xFF800000u;
 }
 
-__global__ void __launch_bounds__(AsCfg::THREADS, 1)
+template <bool FEW>
+__global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
     attn_scaled_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ck,
                        const __grid_constant__ CUtensorMap tm_cv) {
-  using C = AsCfg;
+  using C = AsCfg<FEW>;
   constexpr int D = C::D;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -291,11 +334,11 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
   if (tid == 0) {
     mbar_init(&bar.q_full, 1);
     mbar_init(&bar.q_empty, 1);
-    mbar_init(&bar.q_conv, C::NCONV);
+    mbar_init(&bar.q_conv, C::NK);
     for (int b = 0; b < C::NBUF; ++b) {
       mbar_init(&bar.kv_full[b], 1 + C::TBLK);  // the producer's bytes, and each block's scales
       mbar_init(&bar.kv_empty[b], 1);
-      mbar_init(&bar.conv_full[b], C::NCONV);
+      mbar_init(&bar.conv_full[b], FEW ? C::NK : C::NCONV);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
@@ -307,6 +350,7 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
       mbar_init(&bar.item_empty[i], C::ITEM_READERS);
     }
     mbar_init(&bar.drained, 1);
+    mbar_init(&bar.rep_full, 128);
     mbar_init(&bar.merge_full, 128);
     mbar_init(&bar.merge_done, 128);
     s_abort = 0;
@@ -319,8 +363,12 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
     const int r = p.order ? p.order[begin + i] : begin + i;
     int4 q = make_int4(0, 0, 0, 0);
     if (r >= 0 && r < p.batch_reqs) {
-      const int q_len = max(0, p.cu_q[r + 1] - p.cu_q[r]);
+      int q_len = max(0, p.cu_q[r + 1] - p.cu_q[r]);
       int c = max(0, p.seq_lens[r] - q_len);
+      if (q_len > p.max_q_len) {
+        if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_LEN);
+        q_len = p.max_q_len;
+      }
       if (c > static_cast<int64_t>(p.max_blocks) * C::BS) {
         if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_LEN);
         c = p.max_blocks * C::BS;
@@ -366,8 +414,9 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
   const int W = s_start[n];
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+    if constexpr (!FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     // ======================= softmax warpgroups =======================
+    if constexpr (!FEW) {
     const int slot = warp >> 2;
     const int t = tid & 127;  // row of the tile = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -379,7 +428,7 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
       if (w < 0) break;
       float m = -CUDART_INF_F, l = 0.f;
       {
-        const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
+        const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
         if (slot == 1 && it.split && it.NT == 1) {  // its one key tile is slot 0's
           tile0 += it.NT;
           continue;
@@ -479,7 +528,7 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
         tile0 += it.NT;
       }
       // ---- epilogue (the item found again, so that its fields need not stay in registers above) ----
-      const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
+      const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
       const bool both = it.split && it.NT > 1;  // two states of the same rows
       float2* mrg = reinterpret_cast<float2*>(smem + C::MERGE_OFF);
       if (both && slot == 1) {
@@ -565,8 +614,218 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
         if (fr >= 0) p.lse[fr] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
       }
     }
+    } else {
+    const int slot = warp >> 2;
+    const int t = tid & 127;  // row of the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t sc = 0, oc = 0;  // S tiles of this slot; its O's
+    uint32_t tile0 = 0;       // the CTA's key tiles before this item
+    uint32_t par = 0;         // parities of the items whose slot 1 has an O (bit 0), of the merges (bit 1)
+    uint32_t rc = 0;          // phases of rep_full
+    for (uint32_t k = 0;; ++k) {
+      const int w = as_take(s_item, bar, k, &s_abort, p.err, lane);
+      if (w < 0) break;
+      const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
+      if (slot == 1 && it.NT == 1) {  // its one key tile is slot 0's
+        tile0 += 1;
+        continue;
+      }
+      // thread t: row t % span, keys [t / span * span, + span) of each tile
+      const int span = as_span(it.q_len * p.G), row = t & (span - 1), c_lo = (t & ~(span - 1)) / 32, c_hi = c_lo + span / 32;
+      const int g_log = __ffs(p.G) - 1;  // G is a power of two
+      const int tok = row >> g_log;
+      const bool idle = __all_sync(0xffffffffu, tok >= it.q_len);
+      const uint32_t srow = tmem + lane_off + as_scol(slot);
+      float m = -CUDART_INF_F, l = 0.f;
+      bool ok = true;
+      for (int j = slot; j < it.NT; j += 2) {
+        if (!as_wait(&bar.s_full[slot], sc & 1, &s_abort, p.err)) { ok = false; break; }
+        ++sc;
+        tc::fence_after_sync();
+        if (!idle) {
+          const bool ctx = j < it.nct;
+          const int kv = ctx ? min(128, it.C - j * 128) : min(128, tok - (j - it.nct) * 128 + 1);
+          const float4* fac = reinterpret_cast<const float4*>(smem + C::FACTOR_OFF) + (tile0 + j) % C::SCALE_RING * 8;
+          uint32_t v[32];
+          auto load = [&](int c) {
+            tc::ld32(srow + c * 32, v);
+            tc::wait_ld();
+            tc::touch32(v);
+            as_mask(v, kv - c * 32);
+          };
+          float mx = -CUDART_INF_F;
+#pragma unroll 1
+          for (int c = c_hi - 1; c >= c_lo; --c) {
+            load(c);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              float mg = -CUDART_INF_F;
+#pragma unroll
+              for (int e = 16 * g; e < 16 * g + 16; e += 2) mg = sm::max3(mg, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              const float4 f = fac[2 * c + g];
+              mx = fmaxf(mx, fmaf(mg, f.x, f.y));
+            }
+          }
+          float alpha = 1.f;
+          if (mx > m + 8.f || m == -CUDART_INF_F) {  // lazy rescale: only when the max really grows
+            const float m_new = fmaxf(m, mx);
+            if (m_new != -CUDART_INF_F) {
+              alpha = (m == -CUDART_INF_F) ? 0.f : ex2_approx(m - m_new);
+              m = m_new;
+            }
+          }
+          const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+          uint64_t rs2 = sm::f2(0.f, 0.f);
+          uint32_t pk[16];
+#pragma unroll 1
+          for (int c = c_lo; c < c_hi; ++c) {
+            if (c > c_lo) load(c);  // P so far lies below this chunk of S
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const float4 f = fac[2 * c + g];
+              const uint64_t sc2 = sm::f2(f.x, f.x), nm2 = sm::f2(neg_m + f.y, neg_m + f.y), iv2 = sm::f2(f.z, f.z);
+#pragma unroll
+              for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+                const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nm2);
+                float x0, x1;
+                sm::unf2(x, x0, x1);
+                const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
+                rs2 = sm::fma2(pp, iv2, rs2);
+                pk[e / 2] = ctx ? sm::f16x2(pp) : sm::bf16x2(pp);
+              }
+            }
+            tc::st16(srow + c * 16, pk);
+          }
+          // the other copies' keys
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c < c_lo || c >= c_hi) tc::st16(srow + c * 16, pk);
+          float r0, r1;
+          sm::unf2(rs2, r0, r1);
+          l = l * alpha + (r0 + r1);
+          if (j > slot && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              tc::ld32(tmem + lane_off + as_ocol(slot) + c * 32, v);
+              tc::wait_ld();
+              tc::touch32(v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tc::st32(tmem + lane_off + as_ocol(slot) + c * 32, v);
+            }
+          }
+          tc::wait_st();
+        }
+        tc::fence_before_sync();
+        mbar_arrive(&bar.p_full[slot]);
+      }
+      if (!ok) break;
+      tile0 += it.NT;
+      // ---- epilogue: slot 0 joins the slots' states, then the copies', and writes the rows ----
+      const bool both = it.NT > 1;
+      float2* mrg = reinterpret_cast<float2*>(smem + C::MERGE_OFF);
+      float2* rml = reinterpret_cast<float2*>(smem + C::REP_OFF);
+      if (slot == 1) {
+        mrg[t] = make_float2(m, l);
+        mbar_arrive(&bar.merge_full);
+        if (!as_wait(&bar.merge_done, (par >> 1) & 1, &s_abort, p.err)) break;
+        par ^= 2;
+        ++oc;
+        continue;
+      }
+      if (!as_wait(&bar.o_final[0], oc & 1, &s_abort, p.err)) break;
+      ++oc;
+      float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and of slot 1's
+      if (both) {
+        if (!as_wait(&bar.o_final[1], par & 1, &s_abort, p.err) || !as_wait(&bar.merge_full, (par >> 1) & 1, &s_abort, p.err))
+          break;
+        par ^= 3;
+        const float2 o1 = mrg[t];
+        const float mm = fmaxf(m, o1.x);
+        w0 = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mm);
+        w1 = o1.x == -CUDART_INF_F ? 0.f : ex2_approx(o1.x - mm);
+        l = l * w0 + o1.y * w1;
+        m = mm;
+      }
+      // the copies of a row: their common max and sum
+      rml[t] = make_float2(m, l);
+      mbar_arrive(&bar.rep_full);
+      if (!as_wait(&bar.rep_full, rc & 1, &s_abort, p.err)) break;
+      ++rc;
+      float mm = -CUDART_INF_F, ll = 0.f;
+      for (int i = row; i < 128; i += span) mm = fmaxf(mm, rml[i].x);
+      for (int i = row; i < 128; i += span) {
+        const float2 o = rml[i];
+        ll += o.x == -CUDART_INF_F ? 0.f : o.y * ex2_approx(o.x - mm);
+      }
+      const float wr = ll > 0.f && m != -CUDART_INF_F ? ex2_approx(m - mm) / ll : 0.f;
+      w0 *= wr, w1 *= wr;
+      tc::fence_after_sync();
+      const int rows = min(it.q_len, static_cast<int>(min(static_cast<int64_t>(it.q_len), p.num_tokens - it.row0))) * p.G;
+      const uint32_t stg = smem_u32(smem) + C::STAGE_OFF;  // [128 rows][32 fp32], 128-byte swizzle
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tc::ld32(tmem + as_ocol(0) + lane_off + c * 32, o);
+        tc::wait_ld();
+        tc::touch32(o);
+        // (a state without keys has no part, whatever the tensor core made of its row)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = w0 > 0.f ? __float_as_uint(__uint_as_float(o[e]) * w0) : 0u;
+        if (both) {
+          uint32_t o1[32];
+          tc::ld32(tmem + as_ocol(1) + lane_off + c * 32, o1);
+          tc::wait_ld();
+          tc::touch32(o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (w1 > 0.f) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          st_shared_v4(stg + t * 128 + ((q ^ (t & 7)) << 4), make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
+        mbar_arrive(&bar.rep_full);
+        if (!as_wait(&bar.rep_full, rc & 1, &s_abort, p.err)) { ok = false; break; }
+        ++rc;
+        // 8 rows x 32 columns a warp at a time, 8 columns a thread
+        for (int r0 = (warp & 3) * 8; r0 < min(span, rows); r0 += 32) {
+          const int rr = r0 + (lane >> 2), kk = lane & 3;
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = 0.f;
+          for (int i = rr; i < 128; i += span) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 y = ld_shared_v4(stg + i * 128 + (((2 * kk + h) ^ (i & 7)) << 4));
+              x[4 * h] += __uint_as_float(y.x);
+              x[4 * h + 1] += __uint_as_float(y.y);
+              x[4 * h + 2] += __uint_as_float(y.z);
+              x[4 * h + 3] += __uint_as_float(y.w);
+            }
+          }
+          if (rr < rows) {
+            const int64_t fr = (it.row0 + (rr >> g_log)) * p.Hq + it.kh * p.G + (rr & (p.G - 1));
+            *reinterpret_cast<uint4*>(p.out + fr * D + c * 32 + kk * 8) =
+                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+          }
+        }
+        // the staging tile is free again
+        mbar_arrive(&bar.rep_full);
+        if (!as_wait(&bar.rep_full, rc & 1, &s_abort, p.err)) { ok = false; break; }
+        ++rc;
+      }
+      if (!ok) break;
+      tc::fence_before_sync();
+      if (both) mbar_arrive(&bar.merge_done);
+      if (p.lse && t < min(span, rows))
+        p.lse[(it.row0 + tok) * p.Hq + it.kh * p.G + (row & (p.G - 1))] =
+            ll > 0.f ? (mm + __log2f(ll)) * 0.69314718055994531f : -CUDART_INF_F;
+    }
+    }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+    if constexpr (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (warp == C::W_LOAD) {
       // ======================= TMA producer =======================
       if (lane == 0) {
@@ -592,7 +851,7 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
         }
         w = __shfl_sync(0xffffffffu, w, 0);
         if (w < 0) break;
-        const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
+        const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
         if (lane == 0) {
           const int nq = it.split ? 1 : 2;
           mbar_arrive_expect_tx(&bar.q_full, nq * C::TILE_BYTES);
@@ -695,7 +954,7 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
         for (uint32_t items = 0; ok; ++items) {
           const int w = as_take1(s_item, bar, items, &s_abort, p.err);
           if (w < 0) break;
-          const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
+          const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
           if (!as_wait1(&bar.q_conv, items & 1, &s_abort, p.err)) break;
           if (it.split) {
             // key tile j goes to slot j % 2: S(j) and the other slot's O += P V of tile j - 1, whichever has
@@ -709,23 +968,22 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
               if (j == it.NT - 1) tc::commit(&bar.q_empty);
               return true;
             };
+            auto do_pv = [&](int j) {
+              const uint32_t vh = kvc + 2 * j + 1;
+              if (!as_wait1(&bar.conv_full[vh % C::NBUF], (vh / C::NBUF) & 1, &s_abort, p.err) || !wait_p(j & 1)) return false;
+              pv(j & 1, vh % C::NBUF, j >= 2, j < it.nct);
+              tc::commit(&bar.kv_empty[vh % C::NBUF]);
+              if (j >= it.NT - 2) tc::commit(&bar.o_final[j & 1]);
+              return true;
+            };
             for (int j = 0; j <= it.NT && ok; ++j) {
               const uint32_t kh = kvc + 2 * j;
-              const bool now = j < it.NT && (j == 0 || mbar_test(&bar.conv_full[kh % C::NBUF], (kh / C::NBUF) & 1));
-              if (now) ok = do_s(j);
-              if (ok && j > 0) {
-                const int s = (j - 1) & 1;
-                const uint32_t vh = kvc + 2 * j - 1;
-                ok = as_wait1(&bar.conv_full[vh % C::NBUF], (vh / C::NBUF) & 1, &s_abort, p.err) && wait_p(s);
-                if (ok) {
-                  pv(s, vh % C::NBUF, j - 1 >= 2, j - 1 < it.nct);
-                  tc::commit(&bar.kv_empty[vh % C::NBUF]);
-                  if (j - 1 >= it.NT - 2) tc::commit(&bar.o_final[s]);
-                }
-              }
-              if (ok && !now && j < it.NT) ok = do_s(j);
+              const bool s_first = j == 0 || (j < it.NT && mbar_test(&bar.conv_full[kh % C::NBUF], (kh / C::NBUF) & 1));
+              if (s_first) ok = do_s(j);
+              if (ok && j > 0) ok = do_pv(j - 1);
+              if (ok && !s_first && j < it.NT) ok = do_s(j);
             }
-          } else {
+          } else if constexpr (!FEW) {
             // per key tile: S_0(j), O_1 += P_1 V (j - 1), S_1(j), O_0 += P_0 V (j), so that each softmax
             // warpgroup works while the tensor core serves the other
             for (int j = 0; j < it.NT; ++j) {
@@ -764,26 +1022,36 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
       __syncwarp();
     } else {
       // ======================= converters =======================
-      // Thread ct converts rows ct and ct + 64 of every tile: Q once per item, then each K and V tile as it lands.
-      const int ct = tid - C::W_CONV * 32;
+      // The first NK warps convert Q once per item, then each K tile as it lands, the others (or, if there are
+      // none, the same) each V tile: rows ct, ct + 32 NK, .. a thread.
+      const bool of_v = FEW && warp >= C::W_CONV + C::NK;
+      const int ct = tid - (C::W_CONV + (of_v ? C::NK : 0)) * 32;
       const uint32_t q_base = smem_u32(sQ), ring_base = smem_u32(ring);
       uint32_t kvc = 0;
       bool ok = true;
       for (uint32_t k = 0; ok; ++k) {
         const int w = as_take(s_item, bar, k, &s_abort, p.err, lane);
         if (w < 0) break;
-        const AsItem it = as_item(p, s_start, s_req, s_perm, n, w);
-        if (!as_wait(&bar.q_full, k & 1, &s_abort, p.err)) break;
-        for (int s = 0; s < (it.split ? 1 : 2); ++s) {
-          as_conv_bf16(q_base + s * C::TILE_BYTES, ct);
-          as_conv_bf16(q_base + s * C::TILE_BYTES, ct + 64);
+        const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
+        if (!of_v) {
+          if (!as_wait(&bar.q_full, k & 1, &s_abort, p.err)) break;
+          if constexpr (FEW) {
+            const int span = as_span(it.q_len * p.G);
+            for (int R = ct; R < span; R += C::NK * 32) as_conv_copies(q_base, R, span);
+          } else {
+            for (int s = 0; s < (it.split ? 1 : 2); ++s) {
+              as_conv_bf16(q_base + s * C::TILE_BYTES, ct);
+              as_conv_bf16(q_base + s * C::TILE_BYTES, ct + 64);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.q_conv);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.q_conv);
         for (int j = 0; j < it.NT && ok; ++j) {
 #pragma unroll 1
           for (int sel = 0; sel < 2; ++sel, ++kvc) {
+            if (FEW && (sel != 0) != of_v) continue;
             const int b = kvc % C::NBUF;
             if (!as_wait(&bar.kv_full[b], (kvc / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
             const uint32_t tile = ring_base + b * C::TILE_BYTES;
@@ -800,7 +1068,7 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
               reinterpret_cast<float4*>(smem + C::FACTOR_OFF)[at * 8 + ct] = f;
             }
 #pragma unroll 1
-            for (int R = ct; R < 128; R += 64) {
+            for (int R = ct; R < 128; R += FEW && of_v ? C::NV * 32 : C::NK * 32) {
               if (j < it.nct) {
                 // V rows past the context's end become zeros (P = 0 there must not meet a NaN code)
                 as_conv_codes(tile, R, sel == 0 || R < it.C - j * 128);
@@ -813,7 +1081,8 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.conv_full[b]);
+            // NK arrivals a tile, of K and of V
+            if (FEW ? lane < (of_v ? C::NK / C::NV : 1) : lane == 0) mbar_arrive(&bar.conv_full[b]);
           }
         }
       }
@@ -838,12 +1107,21 @@ __global__ void __launch_bounds__(AsCfg::THREADS, 1)
 
 }  // namespace
 
+template <bool FEW>
+static cudaError_t launch_scaled(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream) {
+  using C = AsCfg<FEW>;
+  const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attn_scaled_kernel<FEW>), C::SMEM,
+                                           FEW ? kAttrAttn128BlockFew : kAttrAttn128Block);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_scaled_kernel<FEW>, dim3(num_sms()), dim3(C::THREADS), C::SMEM, stream, p, tq, tk, tv, tck, tcv);
+}
+
 cudaError_t launch_attn_scaled(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream, int* launches) {
-  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attn_scaled_kernel), kAsSmem, kAttrAttn128Block);
-  if (e != cudaSuccess) return e;
   *launches += 1;
-  return launch_pdl(attn_scaled_kernel, dim3(num_sms()), dim3(AsCfg::THREADS), kAsSmem, stream, p, tq, tk, tv, tck, tcv);
+  return static_cast<int64_t>(p.max_q_len) * p.G <= 128 ? launch_scaled<true>(p, tq, tk, tv, tck, tcv, stream)
+                                                        : launch_scaled<false>(p, tq, tk, tv, tck, tcv, stream);
 }
 
 }  // namespace pkv

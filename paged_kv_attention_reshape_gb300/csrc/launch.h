@@ -166,6 +166,7 @@ enum AttrSlot {
   kAttrAttn128Scaled,
   kAttrAttn128Fp8,
   kAttrAttn128Block,
+  kAttrAttn128BlockFew,
   kAttrDecodeScaled8,
   kAttrDecodeScaled16,
   kAttrAppend0,  // + the cache kind (three)

@@ -664,6 +664,57 @@ def test_extend_edge_lengths(G, Hkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G,Hkv,most", [(1, 2, 128), (1, 1, 32), (2, 3, 32), (4, 2, 16), (4, 1, 32), (8, 2, 4), (8, 1, 9), (16, 1, 8),
+                                         (16, 2, 1)])
+def test_extend_of_a_few_tokens(G, Hkv, most):
+    """Sets whose requests have up to 128 rows for a KV head (up to 32, 64 and 128: four, two and one copies)."""
+    ctx = [0, 1, 15, 16, 17, 127, 128, 129, 300, 5, 0, 1000, 2500]
+    new = [1, most, 1 + most // 2, most, 1, 1 + most // 3, most, max(1, most - 1), most, 0, most, 1 + most // 4, most]
+    st = extend_state(ctx, new, G * Hkv, Hkv, seed=G + most, qs=1.5, gap=1)
+    check_extend(st, *gpu_extend(st), SCALE)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["wide_v", "wide_k", "tiny", "sink"])
+def test_extend_of_a_few_tokens_extreme_scales(what):
+    st = extend_state([700, 130, 1300], [3, 4, 2], 16, 2, seed=19, qs=1.0 if what != "sink" else 4.0)
+    g = gen(3)
+    if what == "wide_v":
+        st["vs"] = st["vs"] * torch.exp2(torch.randint(-30, 31, st["vs"].shape, generator=g).float())
+    elif what == "wide_k":
+        st["ks"] = st["ks"] * torch.exp2(torch.randint(-12, 3, st["ks"].shape, generator=g).float())
+    elif what == "tiny":
+        st["vs"] = st["vs"] * 2.0 ** -80
+        st["v_new"] = (st["v_new"].float() * 2.0 ** -80).to(torch.bfloat16)
+    elif what == "sink":
+        st["ks"][int(st["table"][0, 0])] *= 12.0
+    check_extend(st, *gpu_extend(st), SCALE)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("most", [3, 200])
+def test_extend_cuts_and_flags_more_tokens_than_its_bound(most):
+    """A request with more new tokens than max_q_len: its first max_q_len rows are right, the others stay as they were."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    st = extend_state([100, 40, 7], [most, most + 2, 1], 8, 2, seed=23)
+    kc, vc = pools(st)
+    out = torch.full(st["q"].shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(st["q"].shape[:2], 5.0, device="cuda")
+    total = torch.tensor([c + n for c, n in zip(st["ctx"], st["new"])], dtype=torch.int32)
+    pkv.extend_attn(on(st["q"]), on(st["k_new"]), on(st["v_new"]), on(st["cu"]), on(total), kc, vc, on(st["table"]), most,
+                    int(total.max()), out=out, lse=lse, k_scale=on(st["ks"]), v_scale=on(st["vs"]))
+    assert pkv.device_errors() == 0x8
+    cut = slice(int(st["cu"][1]) + most, int(st["cu"][2]))
+    assert bool((out[cut] == 5.0).all()) and bool((lse[cut] == 5.0).all())
+    check_extend(st, out, lse, SCALE, reqs=[0, 2])
+    few = dict(st, new=[most] * 2 + [1], cu=torch.tensor([0, most, 2 * most, 2 * most + 1], dtype=torch.int32))
+    keep = torch.ones(len(st["q"]), dtype=torch.bool)
+    keep[cut] = False
+    few.update(q=st["q"][keep], k_new=st["k_new"][keep], v_new=st["v_new"][keep])
+    check_extend(few, out.cpu()[keep], lse.cpu()[keep], SCALE)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("ctx,new,G,Hkv,qs", [([5000, 40], [20, 300], 8, 2, 1.0), ([1037] * 6, [4] * 6, 4, 2, 3.0),
                                               ([2500], [1], 16, 2, 1.0), ([800, 900], [200, 1], 1, 4, 2.0)])
 def test_extend_longer_contexts(ctx, new, G, Hkv, qs):
