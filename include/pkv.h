@@ -363,11 +363,21 @@ pkv_status pkv_mla_decode_attn(const void* q, pkv_cache cache, const int32_t* bl
  * section's "gather and maybe dequant"), exactly the E4M3 values. Either way the scales are
  * applied in the attention (keys with the softmax scale, values on the output). The workspace
  * is rewritten by every such call.
+ * For a block-scaled cache (PKV_KV_FP8_E4M3_BLOCK) the queries and new keys must lie within the
+ * fp16 range; new values may have any size. A request with more than max_q_len new tokens flags
+ * PKV_DEVERR_LEN and is cut to its first max_q_len. workspace: NULL, or at least
+ * pkv_extend_block_workspace_size(max_q_len, max_seq_len, num_q_heads, num_kv_heads) bytes (else
+ * PKV_ERR_WORKSPACE), rewritten by the call: with it, contexts are cut where that spreads the
+ * work better, and the pieces merged by a second kernel; without it a few long contexts occupy
+ * one SM for each KV head and 256 rows of queries. A value that is not finite in a new token may
+ * reach the rows of the same request that do not attend to it.
  * ------------------------------------------------------------------------------------- */
 size_t pkv_extend_workspace_size(int32_t max_reqs, int32_t max_q_len, int32_t num_q_heads,
                                  int32_t head_dim, int32_t chunk_budget_tokens);
 size_t pkv_extend_fp8_workspace_size(int32_t max_reqs, int32_t batch_reqs, int32_t max_seq_len,
                                      int32_t max_blocks, int32_t num_kv_heads, int32_t head_dim);
+size_t pkv_extend_block_workspace_size(int32_t max_q_len, int32_t max_seq_len, int32_t num_q_heads,
+                                       int32_t num_kv_heads);
 pkv_status pkv_extend_attn(const void* q, const void* k_new, const void* v_new, int64_t num_tokens,
                            const int32_t* cu_q, const int32_t* seq_lens, pkv_cache cache,
                            const int32_t* block_tables, int32_t max_blocks, pkv_reqs reqs,

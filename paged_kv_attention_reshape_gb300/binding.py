@@ -410,7 +410,8 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
     cache (uint8 / float8 codes with per-tensor scales) is read as codes and converted in the
     kernel at head_dim 128; at head_dim 64 it is gathered into a bf16 workspace of the set's
     context first (allocated here when not given). k_scale / v_scale may be fp32 tensors
-    [num_blocks, Hkv], a scale for each block and KV head (head_dim 128)."""
+    [num_blocks, Hkv], a scale for each block and KV head (head_dim 128); the workspace then holds the
+    partial results of contexts that are cut (allocated here when not given)."""
     lib = _lib.load()
     for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
         _need(t, torch.bfloat16, n)
@@ -429,13 +430,19 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
     if cache.kv_dtype == _lib.KV_FP8_E4M3:
         need = extend_fp8_workspace_size(reqs.max_reqs, reqs.batch_reqs, max_seq_len, block_tables.shape[1],
                                          cache.num_kv_heads, cache.head_dim)
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif cache.kv_dtype == _lib.KV_FP8_E4M3_BLOCK:
+        need = extend_block_workspace_size(max_q_len, max_seq_len, Hq, cache.num_kv_heads)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _check(lib.pkv_extend_attn(_ptr(q), _ptr(k_new), _ptr(v_new), T, _ptr(cu_q), _ptr(seq_lens), cache,
                                _ptr(block_tables), block_tables.shape[1], reqs.c(), Hq, max_q_len,
                                max_seq_len, chunk_budget_tokens, _scale(scale, D), _ptr(out),
                                _ptr(lse), _ptr(workspace) if need else None, need, _stream(stream)), "extend_attn")
     return out, lse
+
+
+def extend_block_workspace_size(max_q_len, max_seq_len, num_q_heads, num_kv_heads) -> int:
+    return int(_lib.load().pkv_extend_block_workspace_size(max_q_len, max_seq_len, num_q_heads, num_kv_heads))
 
 
 def extend_fp8_workspace_size(max_reqs, batch_reqs, max_seq_len, max_blocks, num_kv_heads, head_dim) -> int:

@@ -688,7 +688,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
                                 int32_t max_blocks, pkv_reqs reqs, int32_t Hq, int32_t Hkv,
                                 int32_t D, int32_t max_q_len, int32_t max_seq_len, float scale,
                                 void* out, float* lse, pkv_stream_t stream, int ctx_kind = kAttnCtxBf16,
-                                float ctx_k_scale = 1.f, float ctx_v_scale = 1.f) {
+                                float ctx_k_scale = 1.f, float ctx_v_scale = 1.f, void* workspace = nullptr) {
   pkv_status st = check_reqs(reqs);
   if (st != PKV_OK) return st;
   if (cache != nullptr && (st = check_cache(*cache, true, true)) != PKV_OK) return st;
@@ -748,7 +748,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   for (int32_t off = 0; off < reqs.max_reqs && st == PKV_OK; off += kAttnSetChunk) {
     p.set_offset = off;
     p.sched_slot = next_sched_slot();
-    st = cuda_status(packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, reinterpret_cast<cudaStream_t>(stream), &launches)
+    st = cuda_status(packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, workspace, reinterpret_cast<cudaStream_t>(stream), &launches)
                             : launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
                                                reinterpret_cast<cudaStream_t>(stream), &launches));
   }
@@ -786,6 +786,11 @@ size_t pkv_extend_fp8_workspace_size(int32_t max_reqs, int32_t batch_reqs, int32
   return fp8_extend_layout(max_reqs, batch_reqs, max_seq_len, max_blocks, num_kv_heads, head_dim).bytes;
 }
 
+size_t pkv_extend_block_workspace_size(int32_t max_q_len, int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads) {
+  if (max_q_len <= 0 || max_seq_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0) return 0;
+  return attn_scaled_workspace(max_q_len, max_seq_len, num_q_heads / num_kv_heads);
+}
+
 pkv_status pkv_extend_attn(const void* q, const void* k_new, const void* v_new, int64_t num_tokens,
                            const int32_t* cu_q, const int32_t* seq_lens, pkv_cache cache,
                            const int32_t* block_tables, int32_t max_blocks, pkv_reqs reqs,
@@ -793,10 +798,14 @@ pkv_status pkv_extend_attn(const void* q, const void* k_new, const void* v_new, 
                            int32_t chunk_budget_tokens, float scale, void* out, float* lse,
                            void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
   if (chunk_budget_tokens < 0) return PKV_ERR_INVALID_ARG;
-  if (cache.kv_dtype == PKV_KV_FP8_E4M3_BLOCK)
+  if (cache.kv_dtype == PKV_KV_FP8_E4M3_BLOCK) {
+    if (workspace != nullptr && (!aligned16(workspace) || workspace_bytes < pkv_extend_block_workspace_size(
+                                     max_q_len, max_seq_len, num_q_heads, cache.num_kv_heads)))
+      return PKV_ERR_WORKSPACE;
     return run_attention(q, k_new, v_new, num_tokens, cu_q, seq_lens, &cache, block_tables, max_blocks, reqs,
                          num_q_heads, cache.num_kv_heads, cache.head_dim, max_q_len, max_seq_len, scale, out, lse,
-                         stream, kAttnCtxBlock);
+                         stream, kAttnCtxBlock, 1.f, 1.f, workspace);
+  }
   if (cache.kv_dtype != PKV_KV_FP8_E4M3)
     return run_attention(q, k_new, v_new, num_tokens, cu_q, seq_lens, &cache, block_tables,
                          max_blocks, reqs, num_q_heads, cache.num_kv_heads, cache.head_dim,

@@ -36,13 +36,19 @@
 // softmax, which one would else do for all (a slot's step 1050 clocks against 2000 to 2700). The
 // copies' states are joined with the slots' at the end. There are more converter warps, a fifth buffer in
 // place of the second Q tile, and S is read 32 columns at a time, for which no registers need to change
-// hands. 32 x 4 tokens over contexts of 1K to 4K, Hq 64 / Hkv 8: 66 us, 93 by the general launch.
+// hands. 32 x 4 tokens over contexts of 1K to 4K, Hq 64 / Hkv 8: 66 us, 93 by the general launch (before
+// either had a plan).
+//
+// Few items. With a workspace, items that are longer than a CTA's part of all, or that would leave CTAs idle
+// in a last round, are dealt as equal shares of key tiles; a cut item's pieces leave fp32 partials, which
+// a second kernel merges by their maxima and sums. (The plan is the same whoever claims what, so the
+// results do not depend on timing.)
 //
 // What bounds it. Many rows: tensor core and shared memory together (a key tile of 256 rows takes 4000
 // clocks; its products alone 2200, their operands' and the conversions' reads and writes of shared
-// memory 2500): 8 x 512 tokens over 4K to 32K 1.98 ms, 0.65 of the measured bf16 rate, 2048 tokens over
-// 100K 6.17 ms, 0.58. FEW: the same for a tile of which only every copy's part is new, 2500 clocks of
-// products and conversions a key tile; 0.38 of the measured HBM rate.
+// memory 2500): 8 x 512 tokens over 4K to 32K 2.00 ms, 0.64 of the measured bf16 rate, 2048 tokens over
+// 100K 5.33 ms, 0.66. FEW: the same for a tile of which only every copy's part is new, 2500 clocks of
+// products and conversions a key tile: 32 x 4 tokens over 1K to 4K 69 us, 0.36 of the measured HBM rate.
 //
 // Roles (12 warps, or 16 in FEW, one CTA per SM, persistent):
 //   warps 0-3, 4-7  softmax of slot 0, 1 (thread t owns row t = TMEM lane t) and the epilogue
@@ -84,6 +90,8 @@ struct AsBase {
   // five buffers, P V of tile k + 1) is done, which needs P of tile k + 1 (of tile k, in a split item,
   // where the products P V are issued in order): every reader is past tile k.
   static constexpr int SCALE_RING = 4;
+  // Key tiles of a share, at least: 4 tokens over 32,000, Hkv 1: 47 us with 4, 37 with 8, 38 with 12, 41 with 16.
+  static constexpr int MIN_TILES = 8;
   static constexpr uint32_t IDESC_QK = tc::idesc_f16(128, 128, 0, 0);
   static constexpr uint32_t IDESC_PV = tc::idesc_f16(128, D, 0, 1), IDESC_PV_NEW = tc::idesc_bf16(128, D, 0, 1);
 };
@@ -103,20 +111,24 @@ struct AsCfg : AsBase {
   static constexpr int NK = FEW ? 4 : 2, NV = FEW ? 2 : 0, NCONV = NK + NV;
   static constexpr int WARPS = W_CONV + NCONV, THREADS = WARPS * 32;
   // The general launch has 168 registers a thread; the softmax warpgroups hold a whole row of S and take
-  // more, the third warpgroup gives them up.
-  static constexpr int REGS_SOFTMAX = 192, REGS_OTHER = 120;
+  // more, the third warpgroup gives them up. (8 x 512 tokens over 4K-32K: 184 and 136 registers 2.07 ms, 192
+  // and 120 2.04, 200 and 104 1.99; 208 and 88 spill, 2.60.)
+  static constexpr int REGS_SOFTMAX = 200, REGS_OTHER = 104;
   static_assert(FEW || 256 * REGS_SOFTMAX + 128 * REGS_OTHER == THREADS * 168, "register split");
   static constexpr int NBUF = FEW ? 5 : 4;           // K/V ring: one tile per buffer
   static constexpr int NQ = FEW ? 1 : 2;             // Q tiles of an item
+  static constexpr int ROWS = NQ * 128;
   static constexpr int RING_OFF = NQ * TILE_BYTES;
   static constexpr int REQ_OFF = RING_OFF + NBUF * TILE_BYTES;  // int4 {r, row0, q_len, C}
   static constexpr int START_OFF = REQ_OFF + MAXR * 16;
   static constexpr int PERM_OFF = START_OFF + (MAXR + 2) * 4;   // set positions by cost, heaviest first
+  static constexpr int WHOLE_OFF = PERM_OFF + MAXR * 4;         // items that are dealt whole
+  static constexpr int TAIL_OFF = WHOLE_OFF + MAXR * 4;         // prefix of the key tiles of those in shares
   // output staging: per softmax warp, 32 rows x 32 bf16 columns (64-byte rows, 64-byte swizzle)
-  static constexpr int STAGE_OFF = (PERM_OFF + MAXR * 4 + 127) / 128 * 128;
+  static constexpr int STAGE_OFF = (TAIL_OFF + MAXR * 4 + 127) / 128 * 128;
   static constexpr int ITEM_READERS = 1 + 8 + NCONV;
   static constexpr int ITEM_OFF = STAGE_OFF + 8 * STAGE_WARP_BYTES;
-  static constexpr int SCALE_OFF = (ITEM_OFF + ITEM_RING * 8 + 15) / 16 * 16;
+  static constexpr int SCALE_OFF = ITEM_OFF + ITEM_RING * 48;
   static constexpr int FACTOR_OFF = SCALE_OFF + SCALE_RING * 2 * TBLK * 4;
   static constexpr int MERGE_OFF = FACTOR_OFF + SCALE_RING * TBLK * 16;  // slot 1's {m, l} by row (split items)
   static constexpr int REP_OFF = MERGE_OFF + 128 * 8;            // slot 0's {m, l} by row (FEW)
@@ -128,14 +140,35 @@ struct AsCfg : AsBase {
 __device__ __forceinline__ constexpr uint32_t as_scol(int slot) { return slot * 128u; }
 __device__ __forceinline__ constexpr uint32_t as_ocol(int slot) { return 256u + slot * 128u; }
 
+// What a launch leaves in the workspace: {shares} | per share the cut item that begins in it | per slot (two a
+// share: of the item that is cut at its start, and of the one at its end) {m, l} of a piece's rows | its O.
+struct AsPartials {
+  int* head;
+  int4* items;  // two a share: {pieces (0: none), the request's first row, the item's, KV head}, {rows, -, -, -}
+  float2* ml;   // [slot][ROWS]
+  float4* o;    // [slot][32 column quads][ROWS]
+};
+__host__ __device__ __forceinline__ int64_t as_ml_off(int slots) { return 128 + slots * 32ll; }
+__host__ __device__ __forceinline__ int64_t as_o_off(int slots, int rows) { return as_ml_off(slots) + 8ll * slots * rows; }
+__host__ __device__ __forceinline__ int64_t as_ws_bytes(int slots, int rows) { return as_o_off(slots, rows) + 512ll * slots * rows; }
+__device__ __forceinline__ AsPartials as_partials(char* ws, int slots, int rows) {
+  return AsPartials{reinterpret_cast<int*>(ws), reinterpret_cast<int4*>(ws + 128), reinterpret_cast<float2*>(ws + as_ml_off(slots)),
+                    reinterpret_cast<float4*>(ws + as_o_off(slots, rows))};
+}
+
+// A piece of work, published in shared memory by the producer.
 struct AsItem {
-  int r, q_len, C;      // request, new tokens, cached tokens
+  int r, q_len;         // request, new tokens
+  int row0;             // the request's first row of q
   int kh;               // KV head
   int base;             // first of the item's rows (rows of the request: token * G + head of the group)
   int split;            // 1: one tile of rows, key tiles dealt to the two slots
-  int nct, NT;          // context key tiles, all key tiles
-  int64_t row0;         // the request's first row of q
+  int slot;             // of its partial; -1: the item is whole
+  int j0;               // the piece's first key tile; from there on:
+  int C, nct, NT;       // cached tokens and their key tiles (none if negative), all key tiles (0: no more work)
+  int unused;
 };
+static_assert(sizeof(AsItem) == 48, "ring entry");
 __device__ __forceinline__ int as_pairs(const int4& q, int G) { return (q.z * G + 255) / 256; }
 // FEW: rows of a copy. A tile of up to 32 (64) rows holds four (two) copies of them, each of which takes
 // its own quarter (half) of every key tile, so that all four warps have the same part of the softmax.
@@ -143,30 +176,32 @@ __device__ __forceinline__ int as_span(int rows) { return rows <= 32 ? 32 : rows
 // Key tiles an item of the request walks at most: the schedule's order.
 __device__ __forceinline__ int as_cost(const int4& q) { return (q.w + 127) / 128 + (q.z + 127) / 128; }
 
-// Work item w: s_req holds {request id, first query row, q_len, cached tokens} of each request of the
-// set, s_perm the set positions by decreasing cost, s_start the prefix of items in that order.
+// Item idx of a request {request id, first query row, q_len, cached tokens}, as a whole.
 template <bool FEW>
-__device__ __forceinline__ AsItem as_item(const AttnParams& p, const int* s_start, const int4* s_req, const int* s_perm,
-                                          int n, int w) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s_start[mid] <= w) lo = mid; else hi = mid - 1;
-  }
-  const int4 q = s_req[s_perm[lo]];
-  const int idx = w - s_start[lo];
+__device__ __forceinline__ AsItem as_item(const AttnParams& p, const int4& q, int idx) {
   AsItem it;
   it.r = q.x;
   it.row0 = q.y;
   it.q_len = q.z;
-  it.C = q.w;
   it.kh = idx % p.Hkv;
   it.base = 256 * (as_pairs(q, p.G) - 1 - idx / p.Hkv);  // later (heavier) rows of a request first
   const int rows = min(256, q.z * p.G - it.base);
   it.split = FEW || rows <= 128;
-  it.nct = (it.C + 127) / 128;
+  it.slot = -1;
+  it.j0 = 0;
+  it.C = q.w;
+  it.nct = (q.w + 127) / 128;
   it.NT = it.nct + (it.base + rows - 1) / p.G / 128 + 1;
   return it;
+}
+// The last rank whose prefix is at most x.
+__device__ __forceinline__ int as_rank(const int* prefix, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
 }
 
 // Counters of claimed items and of finished CTAs; launch k uses slot k % kAttnSchedSlots and its last
@@ -211,25 +246,18 @@ __device__ __forceinline__ bool as_wait1(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
-// The k-th work item (-1: no more, or a wait gave up). Lane 0 reads the entry and frees it.
-__device__ __forceinline__ int as_take(const int* s_item, AsBars& bar, uint32_t k, volatile int* abort_flag,
-                                       unsigned int* err, int lane) {
-  const int e = static_cast<int>(k % AsBase::ITEM_RING);
-  if (!as_wait(&bar.item_full[e], (k / AsBase::ITEM_RING) & 1, abort_flag, err)) return -1;
-  int w = 0;
-  if (lane == 0) {
-    w = *reinterpret_cast<const volatile int*>(&s_item[e]);
-    mbar_arrive(&bar.item_empty[e]);
-  }
-  return __shfl_sync(0xffffffffu, w, 0);
+// The k-th piece of work (null: no more, or a wait gave up). A reader frees it when it is through.
+template <bool FEW>
+__device__ __forceinline__ const AsItem* as_take(const uint8_t* smem, AsBars& bar, uint32_t k, volatile int* abort_flag,
+                                                 unsigned int* err) {
+  const uint32_t e = k % AsBase::ITEM_RING;
+  if (!as_wait(&bar.item_full[e], (k / AsBase::ITEM_RING) & 1, abort_flag, err)) return nullptr;
+  const AsItem* it = reinterpret_cast<const AsItem*>(smem + AsCfg<FEW>::ITEM_OFF) + e;
+  return it->NT > 0 ? it : nullptr;
 }
-
-__device__ __forceinline__ int as_take1(const int* s_item, AsBars& bar, uint32_t k, volatile int* abort_flag, unsigned int* err) {
-  const int e = static_cast<int>(k % AsBase::ITEM_RING);
-  if (!as_wait1(&bar.item_full[e], (k / AsBase::ITEM_RING) & 1, abort_flag, err)) return -1;
-  const int w = *reinterpret_cast<const volatile int*>(&s_item[e]);
-  mbar_arrive(&bar.item_empty[e]);
-  return w;
+__device__ __forceinline__ void as_free(AsBars& bar, uint32_t k, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar.item_empty[k % AsBase::ITEM_RING]);
 }
 
 // ---- conversions ------------------------------------------------------------------------------------
@@ -297,7 +325,7 @@ template <bool FEW>
 __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
     attn_scaled_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ck,
-                       const __grid_constant__ CUtensorMap tm_cv) {
+                       const __grid_constant__ CUtensorMap tm_cv, char* ws, int ws_slots) {
   using C = AsCfg<FEW>;
   constexpr int D = C::D;
   extern __shared__ uint8_t smem_raw[];
@@ -307,11 +335,12 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
   int* s_start = reinterpret_cast<int*>(smem + C::START_OFF);
   int* s_perm = reinterpret_cast<int*>(smem + C::PERM_OFF);
   int4* s_req = reinterpret_cast<int4*>(smem + C::REQ_OFF);
-  int* s_item = reinterpret_cast<int*>(smem + C::ITEM_OFF);
+  int* s_whole = reinterpret_cast<int*>(smem + C::WHOLE_OFF);
+  int* s_tail = reinterpret_cast<int*>(smem + C::TAIL_OFF);
   AsBars& bar = *reinterpret_cast<AsBars*>(smem + C::BAR_OFF);
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int s_scan[C::WARPS];
+  __shared__ int s_plan[3];  // items dealt whole; key tiles dealt in shares; tiles of a share
 
   pdl_wait();
   pdl_release();
@@ -391,27 +420,85 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
     s_perm[rank] = i;
   }
   __syncthreads();
-  // exclusive prefix of the requests' items in that order (n <= MAXR <= THREADS)
-  static_assert(C::MAXR <= C::THREADS, "one request a thread");
-  {
-    const int t = tid < n ? p.Hkv * as_pairs(s_req[s_perm[tid]], p.G) : 0;
-    int x = t;
+  // Plan, by one warp: lane i has the ranks from i * PER on. Items are claimed whole, longest first, unless
+  //  - one is longer than 1.2 times a CTA's part of all: then all are dealt as equal shares of key tiles;
+  //  - they are nearly alike and the last round would leave a fifth of the CTAs idle: then its items are.
+  // (One context of 32,000 tokens for one KV head and 4 new tokens 322 us whole and 37 us in shares; 2048
+  // tokens over 100K, 512 items in 3.4 rounds, 6.16 and 5.33 ms. Contexts from 1K to 4K for 256 items
+  // balance to 5% whole; a share's two ends cost it some ten tiles.)
+  if (warp == 0) {
+    constexpr int PER = C::MAXR / 32;
+    const int grid = gridDim.x;
+    int64_t all = 0;
+    int count = 0, longest = 0, shortest = INT_MAX;
+#pragma unroll 1
+    for (int i = lane * PER; i < min(n, lane * PER + PER); ++i) {
+      const int4 q = s_req[s_perm[i]];
+      const int items = p.Hkv * as_pairs(q, p.G), cost = as_cost(q);
+      if (items > 0) {
+        all += static_cast<int64_t>(items) * cost;
+        count += items;
+        longest = max(longest, cost);
+        shortest = min(shortest, cost);
+      }
+    }
+    int before = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+      all += __shfl_xor_sync(0xffffffffu, all, o);
     }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) x += s_scan[w];
-    if (tid < n) s_start[tid] = x - t;
-    if (tid == C::THREADS - 1) s_start[n] = x;
+    const int items_all = __shfl_sync(0xffffffffu, before, 31);
+    before -= count;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    shortest = __reduce_min_sync(0xffffffffu, shortest);
+    int whole_all = items_all;
+    if (ws != nullptr && longest > C::MIN_TILES) {
+      if (5ll * longest * grid > 6 * all)
+        whole_all = 0;
+      else if (5ll * shortest >= 4ll * longest && items_all % grid <= grid / 5 * 4)
+        whole_all = items_all / grid * grid;
+    }
+    int tail = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      int at = before, sum = tail;
+      for (int i = lane * PER; i < min(n, lane * PER + PER); ++i) {
+        const int4 q = s_req[s_perm[i]];
+        const int items = p.Hkv * as_pairs(q, p.G), whole = min(max(whole_all - at, 0), items);
+        if (pass == 1) {
+          s_start[i] = min(at, whole_all);
+          s_whole[i] = whole;
+          s_tail[i] = sum;
+        }
+        at += items;
+        sum += (items - whole) * as_cost(q);
+      }
+      if (pass == 0) {  // to the exclusive prefix
+        const int own = sum;
+        tail = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, tail, o);
+          if (lane >= o) tail += y;
+        }
+        const int total = __shfl_sync(0xffffffffu, tail, 31);
+        tail -= own;
+        if (lane == 0) {
+          s_plan[0] = whole_all;
+          s_plan[1] = total;
+          s_plan[2] = max(C::MIN_TILES, (total + grid - 1) / grid);
+        }
+      }
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
-  const int W = s_start[n];
+  const int shares = (s_plan[1] + s_plan[2] - 1) / s_plan[2], W = s_plan[0] + shares;
+  if (ws != nullptr && blockIdx.x == 0 && tid == 0) *as_partials(ws, ws_slots, C::ROWS).head = shares;
 
   if (warp < 8) {
     if constexpr (!FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
@@ -424,13 +511,14 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
     uint32_t tile0 = 0;       // the CTA's key tiles before this item
     uint32_t par = 0;         // parities of the items whose slot 1 has an O (bit 0), of the merges (bit 1)
     for (uint32_t k = 0;; ++k) {
-      const int w = as_take(s_item, bar, k, &s_abort, p.err, lane);
-      if (w < 0) break;
+      const AsItem* taken = as_take<FEW>(smem, bar, k, &s_abort, p.err);
+      if (taken == nullptr) break;
       float m = -CUDART_INF_F, l = 0.f;
       {
-        const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
+        const AsItem it = *taken;
         if (slot == 1 && it.split && it.NT == 1) {  // its one key tile is slot 0's
           tile0 += it.NT;
+          as_free(bar, k, lane);
           continue;
         }
         const int tok = (it.base + (it.split ? 0 : slot * 128) + t) / p.G;  // this row's token
@@ -527,8 +615,9 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         if (!ok) break;
         tile0 += it.NT;
       }
-      // ---- epilogue (the item found again, so that its fields need not stay in registers above) ----
-      const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
+      // ---- epilogue (the item read again, so that its fields need not stay in registers above) ----
+      const AsItem it = reinterpret_cast<const AsItem*>(smem + C::ITEM_OFF)[k % C::ITEM_RING];
+      as_free(bar, k, lane);
       const bool both = it.split && it.NT > 1;  // two states of the same rows
       float2* mrg = reinterpret_cast<float2*>(smem + C::MERGE_OFF);
       if (both && slot == 1) {
@@ -556,11 +645,40 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       }
       if (both || !it.split) par ^= 1;
       tc::fence_after_sync();
+      if (it.slot >= 0) {  // a piece: its O over 2^m and {m, l} to the workspace
+        const AsPartials part = as_partials(ws, ws_slots, C::ROWS);
+        const int row = (it.split ? 0 : slot * 128) + t;
+        part.ml[static_cast<int64_t>(it.slot) * C::ROWS + row] = make_float2(m, l);
+        float4* dst = part.o + static_cast<int64_t>(it.slot) * 32 * C::ROWS + row;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32], o1[32];
+          tc::ld32(tmem + lane_off + as_ocol(slot) + c * 32, o);
+          tc::ld32(tmem + lane_off + as_ocol(both ? 1 : slot) + c * 32, o1);
+          tc::wait_ld();
+          tc::touch32(o);
+          tc::touch32(o1);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] = __uint_as_float(o[e + i]) * w0;
+              if (both) x[i] = fmaf(__uint_as_float(o1[e + i]), w1, x[i]);
+            }
+            dst[static_cast<int64_t>(c * 8 + e / 4) * C::ROWS] = make_float4(x[0], x[1], x[2], x[3]);
+          }
+        }
+        tc::fence_before_sync();
+        if (both) mbar_arrive(&bar.merge_done);
+        continue;
+      }
       const int base = it.base + (it.split ? 0 : slot * 128);  // the tile's first row of the request
       // flat row of [T * Hq] of tile row tr, or -1 for a row that is not there
       auto flat_row = [&](int tr) -> int64_t {
         const int rr = base + tr, tok = rr / p.G;
-        return tok < it.q_len && it.row0 + tok < p.num_tokens ? (it.row0 + tok) * p.Hq + it.kh * p.G + rr % p.G : -1;
+        const int64_t tk = static_cast<int64_t>(it.row0) + tok;
+        return tok < it.q_len && tk < p.num_tokens ? tk * p.Hq + it.kh * p.G + rr % p.G : -1;
       };
       const float inv = l > 0.f ? w0 / l : 0.f, inv1 = l > 0.f ? w1 / l : 0.f;
       // O leaves through the warp's staging tile (32 rows x 32 columns at a time): each thread puts
@@ -623,9 +741,10 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
     uint32_t par = 0;         // parities of the items whose slot 1 has an O (bit 0), of the merges (bit 1)
     uint32_t rc = 0;          // phases of rep_full
     for (uint32_t k = 0;; ++k) {
-      const int w = as_take(s_item, bar, k, &s_abort, p.err, lane);
-      if (w < 0) break;
-      const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
+      const AsItem* taken = as_take<FEW>(smem, bar, k, &s_abort, p.err);
+      if (taken == nullptr) break;
+      const AsItem it = *taken;
+      as_free(bar, k, lane);
       if (slot == 1 && it.NT == 1) {  // its one key tile is slot 0's
         tile0 += 1;
         continue;
@@ -760,7 +879,9 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         const float2 o = rml[i];
         ll += o.x == -CUDART_INF_F ? 0.f : o.y * ex2_approx(o.x - mm);
       }
-      const float wr = ll > 0.f && m != -CUDART_INF_F ? ex2_approx(m - mm) / ll : 0.f;
+      const bool whole = it.slot < 0;
+      const AsPartials part = as_partials(ws, ws_slots, C::ROWS);
+      const float wr = m == -CUDART_INF_F ? 0.f : whole ? (ll > 0.f ? ex2_approx(m - mm) / ll : 0.f) : ex2_approx(m - mm);
       w0 *= wr, w1 *= wr;
       tc::fence_after_sync();
       const int rows = min(it.q_len, static_cast<int>(min(static_cast<int64_t>(it.q_len), p.num_tokens - it.row0))) * p.G;
@@ -805,8 +926,12 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
               x[4 * h + 3] += __uint_as_float(y.w);
             }
           }
-          if (rr < rows) {
-            const int64_t fr = (it.row0 + (rr >> g_log)) * p.Hq + it.kh * p.G + (rr & (p.G - 1));
+          if (!whole) {  // a piece: its O over 2^m to the workspace
+            float4* dst = part.o + (static_cast<int64_t>(it.slot) * 32 + c * 8 + kk * 2) * C::ROWS + rr;
+            dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+            dst[C::ROWS] = make_float4(x[4], x[5], x[6], x[7]);
+          } else if (rr < rows) {
+            const int64_t fr = (static_cast<int64_t>(it.row0) + (rr >> g_log)) * p.Hq + it.kh * p.G + (rr & (p.G - 1));
             *reinterpret_cast<uint4*>(p.out + fr * D + c * 32 + kk * 8) =
                 make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
           }
@@ -819,8 +944,10 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       if (!ok) break;
       tc::fence_before_sync();
       if (both) mbar_arrive(&bar.merge_done);
-      if (p.lse && t < min(span, rows))
-        p.lse[(it.row0 + tok) * p.Hq + it.kh * p.G + (row & (p.G - 1))] =
+      if (!whole) {
+        if (t < span) part.ml[static_cast<int64_t>(it.slot) * C::ROWS + t] = make_float2(mm, ll);
+      } else if (p.lse && t < min(span, rows))
+        p.lse[(static_cast<int64_t>(it.row0) + tok) * p.Hq + it.kh * p.G + (row & (p.G - 1))] =
             ll > 0.f ? (mm + __log2f(ll)) * 0.69314718055994531f : -CUDART_INF_F;
     }
     }
@@ -837,21 +964,60 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       }
       uint32_t kvc = 0;
       bool ok = true;
+      AsItem* s_item = reinterpret_cast<AsItem*>(smem + C::ITEM_OFF);
+      int share = 0, pos = 0, end = 0;  // the share whose pieces are being dealt: tiles [pos, end) of the tail
       for (uint32_t items = 0; ok; ++items) {
-        // take the next item once the Q buffer is free, and publish it to the other roles
+        // take the next piece once the Q buffer is free, and publish it to the other roles
         if (items > 0 && !as_wait(&bar.q_empty, (items - 1) & 1, &s_abort, p.err)) break;
         const int e = static_cast<int>(items % C::ITEM_RING);
         if (items >= C::ITEM_RING && !as_wait(&bar.item_empty[e], (items / C::ITEM_RING - 1) & 1, &s_abort, p.err)) break;
-        int w = 0;
+        AsItem it;
+        for (;;) {
+          if (pos >= end) {
+            int w = 0;
+            if (lane == 0) w = static_cast<int>(atomicAdd(&g_as_next[p.sched_slot], 1u));
+            w = __shfl_sync(0xffffffffu, w, 0);
+            if (w >= W) {
+              it.NT = 0;
+              break;
+            }
+            if (w < s_plan[0]) {
+              const int lo = as_rank(s_start, n, w);
+              it = as_item<FEW>(p, s_req[s_perm[lo]], w - s_start[lo]);
+              break;
+            }
+            share = w - s_plan[0];
+            pos = share * s_plan[2];
+            end = min(pos + s_plan[2], s_plan[1]);
+            if (lane == 0) as_partials(ws, ws_slots, C::ROWS).items[2 * share] = make_int4(0, 0, 0, 0);
+          }
+          // the item at tile pos of the tail, and the part of it that lies in the share
+          const int lo = as_rank(s_tail, n, pos);
+          const int4 q = s_req[s_perm[lo]];
+          const int cost = as_cost(q), k = (pos - s_tail[lo]) / cost, first = s_tail[lo] + k * cost, from = pos - first;
+          pos = min(first + cost, end);
+          it = as_item<FEW>(p, q, s_whole[lo] + k);
+          if (from >= it.NT) continue;  // (an item of earlier rows has fewer tiles than its request's cost)
+          const int pieces = (first + it.NT - 1) / s_plan[2] - first / s_plan[2] + 1;
+          if (pieces > 1) {
+            if (from == 0 && lane == 0) {
+              int4* entry = as_partials(ws, ws_slots, C::ROWS).items + 2 * share;
+              entry[0] = make_int4(pieces, it.row0, it.base, it.kh);
+              entry[1] = make_int4(min(256, q.z * p.G - it.base), 0, 0, 0);
+            }
+            it.slot = 2 * share + (from == 0 ? 1 : 0);
+            it.j0 = from;
+            it.C -= from * 128;
+            it.nct -= from;
+            it.NT = min(it.NT, pos - first) - from;
+          }
+          break;
+        }
         if (lane == 0) {
-          w = static_cast<int>(atomicAdd(&g_as_next[p.sched_slot], 1u));
-          if (w >= W) w = -1;
-          *reinterpret_cast<volatile int*>(&s_item[e]) = w;
+          s_item[e] = it;
           mbar_arrive(&bar.item_full[e]);
         }
-        w = __shfl_sync(0xffffffffu, w, 0);
-        if (w < 0) break;
-        const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
+        if (it.NT == 0) break;
         if (lane == 0) {
           const int nq = it.split ? 1 : 2;
           mbar_arrive_expect_tx(&bar.q_full, nq * C::TILE_BYTES);
@@ -859,9 +1025,9 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
               tma_load_4d(sQ + s * C::TILE_BYTES + hf * C::HALF_BYTES, &tm_q, &bar.q_full, 0, hf, it.kh * p.G,
-                          static_cast<int>(it.row0) + (it.base + s * 128) / p.G);
+                          it.row0 + (it.base + s * 128) / p.G);
         }
-        const int32_t* table = p.block_tables + static_cast<int64_t>(it.r) * p.max_blocks;
+        const int32_t* table = p.block_tables + static_cast<int64_t>(it.r) * p.max_blocks + it.j0 * 8;
         const int ctx_blocks = (it.C + 15) / 16;
         // a tile's table entries (lanes 0..7, a block each) are read a tile ahead: the loads are on a
         // split item's critical path
@@ -902,7 +1068,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
               if (ctx) tma_load_4d(dst + C::HALF_BYTES + lane * 2048, sel ? &tm_cv : &tm_ck, &bar.kv_full[b], 0, it.kh, 0, blk);
             }
             if (!ctx && lane == 0) {
-              const int row = static_cast<int>(it.row0) + (j - it.nct) * 128;
+              const int row = it.row0 + (j - it.nct) * 128;
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf)
                 tma_load_3d(dst + hf * C::HALF_BYTES, sel ? &tm_v : &tm_k, &bar.kv_full[b], 0, it.kh * 2 + hf, row);
@@ -952,9 +1118,11 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
           return true;
         };
         for (uint32_t items = 0; ok; ++items) {
-          const int w = as_take1(s_item, bar, items, &s_abort, p.err);
-          if (w < 0) break;
-          const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
+          const uint32_t e = items % C::ITEM_RING;
+          if (!as_wait1(&bar.item_full[e], (items / C::ITEM_RING) & 1, &s_abort, p.err)) break;
+          const AsItem it = reinterpret_cast<const AsItem*>(smem + C::ITEM_OFF)[e];
+          mbar_arrive(&bar.item_empty[e]);
+          if (it.NT == 0) break;
           if (!as_wait1(&bar.q_conv, items & 1, &s_abort, p.err)) break;
           if (it.split) {
             // key tile j goes to slot j % 2: S(j) and the other slot's O += P V of tile j - 1, whichever has
@@ -1030,9 +1198,10 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       uint32_t kvc = 0;
       bool ok = true;
       for (uint32_t k = 0; ok; ++k) {
-        const int w = as_take(s_item, bar, k, &s_abort, p.err, lane);
-        if (w < 0) break;
-        const AsItem it = as_item<FEW>(p, s_start, s_req, s_perm, n, w);
+        const AsItem* taken = as_take<FEW>(smem, bar, k, &s_abort, p.err);
+        if (taken == nullptr) break;
+        const AsItem it = *taken;
+        as_free(bar, k, lane);
         if (!of_v) {
           if (!as_wait(&bar.q_full, k & 1, &s_abort, p.err)) break;
           if constexpr (FEW) {
@@ -1105,23 +1274,101 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
   }
 }
 
+// The pieces of the items that were cut, joined by their maxima and sums. A CTA takes 32 rows and 32 columns of
+// an item at a time: a warp four of the columns, a thread one of the rows.
+constexpr int kMergeShares = 1024;  // CTAs of a launch of the kernel above, at most
+__global__ void __launch_bounds__(256) attn_scaled_merge_kernel(const AttnParams p, char* ws, int ws_slots, int ROWS) {
+  __shared__ int s_cut[kMergeShares], s_warp[8], s_count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_count = 0;
+  pdl_wait();
+  pdl_release();
+  const AsPartials part = as_partials(ws, ws_slots, ROWS);
+  const int shares = *part.head;
+  __syncthreads();
+  for (int i0 = 0; i0 < shares; i0 += 256) {  // the shares in which a cut item begins, in order
+    const bool cut = i0 + tid < shares && part.items[2 * (i0 + tid)].x > 0;
+    const uint32_t mask = __ballot_sync(0xffffffffu, cut);
+    if (lane == 0) s_warp[warp] = __popc(mask);
+    __syncthreads();
+    int at = s_count + __popc(mask & ((1u << lane) - 1u));
+    for (int w = 0; w < warp; ++w) at += s_warp[w];
+    if (cut) s_cut[at] = i0 + tid;
+    __syncthreads();
+    if (tid == 255) s_count = at + (cut ? 1 : 0);
+    __syncthreads();
+  }
+  const int per = ROWS / 32 * 4, units = s_count * per;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int share = s_cut[u / per], part_of = u % per;
+    const int4 it = part.items[2 * share];
+    const int np = it.x, rows = part.items[2 * share + 1].x;
+    const int row = part_of / 4 * 32 + lane, c4 = part_of % 4 * 8 + warp;
+    if (part_of / 4 * 32 >= rows) continue;
+    // piece 0 is in slot 2 share + 1, piece i in 2 (share + i)
+    auto ml = [&](int i) { return part.ml[static_cast<int64_t>(2 * (share + i) + (i == 0)) * ROWS + row]; };
+    float m = -CUDART_INF_F, l = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < np; ++i) m = fmaxf(m, ml(i).x);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < np; ++i) {
+      const float2 x = ml(i);
+      const float4 y = part.o[(static_cast<int64_t>(2 * (share + i) + (i == 0)) * 32 + c4) * ROWS + row];
+      if (x.x != -CUDART_INF_F) {  // (a piece without a key for the row has no part)
+        const float w = ex2_approx(x.x - m);
+        l = fmaf(x.y, w, l);
+        s = make_float4(fmaf(y.x, w, s.x), fmaf(y.y, w, s.y), fmaf(y.z, w, s.z), fmaf(y.w, w, s.w));
+      }
+    }
+    const int rr = it.z + row;
+    const int64_t tok = static_cast<int64_t>(it.y) + rr / p.G;
+    if (row >= rows || tok >= p.num_tokens) continue;
+    const int64_t fr = tok * p.Hq + it.w * p.G + rr % p.G;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    *reinterpret_cast<uint2*>(p.out + fr * 128 + c4 * 4) = make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
+    if (p.lse && c4 == 0) p.lse[fr] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+  }
+}
+
 }  // namespace
+
+// Whether an item of such a set can be cut, and how many rows a piece has.
+static bool scaled_can_cut(int32_t max_seq_len) { return (static_cast<int64_t>(max_seq_len) + 127) / 128 + 1 > AsBase::MIN_TILES; }
+static int scaled_rows(int32_t max_q_len, int G) { return static_cast<int64_t>(max_q_len) * G <= 128 ? 128 : 256; }
+static int scaled_slots() { return 2 * num_sms(); }  // two for each CTA's share
+size_t attn_scaled_workspace(int32_t max_q_len, int32_t max_seq_len, int G) {
+  return scaled_can_cut(max_seq_len) ? static_cast<size_t>(as_ws_bytes(scaled_slots(), scaled_rows(max_q_len, G))) : 0;
+}
 
 template <bool FEW>
 static cudaError_t launch_scaled(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                 const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream) {
+                                 const CUtensorMap& tck, const CUtensorMap& tcv, char* ws, cudaStream_t stream, int* launches) {
   using C = AsCfg<FEW>;
-  const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attn_scaled_kernel<FEW>), C::SMEM,
-                                           FEW ? kAttrAttn128BlockFew : kAttrAttn128Block);
+  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attn_scaled_kernel<FEW>), C::SMEM,
+                                     FEW ? kAttrAttn128BlockFew : kAttrAttn128Block);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_scaled_kernel<FEW>, dim3(num_sms()), dim3(C::THREADS), C::SMEM, stream, p, tq, tk, tv, tck, tcv);
+  const int slots = ws != nullptr ? scaled_slots() : 0;
+  e = launch_pdl(attn_scaled_kernel<FEW>, dim3(num_sms()), dim3(C::THREADS), C::SMEM, stream, p, tq, tk, tv, tck, tcv, ws, slots);
+  *launches += 1;
+  if (e != cudaSuccess || ws == nullptr) return e;
+  *launches += 1;
+  // (launched early, behind a long kernel, the merge's waiting CTAs cost the next call 3%; behind a short one
+  // its early launch saves 3 us)
+  if constexpr (FEW) return launch_pdl(attn_scaled_merge_kernel, dim3(4 * num_sms()), dim3(256), 0, stream, p, ws, slots, C::ROWS);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4 * num_sms());
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, attn_scaled_merge_kernel, p, ws, slots, C::ROWS);
 }
 
+// ws: attn_scaled_workspace(..) bytes, or null: no item is cut.
 cudaError_t launch_attn_scaled(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream, int* launches) {
-  *launches += 1;
-  return static_cast<int64_t>(p.max_q_len) * p.G <= 128 ? launch_scaled<true>(p, tq, tk, tv, tck, tcv, stream)
-                                                        : launch_scaled<false>(p, tq, tk, tv, tck, tcv, stream);
+                               const CUtensorMap& tck, const CUtensorMap& tcv, void* workspace, cudaStream_t stream, int* launches) {
+  char* ws = scaled_can_cut(p.max_seq_len) ? static_cast<char*>(workspace) : nullptr;
+  return scaled_rows(p.max_q_len, p.G) == 128 ? launch_scaled<true>(p, tq, tk, tv, tck, tcv, ws, stream, launches)
+                                              : launch_scaled<false>(p, tq, tk, tv, tck, tcv, ws, stream, launches);
 }
 
 }  // namespace pkv

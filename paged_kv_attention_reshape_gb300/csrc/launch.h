@@ -223,8 +223,8 @@ cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_q, const
 // Extend over a block-scaled FP8 cache (head_dim 128): tm_q over q as (64, D/64, Hq, T) with boxes of a
 // group's heads (api.cu), the others as for launch_attention.
 constexpr int kAttnCtxBlock = 3;
-cudaError_t launch_attn_scaled(const AttnParams& p, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                               const CUtensorMap& tm_v, const CUtensorMap& tm_ck, const CUtensorMap& tm_cv,
-                               cudaStream_t stream, int* launches);
+cudaError_t launch_attn_scaled(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& tck, const CUtensorMap& tcv, void* workspace, cudaStream_t stream, int* launches);
+size_t attn_scaled_workspace(int32_t max_q_len, int32_t max_seq_len, int G);
 
 }  // namespace pkv

@@ -692,6 +692,71 @@ def test_extend_of_a_few_tokens_extreme_scales(what):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("ctx,new,G,Hkv", [
+    ([9001], [4], 8, 1), ([5000, 17, 700], [1, 16, 3], 8, 2), ([1100], [64], 2, 1),     # up to 128 rows
+    ([4000, 3000, 5], [200, 90, 1], 4, 2), ([2047], [700], 16, 1), ([6001], [130], 1, 3), ([900, 0], [300, 1000], 2, 1)])
+def test_extend_of_few_long_contexts(ctx, new, G, Hkv):
+    """Contexts that are cut into pieces; without a workspace they are not."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    st = extend_state(ctx, new, G * Hkv, Hkv, seed=len(ctx) + G, qs=1.5, gap=1)
+    n = pkv.launch_count()
+    out, lse = gpu_extend(st)
+    assert pkv.launch_count() == n + 2
+    check_extend(st, out, lse, SCALE)
+    kc, vc = pools(st)
+    total = torch.tensor([c + m for c, m in zip(ctx, new)], dtype=torch.int32)
+    args = [on(st[n]) for n in ("q", "k_new", "v_new", "cu", "table", "ks", "vs")]
+    q, k, v, cu, table, ks, vs = args
+    total = total.cuda()
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    lib = pkv._lib.load()
+    status = lib.pkv_extend_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), len(q), cu.data_ptr(), total.data_ptr(),
+                                 pkv.make_cache(kc, vc, ks, vs), table.data_ptr(), table.shape[1],
+                                 pkv.Reqs(max_reqs=len(ctx), batch_reqs=len(ctx)).c(), G * Hkv, max(new), int(total.max()),
+                                 0, SCALE, out.data_ptr(), lse.data_ptr(), None, 0, torch.cuda.current_stream().cuda_stream)
+    assert status == 0 and pkv.device_errors() == 0
+    check_extend(st, out, lse, SCALE)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,G,Hkv", [([4, 2], 8, 1), ([200, 90], 4, 2)])
+def test_extend_in_a_graph_with_other_lengths_and_beside_another_stream(new, G, Hkv):
+    """A captured call replayed for other contexts (cut otherwise, then not at all), and two calls at once."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    st = extend_state([6000, 1500], new, G * Hkv, Hkv, seed=40 + G)
+    kc, vc = pools(st)
+    q, k, v, cu, table, ks, vs = (on(st[n]) for n in ("q", "k_new", "v_new", "cu", "table", "ks", "vs"))
+    lens = torch.tensor([c + m for c, m in zip(st["ctx"], new)], dtype=torch.int32).cuda()
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    need = pkv.extend_block_workspace_size(max(new), 6300, G * Hkv, Hkv)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+
+    def call(out, lse, ws):
+        pkv.extend_attn(q, k, v, cu, lens, kc, vc, table, max(new), 6300, out=out, lse=lse, workspace=ws, k_scale=ks, v_scale=vs)
+
+    call(out, lse, ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, lse, ws)
+    for ctx in ([6000, 1500], [5, 700], [4001, 0], [0, 3], [6000, 1500]):
+        lens.copy_(torch.tensor([c + m for c, m in zip(ctx, new)], dtype=torch.int32))
+        out.zero_(), lse.zero_()
+        graph.replay()
+        check_extend(dict(st, ctx=ctx), out, lse, SCALE)
+    other = torch.cuda.Stream()
+    out2, lse2, ws2 = torch.zeros_like(out), torch.zeros_like(lse), torch.zeros_like(ws)
+    other.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        call(out, lse, ws)
+        with torch.cuda.stream(other):
+            call(out2, lse2, ws2)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    check_extend(st, out2, lse2, SCALE)
+    assert pkv.device_errors() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("most", [3, 200])
 def test_extend_cuts_and_flags_more_tokens_than_its_bound(most):
     """A request with more new tokens than max_q_len: its first max_q_len rows are right, the others stay as they were."""
@@ -916,6 +981,17 @@ def test_block_scaled_cache_is_refused_where_it_is_not_known():
     d64 = L.PkvCache(fake, fake, 10, 16, 2, 64, 2048, L.KV_FP8_E4M3_BLOCK, 1.0, 1.0, fake, fake)
     b32 = L.PkvCache(fake, fake, 10, 32, 2, 128, 8192, L.KV_FP8_E4M3_BLOCK, 1.0, 1.0, fake, fake)
     assert dec(d64) == 2 and ext(d64) == 2 and dec(b32) == 2 and ext(b32) == 2
+    # a workspace that is too small, or not aligned; contexts that no call can cut need none
+    need = lib.pkv_extend_block_workspace_size(8, 5000, 8, 2)
+    # (896 tokens are at most 7 key tiles of context and one of new tokens, the 8 that a share has at least)
+    assert lib.pkv_extend_block_workspace_size(8, 897, 8, 2) == need > lib.pkv_extend_block_workspace_size(8, 896, 8, 2) == 0
+    assert lib.pkv_extend_block_workspace_size(33, 5000, 8, 2) > need and lib.pkv_extend_block_workspace_size(8, 5000, 8, 0) == 0
+    for w, size in ((ws, need - 1), (P((1 << 21) + 8), need)):
+        assert lib.pkv_extend_attn(fake, fake, fake, 8, fake, fake, blk, fake, 4, reqs, 8, 8, 5000, 0, 1.0, fake, None, w, size,
+                                   None) == 3
+    # more KV heads than the decode's tables hold
+    wide = L.PkvCache(fake, fake, 10, 16, 257, 128, 257 * 2048, L.KV_FP8_E4M3_BLOCK, 1.0, 1.0, fake, fake)
+    assert dec(wide, hq=257) == 2
     empty = L.PkvReqs(None, None, 0, 0, 4)
     assert lib.pkv_paged_decode_attn(fake, blk, fake, 4, fake, None, empty, 8, 100, 1.0, fake, None, None, 0, None) == 0
 
