@@ -14,7 +14,7 @@
  *     comment says "host". The library allocates no device memory and keeps no state
  *     between calls other than one per-device error word (pkv_device_errors), the handoff
  *     handles the caller creates (pkv_handoff_create) and, per device, 64 work-item counter
- *     slots of the extend/prefill kernel (each launch takes the next slot and leaves it at zero;
+ *     slots of the extend/prefill kernel and 64 of the extend kernel of block-scaled caches (each launch takes the next slot and leaves it at zero;
  *     a launch shares its slot only with the launch 64 extend/prefill launches later, so at
  *     most 63 other such launches may be in flight at once on one device, and one captured
  *     graph must not be replayed on two streams at the same time).
@@ -85,7 +85,10 @@
  *   decode takes one 576-wide latent head, 512 value dims and 16 to 128 query heads in
  *   groups of 16. Request sets: reqs.max_reqs <= 65535 for the decode and MLA calls (larger
  *   returns PKV_ERR_UNSUPPORTED), any int32 for prefill and extend, except extend over an FP8
- *   cache at head_dim 64, <= 1024 (its context gather holds one pool per request).
+ *   cache at head_dim 64, <= 1024 (its context gather holds one pool per request). Block-scaled
+ *   caches: head_dim 128, block_size 16, for decode at most 256 KV heads. kv_append takes any
+ *   head_dim and rotation in multiples of 16 up to 1024 and, block-scaled caches aside, any
+ *   block_size.
  */
 #ifndef PKV_H_
 #define PKV_H_
@@ -109,10 +112,11 @@ typedef enum {
 } pkv_status;
 
 /* Bits of the per-device error word (pkv_device_errors). */
-#define PKV_DEVERR_SLOT 0x1u      /* kv_cache_write: slot >= num_blocks * block_size */
+#define PKV_DEVERR_SLOT 0x1u      /* kv_cache_write, kv_append: slot >= num_blocks * block_size */
 #define PKV_DEVERR_BLOCK 0x2u     /* a block id outside [0, num_blocks) */
 #define PKV_DEVERR_REQS 0x4u      /* request set larger than max_reqs, or a request id outside [0, R) */
-#define PKV_DEVERR_LEN 0x8u       /* a length beyond a host bound (max_seq_len, max_q_len, table) */
+#define PKV_DEVERR_LEN 0x8u       /* a length beyond a host bound (max_seq_len, max_q_len, table); a position
+                                   * outside kv_append's table */
 #define PKV_DEVERR_TIMEOUT 0x10u  /* a pipeline wait gave up (a library bug; results are wrong) */
 
 #define PKV_KV_BF16 0
@@ -255,7 +259,7 @@ pkv_status pkv_batch_classify_reorder(const int32_t* cu_q, const int32_t* seq_le
  * For each request r of `reqs` (q_len must be 1; its query row is cu_q[r], or r when cu_q is
  * NULL), each query head h: keys/values are positions 0 .. seq_lens[r]-1 of the sequence,
  * read from the cache through block_tables (the new token's K/V must already be written, e.g.
- * by pkv_kv_cache_write), and
+ * by pkv_kv_cache_write or pkv_kv_append), and
  *   out[row, h] = softmax(scale * q[row, h] . K^T) V   (bf16, round to nearest even),
  *   lse[row, h] = ln sum_j exp(scale * q . k_j)       (fp32; lse may be NULL).
  * seq_lens[r] == 0 gives out = 0, lse = -inf. seq_lens[r] > max_seq_len or beyond the table
