@@ -46,6 +46,18 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _scratch(need: int, workspace, device, stream):
+    """The caller's workspace if it is large enough, else one of `need` bytes (None for 0) that the allocator
+    gives to nobody else before the call's work on `stream` is done."""
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        if not need:
+            return workspace
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return workspace
+
+
 def _need(t: torch.Tensor, dtype, name: str, contiguous: bool = True):
     if not t.is_cuda:
         raise PkvError(f"{name} must be a CUDA tensor")
@@ -342,8 +354,7 @@ def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, 
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     need = lib.pkv_paged_decode_workspace_size(reqs.max_reqs, Hq, cache.num_kv_heads, D, max_seq_len)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = _scratch(need, workspace, q.device, stream)
     _check(lib.pkv_paged_decode_attn(_ptr(q), cache, _ptr(block_tables), block_tables.shape[1],
                                      _ptr(seq_lens), _ptr(cu_q), reqs.c(), Hq, max_seq_len,
                                      _scale(scale, D), _ptr(out), _ptr(lse), _ptr(workspace),
@@ -432,8 +443,7 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
                                          cache.num_kv_heads, cache.head_dim)
     elif cache.kv_dtype == _lib.KV_FP8_E4M3_BLOCK:
         need = extend_block_workspace_size(max_q_len, max_seq_len, Hq, cache.num_kv_heads)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = _scratch(need, workspace, q.device, stream)
     _check(lib.pkv_extend_attn(_ptr(q), _ptr(k_new), _ptr(v_new), T, _ptr(cu_q), _ptr(seq_lens), cache,
                                _ptr(block_tables), block_tables.shape[1], reqs.c(), Hq, max_q_len,
                                max_seq_len, chunk_budget_tokens, _scale(scale, D), _ptr(out),

@@ -757,6 +757,47 @@ def test_extend_in_a_graph_with_other_lengths_and_beside_another_stream(new, G, 
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G,longest", [(8, 4), (2, 90)])
+def test_extend_of_many_requests_beside_a_long_context(G, longest):
+    """More requests than a launch holds, one of the first and one of the last far longer than the others: short
+    items in shares whole, long ones cut over many of them."""
+    n = 290
+    ctx, new = [(13 * i) % 90 for i in range(n)], [1 + i % 3 for i in range(n)]
+    ctx[3], ctx[280], new[3] = 12000, 5000, longest
+    st = extend_state(ctx, new, G, 1, seed=50 + G)
+    check_extend(st, *gpu_extend(st), SCALE)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["extend", "decode"])
+def test_a_workspace_of_the_binding_on_another_stream(what):
+    """The scratch that the binding allocates is not given to the current stream's tensors while the other's call runs."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    st = extend_state([20000, 9000], [4, 4] if what == "extend" else [1, 1], 8, 1, seed=60)
+    kc, vc = pools(st)
+    q, k, v, cu, table, ks, vs = (on(st[n]) for n in ("q", "k_new", "v_new", "cu", "table", "ks", "vs"))
+    lens = torch.tensor([c + (m if what == "extend" else 0) for c, m in zip(st["ctx"], st["new"])], dtype=torch.int32).cuda()
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for handle in (other, other.cuda_stream):
+        for _ in range(4):
+            if what == "extend":
+                outs.append(pkv.extend_attn(q, k, v, cu, lens, kc, vc, table, 4, 20100, stream=handle, k_scale=ks, v_scale=vs))
+                need = pkv.extend_block_workspace_size(4, 20100, 8, 1)
+            else:
+                outs.append(pkv.paged_decode_attn(q, kc, vc, table, lens, 20100, stream=handle, k_scale=ks, v_scale=vs))
+                need = pkv.paged_decode_workspace_size(2, 8, 1, 128, 20100)
+            torch.empty(need, dtype=torch.uint8, device="cuda").fill_(0x7F)
+    torch.cuda.synchronize()
+    assert pkv.device_errors() == 0
+    for out, lse in outs:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+    if what == "extend":
+        check_extend(st, *outs[0], SCALE)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("most", [3, 200])
 def test_extend_cuts_and_flags_more_tokens_than_its_bound(most):
     """A request with more new tokens than max_q_len: its first max_q_len rows are right, the others stay as they were."""
