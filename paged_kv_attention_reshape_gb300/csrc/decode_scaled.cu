@@ -30,6 +30,11 @@
 //   * A sequence cut at share edges is merged by its log-sum-exps along a tree of fan-in 8: fp32
 //     partials in the workspace, an arrival counter per tree node (tagged with the call's epoch, set
 //     back to zero by the arrival that completes it, so a replayed graph finds none of its own).
+//
+// What bounds it: with 8 heads a KV head HBM (192 sequences of 1000 to 8000 tokens, Hq 64 / Hkv 8: 290 us, 6.1 TB/s,
+// 0.90 of the measured copy); with 16 the softmax warps, 2450 clocks a tile against 1900 for its bytes (256 sequences of
+// 2000 to 3000, Hq 64 / Hkv 4: 132 us, 0.74); one sequence of 100,000 tokens its ramp and merge (50 us, 0.61); four of
+// at most 200 the set-up and the first tile (8.8 us on the GPU).
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -704,6 +709,9 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
       }
       wk.advance();
       next = entry(wk);
+      int blks[C::TBLK];
+#pragma unroll
+      for (int i = 0; i < C::TBLK; ++i) blks[i] = __shfl_sync(0xffffffffu, blk, i);
 #pragma unroll 1
       for (int sel = 0; sel < 2; ++sel, ++h) {
         const uint32_t b = h % C::NB;
@@ -711,8 +719,6 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[b], nbl * 2048);
-        __syncwarp();
         if (lane < C::TBLK) {
           if (lane < nbl) {
             if (sel == 0) {  // both scales come with K
@@ -724,10 +730,18 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
             } else {
               mbar_arrive(&bar.kv_full[b]);
             }
-            tma_load_4d(base + b * C::HALF + lane * 2048, sel ? &tm_v : &tm_k, &bar.kv_full[b], 0, kh, 0, blk);
           } else {
             mbar_arrive(&bar.kv_full[b]);
           }
+        }
+        __syncwarp();
+        // one elected thread for all the copies (a lane each: 137 us against 132 on 256 sequences of 2000 to 3000
+        // tokens, 297 against 290 on 192 of 1000 to 8000)
+        if (tc::elect()) {
+          mbar_arrive_expect_tx(&bar.kv_full[b], nbl * 2048);
+#pragma unroll
+          for (int i = 0; i < C::TBLK; ++i)
+            if (i < nbl) tma_load_4d(base + b * C::HALF + i * 2048, sel ? &tm_v : &tm_k, &bar.kv_full[b], 0, kh, 0, blks[i]);
         }
         __syncwarp();
       }

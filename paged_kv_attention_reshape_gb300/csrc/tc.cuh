@@ -69,6 +69,16 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t k_s
   return d;
 }
 
+// One thread of a converged warp (always the same one). A branch on it is known to the compiler as a single
+// thread's, and the operands of the MMAs in it then need no move from per-thread registers each: eight
+// products of an otherwise busy SM's warp are issued at 82 clocks each (65 is the pipe's rate for 128 x 128 x 16), and
+// at 205 in a branch on lane == 0.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---- MMA ---------------------------------------------------------------------------------------
 // D[tmem] (+)= A[smem desc] * B[smem desc]
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
