@@ -44,23 +44,27 @@
 // a second kernel merges by their maxima and sums. (The plan is the same whoever claims what, so the
 // results do not depend on timing.)
 //
-// What bounds it. Many rows: tensor core and shared memory together (a key tile of 256 rows takes 4000
-// clocks; its products alone 2200, their operands' and the conversions' reads and writes of shared
-// memory 2500): 8 x 512 tokens over 4K to 32K 2.00 ms, 0.64 of the measured bf16 rate, 2048 tokens over
-// 100K 5.33 ms, 0.66. FEW: the same for a tile of which only every copy's part is new, 2500 clocks of
-// products and conversions a key tile: 32 x 4 tokens over 1K to 4K 69 us, 0.36 of the measured HBM rate.
+// What bounds it. Many rows: each slot's chain S, softmax (1900 clocks), P V, S of the next tile, 3650 clocks a
+// key tile of 256 rows, in which the tensor core works 2080 (S and P share columns, and two slots fill
+// tensor memory): 8 x 512 tokens over 4K to 32K 1.79 ms, 0.72 of the measured bf16 rate, 2048 tokens over
+// 100K 4.86 ms, 0.73. FEW: the ring (a tile is loaded in 2400 clocks, converted in 900 to 1500 and held
+// through its softmax, and five buffers hold two and a half): 32 x 4 tokens over 1K to 4K 65 us, 0.38 of
+// the measured HBM rate.
 //
-// Roles (12 warps, or 16 in FEW, one CTA per SM, persistent):
-//   warps 0-3, 4-7  softmax of slot 0, 1 (thread t owns row t = TMEM lane t) and the epilogue
-//   warp 8          TMA producer: claims the items, loads Q and the ring of K and V tiles (128 keys)
-//   warp 9          MMA issuer (one thread, which also does its waits: as a whole warp with votes
-//                   around each of them 2.30 ms against 2.18): S = Q K^T, O += P V (P read from
-//                   tensor memory)
-//   warps 10-11     converters: E4M3 code tiles, Q and new keys to fp16 in shared memory, two rows a
-//                   thread (FEW: warps 10-13 for K and Q, 14-15 for V, 66 us against 71 with two and two; in
-//                   the general launch four warps convert faster but slow the products, whose operands they
-//                   compete with for shared memory; and unrolled loops over the rows and over K and V
-//                   measured 2.18 ms against 2.02 on the 8 x 512 tokens)
+// Roles (16 warps, one CTA per SM, persistent):
+//   warps 0-3, 4-7  softmax of slot 0, 1 (thread t owns row t = TMEM lane t) and the epilogue; a row of S in
+//                   two halves, the second read twice, which leaves registers for four converter warps
+//                   (whole rows in 200 registers and two converters: 2.00 ms on the 8 x 512 tokens)
+//   warp 8          TMA producer: claims the items, loads Q and the ring of K and V tiles (128 keys). One elected
+//                   thread issues a tile's eight copies (eight lanes, one each: 1.83 ms against 1.79)
+//   warp 9          MMA issuer, one elected thread, waits included: S = Q K^T, O += P V (P read from tensor
+//                   memory). In a branch on lane == 0 every product's operands are moved from per-thread registers,
+//                   135 clocks an MMA in this kernel, and the issue bounds it (a slot's softmax then takes 1600 of
+//                   4000 clocks); waits by the whole warp and products in elected branches: 1.93 ms
+//   warps 12-15     converters: E4M3 code tiles, Q and new keys to fp16 in shared memory, a row a thread (two warps, 1600
+//                   clocks a tile of K or V, hold the faster issue back: 2.09 ms; two for K and two for V 1.89).
+//                   Rolled loops over the rows and over K and V: unrolled ones cost 8%
+//   FEW: warps 10-13 convert K and Q, 14-15 V, 66 us against 71 with two and two
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; P_s overwrites the first half of S_s.
 #include <math_constants.h>
 
@@ -80,7 +84,7 @@ struct AsBase {
   static constexpr int HALF_BYTES = 128 * 128;       // 128 rows x 128 bytes
   static constexpr int TILE_BYTES = 2 * HALF_BYTES;  // one 128-row tile of Q, K or V in 16 bits
   static constexpr int MAXR = kAttnSetChunk;         // requests of the set one launch holds
-  static constexpr int W_LOAD = 8, W_MMA = 9, W_CONV = 10;
+  static constexpr int W_LOAD = 8, W_MMA = 9;
   static constexpr int MAXBUF = 5;
   static constexpr int STAGE_WARP_BYTES = 32 * 64;
   static constexpr int ITEM_RING = 4;                // claimed items published to the other roles
@@ -107,14 +111,14 @@ struct AsBars {
 // FEW: the launch for sets in which every request's rows for a KV head fit one tile (all items are split).
 template <bool FEW>
 struct AsCfg : AsBase {
-  // converter warps: of K (Q and new keys too) and of V; the general launch's two convert both
-  static constexpr int NK = FEW ? 4 : 2, NV = FEW ? 2 : 0, NCONV = NK + NV;
+  // converter warps: of K (Q and new keys too) and of V; the general launch's four convert both (its warps 10
+  // and 11 are idle: a register split is by groups of four)
+  static constexpr int W_CONV = FEW ? 10 : 12, NK = 4, NV = FEW ? 2 : 0, NCONV = NK + NV;
   static constexpr int WARPS = W_CONV + NCONV, THREADS = WARPS * 32;
-  // The general launch has 168 registers a thread; the softmax warpgroups hold a whole row of S and take
-  // more, the third warpgroup gives them up. (8 x 512 tokens over 4K-32K: 184 and 136 registers 2.07 ms, 192
-  // and 120 2.04, 200 and 104 1.99; 208 and 88 spill, 2.60.)
-  static constexpr int REGS_SOFTMAX = 200, REGS_OTHER = 104;
-  static_assert(FEW || 256 * REGS_SOFTMAX + 128 * REGS_OTHER == THREADS * 168, "register split");
+  // The general launch has 128 registers a thread. (144, 120 and 104 spill nothing: 1.83 ms on 8 x 512 tokens; 144, 128
+  // and 96 1.83, 152, 120 and 88 1.84, 152, 104 and 104 1.86, 128 each 1.86.)
+  static constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 120, REGS_CONV = 104;
+  static_assert(FEW || 256 * REGS_SOFTMAX + 128 * REGS_OTHER + 128 * REGS_CONV == THREADS * 128, "register split");
   static constexpr int NBUF = FEW ? 5 : 4;           // K/V ring: one tile per buffer
   static constexpr int NQ = FEW ? 1 : 2;             // Q tiles of an item
   static constexpr int ROWS = NQ * 128;
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
     for (int b = 0; b < C::NBUF; ++b) {
       mbar_init(&bar.kv_full[b], 1 + C::TBLK);  // the producer's bytes, and each block's scales
       mbar_init(&bar.kv_empty[b], 1);
-      mbar_init(&bar.conv_full[b], FEW ? C::NK : C::NCONV);
+      mbar_init(&bar.conv_full[b], C::NK);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
@@ -500,6 +504,72 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
   const int shares = (s_plan[1] + s_plan[2] - 1) / s_plan[2], W = s_plan[0] + shares;
   if (ws != nullptr && blockIdx.x == 0 && tid == 0) *as_partials(ws, ws_slots, C::ROWS).head = shares;
 
+  auto convert = [&]() {
+      // ======================= converters =======================
+      // The first NK warps convert Q once per item, then each K tile as it lands, the others (or, if there are
+      // none, the same) each V tile: rows ct, ct + 32 NK, .. a thread.
+      const bool of_v = FEW && warp >= C::W_CONV + C::NK;
+      const int ct = tid - (C::W_CONV + (of_v ? C::NK : 0)) * 32;
+      const uint32_t q_base = smem_u32(sQ), ring_base = smem_u32(ring);
+      uint32_t kvc = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok; ++k) {
+        const AsItem* taken = as_take<FEW>(smem, bar, k, &s_abort, p.err);
+        if (taken == nullptr) break;
+        const AsItem it = *taken;
+        as_free(bar, k, lane);
+        if (!of_v) {
+          if (!as_wait(&bar.q_full, k & 1, &s_abort, p.err)) break;
+          if constexpr (FEW) {
+            const int span = as_span(it.q_len * p.G);
+            for (int R = ct; R < span; R += C::NK * 32) as_conv_copies(q_base, R, span);
+          } else {
+            for (int s = 0; s < (it.split ? 1 : 2); ++s) as_conv_bf16(q_base + s * C::TILE_BYTES, ct);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.q_conv);
+        }
+        for (int j = 0; j < it.NT && ok; ++j) {
+#pragma unroll 1
+          for (int sel = 0; sel < 2; ++sel, ++kvc) {
+            if (FEW && (sel != 0) != of_v) continue;
+            const int b = kvc % C::NBUF;
+            if (!as_wait(&bar.kv_full[b], (kvc / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
+            const uint32_t tile = ring_base + b * C::TILE_BYTES;
+            if (sel == 0 && ct < 8) {
+              // the tile's softmax factors of block ct
+              const uint32_t at = kvc / 2 % C::SCALE_RING;
+              float4 f = make_float4(p.scale_log2, 0.f, 1.f, 0.f);
+              if (j < it.nct) {
+                const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + at * 16;
+                // a zero scale counts as 2^-100: no logarithm of 0, no product of 0 and a masked -inf
+                const float ks = fmaxf(sc[ct], 0x1p-100f), vs = fmaxf(sc[8 + ct], 0x1p-100f);
+                f = make_float4(ks * p.scale_log2, __log2f(vs), 1.f / vs, 0.f);
+              }
+              reinterpret_cast<float4*>(smem + C::FACTOR_OFF)[at * 8 + ct] = f;
+            }
+#pragma unroll 1
+            for (int R = ct; R < 128; R += FEW && of_v ? C::NV * 32 : C::NK * 32) {
+              if (j < it.nct) {
+                // V rows past the context's end become zeros (P = 0 there must not meet a NaN code)
+                as_conv_codes(tile, R, sel == 0 || R < it.C - j * 128);
+              } else if (sel == 0) {
+                as_conv_bf16(tile, R);
+              } else if (R >= it.q_len - (j - it.nct) * 128) {
+                // new values stay as they come, but for rows past the request's own tokens
+                as_zero_row(tile, R);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            // NK arrivals a tile, of K and of V
+            if (FEW ? lane < (of_v ? C::NK / C::NV : 1) : lane == 0) mbar_arrive(&bar.conv_full[b]);
+          }
+        }
+      }
+  };
+
   if (warp < 8) {
     if constexpr (!FEW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     // ======================= softmax warpgroups =======================
@@ -533,29 +603,36 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
           const int kv = ctx ? min(128, it.C - j * 128) : min(128, tok - (j - it.nct) * 128 + 1);
           const bool full = __all_sync(0xffffffffu, kv >= 128);
           const uint32_t srow = tmem + lane_off + as_scol(slot);
-          // the whole row of S into registers (four loads, one wait)
-          uint32_t v[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc::ld32(srow + c * 32, v[c]);
-          tc::wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
           // the factors of block g of the tile: {key scale * softmax scale, log2 vs, 1 / vs}
           const float4* fac = reinterpret_cast<const float4*>(smem + C::FACTOR_OFF) + (tile0 + j) % C::SCALE_RING * 8;
-          if (!full) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) as_mask(v[c], kv - c * 32);
-          }
+          // half a row of S at a time: the second and then the first for the max, and for P the first (whose P lies over
+          // its own columns), the second read again
+          uint32_t v[2][32];
+          auto load = [&](int c0) {
+            tc::ld32(srow + c0 * 32, v[0]);
+            tc::ld32(srow + (c0 + 1) * 32, v[1]);
+            tc::wait_ld();
+            tc::touch32(v[0]);  // no use of v may move above the wait
+            tc::touch32(v[1]);
+            if (!full) {
+              as_mask(v[0], kv - c0 * 32);
+              as_mask(v[1], kv - (c0 + 1) * 32);
+            }
+          };
           // the max of a block's raw scores (its factor is positive), then of the blocks' u
           float mx = -CUDART_INF_F;
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            float mg = -CUDART_INF_F;
+          for (int c0 = 2; c0 >= 0; c0 -= 2) {
+            load(c0);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2)
-              mg = sm::max3(mg, __uint_as_float(v[g / 2][(g & 1) * 16 + e]), __uint_as_float(v[g / 2][(g & 1) * 16 + e + 1]));
-            const float4 f = fac[g];
-            mx = fmaxf(mx, fmaf(mg, f.x, f.y));
+            for (int g = 0; g < 4; ++g) {
+              float mg = -CUDART_INF_F;
+#pragma unroll
+              for (int e = 0; e < 16; e += 2)
+                mg = sm::max3(mg, __uint_as_float(v[g / 2][(g & 1) * 16 + e]), __uint_as_float(v[g / 2][(g & 1) * 16 + e + 1]));
+              const float4 f = fac[2 * c0 + g];
+              mx = fmaxf(mx, fmaf(mg, f.x, f.y));
+            }
           }
           float alpha = 1.f;
           if (mx > m + 8.f || m == -CUDART_INF_F) {  // lazy rescale: only when the max really grows
@@ -569,13 +646,13 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
           // P of the 16 columns of block g, packed over the first half of S: fp16 beside the context's
           // codes, bf16 beside new values; the row sum takes each P over its block's vs
           uint64_t rs2 = sm::f2(0.f, 0.f);
-          auto exp_pass = [&](auto f16) {
+          auto exp_pass = [&](auto f16, int c0) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
               uint32_t pk[16];
 #pragma unroll
               for (int gg = 0; gg < 2; ++gg) {
-                const float4 f = fac[2 * c + gg];
+                const float4 f = fac[2 * (c0 + c) + gg];
                 const uint64_t sc2 = sm::f2(f.x, f.x), nm2 = sm::f2(neg_m + f.y, neg_m + f.y), iv2 = sm::f2(f.z, f.z);
 #pragma unroll
                 for (int e = 16 * gg; e < 16 * gg + 16; e += 2) {
@@ -587,10 +664,18 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
                   pk[e / 2] = decltype(f16)::value ? sm::f16x2(pp) : sm::bf16x2(pp);
                 }
               }
-              tc::st16(srow + c * 16, pk);
+              tc::st16(srow + (c0 + c) * 16, pk);
             }
           };
-          if (ctx) exp_pass(std::true_type{}); else exp_pass(std::false_type{});
+          if (ctx) {
+            exp_pass(std::true_type{}, 0);
+            load(2);
+            exp_pass(std::true_type{}, 2);
+          } else {
+            exp_pass(std::false_type{}, 0);
+            load(2);
+            exp_pass(std::false_type{}, 2);
+          }
           float r0, r1;
           sm::unf2(rs2, r0, r1);
           l = l * alpha + (r0 + r1);
@@ -951,6 +1036,9 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
             ll > 0.f ? (mm + __log2f(ll)) * 0.69314718055994531f : -CUDART_INF_F;
     }
     }
+  } else if (!FEW && warp >= C::W_CONV) {
+    if constexpr (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONV));
+    convert();
   } else {
     if constexpr (!FEW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (warp == C::W_LOAD) {
@@ -1035,6 +1123,8 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
           const int lb = j * 8 + lane;
           return j < it.nct && lane < 8 ? table[lb < ctx_blocks ? lb : j * 8] : 0;
         };
+        const int kh = __shfl_sync(0xffffffffu, it.kh, 0), row0 = __shfl_sync(0xffffffffu, it.row0, 0);
+        const int nct = __shfl_sync(0xffffffffu, it.nct, 0);
         int next = entry(0);
         for (int j = 0; j < it.NT && ok; ++j) {
           const bool ctx = j < it.nct;
@@ -1044,6 +1134,9 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
             blk = 0;
           }
           next = entry(j + 1);
+          int blks[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) blks[i] = __shfl_sync(0xffffffffu, blk, i);
 #pragma unroll 1
           for (int sel = 0; sel < 2; ++sel, ++kvc) {
             const int b = kvc % C::NBUF;
@@ -1052,8 +1145,6 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
               break;
             }
             uint8_t* dst = ring + b * C::TILE_BYTES;
-            if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[b], ctx ? C::HALF_BYTES : C::TILE_BYTES);
-            __syncwarp();
             if (lane < 8) {
               if (ctx && sel == 0) {  // both scales come with K; kvc / 2 counts the CTA's key tiles
                 const int64_t at = static_cast<int64_t>(blk) * p.Hkv + it.kh;
@@ -1064,14 +1155,21 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
               } else {
                 mbar_arrive(&bar.kv_full[b]);
               }
-              // the block's 16 rows of codes into the upper half of the buffer
-              if (ctx) tma_load_4d(dst + C::HALF_BYTES + lane * 2048, sel ? &tm_cv : &tm_ck, &bar.kv_full[b], 0, it.kh, 0, blk);
             }
-            if (!ctx && lane == 0) {
-              const int row = it.row0 + (j - it.nct) * 128;
+            __syncwarp();
+            if (tc::elect()) {
+              mbar_arrive_expect_tx(&bar.kv_full[b], ctx ? C::HALF_BYTES : C::TILE_BYTES);
+              if (ctx) {
+                // the blocks' 16 rows of codes each into the upper half of the buffer
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-                tma_load_3d(dst + hf * C::HALF_BYTES, sel ? &tm_v : &tm_k, &bar.kv_full[b], 0, it.kh * 2 + hf, row);
+                for (int i = 0; i < 8; ++i)
+                  tma_load_4d(dst + C::HALF_BYTES + i * 2048, sel ? &tm_cv : &tm_ck, &bar.kv_full[b], 0, kh, 0, blks[i]);
+              } else {
+                const int row = row0 + (j - nct) * 128;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                  tma_load_3d(dst + hf * C::HALF_BYTES, sel ? &tm_v : &tm_k, &bar.kv_full[b], 0, kh * 2 + hf, row);
+              }
             }
             __syncwarp();
           }
@@ -1084,7 +1182,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       }
     } else if (warp == C::W_MMA) {
       // ======================= MMA issuer =======================
-      if (lane == 0) {
+      if (tc::elect()) {
         uint32_t kvc = 0, pc0 = 0, pc1 = 0;  // K and V tiles before this item; P tiles consumed per slot
         bool ok = true;
         const uint64_t q_desc = tc::smem_desc(smem_u32(sQ), 16, 1024), k_desc = tc::smem_desc(smem_u32(ring), 16, 1024);
@@ -1188,73 +1286,8 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         }
       }
       __syncwarp();
-    } else {
-      // ======================= converters =======================
-      // The first NK warps convert Q once per item, then each K tile as it lands, the others (or, if there are
-      // none, the same) each V tile: rows ct, ct + 32 NK, .. a thread.
-      const bool of_v = FEW && warp >= C::W_CONV + C::NK;
-      const int ct = tid - (C::W_CONV + (of_v ? C::NK : 0)) * 32;
-      const uint32_t q_base = smem_u32(sQ), ring_base = smem_u32(ring);
-      uint32_t kvc = 0;
-      bool ok = true;
-      for (uint32_t k = 0; ok; ++k) {
-        const AsItem* taken = as_take<FEW>(smem, bar, k, &s_abort, p.err);
-        if (taken == nullptr) break;
-        const AsItem it = *taken;
-        as_free(bar, k, lane);
-        if (!of_v) {
-          if (!as_wait(&bar.q_full, k & 1, &s_abort, p.err)) break;
-          if constexpr (FEW) {
-            const int span = as_span(it.q_len * p.G);
-            for (int R = ct; R < span; R += C::NK * 32) as_conv_copies(q_base, R, span);
-          } else {
-            for (int s = 0; s < (it.split ? 1 : 2); ++s) {
-              as_conv_bf16(q_base + s * C::TILE_BYTES, ct);
-              as_conv_bf16(q_base + s * C::TILE_BYTES, ct + 64);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.q_conv);
-        }
-        for (int j = 0; j < it.NT && ok; ++j) {
-#pragma unroll 1
-          for (int sel = 0; sel < 2; ++sel, ++kvc) {
-            if (FEW && (sel != 0) != of_v) continue;
-            const int b = kvc % C::NBUF;
-            if (!as_wait(&bar.kv_full[b], (kvc / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
-            const uint32_t tile = ring_base + b * C::TILE_BYTES;
-            if (sel == 0 && ct < 8) {
-              // the tile's softmax factors of block ct
-              const uint32_t at = kvc / 2 % C::SCALE_RING;
-              float4 f = make_float4(p.scale_log2, 0.f, 1.f, 0.f);
-              if (j < it.nct) {
-                const float* sc = reinterpret_cast<const float*>(smem + C::SCALE_OFF) + at * 16;
-                // a zero scale counts as 2^-100: no logarithm of 0, no product of 0 and a masked -inf
-                const float ks = fmaxf(sc[ct], 0x1p-100f), vs = fmaxf(sc[8 + ct], 0x1p-100f);
-                f = make_float4(ks * p.scale_log2, __log2f(vs), 1.f / vs, 0.f);
-              }
-              reinterpret_cast<float4*>(smem + C::FACTOR_OFF)[at * 8 + ct] = f;
-            }
-#pragma unroll 1
-            for (int R = ct; R < 128; R += FEW && of_v ? C::NV * 32 : C::NK * 32) {
-              if (j < it.nct) {
-                // V rows past the context's end become zeros (P = 0 there must not meet a NaN code)
-                as_conv_codes(tile, R, sel == 0 || R < it.C - j * 128);
-              } else if (sel == 0) {
-                as_conv_bf16(tile, R);
-              } else if (R >= it.q_len - (j - it.nct) * 128) {
-                // new values stay as they come, but for rows past the request's own tokens
-                as_zero_row(tile, R);
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            // NK arrivals a tile, of K and of V
-            if (FEW ? lane < (of_v ? C::NK / C::NV : 1) : lane == 0) mbar_arrive(&bar.conv_full[b]);
-          }
-        }
-      }
+    } else if (FEW) {
+      convert();
     }
   }
   tc::fence_before_sync();
