@@ -11,7 +11,7 @@
 //   out = O / l,   lse = (m + log2 l) ln 2.
 // The tensor core multiplies the E4M3 values themselves, exact in fp16, and the softmax applies both
 // scales in fp32, where nothing is rounded to few bits. Taking the max over u rather than over the
-// scores keeps P within [0, 2^8] whatever the scales, and costs nothing per column: the shift of the
+// scores keeps P within [0, 2^15] whatever the scales, and costs nothing per column: the shift of the
 // exponent and the factor of the sum are the block's. (Rounding scale * code to bf16 in the
 // converter warps, the first form, put 2^-8 of each product into the exponent and of each value into
 // the sum, and its conversions, 9 instructions for a pair of codes against 2, took 2.5 times as long:
@@ -86,6 +86,9 @@ struct AsBase {
   static constexpr int MAXR = kAttnSetChunk;         // requests of the set one launch holds
   static constexpr int W_LOAD = 8, W_MMA = 9;
   static constexpr int MAXBUF = 5;
+  // P = 2^(u - m + RAISE): with the lazy maximum (u <= m + 8) at most 2^15, so that fp16 holds 11 bits of every P down to
+  // 2^-21 of the largest possible and rounds smaller ones to 2^-32 of a row's largest term.
+  static constexpr float RAISE = 7.f;
   static constexpr int STAGE_WARP_BYTES = 32 * 64;
   static constexpr int ITEM_RING = 4;                // claimed items published to the other roles
   // key tile k of the CTA in slot k % SCALE_RING: the blocks' scales as they land (8 of K, 8 of V), and
@@ -533,9 +536,11 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         for (int j = 0; j < it.NT && ok; ++j) {
 #pragma unroll 1
           for (int sel = 0; sel < 2; ++sel, ++kvc) {
-            if (FEW && (sel != 0) != of_v) continue;
+            // (every tile is waited for, the other group's too: five buffers hold K and V in turn, and a parity
+            // tells a barrier's phase only to one who waited for the phase before)
             const int b = kvc % C::NBUF;
             if (!as_wait(&bar.kv_full[b], (kvc / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
+            if (FEW && (sel != 0) != of_v) continue;
             const uint32_t tile = ring_base + b * C::TILE_BYTES;
             if (sel == 0 && ct < 8) {
               // the tile's softmax factors of block ct
@@ -642,7 +647,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
               m = m_new;
             }
           }
-          const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+          const float neg_m = m == -CUDART_INF_F ? 0.f : C::RAISE - m;
           // P of the 16 columns of block g, packed over the first half of S: fp16 beside the context's
           // codes, bf16 beside new values; the row sum takes each P over its block's vs
           uint64_t rs2 = sm::f2(0.f, 0.f);
@@ -814,7 +819,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       if (both) mbar_arrive(&bar.merge_done);
       if (p.lse) {
         const int64_t fr = flat_row(t);
-        if (fr >= 0) p.lse[fr] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+        if (fr >= 0) p.lse[fr] = l > 0.f ? (m - AsBase::RAISE + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
       }
     }
     } else {
@@ -878,7 +883,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
               m = m_new;
             }
           }
-          const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+          const float neg_m = m == -CUDART_INF_F ? 0.f : C::RAISE - m;
           uint64_t rs2 = sm::f2(0.f, 0.f);
           uint32_t pk[16];
 #pragma unroll 1
@@ -1033,7 +1038,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         if (t < span) part.ml[static_cast<int64_t>(it.slot) * C::ROWS + t] = make_float2(mm, ll);
       } else if (p.lse && t < min(span, rows))
         p.lse[(static_cast<int64_t>(it.row0) + tok) * p.Hq + it.kh * p.G + (row & (p.G - 1))] =
-            ll > 0.f ? (mm + __log2f(ll)) * 0.69314718055994531f : -CUDART_INF_F;
+            ll > 0.f ? (mm - AsBase::RAISE + __log2f(ll)) * 0.69314718055994531f : -CUDART_INF_F;
     }
     }
   } else if (!FEW && warp >= C::W_CONV) {
@@ -1360,7 +1365,7 @@ __global__ void __launch_bounds__(256) attn_scaled_merge_kernel(const AttnParams
     const int64_t fr = tok * p.Hq + it.w * p.G + rr % p.G;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     *reinterpret_cast<uint2*>(p.out + fr * 128 + c4 * 4) = make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
-    if (p.lse && c4 == 0) p.lse[fr] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+    if (p.lse && c4 == 0) p.lse[fr] = l > 0.f ? (m - AsBase::RAISE + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
   }
 }
 
