@@ -10,14 +10,15 @@
 // Rounding: bf16 -> fp32 is exact, each product and sum of the rotation is rounded to fp32 by
 // itself (no contraction, so the result does not depend on the compiler), then there is one
 // rounding to the type that is stored.
-// What bounds it: memory for long batches (each row is read and written once: 5.4 to 6.2 TB/s below),
+// What bounds it: memory for long batches (each row is read and written once: 5.0 to 6.5 TB/s below),
 // the round trips of slot, row and angle for short ones (2 us for one token, 5.5 us for 256 sequences).
-// 10,000 tokens of 64 query and 8 KV heads of 128: 69.5 us into a bf16 cache; 84 us into a block-scaled
+// 10,000 tokens of 64 query and 8 KV heads of 128: 66 us into a bf16 cache; 84 us into a block-scaled
 // one, where the runs need their rows in registers twice, for the maximum and for the codes.
 #include <algorithm>
 
 #include "common.cuh"
 #include "launch.h"
+#include "tc.cuh"
 
 namespace pkv {
 
@@ -342,7 +343,7 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, int64_t group
 // go as bulk copies: a persistent CTA's issuing warp keeps S - 1 tokens' loads in flight whatever the
 // other warps do, they turn a token's rows in place, and it sends them on. (kv_append_kernel has as many
 // loads in flight as its registers hold: 10,000 tokens of 64 query and 8 KV heads of 128 into a bf16
-// cache 90 us, 4.6 TB/s; here 69.5 us, 6.2 TB/s. 4072 tokens with tensor scales 39.6 and 29 us.)
+// cache 90 us, 4.6 TB/s; here 66 us, 6.5 TB/s. 4072 tokens with tensor scales 39.6 and 29 us.)
 constexpr int kTurnWarps = kThreads / 32;
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -384,7 +385,8 @@ __global__ void __launch_bounds__(kThreads + 32) kv_append_stream_kernel(AppendP
   __syncthreads();
   const int64_t step = gridDim.x;
   if (tid >= kThreads) {  // the issuing warp
-    if (tid != kThreads) return;
+    // one elected thread (in a branch on the thread index the copies' operands take longer: 69.5 us against 66)
+    if (!tc::elect()) return;
     // Token t into stage s; its slot and position were read a token earlier.
     int64_t slot_next = -1, pos_next = 0;
     auto peek = [&](int64_t t) {
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_runs_kernel(AppendParams p
 // Rows through shared memory, if two CTAs of S stages fit an SM (three at most do, by their registers).
 // More CTAs with fewer stages where codes are made or little is stored beside q, more stages where the
 // copies are all there is: 10,000 tokens of 64 query and 8 KV heads of 128 into a bf16 cache 73.7 us
-// with 3 stages and 69.5 with 4; into a block-scaled one 84.5 and 86.
+// with 3 stages and 69.5 with 4 (66 since an elected thread issues); into a block-scaled one 84.5 and 86.
 template <int KIND>
 static bool launch_stream(const AppendParams& p, cudaStream_t stream, cudaError_t* e) {
   constexpr uint32_t S = KIND == PKV_KV_BF16 ? 4 : 3;
