@@ -62,8 +62,8 @@ struct SdCfg {
   static constexpr int SC_OFF = P_OFF + 2 * P_BYTES;      // [SRING][8 ks, 8 vs]
   static constexpr int WMAX_OFF = SC_OFF + SRING * 64;    // [2][4 warps][NG] a warp's max of u
   static constexpr int FAC_OFF = WMAX_OFF + 2 * 4 * NG * 4;  // [4 warps][2][3: M, a, c][NG]
-  static constexpr int LSUM_OFF = FAC_OFF + 4 * 2 * 3 * NG * 4;  // [4 warps][NG]
-  static constexpr int INV_OFF = LSUM_OFF + 4 * NG * 4;   // [4 warps][NG]
+  static constexpr int LSUM_OFF = FAC_OFF + 4 * 2 * 3 * NG * 4;  // [2][4 warps][NG]
+  static constexpr int INV_OFF = LSUM_OFF + 2 * 4 * NG * 4;  // [4 warps][NG]
   static constexpr int QMAX_OFF = INV_OFF + 4 * NG * 4;   // [2][4 warps]
   static constexpr int BAR_OFF = QMAX_OFF + 32;
   static constexpr int NBAR = 2 * NB + 13;
@@ -441,6 +441,7 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
     wk.start(s_pre, n, b0, b1);
     uint32_t gt = 0, pieces = 0;
     Piece prev = wk.pc;
+    uint32_t done = 0;  // pieces finished
     bool bad = false;
 
     // fold tile g's O (and its P sums) into the registers
@@ -486,12 +487,15 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
       }
 #pragma unroll
       for (int bit = 16 / NG; bit > 0; bit >>= 1) r[0] += __shfl_xor_sync(0xffffffffu, r[0], bit);
+      // (two buffers: at the end of a share two pieces may finish with no other barrier of the chain in between, and
+      // a warp may still read the first one's sums when another writes the second one's)
       constexpr int SH = NG == 16 ? 1 : 2;
-      if ((lane & ((1 << SH) - 1)) == 0) lsum[w4 * NG + (lane >> SH)] = r[0];
+      float* ls = lsum + (done++ & 1) * 4 * NG;
+      if ((lane & ((1 << SH) - 1)) == 0) ls[w4 * NG + (lane >> SH)] = r[0];
       chain_sync(chain);
       float lse = 0.f;
       if (lane < NG) {
-        const float L = lsum[lane] + lsum[NG + lane] + lsum[2 * NG + lane] + lsum[3 * NG + lane];
+        const float L = ls[lane] + ls[NG + lane] + ls[2 * NG + lane] + ls[3 * NG + lane];
         invs[lane] = 1.f / L;
         lse = (m_fin + __log2f(L)) * 0.69314718055994531f;
       }

@@ -535,6 +535,32 @@ def test_decode_extreme_scales_and_scores(what):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G,Hkv", [(8, 8), (16, 4), (1, 2)])
+def test_decode_gives_the_same_bits_every_time(G, Hkv):
+    """Shares that end in a piece of one tile, whose sums follow those of the piece before without another tile in
+    between: 300 calls with the cache now in L2 and now not."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    g = gen(80 + G)
+    lens = torch.randint(1, 260, (400,), generator=g).tolist()
+    st = decode_state(lens, G * Hkv, Hkv, seed=80 + G, qs=2.0)
+    kc, vc = pools(st)
+    q, table, ks, vs = (on(st[n]) for n in ("q", "table", "ks", "vs"))
+    dev = torch.tensor(lens, dtype=torch.int32).cuda()
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    first, differ = None, torch.zeros((), dtype=torch.bool, device="cuda")
+    for i in range(300):
+        if i % 3 == 0:
+            flush.fill_(i & 127)
+        out, lse = pkv.paged_decode_attn(q, kc, vc, table, dev, 260, k_scale=ks, v_scale=vs)
+        if first is None:
+            first = out, lse
+        else:
+            differ |= (out != first[0]).any() | (lse != first[1]).any()
+    assert not bool(differ) and pkv.device_errors() == 0
+    check_decode(st, *first, SCALE)
+
+
+@pytest.mark.gpu
 def test_decode_request_sets_rows_and_block_strides():
     """A reordered set of the batch with query rows from cu_q; rows outside it are left as they were."""
     import paged_kv_attention_reshape_gb300 as pkv
