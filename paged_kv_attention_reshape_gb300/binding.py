@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the computation runs in libpkv.so's CUDA kernels.
 Tensors must be CUDA tensors on the current device; outputs that are not passed in are
 allocated here with torch (the library itself never allocates). Calls are asynchronous on the
-current torch stream unless ``stream`` is given.
+current torch stream unless ``stream`` is given; what a call on another stream is not given is
+allocated there, so that nothing queued on the current stream still writes it.
 """
 from __future__ import annotations
 
@@ -46,15 +47,41 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
-def _scratch(need: int, workspace, device, stream):
-    """The caller's workspace if it is large enough, else one of `need` bytes (None for 0) that the allocator
-    gives to nobody else before the call's work on `stream` is done."""
+def _other(stream) -> Optional[torch.cuda.Stream]:
+    """The call's stream if it is another than the current one, else None."""
+    if stream is None:
+        return None
+    handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if handle == (_stream(None).value or 0):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)  # (1: the legacy default)
+
+
+def _empty(shape, dtype, device, other) -> torch.Tensor:
+    """A tensor that a call on `other` (None: the current stream) writes and the current stream reads. It comes from
+    `other`'s memory: a block that the current stream has just given back may still be written by what is queued
+    there, which the call does not wait for. Given back, it is kept until what the current stream has queued is done."""
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
+def _scratch(need: int, workspace, device, other):
+    """The caller's workspace if it is large enough, else one of `need` bytes (None for 0) from the memory of the
+    call's stream, which is all that uses it."""
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         if not need:
             return workspace
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+        if other is None:
+            return torch.empty(need, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(other):
+            return torch.empty(need, dtype=torch.uint8, device=device)
     return workspace
 
 
@@ -172,9 +199,9 @@ def _token_index(t: torch.Tensor, name: str, rows: int, device_index: int) -> in
     return t.data_ptr()
 
 
-def _token_out(t: Optional[torch.Tensor], name: str, rows: int, heads: int, dim: int, like: torch.Tensor) -> torch.Tensor:
+def _token_out(t: Optional[torch.Tensor], name: str, rows: int, heads: int, dim: int, like: torch.Tensor, other) -> torch.Tensor:
     if t is None:
-        return torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=like.device)
+        return _empty((rows, heads, dim), torch.bfloat16, like.device, other)
     if _token_rows(t, name, rows, heads, dim, like.get_device()) != heads * dim or not t.is_contiguous():
         raise PkvError(f"{name} must be contiguous")
     return t
@@ -198,6 +225,7 @@ def kv_append(q, key, value, positions, slot_mapping, k_cache, v_cache, cos_sin=
     dev, hkv, d = k_cache.get_device(), cache.num_kv_heads, cache.head_dim
     if dev != torch.cuda.current_device():
         raise PkvError("the cache must be on the current device")
+    other = _other(stream)
     T = key.shape[0]
     k_stride = _token_rows(key, "key", T, hkv, d, dev)
     v_ptr, v_stride = None, 0
@@ -207,9 +235,9 @@ def kv_append(q, key, value, positions, slot_mapping, k_cache, v_cache, cos_sin=
     if q is not None:
         hq = q.shape[1]
         q_ptr, q_stride = q.data_ptr(), _token_rows(q, "q", T, hq, d, dev)
-        q_out = _token_out(q_out, "q_out", T, hq, d, k_cache)
+        q_out = _token_out(q_out, "q_out", T, hq, d, k_cache, other)
         qo_ptr = q_out.data_ptr()
-    k_out = _token_out(k_out, "k_out", T, hkv, d, k_cache)
+    k_out = _token_out(k_out, "k_out", T, hkv, d, k_cache, other)
     pos_ptr = None
     if cos_sin is not None:
         if cos_sin.get_device() != dev or cos_sin.dtype is not torch.float32 \
@@ -233,7 +261,7 @@ def kv_block_pack(k_cache, v_cache, block_ids, dst=None, stream=None):
     cache = make_cache(k_cache, v_cache)
     n = block_ids.numel()
     if dst is None:
-        dst = torch.empty((2, n) + tuple(k_cache.shape[1:]), dtype=k_cache.dtype, device=k_cache.device)
+        dst = _empty((2, n) + tuple(k_cache.shape[1:]), k_cache.dtype, k_cache.device, _other(stream))
     _need(dst, k_cache.dtype, "dst")
     _check(lib.pkv_kv_block_pack(cache, _ptr(block_ids), n, _ptr(dst), _stream(stream)), "kv_block_pack")
     return dst
@@ -312,14 +340,14 @@ def batch_classify_reorder(cu_q, seq_lens, decode_threshold=1, perm=None, bounds
     _need(cu_q, torch.int32, "cu_q")
     _need(seq_lens, torch.int32, "seq_lens")
     R = seq_lens.numel()
-    dev = seq_lens.device
-    perm = perm if perm is not None else torch.empty(R, dtype=torch.int32, device=dev)
-    bounds = bounds if bounds is not None else torch.empty(4, dtype=torch.int32, device=dev)
-    cu_q_reordered = cu_q_reordered if cu_q_reordered is not None else torch.empty(R + 1, dtype=torch.int32, device=dev)
+    dev, other = seq_lens.device, _other(stream)
+    perm = perm if perm is not None else _empty(R, torch.int32, dev, other)
+    bounds = bounds if bounds is not None else _empty(4, torch.int32, dev, other)
+    cu_q_reordered = cu_q_reordered if cu_q_reordered is not None else _empty(R + 1, torch.int32, dev, other)
     if with_token_map and token_map is None:
         if num_tokens is None:
             raise PkvError("num_tokens (host) is needed for the token map")
-        token_map = torch.empty(num_tokens, dtype=torch.int32, device=dev)
+        token_map = _empty(num_tokens, torch.int32, dev, other)
     T = token_map.numel() if token_map is not None else (num_tokens or 0)
     _check(lib.pkv_batch_classify_reorder(_ptr(cu_q), _ptr(seq_lens), R, decode_threshold, _ptr(perm),
                                           _ptr(bounds), _ptr(cu_q_reordered), _ptr(token_map), T,
@@ -349,12 +377,13 @@ def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, 
     T, Hq, D = q.shape
     R = seq_lens.numel()
     reqs = reqs or Reqs(max_reqs=R, batch_reqs=R)
+    other = _other(stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, other)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((T, Hq), torch.float32, q.device, other)
     need = lib.pkv_paged_decode_workspace_size(reqs.max_reqs, Hq, cache.num_kv_heads, D, max_seq_len)
-    workspace = _scratch(need, workspace, q.device, stream)
+    workspace = _scratch(need, workspace, q.device, other)
     _check(lib.pkv_paged_decode_attn(_ptr(q), cache, _ptr(block_tables), block_tables.shape[1],
                                      _ptr(seq_lens), _ptr(cu_q), reqs.c(), Hq, max_seq_len,
                                      _scale(scale, D), _ptr(out), _ptr(lse), _ptr(workspace),
@@ -397,13 +426,13 @@ def mla_decode_attn(q, latent_cache, block_tables, seq_lens, max_seq_len, scale,
     T, Hq, Dk = q.shape
     R = seq_lens.numel()
     reqs = reqs or Reqs(max_reqs=R, batch_reqs=R)
+    other = _other(stream)
     if out is None:
-        out = torch.empty((T, Hq, v_dim), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, Hq, v_dim), torch.bfloat16, q.device, other)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((T, Hq), torch.float32, q.device, other)
     need = lib.pkv_mla_decode_workspace_size(reqs.max_reqs, Hq, max_seq_len)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = _scratch(need, workspace, q.device, other)
     _check(lib.pkv_mla_decode_attn(_ptr(q), cache, _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
                                    _ptr(cu_q), reqs.c(), Hq, max_seq_len, float(scale), int(v_dim), _ptr(out),
                                    _ptr(lse), _ptr(workspace), need, _stream(stream)), "mla_decode_attn")
@@ -433,17 +462,18 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
     T, Hq, D = q.shape
     R = seq_lens.numel()
     reqs = reqs or Reqs(max_reqs=R, batch_reqs=R)
+    other = _other(stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, other)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((T, Hq), torch.float32, q.device, other)
     need = 0
     if cache.kv_dtype == _lib.KV_FP8_E4M3:
         need = extend_fp8_workspace_size(reqs.max_reqs, reqs.batch_reqs, max_seq_len, block_tables.shape[1],
                                          cache.num_kv_heads, cache.head_dim)
     elif cache.kv_dtype == _lib.KV_FP8_E4M3_BLOCK:
         need = extend_block_workspace_size(max_q_len, max_seq_len, Hq, cache.num_kv_heads)
-    workspace = _scratch(need, workspace, q.device, stream)
+    workspace = _scratch(need, workspace, q.device, other)
     _check(lib.pkv_extend_attn(_ptr(q), _ptr(k_new), _ptr(v_new), T, _ptr(cu_q), _ptr(seq_lens), cache,
                                _ptr(block_tables), block_tables.shape[1], reqs.c(), Hq, max_q_len,
                                max_seq_len, chunk_budget_tokens, _scale(scale, D), _ptr(out),
@@ -471,10 +501,11 @@ def varlen_prefill_attn(q, k, v, cu_seqlens, max_seqlen, reqs: Optional[Reqs] = 
     Hkv = k.shape[1]
     R = cu_seqlens.numel() - 1
     reqs = reqs or Reqs(max_reqs=R, batch_reqs=R)
+    other = _other(stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, other)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((T, Hq), torch.float32, q.device, other)
     _check(lib.pkv_varlen_prefill_attn(_ptr(q), _ptr(k), _ptr(v), T, _ptr(cu_seqlens), reqs.c(), Hq,
                                        Hkv, D, max_seqlen, _scale(scale, D), _ptr(out), _ptr(lse),
                                        _stream(stream)), "varlen_prefill_attn")
