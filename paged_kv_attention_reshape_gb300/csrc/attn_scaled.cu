@@ -17,7 +17,9 @@
 // the sum, and its conversions, 9 instructions for a pair of codes against 2, took 2.5 times as long:
 // 5.7 ms against 2.3 on 8 x 512 tokens over contexts of 4K to 32K, Hq 64 / Hkv 8.)
 // Queries and new keys become fp16 and must lie within its range; new values and their P stay bf16,
-// so values of any size pass.
+// so values of any size pass. A score that is no number makes l one and so the row's out and lse: the max of u
+// passes over it, so a part of the keys (a slot's, a copy's, a piece's) is one without keys for a row where its l
+// is 0, whatever its m. A row has a key at least, its own, so that its l is never 0 as a whole.
 //
 // Work items. The rows of a request for one KV head are its (token, query head of the group) pairs,
 // tokens outermost, in tiles of 128 (a box of Q is G heads x 128 / G tokens). An item is two such
@@ -728,8 +730,8 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         par ^= 2;
         const float2 o1 = mrg[t];
         const float mm = fmaxf(m, o1.x);
-        w0 = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mm);
-        w1 = o1.x == -CUDART_INF_F ? 0.f : ex2_approx(o1.x - mm);
+        w0 = l == 0.f ? 0.f : ex2_approx(m - mm);
+        w1 = o1.y == 0.f ? 0.f : ex2_approx(o1.x - mm);
         l = l * w0 + o1.y * w1;
         m = mm;
       }
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         const int64_t tk = static_cast<int64_t>(it.row0) + tok;
         return tok < it.q_len && tk < p.num_tokens ? tk * p.Hq + it.kh * p.G + rr % p.G : -1;
       };
-      const float inv = l > 0.f ? w0 / l : 0.f, inv1 = l > 0.f ? w1 / l : 0.f;
+      const float inv = w0 / l, inv1 = w1 / l;
       // O leaves through the warp's staging tile (32 rows x 32 columns at a time): each thread puts
       // its row there, then every store instruction writes 8 rows x 64 contiguous bytes
       uint32_t tid_now;
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       if (both) mbar_arrive(&bar.merge_done);
       if (p.lse) {
         const int64_t fr = flat_row(t);
-        if (fr >= 0) p.lse[fr] = l > 0.f ? (m - AsBase::RAISE + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+        if (fr >= 0) p.lse[fr] = (m - AsBase::RAISE + __log2f(l)) * 0.69314718055994531f;
       }
     }
     } else {
@@ -947,14 +949,16 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       if (!as_wait(&bar.o_final[0], oc & 1, &s_abort, p.err)) break;
       ++oc;
       float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and of slot 1's
+      bool has0 = l != 0.f, has1 = false;  // whether they had keys
       if (both) {
         if (!as_wait(&bar.o_final[1], par & 1, &s_abort, p.err) || !as_wait(&bar.merge_full, (par >> 1) & 1, &s_abort, p.err))
           break;
         par ^= 3;
         const float2 o1 = mrg[t];
         const float mm = fmaxf(m, o1.x);
-        w0 = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mm);
-        w1 = o1.x == -CUDART_INF_F ? 0.f : ex2_approx(o1.x - mm);
+        has1 = o1.y != 0.f;
+        w0 = has0 ? ex2_approx(m - mm) : 0.f;
+        w1 = has1 ? ex2_approx(o1.x - mm) : 0.f;
         l = l * w0 + o1.y * w1;
         m = mm;
       }
@@ -967,12 +971,13 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       for (int i = row; i < 128; i += span) mm = fmaxf(mm, rml[i].x);
       for (int i = row; i < 128; i += span) {
         const float2 o = rml[i];
-        ll += o.x == -CUDART_INF_F ? 0.f : o.y * ex2_approx(o.x - mm);
+        ll += o.y == 0.f ? 0.f : o.y * ex2_approx(o.x - mm);
       }
       const bool whole = it.slot < 0;
       const AsPartials part = as_partials(ws, ws_slots, C::ROWS);
-      const float wr = m == -CUDART_INF_F ? 0.f : whole ? (ll > 0.f ? ex2_approx(m - mm) / ll : 0.f) : ex2_approx(m - mm);
+      const float wr = ex2_approx(m - mm) / (whole ? ll : 1.f);
       w0 *= wr, w1 *= wr;
+      if (whole && ll == 0.f) has0 = true;  // every score is -inf: no number
       tc::fence_after_sync();
       const int rows = min(it.q_len, static_cast<int>(min(static_cast<int64_t>(it.q_len), p.num_tokens - it.row0))) * p.G;
       const uint32_t stg = smem_u32(smem) + C::STAGE_OFF;  // [128 rows][32 fp32], 128-byte swizzle
@@ -984,7 +989,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         tc::touch32(o);
         // (a state without keys has no part, whatever the tensor core made of its row)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = w0 > 0.f ? __float_as_uint(__uint_as_float(o[e]) * w0) : 0u;
+        for (int e = 0; e < 32; ++e) o[e] = has0 ? __float_as_uint(__uint_as_float(o[e]) * w0) : 0u;
         if (both) {
           uint32_t o1[32];
           tc::ld32(tmem + as_ocol(1) + lane_off + c * 32, o1);
@@ -992,7 +997,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
           tc::touch32(o1);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (w1 > 0.f) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
+            if (has1) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -1038,7 +1043,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         if (t < span) part.ml[static_cast<int64_t>(it.slot) * C::ROWS + t] = make_float2(mm, ll);
       } else if (p.lse && t < min(span, rows))
         p.lse[(static_cast<int64_t>(it.row0) + tok) * p.Hq + it.kh * p.G + (row & (p.G - 1))] =
-            ll > 0.f ? (mm - AsBase::RAISE + __log2f(ll)) * 0.69314718055994531f : -CUDART_INF_F;
+            (mm - AsBase::RAISE + __log2f(ll)) * 0.69314718055994531f;
     }
     }
   } else if (!FEW && warp >= C::W_CONV) {
@@ -1353,7 +1358,7 @@ __global__ void __launch_bounds__(256) attn_scaled_merge_kernel(const AttnParams
     for (int i = 0; i < np; ++i) {
       const float2 x = ml(i);
       const float4 y = part.o[(static_cast<int64_t>(2 * (share + i) + (i == 0)) * 32 + c4) * ROWS + row];
-      if (x.x != -CUDART_INF_F) {  // (a piece without a key for the row has no part)
+      if (x.y != 0.f) {  // (a piece without a key for the row has no part)
         const float w = ex2_approx(x.x - m);
         l = fmaf(x.y, w, l);
         s = make_float4(fmaf(y.x, w, s.x), fmaf(y.y, w, s.y), fmaf(y.z, w, s.z), fmaf(y.w, w, s.w));
@@ -1363,9 +1368,9 @@ __global__ void __launch_bounds__(256) attn_scaled_merge_kernel(const AttnParams
     const int64_t tok = static_cast<int64_t>(it.y) + rr / p.G;
     if (row >= rows || tok >= p.num_tokens) continue;
     const int64_t fr = tok * p.Hq + it.w * p.G + rr % p.G;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = 1.f / l;
     *reinterpret_cast<uint2*>(p.out + fr * 128 + c4 * 4) = make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
-    if (p.lse && c4 == 0) p.lse[fr] = l > 0.f ? (m - AsBase::RAISE + __log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+    if (p.lse && c4 == 0) p.lse[fr] = (m - AsBase::RAISE + __log2f(l)) * 0.69314718055994531f;
   }
 }
 

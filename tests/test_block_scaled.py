@@ -926,6 +926,57 @@ def test_extend_of_many_requests_and_neighbours_that_are_not_finite():
     check_extend(st, out, lse, SCALE, reqs=[r for r in range(n) if r != 7])
 
 
+def check_rows_that_are_no_numbers(st, out, lse):
+    """out and lse are NaN where the definition in 64 bits says so, and within their bounds elsewhere."""
+    Hkv = st["ks"].shape[1]
+    G = st["q"].shape[1] // Hkv
+    out, lse = out.cpu(), lse.cpu()
+    for r, c in enumerate(st["ctx"]):
+        rows = slice(int(st["cu"][r]), int(st["cu"][r + 1]))
+        for h in range(Hkv):
+            hq = slice(h * G, (h + 1) * G)
+            k, v = context(st, r, h, c)
+            k, v = torch.cat([k, st["k_new"][rows, h].double()]), torch.cat([v, st["v_new"][rows, h].double()])
+            q = st["q"][rows, hq].double()
+            o, z, A, M = dense(q, k, v, SCALE, c)
+            a, b = out[rows, hq].double(), lse[rows, hq].double()
+            assert torch.equal(o.isnan(), a.isnan()), f"request {r} head {h}"
+            assert torch.equal(z.isnan(), b.isnan()) and torch.equal(z.isinf(), b.isinf()), f"request {r} head {h}"
+            e = 2.0 ** -16 * M + 2.0 ** -20 * (1 + z.abs())
+            fixed = fixed_steps(st, r, h, c, q, k, SCALE, c, 2.0 ** -32)
+            assert bool(((b - z).abs() <= e)[z.isfinite()].all()), f"request {r} head {h}"
+            tol = U * o.abs() + (U + 2 * e[..., None]) * A + fixed + 1e-37
+            assert bool(((a - o).abs() <= tol)[o.isfinite()].all()), f"request {r} head {h}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["q", "k", "v", "new_k", "all", "below"])
+@pytest.mark.parametrize("ctx,new,G,Hkv", [
+    ([300, 40], [4, 2], 8, 2), ([257, 3], [8, 8], 16, 1), ([9001, 20], [4, 3], 8, 1),          # up to 128 rows; the last in pieces
+    ([130, 20], [200, 9], 4, 2), ([700, 33], [40, 100], 2, 1), ([4000, 3000, 5], [200, 90, 1], 4, 2)])
+def test_extend_of_what_is_no_number(ctx, new, G, Hkv, what):
+    """A NaN in a query, in a cached key or value, in a new key: NaN in the rows (or dims) that attend to it, in out and
+    lse, whatever the launch and the plan; the other rows as they are. Scores that are all -inf: NaN, and lse -inf."""
+    st = extend_state(ctx, new, G * Hkv, Hkv, seed=90 + G, qs=1.0)
+    if what == "q":
+        st["q"][1, 0, 77] = math.nan
+        st["q"][int(st["cu"][1]), G * Hkv - 1] = math.nan
+    elif what in ("k", "v"):
+        st[what + "c"][int(st["table"][0, ctx[0] // 32]), 5, 0, 9] = 0x7F
+    elif what == "new_k":  # the second token's key: every row of the request but the first
+        st["k_new"][int(st["cu"][1]) + 1, Hkv - 1, 100] = math.nan
+    elif what == "all":
+        st["q"][0] = math.nan
+        for r in range(len(ctx)):
+            st["kc"][st["table"][r, :(ctx[r] + 15) // 16].long()] = 0xFF
+    else:  # a token without context, its one score -inf
+        st["ctx"] = [ctx[0], 0] + ctx[2:]
+        t = int(st["cu"][1])
+        st["q"][t, 0], st["k_new"][t, 0] = 0.5, 0.5
+        st["q"][t, 0, 3], st["k_new"][t, 0, 3] = math.inf, -1.0
+    check_rows_that_are_no_numbers(st, *gpu_extend(st))
+
+
 @pytest.mark.gpu
 def test_extend_flags_bad_blocks():
     st = extend_state([100, 200], [5, 6], 8, 2, seed=30)
