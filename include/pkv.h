@@ -13,16 +13,14 @@
  *   - Every pointer argument is a DEVICE pointer owned by the caller, except where a
  *     comment says "host". The library allocates no device memory and keeps no state
  *     between calls other than one per-device error word (pkv_device_errors), the handoff
- *     handles the caller creates (pkv_handoff_create) and, per device, 64 work-item counter
- *     slots of the extend/prefill kernel and 64 of the extend kernel of block-scaled caches (each launch takes the next slot and leaves it at zero;
- *     a launch shares its slot only with the launch 64 extend/prefill launches later, so at
- *     most 63 other such launches may be in flight at once on one device, and one captured
- *     graph must not be replayed on two streams at the same time).
- *   - Every call is asynchronous on `stream` (a cudaStream_t; NULL = legacy default stream)
- *     and returns after checking its host-side arguments and enqueueing its kernels. It
- *     never synchronises, except pkv_device_errors.
- *   - bf16 is IEEE bfloat16 (raw 16-bit storage). Accumulation is fp32.
- *   - A status other than PKV_OK means nothing was enqueued.
+ *     handles the caller creates (pkv_handoff_create) and, per device, work-item counter slots
+ *     of the extend/prefill kernel and of the extend kernel of block-scaled caches. A launch
+ *     issued directly takes the next of 4096 slots and leaves it at zero; it shares its slot only
+ *     with the launch 4096 extend/prefill launches later, so at most 4095 other such launches
+ *     may be in flight at once on one device. A launch captured into a graph takes a slot that
+ *     no other launch of the process ever has (8192 of them; later captured launches deal their
+ *     work without one, somewhat less evenly), so replays may run beside direct calls and beside
+ *     other graphs. One captured graph must not run twice at the same time.
  *   - Indices that live in device memory (slots, block ids, request ids, lengths) cannot be
  *     checked on the host. Kernels check them instead: an out-of-range index is skipped (no
  *     memory outside the caller's buffers is touched) and a bit is set in the device error

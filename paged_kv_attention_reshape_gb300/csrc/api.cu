@@ -69,10 +69,22 @@ uint32_t next_epoch() {
   return e;
 }
 
-// The extend/prefill kernel's work-item counter slot of the next launch (process-wide, in turn).
-int32_t next_sched_slot() {
-  static std::atomic<uint32_t> seq{0};
-  return static_cast<int32_t>(seq.fetch_add(1, std::memory_order_relaxed) % kAttnSchedSlots);
+// The work-item counter slot of the next extend/prefill launch on the stream (see launch.h). A captured launch keeps
+// its slot for as long as its graph lives, so it must not come round to it again for any other launch: that one and a
+// replay may run at the same time.
+int32_t next_sched_slot(cudaStream_t stream) {
+  static std::atomic<uint32_t> seq{0}, captured{0};
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &st) != cudaSuccess) {
+    cudaGetLastError();  // (the legacy stream while another one captures: the launch itself says so)
+    st = cudaStreamCaptureStatusNone;
+  }
+  if (st == cudaStreamCaptureStatusNone)
+    return static_cast<int32_t>(seq.fetch_add(1, std::memory_order_relaxed) % kAttnEagerSlots);
+  uint32_t n = captured.load(std::memory_order_relaxed);
+  while (n < kAttnCaptureSlots && !captured.compare_exchange_weak(n, n + 1, std::memory_order_relaxed)) {
+  }
+  return n < kAttnCaptureSlots ? static_cast<int32_t>(kAttnEagerSlots + n) : -1;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -747,7 +759,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   int launches = 0;
   for (int32_t off = 0; off < reqs.max_reqs && st == PKV_OK; off += kAttnSetChunk) {
     p.set_offset = off;
-    p.sched_slot = next_sched_slot();
+    p.sched_slot = next_sched_slot(reinterpret_cast<cudaStream_t>(stream));
     st = cuda_status(packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, workspace, reinterpret_cast<cudaStream_t>(stream), &launches)
                             : launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
                                                reinterpret_cast<cudaStream_t>(stream), &launches));

@@ -213,8 +213,8 @@ __device__ __forceinline__ int as_rank(const int* prefix, int n, int x) {
   return lo;
 }
 
-// Counters of claimed items and of finished CTAs; launch k uses slot k % kAttnSchedSlots and its last
-// CTA to finish sets the slot back to zero.
+// Counters of claimed items and of finished CTAs, in the launch's slot (launch.h); its last CTA to finish sets
+// the slot back to zero. Without a slot the pieces are dealt statically, in snake order.
 __device__ unsigned int g_as_next[kAttnSchedSlots];
 __device__ unsigned int g_as_done[kAttnSchedSlots];
 
@@ -1064,6 +1064,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       bool ok = true;
       AsItem* s_item = reinterpret_cast<AsItem*>(smem + C::ITEM_OFF);
       int share = 0, pos = 0, end = 0;  // the share whose pieces are being dealt: tiles [pos, end) of the tail
+      int turn = 0;                     // pieces taken of a static deal
       for (uint32_t items = 0; ok; ++items) {
         // take the next piece once the Q buffer is free, and publish it to the other roles
         if (items > 0 && !as_wait(&bar.q_empty, (items - 1) & 1, &s_abort, p.err)) break;
@@ -1073,8 +1074,13 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
         for (;;) {
           if (pos >= end) {
             int w = 0;
-            if (lane == 0) w = static_cast<int>(atomicAdd(&g_as_next[p.sched_slot], 1u));
-            w = __shfl_sync(0xffffffffu, w, 0);
+            if (p.sched_slot >= 0) {
+              if (lane == 0) w = static_cast<int>(atomicAdd(&g_as_next[p.sched_slot], 1u));
+              w = __shfl_sync(0xffffffffu, w, 0);
+            } else {
+              w = turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+              ++turn;
+            }
             if (w >= W) {
               it.NT = 0;
               break;
@@ -1308,7 +1314,7 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
   }
   // every role of this CTA is done, its producer's claims included: the launch's last CTA to get here
   // sets the scheduler slot back to zero for the next launch that uses it
-  if (tid == 0) {
+  if (tid == 0 && p.sched_slot >= 0) {
     __threadfence();
     if (atomicAdd(&g_as_done[p.sched_slot], 1u) == gridDim.x - 1) {
       atomicExch(&g_as_next[p.sched_slot], 0u);

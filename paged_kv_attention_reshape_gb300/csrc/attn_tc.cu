@@ -176,11 +176,12 @@ __device__ __forceinline__ int tc_cost(const int4& q) { return (q.w + 127) / 128
 //   * long items (long contexts): a static deal in snake order (CTA c takes items c, 2G-1-c,
 //     2G+c, ...; G CTAs), which keeps the CTAs that read the same context in step, so that one
 //     CTA's tiles are still in L2 for the others (claiming measured 2-3 % slower there).
-// The counters live in a small array of slots; the host gives every launch the next slot in
-// turn, and the last CTA of a launch to finish sets its slot back to zero, so the next launch on
-// that slot (or a replay of the same launch) starts from zero. Launches that use one slot must
-// not run at the same time: at most kAttnSchedSlots - 1 other launches of this kernel may be in
-// flight on the device between them.
+// The counters live in an array of slots; the host gives a launch the next slot in turn, or one
+// of its own if it is captured (launch.h), and the last CTA of a launch to finish sets its slot
+// back to zero, so the next launch on that slot (or a replay of the same launch) starts from
+// zero. Launches that use one slot must not run at the same time: at most kAttnEagerSlots - 1
+// other direct launches may be in flight on the device between them. Without a slot all items
+// are dealt statically.
 __device__ unsigned int g_attn_next[kAttnSchedSlots];
 __device__ unsigned int g_attn_done[kAttnSchedSlots];
 constexpr int kDynamicBelow = 64;
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
       qtiles += __shfl_xor_sync(0xffffffffu, qtiles, o);
     }
-    if (lane == 0) s_claim = tiles < static_cast<long long>(kDynamicBelow) * qtiles ? 1 : 0;
+    if (lane == 0) s_claim = p.sched_slot >= 0 && tiles < static_cast<long long>(kDynamicBelow) * qtiles ? 1 : 0;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -1017,7 +1018,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
   }
   // every role of this CTA is done, its producer's claims included: the launch's last CTA to
   // get here sets the scheduler slot back to zero for the next launch that uses it
-  if (tid == 0) {
+  if (tid == 0 && p.sched_slot >= 0) {
     __threadfence();
     if (atomicAdd(&g_attn_done[p.sched_slot], 1u) == gridDim.x - 1) {
       atomicExch(&g_attn_next[p.sched_slot], 0u);

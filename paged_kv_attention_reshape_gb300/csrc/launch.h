@@ -19,9 +19,11 @@ constexpr int kSetChunk = 1024;
 // The extend/prefill kernel holds 256 (its shared memory goes to the K/V ring and the output
 // staging); its sets are chunked the same way.
 constexpr int kAttnSetChunk = 256;
-// Slots of the extend/prefill kernel's work-item counters (attn_tc.cu): launch k uses slot
-// k % kAttnSchedSlots.
-constexpr int kAttnSchedSlots = 64;
+// Slots of the extend/prefill kernels' work-item counters (attn_tc.cu, attn_scaled.cu). Launch k that is issued
+// directly uses slot k % kAttnEagerSlots; a launch that is captured into a graph has a slot of its own, which nothing
+// else ever uses, for the first kAttnCaptureSlots of the process, and none (-1: items are dealt statically) after them.
+constexpr int kAttnEagerSlots = 4096, kAttnCaptureSlots = 8192;
+constexpr int kAttnSchedSlots = kAttnEagerSlots + kAttnCaptureSlots;
 
 struct DecodeParams {
   unsigned int* err;  // device error word
@@ -84,7 +86,7 @@ struct AttnParams {
   float ctx_v_scale;     // cached-context tiles: P is multiplied by the value scale for P V
   const float* k_scales;  // block-scaled cache: [num_blocks][Hkv]
   const float* v_scales;
-  int32_t sched_slot;    // this launch's work-item counter slot (< kAttnSchedSlots)
+  int32_t sched_slot;    // this launch's work-item counter slot (< kAttnSchedSlots); -1: none
 };
 
 // Extend over an FP8 cache: the set's context blocks gathered into a bf16 pool (exact E4M3

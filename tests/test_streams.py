@@ -114,3 +114,117 @@ def test_the_current_stream_by_name_and_the_default_stream():
         torch.cuda.synchronize()
         assert all(_same(x, want) for x in got)
     assert pkv.device_errors() == 0 and math.isfinite(float(got[0][0].float().sum()))
+
+
+@pytest.mark.parametrize("kind", ["prefill", "extend", "extend_block"])
+def test_graphs_beside_direct_calls_and_beside_one_another(kind):
+    """Two graphs of several launches and direct calls, each on a stream of its own and with buffers of its own, all at
+    once: no launch takes another's work items."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    g = torch.Generator().manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    R, n, Hq, Hkv, nb = 24, 40, 16, 2, 24 * 40
+    q, k, v = rnd(R * n, Hq, 128), rnd(R * n, Hkv, 128), rnd(R * n, Hkv, 128)
+    cu, lens = _dev(torch.arange(0, R * n + 1, n, dtype=torch.int32), torch.randint(n, 600, (R,), generator=g).to(torch.int32))
+    table = torch.randperm(nb, generator=g).to(torch.int32).view(R, 40).contiguous().cuda()
+    if kind == "extend_block":
+        cache = [torch.randint(0, 100, (nb, 16, Hkv, 128), generator=g, dtype=torch.uint8).cuda() for _ in "kv"]
+        more = {x: (torch.rand((nb, Hkv), generator=g) * 0.01 + 0.001).cuda() for x in ("k_scale", "v_scale")}
+    else:
+        cache, more = [rnd(nb, 16, Hkv, 128) for _ in "kv"], {}
+
+    def call(out, lse):
+        if kind == "prefill":
+            pkv.varlen_prefill_attn(q, k, v, cu, n, out=out, lse=lse)
+        else:
+            pkv.extend_attn(q, k, v, cu, lens, *cache, table, n, 600, out=out, lse=lse, **more)
+
+    bufs = [(torch.zeros_like(q), torch.zeros((R * n, Hq), device="cuda")) for _ in range(4)]
+    call(*bufs[3])
+    torch.cuda.synchronize()
+    want = [t.clone() for t in bufs[3]]
+    bad = [torch.zeros((), dtype=torch.bool, device="cuda") for _ in range(3)]
+
+    def checked(i):  # a call on cleared buffers, and whether it gave what it has to
+        out, lse = bufs[i]
+        out.fill_(7.0), lse.fill_(7.0)
+        call(out, lse)
+        bad[i] |= (out != want[0]).any() | (lse != want[1]).any()
+
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graphs = []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            for _ in range(6):
+                checked(i)
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        with torch.cuda.stream(streams[2]):
+            for _ in range(6):
+                checked(2)
+    torch.cuda.synchronize()
+    assert not any(bool(b) for b in bad) and pkv.device_errors() == 0
+
+
+_MANY = """
+import sys, torch
+sys.path[:0] = ["tests", "."]
+import paged_kv_attention_reshape_gb300 as pkv
+g = torch.Generator().manual_seed(6)
+rnd = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).cuda()
+codes = [torch.randint(0, 100, (40, 16, 1, 128), generator=g, dtype=torch.uint8).cuda() for _ in "kv"]
+more = {x: (torch.rand((40, 1), generator=g) * 0.01 + 0.001).cuda() for x in ("k_scale", "v_scale")}
+table = torch.randperm(40, generator=g).to(torch.int32).view(2, 20).cuda()
+one, cu1 = rnd(1, 1, 128), torch.tensor([0, 1], dtype=torch.int32).cuda()
+out1, lse1 = torch.empty_like(one), torch.empty((1, 1), device="cuda")
+fill = lambda: pkv.varlen_prefill_attn(one, one, one, cu1, 1, out=out1, lse=lse1)
+R, n = 200, 9
+q, k, v = rnd(R * n, 8, 128), rnd(R * n, 1, 128), rnd(R * n, 1, 128)
+cu = torch.arange(0, R * n + 1, n, dtype=torch.int32).cuda()
+lens = torch.randint(n, 310, (R,), generator=g).to(torch.int32).cuda()
+tables = table[torch.arange(R) % 2].contiguous()
+out, lse = torch.zeros_like(q), torch.zeros((R * n, 8), device="cuda")
+calls = [lambda: pkv.varlen_prefill_attn(q, k, v, cu, n, out=out, lse=lse),
+         lambda: pkv.extend_attn(q, k, v, cu, lens, *codes, tables, n, 310, out=out, lse=lse, **more),
+         lambda: pkv.extend_attn(q, k, v, cu, lens, *codes, tables, 30, 2000, out=out, lse=lse, **more)]
+want = []
+for f in calls:
+    f()
+    want.append((out.clone(), lse.clone()))
+fill()
+s = torch.cuda.Stream()
+torch.cuda.synchronize()
+with torch.cuda.stream(s):
+    graph = torch.cuda.CUDAGraph()
+    graph.capture_begin()
+    for _ in range(8200):
+        fill()
+    graph.capture_end()
+del graph
+for f, (o, l) in zip(calls, want):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f()
+    for _ in range(3):
+        out.zero_(), lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, o) and torch.equal(lse, l)
+assert pkv.device_errors() == 0
+print("as before")
+"""
+
+
+def test_more_captured_launches_than_there_are_slots():
+    """A process that has captured more extend/prefill launches than have a slot of their own: the later ones deal
+    their items statically and give the same."""
+    import os
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", _MANY], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "as before" in r.stdout, r.stdout + r.stderr
