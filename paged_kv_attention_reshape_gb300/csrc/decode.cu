@@ -31,7 +31,8 @@
 //     CTA and head; per tree node an arrival counter, and the arrival that completes a node's
 //     count merges its children), so a long sequence cut into n pieces costs a chain of about
 //     log4(n) small merges. Counters carry the call's epoch, so a counter left by an earlier
-//     call reads as empty and the workspace needs no clearing. No second kernel, no
+//     call reads as empty and the workspace needs no clearing, and are zero again when their node
+//     is complete (a replayed graph has its epoch again). No second kernel, no
 //     shared-memory combine, no block-wide barrier after the prologue.
 #include <math_constants.h>
 

@@ -205,7 +205,9 @@ struct PieceIter {
 // shape may hold fp32 partials where this call's counters lie) and counts as empty. The tag
 // makes the low word a signalling-NaN bit pattern, which no arithmetic result takes (the GPU's
 // NaN results are the canonical quiet NaN), so a stale pair of partial floats never passes for
-// a counter, whatever the epoch has wrapped to.
+// a counter, whatever the epoch has wrapped to. A replay of a captured call has that call's epoch
+// again: whoever finds a node complete sets its counter back to zero, so that the next replay,
+// whose sequences may be cut otherwise, starts from no arrivals.
 constexpr uint32_t kCtrTag = 0x7FA5A500u;
 __device__ __forceinline__ uint32_t arrivals_of(unsigned long long v, uint32_t epoch, int total) {
   const uint32_t lo = static_cast<uint32_t>(v), cnt = lo & 0xFFu;
@@ -227,6 +229,8 @@ __device__ __forceinline__ int arrive_counter(unsigned long long* ctr, uint32_t 
   flag_error(err, PKV_DEVERR_TIMEOUT);
   return 0;
 }
+
+__device__ __forceinline__ void clear_counter(unsigned long long* ctr) { atomicExch(ctr, 0ull); }
 
 // ---- the merge tree of a cut sequence -----------------------------------------------------------
 // The pieces p = 0 .. np-1 of one unit's cut sequence sit in consecutive shares c0 + p: piece 0
@@ -501,6 +505,7 @@ struct CutMerger {
           return;
         }
         __threadfence();
+        if (lane == 0) clear_counter(ctr);
         fold_siblings<D>(p, s, L, a, k, ai - a * kFan, kh, o, lse, lane);
         check = true;  // the siblings were in: the next level is likely complete too
       }
@@ -521,6 +526,7 @@ struct CutMerger {
     if (lane == 0) {
       const int k = st->pend_k;
       if (arrive_counter(st->pend_ctr, p.epoch, k, st->pend_cur, p.err) == k) {
+        clear_counter(st->pend_ctr);
         const int d = st->due;
         if (d < 2) {
           st->due_s[d] = st->pend_s;
@@ -560,7 +566,11 @@ struct CutMerger {
         __threadfence();
         __syncwarp();
         int arrived = 0;
-        if (lane == 0) arrived = arrive_counter(node_ctr(p, s, L, a, kh), p.epoch, k, 0ull, p.err);
+        if (lane == 0) {
+          unsigned long long* ctr = node_ctr(p, s, L, a, kh);
+          arrived = arrive_counter(ctr, p.epoch, k, 0ull, p.err);
+          if (arrived == k) clear_counter(ctr);
+        }
         if (__shfl_sync(0xffffffffu, arrived, 0) != k) break;
         __threadfence();
       }
