@@ -15,7 +15,8 @@
 //     takes the V codes as they lie (M = 128 dims, M-major) and P as N columns.
 //   * q and P are split into E4M3 parts, x = hi + lo / 16, which sit side by side on N: NG columns
 //     of hi and NG of lo (NG = G padded to 8 or 16). E4M3 has 4 significant bits. A bf16 q (8
-//     bits) is exactly hi + lo down to 2^-14 of the group's largest |q|, to 2^-21 of it below. P's
+//     bits) is exactly hi + lo down to 2^-14 of its head's largest |q|, to 2^-21 of it below (each head
+//     has a power of two of its own, so that heads of very different size keep the same bits). P's
 //     error is at most 2^-9 of P, to 2^-14 of the tile's largest P, and at most 2^-22 of the largest
 //     below: better than bf16's 2^-9 where it counts.
 //     The products are exact in fp32.
@@ -64,8 +65,8 @@ struct SdCfg {
   static constexpr int FAC_OFF = WMAX_OFF + 2 * 4 * NG * 4;  // [4 warps][2][3: M, a, c][NG]
   static constexpr int LSUM_OFF = FAC_OFF + 4 * 2 * 3 * NG * 4;  // [2][4 warps][NG]
   static constexpr int INV_OFF = LSUM_OFF + 2 * 4 * NG * 4;  // [4 warps][NG]
-  static constexpr int QMAX_OFF = INV_OFF + 4 * NG * 4;   // [2][4 warps]
-  static constexpr int BAR_OFF = QMAX_OFF + 32;
+  static constexpr int QINV_OFF = INV_OFF + 4 * NG * 4;   // [2][NG] softmax scale over a head's power of two
+  static constexpr int BAR_OFF = QINV_OFF + 2 * NG * 4;
   static constexpr int NBAR = 2 * NB + 13;
   static constexpr int MISC_BYTES = (BAR_OFF + NBAR * 8 - SC_OFF + 127) / 128 * 128;
   static constexpr int CHAIN = (SC_OFF + MISC_BYTES + 1023) / 1024 * 1024;
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
     float* fac = reinterpret_cast<float*>(base + C::FAC_OFF) + w4 * (2 * 3 * NG);
     float* lsum = reinterpret_cast<float*>(base + C::LSUM_OFF);
     float* invs = reinterpret_cast<float*>(base + C::INV_OFF) + w4 * NG;
-    uint32_t* qmax = reinterpret_cast<uint32_t*>(base + C::QMAX_OFF);
+    float* qinv = reinterpret_cast<float*>(base + C::QINV_OFF);
 
     // ---- queries: each piece's tile is converted one piece ahead, its rows loaded two ahead ----
     constexpr int QP = 128 / NG;                  // threads per head
@@ -350,7 +351,6 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
     Piece qpc;
     bool qhave;
     uint32_t qn = 0;                              // pieces converted
-    float qinv[2];                                // 2^-e of the two tiles that are held
     auto load_q = [&]() {
       qhave = qit.next(qpc);
       if (qhave && qh < p.G) {
@@ -374,22 +374,21 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
           x[8 * i + 2 * j + 1] = __uint_as_float(wv[j] & 0xFFFF0000u);
         }
       }
-      uint32_t top = 0;  // the group's largest finite |q|
+      uint32_t top = 0;  // the head's largest finite |q|
 #pragma unroll
       for (int i = 0; i < QE; ++i) {
         const uint32_t m = __float_as_uint(x[i]) & 0x7FFFFFFFu;
         top = max(top, m < 0x7F800000u ? m : 0u);
       }
-      top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+      for (int bit = QP / 2; bit > 0; bit >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, bit));
       const uint32_t b = qn & 1;
-      if (lane == 0) qmax[4 * b + w4] = top;
-      chain_sync(chain);
-      top = max(max(qmax[4 * b], qmax[4 * b + 1]), max(qmax[4 * b + 2], qmax[4 * b + 3]));
       // 2^e |q| in [128, 256) for the largest
-      const int e = min(max(134 - static_cast<int>(top >> 23), -100), 100);
+      const int e = min(max(134 - static_cast<int>(top >> 23), -126), 126);
       const float qs = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      const float qi = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      if (b == 0) qinv[0] = qi; else qinv[1] = qi;
+      // (read a barrier of the chain later: the first piece's after the one below, the next pieces' after the one of a
+      // tile of the piece before)
+      if (qd == 0) qinv[b * NG + qh] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       uint32_t hi[QE / 4], lo[QE / 4];
 #pragma unroll
       for (int i = 0; i < QE; i += 4) {
@@ -430,6 +429,7 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
     qit.start(s_pre, n, 1, b0, b1);
     load_q();
     convert_q();
+    chain_sync(chain);
 
     float o[NG], l[NG], pl[NG];  // the piece's sums; the last tile's P / vs of this token
     float m_run = -CUDART_INF_F, m_fin = 0.f;  // lane h: running max of head h; that of the piece before
@@ -553,14 +553,20 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
         if (lane == 0) mbar_arrive(&bar.s_empty[buf]);
         const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF) + gt % C::SRING * 16;
         // a zero scale counts as 2^-100: no logarithm of 0
-        const float qi = (pieces & 1) ? qinv[0] : qinv[1];
-        const float ks = fmaxf(sc[t >> 4], 0x1p-100f) * (p.scale_log2 * qi), vs = fmaxf(sc[8 + (t >> 4)], 0x1p-100f);
+        const float4* qi4 = reinterpret_cast<const float4*>(qinv + ((pieces & 1) ? 0 : NG));
+        const float ks = fmaxf(sc[t >> 4], 0x1p-100f), vs = fmaxf(sc[8 + (t >> 4)], 0x1p-100f);
         const float lvs = __log2f(vs), ivs = 1.f / vs;
         const bool valid = t < ntok;
 #pragma unroll
-        for (int h = 0; h < NG; ++h) {
-          const float x = fmaf(__uint_as_float(v[NG + h]), 0.0625f, __uint_as_float(v[h]));
-          u[h] = valid ? fmaf(x, ks, lvs) : -CUDART_INF_F;
+        for (int q = 0; q < NG / 4; ++q) {
+          const float4 f4 = qi4[q];
+          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = 4 * q + i;
+            const float x = fmaf(__uint_as_float(v[NG + h]), 0.0625f, __uint_as_float(v[h]));
+            u[h] = valid ? fmaf(x, ks * f[i], lvs) : -CUDART_INF_F;
+          }
         }
         float mw[NG];
 #pragma unroll

@@ -561,6 +561,55 @@ def test_decode_gives_the_same_bits_every_time(G, Hkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G,Hkv", [(16, 1), (8, 2), (4, 3), (2, 2)])
+def test_decode_heads_of_very_different_size(G, Hkv):
+    """Heads 2^20 apart in one group: each keeps its own bits (the scores of the small ones are of ordinary size)."""
+    st = decode_state([300, 5, 2500, 129, 1000], G * Hkv, Hkv, seed=7 + G)
+    size = torch.exp2(torch.tensor([10.0, -10.0] * (G * Hkv // 2)))
+    st["q"] = (st["q"].float() * size[None, :, None]).to(torch.bfloat16)
+    st["q"][1, 0], st["q"][1, 1] = 0, st["q"][0, 1]
+    st["ks"] = st["ks"] * 2.0 ** 10
+    check_decode(st, *gpu_decode(st), SCALE)
+    # the largest and the smallest numbers of bf16
+    st["ks"] = st["ks"] * 2.0 ** -10
+    scale = 2.0 ** -30
+    st["q"] = (st["q"].float() * torch.exp2(torch.tensor([105.0, -100.0] * (G * Hkv // 2)))[None, :, None]).to(torch.bfloat16)
+    st["ks"] = st["ks"] * 2.0 ** -85
+    check_decode(st, *gpu_decode(st, scale=scale), scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["q", "k", "v", "inf"])
+@pytest.mark.parametrize("lens,G,Hkv", [([300, 40, 7], 8, 2), ([9001, 20], 16, 1), ([777] * 60, 4, 8)])
+def test_decode_of_what_is_no_number(lens, G, Hkv, what):
+    """A NaN in a query, a cached key or a cached value: NaN in out and lse of the rows (or dims) that attend to it, whole
+    or cut; the other rows as they are."""
+    st = decode_state(lens, G * Hkv, Hkv, seed=90 + G)
+    if what == "q":
+        st["q"][0, 1, 77] = math.nan
+        st["q"][1, G * Hkv - 1] = math.nan
+    elif what == "inf":
+        st["q"][0, 1, 77] = math.inf
+    else:
+        st[what + "c"][int(st["table"][0, lens[0] // 32]), 5, 0, 9] = 0x7F
+    out, lse = gpu_decode(st)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    for r, c in enumerate(lens):
+        for h in range(Hkv):
+            hq = slice(h * G, (h + 1) * G)
+            q, (k, v) = st["q"][r:r + 1, hq].double(), context(st, r, h, c)
+            o, z, A, M = dense(q, k, v, SCALE)
+            a, b = out[r:r + 1, hq], lse[r:r + 1, hq]
+            if what == "inf" and r == 0 and h == 0:  # (scores that are infinite: no number, in 64 bits or here)
+                o[0, 1], z[0, 1] = math.nan, math.nan
+            assert torch.equal(o.isnan(), a.isnan()) and torch.equal(z.isnan(), b.isnan()), f"request {r} head {h}"
+            e = 2.0 ** -16 * M + 2.0 ** -20 * (1 + z.abs())
+            assert bool(((b - z).abs() <= e)[z.isfinite()].all()), f"request {r} head {h}"
+            tol = U * o.abs() + (U + 2 * e[..., None]) * A + fixed_steps(st, r, h, c, q, k, SCALE, None, 2.0 ** -22) + 1e-37
+            assert bool(((a - o).abs() <= tol)[o.isfinite()].all()), f"request {r} head {h}"
+
+
+@pytest.mark.gpu
 def test_decode_request_sets_rows_and_block_strides():
     """A reordered set of the batch with query rows from cu_q; rows outside it are left as they were."""
     import paged_kv_attention_reshape_gb300 as pkv
