@@ -29,8 +29,12 @@ constexpr int kBlockTokens = 16;  // block size of a block-scaled cache
 // Tokens from which rows go through shared memory. The times (64 query and 8 KV heads of 128, a bf16
 // cache, us on the GPU) through registers and through shared memory: 256 tokens 4.0 and 3.8, 512 5.8 and
 // 4.8, 1024 8.3 and 6.9, 4096 38.8 and 30.2; of 8 and 2 heads of 64: 256 2.3 and 2.8, 512 3.6 and 3.6, 1024
-// 4.8 and 4.4. Beside a block-scaled cache it is a launch more: 2048 17.7 and 22.7, 4096 43.3 and 38.9.
-constexpr int kManyTokens = 512, kManyTokensBlock = 2049;
+// 4.8 and 4.4. Beside a block-scaled cache it is a launch more, worth it later where a token has many query heads (inputs
+// and outputs beyond L2; a prompt's tokens; 64 and 8 heads, 64 and 4, 32 and 8, 8 and 2): 2048 tokens 22.7 and 27.6, 20.6
+// and 22.9, 18.8 and 22.0, 12.8 and 12.7; 2800 30.8 and 32.2, 27.7 and 27.3, 25.4 and 25.6, 16.8 and 15.2; 4096 44.6 and
+// 40.6, 40.5 and 35.7, 36.6 and 32.6, 23.8 and 19.6. (One token a sequence with 64 and 8 heads: 2800 72.8 and 78.6, 4096
+// 106 and 106.)
+constexpr int kManyTokens = 512, kManyTokensBlock = 2900, kManyTokensBlockFewHeads = 2048, kFewHeads = 16;
 
 __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -540,11 +544,16 @@ static bool launch_stream(const AppendParams& p, cudaStream_t stream, cudaError_
   return true;
 }
 
+// Tokens from which launch_rows sends them through shared memory.
+static int many_tokens(const AppendParams& p, int kind) {
+  if (kind != PKV_KV_FP8_E4M3_BLOCK) return kManyTokens;
+  return p.Hq > kFewHeads ? kManyTokensBlock : kManyTokensBlockFewHeads;
+}
+
 template <int KIND>
 static cudaError_t launch_rows(const AppendParams& p, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  constexpr int kMany = KIND == PKV_KV_FP8_E4M3_BLOCK ? kManyTokensBlock : kManyTokens;
-  if (p.num_tokens >= kMany && launch_stream<KIND>(p, stream, &e)) return e;
+  if (p.num_tokens >= many_tokens(p, KIND) && launch_stream<KIND>(p, stream, &e)) return e;
   return launch_pdl(kv_append_kernel<KIND, 1, 2, false>, dim3(static_cast<unsigned>(p.num_tokens)), dim3(kThreads), 0, stream, p);
 }
 
@@ -557,7 +566,7 @@ cudaError_t launch_kv_append(const AppendParams& in, int kind, cudaStream_t stre
   // 11.1, 9.7, 9.1; 4096 49, 39, 37; of one token a sequence 256 8.1, 18.5, 62; 1024 26, 25, 85; 4096 112, 105, 120.
   p.run_tokens = p.num_tokens <= 1024 ? 1 : (p.num_tokens <= 4096 ? 4 : kBlockTokens);
   p.run_groups = static_cast<uint32_t>((p.num_tokens + p.run_tokens - 1) / p.run_tokens);
-  if (p.Hq > 0 && p.num_tokens < kManyTokensBlock)
+  if (p.Hq > 0 && p.num_tokens < many_tokens(p, kind))
     return launch_pdl(kv_append_kernel<PKV_KV_FP8_E4M3_BLOCK, 1, 2, true>,
                       dim3(static_cast<unsigned>(p.run_groups + p.num_tokens)), dim3(kThreads), 0, stream, p);
   cudaError_t e = launch_pdl(kv_append_runs_kernel, dim3(p.run_groups), dim3(kThreads), 0, stream, p);

@@ -311,6 +311,18 @@ def test_append_block_scaled_batch_sizes(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,T", [(16, 2047), (16, 2048), (17, 2048), (17, 2899), (17, 2900)])
+def test_append_block_scaled_where_the_launch_changes(Hq, T):
+    """Batches on both sides of the sizes from which rows go through shared memory."""
+    ctx = [5, 16, 0, 31]
+    new = [T - 700, 600, 1, 99]
+    st = append_state("block", ctx, new, Hq, 1, 128, 128, seed=T + Hq, max_pos=T)
+    got, err = gpu_append(st)
+    assert err == 0
+    assert_append(got, plain_append(st))
+
+
+@pytest.mark.gpu
 def test_append_slices_of_a_fused_projection_in_place_and_a_shared_allocation():
     """q, k, v as slices of one [T, (Hq + 2 Hkv) d] tensor; K and V blocks interleaved in one allocation."""
     Hq, Hkv, d = 6, 2, 128
