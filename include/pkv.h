@@ -45,7 +45,9 @@
  *   pkv_extend_fp8_workspace_size).
  *   PKV_KV_FP8_E4M3_BLOCK: the same codes with a scale of their own for each block and KV head,
  *   code c of head h in block b standing for e4m3(c) * k_scales[b, h] (V: v_scales). Scales are
- *   positive and finite; any such values may be read. kv_append writes such a cache (with
+ *   positive and finite; one below 2^-100 counts as 2^-100. The value scales that a query row
+ *   meets (for its new tokens' values, 1) must lie within a factor 2^100 of one another: further
+ *   apart, its sum of weights loses the terms of the smaller ones. kv_append writes such a cache (with
  *   powers of two), paged_decode_attn, paged_decode_attn_noalloc and extend_attn read it
  *   (head_dim 128, block_size 16); the other calls return PKV_ERR_UNSUPPORTED. kv_block_pack
  *   and kv_block_unpack move its codes when it is described as PKV_KV_FP8_E4M3; the scales of

@@ -987,6 +987,51 @@ def test_extend_of_many_requests_and_neighbours_that_are_not_finite():
     check_extend(st, out, lse, SCALE, reqs=[r for r in range(n) if r != 7])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["decode", "few", "many", "pieces"])
+def test_value_scales_a_factor_2_to_the_100_apart(what):
+    """Blocks of zeros at the smallest scale that kv_append writes beside blocks 2^100 larger: every block counts in the
+    sum of weights."""
+    ctx = [700, 130, 33] if what != "pieces" else [5000, 130, 33]
+    new = {"few": [3, 4, 2], "many": [9, 140, 33], "pieces": [4, 2, 1]}.get(what)
+    st = decode_state(ctx, 16, 2, seed=29) if what == "decode" else extend_state(ctx, new, 16, 2, seed=29)
+    g = gen(4)
+    zero = torch.rand(st["vs"].shape, generator=g) < 0.5
+    st["vc"] = torch.where(zero[:, None, :, None] & (st["vc"] != 0x7F), torch.zeros((), dtype=torch.uint8), st["vc"])
+    if what == "decode":
+        st["vs"] = torch.where(zero, torch.tensor(2.0 ** -64), torch.tensor(2.0 ** 36))
+        check_decode(st, *gpu_decode(st), SCALE)
+    else:  # (the new tokens' values are 1 times themselves: 2^50 of the smallest and of the largest scale)
+        st["vs"] = torch.where(zero, torch.tensor(2.0 ** -50), torch.tensor(2.0 ** 50))
+        check_extend(st, *gpu_extend(st), SCALE)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("most,G", [(4, 8), (90, 4)])
+def test_extend_request_sets(most, G):
+    """The extend part of a reordered batch, its requests in any order; rows outside it are left as they were, also with
+    a set bound far above the set's size."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    ctx, new = [300, 20, 1, 1500, 77, 0, 900], [most, 1, 2, most - 1, 3, most, 1]
+    st = extend_state(ctx, new, 2 * G, 2, seed=31 + G, gap=1)
+    kc, vc = pools(st)
+    total = torch.tensor([c + n for c, n in zip(ctx, new)], dtype=torch.int32)
+    order = torch.tensor([1, 6, 5, 0, 3, 2, 4], dtype=torch.int32).cuda()
+    bounds = torch.tensor([0, 2, 5, 7], dtype=torch.int32).cuda()
+    q, k, v, cu, table, ks, vs = (on(st[n]) for n in ("q", "k_new", "v_new", "cu", "table", "ks", "vs"))
+    for bound in (7, 3, 5000):
+        for cls, reqs in enumerate(([1, 6], [5, 0, 3], [2, 4])):
+            if bound < len(reqs):
+                continue
+            out, lse = torch.full_like(q, 5.0), torch.full(q.shape[:2], 5.0, device="cuda")
+            pkv.extend_attn(q, k, v, cu, on(total), kc, vc, table, most, int(total.max()), out=out, lse=lse, k_scale=ks, v_scale=vs,
+                            reqs=pkv.Reqs(bound, 7, order, bounds, cls))
+            assert pkv.device_errors() == 0
+            check_extend(st, out, lse, SCALE, reqs=reqs)
+            rest = torch.cat([torch.arange(int(st["cu"][r]), int(st["cu"][r + 1])) for r in range(7) if r not in reqs]).cuda()
+            assert bool((out[rest] == 5).all()) and bool((lse[rest] == 5).all())
+
+
 def check_rows_that_are_no_numbers(st, out, lse):
     """out and lse are NaN where the definition in 64 bits says so, and within their bounds elsewhere."""
     Hkv = st["ks"].shape[1]
