@@ -368,7 +368,8 @@ pkv_status pkv_mla_decode_attn(const void* q, pkv_cache cache, const int32_t* bl
  * applied in the attention (keys with the softmax scale, values on the output). The workspace
  * is rewritten by every such call.
  * For a block-scaled cache (PKV_KV_FP8_E4M3_BLOCK) the queries and new keys must lie within the
- * fp16 range; new values may have any size. A request with more than max_q_len new tokens flags
+ * fp16 range (one beyond it, infinite ones too, makes the out and lse of the rows that attend to it NaN;
+ * of one below 2^-14 what is smaller than 2^-25 is lost); new values may have any size. A request with more than max_q_len new tokens flags
  * PKV_DEVERR_LEN and is cut to its first max_q_len. workspace: NULL, or at least
  * pkv_extend_block_workspace_size(max_q_len, max_seq_len, num_q_heads, num_kv_heads) bytes (else
  * PKV_ERR_WORKSPACE), rewritten by the call: with it, contexts are cut where that spreads the

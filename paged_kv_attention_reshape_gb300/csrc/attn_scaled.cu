@@ -16,8 +16,8 @@
 // converter warps, the first form, put 2^-8 of each product into the exponent and of each value into
 // the sum, and its conversions, 9 instructions for a pair of codes against 2, took 2.5 times as long:
 // 5.7 ms against 2.3 on 8 x 512 tokens over contexts of 4K to 32K, Hq 64 / Hkv 8.)
-// Queries and new keys become fp16 and must lie within its range; new values and their P stay bf16,
-// so values of any size pass. A score that is no number makes l one and so the row's out and lse: the max of u
+// Queries and new keys become fp16 and must lie within its range (one that does not makes its scores no numbers);
+// new values and their P stay bf16, so values of any size pass. A score that is no number makes l one and so the row's out and lse: the max of u
 // passes over it, so a part of the keys (a slot's, a copy's, a piece's) is one without keys for a row where its l
 // is 0, whatever its m. A row has a key at least, its own, so that its l is never 0 as a whole.
 //
@@ -293,6 +293,13 @@ __device__ __forceinline__ void as_conv_codes(uint32_t tile, int R, bool keep) {
     st_shared_v4(base + (((2 * (q & 3) + 1) ^ (R & 7)) << 4), b);
   }
 }
+// A pair of bf16 in fp16. What is beyond fp16 becomes no number, y + 0 y: as an infinity it could make a score -inf and
+// its key vanish from the row unseen.
+__device__ __forceinline__ uint32_t as_f16x2(uint32_t v) {
+  uint32_t y = bf16x2_to_f16x2(v);
+  asm("{\n\t.reg .b32 z;\n\tmov.b32 z, 0;\n\tfma.rn.f16x2 %0, %0, z, %0;\n\t}" : "+r"(y));
+  return y;
+}
 // bf16 row R of a tile -> fp16 in place.
 __device__ __forceinline__ void as_conv_bf16(uint32_t tile, int R) {
 #pragma unroll
@@ -301,7 +308,7 @@ __device__ __forceinline__ void as_conv_bf16(uint32_t tile, int R) {
     for (int q = 0; q < 8; ++q) {
       const uint32_t a = tile + h * 16384u + R * 128 + ((q ^ (R & 7)) << 4);  // 8 rows: 8 different bank groups
       const uint4 v = ld_shared_v4(a);
-      st_shared_v4(a, make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w)));
+      st_shared_v4(a, make_uint4(as_f16x2(v.x), as_f16x2(v.y), as_f16x2(v.z), as_f16x2(v.w)));
     }
 }
 // The same, and again every `span` rows below.
@@ -312,7 +319,7 @@ __device__ __forceinline__ void as_conv_copies(uint32_t tile, int R, int span) {
     for (int q = 0; q < 8; ++q) {
       const uint32_t a = tile + h * 16384u + R * 128 + ((q ^ (R & 7)) << 4);
       const uint4 v = ld_shared_v4(a);
-      const uint4 f = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+      const uint4 f = make_uint4(as_f16x2(v.x), as_f16x2(v.y), as_f16x2(v.z), as_f16x2(v.w));
       for (int r = 0; r < 128 - R; r += span) st_shared_v4(a + r * 128, f);
     }
 }
@@ -977,7 +984,6 @@ __global__ void __launch_bounds__(AsCfg<FEW>::THREADS, 1)
       const AsPartials part = as_partials(ws, ws_slots, C::ROWS);
       const float wr = ex2_approx(m - mm) / (whole ? ll : 1.f);
       w0 *= wr, w1 *= wr;
-      if (whole && ll == 0.f) has0 = true;  // every score is -inf: no number
       tc::fence_after_sync();
       const int rows = min(it.q_len, static_cast<int>(min(static_cast<int64_t>(it.q_len), p.num_tokens - it.row0))) * p.G;
       const uint32_t stg = smem_u32(smem) + C::STAGE_OFF;  // [128 rows][32 fp32], 128-byte swizzle

@@ -1032,7 +1032,7 @@ def test_extend_request_sets(most, G):
             assert bool((out[rest] == 5).all()) and bool((lse[rest] == 5).all())
 
 
-def check_rows_that_are_no_numbers(st, out, lse):
+def check_rows_that_are_no_numbers(st, out, lse, infinite=False):
     """out and lse are NaN where the definition in 64 bits says so, and within their bounds elsewhere."""
     Hkv = st["ks"].shape[1]
     G = st["q"].shape[1] // Hkv
@@ -1046,8 +1046,10 @@ def check_rows_that_are_no_numbers(st, out, lse):
             q = st["q"][rows, hq].double()
             o, z, A, M = dense(q, k, v, SCALE, c)
             a, b = out[rows, hq].double(), lse[rows, hq].double()
+            if infinite:
+                z = torch.where(q.isinf().any(-1), math.nan, z)
             assert torch.equal(o.isnan(), a.isnan()), f"request {r} head {h}"
-            assert torch.equal(z.isnan(), b.isnan()) and torch.equal(z.isinf(), b.isinf()), f"request {r} head {h}"
+            assert torch.equal(z.isnan(), b.isnan()) and not bool(b.isinf().any()), f"request {r} head {h}"
             e = 2.0 ** -16 * M + 2.0 ** -20 * (1 + z.abs())
             fixed = fixed_steps(st, r, h, c, q, k, SCALE, c, 2.0 ** -32)
             assert bool(((b - z).abs() <= e)[z.isfinite()].all()), f"request {r} head {h}"
@@ -1062,7 +1064,7 @@ def check_rows_that_are_no_numbers(st, out, lse):
     ([130, 20], [200, 9], 4, 2), ([700, 33], [40, 100], 2, 1), ([4000, 3000, 5], [200, 90, 1], 4, 2)])
 def test_extend_of_what_is_no_number(ctx, new, G, Hkv, what):
     """A NaN in a query, in a cached key or value, in a new key: NaN in the rows (or dims) that attend to it, in out and
-    lse, whatever the launch and the plan; the other rows as they are. Scores that are all -inf: NaN, and lse -inf."""
+    lse, whatever the launch and the plan; the other rows as they are. An infinite query counts as NaN."""
     st = extend_state(ctx, new, G * Hkv, Hkv, seed=90 + G, qs=1.0)
     if what == "q":
         st["q"][1, 0, 77] = math.nan
@@ -1075,12 +1077,47 @@ def test_extend_of_what_is_no_number(ctx, new, G, Hkv, what):
         st["q"][0] = math.nan
         for r in range(len(ctx)):
             st["kc"][st["table"][r, :(ctx[r] + 15) // 16].long()] = 0xFF
-    else:  # a token without context, its one score -inf
+    else:  # a token without context, its one score -inf in 64 bits: no weights
         st["ctx"] = [ctx[0], 0] + ctx[2:]
         t = int(st["cu"][1])
         st["q"][t, 0], st["k_new"][t, 0] = 0.5, 0.5
         st["q"][t, 0, 3], st["k_new"][t, 0, 3] = math.inf, -1.0
-    check_rows_that_are_no_numbers(st, *gpu_extend(st))
+    check_rows_that_are_no_numbers(st, *gpu_extend(st), infinite=what == "below")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["q", "new_k"])
+@pytest.mark.parametrize("ctx,new,G,Hkv", [([300, 40], [4, 3], 8, 2), ([130, 20], [200, 9], 4, 2), ([9001, 20], [4, 3], 8, 1)])
+def test_extend_of_numbers_beyond_fp16(ctx, new, G, Hkv, what):
+    """A query or new key that fp16 does not hold is seen in the rows that attend to it, also where its score is far
+    below the others'; the largest that it holds are multiplied as they are."""
+    st = extend_state(ctx, new, G * Hkv, Hkv, seed=95 + G)
+    t = int(st["cu"][1]) + 1
+    st["q"][0, 0, 3] = 65280.0
+    st["ks"], st["k_new"] = st["ks"] * 2.0 ** -10, (st["k_new"].float() * 2.0 ** -10).to(torch.bfloat16)
+    if what == "q":
+        st["q"][t, 0, 9] = -70000.0
+        rows = slice(t, t + 1)
+    else:
+        st["k_new"][t, 0, 9] = -70000.0
+        st["q"][:, :, 9] = st["q"][:, :, 9].abs() + 0.01
+        rows = slice(t, int(st["cu"][2]))
+    out, lse = gpu_extend(st)
+    heads = slice(0, 1) if what == "q" else slice(0, G)
+    assert bool(out[rows, heads].isnan().all()) and bool(lse[rows, heads].isnan().all())
+    for r in range(2):
+        for h in range(Hkv):
+            at, hq = slice(int(st["cu"][r]), int(st["cu"][r + 1])), slice(h * G, (h + 1) * G)
+            k, v = context(st, r, h, ctx[r])
+            k, v = torch.cat([k, st["k_new"][at, h].double()]), torch.cat([v, st["v_new"][at, h].double()])
+            q = st["q"][at, hq].double()
+            o, z, A, M = dense(q, k, v, SCALE, ctx[r])
+            a, b = out.cpu()[at, hq].double(), lse.cpu()[at, hq].double()
+            fine = ~b.isnan()
+            assert int((~fine).sum()) == (0 if h or not r else 1 if what == "q" else G * (rows.stop - rows.start))
+            e = 2.0 ** -16 * M + 2.0 ** -20 * (1 + z.abs())
+            tol = U * o.abs() + (U + 2 * e[..., None]) * A + fixed_steps(st, r, h, ctx[r], q, k, SCALE, ctx[r], 2.0 ** -32) + 1e-37
+            assert bool(((b - z).abs() <= e)[fine].all()) and bool(((a - o).abs() <= tol)[fine].all()), f"request {r} head {h}"
 
 
 @pytest.mark.gpu
