@@ -97,6 +97,11 @@ def _need(t: torch.Tensor, dtype, name: str, contiguous: bool = True):
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
 
 
+def _is_number(scale, shape) -> bool:
+    """Whether a scale is one for the whole tensor: a number, or a tensor of one element that is not a table."""
+    return not isinstance(scale, torch.Tensor) or (scale.numel() == 1 and scale.shape != shape)
+
+
 def _block_scales(k_scale, v_scale, nb: int, hkv: int, device_index: int):
     """Checks scale tensors [num_blocks, Hkv]; returns their addresses."""
     want = (nb, hkv)
@@ -120,8 +125,8 @@ def make_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale=1.0, v_scal
     """Describe one layer's paged cache: k_cache / v_cache [num_blocks, block_size, Hkv, D]
     with contiguous blocks (any stride between blocks). bf16 tensors are a bf16 cache; uint8
     or float8_e4m3fn tensors are an FP8 (E4M3) cache whose codes stand for e4m3(code) * scale.
-    k_scale and v_scale are numbers (one scale for the tensor) or fp32 tensors [num_blocks, Hkv]
-    (a scale for each block and KV head)."""
+    k_scale and v_scale are numbers (one scale for the tensor; a tensor of one element counts as one, and is
+    read on the host) or fp32 tensors [num_blocks, Hkv] (a scale for each block and KV head)."""
     dtype = k_cache.dtype
     fp8 = dtype in _FP8
     shape = k_cache.shape
@@ -137,7 +142,7 @@ def make_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale=1.0, v_scal
                 raise PkvError(f"{n}: each block must be contiguous [block_size, Hkv, D]")
         if k_cache.shape != v_cache.shape or stride != v_cache.stride(0):
             raise PkvError("k_cache and v_cache must have the same shape and block stride")
-    if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
+    if not (_is_number(k_scale, (nb, hkv)) and _is_number(v_scale, (nb, hkv))):
         if not fp8:
             raise PkvError("block scales belong to an FP8 cache")
         ks, vs = _block_scales(k_scale, v_scale, nb, hkv, k_cache.get_device())
