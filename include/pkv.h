@@ -296,8 +296,9 @@ pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* 
  * up again. Make that first call before any stream capture. A call whose scratch need, pkv_paged_decode_workspace_size(...) with the same
  * arguments, exceeds PKV_NOALLOC_SCRATCH_BYTES returns PKV_ERR_WORKSPACE and enqueues
  * nothing. All calls on a device share the one array and it keeps the last call's contents;
- * nothing in it has to start at zero (each call writes every partial it later reads and tags
- * its arrival counters with a value of its own that no leftover partial or counter matches), but
+ * nothing in it has to start at zero (each call writes every partial it later reads, tags
+ * its arrival counters with a value of its own that no leftover partial or counter matches, and
+ * leaves them at zero for the replays of a captured call), but
  * calls that overlap on the GPU (other streams, other host threads) race on it: serialise
  * them.
  * ------------------------------------------------------------------------------------- */
