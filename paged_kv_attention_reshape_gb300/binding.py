@@ -305,9 +305,9 @@ class LayerHandoff:
         n = block_ids.numel()
         if dst is None:
             # allocated on the copy stream's behalf: the caching allocator must not hand it to
-            # other work before the pack that writes it is done
-            with torch.cuda.stream(self.copy_stream):
-                dst = torch.empty((2, n) + tuple(k_cache.shape[1:]), dtype=k_cache.dtype, device=k_cache.device)
+            # other work before the pack that writes it is done, nor to a later pack before the
+            # current stream has read it
+            dst = _empty((2, n) + tuple(k_cache.shape[1:]), k_cache.dtype, k_cache.device, self.copy_stream)
         _need(dst, k_cache.dtype, "dst")
         _check(lib.pkv_handoff_stage(self._h, int(slot), cache, _ptr(block_ids), n, _ptr(dst), _stream(compute_stream)),
                "handoff_stage")

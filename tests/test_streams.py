@@ -97,6 +97,28 @@ def test_a_call_on_another_stream_shares_no_memory_with_the_current_one(name, ha
     assert pkv.device_errors() == 0
 
 
+def test_a_staged_layer_is_kept_until_the_current_stream_has_read_it():
+    """LayerHandoff.stage without a buffer: what it allocates goes to no later pack while the current stream reads it."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    kc, vc = (torch.randn((64, 16, 2, 128)).to(torch.bfloat16).cuda() for _ in "kv")
+    ids = torch.randperm(64)[:40].to(torch.int32).cuda()
+    want = torch.stack([kc[ids.long()], vc[ids.long()]])
+    handoff = pkv.LayerHandoff(2)
+    torch.cuda.synchronize()
+    dst = handoff.stage(0, kc, vc, ids)
+    handoff.ready(0)
+    n = dst.numel() * dst.element_size()
+    torch.cuda._sleep(200_000_000)
+    copy = dst.clone()
+    del dst
+    with torch.cuda.stream(handoff.copy_stream):
+        more = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x7F) for _ in range(6)]
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
+    del more
+    handoff.close()
+
+
 def test_the_current_stream_by_name_and_the_default_stream():
     """The current stream given explicitly, and the default stream while another one is current."""
     import paged_kv_attention_reshape_gb300 as pkv
