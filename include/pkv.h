@@ -407,6 +407,38 @@ pkv_status pkv_varlen_prefill_attn(const void* q, const void* k, const void* v, 
                                    float scale, void* out, float* lse, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Windowed attention with sinks — decode, extend and prefill over a part of the keys.
+ * The pages have no counterpart; models whose layers look back a bounded distance take these
+ * calls in the places of paged_decode_attn, extend_attn and varlen_prefill_attn. The row at
+ * position i (decode: seq_lens[r] - 1; extend: C + i; prefill: i) sees the keys at positions
+ *   j <= i with j > i - window, or with j < sinks
+ * (window >= 1: the row's own key counts; sinks >= 0 first keys stay visible however far the row
+ * is; else PKV_ERR_INVALID_ARG). out and lse are the softmax over those keys. Everything else is
+ * as in the call without a window, with these differences:
+ *   - only blocks with a key that some row sees are read: table entries of other blocks may
+ *     hold anything (pages that slid out of the window may have been given back);
+ *   - caches: bf16, or PKV_KV_FP8_E4M3 at head_dim 128; others return PKV_ERR_UNSUPPORTED;
+ *   - a value that is not finite in a key that some row sees may reach the rows of the same
+ *     request and KV head that do not see it, for extend and prefill. Keys that no row sees
+ *     touch nothing, whatever they hold.
+ * The decode takes the workspace of paged_decode_attn; extend and prefill need none.
+ * ------------------------------------------------------------------------------------- */
+pkv_status pkv_window_decode_attn(const void* q, pkv_cache cache, const int32_t* block_tables,
+                                  int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_q,
+                                  pkv_reqs reqs, int32_t num_q_heads, int32_t max_seq_len, int32_t window,
+                                  int32_t sinks, float scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, pkv_stream_t stream);
+pkv_status pkv_window_extend_attn(const void* q, const void* k_new, const void* v_new, int64_t num_tokens,
+                                  const int32_t* cu_q, const int32_t* seq_lens, pkv_cache cache,
+                                  const int32_t* block_tables, int32_t max_blocks, pkv_reqs reqs,
+                                  int32_t num_q_heads, int32_t max_q_len, int32_t max_seq_len, int32_t window,
+                                  int32_t sinks, float scale, void* out, float* lse, pkv_stream_t stream);
+pkv_status pkv_window_prefill_attn(const void* q, const void* k, const void* v, int64_t num_tokens,
+                                   const int32_t* cu_seqlens, pkv_reqs reqs, int32_t num_q_heads,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t max_seqlen, int32_t window,
+                                   int32_t sinks, float scale, void* out, float* lse, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * kv_block_pack — gather one layer's KV blocks by id into a contiguous staging buffer.
  * Source: vLLM blog "moriio-kv-connector", sections "Write mode" (the prefill instance pushes
  * each layer's KV as soon as the layer is computed) and "Read mode vs write mode" (the

@@ -55,6 +55,9 @@ SIGNATURES = [
     ("pkv_extend_attn", i32, [P, P, P, i64, P, P, PkvCache, P, i32, PkvReqs, i32, i32, i32, i32, f32,
                               P, P, P, sz, P]),
     ("pkv_varlen_prefill_attn", i32, [P, P, P, i64, P, PkvReqs, i32, i32, i32, i32, f32, P, P, P]),
+    ("pkv_window_decode_attn", i32, [P, PkvCache, P, i32, P, P, PkvReqs, i32, i32, i32, i32, f32, P, P, P, sz, P]),
+    ("pkv_window_extend_attn", i32, [P, P, P, i64, P, P, PkvCache, P, i32, PkvReqs, i32, i32, i32, i32, i32, f32, P, P, P]),
+    ("pkv_window_prefill_attn", i32, [P, P, P, i64, P, PkvReqs, i32, i32, i32, i32, i32, i32, f32, P, P, P]),
     ("pkv_kv_block_pack", i32, [PkvCache, P, i32, P, P]),
     ("pkv_kv_block_unpack", i32, [P, P, i32, PkvCache, P]),
     ("pkv_handoff_create", i32, [i32, P, P]),

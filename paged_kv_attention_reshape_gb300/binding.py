@@ -368,12 +368,25 @@ def paged_decode_workspace_size(max_reqs, Hq, Hkv, D, max_seq_len) -> int:
     return int(_lib.load().pkv_paged_decode_workspace_size(max_reqs, Hq, Hkv, D, max_seq_len))
 
 
+def _window(window, sinks):
+    """The (window, sinks) of a windowed call as integers, or None for a call without a window."""
+    if window is None:
+        if sinks:
+            raise PkvError("sinks belong to a window")
+        return None
+    return min(int(window), 2**31 - 1), min(int(sinks), 2**31 - 1)
+
+
 def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, cu_q=None,
                       reqs: Optional[Reqs] = None, scale=None, out=None, lse=None, workspace=None,
-                      stream=None, k_scale=1.0, v_scale=1.0):
+                      stream=None, k_scale=1.0, v_scale=1.0, window=None, sinks=0):
     """One query token per request against its paged context. q [T, Hq, D]. An FP8 cache is
     dequantised as it is read, with the per-tensor scales or with the scale of each block and KV
-    head (k_scale, v_scale: fp32 tensors [num_blocks, Hkv])."""
+    head (k_scale, v_scale: fp32 tensors [num_blocks, Hkv]).
+
+    With a window the token sees the last `window` keys, its own among them, and the first `sinks`
+    keys (a bf16 cache, or an FP8 one with per-tensor scales); table entries of the blocks between
+    them are not read."""
     lib = _lib.load()
     _need(q, torch.bfloat16, "q")
     _need(block_tables, torch.int32, "block_tables")
@@ -388,7 +401,14 @@ def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, 
     if lse is None:
         lse = _empty((T, Hq), torch.float32, q.device, other)
     need = lib.pkv_paged_decode_workspace_size(reqs.max_reqs, Hq, cache.num_kv_heads, D, max_seq_len)
+    win = _window(window, sinks)
     workspace = _scratch(need, workspace, q.device, other)
+    if win is not None:
+        _check(lib.pkv_window_decode_attn(_ptr(q), cache, _ptr(block_tables), block_tables.shape[1],
+                                          _ptr(seq_lens), _ptr(cu_q), reqs.c(), Hq, max_seq_len, *win,
+                                          _scale(scale, D), _ptr(out), _ptr(lse), _ptr(workspace),
+                                          need, _stream(stream)), "paged_decode_attn")
+        return out, lse
     _check(lib.pkv_paged_decode_attn(_ptr(q), cache, _ptr(block_tables), block_tables.shape[1],
                                      _ptr(seq_lens), _ptr(cu_q), reqs.c(), Hq, max_seq_len,
                                      _scale(scale, D), _ptr(out), _ptr(lse), _ptr(workspace),
@@ -450,13 +470,17 @@ def mla_decode_workspace_size(max_reqs, num_q_heads, max_seq_len) -> int:
 
 def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables, max_q_len,
                 max_seq_len, reqs: Optional[Reqs] = None, chunk_budget_tokens=32768, scale=None,
-                out=None, lse=None, stream=None, k_scale=1.0, v_scale=1.0, workspace=None):
+                out=None, lse=None, stream=None, k_scale=1.0, v_scale=1.0, workspace=None, window=None, sinks=0):
     """New tokens attend to their cached context (paged) and causally to themselves. An FP8
     cache (uint8 / float8 codes with per-tensor scales) is read as codes and converted in the
     kernel at head_dim 128; at head_dim 64 it is gathered into a bf16 workspace of the set's
     context first (allocated here when not given). k_scale / v_scale may be fp32 tensors
     [num_blocks, Hkv], a scale for each block and KV head (head_dim 128); the workspace then holds the
-    partial results of contexts that are cut (allocated here when not given)."""
+    partial results of contexts that are cut (allocated here when not given).
+
+    With a window each row sees the last `window` keys up to its own and the first `sinks` keys (a
+    bf16 cache, or an FP8 one with per-tensor scales at head_dim 128; no workspace); table entries of
+    blocks that no row sees are not read."""
     lib = _lib.load()
     for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
         _need(t, torch.bfloat16, n)
@@ -472,6 +496,13 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
         out = _empty(q.shape, q.dtype, q.device, other)
     if lse is None:
         lse = _empty((T, Hq), torch.float32, q.device, other)
+    win = _window(window, sinks)
+    if win is not None:
+        _check(lib.pkv_window_extend_attn(_ptr(q), _ptr(k_new), _ptr(v_new), T, _ptr(cu_q), _ptr(seq_lens), cache,
+                                          _ptr(block_tables), block_tables.shape[1], reqs.c(), Hq, max_q_len,
+                                          max_seq_len, *win, _scale(scale, D), _ptr(out), _ptr(lse),
+                                          _stream(stream)), "extend_attn")
+        return out, lse
     need = 0
     if cache.kv_dtype == _lib.KV_FP8_E4M3:
         need = extend_fp8_workspace_size(reqs.max_reqs, reqs.batch_reqs, max_seq_len, block_tables.shape[1],
@@ -496,8 +527,9 @@ def extend_fp8_workspace_size(max_reqs, batch_reqs, max_seq_len, max_blocks, num
 
 
 def varlen_prefill_attn(q, k, v, cu_seqlens, max_seqlen, reqs: Optional[Reqs] = None, scale=None,
-                        out=None, lse=None, stream=None):
-    """Causal attention over packed variable-length prompts."""
+                        out=None, lse=None, stream=None, window=None, sinks=0):
+    """Causal attention over packed variable-length prompts. With a window each row sees the last
+    `window` keys up to its own and the first `sinks` keys of its prompt."""
     lib = _lib.load()
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, torch.bfloat16, n)
@@ -511,6 +543,12 @@ def varlen_prefill_attn(q, k, v, cu_seqlens, max_seqlen, reqs: Optional[Reqs] = 
         out = _empty(q.shape, q.dtype, q.device, other)
     if lse is None:
         lse = _empty((T, Hq), torch.float32, q.device, other)
+    win = _window(window, sinks)
+    if win is not None:
+        _check(lib.pkv_window_prefill_attn(_ptr(q), _ptr(k), _ptr(v), T, _ptr(cu_seqlens), reqs.c(), Hq, Hkv, D,
+                                           max_seqlen, *win, _scale(scale, D), _ptr(out), _ptr(lse),
+                                           _stream(stream)), "varlen_prefill_attn")
+        return out, lse
     _check(lib.pkv_varlen_prefill_attn(_ptr(q), _ptr(k), _ptr(v), T, _ptr(cu_seqlens), reqs.c(), Hq,
                                        Hkv, D, max_seqlen, _scale(scale, D), _ptr(out), _ptr(lse),
                                        _stream(stream)), "varlen_prefill_attn")

@@ -228,6 +228,9 @@ int max_smem_optin() {
 // The softmax scale: positive and finite (each row's max is taken over the raw scores).
 static bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.f; }
 
+// A window holds at least the row's own key; any number of first keys may stay visible.
+static bool window_ok(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
+
 cudaError_t set_smem_attr_once(const void* func, int bytes, int slot) {
   static std::mutex mu;
   static bool done[kAttrCount][kMaxDevices] = {};
@@ -549,12 +552,12 @@ size_t pkv_paged_decode_workspace_size(int32_t max_reqs, int32_t num_q_heads, in
   return decode_workspace_bytes(num_q_heads, num_kv_heads, head_dim);
 }
 
-pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* block_tables,
-                                 int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_q,
-                                 pkv_reqs reqs, int32_t num_q_heads, int32_t max_seq_len,
-                                 float scale, void* out, float* lse, void* workspace,
-                                 size_t workspace_bytes, pkv_stream_t stream) {
-  pkv_status st = check_cache(cache, true, true);
+// paged_decode_attn and, with a window (window > 0), window_decode_attn.
+static pkv_status run_decode(const void* q, pkv_cache cache, const int32_t* block_tables, int32_t max_blocks,
+                             const int32_t* seq_lens, const int32_t* cu_q, pkv_reqs reqs, int32_t num_q_heads,
+                             int32_t max_seq_len, int32_t window, int32_t sinks, float scale, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  pkv_status st = check_cache(cache, true, window == 0);
   if (st != PKV_OK) return st;
   if ((st = check_reqs(reqs)) != PKV_OK) return st;
   if (!group_ok(num_q_heads, cache.num_kv_heads)) return PKV_ERR_UNSUPPORTED;
@@ -585,6 +588,8 @@ pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* 
   p.out_dim = cache.head_dim;
   p.num_blocks = cache.num_blocks;
   p.max_seq_len = max_seq_len;
+  p.window = window;
+  p.sinks = sinks;
   const bool fp8 = cache.kv_dtype == PKV_KV_FP8_E4M3;
   // an FP8 cache holds codes: the key scale folds into the softmax scale, the value scale
   // into the output
@@ -608,12 +613,32 @@ pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* 
   for (int32_t off = 0; off < reqs.max_reqs && st == PKV_OK; off += kSetChunk) {
     p.set_offset = off;
     p.epoch = next_epoch();
-    st = cuda_status(scaled ? launch_decode_scaled(p, tk, tv, reinterpret_cast<cudaStream_t>(stream), &launches)
-                            : launch_paged_decode(p, tk, tv, cache.head_dim, fp8, reinterpret_cast<cudaStream_t>(stream),
-                                                  &launches));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    st = cuda_status(scaled       ? launch_decode_scaled(p, tk, tv, s, &launches)
+                     : window > 0 ? launch_window_decode(p, tk, tv, cache.head_dim, fp8, s, &launches)
+                                  : launch_paged_decode(p, tk, tv, cache.head_dim, fp8, s, &launches));
   }
   t_launches += launches;
   return st;
+}
+
+pkv_status pkv_paged_decode_attn(const void* q, pkv_cache cache, const int32_t* block_tables,
+                                 int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_q,
+                                 pkv_reqs reqs, int32_t num_q_heads, int32_t max_seq_len,
+                                 float scale, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, pkv_stream_t stream) {
+  return run_decode(q, cache, block_tables, max_blocks, seq_lens, cu_q, reqs, num_q_heads, max_seq_len, 0, 0, scale,
+                    out, lse, workspace, workspace_bytes, stream);
+}
+
+pkv_status pkv_window_decode_attn(const void* q, pkv_cache cache, const int32_t* block_tables,
+                                  int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_q,
+                                  pkv_reqs reqs, int32_t num_q_heads, int32_t max_seq_len, int32_t window,
+                                  int32_t sinks, float scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, pkv_stream_t stream) {
+  if (!window_ok(window, sinks)) return PKV_ERR_INVALID_ARG;
+  return run_decode(q, cache, block_tables, max_blocks, seq_lens, cu_q, reqs, num_q_heads, max_seq_len, window, sinks,
+                    scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 size_t pkv_mla_decode_workspace_size(int32_t max_reqs, int32_t num_q_heads, int32_t max_seq_len) {
@@ -700,7 +725,8 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
                                 int32_t max_blocks, pkv_reqs reqs, int32_t Hq, int32_t Hkv,
                                 int32_t D, int32_t max_q_len, int32_t max_seq_len, float scale,
                                 void* out, float* lse, pkv_stream_t stream, int ctx_kind = kAttnCtxBf16,
-                                float ctx_k_scale = 1.f, float ctx_v_scale = 1.f, void* workspace = nullptr) {
+                                float ctx_k_scale = 1.f, float ctx_v_scale = 1.f, void* workspace = nullptr,
+                                int32_t window = 0, int32_t sinks = 0) {
   pkv_status st = check_reqs(reqs);
   if (st != PKV_OK) return st;
   if (cache != nullptr && (st = check_cache(*cache, true, true)) != PKV_OK) return st;
@@ -743,6 +769,8 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   p.scale_log2 = scale * 1.4426950408889634f;
   p.ctx_scale_log2 = scale * ctx_k_scale * 1.4426950408889634f;
   p.ctx_v_scale = ctx_v_scale;
+  p.window = window;
+  p.sinks = sinks;
   p.k_scales = cache ? cache->k_scales : nullptr;
   p.v_scales = cache ? cache->v_scales : nullptr;
   CUtensorMap tq, tk, tv, tck, tcv, tqf;
@@ -892,6 +920,30 @@ pkv_status pkv_varlen_prefill_attn(const void* q, const void* k, const void* v, 
   return run_attention(q, k, v, num_tokens, cu_seqlens, nullptr, nullptr, nullptr, 0, reqs,
                        num_q_heads, num_kv_heads, head_dim, max_seqlen, max_seqlen, scale, out,
                        lse, stream);
+}
+
+pkv_status pkv_window_extend_attn(const void* q, const void* k_new, const void* v_new, int64_t num_tokens,
+                                  const int32_t* cu_q, const int32_t* seq_lens, pkv_cache cache,
+                                  const int32_t* block_tables, int32_t max_blocks, pkv_reqs reqs,
+                                  int32_t num_q_heads, int32_t max_q_len, int32_t max_seq_len, int32_t window,
+                                  int32_t sinks, float scale, void* out, float* lse, pkv_stream_t stream) {
+  if (!window_ok(window, sinks)) return PKV_ERR_INVALID_ARG;
+  const bool fp8 = cache.kv_dtype == PKV_KV_FP8_E4M3;
+  if (cache.kv_dtype == PKV_KV_FP8_E4M3_BLOCK) return PKV_ERR_UNSUPPORTED;
+  return run_attention(q, k_new, v_new, num_tokens, cu_q, seq_lens, &cache, block_tables, max_blocks, reqs, num_q_heads,
+                       cache.num_kv_heads, cache.head_dim, max_q_len, max_seq_len, scale, out, lse, stream,
+                       fp8 ? kAttnCtxFp8 : kAttnCtxBf16, fp8 ? cache.k_scale : 1.f, fp8 ? cache.v_scale : 1.f, nullptr,
+                       window, sinks);
+}
+
+pkv_status pkv_window_prefill_attn(const void* q, const void* k, const void* v, int64_t num_tokens,
+                                   const int32_t* cu_seqlens, pkv_reqs reqs, int32_t num_q_heads,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t max_seqlen, int32_t window,
+                                   int32_t sinks, float scale, void* out, float* lse, pkv_stream_t stream) {
+  if (!window_ok(window, sinks)) return PKV_ERR_INVALID_ARG;
+  return run_attention(q, k, v, num_tokens, cu_seqlens, nullptr, nullptr, nullptr, 0, reqs, num_q_heads, num_kv_heads,
+                       head_dim, max_seqlen, max_seqlen, scale, out, lse, stream, kAttnCtxBf16, 1.f, 1.f, nullptr, window,
+                       sinks);
 }
 
 }  // extern "C"

@@ -66,7 +66,23 @@ struct DecodeCfg {
   static constexpr int smem(int nw) { return 1024 + TAB_BYTES + nw * WARP_BYTES + nw * NSW * 8; }
 };
 
-template <int D, bool FP8>
+// Where a piece's block-table entries lie: entry v of the piece (see Seen for the numbering of WIN).
+template <bool WIN>
+struct TableRow {
+  const int32_t* row = nullptr;
+  __device__ int operator[](int v) const { return row[v]; }
+};
+template <>
+struct TableRow<true> {
+  const int32_t* row = nullptr;
+  int head = 0, gap = 0;
+  __device__ int operator[](int v) const { return row[v < head ? v : v + gap]; }
+};
+
+// WIN: a windowed decode. Of every sequence only the blocks with keys that its last token sees are
+// streamed (Seen): they are the units of the shares, so the work is the window's and not the
+// context's, and a table entry between the sinks and the window is never read.
+template <int D, bool FP8, bool WIN>
 __global__ void __launch_bounds__(DecodeCfg<D, FP8>::MAXW * 32) __maxnreg__((DecodeCfg<D, FP8>::MAXREG)) paged_decode_kernel(
     const DecodeParams p, const __grid_constant__ CUtensorMap tm_k,
     const __grid_constant__ CUtensorMap tm_v) {
@@ -94,8 +110,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8>::MAXW * 32) __maxnreg__((Dec
   }
   static_assert(C::MAXR >= kSetChunk, "a launch holds a whole chunk of the set");
   const int cap = min(p.max_seq_len, p.max_blocks * C::BS);
-  const int carry = static_cast<int>(scan_set<C::BS>(p.order, p.seq_lens, p.cu_q, begin, n, p.batch_reqs, cap,
-                                                     p.err, s_pre, s_ctx, s_r, s_row, s_scan));
+  const int carry = static_cast<int>(scan_set<C::BS, WIN>(p.order, p.seq_lens, p.cu_q, begin, n, p.batch_reqs, cap,
+                                                          p.err, s_pre, s_ctx, s_r, s_row, s_scan, p.window,
+                                                          p.sinks));
   const int64_t TB = carry;
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     // sequences with no context: out = 0, lse = -inf (no share covers them)
@@ -160,10 +177,16 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8>::MAXW * 32) __maxnreg__((Dec
   int lbatch = 0, lnext = 0;  // this lane's table entries: block lpc.lo + lbase + lane (and +32)
   int lfirst = 0;             // entry `lane` of the piece after lpc, loaded one piece early
   int lbase = 0;
-  const int32_t* ltable = nullptr;
+  TableRow<WIN> ltable;
   uint32_t issued = 0;        // blocks whose loads were issued
   auto table_of = [&](const Piece& q) {
-    return p.block_tables + static_cast<int64_t>(s_r[q.i]) * p.max_blocks + q.lo;
+    const int32_t* row = p.block_tables + static_cast<int64_t>(s_r[q.i]) * p.max_blocks + q.lo;
+    if constexpr (WIN) {
+      const Seen sn(s_ctx[q.i], p.window, p.sinks);
+      return TableRow<WIN>{row, sn.head<C::BS>() - q.lo, sn.gap<C::BS>()};
+    } else {
+      return TableRow<WIN>{row};
+    }
   };
   // entry `lane` of the piece after lpc: its load is in flight while lpc streams
   auto prefetch_following = [&]() {
@@ -265,6 +288,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8>::MAXW * 32) __maxnreg__((Dec
       if (nx.next(np)) request_q(s_row[np.i]);
     }
     const int ctx = s_ctx[pc.i];
+    const Seen sn(ctx, p.window, p.sinks);  // (WIN)
+    const int head = sn.head<C::BS>(), gap = sn.gap<C::BS>();
     float m_run[2] = {-CUDART_INF_F, -CUDART_INF_F};  // rows r0 and r0 + 8 (log2 units)
     float l_run[2] = {0.f, 0.f};
     float o[D / 8][4];
@@ -278,8 +303,20 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8>::MAXW * 32) __maxnreg__((Dec
       }
       uint8_t* sK = ring + s * C::STAGE_BYTES;
       uint8_t* sV = sK + C::TILE_BYTES;
-      const int valid = min(C::BS, ctx - j * C::BS);  // tokens of this block
-      if (valid < C::BS) {
+      // tokens of this block: the first `valid`, or (WIN) those of the bits of `seen`
+      const int valid = min(C::BS, ctx - j * C::BS);
+      uint32_t seen = 0;
+      if constexpr (WIN) {
+        seen = sn.mask((j < head ? j : j + gap) * C::BS) & 0xFFFFu;
+        if (seen != 0xFFFFu) {
+          for (int c = lane; c < C::BS * C::HALVES * 8; c += 32) {
+            const int rrow = c / (C::HALVES * 8), rest = c % (C::HALVES * 8);
+            if (!((seen >> rrow) & 1u))
+              *reinterpret_cast<uint4*>(sV + (rest / 8) * 2048 + rrow * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
+        }
+      } else if (valid < C::BS) {
         // zero the V rows past the end so that P = 0 there cannot meet a non-finite value
         // (whole 128-byte rows: the swizzle only permutes chunks within a row)
         for (int c = lane; c < (C::BS - valid) * C::HALVES * 8; c += 32) {
@@ -326,7 +363,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8>::MAXW * 32) __maxnreg__((Dec
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = nt * 8 + 2 * (lane & 3) + (e & 1);
-          if (tok < valid) mx[e >> 1] = fmaxf(mx[e >> 1], sc[nt][e]);
+          if (WIN ? (seen >> tok) & 1u : tok < valid) mx[e >> 1] = fmaxf(mx[e >> 1], sc[nt][e]);
         }
       float alpha[2], neg_m[2];
 #pragma unroll
@@ -344,7 +381,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8>::MAXW * 32) __maxnreg__((Dec
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = nt * 8 + 2 * (lane & 3) + (e & 1);
-          const float pv = tok < valid ? ex2_approx(fmaf(sc[nt][e], p.scale_log2, neg_m[e >> 1])) : 0.f;
+          const float pv = (WIN ? (seen >> tok) & 1u : tok < valid)
+                               ? ex2_approx(fmaf(sc[nt][e], p.scale_log2, neg_m[e >> 1]))
+                               : 0.f;
           sc[nt][e] = pv;
           rs[e >> 1] += pv;
         }
@@ -413,7 +452,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8>::MAXW * 32) __maxnreg__((Dec
       l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 1);
       l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 2);
     }
-    const int unit_blocks = (ctx + C::BS - 1) / C::BS;
+    const int unit_blocks = WIN ? s_pre[pc.i + 1] - s_pre[pc.i] : (ctx + C::BS - 1) / C::BS;
     const bool whole = pc.lo == 0 && pc.hi == unit_blocks;
     float inv[2], lse[2];
 #pragma unroll
@@ -526,18 +565,20 @@ size_t decode_workspace_bytes(int Hq, int Hkv, int D) {
          static_cast<size_t>(merge_levels(shares)) * shares * 2 * Hkv * sizeof(unsigned long long);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool WIN>
 static cudaError_t launch_decode_impl(const DecodeParams& p, const CUtensorMap& tk,
                                       const CUtensorMap& tv, cudaStream_t stream, int* launches) {
   using C = DecodeCfg<D, FP8>;
-  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&paged_decode_kernel<D, FP8>), max_dyn_smem(),
-                                     FP8 ? kAttrDecode128Fp8 : (D == 64 ? kAttrDecode64 : kAttrDecode128));
+  constexpr int kSlot = WIN ? (FP8 ? kAttrWinDecode128Fp8 : (D == 64 ? kAttrWinDecode64 : kAttrWinDecode128))
+                            : (FP8 ? kAttrDecode128Fp8 : (D == 64 ? kAttrDecode64 : kAttrDecode128));
+  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&paged_decode_kernel<D, FP8, WIN>), max_dyn_smem(),
+                                     kSlot);
   if (e != cudaSuccess) return e;
   const DecodeShape sh = decode_shape<D, FP8>(p.Hkv);
   DecodeParams q = p;
   q.share_warps = sh.hw;
   q.launch_shares = sh.shares;
-  e = launch_pdl(paged_decode_kernel<D, FP8>, dim3(sh.ctas_x, sh.groups), dim3(sh.nw * 32), C::smem(sh.nw), stream,
+  e = launch_pdl(paged_decode_kernel<D, FP8, WIN>, dim3(sh.ctas_x, sh.groups), dim3(sh.nw * 32), C::smem(sh.nw), stream,
                  q, tk, tv);
   *launches += 1;
   return e;
@@ -549,9 +590,16 @@ int decode_smem_bytes(int D) {
 
 cudaError_t launch_paged_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                 int D, bool fp8, cudaStream_t stream, int* launches) {
-  if (fp8) return launch_decode_impl<128, true>(p, tk, tv, stream, launches);
-  return D == 64 ? launch_decode_impl<64, false>(p, tk, tv, stream, launches)
-                 : launch_decode_impl<128, false>(p, tk, tv, stream, launches);
+  if (fp8) return launch_decode_impl<128, true, false>(p, tk, tv, stream, launches);
+  return D == 64 ? launch_decode_impl<64, false, false>(p, tk, tv, stream, launches)
+                 : launch_decode_impl<128, false, false>(p, tk, tv, stream, launches);
+}
+
+cudaError_t launch_window_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 int D, bool fp8, cudaStream_t stream, int* launches) {
+  if (fp8) return launch_decode_impl<128, true, true>(p, tk, tv, stream, launches);
+  return D == 64 ? launch_decode_impl<64, false, true>(p, tk, tv, stream, launches)
+                 : launch_decode_impl<128, false, true>(p, tk, tv, stream, launches);
 }
 
 }  // namespace pkv

@@ -39,6 +39,27 @@ __device__ __forceinline__ void resolve_set(const DecodeParams& p, int& begin, i
   if (n < 0) n = 0;
 }
 
+// The keys that the last token of a sequence of ctx tokens sees: positions 0 .. sinks - 1 and
+// from .. ctx - 1 (sinks cut to ctx). They lie in the blocks 0 .. head - 1 and those from
+// `first` on; the blocks between are never looked up. Blocks are numbered without that gap: the
+// v-th block read is logical block v, or v + gap from `head` on.
+struct Seen {
+  int ctx, sinks, from;
+  __device__ Seen(int ctx_, int window, int sinks_)
+      : ctx(ctx_), sinks(min(sinks_, ctx_)), from(ctx_ > window ? ctx_ - window : 0) {}
+  template <int BS>
+  __device__ int head() const { return (sinks + BS - 1) / BS; }
+  template <int BS>
+  __device__ int gap() const { return max(from / BS - head<BS>(), 0); }
+  template <int BS>
+  __device__ int blocks() const { return (ctx + BS - 1) / BS - gap<BS>(); }
+  // bit t: position pos0 + t is seen (t < 32)
+  __device__ uint32_t mask(int pos0) const {
+    return below(ctx - pos0) & (below(sinks - pos0) | ~below(from - pos0));
+  }
+  __device__ static uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+};
+
 // The set's sequences into shared memory (every CTA, redundantly): per position i < n, the
 // request s_r[i] (-1 if out of range, flagged), its query row s_row[i], its context length
 // s_ctx[i] (cut to `cap` tokens, flagged), and the exclusive prefix s_pre[i] of the BS-token
@@ -46,10 +67,12 @@ __device__ __forceinline__ void resolve_set(const DecodeParams& p, int& begin, i
 // any is waited for (two dependent rounds: the order, then lengths and rows), and the prefix
 // is one block-wide scan. All threads of the CTA call it; s_scan holds one int per warp.
 // Kept out of line: it runs once per CTA, and the streaming loop after it keeps its registers.
-template <int BS>
+// WIN: the counts are of the blocks that a windowed decode reads (Seen).
+template <int BS, bool WIN = false>
 __device__ __noinline__ int64_t scan_set(const int32_t* order, const int32_t* seq_lens, const int32_t* cu_q,
                                          int begin, int n, int batch_reqs, int cap, unsigned int* err, int* s_pre,
-                                         int* s_ctx, int* s_r, int* s_row, int* s_scan) {
+                                         int* s_ctx, int* s_r, int* s_row, int* s_scan, int window = 0,
+                                         int sinks = 0) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nthreads = blockDim.x, nw = nthreads >> 5;
   const bool report = blockIdx.x == 0 && blockIdx.y == 0;
@@ -73,7 +96,7 @@ __device__ __noinline__ int64_t scan_set(const int32_t* order, const int32_t* se
     }
     s_ctx[i] = ctx;
     s_row[i] = row;
-    s_pre[i] = (ctx + BS - 1) / BS;
+    s_pre[i] = WIN ? Seen(ctx, window, sinks).blocks<BS>() : (ctx + BS - 1) / BS;
   }
   __syncthreads();
   // exclusive scan of the block counts: each thread a contiguous segment

@@ -58,6 +58,7 @@ struct DecodeParams {
   int64_t kv_block_bytes;
   const float* k_scales;    // block-scaled cache: [num_blocks][Hkv]
   const float* v_scales;
+  int32_t window, sinks;    // windowed decode: keys seen behind the query's position, and first keys always seen
 };
 
 // Extend and prefill share one kernel; prefill is the case without cached context.
@@ -87,6 +88,7 @@ struct AttnParams {
   const float* k_scales;  // block-scaled cache: [num_blocks][Hkv]
   const float* v_scales;
   int32_t sched_slot;    // this launch's work-item counter slot (< kAttnSchedSlots); -1: none
+  int32_t window, sinks;  // windowed attention: see DecodeParams (window 0: every key up to the row's own)
 };
 
 // Extend over an FP8 cache: the set's context blocks gathered into a bf16 pool (exact E4M3
@@ -174,6 +176,12 @@ enum AttrSlot {
   kAttrAppend0,  // + the cache kind (three)
   kAttrAppendLast = kAttrAppend0 + 2,
   kAttrMla,
+  kAttrWinDecode64,
+  kAttrWinDecode128,
+  kAttrWinDecode128Fp8,
+  kAttrWinAttn64,
+  kAttrWinAttn128,
+  kAttrWinAttn128Fp8,
   kAttrCount
 };
 
@@ -198,6 +206,9 @@ cudaError_t launch_batch_classify_reorder(const int32_t* cu_q, const int32_t* se
                                           int64_t num_tokens, cudaStream_t stream, int* launches);
 cudaError_t launch_paged_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                 int D, bool fp8, cudaStream_t stream, int* launches);
+// The same over the keys of p.window and p.sinks (p.window >= 1).
+cudaError_t launch_window_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 int D, bool fp8, cudaStream_t stream, int* launches);
 // Decode over a block-scaled E4M3 cache (its workspace is never larger than paged_decode's).
 cudaError_t launch_decode_scaled(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream,
                                  int* launches);
