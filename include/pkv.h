@@ -227,6 +227,31 @@ pkv_status pkv_kv_append(const void* q, int64_t q_stride, const void* key, int64
                          pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * kv_append_norm — kv_append with a norm of every query and key head before the rotation.
+ * The pages have no counterpart; models that norm their queries and keys head by head take it
+ * in the place of kv_append. Each query head x of a token becomes
+ *   x / sqrt(sum_d x_d^2 / head_dim + eps) * q_weight   (keys alike with k_weight; values are
+ * left as they are) in fp32, every operation rounded by itself (the root's inverse is off by at
+ * most two units in the last place), and is not rounded further before the rotation. Everything
+ * else is as in kv_append: what is turned, stored, returned and scaled is the normed row.
+ * norm: q_weight, k_weight device [head_dim], 16-byte aligned, one of them NULL for a side that
+ * has no norm (both NULL: PKV_ERR_INVALID_ARG); bf16, or fp32 when weight_f32 != 0; eps > 0 and
+ * finite. head_dim: a power of two of at most 512, no latent cache (others PKV_ERR_UNSUPPORTED).
+ * Elements whose squares sum up beyond fp32 give zeros (of magnitudes up to 2^59 none do).
+ * ------------------------------------------------------------------------------------- */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  int32_t weight_f32;
+} pkv_head_norm;
+pkv_status pkv_kv_append_norm(const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+                              const void* value, int64_t value_stride, const int64_t* positions,
+                              const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                              pkv_rope rope, pkv_head_norm norm, pkv_cache cache, void* q_out,
+                              void* key_out, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * batch_classify_reorder — sort the batch's requests into [decode : extend : prefill].
  * Source: vLLM blog "rocm-attention-backend", section "ROCM_AITER_FA key innovations"
  * (three-way routing; the model runner reorders the batch to [decode:extend:prefill],
@@ -465,6 +490,26 @@ pkv_status pkv_kv_block_pack(pkv_cache cache, const int32_t* block_ids, int32_t 
  * ------------------------------------------------------------------------------------- */
 pkv_status pkv_kv_block_unpack(const void* src, const int32_t* block_ids, int32_t num_ids,
                                pkv_cache cache, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * kv_block_copy — copy blocks of a pool onto other blocks of it, in every layer of a cache.
+ * The pages have no counterpart to this call; it is what a block table (51CTO serving article,
+ * section "Paged Attention") needs when sequences fork (each fork takes a copy of the last,
+ * partly filled block and shares the full ones) and when a pool is compacted.
+ * layers: host array of num_layers caches (read before the call returns) that agree in
+ * num_blocks, block_size, num_kv_heads, head_dim, stride_block and kv_dtype; K, V and, for
+ * PKV_KV_FP8_E4M3_BLOCK, the scales of both are copied. v NULL or equal to k in every layer: a
+ * latent cache, one row a token.
+ * For each i < num_pairs with s = src_ids[i], d = dst_ids[i] (device int32) and each layer:
+ *   s < 0 or d < 0                 -> skipped (padding);
+ *   s or d >= num_blocks           -> skipped, PKV_DEVERR_BLOCK set;
+ *   otherwise                      -> block d becomes what block s was before the call.
+ * A source may appear in any number of pairs. A destination must appear in one pair only and be
+ * no pair's source (a pair with s == d copies nothing and is no pair in this sense): else what
+ * the blocks involved hold afterwards is unspecified.
+ * ------------------------------------------------------------------------------------- */
+pkv_status pkv_kv_block_copy(const pkv_cache* layers, int32_t num_layers, const int32_t* src_ids,
+                             const int32_t* dst_ids, int32_t num_pairs, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * Layer handoff staging — the per-layer pack of a prefill instance, overlapped with the work

@@ -37,12 +37,17 @@ class PkvRope(ctypes.Structure):
     _fields_ = [("cos_sin", P), ("max_pos", i64), ("dim", i32), ("offset", i32), ("interleaved", i32)]
 
 
+class PkvHeadNorm(ctypes.Structure):
+    _fields_ = [("q_weight", P), ("k_weight", P), ("eps", ctypes.c_float), ("weight_f32", i32)]
+
+
 # (name, restype, argtypes) of every exported entry point; the tests check this list against
 # include/pkv.h and the library's symbol table.
 SIGNATURES = [
     ("pkv_status_string", ctypes.c_char_p, [i32]),
     ("pkv_kv_cache_write", i32, [P, P, P, i64, PkvCache, P]),
     ("pkv_kv_append", i32, [P, i64, P, i64, P, i64, P, P, i64, i32, PkvRope, PkvCache, P, P, P]),
+    ("pkv_kv_append_norm", i32, [P, i64, P, i64, P, i64, P, P, i64, i32, PkvRope, PkvHeadNorm, PkvCache, P, P, P]),
     ("pkv_batch_classify_reorder", i32, [P, P, i32, i32, P, P, P, P, i64, P]),
     ("pkv_paged_decode_workspace_size", sz, [i32, i32, i32, i32, i32]),
     ("pkv_paged_decode_attn", i32, [P, PkvCache, P, i32, P, P, PkvReqs, i32, i32, f32, P, P, P, sz, P]),
@@ -60,6 +65,7 @@ SIGNATURES = [
     ("pkv_window_prefill_attn", i32, [P, P, P, i64, P, PkvReqs, i32, i32, i32, i32, i32, i32, f32, P, P, P]),
     ("pkv_kv_block_pack", i32, [PkvCache, P, i32, P, P]),
     ("pkv_kv_block_unpack", i32, [P, P, i32, PkvCache, P]),
+    ("pkv_kv_block_copy", i32, [P, i32, P, P, i32, P]),
     ("pkv_handoff_create", i32, [i32, P, P]),
     ("pkv_handoff_stage", i32, [P, i32, PkvCache, P, i32, P, P]),
     ("pkv_handoff_ready", i32, [P, i32, P]),

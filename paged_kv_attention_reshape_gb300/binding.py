@@ -212,8 +212,21 @@ def _token_out(t: Optional[torch.Tensor], name: str, rows: int, heads: int, dim:
     return t
 
 
+def _head_norm(q_norm, k_norm, eps, dim: int, device_index: int) -> "_lib.PkvHeadNorm":
+    some = k_norm if q_norm is None else q_norm
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is None:
+            continue
+        if w.get_device() != device_index or w.dtype not in (torch.bfloat16, torch.float32) or w.shape != (dim,) \
+                or not w.is_contiguous() or w.dtype is not some.dtype:
+            raise PkvError(f"{name} must be contiguous [{dim}] bf16 or fp32 on the cache's device, alike for q and k")
+    return _lib.PkvHeadNorm(None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                            float(eps), 1 if some.dtype is torch.float32 else 0)
+
+
 def kv_append(q, key, value, positions, slot_mapping, k_cache, v_cache, cos_sin=None, *, rope_offset=0,
-              interleaved=False, q_out=None, k_out=None, k_scale=1.0, v_scale=1.0, stream=None):
+              interleaved=False, q_out=None, k_out=None, k_scale=1.0, v_scale=1.0, stream=None, q_norm=None,
+              k_norm=None, norm_eps=1e-6):
     """Rotate q and key by their positions and append key and value to the cache slots.
 
     q [T, Hq, D] (or None), key and value [T, Hkv, D] bf16, tokens any stride apart; positions and
@@ -222,7 +235,11 @@ def kv_append(q, key, value, positions, slot_mapping, k_cache, v_cache, cos_sin=
     bf16 or FP8 cache; with k_scale / v_scale tensors [num_blocks, Hkv] the scales of the blocks
     written are updated too. A latent cache: value and v_cache None. Returns (q_out, k_out): the
     rotated rows, [T, H, D] contiguous, allocated here when not given (rows of skipped tokens are
-    left as they were)."""
+    left as they were).
+
+    q_norm and k_norm, weights [D] (bf16 or fp32, both alike; either may be None): every query (key) head is
+    divided by the root of its mean square plus norm_eps and multiplied by them before it is rotated
+    (D a power of two of at most 512, no latent cache)."""
     lib = _lib.load()
     if (value is None) != (v_cache is None):
         raise PkvError("a latent cache has neither value nor v_cache; any other has both")
@@ -254,6 +271,11 @@ def kv_append(q, key, value, positions, slot_mapping, k_cache, v_cache, cos_sin=
     else:
         rope = _lib.PkvRope(None, 0, 0, 0, 0)
     slots = _token_index(slot_mapping, "slot_mapping", T, dev)
+    if q_norm is not None or k_norm is not None:
+        norm = _head_norm(q_norm, k_norm, norm_eps, d, dev)
+        _check(lib.pkv_kv_append_norm(q_ptr, q_stride, key.data_ptr(), k_stride, v_ptr, v_stride, pos_ptr, slots, T, hq,
+                                      rope, norm, cache, qo_ptr, k_out.data_ptr(), _stream(stream)), "kv_append")
+        return q_out, k_out
     _check(lib.pkv_kv_append(q_ptr, q_stride, key.data_ptr(), k_stride, v_ptr, v_stride, pos_ptr, slots, T, hq, rope,
                              cache, qo_ptr, k_out.data_ptr(), _stream(stream)), "kv_append")
     return q_out, k_out
@@ -282,6 +304,51 @@ def kv_block_unpack(src, block_ids, k_cache, v_cache, stream=None):
     if tuple(src.shape) != (2, n) + tuple(k_cache.shape[1:]):
         raise ValueError(f"src shape {tuple(src.shape)} does not match 2 x {n} blocks of {tuple(k_cache.shape[1:])}")
     _check(lib.pkv_kv_block_unpack(_ptr(src), _ptr(block_ids), n, cache, _stream(stream)), "kv_block_unpack")
+
+
+class CacheLayers:
+    """The layers of one pool of blocks, described once for kv_block_copy: k_caches and v_caches are lists of
+    [num_blocks, block_size, Hkv, D] tensors alike in shape, stride and type (v_caches None: a latent cache);
+    k_scales and v_scales, for a block-scaled cache, lists of fp32 [num_blocks, Hkv]. Scales that are numbers
+    count for nothing here. The tensors are kept alive with the handle."""
+
+    def __init__(self, k_caches, v_caches=None, k_scales=None, v_scales=None):
+        k_caches = list(k_caches)
+        v_caches = k_caches if v_caches is None else list(v_caches)
+
+        def per_layer(s, name):
+            if s is None or not isinstance(s, (list, tuple)):
+                return [1.0 if s is None else s] * len(k_caches)
+            if len(s) != len(k_caches):
+                raise PkvError(f"{name}: one for each layer")
+            return list(s)
+
+        k_scales, v_scales = per_layer(k_scales, "k_scales"), per_layer(v_scales, "v_scales")
+        if not k_caches or len(v_caches) != len(k_caches):
+            raise PkvError("k_caches and v_caches must hold one tensor for each layer")
+        made = [make_cache(*layer) for layer in zip(k_caches, v_caches, k_scales, v_scales)]
+        self.device_index = k_caches[0].get_device()
+        if any(t.get_device() != self.device_index for t in k_caches + v_caches):
+            raise PkvError("all layers must be on one device")
+        self._layers = (_lib.PkvCache * len(made))(*made)
+        self._kept = (k_caches, v_caches, k_scales, v_scales)
+
+    def __len__(self):
+        return len(self._layers)
+
+
+def kv_block_copy(layers: CacheLayers, src_ids, dst_ids, stream=None):
+    """In every layer, block dst_ids[i] becomes a copy of block src_ids[i] (int32 ids; a negative one skips the
+    pair). A source may be copied many times; a destination must be in one pair only and be no pair's source."""
+    lib = _lib.load()
+    n, dev = src_ids.numel(), layers.device_index
+    if dev != torch.cuda.current_device():
+        raise PkvError("the cache must be on the current device")
+    for t, name in ((src_ids, "src_ids"), (dst_ids, "dst_ids")):
+        if t.dtype is not torch.int32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+            raise PkvError(f"{name} must be {n} contiguous int32 ids on the cache's device")
+    _check(lib.pkv_kv_block_copy(layers._layers, len(layers._layers), src_ids.data_ptr(), dst_ids.data_ptr(), n,
+                                 _stream(stream)), "kv_block_copy")
 
 
 class LayerHandoff:

@@ -320,11 +320,11 @@ pkv_status pkv_kv_cache_write(const void* key, const void* value, const int64_t*
   return st;
 }
 
-pkv_status pkv_kv_append(const void* q, int64_t q_stride, const void* key, int64_t key_stride,
-                         const void* value, int64_t value_stride, const int64_t* positions,
-                         const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
-                         pkv_rope rope, pkv_cache cache, void* q_out, void* key_out,
-                         pkv_stream_t stream) {
+// kv_append and, with norms, kv_append_norm.
+static pkv_status run_append(const void* q, int64_t q_stride, const void* key, int64_t key_stride, const void* value,
+                             int64_t value_stride, const int64_t* positions, const int64_t* slot_mapping,
+                             int64_t num_tokens, int32_t num_q_heads, pkv_rope rope, const pkv_head_norm* norm,
+                             pkv_cache cache, void* q_out, void* key_out, pkv_stream_t stream) {
   if (num_tokens < 0 || num_q_heads < 0) return PKV_ERR_INVALID_ARG;
   const bool latent = cache.kv_dtype == PKV_KV_BF16 && cache.num_kv_heads == 1 &&
                       (cache.v == nullptr || cache.v == cache.k);
@@ -336,6 +336,13 @@ pkv_status pkv_kv_append(const void* q, int64_t q_stride, const void* key, int64
   if (D % 16 != 0 || D > 1024 || rope.dim % 16 != 0 || rope.offset % 16 != 0 ||
       static_cast<int64_t>(rope.offset) + rope.dim > D)
     return PKV_ERR_UNSUPPORTED;
+  if (norm != nullptr) {
+    // a norm's head is one row of a warp's lanes, 16 dims a lane; a latent row is no head
+    if (latent || (D & (D - 1)) != 0 || D > 512) return PKV_ERR_UNSUPPORTED;
+    if (!(std::isfinite(norm->eps) && norm->eps > 0.f) || (norm->q_weight == nullptr && norm->k_weight == nullptr) ||
+        !aligned16(norm->q_weight) || !aligned16(norm->k_weight))
+      return PKV_ERR_INVALID_ARG;
+  }
   // an item's flat row index and its offset in a row stay within 32 bits
   const int64_t rows = num_q_heads + 2 * static_cast<int64_t>(cache.num_kv_heads);
   if (rows * D > INT32_MAX || num_tokens > (int64_t(1) << 30)) return PKV_ERR_UNSUPPORTED;
@@ -385,10 +392,34 @@ pkv_status pkv_kv_append(const void* q, int64_t q_stride, const void* key, int64
   }
   p.k_scales = cache.k_scales;
   p.v_scales = cache.v_scales;
+  if (norm != nullptr) {
+    p.q_norm = norm->q_weight;
+    p.k_norm = norm->k_weight;
+    p.norm_eps = norm->eps;
+    p.norm_f32 = norm->weight_f32;
+  }
   int launches = 0;
   st = cuda_status(launch_kv_append(p, cache.kv_dtype, reinterpret_cast<cudaStream_t>(stream), &launches));
   t_launches += launches;
   return st;
+}
+
+pkv_status pkv_kv_append(const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+                         const void* value, int64_t value_stride, const int64_t* positions,
+                         const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                         pkv_rope rope, pkv_cache cache, void* q_out, void* key_out,
+                         pkv_stream_t stream) {
+  return run_append(q, q_stride, key, key_stride, value, value_stride, positions, slot_mapping, num_tokens, num_q_heads,
+                    rope, nullptr, cache, q_out, key_out, stream);
+}
+
+pkv_status pkv_kv_append_norm(const void* q, int64_t q_stride, const void* key, int64_t key_stride,
+                              const void* value, int64_t value_stride, const int64_t* positions,
+                              const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                              pkv_rope rope, pkv_head_norm norm, pkv_cache cache, void* q_out,
+                              void* key_out, pkv_stream_t stream) {
+  return run_append(q, q_stride, key, key_stride, value, value_stride, positions, slot_mapping, num_tokens, num_q_heads,
+                    rope, &norm, cache, q_out, key_out, stream);
 }
 
 pkv_status pkv_kv_block_pack(pkv_cache cache, const int32_t* block_ids, int32_t num_ids, void* dst,
@@ -420,6 +451,49 @@ pkv_status pkv_kv_block_unpack(const void* src, const int32_t* block_ids, int32_
   st = cuda_status(launch_kv_block_unpack(src, block_ids, num_ids, cache, error_word(),
                                           reinterpret_cast<cudaStream_t>(stream)));
   t_launches += 1;
+  return st;
+}
+
+pkv_status pkv_kv_block_copy(const pkv_cache* layers, int32_t num_layers, const int32_t* src_ids,
+                             const int32_t* dst_ids, int32_t num_pairs, pkv_stream_t stream) {
+  if (layers == nullptr || num_layers < 1 || num_pairs < 0) return PKV_ERR_INVALID_ARG;
+  const pkv_cache& a = layers[0];
+  const bool latent = a.v == nullptr || a.v == a.k;
+  for (int32_t l = 0; l < num_layers; ++l) {
+    pkv_cache c = layers[l];
+    if ((c.v == nullptr || c.v == c.k) != latent) return PKV_ERR_INVALID_ARG;
+    if (c.v == nullptr) c.v = c.k;
+    const pkv_status st = check_cache(c, false, true);
+    if (st != PKV_OK) return st;
+    if (c.num_blocks != a.num_blocks || c.block_size != a.block_size || c.num_kv_heads != a.num_kv_heads ||
+        c.head_dim != a.head_dim || c.stride_block != a.stride_block || c.kv_dtype != a.kv_dtype)
+      return PKV_ERR_INVALID_ARG;
+  }
+  if (latent && a.kv_dtype == PKV_KV_FP8_E4M3_BLOCK) return PKV_ERR_UNSUPPORTED;
+  BlockCopyParams p{};
+  p.block_bytes = static_cast<int64_t>(a.block_size) * a.num_kv_heads * a.head_dim * elem_bytes(a);
+  if (p.block_bytes % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  if (num_pairs == 0) return PKV_OK;
+  if (src_ids == nullptr || dst_ids == nullptr) return PKV_ERR_INVALID_ARG;
+  p.err = error_word();
+  p.src = src_ids;
+  p.dst = dst_ids;
+  p.num_pairs = num_pairs;
+  p.parts = latent ? 1 : 2;
+  p.Hkv = a.num_kv_heads;
+  p.num_blocks = a.num_blocks;
+  p.stride_bytes = a.stride_block * elem_bytes(a);
+  const bool scaled = a.kv_dtype == PKV_KV_FP8_E4M3_BLOCK;
+  pkv_status st = PKV_OK;
+  for (int32_t l0 = 0; l0 < num_layers && st == PKV_OK; l0 += kCopyLayers) {
+    p.layers = std::min(num_layers - l0, kCopyLayers);
+    for (int32_t l = 0; l < p.layers; ++l) {
+      const pkv_cache& c = layers[l0 + l];
+      p.layer[l] = CopyLayer{c.k, latent ? c.k : c.v, scaled ? c.k_scales : nullptr, scaled ? c.v_scales : nullptr};
+    }
+    st = cuda_status(launch_kv_block_copy(p, reinterpret_cast<cudaStream_t>(stream)));
+    t_launches += 1;
+  }
   return st;
 }
 

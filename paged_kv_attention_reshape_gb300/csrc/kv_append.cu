@@ -103,6 +103,32 @@ __device__ __forceinline__ void turn(float* x, const Angles& g, bool interleaved
   }
 }
 
+// The norm of a head: x / sqrt(mean of squares + eps) times the weights, in fp32, before the rotation. A row's
+// D / 16 items are neighbouring lanes of one warp (D / 16 is a power of two), which add up their squares along a
+// tree of fixed order.
+__device__ __forceinline__ void load_weights(const void* w, bool f32, int at, float* out) {
+  if (f32) {
+    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
+    const float4 a = __ldg(src), b = __ldg(src + 1);
+    out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w, out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
+  } else {
+    unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + at)), out);
+  }
+}
+__device__ __forceinline__ void norm_item(const AppendParams& p, const void* w, const Item& it, int items, int lane, float* x) {
+  float sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
+  const uint32_t group = items == 32 ? 0xffffffffu : ((1u << items) - 1u) << (lane & ~(items - 1));
+  for (int o = items >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(group, sum, o);
+  const float inv = rsqrtf(__fadd_rn(sum / static_cast<float>(p.D), p.norm_eps));
+  float wt[16];
+  load_weights(w, p.norm_f32, it.a, wt);
+  load_weights(w, p.norm_f32, it.b, wt + 8);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], inv), wt[e]);
+}
+
 // Whether token t's row is to be written: its slot and position are in range (flagged if not).
 __device__ __forceinline__ bool token_ok(const AppendParams& p, int64_t slot, int64_t pos, bool report) {
   if (slot < 0) return false;
@@ -121,7 +147,7 @@ __device__ __forceinline__ bool token_ok(const AppendParams& p, int64_t slot, in
 // value rows, U rows of each token at a time a thread. The rows' loads, which depend on nothing but
 // the token's index, are issued together with those of its slot and position and before those of its
 // angles, so that a CTA costs two round trips to memory.
-template <int KIND, int TW, int U>
+template <int KIND, int TW, int U, bool NORM>
 __device__ __forceinline__ void append_rows(const AppendParams& p, int64_t group) {
   const int items = p.D / 16;
   const int i = threadIdx.x % items, h0 = threadIdx.x / items, hstep = blockDim.x / items;
@@ -175,6 +201,10 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int64_t group
         float x[16];
         unpack8(va[w][u], x);
         unpack8(vb[w][u], x + 8);
+        if constexpr (NORM) {
+          const void* wt = is_v ? nullptr : (r < p.Hq ? p.q_norm : p.k_norm);
+          if (wt != nullptr) norm_item(p, wt, it, items, threadIdx.x & 31, x);
+        }
         if (it.turn && !is_v) {
           if (p.interleaved) turn(x, g[w], true); else turn(x, g[w], false);
         }
@@ -219,6 +249,7 @@ __device__ __forceinline__ float scale_for(float amax) {
 // 8 items a row, 4 rows a pass). The run is those of tokens t .. t + 15 that have slots in block blk (rows
 // skipped for what is wrong with them, or padding, may lie in between); which they are is read together with
 // all the rows that there can be, so a run costs two round trips to memory (the second for the angles).
+template <bool NORM>
 __device__ __forceinline__ void append_run(const AppendParams& p, int64_t t, int64_t blk, int h, bool is_v, bool report,
                                            int lane) {
   constexpr int DH = 128, PASSES = kBlockTokens / 4;
@@ -259,6 +290,9 @@ __device__ __forceinline__ void append_run(const AppendParams& p, int64_t t, int
     const bool live = (mask >> j) & 1u;
     unpack8(va[w], x[w]);
     unpack8(vb[w], x[w] + 8);
+    if constexpr (NORM) {
+      if (!is_v && live && p.k_norm != nullptr) norm_item(p, p.k_norm, it, DH / 16, lane, x[w]);
+    }
     if (it.turn && !is_v && live) {
       Angles g;
       load_angles(p, pos, i, g);
@@ -313,6 +347,7 @@ __device__ __forceinline__ void append_run(const AppendParams& p, int64_t t, int
 
 // One CTA: the runs that begin in its group of tokens. A run begins at a token with a slot in a block that
 // none of the 15 tokens before it has a slot in.
+template <bool NORM>
 __device__ __forceinline__ void append_runs(const AppendParams& p, int64_t group) {
   __shared__ int64_t s_block[kBlockTokens];
   __shared__ int s_lead[kBlockTokens];
@@ -338,7 +373,7 @@ __device__ __forceinline__ void append_runs(const AppendParams& p, int64_t group
   const int per = 2 * p.Hkv;  // K and V of each head
   for (int u = warp; u < s_count * per; u += nw) {
     const int l = u / per, v = u % per;
-    append_run(p, t0 + s_lead[l], s_block[l], v >> 1, v & 1, v == 0, lane);
+    append_run<NORM>(p, t0 + s_lead[l], s_block[l], v >> 1, v & 1, v == 0, lane);
   }
 }
 
@@ -370,7 +405,7 @@ __host__ __device__ __forceinline__ int64_t row_bytes(const AppendParams& p) {
   return 2ll * p.D * (p.Hq + (KIND == PKV_KV_FP8_E4M3_BLOCK ? 0 : p.Hkv * (p.v != nullptr ? 2 : 1)));
 }
 
-template <int KIND, uint32_t S>
+template <int KIND, uint32_t S, bool NORM>
 __global__ void __launch_bounds__(kThreads + 32) kv_append_stream_kernel(AppendParams p) {
   extern __shared__ __align__(128) uint8_t sm_rows[];
   __shared__ uint64_t full[S], done[S];
@@ -476,12 +511,18 @@ __global__ void __launch_bounds__(kThreads + 32) kv_append_stream_kernel(AppendP
         uint4* a = reinterpret_cast<uint4*>(stage + 2 * (r * p.D + it.a));
         uint4* b = reinterpret_cast<uint4*>(stage + 2 * (r * p.D + it.b));
         const bool turns = it.turn && !is_v;
-        if (!turns && (KIND != PKV_KV_FP8_E4M3 || r < p.Hq)) continue;  // goes out as it came
+        const void* wt = NORM && !is_v ? (r < p.Hq ? p.q_norm : p.k_norm) : nullptr;
+        if (!turns && wt == nullptr && (KIND != PKV_KV_FP8_E4M3 || r < p.Hq)) continue;  // goes out as it came
         float x[16];
         unpack8(*a, x);
         unpack8(*b, x + 8);
-        if (turns) {
-          if (p.interleaved) turn(x, g, true); else turn(x, g, false);
+        if constexpr (NORM) {
+          if (wt != nullptr) norm_item(p, wt, it, items, tid & 31, x);
+        }
+        if (turns || wt != nullptr) {
+          if (turns) {
+            if (p.interleaved) turn(x, g, true); else turn(x, g, false);
+          }
           *a = pack8(x);
           *b = pack8(x + 8);
         }
@@ -503,24 +544,25 @@ __global__ void __launch_bounds__(kThreads + 32) kv_append_stream_kernel(AppendP
 }
 
 // The rows of TW tokens a CTA and, for a block-scaled cache (RUNS), before them the CTAs that append runs.
-template <int KIND, int TW, int U, bool RUNS>
+template <int KIND, int TW, int U, bool RUNS, bool NORM>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendParams p) {
   pdl_wait();
   pdl_release();
   if constexpr (RUNS) {
     if (blockIdx.x < p.run_groups) {
-      append_runs(p, blockIdx.x);
+      append_runs<NORM>(p, blockIdx.x);
       return;
     }
-    append_rows<KIND, TW, U>(p, static_cast<int64_t>(blockIdx.x) - p.run_groups);
+    append_rows<KIND, TW, U, NORM>(p, static_cast<int64_t>(blockIdx.x) - p.run_groups);
   } else {
-    append_rows<KIND, TW, U>(p, blockIdx.x);
+    append_rows<KIND, TW, U, NORM>(p, blockIdx.x);
   }
 }
+template <bool NORM>
 __global__ void __launch_bounds__(kThreads) kv_append_runs_kernel(AppendParams p) {
   pdl_wait();
   pdl_release();
-  append_runs(p, blockIdx.x);
+  append_runs<NORM>(p, blockIdx.x);
 }
 
 }  // namespace
@@ -529,17 +571,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_runs_kernel(AppendParams p
 // More CTAs with fewer stages where codes are made or little is stored beside q, more stages where the
 // copies are all there is: 10,000 tokens of 64 query and 8 KV heads of 128 into a bf16 cache 73.7 us
 // with 3 stages and 69.5 with 4 (66 since an elected thread issues); into a block-scaled one 84.5 and 86.
-template <int KIND>
+template <int KIND, bool NORM>
 static bool launch_stream(const AppendParams& p, cudaStream_t stream, cudaError_t* e) {
   constexpr uint32_t S = KIND == PKV_KV_BF16 ? 4 : 3;
   constexpr int64_t kRoom = 222 * 1024, kPerSm = 3;
   const int64_t bytes = (row_bytes<KIND>(p) + p.rot * 4) * S, taken = bytes + 1280;  // with the static and reserved bytes
   if (2 * taken > kRoom) return false;
-  *e = set_smem_attr_once(reinterpret_cast<const void*>(&kv_append_stream_kernel<KIND, S>), static_cast<int>(kRoom / 2),
-                          kAttrAppend0 + KIND);
+  *e = set_smem_attr_once(reinterpret_cast<const void*>(&kv_append_stream_kernel<KIND, S, NORM>), static_cast<int>(kRoom / 2),
+                          (NORM ? kAttrAppendNorm0 : kAttrAppend0) + KIND);
   if (*e != cudaSuccess) return true;
   const int64_t grid = std::min<int64_t>(p.num_tokens, num_sms() * std::min<int64_t>(kRoom / taken, kPerSm));
-  *e = launch_pdl(kv_append_stream_kernel<KIND, S>, dim3(static_cast<unsigned>(grid)), dim3(kThreads + 32),
+  *e = launch_pdl(kv_append_stream_kernel<KIND, S, NORM>, dim3(static_cast<unsigned>(grid)), dim3(kThreads + 32),
                   static_cast<size_t>(bytes), stream, p);
   return true;
 }
@@ -550,29 +592,36 @@ static int many_tokens(const AppendParams& p, int kind) {
   return p.Hq > kFewHeads ? kManyTokensBlock : kManyTokensBlockFewHeads;
 }
 
-template <int KIND>
+template <int KIND, bool NORM>
 static cudaError_t launch_rows(const AppendParams& p, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  if (p.num_tokens >= many_tokens(p, KIND) && launch_stream<KIND>(p, stream, &e)) return e;
-  return launch_pdl(kv_append_kernel<KIND, 1, 2, false>, dim3(static_cast<unsigned>(p.num_tokens)), dim3(kThreads), 0, stream, p);
+  if (p.num_tokens >= many_tokens(p, KIND) && launch_stream<KIND, NORM>(p, stream, &e)) return e;
+  return launch_pdl(kv_append_kernel<KIND, 1, 2, false, NORM>, dim3(static_cast<unsigned>(p.num_tokens)), dim3(kThreads), 0,
+                    stream, p);
 }
 
-cudaError_t launch_kv_append(const AppendParams& in, int kind, cudaStream_t stream, int* launches) {
+template <bool NORM>
+static cudaError_t launch_append(const AppendParams& in, int kind, cudaStream_t stream, int* launches) {
   AppendParams p = in;
   *launches = 1;
-  if (kind == PKV_KV_FP8_E4M3) return launch_rows<PKV_KV_FP8_E4M3>(p, stream);
-  if (kind == PKV_KV_BF16) return launch_rows<PKV_KV_BF16>(p, stream);
+  if (kind == PKV_KV_FP8_E4M3) return launch_rows<PKV_KV_FP8_E4M3, NORM>(p, stream);
+  if (kind == PKV_KV_BF16) return launch_rows<PKV_KV_BF16, NORM>(p, stream);
   // Tokens of a CTA that appends runs: 1, 4 or 16 of one long sequence (64 query and 8 KV heads, us) 1024
   // 11.1, 9.7, 9.1; 4096 49, 39, 37; of one token a sequence 256 8.1, 18.5, 62; 1024 26, 25, 85; 4096 112, 105, 120.
   p.run_tokens = p.num_tokens <= 1024 ? 1 : (p.num_tokens <= 4096 ? 4 : kBlockTokens);
   p.run_groups = static_cast<uint32_t>((p.num_tokens + p.run_tokens - 1) / p.run_tokens);
   if (p.Hq > 0 && p.num_tokens < many_tokens(p, kind))
-    return launch_pdl(kv_append_kernel<PKV_KV_FP8_E4M3_BLOCK, 1, 2, true>,
+    return launch_pdl(kv_append_kernel<PKV_KV_FP8_E4M3_BLOCK, 1, 2, true, NORM>,
                       dim3(static_cast<unsigned>(p.run_groups + p.num_tokens)), dim3(kThreads), 0, stream, p);
-  cudaError_t e = launch_pdl(kv_append_runs_kernel, dim3(p.run_groups), dim3(kThreads), 0, stream, p);
+  cudaError_t e = launch_pdl(kv_append_runs_kernel<NORM>, dim3(p.run_groups), dim3(kThreads), 0, stream, p);
   if (e != cudaSuccess || p.Hq == 0) return e;
   *launches = 2;
-  return launch_rows<PKV_KV_FP8_E4M3_BLOCK>(p, stream);
+  return launch_rows<PKV_KV_FP8_E4M3_BLOCK, NORM>(p, stream);
+}
+
+cudaError_t launch_kv_append(const AppendParams& p, int kind, cudaStream_t stream, int* launches) {
+  return p.q_norm != nullptr || p.k_norm != nullptr ? launch_append<true>(p, kind, stream, launches)
+                                                    : launch_append<false>(p, kind, stream, launches);
 }
 
 }  // namespace pkv

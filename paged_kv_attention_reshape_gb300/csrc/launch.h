@@ -137,8 +137,34 @@ struct AppendParams {
   float k_inv, v_inv;      // FP8 with tensor scales: 1 / scale
   float* k_scales;         // FP8 with block scales
   float* v_scales;
+  const void* q_norm;      // [D] weights of the heads' norms (NULL: that side has none)
+  const void* k_norm;
+  float norm_eps;
+  int32_t norm_f32;        // the weights are fp32 (else bf16)
   int32_t run_tokens;      // block scales: tokens whose runs one CTA appends (set by the launcher)
   uint32_t run_groups;     // block scales: groups of tokens whose runs a CTA appends (set by the launcher)
+};
+
+// kv_block_copy: pairs of blocks, in up to kCopyLayers layers a launch.
+constexpr int kCopyLayers = 96;
+struct CopyLayer {
+  void* k;
+  void* v;
+  float* k_scales;  // block-scaled cache, else NULL
+  float* v_scales;
+};
+struct BlockCopyParams {
+  unsigned int* err;
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t num_pairs;
+  int32_t layers;        // of this launch
+  int32_t parts;         // 2: K and V; 1: a latent cache
+  int32_t Hkv;
+  int64_t num_blocks;
+  int64_t stride_bytes;  // between consecutive blocks
+  int64_t block_bytes;
+  CopyLayer layer[kCopyLayers];
 };
 
 // Launch with programmatic stream serialisation: the kernel may begin launching while the
@@ -175,6 +201,8 @@ enum AttrSlot {
   kAttrDecodeScaled16,
   kAttrAppend0,  // + the cache kind (three)
   kAttrAppendLast = kAttrAppend0 + 2,
+  kAttrAppendNorm0,  // with norms
+  kAttrAppendNormLast = kAttrAppendNorm0 + 2,
   kAttrMla,
   kAttrWinDecode64,
   kAttrWinDecode128,
@@ -195,11 +223,13 @@ cudaError_t launch_kv_cache_write(const void* key, const void* value, const int6
                                   int64_t num_tokens, const pkv_cache& c, unsigned int* err,
                                   cudaStream_t stream);
 // kind: the cache's kv_dtype
+// (p.q_norm or p.k_norm set: D / 16 a power of two of at most 32)
 cudaError_t launch_kv_append(const AppendParams& p, int kind, cudaStream_t stream, int* launches);
 cudaError_t launch_kv_block_pack(const pkv_cache& c, const int32_t* block_ids, int32_t num_ids,
                                  void* dst, unsigned int* err, cudaStream_t stream);
 cudaError_t launch_kv_block_unpack(const void* src, const int32_t* block_ids, int32_t num_ids,
                                    const pkv_cache& c, unsigned int* err, cudaStream_t stream);
+cudaError_t launch_kv_block_copy(const BlockCopyParams& p, cudaStream_t stream);
 cudaError_t launch_batch_classify_reorder(const int32_t* cu_q, const int32_t* seq_lens, int32_t R,
                                           int32_t threshold, int32_t* perm, int32_t* bounds,
                                           int32_t* cu_q_reordered, int32_t* token_map,
