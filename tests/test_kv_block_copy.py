@@ -69,8 +69,9 @@ def test_refusals():
     from paged_kv_attention_reshape_gb300 import _lib
     lib = _lib.load()
     fake = ctypes.c_void_p(1 << 20)
+    other = ctypes.c_void_p(1 << 21)
     C = _lib.PkvCache
-    good = C(fake, fake, 10, 16, 2, 128, 16 * 2 * 128)
+    good = C(fake, other, 10, 16, 2, 128, 16 * 2 * 128)
 
     def run(*caches, n=3, src=fake, dst=fake):
         return lib.pkv_kv_block_copy((C * len(caches))(*caches), len(caches), src, dst, n, None)
@@ -80,16 +81,16 @@ def test_refusals():
     assert lib.pkv_kv_block_copy(None, 1, fake, fake, 0, None) == 1
     assert lib.pkv_kv_block_copy((C * 1)(good), 0, fake, fake, 0, None) == 1
     # layers that differ
-    for other in (C(fake, fake, 11, 16, 2, 128, 16 * 2 * 128), C(fake, fake, 10, 8, 2, 128, 16 * 2 * 128),
-                  C(fake, fake, 10, 16, 1, 128, 16 * 2 * 128), C(fake, fake, 10, 16, 2, 64, 16 * 2 * 128),
-                  C(fake, fake, 10, 16, 2, 128, 16 * 2 * 128 + 8), C(fake, fake, 10, 16, 2, 128, 16 * 2 * 128, 1, 1.0, 1.0),
+    for differs in (C(fake, other, 11, 16, 2, 128, 16 * 2 * 128), C(fake, other, 10, 8, 2, 128, 16 * 2 * 128),
+                  C(fake, other, 10, 16, 1, 128, 16 * 2 * 128), C(fake, other, 10, 16, 2, 64, 16 * 2 * 128),
+                  C(fake, other, 10, 16, 2, 128, 16 * 2 * 128 + 8), C(fake, other, 10, 16, 2, 128, 16 * 2 * 128, 1, 1.0, 1.0),
                   C(fake, None, 10, 16, 2, 128, 16 * 2 * 128)):
-        assert run(good, other, n=0) == 1
-    assert run(C(None, fake, 10, 16, 2, 128, 16 * 2 * 128), n=0) == 1
-    assert run(C(ctypes.c_void_p((1 << 20) + 2), fake, 10, 16, 2, 128, 16 * 2 * 128), n=0) == 1
+        assert run(good, differs, n=0) == 1
+    assert run(C(None, other, 10, 16, 2, 128, 16 * 2 * 128), n=0) == 1
+    assert run(C(ctypes.c_void_p((1 << 20) + 2), other, 10, 16, 2, 128, 16 * 2 * 128), n=0) == 1
     # block-scaled: both scales, K and V
     blk = lambda v, ks: C(fake, v, 10, 16, 2, 128, 16 * 2 * 128, _lib.KV_FP8_E4M3_BLOCK, 1.0, 1.0, ks, fake)
-    assert run(blk(fake, fake), n=0) == 0 and run(blk(fake, None), n=0) == 1 and run(blk(None, fake), n=0) == 2
+    assert run(blk(other, fake), n=0) == 0 and run(blk(other, None), n=0) == 1 and run(blk(None, fake), n=0) == 2
 
 
 # ---- the operator --------------------------------------------------------------------------------------
