@@ -850,10 +850,11 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   CUtensorMap tq, tk, tv, tck, tcv, tqf;
   std::memset(&tck, 0, sizeof tck);
   std::memset(&tcv, 0, sizeof tcv);
-  const bool packed = ctx_kind == kAttnCtxBlock;
-  if (!(packed ? encode_packed_q(&tq, q, num_tokens, Hq, p.G, D) : encode_rows(&tq, q, num_tokens, Hq, D, 128)) ||
-      !encode_rows(&tk, k, num_tokens, Hkv, D, 128) ||
-      !encode_rows(&tv, v, num_tokens, Hkv, D, 128) || !encode_rows(&tqf, q, num_tokens * Hq, 1, D, 128))
+  const bool windowed = window > 0 && ctx_kind == kAttnCtxBf16, packed = ctx_kind == kAttnCtxBlock;
+  const int rows = windowed ? 16 : 128;  // of a box of new keys
+  if (!(packed || windowed ? encode_packed_q(&tq, q, num_tokens, Hq, p.G, D) : encode_rows(&tq, q, num_tokens, Hq, D, 128)) ||
+      !encode_rows(&tk, k, num_tokens, Hkv, D, rows) ||
+      !encode_rows(&tv, v, num_tokens, Hkv, D, rows) || !encode_rows(&tqf, q, num_tokens * Hq, 1, D, 128))
     return PKV_ERR_CUDA;
   if (cache != nullptr &&
       (!encode_cache(&tck, cache->k, *cache) || !encode_cache(&tcv, cache->v, *cache)))
@@ -862,9 +863,11 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   for (int32_t off = 0; off < reqs.max_reqs && st == PKV_OK; off += kAttnSetChunk) {
     p.set_offset = off;
     p.sched_slot = next_sched_slot(reinterpret_cast<cudaStream_t>(stream));
-    st = cuda_status(packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, workspace, reinterpret_cast<cudaStream_t>(stream), &launches)
-                            : launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
-                                               reinterpret_cast<cudaStream_t>(stream), &launches));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    st = cuda_status(windowed ? launch_attn_window(p, tq, tk, tv, tck, tcv, D, s, &launches)
+                     : packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, workspace, s, &launches)
+                              : launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
+                                                 s, &launches));
   }
   t_launches += launches;
   return st;

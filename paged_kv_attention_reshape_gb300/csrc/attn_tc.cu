@@ -341,7 +341,7 @@ __device__ __forceinline__ void conv_bf16_row(uint32_t tile, int R, float sc, bo
 // core multiplies fp16 operands (kind::f16), P is packed as fp16, and the MMA warp waits on
 // the converters' barriers (q_conv, conv_full) instead of the loads'. Queries, new keys and
 // new values divided by vs must lie within the fp16 range.
-// WIN (kCtxBf16 and kCtxFp8): a key is seen by the rows up to p.window - 1 positions behind it, and by all
+// WIN (kCtxFp8; over bf16 attn_window.cu serves windows): a key is seen by the rows up to p.window - 1 positions behind it, and by all
 // later ones if it is among the first p.sinks. Tiles that no row of the item sees are left out (tc_window),
 // pages that no row sees are not looked up, and value rows that no row sees are zeroed like those past the
 // context's end.
@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
     const __grid_constant__ CUtensorMap tm_ck, const __grid_constant__ CUtensorMap tm_cv,
     const __grid_constant__ CUtensorMap tm_qf) {
   using C = TcCfg<D, KIND>;
+  static_assert(!WIN || C::CONV, "windows over bf16 are attn_window.cu's");
   constexpr bool SCALED = KIND != kCtxBf16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
 #pragma unroll
             for (int e = 0; e < 32; e += 2) mx = sm::max3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
           } else {
-            if constexpr (WIN) mask_bits(v, cols(c * 32)); else mask_cols(v, kv - c * 32);
+            mask_cols(v, kv - c * 32);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) mx = sm::max3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
           }
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             uint32_t v[32];
             tc::ld32(srow + c * 32, v);
             tc::wait_ld();
-            if constexpr (WIN) mask_bits(v, cols(c * 32)); else mask_cols(v, kv - c * 32);
+            mask_cols(v, kv - c * 32);
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
@@ -974,22 +975,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         }
         __syncwarp();
         if (!tc_wait_warp(C::CONV ? &conv_full[vbuf] : &kv_full[vbuf], vuse & 1, &s_abort, p.err)) { ok = false; break; }
-        if constexpr (WIN && !C::CONV) {
-          // value rows of a tile at an edge of what the item's rows see: P = 0 there must not meet a
-          // non-finite value
-          const int t = it.tile(j), p0 = it.pos(t), end = t < it.nct ? min(it.C, p0 + 128) : p0 + 128;
-          if ((p0 < it.low && end > it.sinks) || end < p0 + 128 || end - 1 > it.last()) {
-            uint8_t* vb = ring + vbuf * C::TILE_BYTES;
-            for (int c = lane; c < 128 * C::HALVES * 8; c += 32) {
-              const int rrow = c / (C::HALVES * 8), rest = c % (C::HALVES * 8);
-              if (!it.seen(p0 + rrow) || p0 + rrow >= end)
-                *reinterpret_cast<uint4*>(vb + (rest / 8) * C::HALF_BYTES + rrow * 128 + (rest % 8) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        } else if (!C::CONV && j == it.nct - 1 && (it.C & 127) != 0) {
+        if (!C::CONV && j == it.nct - 1 && (it.C & 127) != 0) {
           // keys past the context end in the last context tile: zero their V rows so that
           // P = 0 there cannot meet a non-finite value
           const int vr = it.C - j * 128;
@@ -1109,7 +1095,7 @@ static cudaError_t launch_attention_tc_impl(const AttnParams& p, const CUtensorM
                                             const CUtensorMap& tck, const CUtensorMap& tcv,
                                             const CUtensorMap& tqf, cudaStream_t stream, int* launches) {
   using C = TcCfg<D, KIND>;
-  const int slot = WIN               ? (KIND == kCtxFp8 ? kAttrWinAttn128Fp8 : (D == 64 ? kAttrWinAttn64 : kAttrWinAttn128))
+  const int slot = WIN               ? kAttrWinAttn128Fp8
                    : KIND == kCtxFp8 ? kAttrAttn128Fp8
                                    : (KIND == kCtxPool ? (D == 64 ? kAttrAttn64Scaled : kAttrAttn128Scaled)
                                                        : (D == 64 ? kAttrAttn64 : kAttrAttn128));
@@ -1126,11 +1112,8 @@ cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_q, const
                              const CUtensorMap& tm_cv, const CUtensorMap& tm_qf, int D, int ctx_kind,
                              cudaStream_t stream, int* launches) {
   if (p.window > 0) {
-    if (ctx_kind == kAttnCtxFp8 && D == 128)
-      return launch_attention_tc_impl<128, kCtxFp8, true>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
-    if (ctx_kind != kAttnCtxBf16) return cudaErrorInvalidValue;
-    return D == 64 ? launch_attention_tc_impl<64, kCtxBf16, true>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches)
-                   : launch_attention_tc_impl<128, kCtxBf16, true>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
+    if (ctx_kind != kAttnCtxFp8 || D != 128) return cudaErrorInvalidValue;
+    return launch_attention_tc_impl<128, kCtxFp8, true>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
   }
   if (ctx_kind == kAttnCtxFp8) {
     if (D != 128) return cudaErrorInvalidValue;

@@ -1,0 +1,774 @@
+// attn_window.cu — windowed extend_attn and varlen_prefill_attn on the tcgen05 tensor cores: new tokens against
+// their cached context and causally against themselves, where the row at position i sees the keys
+// j <= i with j > i - window (the window) or j < sinks (the first tokens, which stay visible).
+//
+// Mathematics: with s_j = log2(e) scale (q . k_j) over the keys that a row sees, m the running max of s,
+// P_j = 2^(s_j - m):  O = sum P_j v_j,  l = sum P_j,  out = O / l,  lse = (m + log2 l) ln 2. The max is lazy: it
+// follows a row's scores only when they pass it by more than 8, so P <= 2^8, and O and l are rescaled seldom.
+//
+// Work items. The rows of a request for one KV head are its (token, query head of the group) pairs, tokens
+// outermost (a box of Q is G heads x 128 / G tokens), and an item is 256 of them: two tiles of 128, one a
+// slot. So an item spans 256 / G tokens, and the keys that some row of it sees are sinks + window + 256 / G - 1.
+// (Items of 128 tokens and two heads, as without a window, span up to 128 more: a window of 128 then
+// takes twice the products, and every KV head's keys are read G / 2 times.) An item whose rows fit one tile deals
+// its key tiles to the slots in turn, both on the one Q tile, and the two states are merged at the end.
+//
+// Keys come in chunks of 16: a cache block, or 16 new tokens of the request. The chunks that an item walks are
+// the first `head` ones, which hold sinks, and those from the first row's window on (WnItem); eight make a key
+// tile, whatever they are, so sinks and window share a tile, and the last tile takes products of its chunks
+// alone. Tiles that every row sees whole skip the masks; in the others the value rows that no row sees are
+// zeroed (P = 0 there must not meet what is not finite).
+//
+// Roles (20 warps, one CTA per SM, persistent):
+//   warps 0-7, 8-15  softmax of slot 0, 1 and the epilogue. A row of S is shared by two threads, 64 columns
+//                    each (warps 4-7 and 12-15 have the upper halves), which agree on its maximum through shared
+//                    memory: a slot's softmax then fits the time in which the tensor core serves the other slot
+//   warp 16          TMA producer: claims the items, loads Q and the ring of K and V tiles
+//   warp 17          MMA issuer, one elected thread, waits included: S = Q K^T, O += P V (P from tensor memory)
+//   warps 18-19      zero value rows of tiles at an edge
+// Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; P_s (bf16 pairs) overwrites the first half of each half of S_s.
+#include <math_constants.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "softmax.cuh"
+#include "tc.cuh"
+
+namespace pkv {
+
+namespace {
+
+template <int D>
+struct WnCfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int HALF_BYTES = 128 * 128;            // 128 rows x 128 bytes
+  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;  // one 128-row tile of Q, K or V
+  static constexpr int NBUF = D == 128 ? 4 : 8;           // K/V ring: one tile per buffer
+  static constexpr int MAXR = kAttnSetChunk;              // requests of the set one launch holds
+  static constexpr int W_LOAD = 16, W_MMA = 17, W_FIX = 18, NFIX = 2;
+  static constexpr int THREADS = 640;
+  // 640 threads are launched at 96 registers; the softmax warps take 104, the others keep 64
+  static constexpr int REGS_SOFTMAX = 104, REGS_OTHER = 64;
+  static_assert(512 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * 96, "register split");
+  static constexpr int ITEM_RING = 4;                     // claimed items published to the other roles
+  static constexpr int ITEM_READERS = 16 + 1 + NFIX;
+  static constexpr int RING_OFF = 2 * TILE_BYTES;
+  static constexpr int REQ_OFF = RING_OFF + NBUF * TILE_BYTES;  // int4 {r, row0, q_len, C}
+  static constexpr int START_OFF = REQ_OFF + MAXR * 16;         // prefix of the items, by rank
+  static constexpr int PERM_OFF = START_OFF + (MAXR + 4) * 4;   // set positions by cost, heaviest first
+  static constexpr int ITEM_OFF = PERM_OFF + MAXR * 4;
+  static constexpr int PEER_OFF = ITEM_OFF + ITEM_RING * 64;    // [2][slot][half][128] fp32: what the halves of a row exchange
+  static constexpr int MERGE_OFF = PEER_OFF + 2 * 2 * 2 * 128 * 4;  // [slot][half][128] {m, l} of split items
+  static constexpr int BAR_OFF = MERGE_OFF + 2 * 2 * 128 * 8;
+};
+struct WnBars {
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[8], kv_empty[8], v_ready[8];
+  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t o_both;        // both slots' O of a split item
+  uint64_t item_full[4], item_empty[4];
+  uint64_t pair[2][4];    // the two warps that share a slot's 32 rows
+  uint64_t quad[4];       // the four warps that share a split item's 32 rows
+  uint64_t drained;       // the products in flight when a role gave up
+};
+template <int D>
+constexpr int wn_smem() { return 1024 + WnCfg<D>::BAR_OFF + static_cast<int>(sizeof(WnBars)); }
+
+__device__ __forceinline__ constexpr uint32_t wn_scol(int slot) { return slot * 128u; }
+__device__ __forceinline__ constexpr uint32_t wn_ocol(int slot) { return 256u + slot * 128u; }
+
+// A piece of work, published in shared memory by the producer. Chunks are numbered u = 0, 1, ..: the cache blocks
+// first (cb of them), then the new tokens sixteen by sixteen; the v-th chunk walked is u = v, or v + gap from
+// v = head on.
+struct WnItem {
+  int row0, q_len, C, kh;   // the request's first row of q, its new and its cached tokens; KV head
+  int tok0, ntok;           // the item's first new token and its tokens
+  int split;                // 1: one tile of rows, key tiles dealt to the slots in turn
+  int NV;                   // chunks walked (0: no more work)
+  int head, gap, cb;
+  int low;                  // the first key in the first row's window
+  int fs, f0, f1, vt;       // chunks 0 .. fs - 1 and f0 .. f1 - 1 of the walk, but for vt, every row sees whole
+  __device__ int tiles() const { return (NV + 7) >> 3; }
+  __device__ int last() const { return C + tok0 + ntok - 1; }  // position of the last row
+  __device__ int chunk(int v) const { return v < head ? v : v + gap; }
+  __device__ int pos(int u) const { return u < cb ? 16 * u : C + 16 * (u - cb); }
+  __device__ bool full(int j) const {
+    const int a = 8 * j, b = a + 8;
+    return b <= fs || (a >= f0 && b <= f1 && (vt < a || vt >= b));
+  }
+};
+static_assert(sizeof(WnItem) == 64, "ring entry");
+
+__device__ __forceinline__ int wn_count(const int4& q, int G) { return (q.z * G + 255) / 256; }
+// Keys an item of the request walks, about: the schedule's order.
+__device__ __forceinline__ int wn_cost(const AttnParams& p, const int4& q) {
+  return static_cast<int>(min(static_cast<int64_t>(q.z) + q.w, static_cast<int64_t>(p.window) + p.sinks));
+}
+
+// Item idx of a request {request id, first query row, q_len, cached tokens}.
+__device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, int idx) {
+  WnItem it;
+  it.row0 = q.y;
+  it.q_len = q.z;
+  it.C = q.w;
+  it.kh = idx % p.Hkv;
+  const int span = 256 / p.G;
+  it.tok0 = span * (wn_count(q, p.G) - 1 - idx / p.Hkv);  // later (heavier) rows of a request first
+  it.ntok = min(span, q.z - it.tok0);
+  it.split = it.ntok * p.G <= 128;
+  const int P0 = it.C + it.tok0, P1 = it.last();
+  it.cb = (it.C + 15) / 16;
+  it.low = P0 >= p.window ? P0 - p.window + 1 : 0;
+  const int sinks = min(p.sinks, P1 + 1);
+  it.head = sinks <= it.C ? (sinks + 15) / 16 : it.cb + (sinks - it.C + 15) / 16;
+  const int from = it.low < it.C ? it.low / 16 : it.cb + (it.low - it.C) / 16;
+  it.gap = max(from - it.head, 0);
+  it.NV = it.cb + (it.tok0 + it.ntok + 15) / 16 - it.gap;
+  // chunks that every row sees whole: those of sinks alone (of the cache), and those from the last row's window
+  // on up to the first row; the cache's last, partly filled one is none of them
+  it.fs = min(it.head, min(sinks, it.C) / 16);
+  const int all = P1 >= p.window ? P1 - p.window + 1 : 0;
+  it.f0 = (all <= it.C ? min((all + 15) / 16, it.cb) : it.cb + (all - it.C + 15) / 16) - it.gap;
+  it.f1 = it.cb + (it.tok0 + 1) / 16 - it.gap;
+  it.vt = (it.C & 15) == 0 ? -1 : it.cb - 1 < it.head ? it.cb - 1 : it.cb - 1 - it.gap;
+  if (it.vt < it.head && it.cb - 1 >= it.head) it.vt = -1;  // (it lies in the gap)
+  return it;
+}
+
+// Counters of claimed items and of finished CTAs, in the launch's slot (launch.h); its last CTA to finish sets
+// the slot back to zero. Without a slot the items are dealt statically, in snake order.
+__device__ unsigned int g_wn_next[kAttnSchedSlots];
+__device__ unsigned int g_wn_done[kAttnSchedSlots];
+
+// Bounded wait by one thread that also gives up as soon as another role has given up.
+__device__ __forceinline__ bool wn_wait1(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        flag_error(err, PKV_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+// The same answer in all lanes, so that warp-collective instructions after it see a whole warp.
+__device__ __forceinline__ bool wn_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  return __all_sync(0xffffffffu, wn_wait1(bar, parity, abort_flag, err));
+}
+
+// The low n bits (none, or all 32, beyond that range).
+__device__ __forceinline__ uint32_t wn_below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+
+// Which of the 32 keys of chunks v and v + 1 of the walk the row at position i sees, a bit each.
+__device__ __forceinline__ uint32_t wn_seen(const AttnParams& p, const WnItem& it, int v, int i) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int u = it.chunk(v + c), base = it.pos(u);
+    const int end = v + c < it.NV ? min(i + 1, u < it.cb ? it.C : INT_MAX) - base : 0;
+    const uint32_t b = wn_below(end) & (wn_below(p.sinks - base) | ~wn_below(i - p.window + 1 - base)) & 0xFFFFu;
+    bits |= b << (16 * c);
+  }
+  return bits;
+}
+
+template <int D>
+__global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
+    attn_window_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ck,
+                       const __grid_constant__ CUtensorMap tm_cv) {
+  using C = WnCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                  // [slot][half][128][128 B]
+  uint8_t* ring = smem + C::RING_OFF;  // [NBUF][half][128][128 B]
+  int4* s_req = reinterpret_cast<int4*>(smem + C::REQ_OFF);
+  int* s_start = reinterpret_cast<int*>(smem + C::START_OFF);
+  int* s_perm = reinterpret_cast<int*>(smem + C::PERM_OFF);
+  WnItem* s_item = reinterpret_cast<WnItem*>(smem + C::ITEM_OFF);
+  WnBars& bar = *reinterpret_cast<WnBars*>(smem + C::BAR_OFF);
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ int s_scan[C::MAXR / 32];
+
+  pdl_wait();
+  pdl_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // this launch's chunk of the request set
+  int begin = 0, n = p.max_reqs;
+  if (p.bounds != nullptr) {
+    begin = p.bounds[p.cls];
+    n = p.bounds[p.cls + 1] - begin;
+    if (n > p.max_reqs) {
+      if (blockIdx.x == 0 && tid == 0) flag_error(p.err, PKV_DEVERR_REQS);
+      n = p.max_reqs;
+    }
+    n = max(n, 0);
+  }
+  begin += p.set_offset;
+  n = max(0, min(n - p.set_offset, C::MAXR));
+
+  if (tid == 0) {
+    mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.q_empty, 1);
+    for (int b = 0; b < C::NBUF; ++b) {
+      mbar_init(&bar.kv_full[b], 1);
+      mbar_init(&bar.kv_empty[b], 1);
+      mbar_init(&bar.v_ready[b], C::NFIX);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 8);
+      mbar_init(&bar.o_final[i], 1);
+      for (int w = 0; w < 4; ++w) mbar_init(&bar.pair[i][w], 2);
+    }
+    for (int w = 0; w < 4; ++w) mbar_init(&bar.quad[w], 4);
+    for (int i = 0; i < C::ITEM_RING; ++i) {
+      mbar_init(&bar.item_full[i], 1);
+      mbar_init(&bar.item_empty[i], C::ITEM_READERS);
+    }
+    mbar_init(&bar.o_both, 1);
+    mbar_init(&bar.drained, 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::W_MMA) tc::tmem_alloc(&s_tmem, 512);
+
+  // the set's requests
+  if (tid < n) {
+    const int i = tid;
+    const int r = p.order ? p.order[begin + i] : begin + i;
+    int4 q = make_int4(0, 0, 0, 0);
+    if (r >= 0 && r < p.batch_reqs) {
+      const int q_len = max(0, p.cu_q[r + 1] - p.cu_q[r]);
+      int c = 0;
+      if (p.seq_lens != nullptr) {
+        c = max(0, p.seq_lens[r] - q_len);
+        if (c > static_cast<int64_t>(p.max_blocks) * 16) {
+          if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_LEN);
+          c = p.max_blocks * 16;
+        }
+      }
+      q = make_int4(r, p.cu_q[r], q_len, c);
+    } else if (blockIdx.x == 0) {
+      flag_error(p.err, PKV_DEVERR_REQS);
+    }
+    s_req[i] = q;
+  }
+  static_assert(C::MAXR <= C::THREADS, "a thread a request");
+  __syncthreads();
+  // rank by cost, heaviest first, ties in set order (a stable order every CTA computes alike)
+  if (tid < n) {
+    const int ki = wn_cost(p, s_req[tid]);
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const int kj = wn_cost(p, s_req[j]);
+      rank += (kj > ki || (kj == ki && j < tid)) ? 1 : 0;
+    }
+    s_perm[rank] = tid;
+  }
+  __syncthreads();
+  // exclusive prefix of the requests' items in that order
+  {
+    const int t = tid < n ? p.Hkv * wn_count(s_req[s_perm[tid]], p.G) : 0;
+    int x = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31 && warp < C::MAXR / 32) s_scan[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < C::MAXR / 32; ++w) {
+      if (w < warp) before += s_scan[w];
+      all += s_scan[w];
+    }
+    if (tid < n) s_start[tid] = before + x - t;
+    if (tid == 0) s_start[C::MAXR] = all;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  const int W = s_start[C::MAXR];
+
+  // The k-th item (null: no more, or a wait gave up). A reader frees it when it is through.
+  auto take = [&](uint32_t k) -> const WnItem* {
+    const uint32_t e = k % C::ITEM_RING;
+    if (!wn_wait(&bar.item_full[e], (k / C::ITEM_RING) & 1, &s_abort, p.err)) return nullptr;
+    return s_item[e].NV > 0 ? s_item + e : nullptr;
+  };
+  auto release = [&](uint32_t k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.item_empty[k % C::ITEM_RING]);
+  };
+
+  if (warp < 16) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+    // ======================= softmax =======================
+    const int slot = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+    const int t = quad * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t srow = tmem + lane_off + wn_scol(slot) + half * 64;
+    float* peer = reinterpret_cast<float*>(smem + C::PEER_OFF) + slot * 256;  // [parity][slot][half][128]
+    uint32_t sc = 0, oc = 0, xc = 0, bc = 0, qc = 0;  // phases of s_full, o_final, pair, o_both, quad
+    // One value of each row to its other half, and that half's.
+    auto exchange = [&](float mine, float& other) -> bool {
+      float* x = peer + (xc & 1) * 512;
+      x[half * 128 + t] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.pair[slot][quad]);
+      const bool ok = wn_wait(&bar.pair[slot][quad], xc & 1, &s_abort, p.err);
+      ++xc;
+      other = x[(half ^ 1) * 128 + t];
+      return ok;
+    };
+    for (uint32_t k = 0;; ++k) {
+      const WnItem* taken = take(k);
+      if (taken == nullptr) break;
+      float m = -CUDART_INF_F, l = 0.f;
+      bool ok = true;
+      const int split = taken->split;
+      bool live;  // whether the warp has rows of the item
+      {
+        const int tok = taken->tok0 + ((split ? 0 : slot * 128) + t) / p.G;
+        live = __any_sync(0xffffffffu, tok < taken->tok0 + taken->ntok);
+        const int at = taken->C + tok, nt = taken->tiles();
+        for (int j = split ? slot : 0; j < nt; j += 1 + split) {
+          if (!wn_wait(&bar.s_full[slot], sc & 1, &s_abort, p.err)) { ok = false; break; }
+          ++sc;
+          tc::fence_after_sync();
+          if (live) {
+            // this half's 64 columns of S
+            uint32_t v[2][32];
+            tc::ld32(srow, v[0]);
+            tc::ld32(srow + 32, v[1]);
+            tc::wait_ld();
+            tc::touch32(v[0]);  // no use of v may move above the wait
+            tc::touch32(v[1]);
+            if (!taken->full(j)) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t seen = wn_seen(p, *taken, 8 * j + 4 * half + 2 * c, at);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[c][e] = (seen >> e) & 1u ? v[c][e] : 0xFF800000u;
+              }
+            }
+            // row max of the raw scores (the scale is positive, so it commutes with max)
+            float mx = -CUDART_INF_F;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) mx = sm::max3(mx, __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+            float other;
+            if (!exchange(mx, other)) { ok = false; break; }
+            mx = fmaxf(mx, other) * p.scale_log2;  // -inf stays -inf
+            float alpha = 1.f;
+            if (mx > m + 8.f || m == -CUDART_INF_F) {  // lazy rescale: only when the max really grows
+              const float m_new = fmaxf(m, mx);
+              if (m_new != -CUDART_INF_F) {
+                alpha = (m == -CUDART_INF_F) ? 0.f : ex2_approx(m - m_new);
+                m = m_new;
+              }
+            }
+            // P = 2^(s * scale_log2 - m), packed to bf16 pairs over the first half of these columns
+            const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+            const uint64_t sc2 = sm::f2(p.scale_log2, p.scale_log2), nm2 = sm::f2(neg_m, neg_m);
+            uint64_t rs2 = sm::f2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
+                float x0, x1;
+                sm::unf2(x, x0, x1);
+                const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
+                rs2 = sm::add2(rs2, pp);
+                pk[e / 2] = sm::bf16x2(pp);
+              }
+              tc::st16(srow + c * 16, pk);
+            }
+            float r0, r1;
+            sm::unf2(rs2, r0, r1);
+            l = l * alpha + (r0 + r1);
+            // The rescale decision is per row, but tcgen05.ld/st are warp-collective: the whole warp takes the
+            // branch when any of its rows needs it (alpha is 1 for the others). Each half has its part of O,
+            // which is quiescent: the previous P V product finished before S(j) did.
+            if (j > (split ? slot : 0) && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c) {
+                const uint32_t a = tmem + lane_off + wn_ocol(slot) + half * (D / 2) + c * 32;
+                uint32_t o[32];
+                tc::ld32(a, o);
+                tc::wait_ld();
+                tc::touch32(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tc::st32(a, o);
+              }
+            }
+            tc::wait_st();
+          }
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_full[slot]);
+        }
+      }
+      if (!ok) break;
+      // ---- epilogue (the item read again, so that its fields need not stay in registers above) ----
+      const WnItem it = s_item[k % C::ITEM_RING];
+      release(k);
+      const int tok = it.tok0 + ((split ? 0 : slot * 128) + t) / p.G;
+      const int64_t row = static_cast<int64_t>(it.row0) + tok;
+      const bool write = tok < it.tok0 + it.ntok && row < p.num_tokens;
+      const int64_t flat = row * p.Hq + it.kh * p.G + t % p.G;  // (128 is a multiple of G)
+      if (!split) {
+        if (!wn_wait(&bar.o_final[slot], oc & 1, &s_abort, p.err)) break;
+        ++oc;
+        if (!live) continue;
+        float other;
+        if (!exchange(l, other)) break;
+        tc::fence_after_sync();
+        const float sum = half ? other + l : l + other;  // (the same order in both halves)
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t o[32];
+          tc::ld32(tmem + lane_off + wn_ocol(slot) + half * (D / 2) + c * 32, o);
+          tc::wait_ld();
+          tc::touch32(o);
+          if (write) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + flat * D + half * (D / 2) + c * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * q + e]) * inv;
+              dst[q] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            }
+          }
+        }
+        if (write && half == 0 && p.lse)
+          p.lse[flat] = sum > 0.f ? (m + __log2f(sum)) * 0.69314718055994531f : -CUDART_INF_F;
+        tc::fence_before_sync();
+        continue;
+      }
+      // a split item: the slots' states of the same rows, merged by all four warps of the rows, a quarter of the
+      // dims each
+      float2* mrg = reinterpret_cast<float2*>(smem + C::MERGE_OFF);
+      mrg[(slot * 2 + half) * 128 + t] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.quad[quad]);
+      if (!wn_wait(&bar.quad[quad], qc & 1, &s_abort, p.err)) break;
+      ++qc;
+      if (!wn_wait(&bar.o_both, bc & 1, &s_abort, p.err)) break;
+      ++bc;
+      tc::fence_after_sync();
+      if (live) {
+        const float2 a0 = mrg[t], a1 = mrg[128 + t], b0 = mrg[256 + t], b1 = mrg[384 + t];
+        const float l0 = a0.y + a1.y, l1 = b0.y + b1.y, mm = fmaxf(a0.x, b0.x);
+        // (a slot without a key for the row has l = 0; what its O holds is not read as a number)
+        const float w0 = l0 == 0.f ? 0.f : ex2_approx(a0.x - mm), w1 = l1 == 0.f ? 0.f : ex2_approx(b0.x - mm);
+        const float sum = l0 * w0 + l1 * w1, inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int col = (slot * 2 + half) * (D / 4);
+        uint32_t o0[D / 4], o1[D / 4];
+        tc::ld_cols(tmem + lane_off + wn_ocol(0) + col, o0);
+        tc::ld_cols(tmem + lane_off + wn_ocol(1) + col, o1);
+        tc::wait_ld();
+        tc::touch_cols(o0);
+        tc::touch_cols(o1);
+        if (write) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + flat * D + col);
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              x[e] = w0 == 0.f ? 0.f : __uint_as_float(o0[8 * q + e]) * (w0 * inv);
+              x[e] = w1 == 0.f ? x[e] : fmaf(__uint_as_float(o1[8 * q + e]), w1 * inv, x[e]);
+            }
+            dst[q] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+          }
+          if (slot + half == 0 && p.lse)
+            p.lse[flat] = sum > 0.f ? (mm + __log2f(sum)) * 0.69314718055994531f : -CUDART_INF_F;
+        }
+      }
+      tc::fence_before_sync();
+      // all four have read O and the states before any lets the next item's products at them
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.quad[quad]);
+      if (!wn_wait(&bar.quad[quad], qc & 1, &s_abort, p.err)) break;
+      ++qc;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+    if (warp == C::W_LOAD) {
+      // ======================= TMA producer =======================
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        if (p.seq_lens != nullptr) {
+          tma_prefetch_desc(&tm_ck);
+          tma_prefetch_desc(&tm_cv);
+        }
+      }
+      uint32_t kvc = 0, qn = 0;
+      bool ok = true;
+      int w_static = blockIdx.x, odd = 0;
+      for (uint32_t k = 0; ok; ++k) {
+        const uint32_t e = k % C::ITEM_RING;
+        if (k >= C::ITEM_RING && !wn_wait(&bar.item_empty[e], (k / C::ITEM_RING - 1) & 1, &s_abort, p.err)) break;
+        int w = 0;
+        if (p.sched_slot >= 0) {
+          if (lane == 0) w = static_cast<int>(min(atomicAdd(&g_wn_next[p.sched_slot], 1u), static_cast<unsigned>(W)));
+          w = __shfl_sync(0xffffffffu, w, 0);
+        } else {
+          w = w_static;
+          w_static += odd ? 2 * blockIdx.x + 1 : 2 * (gridDim.x - blockIdx.x) - 1;
+          odd ^= 1;
+        }
+        WnItem it;
+        int r = 0;
+        it.NV = 0;
+        if (w < W) {
+          int lo = 0, hi = n - 1;  // the last rank whose prefix is at most w
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_start[mid] <= w) lo = mid; else hi = mid - 1;
+          }
+          const int4 q = s_req[s_perm[lo]];
+          r = q.x;
+          it = wn_item(p, q, w - s_start[lo]);
+        }
+        if (lane == 0) {
+          s_item[e] = it;
+          mbar_arrive(&bar.item_full[e]);
+        }
+        __syncwarp();
+        if (it.NV == 0) break;
+        // the Q buffer is free once the previous item's S products are done
+        if (k > 0 && !wn_wait(&bar.q_empty, (k - 1) & 1, &s_abort, p.err)) break;
+        if (tc::elect()) {
+          const int tiles = it.split ? 1 : 2;
+          mbar_arrive_expect_tx(&bar.q_full, tiles * C::TILE_BYTES);
+          for (int s = 0; s < tiles; ++s)
+#pragma unroll
+            for (int hf = 0; hf < C::HALVES; ++hf)
+              tma_load_4d(sQ + s * C::TILE_BYTES + hf * C::HALF_BYTES, &tm_q, &bar.q_full, 0, hf, it.kh * p.G,
+                          it.row0 + it.tok0 + s * (128 / p.G));
+        }
+        __syncwarp();
+        ++qn;
+        const int32_t* table = p.block_tables + static_cast<int64_t>(r) * p.max_blocks;
+        const int nt = it.tiles();
+        // lanes 0 .. 7: where chunk `lane` of tile j lies: its cache block, or ~ its first row of new tokens
+        auto look_up = [&](int j) {
+          int at = 0;
+          const int v = 8 * j + lane;
+          if (lane < 8 && v < it.NV) {
+            const int u = it.chunk(v);
+            if (u < it.cb) {
+              at = table[u];
+              if (at < 0 || at >= p.num_blocks) {
+                flag_error(p.err, PKV_DEVERR_BLOCK);
+                at = 0;
+              }
+            } else {
+              at = ~(it.row0 + 16 * (u - it.cb));
+            }
+          }
+          return at;
+        };
+        int next = look_up(0);
+        for (int j = 0; j < nt && ok; ++j) {
+          const int at = next, chunks = min(8, it.NV - 8 * j);
+          if (j + 1 < nt) next = look_up(j + 1);
+          for (int sel = 0; sel < 2; ++sel, ++kvc) {
+            const int b = kvc % C::NBUF;
+            const uint32_t use = kvc / C::NBUF;
+            if (use > 0 && !wn_wait(&bar.kv_empty[b], (use - 1) & 1, &s_abort, p.err)) { ok = false; break; }
+            uint8_t* dst = ring + b * C::TILE_BYTES;
+            if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[b], chunks * 16 * D * 2);
+            __syncwarp();
+            if (lane < chunks) {
+#pragma unroll
+              for (int hf = 0; hf < C::HALVES; ++hf) {
+                uint8_t* to = dst + hf * C::HALF_BYTES + lane * 2048;
+                if (at >= 0)
+                  tma_load_4d(to, sel ? &tm_cv : &tm_ck, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, 0, at);
+                else
+                  tma_load_3d(to, sel ? &tm_v : &tm_k, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, ~at);
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (!ok || *static_cast<volatile int*>(&s_abort)) {
+        // a wait gave up: the loads in flight are waited for (bounded), so that none lands after the CTA is gone
+        for (uint32_t i = kvc > C::NBUF ? kvc - C::NBUF : 0; i < kvc; ++i)
+          mbar_wait(&bar.kv_full[i % C::NBUF], (i / C::NBUF) & 1, p.err);
+        if (qn > 0) mbar_wait(&bar.q_full, (qn - 1) & 1, p.err);
+      }
+    } else if (warp == C::W_MMA) {
+      // ======================= MMA issuer =======================
+      if (tc::elect()) {
+        constexpr uint32_t kQk = tc::idesc_bf16(128, 0, 0, 0), kPv = tc::idesc_bf16(128, D, 0, 1);
+        uint32_t kvc = 0, pc0 = 0, pc1 = 0;
+        auto ring_at = [&](int b) { return smem_u32(ring + b * C::TILE_BYTES); };
+        auto qk = [&](int slot, int qtile, int kbuf, int chunks) {
+          const uint32_t qa = smem_u32(sQ + qtile * C::TILE_BYTES), kb = ring_at(kbuf);
+          const uint32_t idesc = kQk | static_cast<uint32_t>(2 * chunks) << 17;  // N = 16 chunks
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = (s / 4) * C::HALF_BYTES + (s % 4) * 32;
+            tc::mma_ss(tmem + wn_scol(slot), tc::smem_desc(qa + off, 16, 1024), tc::smem_desc(kb + off, 16, 1024), idesc,
+                       s > 0);
+          }
+          tc::commit(&bar.s_full[slot]);
+        };
+        auto pv = [&](int slot, int vbuf, int chunks, bool acc) {
+          const uint32_t vb = ring_at(vbuf);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)  // P of chunks 4 .. 7 lies in the other half's columns
+            if (c < chunks)
+              tc::mma_ts(tmem + wn_ocol(slot), tmem + wn_scol(slot) + (c >> 2) * 64 + (c & 3) * 8,
+                         tc::smem_desc(vb + c * 2048, C::HALF_BYTES, 1024), kPv, (acc || c > 0) ? 1u : 0u);
+        };
+        bool ok = true;
+        auto wait = [&](uint64_t* b, uint32_t parity) {
+          if (!wn_wait1(b, parity, &s_abort, p.err)) return false;
+          tc::fence_after_sync();
+          return true;
+        };
+        for (uint32_t k = 0; ok; ++k) {
+          const uint32_t e = k % C::ITEM_RING;
+          if (!wait(&bar.item_full[e], (k / C::ITEM_RING) & 1)) { ok = false; break; }
+          const int NV = *static_cast<volatile int*>(&s_item[e].NV), split = *static_cast<volatile int*>(&s_item[e].split);
+          mbar_arrive(&bar.item_empty[e]);
+          if (NV == 0) break;
+          const int nt = (NV + 7) >> 3;
+          if (!wait(&bar.q_full, k & 1)) { ok = false; break; }
+          int vprev = -1;  // V buffer of tile j - 1
+          for (int j = 0; j <= nt && ok; ++j) {
+            // S of tile j; then O += P V of tile j - 1 (of slot 1; in a split item of the tile's slot), and of
+            // tile j of slot 0
+            const int kb = kvc % C::NBUF, vb = (kvc + 1) % C::NBUF, chunks = min(8, NV - 8 * j);
+            const uint32_t kuse = kvc / C::NBUF, vuse = (kvc + 1) / C::NBUF;
+            const int s0 = split ? j & 1 : 0;
+            if (j < nt) {
+              if (!(ok = wait(&bar.kv_full[kb], kuse & 1))) break;
+              qk(s0, 0, kb, chunks);
+            }
+            if (j > 0) {
+              // (V of tile j - 1 was waited for by slot 0's product, or is now)
+              const int s = split ? (j - 1) & 1 : 1;
+              if (split && !(ok = wait(&bar.v_ready[vprev], ((kvc - 1) / C::NBUF) & 1))) break;
+              if (!(ok = wait(&bar.p_full[s], (s ? pc1 : pc0) & 1))) break;
+              if (s) ++pc1; else ++pc0;
+              pv(s, vprev, min(8, NV - 8 * (j - 1)), split ? j > 2 : j > 1);
+              tc::commit(&bar.kv_empty[vprev]);
+              if (j == nt) tc::commit(split ? &bar.o_both : &bar.o_final[1]);
+            }
+            if (j == nt) break;
+            if (!split) qk(1, 1, kb, chunks);
+            tc::commit(&bar.kv_empty[kb]);
+            if (j == nt - 1) tc::commit(&bar.q_empty);
+            if (!split) {
+              if (!(ok = wait(&bar.v_ready[vb], vuse & 1))) break;
+              if (!(ok = wait(&bar.p_full[0], pc0 & 1))) break;
+              ++pc0;
+              pv(0, vb, chunks, j > 0);
+              if (j == nt - 1) tc::commit(&bar.o_final[0]);
+            }
+            vprev = vb;
+            kvc += 2;
+          }
+        }
+        if (!ok) {  // the products in flight are waited for (bounded) before tensor memory is freed
+          tc::commit(&bar.drained);
+          mbar_wait(&bar.drained, 0, p.err);
+        }
+      }
+      __syncwarp();
+    } else {
+      // ======================= value rows that no row sees =======================
+      const int ft = tid - C::W_FIX * 32;
+      const uint32_t ring_base = smem_u32(ring);
+      uint32_t kvc = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok; ++k) {
+        const WnItem* taken = take(k);
+        if (taken == nullptr) break;
+        const WnItem it = *taken;
+        release(k);
+        const int nt = it.tiles(), last = it.last(), sinks = p.sinks;
+        for (int j = 0; j < nt; ++j, kvc += 2) {
+          const int b = (kvc + 1) % C::NBUF;
+          if (!wn_wait(&bar.kv_full[b], ((kvc + 1) / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
+          if (!it.full(j)) {
+            const uint32_t tile = ring_base + b * C::TILE_BYTES;
+#pragma unroll 1
+            for (int R = ft; R < 128; R += 32 * C::NFIX) {
+              const int v = 8 * j + R / 16;
+              if (v >= it.NV) continue;  // (no product takes it)
+              const int u = it.chunk(v), key = it.pos(u) + R % 16;
+              const bool seen = (key >= it.low || key < sinks) && key <= last && (u >= it.cb || key < it.C);
+              if (seen) continue;
+#pragma unroll
+              for (int c = 0; c < C::HALVES * 8; ++c)
+                st_shared_v4(tile + (c / 8) * C::HALF_BYTES + R * 128 + (c % 8) * 16, make_uint4(0, 0, 0, 0));
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.v_ready[b]);
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == C::W_MMA) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+  // every role of this CTA is done, its producer's claims included: the launch's last CTA to get here sets the
+  // slot back to zero for the next launch that uses it
+  if (tid == 0 && p.sched_slot >= 0) {
+    __threadfence();
+    if (atomicAdd(&g_wn_done[p.sched_slot], 1u) == gridDim.x - 1) {
+      atomicExch(&g_wn_next[p.sched_slot], 0u);
+      atomicExch(&g_wn_done[p.sched_slot], 0u);
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream) {
+  const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attn_window_kernel<D>), wn_smem<D>(),
+                                           D == 64 ? kAttrWinAttn64 : kAttrWinAttn128);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_window_kernel<D>, dim3(num_sms()), dim3(WnCfg<D>::THREADS), wn_smem<D>(), stream, p, tq, tk, tv, tck,
+                    tcv);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_window(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& tck, const CUtensorMap& tcv, int D, cudaStream_t stream, int* launches) {
+  *launches += 1;
+  return D == 64 ? launch<64>(p, tq, tk, tv, tck, tcv, stream) : launch<128>(p, tq, tk, tv, tck, tcv, stream);
+}
+
+}  // namespace pkv
