@@ -2,9 +2,11 @@
 // their cached context and causally against themselves, where the row at position i sees the keys
 // j <= i with j > i - window (the window) or j < sinks (the first tokens, which stay visible).
 //
-// Mathematics: with s_j = log2(e) scale (q . k_j) over the keys that a row sees, m the running max of s,
-// P_j = 2^(s_j - m):  O = sum P_j v_j,  l = sum P_j,  out = O / l,  lse = (m + log2 l) ln 2. The max is lazy: it
-// follows a row's scores only when they pass it by more than 8, so P <= 2^8, and O and l are rescaled seldom.
+// Mathematics: with s_j = log2(e) scale (q . k_j) over the keys that a row sees and m any number of their size,
+// P_j = 2^(s_j - m):  O = sum P_j v_j,  l = sum P_j,  out = O / l,  lse = (m + log2 l) ln 2. m is the max of the
+// scores when the row first meets one, and follows them only when they pass it by more than kLazy = 20: P and O
+// keep the precision of their types whatever the power of two in front, P <= 2^20 leaves values up to 2^100
+// room, and O is rescaled in nearly no tile.
 //
 // Work items. The rows of a request for one KV head are its (token, query head of the group) pairs, tokens
 // outermost (a box of Q is G heads x 128 / G tokens), and an item is 256 of them: two tiles of 128, one a
@@ -14,19 +16,22 @@
 // its key tiles to the slots in turn, both on the one Q tile, and the two states are merged at the end.
 //
 // Keys come in chunks of 16: a cache block, or 16 new tokens of the request. The chunks that an item walks are
-// the first `head` ones, which hold sinks, and those from the first row's window on (WnItem); eight make a key
+// the first `head` ones, which hold sinks, and those from the first row's window on (WnItem); four make a key
 // tile, whatever they are, so sinks and window share a tile, and the last tile takes products of its chunks
 // alone. Tiles that every row sees whole skip the masks; in the others the value rows that no row sees are
 // zeroed (P = 0 there must not meet what is not finite).
 //
-// Roles (20 warps, one CTA per SM, persistent):
-//   warps 0-7, 8-15  softmax of slot 0, 1 and the epilogue. A row of S is shared by two threads, 64 columns
-//                    each (warps 4-7 and 12-15 have the upper halves), which agree on its maximum through shared
-//                    memory: a slot's softmax then fits the time in which the tensor core serves the other slot
-//   warp 16          TMA producer: claims the items, loads Q and the ring of K and V tiles
-//   warp 17          MMA issuer, one elected thread, waits included: S = Q K^T, O += P V (P from tensor memory)
-//   warps 18-19      zero value rows of tiles at an edge
-// Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1; P_s (bf16 pairs) overwrites the first half of each half of S_s.
+// Key tiles of 64, so that tensor memory holds two S of each slot beside the two O of 128 columns: S of the next tile
+// is there when the softmax of this one is done, and the chain S, softmax, P V, S of one buffer (with one S of
+// 128 keys a slot: 3900 clocks a 128 keys, of which the tensor core worked 2080) bounds nothing.
+//
+// Roles (12 warps, one CTA per SM, persistent):
+//   warps 0-3, 4-7  softmax of slot 0, 1 (thread t owns row t = TMEM lane t) and the epilogue
+//   warp 8          TMA producer: claims the items, loads Q and the ring of K and V tiles
+//   warp 9          MMA issuer, one elected thread, waits included: S = Q K^T, O += P V (P from tensor memory)
+//   warps 10-11     zero value rows of tiles at an edge
+// Tensor memory (512 columns): S_0 (two buffers) | S_1 (two buffers) | O_0 | O_1; P_s (bf16 pairs) overwrites the
+// first half of its S.
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -40,41 +45,40 @@ namespace {
 
 template <int D>
 struct WnCfg {
+  static constexpr int BN = 64, CHUNKS = BN / 16;         // keys of a tile
   static constexpr int HALVES = D / 64;
-  static constexpr int HALF_BYTES = 128 * 128;            // 128 rows x 128 bytes
-  static constexpr int TILE_BYTES = HALVES * HALF_BYTES;  // one 128-row tile of Q, K or V
-  static constexpr int NBUF = D == 128 ? 4 : 8;           // K/V ring: one tile per buffer
+  static constexpr int Q_HALF = 128 * 128;                // 128 rows x 128 bytes
+  static constexpr int Q_BYTES = HALVES * Q_HALF;         // one 128-row tile of Q
+  static constexpr int KV_HALF = BN * 128;
+  static constexpr int KV_BYTES = HALVES * KV_HALF;       // one tile of K or V
+  static constexpr int NBUF = D == 128 ? 8 : 16;          // K/V ring: one tile per buffer
   static constexpr int MAXR = kAttnSetChunk;              // requests of the set one launch holds
-  static constexpr int W_LOAD = 16, W_MMA = 17, W_FIX = 18, NFIX = 2;
-  static constexpr int THREADS = 640;
-  // 640 threads are launched at 96 registers; the softmax warps take 104, the others keep 64
-  static constexpr int REGS_SOFTMAX = 104, REGS_OTHER = 64;
-  static_assert(512 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * 96, "register split");
+  static constexpr int W_LOAD = 8, W_MMA = 9, W_FIX = 10, NFIX = 2;
+  static constexpr int THREADS = 384;
   static constexpr int ITEM_RING = 4;                     // claimed items published to the other roles
-  static constexpr int ITEM_READERS = 16 + 1 + NFIX;
-  static constexpr int RING_OFF = 2 * TILE_BYTES;
-  static constexpr int REQ_OFF = RING_OFF + NBUF * TILE_BYTES;  // int4 {r, row0, q_len, C}
+  static constexpr int ITEM_READERS = 8 + 1 + NFIX;
+  static constexpr int RING_OFF = 2 * Q_BYTES;
+  static constexpr int REQ_OFF = RING_OFF + NBUF * KV_BYTES;    // int4 {r, row0, q_len, C}
   static constexpr int START_OFF = REQ_OFF + MAXR * 16;         // prefix of the items, by rank
   static constexpr int PERM_OFF = START_OFF + (MAXR + 4) * 4;   // set positions by cost, heaviest first
   static constexpr int ITEM_OFF = PERM_OFF + MAXR * 4;
-  static constexpr int PEER_OFF = ITEM_OFF + ITEM_RING * 64;    // [2][slot][half][128] fp32: what the halves of a row exchange
-  static constexpr int MERGE_OFF = PEER_OFF + 2 * 2 * 2 * 128 * 4;  // [slot][half][128] {m, l} of split items
-  static constexpr int BAR_OFF = MERGE_OFF + 2 * 2 * 128 * 8;
+  static constexpr int MERGE_OFF = ITEM_OFF + ITEM_RING * 64;   // [slot][128] {m, l} of split items
+  static constexpr int BAR_OFF = MERGE_OFF + 2 * 128 * 8;
 };
 struct WnBars {
   uint64_t q_full, q_empty;
-  uint64_t kv_full[8], kv_empty[8], v_ready[8];
-  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t kv_full[16], kv_empty[16], v_ready[16];
+  uint64_t s_full[2][2], p_full[2][2];  // by slot and buffer
+  uint64_t pv_done[2], o_final[2];
   uint64_t o_both;        // both slots' O of a split item
   uint64_t item_full[4], item_empty[4];
-  uint64_t pair[2][4];    // the two warps that share a slot's 32 rows
-  uint64_t quad[4];       // the four warps that share a split item's 32 rows
+  uint64_t rows[4];       // the two warps that share a split item's 32 rows
   uint64_t drained;       // the products in flight when a role gave up
 };
 template <int D>
 constexpr int wn_smem() { return 1024 + WnCfg<D>::BAR_OFF + static_cast<int>(sizeof(WnBars)); }
 
-__device__ __forceinline__ constexpr uint32_t wn_scol(int slot) { return slot * 128u; }
+__device__ __forceinline__ constexpr uint32_t wn_scol(int slot, int b) { return slot * 128u + b * 64u; }
 __device__ __forceinline__ constexpr uint32_t wn_ocol(int slot) { return 256u + slot * 128u; }
 
 // A piece of work, published in shared memory by the producer. Chunks are numbered u = 0, 1, ..: the cache blocks
@@ -88,12 +92,12 @@ struct WnItem {
   int head, gap, cb;
   int low;                  // the first key in the first row's window
   int fs, f0, f1, vt;       // chunks 0 .. fs - 1 and f0 .. f1 - 1 of the walk, but for vt, every row sees whole
-  __device__ int tiles() const { return (NV + 7) >> 3; }
+  __device__ int tiles() const { return (NV + 3) >> 2; }
   __device__ int last() const { return C + tok0 + ntok - 1; }  // position of the last row
   __device__ int chunk(int v) const { return v < head ? v : v + gap; }
   __device__ int pos(int u) const { return u < cb ? 16 * u : C + 16 * (u - cb); }
   __device__ bool full(int j) const {
-    const int a = 8 * j, b = a + 8;
+    const int a = 4 * j, b = a + 4;
     return b <= fs || (a >= f0 && b <= f1 && (vt < a || vt >= b));
   }
 };
@@ -134,6 +138,9 @@ __device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, in
   if (it.vt < it.head && it.cb - 1 >= it.head) it.vt = -1;  // (it lies in the gap)
   return it;
 }
+
+// How far (in powers of two) scores may pass a row's m before it follows them.
+constexpr float kLazy = 20.f;
 
 // Counters of claimed items and of finished CTAs, in the launch's slot (launch.h); its last CTA to finish sets
 // the slot back to zero. Without a slot the items are dealt statically, in snake order.
@@ -180,13 +187,14 @@ __device__ __forceinline__ uint32_t wn_seen(const AttnParams& p, const WnItem& i
 template <int D>
 __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
     attn_window_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ck,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k64,
+                       const __grid_constant__ CUtensorMap tm_v64, const __grid_constant__ CUtensorMap tm_ck,
                        const __grid_constant__ CUtensorMap tm_cv) {
   using C = WnCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                  // [slot][half][128][128 B]
-  uint8_t* ring = smem + C::RING_OFF;  // [NBUF][half][128][128 B]
+  uint8_t* ring = smem + C::RING_OFF;  // [NBUF][half][64][128 B]
   int4* s_req = reinterpret_cast<int4*>(smem + C::REQ_OFF);
   int* s_start = reinterpret_cast<int*>(smem + C::START_OFF);
   int* s_perm = reinterpret_cast<int*>(smem + C::PERM_OFF);
@@ -223,12 +231,14 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       mbar_init(&bar.v_ready[b], C::NFIX);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 8);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bar.s_full[i][b], 1);
+        mbar_init(&bar.p_full[i][b], 4);
+      }
+      mbar_init(&bar.pv_done[i], 1);
       mbar_init(&bar.o_final[i], 1);
-      for (int w = 0; w < 4; ++w) mbar_init(&bar.pair[i][w], 2);
     }
-    for (int w = 0; w < 4; ++w) mbar_init(&bar.quad[w], 4);
+    for (int w = 0; w < 4; ++w) mbar_init(&bar.rows[w], 2);
     for (int i = 0; i < C::ITEM_RING; ++i) {
       mbar_init(&bar.item_full[i], 1);
       mbar_init(&bar.item_empty[i], C::ITEM_READERS);
@@ -310,102 +320,67 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
     if (lane == 0) mbar_arrive(&bar.item_empty[k % C::ITEM_RING]);
   };
 
-  if (warp < 16) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+  if (warp < 8) {
     // ======================= softmax =======================
-    const int slot = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
-    const int t = quad * 32 + lane;  // row of the tile = TMEM lane
-    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t srow = tmem + lane_off + wn_scol(slot) + half * 64;
-    float* peer = reinterpret_cast<float*>(smem + C::PEER_OFF) + slot * 256;  // [parity][slot][half][128]
-    uint32_t sc = 0, oc = 0, xc = 0, bc = 0, qc = 0;  // phases of s_full, o_final, pair, o_both, quad
-    // One value of each row to its other half, and that half's.
-    auto exchange = [&](float mine, float& other) -> bool {
-      float* x = peer + (xc & 1) * 512;
-      x[half * 128 + t] = mine;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.pair[slot][quad]);
-      const bool ok = wn_wait(&bar.pair[slot][quad], xc & 1, &s_abort, p.err);
-      ++xc;
-      other = x[(half ^ 1) * 128 + t];
-      return ok;
-    };
+    const int slot = warp >> 2, quad = warp & 3;
+    const int t = tid & 127;  // row of the tile = TMEM lane
+    const uint32_t lane_at = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint64_t sc2 = sm::f2(p.scale_log2, p.scale_log2);
+    uint32_t sc = 0, oc = 0, bc = 0, rc = 0;  // phases: S of this slot, o_final, o_both, rows
     for (uint32_t k = 0;; ++k) {
       const WnItem* taken = take(k);
       if (taken == nullptr) break;
+      const WnItem it = *taken;
+      release(k);
       float m = -CUDART_INF_F, l = 0.f;
       bool ok = true;
-      const int split = taken->split;
-      bool live;  // whether the warp has rows of the item
-      {
-        const int tok = taken->tok0 + ((split ? 0 : slot * 128) + t) / p.G;
-        live = __any_sync(0xffffffffu, tok < taken->tok0 + taken->ntok);
-        const int at = taken->C + tok, nt = taken->tiles();
-        for (int j = split ? slot : 0; j < nt; j += 1 + split) {
-          if (!wn_wait(&bar.s_full[slot], sc & 1, &s_abort, p.err)) { ok = false; break; }
-          ++sc;
-          tc::fence_after_sync();
-          if (live) {
-            // this half's 64 columns of S
-            uint32_t v[2][32];
-            tc::ld32(srow, v[0]);
-            tc::ld32(srow + 32, v[1]);
-            tc::wait_ld();
-            tc::touch32(v[0]);  // no use of v may move above the wait
-            tc::touch32(v[1]);
-            if (!taken->full(j)) {
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint32_t seen = wn_seen(p, *taken, 8 * j + 4 * half + 2 * c, at);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[c][e] = (seen >> e) & 1u ? v[c][e] : 0xFF800000u;
-              }
-            }
-            // row max of the raw scores (the scale is positive, so it commutes with max)
-            float mx = -CUDART_INF_F;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) mx = sm::max3(mx, __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-            float other;
-            if (!exchange(mx, other)) { ok = false; break; }
-            mx = fmaxf(mx, other) * p.scale_log2;  // -inf stays -inf
-            float alpha = 1.f;
-            if (mx > m + 8.f || m == -CUDART_INF_F) {  // lazy rescale: only when the max really grows
-              const float m_new = fmaxf(m, mx);
-              if (m_new != -CUDART_INF_F) {
-                alpha = (m == -CUDART_INF_F) ? 0.f : ex2_approx(m - m_new);
-                m = m_new;
-              }
-            }
-            // P = 2^(s * scale_log2 - m), packed to bf16 pairs over the first half of these columns
-            const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
-            const uint64_t sc2 = sm::f2(p.scale_log2, p.scale_log2), nm2 = sm::f2(neg_m, neg_m);
-            uint64_t rs2 = sm::f2(0.f, 0.f);
+      const int tok = it.tok0 + ((it.split ? 0 : slot * 128) + t) / p.G;
+      const bool live = __any_sync(0xffffffffu, tok < it.tok0 + it.ntok);  // the warp has rows of the item
+      const int at = it.C + tok, nt = it.tiles(), first = it.split ? slot : 0;
+      for (int j = first; j < nt; j += 1 + it.split, ++sc) {
+        const int b = sc & 1;
+        if (!wn_wait(&bar.s_full[slot][b], (sc >> 1) & 1, &s_abort, p.err)) { ok = false; break; }
+        tc::fence_after_sync();
+        if (live) {
+          const uint32_t srow = lane_at + wn_scol(slot, b);
+          uint32_t v[2][32];
+          tc::ld32(srow, v[0]);
+          tc::ld32(srow + 32, v[1]);
+          tc::wait_ld();
+          tc::touch32(v[0]);  // no use of v may move above the wait
+          tc::touch32(v[1]);
+          if (!it.full(j)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              uint32_t pk[16];
+              const uint32_t seen = wn_seen(p, it, 4 * j + 2 * c, at);
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
-                float x0, x1;
-                sm::unf2(x, x0, x1);
-                const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
-                rs2 = sm::add2(rs2, pp);
-                pk[e / 2] = sm::bf16x2(pp);
-              }
-              tc::st16(srow + c * 16, pk);
+              for (int e = 0; e < 32; ++e) v[c][e] = (seen >> e) & 1u ? v[c][e] : 0xFF800000u;
             }
-            float r0, r1;
-            sm::unf2(rs2, r0, r1);
-            l = l * alpha + (r0 + r1);
-            // The rescale decision is per row, but tcgen05.ld/st are warp-collective: the whole warp takes the
-            // branch when any of its rows needs it (alpha is 1 for the others). Each half has its part of O,
-            // which is quiescent: the previous P V product finished before S(j) did.
-            if (j > (split ? slot : 0) && __any_sync(0xffffffffu, alpha != 1.f)) {
+          }
+          // row max of the raw scores (the scale is positive, so it commutes with max)
+          float mq[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c) {
-                const uint32_t a = tmem + lane_off + wn_ocol(slot) + half * (D / 2) + c * 32;
+          for (int e = 0; e < 32; e += 4)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              mq[c] = sm::max3(mq[c], __uint_as_float(v[c & 1][e + (c & 2)]), __uint_as_float(v[c & 1][e + (c & 2) + 1]));
+          const float mx = fmaxf(sm::max3(mq[0], mq[1], mq[2]), mq[3]) * p.scale_log2;  // -inf stays -inf
+          // The decision to follow is per row, but tcgen05.ld/st are warp-collective: the whole warp takes the
+          // branch when any of its rows does (alpha is 1 for the others).
+          if (__any_sync(0xffffffffu, mx > m + kLazy)) {  // (m may be -inf)
+            float alpha = 1.f;
+            if (mx > m + kLazy) {
+              alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mx);
+              m = mx;
+            }
+            l *= alpha;
+            if (j > first) {
+              // O is quiescent once P V of the slot's tile before is done (the one before that was, before S of this tile)
+              if (!wn_wait(&bar.pv_done[slot], (sc - 1) & 1, &s_abort, p.err)) { ok = false; break; }
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                const uint32_t a = lane_at + wn_ocol(slot) + c * 32;
                 uint32_t o[32];
                 tc::ld32(a, o);
                 tc::wait_ld();
@@ -415,101 +390,116 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
                 tc::st32(a, o);
               }
             }
-            tc::wait_st();
           }
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.p_full[slot]);
+          // P = 2^(s * scale_log2 - m), packed to bf16 pairs over the first half of S
+          const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+          const uint64_t nm2 = sm::f2(neg_m, neg_m);
+          uint64_t rs2 = sm::f2(0.f, 0.f);
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
+              float x0, x1;
+              sm::unf2(x, x0, x1);
+              const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
+              rs2 = sm::add2(rs2, pp);
+              pk[16 * c + e / 2] = sm::bf16x2(pp);
+            }
+          tc::st32(srow, pk);
+          float r0, r1;
+          sm::unf2(rs2, r0, r1);
+          l += r0 + r1;
+          tc::wait_st();
         }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[slot][b]);
       }
       if (!ok) break;
-      // ---- epilogue (the item read again, so that its fields need not stay in registers above) ----
-      const WnItem it = s_item[k % C::ITEM_RING];
-      release(k);
-      const int tok = it.tok0 + ((split ? 0 : slot * 128) + t) / p.G;
+      // ---- epilogue ----
       const int64_t row = static_cast<int64_t>(it.row0) + tok;
       const bool write = tok < it.tok0 + it.ntok && row < p.num_tokens;
       const int64_t flat = row * p.Hq + it.kh * p.G + t % p.G;  // (128 is a multiple of G)
-      if (!split) {
+      if (!it.split) {
         if (!wn_wait(&bar.o_final[slot], oc & 1, &s_abort, p.err)) break;
         ++oc;
-        if (!live) continue;
-        float other;
-        if (!exchange(l, other)) break;
         tc::fence_after_sync();
-        const float sum = half ? other + l : l + other;  // (the same order in both halves)
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        if (live) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t o[32];
-          tc::ld32(tmem + lane_off + wn_ocol(slot) + half * (D / 2) + c * 32, o);
-          tc::wait_ld();
-          tc::touch32(o);
-          if (write) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + flat * D + half * (D / 2) + c * 32);
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tc::ld32(lane_at + wn_ocol(slot) + c * 32, o);
+            tc::wait_ld();
+            tc::touch32(o);
+            if (write) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + flat * D + c * 32);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float x[8];
+              for (int q = 0; q < 4; ++q) {
+                float x[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * q + e]) * inv;
-              dst[q] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * q + e]) * inv;
+                dst[q] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+              }
             }
           }
+          if (write && p.lse) p.lse[flat] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
         }
-        if (write && half == 0 && p.lse)
-          p.lse[flat] = sum > 0.f ? (m + __log2f(sum)) * 0.69314718055994531f : -CUDART_INF_F;
         tc::fence_before_sync();
         continue;
       }
-      // a split item: the slots' states of the same rows, merged by all four warps of the rows, a quarter of the
-      // dims each
+      // a split item: the slots' states of the same rows, merged by both warps of the rows, half of the dims each
       float2* mrg = reinterpret_cast<float2*>(smem + C::MERGE_OFF);
-      mrg[(slot * 2 + half) * 128 + t] = make_float2(m, l);
+      mrg[slot * 128 + t] = make_float2(m, l);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.quad[quad]);
-      if (!wn_wait(&bar.quad[quad], qc & 1, &s_abort, p.err)) break;
-      ++qc;
+      if (lane == 0) mbar_arrive(&bar.rows[quad]);
+      if (!wn_wait(&bar.rows[quad], rc & 1, &s_abort, p.err)) break;
+      ++rc;
       if (!wn_wait(&bar.o_both, bc & 1, &s_abort, p.err)) break;
       ++bc;
       tc::fence_after_sync();
       if (live) {
-        const float2 a0 = mrg[t], a1 = mrg[128 + t], b0 = mrg[256 + t], b1 = mrg[384 + t];
-        const float l0 = a0.y + a1.y, l1 = b0.y + b1.y, mm = fmaxf(a0.x, b0.x);
+        const float2 a = mrg[t], b = mrg[128 + t];
+        const float mm = fmaxf(a.x, b.x);
         // (a slot without a key for the row has l = 0; what its O holds is not read as a number)
-        const float w0 = l0 == 0.f ? 0.f : ex2_approx(a0.x - mm), w1 = l1 == 0.f ? 0.f : ex2_approx(b0.x - mm);
-        const float sum = l0 * w0 + l1 * w1, inv = sum > 0.f ? 1.f / sum : 0.f;
-        const int col = (slot * 2 + half) * (D / 4);
-        uint32_t o0[D / 4], o1[D / 4];
-        tc::ld_cols(tmem + lane_off + wn_ocol(0) + col, o0);
-        tc::ld_cols(tmem + lane_off + wn_ocol(1) + col, o1);
-        tc::wait_ld();
-        tc::touch_cols(o0);
-        tc::touch_cols(o1);
-        if (write) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + flat * D + col);
+        const float w0 = a.y == 0.f ? 0.f : ex2_approx(a.x - mm), w1 = b.y == 0.f ? 0.f : ex2_approx(b.x - mm);
+        const float sum = a.y * w0 + b.y * w1, inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            float x[8];
+        for (int c = 0; c < D / 64; ++c) {
+          const int col = slot * (D / 2) + c * 32;
+          uint32_t o0[32], o1[32];
+          tc::ld32(lane_at + wn_ocol(0) + col, o0);
+          tc::ld32(lane_at + wn_ocol(1) + col, o1);
+          tc::wait_ld();
+          tc::touch32(o0);
+          tc::touch32(o1);
+          if (write) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + flat * D + col);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x[e] = w0 == 0.f ? 0.f : __uint_as_float(o0[8 * q + e]) * (w0 * inv);
-              x[e] = w1 == 0.f ? x[e] : fmaf(__uint_as_float(o1[8 * q + e]), w1 * inv, x[e]);
+            for (int q = 0; q < 4; ++q) {
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                x[e] = w0 == 0.f ? 0.f : __uint_as_float(o0[8 * q + e]) * (w0 * inv);
+                x[e] = w1 == 0.f ? x[e] : fmaf(__uint_as_float(o1[8 * q + e]), w1 * inv, x[e]);
+              }
+              dst[q] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
             }
-            dst[q] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
           }
-          if (slot + half == 0 && p.lse)
-            p.lse[flat] = sum > 0.f ? (mm + __log2f(sum)) * 0.69314718055994531f : -CUDART_INF_F;
         }
+        if (write && slot == 0 && p.lse)
+          p.lse[flat] = sum == 0.f ? -CUDART_INF_F : (mm + __log2f(sum)) * 0.69314718055994531f;
       }
       tc::fence_before_sync();
-      // all four have read O and the states before any lets the next item's products at them
+      // both have read O and the states before either lets the next item's products at them
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.quad[quad]);
-      if (!wn_wait(&bar.quad[quad], qc & 1, &s_abort, p.err)) break;
-      ++qc;
+      if (lane == 0) mbar_arrive(&bar.rows[quad]);
+      if (!wn_wait(&bar.rows[quad], rc & 1, &s_abort, p.err)) break;
+      ++rc;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (warp == C::W_LOAD) {
       // ======================= TMA producer =======================
       if (lane == 0) {
@@ -559,22 +549,22 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         if (k > 0 && !wn_wait(&bar.q_empty, (k - 1) & 1, &s_abort, p.err)) break;
         if (tc::elect()) {
           const int tiles = it.split ? 1 : 2;
-          mbar_arrive_expect_tx(&bar.q_full, tiles * C::TILE_BYTES);
+          mbar_arrive_expect_tx(&bar.q_full, tiles * C::Q_BYTES);
           for (int s = 0; s < tiles; ++s)
 #pragma unroll
             for (int hf = 0; hf < C::HALVES; ++hf)
-              tma_load_4d(sQ + s * C::TILE_BYTES + hf * C::HALF_BYTES, &tm_q, &bar.q_full, 0, hf, it.kh * p.G,
+              tma_load_4d(sQ + s * C::Q_BYTES + hf * C::Q_HALF, &tm_q, &bar.q_full, 0, hf, it.kh * p.G,
                           it.row0 + it.tok0 + s * (128 / p.G));
         }
         __syncwarp();
         ++qn;
         const int32_t* table = p.block_tables + static_cast<int64_t>(r) * p.max_blocks;
         const int nt = it.tiles();
-        // lanes 0 .. 7: where chunk `lane` of tile j lies: its cache block, or ~ its first row of new tokens
+        // lanes 0 .. 3: where chunk `lane` of tile j lies: its cache block, or ~ its first row of new tokens
         auto look_up = [&](int j) {
           int at = 0;
-          const int v = 8 * j + lane;
-          if (lane < 8 && v < it.NV) {
+          const int v = C::CHUNKS * j + lane;
+          if (lane < C::CHUNKS && v < it.NV) {
             const int u = it.chunk(v);
             if (u < it.cb) {
               at = table[u];
@@ -590,19 +580,25 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         };
         int next = look_up(0);
         for (int j = 0; j < nt && ok; ++j) {
-          const int at = next, chunks = min(8, it.NV - 8 * j);
+          const int at = next, chunks = min(C::CHUNKS, it.NV - C::CHUNKS * j);
+          // a tile of new tokens that follow one another comes in one box a half
+          const int at0 = __shfl_sync(0xffffffffu, at, 0);
+          const bool run = at0 < 0 && __all_sync(0xffffffffu, lane >= chunks || at == at0 - 16 * lane);
           if (j + 1 < nt) next = look_up(j + 1);
           for (int sel = 0; sel < 2; ++sel, ++kvc) {
             const int b = kvc % C::NBUF;
             const uint32_t use = kvc / C::NBUF;
             if (use > 0 && !wn_wait(&bar.kv_empty[b], (use - 1) & 1, &s_abort, p.err)) { ok = false; break; }
-            uint8_t* dst = ring + b * C::TILE_BYTES;
-            if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[b], chunks * 16 * D * 2);
+            uint8_t* dst = ring + b * C::KV_BYTES;
+            if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[b], run ? C::KV_BYTES : chunks * 16 * D * 2);
             __syncwarp();
-            if (lane < chunks) {
+            if (run) {
+              if (lane < C::HALVES)
+                tma_load_3d(dst + lane * C::KV_HALF, sel ? &tm_v64 : &tm_k64, &bar.kv_full[b], 0, it.kh * C::HALVES + lane, ~at0);
+            } else if (lane < chunks) {
 #pragma unroll
               for (int hf = 0; hf < C::HALVES; ++hf) {
-                uint8_t* to = dst + hf * C::HALF_BYTES + lane * 2048;
+                uint8_t* to = dst + hf * C::KV_HALF + lane * 2048;
                 if (at >= 0)
                   tma_load_4d(to, sel ? &tm_cv : &tm_ck, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, 0, at);
                 else
@@ -623,31 +619,45 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       // ======================= MMA issuer =======================
       if (tc::elect()) {
         constexpr uint32_t kQk = tc::idesc_bf16(128, 0, 0, 0), kPv = tc::idesc_bf16(128, D, 0, 1);
-        uint32_t kvc = 0, pc0 = 0, pc1 = 0;
-        auto ring_at = [&](int b) { return smem_u32(ring + b * C::TILE_BYTES); };
-        auto qk = [&](int slot, int qtile, int kbuf, int chunks) {
-          const uint32_t qa = smem_u32(sQ + qtile * C::TILE_BYTES), kb = ring_at(kbuf);
-          const uint32_t idesc = kQk | static_cast<uint32_t>(2 * chunks) << 17;  // N = 16 chunks
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t off = (s / 4) * C::HALF_BYTES + (s % 4) * 32;
-            tc::mma_ss(tmem + wn_scol(slot), tc::smem_desc(qa + off, 16, 1024), tc::smem_desc(kb + off, 16, 1024), idesc,
-                       s > 0);
-          }
-          tc::commit(&bar.s_full[slot]);
-        };
-        auto pv = [&](int slot, int vbuf, int chunks, bool acc) {
-          const uint32_t vb = ring_at(vbuf);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)  // P of chunks 4 .. 7 lies in the other half's columns
-            if (c < chunks)
-              tc::mma_ts(tmem + wn_ocol(slot), tmem + wn_scol(slot) + (c >> 2) * 64 + (c & 3) * 8,
-                         tc::smem_desc(vb + c * 2048, C::HALF_BYTES, 1024), kPv, (acc || c > 0) ? 1u : 0u);
-        };
+        // Shared-memory descriptors (tc::smem_desc) as their low words: the address in 16 bytes and the leading
+        // offset; the high word is the same for all.
+        constexpr uint32_t kLboK = (16u >> 4) << 16, kLboV = (static_cast<uint32_t>(C::KV_HALF) >> 4) << 16;
+        auto desc = [](uint32_t lo) { return (static_cast<uint64_t>((1024u >> 4) | 1u << 14 | 2u << 29) << 32) | lo; };
+        const uint32_t ring_at = smem_u32(ring) >> 4, q_at = smem_u32(sQ) >> 4;
+        uint32_t kvc = 0;             // K and V tiles of the items before this one
+        uint32_t sn0 = 0, sn1 = 0, pn0 = 0, pn1 = 0;  // S and P V products of each slot
         bool ok = true;
         auto wait = [&](uint64_t* b, uint32_t parity) {
           if (!wn_wait1(b, parity, &s_abort, p.err)) return false;
           tc::fence_after_sync();
+          return true;
+        };
+        auto kbuf = [&](int j) { return (kvc + 2 * j) % C::NBUF; };
+        auto vbuf = [&](int j) { return (kvc + 2 * j + 1) % C::NBUF; };
+        auto k_there = [&](int j) { return wait(&bar.kv_full[kbuf(j)], ((kvc + 2 * j) / C::NBUF) & 1); };
+        auto v_there = [&](int j) { return wait(&bar.v_ready[vbuf(j)], ((kvc + 2 * j + 1) / C::NBUF) & 1); };
+        // S = Q K^T of tile j into the slot's next buffer (N = 16 chunks)
+        auto qk = [&](int slot, int qtile, int j, int chunks) {
+          const uint32_t qa = (q_at + qtile * (C::Q_BYTES >> 4)) | kLboK, kb = (ring_at + kbuf(j) * (C::KV_BYTES >> 4)) | kLboK;
+          const uint32_t idesc = kQk | static_cast<uint32_t>(2 * chunks) << 17, b = (slot ? sn1 : sn0) & 1;
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            tc::mma_ss(tmem + wn_scol(slot, b), desc(qa + (((s / 4) * C::Q_HALF + (s % 4) * 32) >> 4)),
+                       desc(kb + (((s / 4) * C::KV_HALF + (s % 4) * 32) >> 4)), idesc, s > 0);
+          tc::commit(&bar.s_full[slot][b]);
+          if (slot) ++sn1; else ++sn0;
+        };
+        // O += P V of tile j, once its P is there
+        auto pv = [&](int slot, int j, int chunks, bool acc) {
+          const uint32_t n = slot ? pn1 : pn0, b = n & 1, vb = (ring_at + vbuf(j) * (C::KV_BYTES >> 4)) | kLboV;
+          if (!wait(&bar.p_full[slot][b], (n >> 1) & 1)) return false;
+#pragma unroll
+          for (int c = 0; c < C::CHUNKS; ++c)
+            if (c < chunks)
+              tc::mma_ts(tmem + wn_ocol(slot), tmem + wn_scol(slot, b) + c * 8, desc(vb + c * 128), kPv,
+                         (acc || c > 0) ? 1u : 0u);
+          tc::commit(&bar.pv_done[slot]);
+          if (slot) ++pn1; else ++pn0;
           return true;
         };
         for (uint32_t k = 0; ok; ++k) {
@@ -656,43 +666,50 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           const int NV = *static_cast<volatile int*>(&s_item[e].NV), split = *static_cast<volatile int*>(&s_item[e].split);
           mbar_arrive(&bar.item_empty[e]);
           if (NV == 0) break;
-          const int nt = (NV + 7) >> 3;
+          const int nt = (NV + C::CHUNKS - 1) / C::CHUNKS;
+          auto chunks = [&](int j) { return min(C::CHUNKS, NV - C::CHUNKS * j); };
           if (!wait(&bar.q_full, k & 1)) { ok = false; break; }
-          int vprev = -1;  // V buffer of tile j - 1
-          for (int j = 0; j <= nt && ok; ++j) {
-            // S of tile j; then O += P V of tile j - 1 (of slot 1; in a split item of the tile's slot), and of
-            // tile j of slot 0
-            const int kb = kvc % C::NBUF, vb = (kvc + 1) % C::NBUF, chunks = min(8, NV - 8 * j);
-            const uint32_t kuse = kvc / C::NBUF, vuse = (kvc + 1) / C::NBUF;
-            const int s0 = split ? j & 1 : 0;
-            if (j < nt) {
-              if (!(ok = wait(&bar.kv_full[kb], kuse & 1))) break;
-              qk(s0, 0, kb, chunks);
+          if (!split) {
+            // S runs one tile ahead of P V in each slot
+            if (!(ok = k_there(0))) break;
+            qk(0, 0, 0, chunks(0));
+            qk(1, 1, 0, chunks(0));
+            tc::commit(&bar.kv_empty[kbuf(0)]);
+            for (int j = 0; j < nt; ++j) {
+              const bool more = j + 1 < nt;
+              if (more) {
+                if (!(ok = k_there(j + 1))) break;
+                qk(0, 0, j + 1, chunks(j + 1));
+              } else {
+                tc::commit(&bar.q_empty);
+              }
+              if (!(ok = v_there(j)) || !(ok = pv(0, j, chunks(j), j > 0))) break;
+              if (more) {
+                qk(1, 1, j + 1, chunks(j + 1));
+                tc::commit(&bar.kv_empty[kbuf(j + 1)]);
+              } else {
+                tc::commit(&bar.o_final[0]);
+              }
+              if (!(ok = pv(1, j, chunks(j), j > 0))) break;
+              tc::commit(&bar.kv_empty[vbuf(j)]);
             }
-            if (j > 0) {
-              // (V of tile j - 1 was waited for by slot 0's product, or is now)
-              const int s = split ? (j - 1) & 1 : 1;
-              if (split && !(ok = wait(&bar.v_ready[vprev], ((kvc - 1) / C::NBUF) & 1))) break;
-              if (!(ok = wait(&bar.p_full[s], (s ? pc1 : pc0) & 1))) break;
-              if (s) ++pc1; else ++pc0;
-              pv(s, vprev, min(8, NV - 8 * (j - 1)), split ? j > 2 : j > 1);
-              tc::commit(&bar.kv_empty[vprev]);
-              if (j == nt) tc::commit(split ? &bar.o_both : &bar.o_final[1]);
+            if (ok) tc::commit(&bar.o_final[1]);
+          } else {
+            // the tiles go to the slots in turn; S runs one tile ahead in each
+            for (int j = -2; j < nt; ++j) {
+              if (j + 2 < nt) {
+                if (!(ok = k_there(j + 2))) break;
+                qk(j & 1, 0, j + 2, chunks(j + 2));
+                tc::commit(&bar.kv_empty[kbuf(j + 2)]);
+              }
+              if (j + 2 == nt - 1) tc::commit(&bar.q_empty);
+              if (j < 0) continue;
+              if (!(ok = v_there(j)) || !(ok = pv(j & 1, j, chunks(j), j > 1))) break;
+              tc::commit(&bar.kv_empty[vbuf(j)]);
             }
-            if (j == nt) break;
-            if (!split) qk(1, 1, kb, chunks);
-            tc::commit(&bar.kv_empty[kb]);
-            if (j == nt - 1) tc::commit(&bar.q_empty);
-            if (!split) {
-              if (!(ok = wait(&bar.v_ready[vb], vuse & 1))) break;
-              if (!(ok = wait(&bar.p_full[0], pc0 & 1))) break;
-              ++pc0;
-              pv(0, vb, chunks, j > 0);
-              if (j == nt - 1) tc::commit(&bar.o_final[0]);
-            }
-            vprev = vb;
-            kvc += 2;
+            if (ok) tc::commit(&bar.o_both);
           }
+          kvc += 2 * nt;
         }
         if (!ok) {  // the products in flight are waited for (bounded) before tensor memory is freed
           tc::commit(&bar.drained);
@@ -716,17 +733,17 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           const int b = (kvc + 1) % C::NBUF;
           if (!wn_wait(&bar.kv_full[b], ((kvc + 1) / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
           if (!it.full(j)) {
-            const uint32_t tile = ring_base + b * C::TILE_BYTES;
+            const uint32_t tile = ring_base + b * C::KV_BYTES;
 #pragma unroll 1
-            for (int R = ft; R < 128; R += 32 * C::NFIX) {
-              const int v = 8 * j + R / 16;
+            for (int R = ft; R < C::BN; R += 32 * C::NFIX) {
+              const int v = C::CHUNKS * j + R / 16;
               if (v >= it.NV) continue;  // (no product takes it)
               const int u = it.chunk(v), key = it.pos(u) + R % 16;
               const bool seen = (key >= it.low || key < sinks) && key <= last && (u >= it.cb || key < it.C);
               if (seen) continue;
 #pragma unroll
               for (int c = 0; c < C::HALVES * 8; ++c)
-                st_shared_v4(tile + (c / 8) * C::HALF_BYTES + R * 128 + (c % 8) * 16, make_uint4(0, 0, 0, 0));
+                st_shared_v4(tile + (c / 8) * C::KV_HALF + R * 128 + (c % 8) * 16, make_uint4(0, 0, 0, 0));
             }
             fence_proxy_async_smem();
           }
@@ -755,20 +772,21 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
 
 template <int D>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream) {
+                   const CUtensorMap& tk64, const CUtensorMap& tv64, const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream) {
   const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attn_window_kernel<D>), wn_smem<D>(),
                                            D == 64 ? kAttrWinAttn64 : kAttrWinAttn128);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_window_kernel<D>, dim3(num_sms()), dim3(WnCfg<D>::THREADS), wn_smem<D>(), stream, p, tq, tk, tv, tck,
-                    tcv);
+  return launch_pdl(attn_window_kernel<D>, dim3(num_sms()), dim3(WnCfg<D>::THREADS), wn_smem<D>(), stream, p, tq, tk, tv,
+                    tk64, tv64, tck, tcv);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_window(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const CUtensorMap& tck, const CUtensorMap& tcv, int D, cudaStream_t stream, int* launches) {
+                               const CUtensorMap& tk64, const CUtensorMap& tv64, const CUtensorMap& tck, const CUtensorMap& tcv, int D, cudaStream_t stream, int* launches) {
   *launches += 1;
-  return D == 64 ? launch<64>(p, tq, tk, tv, tck, tcv, stream) : launch<128>(p, tq, tk, tv, tck, tcv, stream);
+  return D == 64 ? launch<64>(p, tq, tk, tv, tk64, tv64, tck, tcv, stream)
+                 : launch<128>(p, tq, tk, tv, tk64, tv64, tck, tcv, stream);
 }
 
 }  // namespace pkv
