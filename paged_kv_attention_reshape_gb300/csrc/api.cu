@@ -847,7 +847,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   p.sinks = sinks;
   p.k_scales = cache ? cache->k_scales : nullptr;
   p.v_scales = cache ? cache->v_scales : nullptr;
-  CUtensorMap tq, tk, tv, tck, tcv, tqf, tk64, tv64;
+  CUtensorMap tq, tk, tv, tck, tcv, tqf, tkt, tvt;
   std::memset(&tck, 0, sizeof tck);
   std::memset(&tcv, 0, sizeof tcv);
   const bool windowed = window > 0 && ctx_kind == kAttnCtxBf16, packed = ctx_kind == kAttnCtxBlock;
@@ -856,7 +856,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
       !encode_rows(&tk, k, num_tokens, Hkv, D, rows) ||
       !encode_rows(&tv, v, num_tokens, Hkv, D, rows) || !encode_rows(&tqf, q, num_tokens * Hq, 1, D, 128))
     return PKV_ERR_CUDA;
-  if (windowed && (!encode_rows(&tk64, k, num_tokens, Hkv, D, 64) || !encode_rows(&tv64, v, num_tokens, Hkv, D, 64)))
+  if (windowed && (!encode_rows(&tkt, k, num_tokens, Hkv, D, 128) || !encode_rows(&tvt, v, num_tokens, Hkv, D, 128)))
     return PKV_ERR_CUDA;
   if (cache != nullptr &&
       (!encode_cache(&tck, cache->k, *cache) || !encode_cache(&tcv, cache->v, *cache)))
@@ -866,7 +866,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
     p.set_offset = off;
     p.sched_slot = next_sched_slot(reinterpret_cast<cudaStream_t>(stream));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    st = cuda_status(windowed ? launch_attn_window(p, tq, tk, tv, tk64, tv64, tck, tcv, D, s, &launches)
+    st = cuda_status(windowed ? launch_attn_window(p, tq, tk, tv, tkt, tvt, tck, tcv, D, s, &launches)
                      : packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, workspace, s, &launches)
                               : launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
                                                  s, &launches));

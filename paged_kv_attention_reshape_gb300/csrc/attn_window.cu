@@ -16,14 +16,15 @@
 // its key tiles to the slots in turn, both on the one Q tile, and the two states are merged at the end.
 //
 // Keys come in chunks of 16: a cache block, or 16 new tokens of the request. The chunks that an item walks are
-// the first `head` ones, which hold sinks, and those from the first row's window on (WnItem); four make a key
+// the first `head` ones, which hold sinks, and those from the first row's window on (WnItem); eight make a key
 // tile, whatever they are, so sinks and window share a tile, and the last tile takes products of its chunks
 // alone. Tiles that every row sees whole skip the masks; in the others the value rows that no row sees are
 // zeroed (P = 0 there must not meet what is not finite).
 //
-// Key tiles of 64, so that tensor memory holds two S of each slot beside the two O of 128 columns: S of the next tile
-// is there when the softmax of this one is done, and the chain S, softmax, P V, S of one buffer (with one S of
-// 128 keys a slot: 3900 clocks a 128 keys, of which the tensor core worked 2080) bounds nothing.
+// A slot's chain is S = Q K^T (520 clocks a tile), softmax, O += P V (520), and the tensor core serves the other slot
+// meanwhile, so a softmax has some 1000 clocks: a whole row in registers, read once, and P handed over in two
+// halves. What the products wait for is issued by single threads (a barrier that is complete costs a warp 110 clocks, and
+// copies issued by eight lanes 1030 a tile instead of 540).
 //
 // Roles (12 warps, one CTA per SM, persistent):
 //   warps 0-3, 4-7  softmax of slot 0, 1 (thread t owns row t = TMEM lane t) and the epilogue
@@ -45,16 +46,19 @@ namespace {
 
 template <int D>
 struct WnCfg {
-  static constexpr int BN = 64, CHUNKS = BN / 16;         // keys of a tile
+  static constexpr int BN = 128, CHUNKS = BN / 16;        // keys of a tile
   static constexpr int HALVES = D / 64;
   static constexpr int Q_HALF = 128 * 128;                // 128 rows x 128 bytes
   static constexpr int Q_BYTES = HALVES * Q_HALF;         // one 128-row tile of Q
   static constexpr int KV_HALF = BN * 128;
   static constexpr int KV_BYTES = HALVES * KV_HALF;       // one tile of K or V
-  static constexpr int NBUF = D == 128 ? 8 : 16;          // K/V ring: one tile per buffer
+  static constexpr int NBUF = D == 128 ? 4 : 8;           // K/V ring: one tile per buffer
   static constexpr int MAXR = kAttnSetChunk;              // requests of the set one launch holds
   static constexpr int W_LOAD = 8, W_MMA = 9, W_FIX = 10, NFIX = 2;
   static constexpr int THREADS = 384;
+  // launched at 168 registers a thread; the softmax warps take some of the others'
+  static constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 80;
+  static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * 168, "register split");
   static constexpr int ITEM_RING = 4;                     // claimed items published to the other roles
   static constexpr int ITEM_READERS = 8 + 1 + NFIX;
   static constexpr int RING_OFF = 2 * Q_BYTES;
@@ -67,9 +71,9 @@ struct WnCfg {
 };
 struct WnBars {
   uint64_t q_full, q_empty;
-  uint64_t kv_full[16], kv_empty[16], v_ready[16];
-  uint64_t s_full[2][2], p_full[2][2];  // by slot and buffer
-  uint64_t pv_done[2], o_final[2];
+  uint64_t kv_full[8], kv_empty[8], v_ready[8];
+  uint64_t s_full[2], o_final[2];
+  uint64_t p_full[2][2];  // P of the first and of the second 64 columns
   uint64_t o_both;        // both slots' O of a split item
   uint64_t item_full[4], item_empty[4];
   uint64_t rows[4];       // the two warps that share a split item's 32 rows
@@ -78,7 +82,7 @@ struct WnBars {
 template <int D>
 constexpr int wn_smem() { return 1024 + WnCfg<D>::BAR_OFF + static_cast<int>(sizeof(WnBars)); }
 
-__device__ __forceinline__ constexpr uint32_t wn_scol(int slot, int b) { return slot * 128u + b * 64u; }
+__device__ __forceinline__ constexpr uint32_t wn_scol(int slot) { return slot * 128u; }
 __device__ __forceinline__ constexpr uint32_t wn_ocol(int slot) { return 256u + slot * 128u; }
 
 // A piece of work, published in shared memory by the producer. Chunks are numbered u = 0, 1, ..: the cache blocks
@@ -92,12 +96,12 @@ struct WnItem {
   int head, gap, cb;
   int low;                  // the first key in the first row's window
   int fs, f0, f1, vt;       // chunks 0 .. fs - 1 and f0 .. f1 - 1 of the walk, but for vt, every row sees whole
-  __device__ int tiles() const { return (NV + 3) >> 2; }
+  __device__ int tiles() const { return (NV + 7) >> 3; }
   __device__ int last() const { return C + tok0 + ntok - 1; }  // position of the last row
   __device__ int chunk(int v) const { return v < head ? v : v + gap; }
   __device__ int pos(int u) const { return u < cb ? 16 * u : C + 16 * (u - cb); }
   __device__ bool full(int j) const {
-    const int a = 4 * j, b = a + 4;
+    const int a = 8 * j, b = a + 8;
     return b <= fs || (a >= f0 && b <= f1 && (vt < a || vt >= b));
   }
 };
@@ -187,14 +191,14 @@ __device__ __forceinline__ uint32_t wn_seen(const AttnParams& p, const WnItem& i
 template <int D>
 __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
     attn_window_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k64,
-                       const __grid_constant__ CUtensorMap tm_v64, const __grid_constant__ CUtensorMap tm_ck,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kt,
+                       const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ CUtensorMap tm_ck,
                        const __grid_constant__ CUtensorMap tm_cv) {
   using C = WnCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                  // [slot][half][128][128 B]
-  uint8_t* ring = smem + C::RING_OFF;  // [NBUF][half][64][128 B]
+  uint8_t* ring = smem + C::RING_OFF;  // [NBUF][half][128][128 B]
   int4* s_req = reinterpret_cast<int4*>(smem + C::REQ_OFF);
   int* s_start = reinterpret_cast<int*>(smem + C::START_OFF);
   int* s_perm = reinterpret_cast<int*>(smem + C::PERM_OFF);
@@ -231,11 +235,8 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       mbar_init(&bar.v_ready[b], C::NFIX);
     }
     for (int i = 0; i < 2; ++i) {
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&bar.s_full[i][b], 1);
-        mbar_init(&bar.p_full[i][b], 4);
-      }
-      mbar_init(&bar.pv_done[i], 1);
+      mbar_init(&bar.s_full[i], 1);
+      for (int h = 0; h < 2; ++h) mbar_init(&bar.p_full[i][h], 4);
       mbar_init(&bar.o_final[i], 1);
     }
     for (int w = 0; w < 4; ++w) mbar_init(&bar.rows[w], 2);
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
   };
 
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     // ======================= softmax =======================
     const int slot = warp >> 2, quad = warp & 3;
     const int t = tid & 127;  // row of the tile = TMEM lane
@@ -338,21 +340,20 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       const bool live = __any_sync(0xffffffffu, tok < it.tok0 + it.ntok);  // the warp has rows of the item
       const int at = it.C + tok, nt = it.tiles(), first = it.split ? slot : 0;
       for (int j = first; j < nt; j += 1 + it.split, ++sc) {
-        const int b = sc & 1;
-        if (!wn_wait(&bar.s_full[slot][b], (sc >> 1) & 1, &s_abort, p.err)) { ok = false; break; }
+        if (!wn_wait(&bar.s_full[slot], sc & 1, &s_abort, p.err)) { ok = false; break; }
         tc::fence_after_sync();
         if (live) {
-          const uint32_t srow = lane_at + wn_scol(slot, b);
-          uint32_t v[2][32];
-          tc::ld32(srow, v[0]);
-          tc::ld32(srow + 32, v[1]);
+          const uint32_t srow = lane_at + wn_scol(slot);
+          uint32_t v[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::ld32(srow + 32 * c, v[c]);
           tc::wait_ld();
-          tc::touch32(v[0]);  // no use of v may move above the wait
-          tc::touch32(v[1]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
           if (!it.full(j)) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t seen = wn_seen(p, it, 4 * j + 2 * c, at);
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t seen = wn_seen(p, it, 8 * j + 2 * c, at);
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[c][e] = (seen >> e) & 1u ? v[c][e] : 0xFF800000u;
             }
@@ -360,10 +361,9 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           // row max of the raw scores (the scale is positive, so it commutes with max)
           float mq[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
+          for (int e = 0; e < 32; e += 2)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              mq[c] = sm::max3(mq[c], __uint_as_float(v[c & 1][e + (c & 2)]), __uint_as_float(v[c & 1][e + (c & 2) + 1]));
+            for (int c = 0; c < 4; ++c) mq[c] = sm::max3(mq[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
           const float mx = fmaxf(sm::max3(mq[0], mq[1], mq[2]), mq[3]) * p.scale_log2;  // -inf stays -inf
           // The decision to follow is per row, but tcgen05.ld/st are warp-collective: the whole warp takes the
           // branch when any of its rows does (alpha is 1 for the others).
@@ -375,9 +375,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
             }
             l *= alpha;
             if (j > first) {
-              // O is quiescent once P V of the slot's tile before is done (the one before that was, before S of this tile)
-              if (!wn_wait(&bar.pv_done[slot], (sc - 1) & 1, &s_abort, p.err)) { ok = false; break; }
-              tc::fence_after_sync();
+              // (O is quiescent: the P V product before was done before S of this tile)
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 const uint32_t a = lane_at + wn_ocol(slot) + c * 32;
@@ -395,27 +393,34 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
           const uint64_t nm2 = sm::f2(neg_m, neg_m);
           uint64_t rs2 = sm::f2(0.f, 0.f);
-          uint32_t pk[32];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const uint64_t x = sm::fma2(sm::f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, nm2);
-              float x0, x1;
-              sm::unf2(x, x0, x1);
-              const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
-              rs2 = sm::add2(rs2, pp);
-              pk[16 * c + e / 2] = sm::bf16x2(pp);
-            }
-          tc::st32(srow, pk);
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const uint64_t x =
+                    sm::fma2(sm::f2(__uint_as_float(v[2 * h + c][e]), __uint_as_float(v[2 * h + c][e + 1])), sc2, nm2);
+                float x0, x1;
+                sm::unf2(x, x0, x1);
+                const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
+                rs2 = sm::add2(rs2, pp);
+                pk[16 * c + e / 2] = sm::bf16x2(pp);
+              }
+            tc::st32(srow + 32 * h, pk);
+            tc::wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.p_full[slot][h]);
+          }
           float r0, r1;
           sm::unf2(rs2, r0, r1);
           l += r0 + r1;
-          tc::wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(&bar.p_full[slot][0]);
+          mbar_arrive(&bar.p_full[slot][1]);
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[slot][b]);
       }
       if (!ok) break;
       // ---- epilogue ----
@@ -500,6 +505,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       ++rc;
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (warp == C::W_LOAD) {
       // ======================= TMA producer =======================
       if (lane == 0) {
@@ -560,7 +566,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         ++qn;
         const int32_t* table = p.block_tables + static_cast<int64_t>(r) * p.max_blocks;
         const int nt = it.tiles();
-        // lanes 0 .. 3: where chunk `lane` of tile j lies: its cache block, or ~ its first row of new tokens
+        // lane c < 8: where chunk c of tile j lies: its cache block, or ~ its first row of new tokens
         auto look_up = [&](int j) {
           int at = 0;
           const int v = C::CHUNKS * j + lane;
@@ -579,34 +585,48 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           return at;
         };
         int next = look_up(0);
-        for (int j = 0; j < nt && ok; ++j) {
-          const int at = next, chunks = min(C::CHUNKS, it.NV - C::CHUNKS * j);
-          // a tile of new tokens that follow one another comes in one box a half
-          const int at0 = __shfl_sync(0xffffffffu, at, 0);
-          const bool run = at0 < 0 && __all_sync(0xffffffffu, lane >= chunks || at == at0 - 16 * lane);
-          if (j + 1 < nt) next = look_up(j + 1);
-          for (int sel = 0; sel < 2; ++sel, ++kvc) {
-            const int b = kvc % C::NBUF;
-            const uint32_t use = kvc / C::NBUF;
-            if (use > 0 && !wn_wait(&bar.kv_empty[b], (use - 1) & 1, &s_abort, p.err)) { ok = false; break; }
-            uint8_t* dst = ring + b * C::KV_BYTES;
-            if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[b], run ? C::KV_BYTES : chunks * 16 * D * 2);
-            __syncwarp();
-            if (run) {
-              if (lane < C::HALVES)
-                tma_load_3d(dst + lane * C::KV_HALF, sel ? &tm_v64 : &tm_k64, &bar.kv_full[b], 0, it.kh * C::HALVES + lane, ~at0);
-            } else if (lane < chunks) {
+        for (int j = 0; j < nt; ++j) {
+          int at[C::CHUNKS];
 #pragma unroll
-              for (int hf = 0; hf < C::HALVES; ++hf) {
-                uint8_t* to = dst + hf * C::KV_HALF + lane * 2048;
-                if (at >= 0)
-                  tma_load_4d(to, sel ? &tm_cv : &tm_ck, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, 0, at);
-                else
-                  tma_load_3d(to, sel ? &tm_v : &tm_k, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, ~at);
+          for (int c = 0; c < C::CHUNKS; ++c) at[c] = __shfl_sync(0xffffffffu, next, c);
+          const int chunks = min(C::CHUNKS, it.NV - C::CHUNKS * j);
+          // a tile of new tokens that follow one another comes in one box a half
+          const bool run = at[0] < 0 && __all_sync(0xffffffffu, lane >= chunks || next == at[0] - 16 * lane);
+          if (j + 1 < nt) next = look_up(j + 1);
+          uint32_t issued = 2;  // of K and V
+          if (tc::elect()) {
+#pragma unroll 1
+            for (int sel = 0; sel < 2; ++sel) {
+              const uint32_t i = kvc + sel, b = i % C::NBUF;
+              if (i >= C::NBUF && !wn_wait1(&bar.kv_empty[b], (i / C::NBUF - 1) & 1, &s_abort, p.err)) {
+                issued = sel;
+                break;
+              }
+              uint8_t* dst = ring + b * C::KV_BYTES;
+              mbar_arrive_expect_tx(&bar.kv_full[b], run ? C::KV_BYTES : chunks * 16 * D * 2);
+              const CUtensorMap* mc = sel ? &tm_cv : &tm_ck;
+              const CUtensorMap* mn = sel ? &tm_v : &tm_k;
+              if (run) {
+#pragma unroll
+                for (int hf = 0; hf < C::HALVES; ++hf)
+                  tma_load_3d(dst + hf * C::KV_HALF, sel ? &tm_vt : &tm_kt, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, ~at[0]);
+              } else {
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c)
+                  if (c < chunks)
+#pragma unroll
+                    for (int hf = 0; hf < C::HALVES; ++hf) {
+                      if (at[c] >= 0)
+                        tma_load_4d(dst + hf * C::KV_HALF + c * 2048, mc, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, 0, at[c]);
+                      else
+                        tma_load_3d(dst + hf * C::KV_HALF + c * 2048, mn, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, ~at[c]);
+                    }
               }
             }
-            __syncwarp();
           }
+          issued = __reduce_min_sync(0xffffffffu, issued);
+          kvc += issued;
+          if (issued < 2) { ok = false; break; }
         }
       }
       if (!ok || *static_cast<volatile int*>(&s_abort)) {
@@ -625,7 +645,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         auto desc = [](uint32_t lo) { return (static_cast<uint64_t>((1024u >> 4) | 1u << 14 | 2u << 29) << 32) | lo; };
         const uint32_t ring_at = smem_u32(ring) >> 4, q_at = smem_u32(sQ) >> 4;
         uint32_t kvc = 0;             // K and V tiles of the items before this one
-        uint32_t sn0 = 0, sn1 = 0, pn0 = 0, pn1 = 0;  // S and P V products of each slot
+        uint32_t pn0 = 0, pn1 = 0;    // P V products of each slot
         bool ok = true;
         auto wait = [&](uint64_t* b, uint32_t parity) {
           if (!wn_wait1(b, parity, &s_abort, p.err)) return false;
@@ -636,27 +656,27 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         auto vbuf = [&](int j) { return (kvc + 2 * j + 1) % C::NBUF; };
         auto k_there = [&](int j) { return wait(&bar.kv_full[kbuf(j)], ((kvc + 2 * j) / C::NBUF) & 1); };
         auto v_there = [&](int j) { return wait(&bar.v_ready[vbuf(j)], ((kvc + 2 * j + 1) / C::NBUF) & 1); };
-        // S = Q K^T of tile j into the slot's next buffer (N = 16 chunks)
+        // S = Q K^T of tile j (N = 16 chunks)
         auto qk = [&](int slot, int qtile, int j, int chunks) {
           const uint32_t qa = (q_at + qtile * (C::Q_BYTES >> 4)) | kLboK, kb = (ring_at + kbuf(j) * (C::KV_BYTES >> 4)) | kLboK;
-          const uint32_t idesc = kQk | static_cast<uint32_t>(2 * chunks) << 17, b = (slot ? sn1 : sn0) & 1;
+          const uint32_t idesc = kQk | static_cast<uint32_t>(2 * chunks) << 17;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
-            tc::mma_ss(tmem + wn_scol(slot, b), desc(qa + (((s / 4) * C::Q_HALF + (s % 4) * 32) >> 4)),
+            tc::mma_ss(tmem + wn_scol(slot), desc(qa + (((s / 4) * C::Q_HALF + (s % 4) * 32) >> 4)),
                        desc(kb + (((s / 4) * C::KV_HALF + (s % 4) * 32) >> 4)), idesc, s > 0);
-          tc::commit(&bar.s_full[slot][b]);
-          if (slot) ++sn1; else ++sn0;
+          tc::commit(&bar.s_full[slot]);
         };
-        // O += P V of tile j, once its P is there
+        // O += P V of tile j, in two parts as its P comes
         auto pv = [&](int slot, int j, int chunks, bool acc) {
-          const uint32_t n = slot ? pn1 : pn0, b = n & 1, vb = (ring_at + vbuf(j) * (C::KV_BYTES >> 4)) | kLboV;
-          if (!wait(&bar.p_full[slot][b], (n >> 1) & 1)) return false;
+          const uint32_t n = slot ? pn1 : pn0, vb = (ring_at + vbuf(j) * (C::KV_BYTES >> 4)) | kLboV;
 #pragma unroll
-          for (int c = 0; c < C::CHUNKS; ++c)
-            if (c < chunks)
-              tc::mma_ts(tmem + wn_ocol(slot), tmem + wn_scol(slot, b) + c * 8, desc(vb + c * 128), kPv,
-                         (acc || c > 0) ? 1u : 0u);
-          tc::commit(&bar.pv_done[slot]);
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(&bar.p_full[slot][h], n & 1)) return false;
+#pragma unroll
+            for (int c = 4 * h; c < 4 * h + 4; ++c)
+              if (c < chunks)
+                tc::mma_ts(tmem + wn_ocol(slot), tmem + wn_scol(slot) + c * 8, desc(vb + c * 128), kPv, (acc || c > 0) ? 1u : 0u);
+          }
           if (slot) ++pn1; else ++pn0;
           return true;
         };
@@ -670,42 +690,40 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           auto chunks = [&](int j) { return min(C::CHUNKS, NV - C::CHUNKS * j); };
           if (!wait(&bar.q_full, k & 1)) { ok = false; break; }
           if (!split) {
-            // S runs one tile ahead of P V in each slot
             if (!(ok = k_there(0))) break;
             qk(0, 0, 0, chunks(0));
             qk(1, 1, 0, chunks(0));
             tc::commit(&bar.kv_empty[kbuf(0)]);
             for (int j = 0; j < nt; ++j) {
+              // (what the next products need is waited for before P, which comes last)
               const bool more = j + 1 < nt;
-              if (more) {
-                if (!(ok = k_there(j + 1))) break;
+              if (!more) tc::commit(&bar.q_empty);
+              if (!(ok = v_there(j)) || (more && !(ok = k_there(j + 1))) || !(ok = pv(0, j, chunks(j), j > 0))) break;
+              if (more)
                 qk(0, 0, j + 1, chunks(j + 1));
-              } else {
-                tc::commit(&bar.q_empty);
-              }
-              if (!(ok = v_there(j)) || !(ok = pv(0, j, chunks(j), j > 0))) break;
+              else
+                tc::commit(&bar.o_final[0]);
+              if (!(ok = pv(1, j, chunks(j), j > 0))) break;
               if (more) {
                 qk(1, 1, j + 1, chunks(j + 1));
                 tc::commit(&bar.kv_empty[kbuf(j + 1)]);
-              } else {
-                tc::commit(&bar.o_final[0]);
               }
-              if (!(ok = pv(1, j, chunks(j), j > 0))) break;
               tc::commit(&bar.kv_empty[vbuf(j)]);
             }
             if (ok) tc::commit(&bar.o_final[1]);
           } else {
-            // the tiles go to the slots in turn; S runs one tile ahead in each
+            // the tiles go to the slots in turn; S runs ahead as far as the slots' columns reach
             for (int j = -2; j < nt; ++j) {
+              if (j >= 0) {
+                if (!(ok = v_there(j)) || !(ok = pv(j & 1, j, chunks(j), j > 1))) break;
+                tc::commit(&bar.kv_empty[vbuf(j)]);
+              }
               if (j + 2 < nt) {
                 if (!(ok = k_there(j + 2))) break;
                 qk(j & 1, 0, j + 2, chunks(j + 2));
                 tc::commit(&bar.kv_empty[kbuf(j + 2)]);
               }
               if (j + 2 == nt - 1) tc::commit(&bar.q_empty);
-              if (j < 0) continue;
-              if (!(ok = v_there(j)) || !(ok = pv(j & 1, j, chunks(j), j > 1))) break;
-              tc::commit(&bar.kv_empty[vbuf(j)]);
             }
             if (ok) tc::commit(&bar.o_both);
           }
@@ -772,21 +790,21 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
 
 template <int D>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const CUtensorMap& tk64, const CUtensorMap& tv64, const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream) {
+                   const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream) {
   const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attn_window_kernel<D>), wn_smem<D>(),
                                            D == 64 ? kAttrWinAttn64 : kAttrWinAttn128);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_window_kernel<D>, dim3(num_sms()), dim3(WnCfg<D>::THREADS), wn_smem<D>(), stream, p, tq, tk, tv,
-                    tk64, tv64, tck, tcv);
+                    tkt, tvt, tck, tcv);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_window(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const CUtensorMap& tk64, const CUtensorMap& tv64, const CUtensorMap& tck, const CUtensorMap& tcv, int D, cudaStream_t stream, int* launches) {
+                               const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, int D, cudaStream_t stream, int* launches) {
   *launches += 1;
-  return D == 64 ? launch<64>(p, tq, tk, tv, tk64, tv64, tck, tcv, stream)
-                 : launch<128>(p, tq, tk, tv, tk64, tv64, tck, tcv, stream);
+  return D == 64 ? launch<64>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream)
+                 : launch<128>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream);
 }
 
 }  // namespace pkv
