@@ -28,12 +28,15 @@
 //
 // Roles (12 warps, one CTA per SM, persistent):
 //   warps 0-3, 4-7  softmax of slot 0, 1 (thread t owns row t = TMEM lane t) and the epilogue
-//   warp 8          TMA producer: claims the items, loads Q and the ring of K and V tiles
+//   warp 8          claims the items, loads Q and the ring of K tiles
 //   warp 9          MMA issuer, one elected thread, waits included: S = Q K^T, O += P V (P from tensor memory)
-//   warps 10-11     zero value rows of tiles at an edge
+//   warp 10         loads the ring of V tiles (a K buffer is free before the V buffer of the tile before)
+//   warp 11         zeroes value rows of tiles at an edge
 // Tensor memory (512 columns): S_0 (two buffers) | S_1 (two buffers) | O_0 | O_1; P_s (bf16 pairs) overwrites the
 // first half of its S.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -52,17 +55,17 @@ struct WnCfg {
   static constexpr int Q_BYTES = HALVES * Q_HALF;         // one 128-row tile of Q
   static constexpr int KV_HALF = BN * 128;
   static constexpr int KV_BYTES = HALVES * KV_HALF;       // one tile of K or V
-  static constexpr int NBUF = D == 128 ? 4 : 8;           // K/V ring: one tile per buffer
+  static constexpr int NBUF = D == 128 ? 2 : 4;           // tiles of the K ring, and of the V ring
   static constexpr int MAXR = kAttnSetChunk;              // requests of the set one launch holds
-  static constexpr int W_LOAD = 8, W_MMA = 9, W_FIX = 10, NFIX = 2;
+  static constexpr int W_K = 8, W_MMA = 9, W_V = 10, W_FIX = 11;
   static constexpr int THREADS = 384;
   // launched at 168 registers a thread; the softmax warps take some of the others'
   static constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 80;
   static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * 168, "register split");
   static constexpr int ITEM_RING = 4;                     // claimed items published to the other roles
-  static constexpr int ITEM_READERS = 8 + 1 + NFIX;
+  static constexpr int ITEM_READERS = 8 + 3;
   static constexpr int RING_OFF = 2 * Q_BYTES;
-  static constexpr int REQ_OFF = RING_OFF + NBUF * KV_BYTES;    // int4 {r, row0, q_len, C}
+  static constexpr int REQ_OFF = RING_OFF + 2 * NBUF * KV_BYTES;  // int4 {r, row0, q_len, C}
   static constexpr int START_OFF = REQ_OFF + MAXR * 16;         // prefix of the items, by rank
   static constexpr int PERM_OFF = START_OFF + (MAXR + 4) * 4;   // set positions by cost, heaviest first
   static constexpr int ITEM_OFF = PERM_OFF + MAXR * 4;
@@ -71,7 +74,7 @@ struct WnCfg {
 };
 struct WnBars {
   uint64_t q_full, q_empty;
-  uint64_t kv_full[8], kv_empty[8], v_ready[8];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], v_ready[4];
   uint64_t s_full[2], o_final[2];
   uint64_t p_full[2][2];  // P of the first and of the second 64 columns
   uint64_t o_both;        // both slots' O of a split item
@@ -89,7 +92,7 @@ __device__ __forceinline__ constexpr uint32_t wn_ocol(int slot) { return 256u + 
 // first (cb of them), then the new tokens sixteen by sixteen; the v-th chunk walked is u = v, or v + gap from
 // v = head on.
 struct WnItem {
-  int row0, q_len, C, kh;   // the request's first row of q, its new and its cached tokens; KV head
+  int r, row0, C, kh;       // request, its first row of q, its cached tokens; KV head
   int tok0, ntok;           // the item's first new token and its tokens
   int split;                // 1: one tile of rows, key tiles dealt to the slots in turn
   int NV;                   // chunks walked (0: no more work)
@@ -107,7 +110,7 @@ struct WnItem {
 };
 static_assert(sizeof(WnItem) == 64, "ring entry");
 
-__device__ __forceinline__ int wn_count(const int4& q, int G) { return (q.z * G + 255) / 256; }
+__device__ __forceinline__ int wn_count(const int4& q, int G) { return (q.z * G + 255) >> 8; }
 // Keys an item of the request walks, about: the schedule's order.
 __device__ __forceinline__ int wn_cost(const AttnParams& p, const int4& q) {
   return static_cast<int>(min(static_cast<int64_t>(q.z) + q.w, static_cast<int64_t>(p.window) + p.sinks));
@@ -116,12 +119,12 @@ __device__ __forceinline__ int wn_cost(const AttnParams& p, const int4& q) {
 // Item idx of a request {request id, first query row, q_len, cached tokens}.
 __device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, int idx) {
   WnItem it;
+  it.r = q.x;
   it.row0 = q.y;
-  it.q_len = q.z;
   it.C = q.w;
-  it.kh = idx % p.Hkv;
-  const int span = 256 / p.G;
-  it.tok0 = span * (wn_count(q, p.G) - 1 - idx / p.Hkv);  // later (heavier) rows of a request first
+  const int span = 256 / p.G, tile = idx / p.Hkv;
+  it.kh = idx - tile * p.Hkv;
+  it.tok0 = span * (wn_count(q, p.G) - 1 - tile);  // later (heavier) rows of a request first
   it.ntok = min(span, q.z - it.tok0);
   it.split = it.ntok * p.G <= 128;
   const int P0 = it.C + it.tok0, P1 = it.last();
@@ -198,7 +201,8 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                  // [slot][half][128][128 B]
-  uint8_t* ring = smem + C::RING_OFF;  // [NBUF][half][128][128 B]
+  uint8_t* ring_k = smem + C::RING_OFF;  // [NBUF][half][128][128 B]
+  uint8_t* ring_v = ring_k + C::NBUF * C::KV_BYTES;
   int4* s_req = reinterpret_cast<int4*>(smem + C::REQ_OFF);
   int* s_start = reinterpret_cast<int*>(smem + C::START_OFF);
   int* s_perm = reinterpret_cast<int*>(smem + C::PERM_OFF);
@@ -230,9 +234,11 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
     mbar_init(&bar.q_full, 1);
     mbar_init(&bar.q_empty, 1);
     for (int b = 0; b < C::NBUF; ++b) {
-      mbar_init(&bar.kv_full[b], 1);
-      mbar_init(&bar.kv_empty[b], 1);
-      mbar_init(&bar.v_ready[b], C::NFIX);
+      mbar_init(&bar.k_full[b], 1);
+      mbar_init(&bar.k_empty[b], 1);
+      mbar_init(&bar.v_full[b], 1);
+      mbar_init(&bar.v_empty[b], 1);
+      mbar_init(&bar.v_ready[b], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
@@ -271,15 +277,17 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       flag_error(p.err, PKV_DEVERR_REQS);
     }
     s_req[i] = q;
+    s_start[i] = wn_cost(p, q);
   }
   static_assert(C::MAXR <= C::THREADS, "a thread a request");
   __syncthreads();
   // rank by cost, heaviest first, ties in set order (a stable order every CTA computes alike)
   if (tid < n) {
-    const int ki = wn_cost(p, s_req[tid]);
+    const int ki = s_start[tid];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) {
-      const int kj = wn_cost(p, s_req[j]);
+      const int kj = s_start[j];
       rank += (kj > ki || (kj == ki && j < tid)) ? 1 : 0;
     }
     s_perm[rank] = tid;
@@ -328,6 +336,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
     const int t = tid & 127;  // row of the tile = TMEM lane
     const uint32_t lane_at = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint64_t sc2 = sm::f2(p.scale_log2, p.scale_log2);
+    const int shift = __ffs(p.G) - 1;  // G is a power of two
     uint32_t sc = 0, oc = 0, bc = 0, rc = 0;  // phases: S of this slot, o_final, o_both, rows
     for (uint32_t k = 0;; ++k) {
       const WnItem* taken = take(k);
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       release(k);
       float m = -CUDART_INF_F, l = 0.f;
       bool ok = true;
-      const int tok = it.tok0 + ((it.split ? 0 : slot * 128) + t) / p.G;
+      const int tok = it.tok0 + (((it.split ? 0 : slot * 128) + t) >> shift);
       const bool live = __any_sync(0xffffffffu, tok < it.tok0 + it.ntok);  // the warp has rows of the item
       const int at = it.C + tok, nt = it.tiles(), first = it.split ? slot : 0;
       for (int j = first; j < nt; j += 1 + it.split, ++sc) {
@@ -426,7 +435,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       // ---- epilogue ----
       const int64_t row = static_cast<int64_t>(it.row0) + tok;
       const bool write = tok < it.tok0 + it.ntok && row < p.num_tokens;
-      const int64_t flat = row * p.Hq + it.kh * p.G + t % p.G;  // (128 is a multiple of G)
+      const int64_t flat = row * p.Hq + it.kh * p.G + (t & (p.G - 1));  // (128 is a multiple of G)
       if (!it.split) {
         if (!wn_wait(&bar.o_final[slot], oc & 1, &s_abort, p.err)) break;
         ++oc;
@@ -506,135 +515,179 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
-    if (warp == C::W_LOAD) {
-      // ======================= TMA producer =======================
+    // ---- loading K or V tiles ----
+    // Lane c < 8: where chunk c of tile j lies: its cache block (`paged`; looked at when it is used, so that nothing
+    // waits for it here), or ~ its first row of new tokens.
+    bool paged = false;
+    auto look_up = [&](const WnItem& it, int j) {
+      int at = 0;
+      paged = false;
+      const int v = C::CHUNKS * j + lane;
+      if (lane < C::CHUNKS && v < it.NV) {
+        const int u = it.chunk(v);
+        paged = u < it.cb;
+        at = paged ? p.block_tables[static_cast<int64_t>(it.r) * p.max_blocks + u] : ~(it.row0 + 16 * (u - it.cb));
+      }
+      return at;
+    };
+    // Tile i of the ring: the chunks at `where` (one a lane), once the buffer is free; then `peek` for the next tile's,
+    // whose round trip to memory passes meanwhile. False: a wait gave up.
+    auto load_tile = [&](uint32_t i, int where, int chunks, int kh, uint8_t* ring, uint64_t* full, uint64_t* empty,
+                         const CUtensorMap* cache, const CUtensorMap* rows, const CUtensorMap* tile, auto peek) {
+      if (paged && (where < 0 || where >= p.num_blocks)) {
+        flag_error(p.err, PKV_DEVERR_BLOCK);
+        where = 0;
+      }
+      int at[C::CHUNKS];
+#pragma unroll
+      for (int c = 0; c < C::CHUNKS; ++c) at[c] = __shfl_sync(0xffffffffu, where, c);
+      // a tile of new tokens that follow one another comes in one box a half
+      const bool run = at[0] < 0 && __all_sync(0xffffffffu, lane >= chunks || where == at[0] - 16 * lane);
+      const bool cached = __all_sync(0xffffffffu, lane >= chunks || where >= 0);
+      peek();
+      const uint32_t b = i % C::NBUF;
+      bool ok = true;
+      if (tc::elect()) {
+        if (i >= C::NBUF) ok = wn_wait1(&empty[b], (i / C::NBUF - 1) & 1, &s_abort, p.err);
+        if (ok) {
+          uint8_t* dst = ring + b * C::KV_BYTES;
+          mbar_arrive_expect_tx(&full[b], run ? C::KV_BYTES : chunks * 16 * D * 2);
+          if (run) {
+#pragma unroll
+            for (int hf = 0; hf < C::HALVES; ++hf)
+              tma_load_3d(dst + hf * C::KV_HALF, tile, &full[b], 0, kh * C::HALVES + hf, ~at[0]);
+          } else if (cached && chunks == C::CHUNKS) {
+#pragma unroll
+            for (int c = 0; c < C::CHUNKS; ++c)
+#pragma unroll
+              for (int hf = 0; hf < C::HALVES; ++hf)
+                tma_load_4d(dst + hf * C::KV_HALF + c * 2048, cache, &full[b], 0, kh * C::HALVES + hf, 0, at[c]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < C::CHUNKS; ++c)
+              if (c < chunks)
+#pragma unroll
+                for (int hf = 0; hf < C::HALVES; ++hf) {
+                  if (at[c] >= 0)
+                    tma_load_4d(dst + hf * C::KV_HALF + c * 2048, cache, &full[b], 0, kh * C::HALVES + hf, 0, at[c]);
+                  else
+                    tma_load_3d(dst + hf * C::KV_HALF + c * 2048, rows, &full[b], 0, kh * C::HALVES + hf, ~at[c]);
+                }
+          }
+        }
+      }
+      return __all_sync(0xffffffffu, ok) != 0;
+    };
+    // a wait gave up: the loads in flight are waited for (bounded), so that none lands after the CTA is gone
+    auto drain = [&](uint32_t n, uint64_t* full) {
+      for (uint32_t i = n > C::NBUF ? n - C::NBUF : 0; i < n; ++i) mbar_wait(&full[i % C::NBUF], (i / C::NBUF) & 1, p.err);
+    };
+
+    if (warp == C::W_K) {
+      // ======================= items, Q and K =======================
       if (lane == 0) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
-        if (p.seq_lens != nullptr) {
-          tma_prefetch_desc(&tm_ck);
-          tma_prefetch_desc(&tm_cv);
-        }
+        tma_prefetch_desc(&tm_kt);
+        if (p.seq_lens != nullptr) tma_prefetch_desc(&tm_ck);
       }
-      uint32_t kvc = 0, qn = 0;
+      uint32_t kc = 0, qn = 0;
       bool ok = true;
-      int w_static = blockIdx.x, odd = 0;
+      int odd = 0;
+      // item w of the launch (NV 0: there is none)
+      WnItem it;
+      auto make = [&](int w) {
+        it.NV = 0;
+        if (w >= W) return;
+        int lo = 0, hi = n - 1;  // the last rank whose prefix is at most w
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (s_start[mid] <= w) lo = mid; else hi = mid - 1;
+        }
+        it = wn_item(p, s_req[s_perm[lo]], w - s_start[lo]);
+      };
+      // A CTA begins with the item of its own number; the next one is claimed as soon as an item begins and looked
+      // up before its last tile, so that neither round trip to memory holds the loads up.
+      int w = blockIdx.x;
+      make(w);
+      int next = look_up(it, 0);
       for (uint32_t k = 0; ok; ++k) {
         const uint32_t e = k % C::ITEM_RING;
-        if (k >= C::ITEM_RING && !wn_wait(&bar.item_empty[e], (k / C::ITEM_RING - 1) & 1, &s_abort, p.err)) break;
-        int w = 0;
-        if (p.sched_slot >= 0) {
-          if (lane == 0) w = static_cast<int>(min(atomicAdd(&g_wn_next[p.sched_slot], 1u), static_cast<unsigned>(W)));
-          w = __shfl_sync(0xffffffffu, w, 0);
-        } else {
-          w = w_static;
-          w_static += odd ? 2 * blockIdx.x + 1 : 2 * (gridDim.x - blockIdx.x) - 1;
-          odd ^= 1;
-        }
-        WnItem it;
-        int r = 0;
-        it.NV = 0;
-        if (w < W) {
-          int lo = 0, hi = n - 1;  // the last rank whose prefix is at most w
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_start[mid] <= w) lo = mid; else hi = mid - 1;
-          }
-          const int4 q = s_req[s_perm[lo]];
-          r = q.x;
-          it = wn_item(p, q, w - s_start[lo]);
-        }
+        if (k >= C::ITEM_RING && !wn_wait(&bar.item_empty[e], (k / C::ITEM_RING - 1) & 1, &s_abort, p.err)) { ok = false; break; }
         if (lane == 0) {
           s_item[e] = it;
           mbar_arrive(&bar.item_full[e]);
         }
         __syncwarp();
         if (it.NV == 0) break;
-        // the Q buffer is free once the previous item's S products are done
-        if (k > 0 && !wn_wait(&bar.q_empty, (k - 1) & 1, &s_abort, p.err)) break;
-        if (tc::elect()) {
-          const int tiles = it.split ? 1 : 2;
-          mbar_arrive_expect_tx(&bar.q_full, tiles * C::Q_BYTES);
-          for (int s = 0; s < tiles; ++s)
-#pragma unroll
-            for (int hf = 0; hf < C::HALVES; ++hf)
-              tma_load_4d(sQ + s * C::Q_BYTES + hf * C::Q_HALF, &tm_q, &bar.q_full, 0, hf, it.kh * p.G,
-                          it.row0 + it.tok0 + s * (128 / p.G));
+        int claimed = 0;
+        if (p.sched_slot < 0) {
+          claimed = w + (odd ? 2 * blockIdx.x + 1 : 2 * (gridDim.x - blockIdx.x) - 1);
+          odd ^= 1;
+        } else if (lane == 0) {
+          claimed = gridDim.x + min(atomicAdd(&g_wn_next[p.sched_slot], 1u), static_cast<unsigned>(W));
         }
-        __syncwarp();
-        ++qn;
-        const int32_t* table = p.block_tables + static_cast<int64_t>(r) * p.max_blocks;
-        const int nt = it.tiles();
-        // lane c < 8: where chunk c of tile j lies: its cache block, or ~ its first row of new tokens
-        auto look_up = [&](int j) {
-          int at = 0;
-          const int v = C::CHUNKS * j + lane;
-          if (lane < C::CHUNKS && v < it.NV) {
-            const int u = it.chunk(v);
-            if (u < it.cb) {
-              at = table[u];
-              if (at < 0 || at >= p.num_blocks) {
-                flag_error(p.err, PKV_DEVERR_BLOCK);
-                at = 0;
-              }
-            } else {
-              at = ~(it.row0 + 16 * (u - it.cb));
+        const int nt = it.tiles(), NV = it.NV, kh = it.kh, q_tiles = it.split ? 1 : 2, q_row = it.row0 + it.tok0;
+        for (int j = 0; j < nt && ok; ++j) {
+          const int where = next;
+          auto peek = [&]() {
+            if (j + 1 == nt) {
+              w = __shfl_sync(0xffffffffu, claimed, 0);
+              make(w);
             }
-          }
-          return at;
-        };
-        int next = look_up(0);
-        for (int j = 0; j < nt; ++j) {
-          int at[C::CHUNKS];
-#pragma unroll
-          for (int c = 0; c < C::CHUNKS; ++c) at[c] = __shfl_sync(0xffffffffu, next, c);
-          const int chunks = min(C::CHUNKS, it.NV - C::CHUNKS * j);
-          // a tile of new tokens that follow one another comes in one box a half
-          const bool run = at[0] < 0 && __all_sync(0xffffffffu, lane >= chunks || next == at[0] - 16 * lane);
-          if (j + 1 < nt) next = look_up(j + 1);
-          uint32_t issued = 2;  // of K and V
-          if (tc::elect()) {
-#pragma unroll 1
-            for (int sel = 0; sel < 2; ++sel) {
-              const uint32_t i = kvc + sel, b = i % C::NBUF;
-              if (i >= C::NBUF && !wn_wait1(&bar.kv_empty[b], (i / C::NBUF - 1) & 1, &s_abort, p.err)) {
-                issued = sel;
-                break;
-              }
-              uint8_t* dst = ring + b * C::KV_BYTES;
-              mbar_arrive_expect_tx(&bar.kv_full[b], run ? C::KV_BYTES : chunks * 16 * D * 2);
-              const CUtensorMap* mc = sel ? &tm_cv : &tm_ck;
-              const CUtensorMap* mn = sel ? &tm_v : &tm_k;
-              if (run) {
+            next = look_up(it, j + 1 < nt ? j + 1 : 0);
+          };
+          if (!(ok = load_tile(kc, where, min(C::CHUNKS, NV - C::CHUNKS * j), kh, ring_k, bar.k_full, bar.k_empty, &tm_ck, &tm_k,
+                               &tm_kt, peek)))
+            break;
+          ++kc;
+          if (j == 0) {
+            // the Q buffer is free once the previous item's S products are done (the first keys need not wait for that)
+            if (k > 0 && !wn_wait(&bar.q_empty, (k - 1) & 1, &s_abort, p.err)) { ok = false; break; }
+            if (tc::elect()) {
+              mbar_arrive_expect_tx(&bar.q_full, q_tiles * C::Q_BYTES);
+              for (int s = 0; s < q_tiles; ++s)
 #pragma unroll
                 for (int hf = 0; hf < C::HALVES; ++hf)
-                  tma_load_3d(dst + hf * C::KV_HALF, sel ? &tm_vt : &tm_kt, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, ~at[0]);
-              } else {
-#pragma unroll
-                for (int c = 0; c < C::CHUNKS; ++c)
-                  if (c < chunks)
-#pragma unroll
-                    for (int hf = 0; hf < C::HALVES; ++hf) {
-                      if (at[c] >= 0)
-                        tma_load_4d(dst + hf * C::KV_HALF + c * 2048, mc, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, 0, at[c]);
-                      else
-                        tma_load_3d(dst + hf * C::KV_HALF + c * 2048, mn, &bar.kv_full[b], 0, it.kh * C::HALVES + hf, ~at[c]);
-                    }
-              }
+                  tma_load_4d(sQ + s * C::Q_BYTES + hf * C::Q_HALF, &tm_q, &bar.q_full, 0, hf, kh * p.G, q_row + s * (128 / p.G));
             }
+            __syncwarp();
+            ++qn;
           }
-          issued = __reduce_min_sync(0xffffffffu, issued);
-          kvc += issued;
-          if (issued < 2) { ok = false; break; }
         }
       }
-      if (!ok || *static_cast<volatile int*>(&s_abort)) {
-        // a wait gave up: the loads in flight are waited for (bounded), so that none lands after the CTA is gone
-        for (uint32_t i = kvc > C::NBUF ? kvc - C::NBUF : 0; i < kvc; ++i)
-          mbar_wait(&bar.kv_full[i % C::NBUF], (i / C::NBUF) & 1, p.err);
+      if (!ok) {
+        drain(kc, bar.k_full);
         if (qn > 0) mbar_wait(&bar.q_full, (qn - 1) & 1, p.err);
       }
+    } else if (warp == C::W_V) {
+      // ======================= V =======================
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tm_vt);
+        if (p.seq_lens != nullptr) tma_prefetch_desc(&tm_cv);
+      }
+      uint32_t vc = 0;
+      bool ok = true;
+      for (uint32_t k = 0; ok; ++k) {
+        const WnItem* taken = take(k);
+        if (taken == nullptr) break;
+        const WnItem it = *taken;
+        release(k);
+        const int nt = it.tiles();
+        int next = look_up(it, 0);
+        for (int j = 0; j < nt; ++j) {
+          const int where = next;
+          auto peek = [&]() {
+            if (j + 1 < nt) next = look_up(it, j + 1);
+          };
+          if (!(ok = load_tile(vc, where, min(C::CHUNKS, it.NV - C::CHUNKS * j), it.kh, ring_v, bar.v_full, bar.v_empty, &tm_cv,
+                               &tm_v, &tm_vt, peek)))
+            break;
+          ++vc;
+        }
+      }
+      if (*static_cast<volatile int*>(&s_abort)) drain(vc, bar.v_full);
     } else if (warp == C::W_MMA) {
       // ======================= MMA issuer =======================
       if (tc::elect()) {
@@ -643,8 +696,8 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         // offset; the high word is the same for all.
         constexpr uint32_t kLboK = (16u >> 4) << 16, kLboV = (static_cast<uint32_t>(C::KV_HALF) >> 4) << 16;
         auto desc = [](uint32_t lo) { return (static_cast<uint64_t>((1024u >> 4) | 1u << 14 | 2u << 29) << 32) | lo; };
-        const uint32_t ring_at = smem_u32(ring) >> 4, q_at = smem_u32(sQ) >> 4;
-        uint32_t kvc = 0;             // K and V tiles of the items before this one
+        const uint32_t k_at = smem_u32(ring_k) >> 4, v_at = smem_u32(ring_v) >> 4, q_at = smem_u32(sQ) >> 4;
+        uint32_t tc0 = 0;             // key tiles of the items before this one
         uint32_t pn0 = 0, pn1 = 0;    // P V products of each slot
         bool ok = true;
         auto wait = [&](uint64_t* b, uint32_t parity) {
@@ -652,13 +705,13 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           tc::fence_after_sync();
           return true;
         };
-        auto kbuf = [&](int j) { return (kvc + 2 * j) % C::NBUF; };
-        auto vbuf = [&](int j) { return (kvc + 2 * j + 1) % C::NBUF; };
-        auto k_there = [&](int j) { return wait(&bar.kv_full[kbuf(j)], ((kvc + 2 * j) / C::NBUF) & 1); };
-        auto v_there = [&](int j) { return wait(&bar.v_ready[vbuf(j)], ((kvc + 2 * j + 1) / C::NBUF) & 1); };
+        auto buf = [&](int j) { return (tc0 + j) % C::NBUF; };
+        auto phase = [&](int j) { return ((tc0 + j) / C::NBUF) & 1; };
+        auto k_there = [&](int j) { return wait(&bar.k_full[buf(j)], phase(j)); };
+        auto v_there = [&](int j) { return wait(&bar.v_ready[buf(j)], phase(j)); };
         // S = Q K^T of tile j (N = 16 chunks)
         auto qk = [&](int slot, int qtile, int j, int chunks) {
-          const uint32_t qa = (q_at + qtile * (C::Q_BYTES >> 4)) | kLboK, kb = (ring_at + kbuf(j) * (C::KV_BYTES >> 4)) | kLboK;
+          const uint32_t qa = (q_at + qtile * (C::Q_BYTES >> 4)) | kLboK, kb = (k_at + buf(j) * (C::KV_BYTES >> 4)) | kLboK;
           const uint32_t idesc = kQk | static_cast<uint32_t>(2 * chunks) << 17;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
@@ -667,15 +720,21 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           tc::commit(&bar.s_full[slot]);
         };
         // O += P V of tile j, in two parts as its P comes
+        auto pv_part = [&](int slot, int j, int chunks, bool acc, int h) {
+          const uint32_t vb = (v_at + buf(j) * (C::KV_BYTES >> 4)) | kLboV;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 4 * h + i;
+            if (c < chunks)
+              tc::mma_ts(tmem + wn_ocol(slot), tmem + wn_scol(slot) + c * 8, desc(vb + c * 128), kPv, (acc || c > 0) ? 1u : 0u);
+          }
+        };
         auto pv = [&](int slot, int j, int chunks, bool acc) {
-          const uint32_t n = slot ? pn1 : pn0, vb = (ring_at + vbuf(j) * (C::KV_BYTES >> 4)) | kLboV;
+          const uint32_t n = slot ? pn1 : pn0;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (!wait(&bar.p_full[slot][h], n & 1)) return false;
-#pragma unroll
-            for (int c = 4 * h; c < 4 * h + 4; ++c)
-              if (c < chunks)
-                tc::mma_ts(tmem + wn_ocol(slot), tmem + wn_scol(slot) + c * 8, desc(vb + c * 128), kPv, (acc || c > 0) ? 1u : 0u);
+            pv_part(slot, j, chunks, acc, h);
           }
           if (slot) ++pn1; else ++pn0;
           return true;
@@ -693,41 +752,66 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
             if (!(ok = k_there(0))) break;
             qk(0, 0, 0, chunks(0));
             qk(1, 1, 0, chunks(0));
-            tc::commit(&bar.kv_empty[kbuf(0)]);
+            tc::commit(&bar.k_empty[buf(0)]);
+            if (!(ok = v_there(0)) || (nt > 1 && !(ok = k_there(1)))) break;
             for (int j = 0; j < nt; ++j) {
-              // (what the next products need is waited for before P, which comes last)
+              // (a tile's V and the next one's K are waited for while products run that were issued before)
               const bool more = j + 1 < nt;
               if (!more) tc::commit(&bar.q_empty);
-              if (!(ok = v_there(j)) || (more && !(ok = k_there(j + 1))) || !(ok = pv(0, j, chunks(j), j > 0))) break;
+              if (!(ok = pv(0, j, chunks(j), j > 0))) break;
               if (more)
                 qk(0, 0, j + 1, chunks(j + 1));
               else
                 tc::commit(&bar.o_final[0]);
+              if (j + 2 < nt && !(ok = k_there(j + 2))) break;
               if (!(ok = pv(1, j, chunks(j), j > 0))) break;
+              tc::commit(&bar.v_empty[buf(j)]);
               if (more) {
                 qk(1, 1, j + 1, chunks(j + 1));
-                tc::commit(&bar.kv_empty[kbuf(j + 1)]);
+                tc::commit(&bar.k_empty[buf(j + 1)]);
+                if (!(ok = v_there(j + 1))) break;
               }
-              tc::commit(&bar.kv_empty[vbuf(j)]);
             }
             if (ok) tc::commit(&bar.o_final[1]);
           } else {
-            // the tiles go to the slots in turn; S runs ahead as far as the slots' columns reach
-            for (int j = -2; j < nt; ++j) {
-              if (j >= 0) {
-                if (!(ok = v_there(j)) || !(ok = pv(j & 1, j, chunks(j), j > 1))) break;
-                tc::commit(&bar.kv_empty[vbuf(j)]);
+            // The tiles go to the slots in turn, and what is issued next is what is there: S of tile jq (its slot's P V
+            // is issued then), or a part of P V of tile jp. (In a fixed order P V of one tile waits for K of the
+            // next but one, and the ring of V with it.)
+            int jq = 0, jp = 0, h = 0;
+            uint64_t t0 = 0;
+            uint32_t idle = 0;
+            while (jp < nt) {
+              const int s = jp & 1;
+              if (jq < nt && jq < jp + 2 && mbar_test(&bar.k_full[buf(jq)], phase(jq))) {
+                tc::fence_after_sync();
+                qk(jq & 1, 0, jq, chunks(jq));
+                tc::commit(&bar.k_empty[buf(jq)]);
+                if (++jq == nt) tc::commit(&bar.q_empty);
+                idle = 0;
+              } else if (jp < jq && mbar_test(&bar.p_full[s][h], (s ? pn1 : pn0) & 1) &&
+                         mbar_test(&bar.v_ready[buf(jp)], phase(jp))) {
+                tc::fence_after_sync();
+                pv_part(s, jp, chunks(jp), jp > 1, h);
+                if (h == 1) {
+                  tc::commit(&bar.v_empty[buf(jp)]);
+                  if (s) ++pn1; else ++pn0;
+                  ++jp;
+                }
+                h ^= 1;
+                idle = 0;
+              } else if ((++idle & 255u) == 0) {  // (bounded, as wn_wait1)
+                const uint64_t now = globaltimer_ns();
+                if (idle == 256u) t0 = now;
+                if (now - t0 > kWaitLimitNs) {
+                  flag_error(p.err, PKV_DEVERR_TIMEOUT);
+                  *static_cast<volatile int*>(&s_abort) = 1;
+                }
+                if (*static_cast<volatile int*>(&s_abort)) { ok = false; break; }
               }
-              if (j + 2 < nt) {
-                if (!(ok = k_there(j + 2))) break;
-                qk(j & 1, 0, j + 2, chunks(j + 2));
-                tc::commit(&bar.kv_empty[kbuf(j + 2)]);
-              }
-              if (j + 2 == nt - 1) tc::commit(&bar.q_empty);
             }
             if (ok) tc::commit(&bar.o_both);
           }
-          kvc += 2 * nt;
+          tc0 += nt;
         }
         if (!ok) {  // the products in flight are waited for (bounded) before tensor memory is freed
           tc::commit(&bar.drained);
@@ -737,9 +821,8 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       __syncwarp();
     } else {
       // ======================= value rows that no row sees =======================
-      const int ft = tid - C::W_FIX * 32;
-      const uint32_t ring_base = smem_u32(ring);
-      uint32_t kvc = 0;
+      const uint32_t ring_base = smem_u32(ring_v);
+      uint32_t vc = 0;
       bool ok = true;
       for (uint32_t k = 0; ok; ++k) {
         const WnItem* taken = take(k);
@@ -747,13 +830,13 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         const WnItem it = *taken;
         release(k);
         const int nt = it.tiles(), last = it.last(), sinks = p.sinks;
-        for (int j = 0; j < nt; ++j, kvc += 2) {
-          const int b = (kvc + 1) % C::NBUF;
-          if (!wn_wait(&bar.kv_full[b], ((kvc + 1) / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
+        for (int j = 0; j < nt; ++j, ++vc) {
+          const int b = vc % C::NBUF;
+          if (!wn_wait(&bar.v_full[b], (vc / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
           if (!it.full(j)) {
             const uint32_t tile = ring_base + b * C::KV_BYTES;
 #pragma unroll 1
-            for (int R = ft; R < C::BN; R += 32 * C::NFIX) {
+            for (int R = lane; R < C::BN; R += 32) {
               const int v = C::CHUNKS * j + R / 16;
               if (v >= it.NV) continue;  // (no product takes it)
               const int u = it.chunk(v), key = it.pos(u) + R % 16;
