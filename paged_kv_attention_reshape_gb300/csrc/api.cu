@@ -120,8 +120,8 @@ bool encode_packed_q(CUtensorMap* m, const void* base, int64_t rows, int heads, 
 }
 
 // TMA map over one paged cache tensor: dims (64, Hkv*D/64, block_size, num_blocks), box
-// 64 x 1 x block_size x 1 (one 64-wide half of one head of one block), 128-byte swizzle.
-bool encode_cache(CUtensorMap* m, const void* base, const pkv_cache& c) {
+// 64 x 1 x block_size (or `box_rows`) x 1 (one 64-wide half of one head of one block), 128-byte swizzle.
+bool encode_cache(CUtensorMap* m, const void* base, const pkv_cache& c, int box_rows = 0) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   const int D = c.head_dim;
@@ -142,7 +142,7 @@ bool encode_cache(CUtensorMap* m, const void* base, const pkv_cache& c) {
                         static_cast<cuuint64_t>(c.block_size), static_cast<cuuint64_t>(c.num_blocks)};
   cuuint64_t strides[3] = {128, static_cast<cuuint64_t>(c.num_kv_heads) * D * 2,
                            static_cast<cuuint64_t>(c.stride_block) * 2};
-  cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(c.block_size), 1};
+  cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows > 0 ? box_rows : c.block_size), 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -847,17 +847,25 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   p.sinks = sinks;
   p.k_scales = cache ? cache->k_scales : nullptr;
   p.v_scales = cache ? cache->v_scales : nullptr;
-  CUtensorMap tq, tk, tv, tck, tcv, tqf, tkt, tvt;
+  CUtensorMap tq, tk, tv, tck, tcv, tqf, tk16, tv16;
   std::memset(&tck, 0, sizeof tck);
   std::memset(&tcv, 0, sizeof tcv);
   const bool windowed = window > 0 && ctx_kind == kAttnCtxBf16, packed = ctx_kind == kAttnCtxBlock;
-  const int rows = windowed ? 16 : 128;  // of a box of new keys
   if (!(packed || windowed ? encode_packed_q(&tq, q, num_tokens, Hq, p.G, D) : encode_rows(&tq, q, num_tokens, Hq, D, 128)) ||
-      !encode_rows(&tk, k, num_tokens, Hkv, D, rows) ||
-      !encode_rows(&tv, v, num_tokens, Hkv, D, rows) || !encode_rows(&tqf, q, num_tokens * Hq, 1, D, 128))
+      !encode_rows(&tk, k, num_tokens, Hkv, D, 128) ||
+      !encode_rows(&tv, v, num_tokens, Hkv, D, 128) || !encode_rows(&tqf, q, num_tokens * Hq, 1, D, 128))
     return PKV_ERR_CUDA;
-  if (windowed && (!encode_rows(&tkt, k, num_tokens, Hkv, D, 128) || !encode_rows(&tvt, v, num_tokens, Hkv, D, 128)))
-    return PKV_ERR_CUDA;
+  if (windowed) {
+    // 16 new rows as a box like that of a block: the rows as one block of all tokens
+    pkv_cache as_block{};
+    as_block.num_blocks = 1;
+    as_block.block_size = static_cast<int32_t>(num_tokens);
+    as_block.num_kv_heads = Hkv;
+    as_block.head_dim = D;
+    as_block.stride_block = num_tokens * Hkv * D;
+    as_block.kv_dtype = PKV_KV_BF16;
+    if (!encode_cache(&tk16, k, as_block, 16) || !encode_cache(&tv16, v, as_block, 16)) return PKV_ERR_CUDA;
+  }
   if (cache != nullptr &&
       (!encode_cache(&tck, cache->k, *cache) || !encode_cache(&tcv, cache->v, *cache)))
     return PKV_ERR_CUDA;
@@ -866,7 +874,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
     p.set_offset = off;
     p.sched_slot = next_sched_slot(reinterpret_cast<cudaStream_t>(stream));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    st = cuda_status(windowed ? launch_attn_window(p, tq, tk, tv, tkt, tvt, tck, tcv, D, s, &launches)
+    st = cuda_status(windowed ? launch_attn_window(p, tq, tk16, tv16, tk, tv, tck, tcv, D, s, &launches)
                      : packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, workspace, s, &launches)
                               : launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
                                                  s, &launches));

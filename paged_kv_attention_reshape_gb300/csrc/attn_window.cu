@@ -70,7 +70,9 @@ struct WnCfg {
   static constexpr int PERM_OFF = START_OFF + (MAXR + 4) * 4;   // set positions by cost, heaviest first
   static constexpr int ITEM_OFF = PERM_OFF + MAXR * 4;
   static constexpr int MERGE_OFF = ITEM_OFF + ITEM_RING * 64;   // [slot][128] {m, l} of split items
-  static constexpr int BAR_OFF = MERGE_OFF + 2 * 128 * 8;
+  // output staging: per softmax warp, 32 rows x 32 bf16 columns (64-byte rows, 64-byte swizzle)
+  static constexpr int STAGE_OFF = (MERGE_OFF + 2 * 128 * 8 + 127) / 128 * 128;
+  static constexpr int BAR_OFF = STAGE_OFF + 8 * 2048;
 };
 struct WnBars {
   uint64_t q_full, q_empty;
@@ -362,7 +364,9 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           if (!it.full(j)) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
+              // (a warp's rows are few tokens: they see most groups of 32 keys whole or not at all)
               const uint32_t seen = wn_seen(p, it, 8 * j + 2 * c, at);
+              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[c][e] = (seen >> e) & 1u ? v[c][e] : 0xFF800000u;
             }
@@ -436,6 +440,33 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       const int64_t row = static_cast<int64_t>(it.row0) + tok;
       const bool write = tok < it.tok0 + it.ntok && row < p.num_tokens;
       const int64_t flat = row * p.Hq + it.kh * p.G + (t & (p.G - 1));  // (128 is a multiple of G)
+      // 32 columns of the warp's rows to `out` from column col on, through the warp's staging tile: a store then
+      // writes 64 bytes of each of 8 rows (of 32 rows 16 bytes, four times the cache lines: 3500 clocks an item)
+      const uint32_t stage = smem_u32(smem) + C::STAGE_OFF + warp * 2048;
+      auto put = [&](const uint32_t (&o)[32], float f, const uint32_t (&o1)[32], float f1, int col) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            // (a factor 0 stands for a part without keys: what its O holds is not read as a number)
+            x[e] = f == 0.f ? 0.f : __uint_as_float(o[8 * q + e]) * f;
+            if (&o != &o1) x[e] = f1 == 0.f ? x[e] : fmaf(__uint_as_float(o1[8 * q + e]), f1, x[e]);
+          }
+          // 16-byte chunk q of row `lane`, 64-byte swizzle: conflict-free both ways
+          st_shared_v4(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4),
+                       make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 2), kk = lane & 3;  // row of the warp's 32, 16-byte chunk
+          const uint4 v = ld_shared_v4(stage + rr * 64 + ((kk ^ ((rr >> 1) & 3)) << 4));
+          const int64_t to = __shfl_sync(0xffffffffu, write ? flat : -1, rr);
+          if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * D + col + kk * 8) = v;
+        }
+        __syncwarp();
+      };
       if (!it.split) {
         if (!wn_wait(&bar.o_final[slot], oc & 1, &s_abort, p.err)) break;
         ++oc;
@@ -448,16 +479,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
             tc::ld32(lane_at + wn_ocol(slot) + c * 32, o);
             tc::wait_ld();
             tc::touch32(o);
-            if (write) {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + flat * D + c * 32);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * q + e]) * inv;
-                dst[q] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-              }
-            }
+            put(o, inv, o, 0.f, c * 32);
           }
           if (write && p.lse) p.lse[flat] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
         }
@@ -477,7 +499,6 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       if (live) {
         const float2 a = mrg[t], b = mrg[128 + t];
         const float mm = fmaxf(a.x, b.x);
-        // (a slot without a key for the row has l = 0; what its O holds is not read as a number)
         const float w0 = a.y == 0.f ? 0.f : ex2_approx(a.x - mm), w1 = b.y == 0.f ? 0.f : ex2_approx(b.x - mm);
         const float sum = a.y * w0 + b.y * w1, inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
@@ -489,19 +510,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           tc::wait_ld();
           tc::touch32(o0);
           tc::touch32(o1);
-          if (write) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + flat * D + col);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float x[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                x[e] = w0 == 0.f ? 0.f : __uint_as_float(o0[8 * q + e]) * (w0 * inv);
-                x[e] = w1 == 0.f ? x[e] : fmaf(__uint_as_float(o1[8 * q + e]), w1 * inv, x[e]);
-              }
-              dst[q] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-            }
-          }
+          put(o0, w0 * inv, o1, w1 * inv, col);
         }
         if (write && slot == 0 && p.lse)
           p.lse[flat] = sum == 0.f ? -CUDART_INF_F : (mm + __log2f(sum)) * 0.69314718055994531f;
@@ -543,7 +552,6 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       for (int c = 0; c < C::CHUNKS; ++c) at[c] = __shfl_sync(0xffffffffu, where, c);
       // a tile of new tokens that follow one another comes in one box a half
       const bool run = at[0] < 0 && __all_sync(0xffffffffu, lane >= chunks || where == at[0] - 16 * lane);
-      const bool cached = __all_sync(0xffffffffu, lane >= chunks || where >= 0);
       peek();
       const uint32_t b = i % C::NBUF;
       bool ok = true;
@@ -556,23 +564,17 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
 #pragma unroll
             for (int hf = 0; hf < C::HALVES; ++hf)
               tma_load_3d(dst + hf * C::KV_HALF, tile, &full[b], 0, kh * C::HALVES + hf, ~at[0]);
-          } else if (cached && chunks == C::CHUNKS) {
+          } else {
+            // (a chunk of new rows is a 4-D box like a block's, the rows' coordinate in place of the block's)
 #pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c)
+            for (int c = 0; c < C::CHUNKS; ++c) {
+              if (c >= chunks) break;
+              const CUtensorMap* map = at[c] >= 0 ? cache : rows;
+              const int row = at[c] >= 0 ? 0 : ~at[c], blk = at[c] >= 0 ? at[c] : 0;
 #pragma unroll
               for (int hf = 0; hf < C::HALVES; ++hf)
-                tma_load_4d(dst + hf * C::KV_HALF + c * 2048, cache, &full[b], 0, kh * C::HALVES + hf, 0, at[c]);
-          } else {
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c)
-              if (c < chunks)
-#pragma unroll
-                for (int hf = 0; hf < C::HALVES; ++hf) {
-                  if (at[c] >= 0)
-                    tma_load_4d(dst + hf * C::KV_HALF + c * 2048, cache, &full[b], 0, kh * C::HALVES + hf, 0, at[c]);
-                  else
-                    tma_load_3d(dst + hf * C::KV_HALF + c * 2048, rows, &full[b], 0, kh * C::HALVES + hf, ~at[c]);
-                }
+                tma_load_4d(dst + hf * C::KV_HALF + c * 2048, map, &full[b], 0, kh * C::HALVES + hf, row, blk);
+            }
           }
         }
       }

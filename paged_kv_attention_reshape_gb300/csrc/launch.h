@@ -269,7 +269,7 @@ constexpr int kAttnCtxBlock = 3;
 cudaError_t launch_attn_scaled(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& tck, const CUtensorMap& tcv, void* workspace, cudaStream_t stream, int* launches);
 // Windowed extend and prefill over bf16 (p.window >= 1): tm_q as for launch_attn_scaled, tm_k and tm_v over the packed
-// new keys and values in boxes of 16 rows, tkt and tvt in boxes of 128.
+// new keys and values as (64, D/64 * Hkv, T, 1) in boxes of 16 rows, tkt and tvt as for launch_attention.
 cudaError_t launch_attn_window(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, int D, cudaStream_t stream, int* launches);
 size_t attn_scaled_workspace(int32_t max_q_len, int32_t max_seq_len, int G);
