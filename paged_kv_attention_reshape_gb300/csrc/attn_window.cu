@@ -180,18 +180,23 @@ __device__ __forceinline__ bool wn_wait(uint64_t* bar, uint32_t parity, volatile
 // The low n bits (none, or all 32, beyond that range).
 __device__ __forceinline__ uint32_t wn_below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
-// Which of the 32 keys of chunks v and v + 1 of the walk the row at position i sees, a bit each.
-__device__ __forceinline__ uint32_t wn_seen(const AttnParams& p, const WnItem& it, int v, int i) {
-  uint32_t bits = 0;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int u = it.chunk(v + c), base = it.pos(u);
-    const int end = v + c < it.NV ? min(i + 1, u < it.cb ? it.C : INT_MAX) - base : 0;
-    const uint32_t b = wn_below(end) & (wn_below(p.sinks - base) | ~wn_below(i - p.window + 1 - base)) & 0xFFFFu;
-    bits |= b << (16 * c);
+// What a row sees of a walk, in walk columns (column x is key x % 16 of chunk x / 16): those before `sinks` and
+// those from `from` on, up to its own, `end` - 1, without the hole behind the last cached token.
+struct WnRow {
+  int sinks, from, end, hole0, hole1;
+  __device__ WnRow(const AttnParams& p, const WnItem& it, int i) {  // the row at position i >= C
+    const int C = it.C, cols = 16 * it.cb, gap = 16 * it.gap, low = i - p.window + 1;
+    sinks = p.sinks <= C ? p.sinks : min(p.sinks, i + 1) - C + cols;
+    from = (low < C ? low : low - C + cols) - gap;
+    end = i - C + cols - gap + 1;
+    hole0 = C - (it.cb - 1 < it.head ? 0 : gap);
+    hole1 = it.vt < 0 ? hole0 : hole0 + (cols - C);
   }
-  return bits;
-}
+  // which of the columns x .. x + 31, a bit each
+  __device__ uint32_t seen(int x) const {
+    return wn_below(end - x) & (wn_below(sinks - x) | ~wn_below(from - x)) & (wn_below(hole0 - x) | ~wn_below(hole1 - x));
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
@@ -349,7 +354,8 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       bool ok = true;
       const int tok = it.tok0 + (((it.split ? 0 : slot * 128) + t) >> shift);
       const bool live = __any_sync(0xffffffffu, tok < it.tok0 + it.ntok);  // the warp has rows of the item
-      const int at = it.C + tok, nt = it.tiles(), first = it.split ? slot : 0;
+      const int nt = it.tiles(), first = it.split ? slot : 0;
+      const WnRow sees(p, it, it.C + tok);
       for (int j = first; j < nt; j += 1 + it.split, ++sc) {
         if (!wn_wait(&bar.s_full[slot], sc & 1, &s_abort, p.err)) { ok = false; break; }
         tc::fence_after_sync();
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               // (a warp's rows are few tokens: they see most groups of 32 keys whole or not at all)
-              const uint32_t seen = wn_seen(p, it, 8 * j + 2 * c, at);
+              const uint32_t seen = sees.seen(128 * j + 32 * c);
               if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[c][e] = (seen >> e) & 1u ? v[c][e] : 0xFF800000u;
@@ -443,15 +449,27 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       // 32 columns of the warp's rows to `out` from column col on, through the warp's staging tile: a store then
       // writes 64 bytes of each of 8 rows (of 32 rows 16 bytes, four times the cache lines: 3500 clocks an item)
       const uint32_t stage = smem_u32(smem) + C::STAGE_OFF + warp * 2048;
+      __nv_bfloat16* dst[4];  // row 8 i + lane / 4 of the warp's (NULL: not there), from 16-byte chunk lane % 4 on
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tr = quad * 32 + 8 * i + (lane >> 2), tk = it.tok0 + (((it.split ? 0 : slot * 128) + tr) >> shift);
+        const int64_t rw = static_cast<int64_t>(it.row0) + tk;
+        dst[i] = tk < it.tok0 + it.ntok && rw < p.num_tokens
+                     ? p.out + (rw * p.Hq + it.kh * p.G + (tr & (p.G - 1))) * D + (lane & 3) * 8
+                     : nullptr;
+      }
       auto put = [&](const uint32_t (&o)[32], float f, const uint32_t (&o1)[32], float f1, int col) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float x[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            // (a factor 0 stands for a part without keys: what its O holds is not read as a number)
-            x[e] = f == 0.f ? 0.f : __uint_as_float(o[8 * q + e]) * f;
-            if (&o != &o1) x[e] = f1 == 0.f ? x[e] : fmaf(__uint_as_float(o1[8 * q + e]), f1, x[e]);
+            x[e] = __uint_as_float(o[8 * q + e]) * f;
+            if (&o != &o1) {
+              // (a factor 0 stands for a part without keys: what its O holds is not read as a number)
+              x[e] = f == 0.f ? 0.f : x[e];
+              x[e] = f1 == 0.f ? x[e] : fmaf(__uint_as_float(o1[8 * q + e]), f1, x[e]);
+            }
           }
           // 16-byte chunk q of row `lane`, 64-byte swizzle: conflict-free both ways
           st_shared_v4(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4),
@@ -462,8 +480,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         for (int i = 0; i < 4; ++i) {
           const int rr = i * 8 + (lane >> 2), kk = lane & 3;  // row of the warp's 32, 16-byte chunk
           const uint4 v = ld_shared_v4(stage + rr * 64 + ((kk ^ ((rr >> 1) & 3)) << 4));
-          const int64_t to = __shfl_sync(0xffffffffu, write ? flat : -1, rr);
-          if (to >= 0) *reinterpret_cast<uint4*>(p.out + to * D + col + kk * 8) = v;
+          if (dst[i] != nullptr) *reinterpret_cast<uint4*>(dst[i] + col) = v;
         }
         __syncwarp();
       };
@@ -473,13 +490,14 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         tc::fence_after_sync();
         if (live) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
+          uint32_t o[D / 32][32];
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) tc::ld32(lane_at + wn_ocol(slot) + c * 32, o[c]);
+          tc::wait_ld();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tc::ld32(lane_at + wn_ocol(slot) + c * 32, o);
-            tc::wait_ld();
-            tc::touch32(o);
-            put(o, inv, o, 0.f, c * 32);
+            tc::touch32(o[c]);
+            put(o[c], inv, o[c], 0.f, c * 32);
           }
           if (write && p.lse) p.lse[flat] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
         }
