@@ -361,22 +361,30 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         tc::fence_after_sync();
         if (live) {
           const uint32_t srow = lane_at + wn_scol(slot);
+          if (!it.full(j)) {
+            // What is hidden becomes -inf in tensor memory, 32 columns at a time (a warp's rows are few tokens: they see
+            // most such groups whole). In registers, with the four groups' code in a row, it is fetched anew
+            // for nearly every edge tile: 1340 clocks.
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t seen = sees.seen(128 * j + 32 * c);
+              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+              uint32_t x[32];
+              tc::ld32(srow + 32 * c, x);
+              tc::wait_ld();
+              tc::touch32(x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = (seen >> e) & 1u ? x[e] : 0xFF800000u;
+              tc::st32(srow + 32 * c, x);
+            }
+            tc::wait_st();
+          }
           uint32_t v[4][32];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc::ld32(srow + 32 * c, v[c]);
           tc::wait_ld();
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
-          if (!it.full(j)) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              // (a warp's rows are few tokens: they see most groups of 32 keys whole or not at all)
-              const uint32_t seen = sees.seen(128 * j + 32 * c);
-              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[c][e] = (seen >> e) & 1u ? v[c][e] : 0xFF800000u;
-            }
-          }
           // row max of the raw scores (the scale is positive, so it commutes with max)
           float mq[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
@@ -490,14 +498,13 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         tc::fence_after_sync();
         if (live) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          uint32_t o[D / 32][32];
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) tc::ld32(lane_at + wn_ocol(slot) + c * 32, o[c]);
-          tc::wait_ld();
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            tc::touch32(o[c]);
-            put(o[c], inv, o[c], 0.f, c * 32);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {  // (unrolled, its code is fetched anew for every item: 3500 clocks)
+            uint32_t o[32];
+            tc::ld32(lane_at + wn_ocol(slot) + c * 32, o);
+            tc::wait_ld();
+            tc::touch32(o);
+            put(o, inv, o, 0.f, c * 32);
           }
           if (write && p.lse) p.lse[flat] = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * 0.69314718055994531f;
         }
@@ -519,7 +526,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         const float mm = fmaxf(a.x, b.x);
         const float w0 = a.y == 0.f ? 0.f : ex2_approx(a.x - mm), w1 = b.y == 0.f ? 0.f : ex2_approx(b.x - mm);
         const float sum = a.y * w0 + b.y * w1, inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           const int col = slot * (D / 2) + c * 32;
           uint32_t o0[32], o1[32];
@@ -769,30 +776,30 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           auto chunks = [&](int j) { return min(C::CHUNKS, NV - C::CHUNKS * j); };
           if (!wait(&bar.q_full, k & 1)) { ok = false; break; }
           if (!split) {
+            // P V of tile t - 1 and S of tile t, slot by slot (one place in the code for each, so that it stays in
+            // the instruction cache beside the other roles'). What is there first is waited for while products run
+            // that were issued before.
             if (!(ok = k_there(0))) break;
-            qk(0, 0, 0, chunks(0));
-            qk(1, 1, 0, chunks(0));
-            tc::commit(&bar.k_empty[buf(0)]);
-            if (!(ok = v_there(0)) || (nt > 1 && !(ok = k_there(1)))) break;
-            for (int j = 0; j < nt; ++j) {
-              // (a tile's V and the next one's K are waited for while products run that were issued before)
-              const bool more = j + 1 < nt;
-              if (!more) tc::commit(&bar.q_empty);
-              if (!(ok = pv(0, j, chunks(j), j > 0))) break;
-              if (more)
-                qk(0, 0, j + 1, chunks(j + 1));
-              else
-                tc::commit(&bar.o_final[0]);
-              if (j + 2 < nt && !(ok = k_there(j + 2))) break;
-              if (!(ok = pv(1, j, chunks(j), j > 0))) break;
-              tc::commit(&bar.v_empty[buf(j)]);
-              if (more) {
-                qk(1, 1, j + 1, chunks(j + 1));
-                tc::commit(&bar.k_empty[buf(j + 1)]);
-                if (!(ok = v_there(j + 1))) break;
+            for (int t = 0; t <= nt && ok; ++t) {
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {
+                if (t > 0) {
+                  if (!(ok = pv(s, t - 1, chunks(t - 1), t > 1))) break;
+                  if (t == nt) tc::commit(&bar.o_final[s]);
+                  if (s == 1) tc::commit(&bar.v_empty[buf(t - 1)]);
+                }
+                if (t < nt) {
+                  qk(s, s, t, chunks(t));
+                  if (s == 0) {
+                    if (t + 1 < nt && !(ok = k_there(t + 1))) break;
+                  } else {
+                    tc::commit(&bar.k_empty[buf(t)]);
+                    if (t + 1 == nt) tc::commit(&bar.q_empty);
+                    if (!(ok = v_there(t))) break;
+                  }
+                }
               }
             }
-            if (ok) tc::commit(&bar.o_final[1]);
           } else {
             // The tiles go to the slots in turn, and what is issued next is what is there: S of tile jq (its slot's P V
             // is issued then), or a part of P V of tile jp. (In a fixed order P V of one tile waits for K of the
