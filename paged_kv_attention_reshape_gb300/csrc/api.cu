@@ -843,6 +843,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   p.scale_log2 = scale * 1.4426950408889634f;
   p.ctx_scale_log2 = scale * ctx_k_scale * 1.4426950408889634f;
   p.ctx_v_scale = ctx_v_scale;
+  p.ctx_k_scale = ctx_k_scale;
   p.window = window;
   p.sinks = sinks;
   p.k_scales = cache ? cache->k_scales : nullptr;
@@ -850,7 +851,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   CUtensorMap tq, tk, tv, tck, tcv, tqf, tk16, tv16;
   std::memset(&tck, 0, sizeof tck);
   std::memset(&tcv, 0, sizeof tcv);
-  const bool windowed = window > 0 && ctx_kind == kAttnCtxBf16, packed = ctx_kind == kAttnCtxBlock;
+  const bool windowed = window > 0, packed = ctx_kind == kAttnCtxBlock;
   if (!(packed || windowed ? encode_packed_q(&tq, q, num_tokens, Hq, p.G, D) : encode_rows(&tq, q, num_tokens, Hq, D, 128)) ||
       !encode_rows(&tk, k, num_tokens, Hkv, D, 128) ||
       !encode_rows(&tv, v, num_tokens, Hkv, D, 128) || !encode_rows(&tqf, q, num_tokens * Hq, 1, D, 128))
@@ -874,7 +875,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
     p.set_offset = off;
     p.sched_slot = next_sched_slot(reinterpret_cast<cudaStream_t>(stream));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    st = cuda_status(windowed ? launch_attn_window(p, tq, tk16, tv16, tk, tv, tck, tcv, D, s, &launches)
+    st = cuda_status(windowed ? launch_attn_window(p, tq, tk16, tv16, tk, tv, tck, tcv, D, ctx_kind == kAttnCtxFp8, s, &launches)
                      : packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, workspace, s, &launches)
                               : launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
                                                  s, &launches));

@@ -96,31 +96,7 @@ __device__ __forceinline__ constexpr uint32_t ocol(int slot) { return 256u + slo
 struct TcItem {
   int r, q_len, C, qr0, nrows, nct, NT, h0, nslot, kh, dec;
   int64_t row0;
-  // windowed attention: of the item's key tiles (context, then new) the ones before `head` hold sinks; the
-  // walk leaves out the `gap` tiles behind them that no row sees, so step j is tile j, or j + gap from `head` on
-  int head, gap;
-  int low, sinks;  // the keys that some row sees: positions below sinks and from low on
-  __device__ int tile(int j) const { return j < head ? j : j + gap; }
-  // position of the first key of a tile
-  __device__ int pos(int t) const { return t < nct ? t * 128 : C + (t - nct) * 128; }
-  // position of the item's last row
-  __device__ int last() const { return C + (dec ? 0 : qr0 + nrows - 1); }
-  // whether some row sees the key
-  __device__ bool seen(int key) const { return (key >= low || key < sinks) && key <= last(); }
 };
-
-// The tiles of an item that some row of it sees: those before `head`, which hold sinks, and those from the
-// first row's window on.
-__device__ __forceinline__ void tc_window(const AttnParams& p, TcItem& it) {
-  const int first = it.C + it.qr0;                             // the position of the item's first row
-  it.low = first >= p.window ? first - p.window + 1 : 0;        // the first key that its window holds
-  it.sinks = min(p.sinks, first + 1);
-  const int head = it.sinks <= it.C ? (it.sinks + 127) / 128 : it.nct + (it.sinks - it.C + 127) / 128;
-  const int from = it.low < it.C ? it.low / 128 : it.nct + (it.low - it.C) / 128;
-  it.head = min(head, it.NT);
-  it.gap = max(from - it.head, 0);
-  it.NT -= it.gap;
-}
 
 // Items of a set request: Hkv for a packed decode, (q-tiles) x HP otherwise.
 __device__ __forceinline__ bool tc_dec(const int4& q, int G) { return q.z == 1 && G >= 2; }
@@ -147,7 +123,6 @@ __device__ __forceinline__ void tc_resolve_set(const AttnParams& p, int& begin, 
 // Work item w (all roles walk the same sequence of items); s_req holds {request id, first
 // query row, q_len, cached tokens} of each request of the set, s_perm the set positions by
 // decreasing tile cost, s_start the prefix of items in that order.
-template <bool WIN>
 __device__ __forceinline__ TcItem tc_item(const AttnParams& p, const int* s_start, const int4* s_req,
                                           const int* s_perm, int n, int64_t w, int HP) {
   TcItem it;
@@ -172,7 +147,6 @@ __device__ __forceinline__ TcItem tc_item(const AttnParams& p, const int* s_star
     it.nslot = 1;
     it.kh = idx;
     it.h0 = idx * p.G;
-    if constexpr (WIN) tc_window(p, it);
     return it;
   }
   it.dec = 0;
@@ -185,7 +159,6 @@ __device__ __forceinline__ TcItem tc_item(const AttnParams& p, const int* s_star
   it.nslot = p.G >= 2 ? 2 : 1;
   it.h0 = p.G >= 2 ? 2 * hp : hp;
   it.kh = it.h0 / p.G;
-  if constexpr (WIN) tc_window(p, it);
   return it;
 }
 
@@ -227,14 +200,6 @@ __device__ __forceinline__ void mask_cols(uint32_t (&v)[32], int n) {
 #pragma unroll
   for (int e = 0; e < 32; ++e) v[e] = e < n ? v[e] : 0xFF800000u;
 }
-
-// Columns whose bit is not set become -inf.
-__device__ __forceinline__ void mask_bits(uint32_t (&v)[32], uint32_t bits) {
-#pragma unroll
-  for (int e = 0; e < 32; ++e) v[e] = (bits >> e) & 1u ? v[e] : 0xFF800000u;
-}
-// The low n bits (none, or all 32, beyond that range).
-__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
 // Bounded wait that also gives up as soon as another role has given up.
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
@@ -341,18 +306,13 @@ __device__ __forceinline__ void conv_bf16_row(uint32_t tile, int R, float sc, bo
 // core multiplies fp16 operands (kind::f16), P is packed as fp16, and the MMA warp waits on
 // the converters' barriers (q_conv, conv_full) instead of the loads'. Queries, new keys and
 // new values divided by vs must lie within the fp16 range.
-// WIN (kCtxFp8; over bf16 attn_window.cu serves windows): a key is seen by the rows up to p.window - 1 positions behind it, and by all
-// later ones if it is among the first p.sinks. Tiles that no row of the item sees are left out (tc_window),
-// pages that no row sees are not looked up, and value rows that no row sees are zeroed like those past the
-// context's end.
-template <int D, int KIND, bool WIN>
+template <int D, int KIND>
 __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kernel(
     const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __grid_constant__ CUtensorMap tm_ck, const __grid_constant__ CUtensorMap tm_cv,
     const __grid_constant__ CUtensorMap tm_qf) {
   using C = TcCfg<D, KIND>;
-  static_assert(!WIN || C::CONV, "windows over bf16 are attn_window.cu's");
   constexpr bool SCALED = KIND != kCtxBf16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -491,8 +451,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
       qtiles += __shfl_xor_sync(0xffffffffu, qtiles, o);
     }
-    // a window makes items alike and short, whatever the context
-    if (lane == 0) s_claim = p.sched_slot >= 0 && (WIN || tiles < static_cast<long long>(kDynamicBelow) * qtiles) ? 1 : 0;
+    if (lane == 0) s_claim = p.sched_slot >= 0 && tiles < static_cast<long long>(kDynamicBelow) * qtiles ? 1 : 0;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -527,7 +486,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         w_static = tc_next(w_static, odd);
       }
       if (w < 0) break;
-      const TcItem it = tc_item<WIN>(p, s_start, s_req, s_perm, n, w, HP);
+      const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
       if (slot >= it.nslot) continue;
       // query index of this row within its request (a packed decode's rows are heads of its one
       // token)
@@ -539,18 +498,14 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         ++sc;
         tc::fence_after_sync();
         // valid keys of this row in tile j: columns [0, kv) (context) or causal (new)
-        const int jt = WIN ? it.tile(j) : j;
         int kv;
-        if (jt < it.nct) kv = min(128, it.C - jt * 128);
-        else kv = min(128, qi - (jt - it.nct) * 128 + 1);
-        // WIN: of those, the columns from wlo on (the row's window) and the ones before wsink
-        const int wlo = WIN ? it.C + qi - p.window + 1 - it.pos(jt) : 0, wsink = WIN ? p.sinks - it.pos(jt) : 0;
-        auto cols = [&](int c0) { return below(kv - c0) & (below(wsink - c0) | ~below(wlo - c0)); };
-        const bool full = __all_sync(0xffffffffu, kv >= 128 && (!WIN || wlo <= 0 || wsink >= 128));
+        if (j < it.nct) kv = min(128, it.C - j * 128);
+        else kv = min(128, qi - (j - it.nct) * 128 + 1);
+        const bool full = __all_sync(0xffffffffu, kv >= 128);
         const uint32_t srow = tmem + lane_off + scol(slot);
         // a context tile of an FP8 cache holds the E4M3 values themselves: its key scale goes
         // with the softmax scale; a new-token tile packs P / vs (the row sum stays unscaled)
-        const bool ctx = jt < it.nct;
+        const bool ctx = j < it.nct;
         const float sl = SCALED && ctx ? p.ctx_scale_log2 : p.scale_log2;
         const bool vsc = KIND == kCtxPool && !ctx && p.ctx_v_scale != 1.f;
         float alpha = 1.f, rs = 0.f;
@@ -562,11 +517,6 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         tc::wait_ld();
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
-        if (WIN && !full) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mask_bits(v[c], cols(32 * c));
-          kv = 128;  // (what is hidden counts as -inf from here on)
-        }
         // row max of the raw scores (the scale is positive, so it commutes with max)
         float mx = -CUDART_INF_F;
         if (full) {
@@ -822,7 +772,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         w_static = tc_next(w_static, odd);
       }
       if (w < 0) break;
-      const TcItem it = tc_item<WIN>(p, s_start, s_req, s_perm, n, w, HP);
+      const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
       if (!C::CONV && items > 0 && lane == 0) {
         if (it.dec) {
 #pragma unroll
@@ -856,19 +806,12 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       }
       const int32_t* table = p.block_tables ? p.block_tables + static_cast<int64_t>(it.r) * p.max_blocks : nullptr;
       const int ctx_blocks = (it.C + 15) / 16;
-      for (int i = 0; i < it.NT && ok; ++i) {
-        const int j = WIN ? it.tile(i) : i;
+      for (int j = 0; j < it.NT && ok; ++j) {
         // per context tile: lanes 0..7 each own one 16-token block
         int blk = 0;
         if (j < it.nct && lane < 8) {
           const int lb = j * 8 + lane;
-          bool use = lb < ctx_blocks;
-          int any = j * 8;  // a block of the tile that is read in any case
-          if constexpr (WIN) {
-            use = use && (lb * 16 < it.sinks || lb * 16 + 15 >= it.low);
-            if (j * 128 >= it.sinks) any = max(any, it.low / 16);
-          }
-          blk = table[use ? lb : any];
+          blk = table[lb < ctx_blocks ? lb : j * 8];
           if (blk < 0 || blk >= p.num_blocks) {
             flag_error(p.err, PKV_DEVERR_BLOCK);
             blk = 0;
@@ -938,7 +881,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         w_static = tc_next(w_static, odd);
       }
       if (w < 0) break;
-      const TcItem it = tc_item<WIN>(p, s_start, s_req, s_perm, n, w, HP);
+      const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
       const bool two = it.nslot == 2;
       if (!tc_wait_warp(C::CONV ? q_conv : q_full, items & 1, &s_abort, p.err)) break;
       int prev_vbuf = -1;
@@ -1033,7 +976,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
         w_static = tc_next(w_static, odd);
       }
       if (w < 0) break;
-      const TcItem it = tc_item<WIN>(p, s_start, s_req, s_perm, n, w, HP);
+      const TcItem it = tc_item(p, s_start, s_req, s_perm, n, w, HP);
       if (!tc_wait_warp(q_full, k & 1, &s_abort, p.err)) break;
       for (int sl = 0; sl < it.nslot; ++sl)
 #pragma unroll
@@ -1041,11 +984,7 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_conv);
-      for (int i = 0; i < it.NT && ok; ++i) {
-        const int j = WIN ? it.tile(i) : i;
-        // (WIN) value rows that no row of the item sees become zeros too
-        const int p0 = WIN ? it.pos(j) : 0;
-        auto seen = [&](int row) { return !WIN || it.seen(p0 + row); };
+      for (int j = 0; j < it.NT && ok; ++j) {
         for (int kvsel = 0; kvsel < 2; ++kvsel, ++kvc) {
           const int buf = kvc % C::NBUF;
           const uint32_t use = kvc / C::NBUF;
@@ -1055,15 +994,14 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
             // V rows past the context end become zeros (P = 0 there must not meet a NaN code)
             const int valid = kvsel ? it.C - j * 128 : 128;
 #pragma unroll
-            for (int rr = 0; rr < 2; ++rr) conv_code_row(tile, ct + 64 * rr, ct + 64 * rr < valid && (!kvsel || seen(ct + 64 * rr)));
+            for (int rr = 0; rr < 2; ++rr) conv_code_row(tile, ct + 64 * rr, ct + 64 * rr < valid);
           } else {
             // new-token values are stored divided by vs; V rows past the request's own tokens
             // become zeros
             const int valid = kvsel ? it.q_len - (j - it.nct) * 128 : 128;
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr)
-              conv_bf16_row<C::HALVES>(tile, ct + 64 * rr, kvsel ? inv_vs : 1.f,
-                                       ct + 64 * rr < valid && (!kvsel || seen(ct + 64 * rr)));
+              conv_bf16_row<C::HALVES>(tile, ct + 64 * rr, kvsel ? inv_vs : 1.f, ct + 64 * rr < valid);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -1089,19 +1027,18 @@ __global__ void __launch_bounds__(TcCfg<D, KIND>::THREADS, 1) attention_tc_kerne
   }
 }
 
-template <int D, int KIND, bool WIN>
+template <int D, int KIND>
 static cudaError_t launch_attention_tc_impl(const AttnParams& p, const CUtensorMap& tq,
                                             const CUtensorMap& tk, const CUtensorMap& tv,
                                             const CUtensorMap& tck, const CUtensorMap& tcv,
                                             const CUtensorMap& tqf, cudaStream_t stream, int* launches) {
   using C = TcCfg<D, KIND>;
-  const int slot = WIN               ? kAttrWinAttn128Fp8
-                   : KIND == kCtxFp8 ? kAttrAttn128Fp8
+  const int slot = KIND == kCtxFp8 ? kAttrAttn128Fp8
                                    : (KIND == kCtxPool ? (D == 64 ? kAttrAttn64Scaled : kAttrAttn128Scaled)
                                                        : (D == 64 ? kAttrAttn64 : kAttrAttn128));
-  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attention_tc_kernel<D, KIND, WIN>), C::SMEM, slot);
+  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attention_tc_kernel<D, KIND>), C::SMEM, slot);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attention_tc_kernel<D, KIND, WIN>, dim3(num_sms()), dim3(C::THREADS), C::SMEM, stream, p, tq, tk, tv,
+  e = launch_pdl(attention_tc_kernel<D, KIND>, dim3(num_sms()), dim3(C::THREADS), C::SMEM, stream, p, tq, tk, tv,
                  tck, tcv, tqf);
   *launches += 1;
   return e;
@@ -1111,18 +1048,14 @@ cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_q, const
                              const CUtensorMap& tm_v, const CUtensorMap& tm_ck,
                              const CUtensorMap& tm_cv, const CUtensorMap& tm_qf, int D, int ctx_kind,
                              cudaStream_t stream, int* launches) {
-  if (p.window > 0) {
-    if (ctx_kind != kAttnCtxFp8 || D != 128) return cudaErrorInvalidValue;
-    return launch_attention_tc_impl<128, kCtxFp8, true>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
-  }
   if (ctx_kind == kAttnCtxFp8) {
     if (D != 128) return cudaErrorInvalidValue;
-    return launch_attention_tc_impl<128, kCtxFp8, false>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
+    return launch_attention_tc_impl<128, kCtxFp8>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
   }
   if (ctx_kind == kAttnCtxPool)
-    return D == 64 ? launch_attention_tc_impl<64, kCtxPool, false>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches)
-                   : launch_attention_tc_impl<128, kCtxPool, false>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
-  return D == 64 ? launch_attention_tc_impl<64, kCtxBf16, false>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches)
-                 : launch_attention_tc_impl<128, kCtxBf16, false>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
+    return D == 64 ? launch_attention_tc_impl<64, kCtxPool>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches)
+                   : launch_attention_tc_impl<128, kCtxPool>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
+  return D == 64 ? launch_attention_tc_impl<64, kCtxBf16>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches)
+                 : launch_attention_tc_impl<128, kCtxBf16>(p, tm_q, tm_k, tm_v, tm_ck, tm_cv, tm_qf, stream, launches);
 }
 }  // namespace pkv

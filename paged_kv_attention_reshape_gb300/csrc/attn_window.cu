@@ -4,7 +4,7 @@
 //
 // Mathematics: with s_j = log2(e) scale (q . k_j) over the keys that a row sees and m any number of their size,
 // P_j = 2^(s_j - m):  O = sum P_j v_j,  l = sum P_j,  out = O / l,  lse = (m + log2 l) ln 2. m is the max of the
-// scores when the row first meets one, and follows them only when they pass it by more than kLazy = 20: P and O
+// scores when the row first meets one, and follows them only when they pass it by more than LAZY: P and O
 // keep the precision of their types whatever the power of two in front, P <= 2^20 leaves values up to 2^100
 // room, and O is rescaled in nearly no tile.
 //
@@ -47,7 +47,10 @@ namespace pkv {
 
 namespace {
 
-template <int D>
+// FP8: the cache holds E4M3 codes. They land as such, converter warps turn them, Q and the new rows into fp16 in
+// shared memory (every E4M3 value is an fp16 number; new values are divided by the value scale), and the products
+// run on fp16.
+template <int D, bool FP8>
 struct WnCfg {
   static constexpr int BN = 128, CHUNKS = BN / 16;        // keys of a tile
   static constexpr int HALVES = D / 64;
@@ -58,12 +61,15 @@ struct WnCfg {
   static constexpr int NBUF = D == 128 ? 2 : 4;           // tiles of the K ring, and of the V ring
   static constexpr int MAXR = kAttnSetChunk;              // requests of the set one launch holds
   static constexpr int W_K = 8, W_MMA = 9, W_V = 10, W_FIX = 11;
-  static constexpr int THREADS = 384;
-  // launched at 168 registers a thread; the softmax warps take some of the others'
-  static constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 80;
-  static_assert(256 * REGS_SOFTMAX + 128 * REGS_OTHER <= THREADS * 168, "register split");
+  static constexpr int W_CONV = 12, NCONV = FP8 ? 4 : 0;  // converter warps
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  // launched at 168 registers a thread (FP8: 128); the softmax warps take some of the others'
+  static constexpr int REGS_LAUNCH = FP8 ? 128 : 168, REGS_SOFTMAX = FP8 ? 144 : 208, REGS_OTHER = FP8 ? 112 : 80;
+  static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "register split");
+  // How far (in powers of two) scores may pass a row's m before it follows them: far in bf16; P <= 2^8 in fp16.
+  static constexpr float LAZY = FP8 ? 8.f : 20.f;
   static constexpr int ITEM_RING = 4;                     // claimed items published to the other roles
-  static constexpr int ITEM_READERS = 8 + 3;
+  static constexpr int ITEM_READERS = 8 + 2 + (FP8 ? NCONV : 1);
   static constexpr int RING_OFF = 2 * Q_BYTES;
   static constexpr int REQ_OFF = RING_OFF + 2 * NBUF * KV_BYTES;  // int4 {r, row0, q_len, C}
   static constexpr int START_OFF = REQ_OFF + MAXR * 16;         // prefix of the items, by rank
@@ -76,7 +82,8 @@ struct WnCfg {
 };
 struct WnBars {
   uint64_t q_full, q_empty;
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], v_ready[4];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t k_ready[4], v_ready[4], q_ready;  // converted (K and Q: FP8 only); value rows that no row sees zeroed
   uint64_t s_full[2], o_final[2];
   uint64_t p_full[2][2];  // P of the first and of the second 64 columns
   uint64_t o_both;        // both slots' O of a split item
@@ -84,8 +91,8 @@ struct WnBars {
   uint64_t rows[4];       // the two warps that share a split item's 32 rows
   uint64_t drained;       // the products in flight when a role gave up
 };
-template <int D>
-constexpr int wn_smem() { return 1024 + WnCfg<D>::BAR_OFF + static_cast<int>(sizeof(WnBars)); }
+template <int D, bool FP8>
+constexpr int wn_smem() { return 1024 + WnCfg<D, FP8>::BAR_OFF + static_cast<int>(sizeof(WnBars)); }
 
 __device__ __forceinline__ constexpr uint32_t wn_scol(int slot) { return slot * 128u; }
 __device__ __forceinline__ constexpr uint32_t wn_ocol(int slot) { return 256u + slot * 128u; }
@@ -109,6 +116,8 @@ struct WnItem {
     const int a = 8 * j, b = a + 8;
     return b <= fs || (a >= f0 && b <= f1 && (vt < a || vt >= b));
   }
+  // chunks of the walk that are cache blocks: the first ones
+  __device__ int cached() const { return cb <= head ? cb : max(head, cb - gap); }
 };
 static_assert(sizeof(WnItem) == 64, "ring entry");
 
@@ -147,9 +156,6 @@ __device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, in
   if (it.vt < it.head && it.cb - 1 >= it.head) it.vt = -1;  // (it lies in the gap)
   return it;
 }
-
-// How far (in powers of two) scores may pass a row's m before it follows them.
-constexpr float kLazy = 20.f;
 
 // Counters of claimed items and of finished CTAs, in the launch's slot (launch.h); its last CTA to finish sets
 // the slot back to zero. Without a slot the items are dealt statically, in snake order.
@@ -198,13 +204,60 @@ struct WnRow {
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
+// ---- conversions (FP8) -------------------------------------------------------------------------------
+// A K or V tile is [2 halves][128 rows][128 B] (64 16-bit values of a row per half, 128-byte swizzle: 16-byte chunk q of
+// row R at R * 128 + ((q ^ (R & 7)) << 4)). A block's codes land, with the same swizzle, where their rows' second half
+// goes, so a thread converts its own code row in place: dims 0 .. 63 into the first half, then dims 64 .. 127, read
+// before, over the codes. The loops are rolled: the roles' code together does not fit the instruction cache.
+__device__ __forceinline__ void wn_conv_codes(uint32_t tile, int R) {
+  const uint32_t codes = tile + 16384u + R * 128;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint4 c[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c[q] = ld_shared_v4(codes + (((4 * h + q) ^ (R & 7)) << 4));
+    const uint32_t at = tile + h * 16384u + R * 128;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {  // 16 codes: two 16-byte chunks of fp16
+      st_shared_v4(at + (((2 * q) ^ (R & 7)) << 4),
+                   make_uint4(e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].x)), e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].x >> 16)),
+                              e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].y)), e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].y >> 16))));
+      st_shared_v4(at + (((2 * q + 1) ^ (R & 7)) << 4),
+                   make_uint4(e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].z)), e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].z >> 16)),
+                              e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].w)), e4m3x2_to_f16x2(static_cast<uint16_t>(c[q].w >> 16))));
+    }
+  }
+}
+// bf16 row R of a tile times f -> fp16 in place.
+__device__ __forceinline__ void wn_conv_row(uint32_t tile, int R, float f) {
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // (8 rows: 8 different bank groups)
+      const uint32_t a = tile + (h >> 1) * 16384u + R * 128 + (((4 * (h & 1) + q) ^ (R & 7)) << 4);
+      const uint4 v = ld_shared_v4(a);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
+      st_shared_v4(a, make_uint4(y[0], y[1], y[2], y[3]));
+    }
+}
+template <int HALVES>
+__device__ __forceinline__ void wn_zero_row(uint32_t tile, int R) {
+#pragma unroll 1
+  for (int c = 0; c < HALVES * 8; ++c) st_shared_v4(tile + (c / 8) * 16384u + R * 128 + (c % 8) * 16, make_uint4(0, 0, 0, 0));
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
     attn_window_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kt,
                        const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ CUtensorMap tm_ck,
                        const __grid_constant__ CUtensorMap tm_cv) {
-  using C = WnCfg<D>;
+  static_assert(!FP8 || D == 128, "a code row is one 128-byte box");
+  using C = WnCfg<D, FP8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                  // [slot][half][128][128 B]
@@ -245,7 +298,8 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       mbar_init(&bar.k_empty[b], 1);
       mbar_init(&bar.v_full[b], 1);
       mbar_init(&bar.v_empty[b], 1);
-      mbar_init(&bar.v_ready[b], 1);
+      mbar_init(&bar.v_ready[b], FP8 ? C::NCONV : 1);
+      if (FP8) mbar_init(&bar.k_ready[b], C::NCONV);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
@@ -257,6 +311,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       mbar_init(&bar.item_full[i], 1);
       mbar_init(&bar.item_empty[i], C::ITEM_READERS);
     }
+    if (FP8) mbar_init(&bar.q_ready, C::NCONV);
     mbar_init(&bar.o_both, 1);
     mbar_init(&bar.drained, 1);
     s_abort = 0;
@@ -342,7 +397,6 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
     const int slot = warp >> 2, quad = warp & 3;
     const int t = tid & 127;  // row of the tile = TMEM lane
     const uint32_t lane_at = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint64_t sc2 = sm::f2(p.scale_log2, p.scale_log2);
     const int shift = __ffs(p.G) - 1;  // G is a power of two
     uint32_t sc = 0, oc = 0, bc = 0, rc = 0;  // phases: S of this slot, o_final, o_both, rows
     for (uint32_t k = 0;; ++k) {
@@ -361,42 +415,62 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         tc::fence_after_sync();
         if (live) {
           const uint32_t srow = lane_at + wn_scol(slot);
-          if (!it.full(j)) {
+          // FP8: a score of a cached key counts in the key scale's units. A tile of both kinds is brought to those of
+          // the new keys.
+          const int nc = FP8 ? 128 * j < 16 * it.cached() ? 16 * it.cached() - 128 * j : 0 : 0;  // its cached columns
+          const bool both = FP8 && nc > 0 && nc < min(128, 16 * it.NV - 128 * j);
+          const float sl = FP8 && nc > 0 && !both ? p.ctx_scale_log2 : p.scale_log2;
+          if (both || !it.full(j)) {
             // What is hidden becomes -inf in tensor memory, 32 columns at a time (a warp's rows are few tokens: they see
             // most such groups whole). In registers, with the four groups' code in a row, it is fetched anew
             // for nearly every edge tile: 1340 clocks.
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const uint32_t seen = sees.seen(128 * j + 32 * c);
-              if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+              if (!both && __all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
               uint32_t x[32];
               tc::ld32(srow + 32 * c, x);
               tc::wait_ld();
               tc::touch32(x);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = (seen >> e) & 1u ? x[e] : 0xFF800000u;
+              for (int e = 0; e < 32; ++e) {
+                if (FP8 && both && 32 * c + e < nc) x[e] = __float_as_uint(__uint_as_float(x[e]) * p.ctx_k_scale);
+                x[e] = (seen >> e) & 1u ? x[e] : 0xFF800000u;
+              }
               tc::st32(srow + 32 * c, x);
             }
             tc::wait_st();
           }
-          uint32_t v[4][32];
+          // FP8: half a row at a time, the second half read twice, which leaves registers for the converters
+          constexpr int G = FP8 ? 2 : 4;  // groups of 32 columns held
+          uint32_t v[G][32];
+          auto load = [&](int c0) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tc::ld32(srow + 32 * c, v[c]);
-          tc::wait_ld();
+            for (int c = 0; c < G; ++c) tc::ld32(srow + 32 * (c0 + c), v[c]);
+            tc::wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
+            for (int c = 0; c < G; ++c) tc::touch32(v[c]);  // no use of v may move above the wait
+          };
           // row max of the raw scores (the scale is positive, so it commutes with max)
           float mq[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
+          for (int c0 = 4 - G; c0 >= 0; c0 -= G) {
+            load(c0);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) mq[c] = sm::max3(mq[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-          const float mx = fmaxf(sm::max3(mq[0], mq[1], mq[2]), mq[3]) * p.scale_log2;  // -inf stays -inf
+            for (int e = 0; e < 32; e += 2)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int g = c % G, i = G == 4 ? e : (e & ~3) + 2 * (c / G);  // (four chains whatever G is)
+                if (G == 4 || (e & 2) == 0)
+                  mq[c] = sm::max3(mq[c], __uint_as_float(v[g][i]), __uint_as_float(v[g][i + 1]));
+              }
+          }
+          const float mx = fmaxf(sm::max3(mq[0], mq[1], mq[2]), mq[3]) * sl;  // -inf stays -inf
           // The decision to follow is per row, but tcgen05.ld/st are warp-collective: the whole warp takes the
           // branch when any of its rows does (alpha is 1 for the others).
-          if (__any_sync(0xffffffffu, mx > m + kLazy)) {  // (m may be -inf)
+          if (__any_sync(0xffffffffu, mx > m + C::LAZY)) {  // (m may be -inf)
             float alpha = 1.f;
-            if (mx > m + kLazy) {
+            if (mx > m + C::LAZY) {
               alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mx);
               m = mx;
             }
@@ -416,24 +490,25 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
               }
             }
           }
-          // P = 2^(s * scale_log2 - m), packed to bf16 pairs over the first half of S
+          // P = 2^(s * scale_log2 - m), packed to 16-bit pairs over the first half of S
           const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
-          const uint64_t nm2 = sm::f2(neg_m, neg_m);
+          const uint64_t nm2 = sm::f2(neg_m, neg_m), sc2 = sm::f2(sl, sl);
           uint64_t rs2 = sm::f2(0.f, 0.f);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            if (FP8 && h == 1) load(2);
             uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const uint64_t x =
-                    sm::fma2(sm::f2(__uint_as_float(v[2 * h + c][e]), __uint_as_float(v[2 * h + c][e + 1])), sc2, nm2);
+                    sm::fma2(sm::f2(__uint_as_float(v[(2 * h + c) % G][e]), __uint_as_float(v[(2 * h + c) % G][e + 1])), sc2, nm2);
                 float x0, x1;
                 sm::unf2(x, x0, x1);
                 const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
                 rs2 = sm::add2(rs2, pp);
-                pk[16 * c + e / 2] = sm::bf16x2(pp);
+                pk[16 * c + e / 2] = FP8 ? sm::f16x2(pp) : sm::bf16x2(pp);
               }
             tc::st32(srow + 32 * h, pk);
             tc::wait_st();
@@ -497,7 +572,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         ++oc;
         tc::fence_after_sync();
         if (live) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const float inv = l == 0.f ? 0.f : (FP8 ? p.ctx_v_scale : 1.f) / l;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {  // (unrolled, its code is fetched anew for every item: 3500 clocks)
             uint32_t o[32];
@@ -525,7 +600,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         const float2 a = mrg[t], b = mrg[128 + t];
         const float mm = fmaxf(a.x, b.x);
         const float w0 = a.y == 0.f ? 0.f : ex2_approx(a.x - mm), w1 = b.y == 0.f ? 0.f : ex2_approx(b.x - mm);
-        const float sum = a.y * w0 + b.y * w1, inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float sum = a.y * w0 + b.y * w1, inv = sum == 0.f ? 0.f : (FP8 ? p.ctx_v_scale : 1.f) / sum;
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           const int col = slot * (D / 2) + c * 32;
@@ -577,6 +652,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
       for (int c = 0; c < C::CHUNKS; ++c) at[c] = __shfl_sync(0xffffffffu, where, c);
       // a tile of new tokens that follow one another comes in one box a half
       const bool run = at[0] < 0 && __all_sync(0xffffffffu, lane >= chunks || where == at[0] - 16 * lane);
+      const int blocks = FP8 ? __popc(__ballot_sync(0xffffffffu, lane < chunks && where >= 0)) : 0;
       peek();
       const uint32_t b = i % C::NBUF;
       bool ok = true;
@@ -584,7 +660,8 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         if (i >= C::NBUF) ok = wn_wait1(&empty[b], (i / C::NBUF - 1) & 1, &s_abort, p.err);
         if (ok) {
           uint8_t* dst = ring + b * C::KV_BYTES;
-          mbar_arrive_expect_tx(&full[b], run ? C::KV_BYTES : chunks * 16 * D * 2);
+          // (a block's codes are half of what its values would be)
+          mbar_arrive_expect_tx(&full[b], run ? C::KV_BYTES : chunks * 16 * D * 2 - blocks * 16 * D);
           if (run) {
 #pragma unroll
             for (int hf = 0; hf < C::HALVES; ++hf)
@@ -596,6 +673,10 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
               if (c >= chunks) break;
               const CUtensorMap* map = at[c] >= 0 ? cache : rows;
               const int row = at[c] >= 0 ? 0 : ~at[c], blk = at[c] >= 0 ? at[c] : 0;
+              if (FP8 && at[c] >= 0) {
+                tma_load_4d(dst + C::KV_HALF + c * 2048, map, &full[b], 0, kh, 0, blk);
+                continue;
+              }
 #pragma unroll
               for (int hf = 0; hf < C::HALVES; ++hf)
                 tma_load_4d(dst + hf * C::KV_HALF + c * 2048, map, &full[b], 0, kh * C::HALVES + hf, row, blk);
@@ -718,7 +799,9 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
     } else if (warp == C::W_MMA) {
       // ======================= MMA issuer =======================
       if (tc::elect()) {
-        constexpr uint32_t kQk = tc::idesc_bf16(128, 0, 0, 0), kPv = tc::idesc_bf16(128, D, 0, 1);
+        constexpr uint32_t kQk = FP8 ? tc::idesc_f16(128, 0, 0, 0) : tc::idesc_bf16(128, 0, 0, 0),
+                           kPv = FP8 ? tc::idesc_f16(128, D, 0, 1) : tc::idesc_bf16(128, D, 0, 1);
+        uint64_t* const k_in = FP8 ? bar.k_ready : bar.k_full;  // K that products may read
         // Shared-memory descriptors (tc::smem_desc) as their low words: the address in 16 bytes and the leading
         // offset; the high word is the same for all.
         constexpr uint32_t kLboK = (16u >> 4) << 16, kLboV = (static_cast<uint32_t>(C::KV_HALF) >> 4) << 16;
@@ -734,7 +817,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         };
         auto buf = [&](int j) { return (tc0 + j) % C::NBUF; };
         auto phase = [&](int j) { return ((tc0 + j) / C::NBUF) & 1; };
-        auto k_there = [&](int j) { return wait(&bar.k_full[buf(j)], phase(j)); };
+        auto k_there = [&](int j) { return wait(&k_in[buf(j)], phase(j)); };
         auto v_there = [&](int j) { return wait(&bar.v_ready[buf(j)], phase(j)); };
         // S = Q K^T of tile j (N = 16 chunks)
         auto qk = [&](int slot, int qtile, int j, int chunks) {
@@ -774,12 +857,12 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
           if (NV == 0) break;
           const int nt = (NV + C::CHUNKS - 1) / C::CHUNKS;
           auto chunks = [&](int j) { return min(C::CHUNKS, NV - C::CHUNKS * j); };
-          if (!wait(&bar.q_full, k & 1)) { ok = false; break; }
+          if (!wait(FP8 ? &bar.q_ready : &bar.q_full, k & 1)) { ok = false; break; }
           if (!split) {
             // P V of tile t - 1 and S of tile t, slot by slot (one place in the code for each, so that it stays in
-            // the instruction cache beside the other roles'). What is there first is waited for while products run
-            // that were issued before.
-            if (!(ok = k_there(0))) break;
+            // the instruction cache beside the other roles'). K and V are looked for while products run that were issued
+            // before, and waited for only where they are needed.
+            bool k_seen = false;
             for (int t = 0; t <= nt && ok; ++t) {
 #pragma unroll
               for (int s = 0; s < 2; ++s) {
@@ -789,9 +872,10 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
                   if (s == 1) tc::commit(&bar.v_empty[buf(t - 1)]);
                 }
                 if (t < nt) {
+                  if (s == 0 && !k_seen && !(ok = k_there(t))) break;
                   qk(s, s, t, chunks(t));
                   if (s == 0) {
-                    if (t + 1 < nt && !(ok = k_there(t + 1))) break;
+                    k_seen = t + 1 < nt && mbar_test(&k_in[buf(t + 1)], phase(t + 1));
                   } else {
                     tc::commit(&bar.k_empty[buf(t)]);
                     if (t + 1 == nt) tc::commit(&bar.q_empty);
@@ -809,7 +893,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
             uint32_t idle = 0;
             while (jp < nt) {
               const int s = jp & 1;
-              if (jq < nt && jq < jp + 2 && mbar_test(&bar.k_full[buf(jq)], phase(jq))) {
+              if (jq < nt && jq < jp + 2 && mbar_test(&k_in[buf(jq)], phase(jq))) {
                 tc::fence_after_sync();
                 qk(jq & 1, 0, jq, chunks(jq));
                 tc::commit(&bar.k_empty[buf(jq)]);
@@ -846,6 +930,72 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
         }
       }
       __syncwarp();
+    } else if constexpr (FP8) {
+      if (warp >= C::W_CONV) {
+        // ======================= conversions =======================
+        // Q once an item, then the K and V tiles in the order in which they land, a row a thread. (In turn, K of the next
+        // tile waits for V of this one, whose buffer comes free late: 420 us on 2048 tokens under 4096.)
+        const int R = tid - C::W_CONV * 32;
+        const uint32_t k_base = smem_u32(ring_k), v_base = smem_u32(ring_v), q_base = smem_u32(sQ);
+        const float inv_vs = 1.f / p.ctx_v_scale;
+        uint32_t n_tiles = 0;  // of the items before this one
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+          const WnItem* taken = take(k);
+          if (taken == nullptr) break;
+          const WnItem it = *taken;
+          release(k);
+          const int nt = it.tiles(), last = it.last(), sinks = p.sinks;
+          if (!wn_wait(&bar.q_full, k & 1, &s_abort, p.err)) break;
+#pragma unroll 1
+          for (int s = 0; s < (it.split ? 1 : 2); ++s) wn_conv_row(q_base + s * C::Q_BYTES, R, 1.f);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.q_ready);
+          int jk = 0, jv = 0;
+          uint32_t idle = 0;
+          uint64_t t0 = 0;
+          while (jv < nt) {
+            const uint32_t ik = n_tiles + jk, iv = n_tiles + jv;
+            // (all lanes take the same way: a lane's own test may be the first to see a phase end)
+            const bool of_k = jk < nt && __any_sync(0xffffffffu, mbar_test(&bar.k_full[ik % C::NBUF], (ik / C::NBUF) & 1));
+            if (!of_k && !__any_sync(0xffffffffu, mbar_test(&bar.v_full[iv % C::NBUF], (iv / C::NBUF) & 1))) {
+              if ((++idle & 255u) == 0) {  // (bounded, as wn_wait1)
+                const uint64_t now = globaltimer_ns();
+                if (idle == 256u) t0 = now;
+                if (now - t0 > kWaitLimitNs) {
+                  flag_error(p.err, PKV_DEVERR_TIMEOUT);
+                  *static_cast<volatile int*>(&s_abort) = 1;
+                }
+                if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&s_abort))) { ok = false; break; }
+              }
+              continue;
+            }
+            idle = 0;
+            const uint32_t b = (of_k ? ik : iv) % C::NBUF;
+            // (the phase has ended: this makes what landed visible to every lane)
+            if (!wn_wait(of_k ? &bar.k_full[b] : &bar.v_full[b], ((of_k ? ik : iv) / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
+            const int v = C::CHUNKS * (of_k ? jk : jv) + R / 16;
+            if (v < it.NV) {  // (no product takes the rows of other chunks)
+              const int u = it.chunk(v), key = it.pos(u) + R % 16;
+              // value rows that no row sees become zeros: P = 0 there must not meet what is not finite
+              const bool keep = of_k || ((key >= it.low || key < sinks) && key <= last && (u >= it.cb || key < it.C));
+              const uint32_t tile = (of_k ? k_base : v_base) + b * C::KV_BYTES;
+              if (!keep)
+                wn_zero_row<C::HALVES>(tile, R);
+              else if (u < it.cb)
+                wn_conv_codes(tile, R);
+              else
+                wn_conv_row(tile, R, of_k ? 1.f : inv_vs);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(of_k ? &bar.k_ready[b] : &bar.v_ready[b]);
+            if (of_k) ++jk; else ++jv;
+          }
+          n_tiles += nt;
+        }
+      }
     } else {
       // ======================= value rows that no row sees =======================
       const uint32_t ring_base = smem_u32(ring_v);
@@ -868,10 +1018,7 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
               if (v >= it.NV) continue;  // (no product takes it)
               const int u = it.chunk(v), key = it.pos(u) + R % 16;
               const bool seen = (key >= it.low || key < sinks) && key <= last && (u >= it.cb || key < it.C);
-              if (seen) continue;
-#pragma unroll
-              for (int c = 0; c < C::HALVES * 8; ++c)
-                st_shared_v4(tile + (c / 8) * C::KV_HALF + R * 128 + (c % 8) * 16, make_uint4(0, 0, 0, 0));
+              if (!seen) wn_zero_row<C::HALVES>(tile, R);
             }
             fence_proxy_async_smem();
           }
@@ -898,23 +1045,27 @@ __global__ void __launch_bounds__(WnCfg<D>::THREADS, 1)
   }
 }
 
-template <int D>
+template <int D, bool FP8>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, cudaStream_t stream) {
-  const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&attn_window_kernel<D>), wn_smem<D>(),
-                                           D == 64 ? kAttrWinAttn64 : kAttrWinAttn128);
+                   const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv,
+                   cudaStream_t stream) {
+  constexpr int kSlot = FP8 ? kAttrWinAttn128Fp8 : D == 64 ? kAttrWinAttn64 : kAttrWinAttn128;
+  const cudaError_t e =
+      set_smem_attr_once(reinterpret_cast<const void*>(&attn_window_kernel<D, FP8>), wn_smem<D, FP8>(), kSlot);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_window_kernel<D>, dim3(num_sms()), dim3(WnCfg<D>::THREADS), wn_smem<D>(), stream, p, tq, tk, tv,
-                    tkt, tvt, tck, tcv);
+  return launch_pdl(attn_window_kernel<D, FP8>, dim3(num_sms()), dim3(WnCfg<D, FP8>::THREADS), wn_smem<D, FP8>(), stream, p, tq,
+                    tk, tv, tkt, tvt, tck, tcv);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_window(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, int D, cudaStream_t stream, int* launches) {
+                               const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, int D,
+                               bool fp8, cudaStream_t stream, int* launches) {
   *launches += 1;
-  return D == 64 ? launch<64>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream)
-                 : launch<128>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream);
+  if (fp8) return launch<128, true>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream);
+  return D == 64 ? launch<64, false>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream)
+                 : launch<128, false>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream);
 }
 
 }  // namespace pkv

@@ -85,6 +85,7 @@ struct AttnParams {
   float scale_log2;
   float ctx_scale_log2;  // cached-context key tiles: softmax scale * key scale * log2(e)
   float ctx_v_scale;     // cached-context tiles: P is multiplied by the value scale for P V
+  float ctx_k_scale;     // the key scale alone (windowed attention)
   const float* k_scales;  // block-scaled cache: [num_blocks][Hkv]
   const float* v_scales;
   int32_t sched_slot;    // this launch's work-item counter slot (< kAttnSchedSlots); -1: none
@@ -268,10 +269,12 @@ cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& tm_q, const
 constexpr int kAttnCtxBlock = 3;
 cudaError_t launch_attn_scaled(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& tck, const CUtensorMap& tcv, void* workspace, cudaStream_t stream, int* launches);
-// Windowed extend and prefill over bf16 (p.window >= 1): tm_q as for launch_attn_scaled, tm_k and tm_v over the packed
-// new keys and values as (64, D/64 * Hkv, T, 1) in boxes of 16 rows, tkt and tvt as for launch_attention.
+// Windowed extend and prefill (p.window >= 1): tm_q as for launch_attn_scaled, tm_k and tm_v over the packed
+// new keys and values as (64, D/64 * Hkv, T, 1) in boxes of 16 rows, tkt and tvt as for launch_attention. fp8: the cache
+// holds E4M3 codes (head_dim 128).
 cudaError_t launch_attn_window(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, int D, cudaStream_t stream, int* launches);
+                               const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, int D, bool fp8,
+                               cudaStream_t stream, int* launches);
 size_t attn_scaled_workspace(int32_t max_q_len, int32_t max_seq_len, int G);
 
 }  // namespace pkv
