@@ -61,15 +61,15 @@ struct WnCfg {
   static constexpr int NBUF = D == 128 ? 2 : 4;           // tiles of the K ring, and of the V ring
   static constexpr int MAXR = kAttnSetChunk;              // requests of the set one launch holds
   static constexpr int W_K = 8, W_MMA = 9, W_V = 10, W_FIX = 11;
-  static constexpr int W_CONV = 12, NCONV = FP8 ? 4 : 0;  // converter warps
-  static constexpr int THREADS = FP8 ? 512 : 384;
-  // launched at 168 registers a thread (FP8: 128); the softmax warps take some of the others'
-  static constexpr int REGS_LAUNCH = FP8 ? 128 : 168, REGS_SOFTMAX = FP8 ? 144 : 208, REGS_OTHER = FP8 ? 112 : 80;
+  static constexpr int W_CONV = 12, NCONV = FP8 ? 4 : 0;  // converter warps of Q and K, and as many of V
+  static constexpr int THREADS = FP8 ? 640 : 384;
+  // launched at 168 registers a thread (FP8: 96); the softmax warps take some of the others'
+  static constexpr int REGS_LAUNCH = FP8 ? 96 : 168, REGS_SOFTMAX = FP8 ? 144 : 208, REGS_OTHER = FP8 ? 64 : 80;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "register split");
   // How far (in powers of two) scores may pass a row's m before it follows them: far in bf16; P <= 2^8 in fp16.
   static constexpr float LAZY = FP8 ? 8.f : 20.f;
   static constexpr int ITEM_RING = 4;                     // claimed items published to the other roles
-  static constexpr int ITEM_READERS = 8 + 2 + (FP8 ? NCONV : 1);
+  static constexpr int ITEM_READERS = 8 + 2 + (FP8 ? 2 * NCONV : 1);
   static constexpr int RING_OFF = 2 * Q_BYTES;
   static constexpr int REQ_OFF = RING_OFF + 2 * NBUF * KV_BYTES;  // int4 {r, row0, q_len, C}
   static constexpr int START_OFF = REQ_OFF + MAXR * 16;         // prefix of the items, by rank
@@ -933,12 +933,14 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
     } else if constexpr (FP8) {
       if (warp >= C::W_CONV) {
         // ======================= conversions =======================
-        // Q once an item, then the K and V tiles in the order in which they land, a row a thread. (In turn, K of the next
-        // tile waits for V of this one, whose buffer comes free late: 420 us on 2048 tokens under 4096.)
-        const int R = tid - C::W_CONV * 32;
-        const uint32_t k_base = smem_u32(ring_k), v_base = smem_u32(ring_v), q_base = smem_u32(sQ);
-        const float inv_vs = 1.f / p.ctx_v_scale;
-        uint32_t n_tiles = 0;  // of the items before this one
+        // Four warps convert Q once an item, then each K tile as it lands, four others each V tile, a row a thread. (One
+        // group for both: 384 us on 2048 tokens under 4096; two warps each, and the loops unrolled: 423.)
+        const bool of_v = warp >= C::W_CONV + C::NCONV;
+        const int R = tid & 127;  // (the groups begin at multiples of 128 threads)
+        const uint32_t ring_base = smem_u32(of_v ? ring_v : ring_k), q_base = smem_u32(sQ);
+        uint64_t *const full = of_v ? bar.v_full : bar.k_full, *const ready = of_v ? bar.v_ready : bar.k_ready;
+        const float f = of_v ? 1.f / p.ctx_v_scale : 1.f;
+        uint32_t n_tiles = 0;
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
           const WnItem* taken = take(k);
@@ -946,54 +948,33 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
           const WnItem it = *taken;
           release(k);
           const int nt = it.tiles(), last = it.last(), sinks = p.sinks;
-          if (!wn_wait(&bar.q_full, k & 1, &s_abort, p.err)) break;
+          if (!of_v) {
+            if (!wn_wait(&bar.q_full, k & 1, &s_abort, p.err)) break;
 #pragma unroll 1
-          for (int s = 0; s < (it.split ? 1 : 2); ++s) wn_conv_row(q_base + s * C::Q_BYTES, R, 1.f);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.q_ready);
-          int jk = 0, jv = 0;
-          uint32_t idle = 0;
-          uint64_t t0 = 0;
-          while (jv < nt) {
-            const uint32_t ik = n_tiles + jk, iv = n_tiles + jv;
-            // (all lanes take the same way: a lane's own test may be the first to see a phase end)
-            const bool of_k = jk < nt && __any_sync(0xffffffffu, mbar_test(&bar.k_full[ik % C::NBUF], (ik / C::NBUF) & 1));
-            if (!of_k && !__any_sync(0xffffffffu, mbar_test(&bar.v_full[iv % C::NBUF], (iv / C::NBUF) & 1))) {
-              if ((++idle & 255u) == 0) {  // (bounded, as wn_wait1)
-                const uint64_t now = globaltimer_ns();
-                if (idle == 256u) t0 = now;
-                if (now - t0 > kWaitLimitNs) {
-                  flag_error(p.err, PKV_DEVERR_TIMEOUT);
-                  *static_cast<volatile int*>(&s_abort) = 1;
-                }
-                if (__any_sync(0xffffffffu, *static_cast<volatile int*>(&s_abort))) { ok = false; break; }
-              }
-              continue;
-            }
-            idle = 0;
-            const uint32_t b = (of_k ? ik : iv) % C::NBUF;
-            // (the phase has ended: this makes what landed visible to every lane)
-            if (!wn_wait(of_k ? &bar.k_full[b] : &bar.v_full[b], ((of_k ? ik : iv) / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
-            const int v = C::CHUNKS * (of_k ? jk : jv) + R / 16;
+            for (int s = 0; s < (it.split ? 1 : 2); ++s) wn_conv_row(q_base + s * C::Q_BYTES, R, 1.f);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.q_ready);
+          }
+          for (int j = 0; j < nt; ++j, ++n_tiles) {
+            const uint32_t b = n_tiles % C::NBUF;
+            if (!wn_wait(&full[b], (n_tiles / C::NBUF) & 1, &s_abort, p.err)) { ok = false; break; }
+            const int v = C::CHUNKS * j + R / 16;
             if (v < it.NV) {  // (no product takes the rows of other chunks)
               const int u = it.chunk(v), key = it.pos(u) + R % 16;
+              const uint32_t tile = ring_base + b * C::KV_BYTES;
               // value rows that no row sees become zeros: P = 0 there must not meet what is not finite
-              const bool keep = of_k || ((key >= it.low || key < sinks) && key <= last && (u >= it.cb || key < it.C));
-              const uint32_t tile = (of_k ? k_base : v_base) + b * C::KV_BYTES;
-              if (!keep)
+              if (of_v && !((key >= it.low || key < sinks) && key <= last && (u >= it.cb || key < it.C)))
                 wn_zero_row<C::HALVES>(tile, R);
               else if (u < it.cb)
                 wn_conv_codes(tile, R);
               else
-                wn_conv_row(tile, R, of_k ? 1.f : inv_vs);
+                wn_conv_row(tile, R, f);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(of_k ? &bar.k_ready[b] : &bar.v_ready[b]);
-            if (of_k) ++jk; else ++jv;
+            if (lane == 0) mbar_arrive(&ready[b]);
           }
-          n_tiles += nt;
         }
       }
     } else {
