@@ -442,7 +442,9 @@ pkv_status pkv_varlen_prefill_attn(const void* q, const void* k, const void* v, 
  * as in the call without a window, with these differences:
  *   - only blocks with a key that some row sees are read: table entries of other blocks may
  *     hold anything (pages that slid out of the window may have been given back);
- *   - caches: bf16, or PKV_KV_FP8_E4M3 at head_dim 128; others return PKV_ERR_UNSUPPORTED;
+ *   - caches: bf16, or PKV_KV_FP8_E4M3 at head_dim 128; decode also PKV_KV_FP8_E4M3_BLOCK; others
+ *     return PKV_ERR_UNSUPPORTED. Decode over either FP8 kind: at most 256 KV heads, and the range of
+ *     scales and queries of a block-scaled decode;
  *   - a value that is not finite in a key that some row sees may reach the rows of the same
  *     request and KV head that do not see it, for extend and prefill. Keys that no row sees
  *     touch nothing, whatever they hold.

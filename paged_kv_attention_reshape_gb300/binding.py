@@ -452,8 +452,7 @@ def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, 
     head (k_scale, v_scale: fp32 tensors [num_blocks, Hkv]).
 
     With a window the token sees the last `window` keys, its own among them, and the first `sinks`
-    keys (a bf16 cache, or an FP8 one with per-tensor scales); table entries of the blocks between
-    them are not read."""
+    keys; table entries of the blocks between them are not read."""
     lib = _lib.load()
     _need(q, torch.bfloat16, "q")
     _need(block_tables, torch.int32, "block_tables")

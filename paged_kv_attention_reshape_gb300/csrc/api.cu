@@ -631,7 +631,7 @@ static pkv_status run_decode(const void* q, pkv_cache cache, const int32_t* bloc
                              const int32_t* seq_lens, const int32_t* cu_q, pkv_reqs reqs, int32_t num_q_heads,
                              int32_t max_seq_len, int32_t window, int32_t sinks, float scale, void* out, float* lse,
                              void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
-  pkv_status st = check_cache(cache, true, window == 0);
+  pkv_status st = check_cache(cache, true, true);
   if (st != PKV_OK) return st;
   if ((st = check_reqs(reqs)) != PKV_OK) return st;
   if (!group_ok(num_q_heads, cache.num_kv_heads)) return PKV_ERR_UNSUPPORTED;
@@ -670,14 +670,16 @@ static pkv_status run_decode(const void* q, pkv_cache cache, const int32_t* bloc
   p.scale_log2 = scale * (fp8 ? cache.k_scale : 1.f) * 1.4426950408889634f;
   p.v_scale = fp8 ? cache.v_scale : 1.f;
   const bool scaled = cache.kv_dtype == PKV_KV_FP8_E4M3_BLOCK;
-  if (scaled && !decode_scaled_supported(p.Hkv)) return PKV_ERR_UNSUPPORTED;
-  p.k_scales = cache.k_scales;
-  p.v_scales = cache.v_scales;
-  const size_t need = scaled ? decode_scaled_workspace_bytes(p.Hq, p.Hkv) : decode_workspace_bytes(p.Hq, p.Hkv, cache.head_dim);
+  // the kernel that takes codes into the tensor cores
+  const bool codes = scaled || (fp8 && window > 0);
+  if (codes && !decode_scaled_supported(p.Hkv)) return PKV_ERR_UNSUPPORTED;
+  p.k_scales = scaled ? cache.k_scales : nullptr;
+  p.v_scales = scaled ? cache.v_scales : nullptr;
+  const size_t need = codes ? decode_scaled_workspace_bytes(p.Hq, p.Hkv) : decode_workspace_bytes(p.Hq, p.Hkv, cache.head_dim);
   if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_WORKSPACE;
   p.ws_part = static_cast<float*>(workspace);
   p.ws_ctr = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) +
-                                                   (scaled ? decode_scaled_ctr_offset(p.Hq, p.Hkv)
+                                                   (codes ? decode_scaled_ctr_offset(p.Hq, p.Hkv)
                                                            : decode_workspace_ctr_offset(p.Hq, p.Hkv, cache.head_dim)));
   CUtensorMap tk, tv;
   if (!encode_cache(&tk, cache.k, cache) || !encode_cache(&tv, cache.v, cache)) return PKV_ERR_CUDA;
@@ -688,8 +690,8 @@ static pkv_status run_decode(const void* q, pkv_cache cache, const int32_t* bloc
     p.set_offset = off;
     p.epoch = next_epoch();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    st = cuda_status(scaled       ? launch_decode_scaled(p, tk, tv, s, &launches)
-                     : window > 0 ? launch_window_decode(p, tk, tv, cache.head_dim, fp8, s, &launches)
+    st = cuda_status(codes        ? launch_decode_scaled(p, tk, tv, s, &launches)
+                     : window > 0 ? launch_window_decode(p, tk, tv, cache.head_dim, s, &launches)
                                   : launch_paged_decode(p, tk, tv, cache.head_dim, fp8, s, &launches));
   }
   t_launches += launches;

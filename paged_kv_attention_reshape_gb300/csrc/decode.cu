@@ -79,7 +79,7 @@ struct TableRow<true> {
   __device__ int operator[](int v) const { return row[v < head ? v : v + gap]; }
 };
 
-// WIN: a windowed decode. Of every sequence only the blocks with keys that its last token sees are
+// WIN (bf16): a windowed decode. Of every sequence only the blocks with keys that its last token sees are
 // streamed (Seen): they are the units of the shares, so the work is the window's and not the
 // context's, and a table entry between the sinks and the window is never read.
 template <int D, bool FP8, bool WIN>
@@ -569,7 +569,8 @@ template <int D, bool FP8, bool WIN>
 static cudaError_t launch_decode_impl(const DecodeParams& p, const CUtensorMap& tk,
                                       const CUtensorMap& tv, cudaStream_t stream, int* launches) {
   using C = DecodeCfg<D, FP8>;
-  constexpr int kSlot = WIN ? (FP8 ? kAttrWinDecode128Fp8 : (D == 64 ? kAttrWinDecode64 : kAttrWinDecode128))
+  static_assert(!WIN || !FP8, "windows over codes are decode_scaled.cu's");
+  constexpr int kSlot = WIN ? (D == 64 ? kAttrWinDecode64 : kAttrWinDecode128)
                             : (FP8 ? kAttrDecode128Fp8 : (D == 64 ? kAttrDecode64 : kAttrDecode128));
   cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&paged_decode_kernel<D, FP8, WIN>), max_dyn_smem(),
                                      kSlot);
@@ -595,9 +596,8 @@ cudaError_t launch_paged_decode(const DecodeParams& p, const CUtensorMap& tk, co
                  : launch_decode_impl<128, false, false>(p, tk, tv, stream, launches);
 }
 
-cudaError_t launch_window_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                                 int D, bool fp8, cudaStream_t stream, int* launches) {
-  if (fp8) return launch_decode_impl<128, true, true>(p, tk, tv, stream, launches);
+cudaError_t launch_window_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int D,
+                                 cudaStream_t stream, int* launches) {
   return D == 64 ? launch_decode_impl<64, false, true>(p, tk, tv, stream, launches)
                  : launch_decode_impl<128, false, true>(p, tk, tv, stream, launches);
 }

@@ -262,7 +262,10 @@ __device__ __forceinline__ void split_e4m3(uint32_t x2, uint16_t& hi, uint16_t& 
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r));
 }
 
-template <int NG>
+// WIN: a windowed decode (window_decode_attn). Of every sequence only the blocks with keys that its token sees are
+// walked (Seen); tokens of those blocks that it does not see are dealt with like tokens past a context's end. The cache
+// may then have one scale for the tensor as well (k_scales NULL): ks is in scale_log2, and out is multiplied by vs.
+template <int NG, bool WIN>
 __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
     decode_scaled_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v) {
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
   int begin, n;
   resolve_set(p, begin, n);
   // (its block-wide barriers also order the set-up above before what follows)
-  const int64_t TB = load_set<C::MAXR, C::BS>(p, begin, n, s_pre, s_ctx, s_r, s_row, s_scan);
+  const int64_t TB = load_set<C::MAXR, C::BS, WIN>(p, begin, n, s_pre, s_ctx, s_r, s_row, s_scan);
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem + chain * C::CHAIN_COLS;
 
@@ -496,12 +499,12 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
       float lse = 0.f;
       if (lane < NG) {
         const float L = ls[lane] + ls[NG + lane] + ls[2 * NG + lane] + ls[3 * NG + lane];
-        invs[lane] = 1.f / L;
+        invs[lane] = (WIN ? p.v_scale : 1.f) / L;
         lse = (m_fin + __log2f(L)) * 0.69314718055994531f;
       }
       __syncwarp();
       const int64_t row = s_row[pc.i];
-      const bool whole = pc.lo == 0 && pc.hi == (s_ctx[pc.i] + C::BS - 1) / C::BS;
+      const bool whole = pc.lo == 0 && pc.hi == (WIN ? s_pre[pc.i + 1] - s_pre[pc.i] : (s_ctx[pc.i] + C::BS - 1) / C::BS);
       if (whole) {
         __nv_bfloat16* dst = p.out + (row * p.Hq + kh * p.G) * 128 + t;
 #pragma unroll
@@ -554,9 +557,16 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
         const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF) + gt % C::SRING * 16;
         // a zero scale counts as 2^-100: no logarithm of 0
         const float4* qi4 = reinterpret_cast<const float4*>(qinv + ((pieces & 1) ? 0 : NG));
-        const float ks = fmaxf(sc[t >> 4], 0x1p-100f), vs = fmaxf(sc[8 + (t >> 4)], 0x1p-100f);
+        const bool table = !WIN || p.k_scales != nullptr;
+        const float ks = table ? fmaxf(sc[t >> 4], 0x1p-100f) : 1.f, vs = table ? fmaxf(sc[8 + (t >> 4)], 0x1p-100f) : 1.f;
         const float lvs = __log2f(vs), ivs = 1.f / vs;
-        const bool valid = t < ntok;
+        bool valid = t < ntok;
+        if constexpr (WIN) {
+          const Seen sn(ctx, p.window, p.sinks);
+          const int vb = wk.blk0() + (t >> 4), head = sn.head<C::BS>();
+          const int pos = (vb < head ? vb : vb + sn.gap<C::BS>()) * C::BS + (t & 15);
+          valid = (t >> 4) < wk.nbl() && pos < ctx && (pos >= sn.from || pos < sn.sinks);
+        }
 #pragma unroll
         for (int q = 0; q < NG / 4; ++q) {
           const float4 f4 = qi4[q];
@@ -613,7 +623,7 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
         } else {
           *reinterpret_cast<uint4*>(pd) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
         }
-        if (ntok < 128) {
+        if (WIN ? __any_sync(0xffffffffu, !valid) : ntok < 128) {
           // V rows past the tile's tokens become zeros: P = 0 there must not meet a NaN code
           const uint32_t hv = 2 * gt + 1;
           bad |= !sd_wait_warp(&bar.kv_full[hv % C::NB], (hv / C::NB) & 1, &s_abort, p.err);
@@ -703,9 +713,13 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
     SdWalk wk;
     wk.start(s_pre, n, b0, b1);
     auto entry = [&](const SdWalk& w) {
-      return w.have && lane < w.nbl()
-                 ? p.block_tables[static_cast<int64_t>(s_r[w.pc.i]) * p.max_blocks + w.blk0() + lane]
-                 : 0;
+      if (!w.have || lane >= w.nbl()) return 0;
+      int b = w.blk0() + lane;
+      if constexpr (WIN) {
+        const Seen sn(s_ctx[w.pc.i], p.window, p.sinks);
+        if (b >= sn.head<C::BS>()) b += sn.gap<C::BS>();
+      }
+      return p.block_tables[static_cast<int64_t>(s_r[w.pc.i]) * p.max_blocks + b];
     };
     int next = entry(wk);
     uint32_t h = 0;  // tiles of K or V requested
@@ -731,7 +745,7 @@ __global__ void __launch_bounds__(SdCfg<NG>::THREADS, 1)
         }
         if (lane < C::TBLK) {
           if (lane < nbl) {
-            if (sel == 0) {  // both scales come with K
+            if (sel == 0 && (!WIN || p.k_scales != nullptr)) {  // both scales come with K
               float* sc = reinterpret_cast<float*>(base + C::SC_OFF) + (h / 2) % C::SRING * 16 + lane;
               const int64_t at = static_cast<int64_t>(blk) * p.Hkv + kh;
               cp_async4(sc, p.k_scales + at);
@@ -855,13 +869,14 @@ size_t decode_scaled_workspace_bytes(int Hq, int Hkv) {
   return decode_scaled_ctr_offset(Hq, Hkv) + static_cast<size_t>(sd_levels(shares)) * shares * 2 * Hkv * 8;
 }
 
-template <int NG>
+template <int NG, bool WIN>
 static cudaError_t launch_sd(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream) {
   using C = SdCfg<NG>;
-  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&decode_scaled_kernel<NG>), C::SMEM,
-                                     NG == 16 ? kAttrDecodeScaled16 : kAttrDecodeScaled8);
+  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(&decode_scaled_kernel<NG, WIN>), C::SMEM,
+                                     WIN ? (NG == 16 ? kAttrWinDecodeScaled16 : kAttrWinDecodeScaled8)
+                                         : (NG == 16 ? kAttrDecodeScaled16 : kAttrDecodeScaled8));
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_scaled_kernel<NG>, dim3(num_sms()), dim3(C::THREADS), C::SMEM, stream, p, tk, tv);
+  return launch_pdl(decode_scaled_kernel<NG, WIN>, dim3(num_sms()), dim3(C::THREADS), C::SMEM, stream, p, tk, tv);
 }
 
 cudaError_t launch_decode_scaled(const DecodeParams& in, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream,
@@ -869,7 +884,8 @@ cudaError_t launch_decode_scaled(const DecodeParams& in, const CUtensorMap& tk, 
   DecodeParams p = in;
   p.launch_shares = sd_shares(p.Hkv);
   *launches += 1;
-  return p.G > 8 ? launch_sd<16>(p, tk, tv, stream) : launch_sd<8>(p, tk, tv, stream);
+  if (p.window > 0) return p.G > 8 ? launch_sd<16, true>(p, tk, tv, stream) : launch_sd<8, true>(p, tk, tv, stream);
+  return p.G > 8 ? launch_sd<16, false>(p, tk, tv, stream) : launch_sd<8, false>(p, tk, tv, stream);
 }
 
 }  // namespace pkv

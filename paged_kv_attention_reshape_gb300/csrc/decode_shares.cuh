@@ -129,7 +129,7 @@ __device__ __noinline__ int64_t scan_set(const int32_t* order, const int32_t* se
 
 // The set's sequences into shared memory (scan_set), the set's size checks, and out = 0,
 // lse = -inf for the sequences with no context, which no share covers (CTA (0, 0)).
-template <int MAXR, int BS>
+template <int MAXR, int BS, bool WIN = false>
 __device__ __forceinline__ int64_t load_set(const DecodeParams& p, int begin, int& n, int* s_pre, int* s_ctx, int* s_r,
                                             int* s_row, int* s_scan) {
   const int tid = threadIdx.x, nthreads = blockDim.x;
@@ -138,8 +138,8 @@ __device__ __forceinline__ int64_t load_set(const DecodeParams& p, int begin, in
   }
   static_assert(MAXR >= kSetChunk, "a launch holds a whole chunk of the set");
   const int cap = min(p.max_seq_len, p.max_blocks * BS);
-  const int64_t total = scan_set<BS>(p.order, p.seq_lens, p.cu_q, begin, n, p.batch_reqs, cap, p.err, s_pre, s_ctx,
-                                     s_r, s_row, s_scan);
+  const int64_t total = scan_set<BS, WIN>(p.order, p.seq_lens, p.cu_q, begin, n, p.batch_reqs, cap, p.err, s_pre, s_ctx,
+                                          s_r, s_row, s_scan, p.window, p.sinks);
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     for (int i = tid; i < n; i += nthreads) {
       if (s_ctx[i] != 0 || s_r[i] < 0) continue;

@@ -207,7 +207,8 @@ enum AttrSlot {
   kAttrMla,
   kAttrWinDecode64,
   kAttrWinDecode128,
-  kAttrWinDecode128Fp8,
+  kAttrWinDecodeScaled8,
+  kAttrWinDecodeScaled16,
   kAttrWinAttn64,
   kAttrWinAttn128,
   kAttrWinAttn128Fp8,
@@ -237,10 +238,11 @@ cudaError_t launch_batch_classify_reorder(const int32_t* cu_q, const int32_t* se
                                           int64_t num_tokens, cudaStream_t stream, int* launches);
 cudaError_t launch_paged_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                 int D, bool fp8, cudaStream_t stream, int* launches);
-// The same over the keys of p.window and p.sinks (p.window >= 1).
-cudaError_t launch_window_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                                 int D, bool fp8, cudaStream_t stream, int* launches);
-// Decode over a block-scaled E4M3 cache (its workspace is never larger than paged_decode's).
+// The same over the keys of p.window and p.sinks (p.window >= 1), of a bf16 cache.
+cudaError_t launch_window_decode(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int D,
+                                 cudaStream_t stream, int* launches);
+// Decode over a block-scaled E4M3 cache (its workspace is never larger than paged_decode's); with p.window >= 1 over
+// the keys of the window and the sinks, and then over a cache with tensor scales too (p.k_scales NULL).
 cudaError_t launch_decode_scaled(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream,
                                  int* launches);
 bool decode_scaled_supported(int Hkv);

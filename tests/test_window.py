@@ -5,13 +5,16 @@ Tolerances (u = 2^-8, half a step of bf16 relative to the value; A = sum_j p_j |
   * a score: D <= 128 fp32 additions of exact products, each off by at most 2^-23 of the sum of magnitudes
     M = scale sum_d |q_d k_d| (a truncating adder): 2^-16 M; 2^-20 (1 + |lse|) for the rounding of
     s * scale * log2(e) - m, of 2^x and of the logarithm (each within 2^-22 of a number of that size). Over an
-    8-bit cache q becomes fp16, which is exact from 2^-14 on and off by at most 2^-25 below: 2^-25 scale sum_d
-    |k_d|, and the extend's new keys likewise. e is the sum of these.
+    8-bit cache the extend's q becomes fp16, which is exact from 2^-14 on and off by at most 2^-25 below: 2^-25 scale
+    sum_d |k_d|, and the new keys likewise. The decode's q is two E4M3 parts, exact down to 2^-14 of the head's largest
+    |q| and off by at most 2^-21 of that below: 2^-21 scale q_top sum_d |k_d|. e is the sum of these.
   * lse: e.
   * out: u |o| for its own rounding; P is rounded to bf16 (u A; fp16 over an 8-bit cache, finer); the exponent's
     error moves p and the sum by e each (2 e A); n fp32 additions of P V (n 2^-23 A). The extend over an 8-bit
     cache rounds new values / v_scale to fp16 (2^-11 A) and P below 2^-14 to steps of 2^-24, where the largest P of the row
-    is 1 at least: 2^-25 sum_j |v_j|.
+    is 1 at least: 2^-25 sum_j |v_j|. The decode over codes rounds P to two E4M3 parts in a frame a tile, off by at most
+    2^-9 P, or 2^-22 of the tile's largest P' = P vs below 2^-14 of it. With values v = vs c and P' <= l vs_top (vs_top: the
+    value scale of the row's largest P'): 2^-22 vs_top sum_j |c_j|, which is 2^-22 sum_j |v_j| where all vs are one.
 """
 import ctypes
 import math
@@ -45,8 +48,11 @@ def make(reqs, Hq, Hkv, D, kind, window, sinks, seed, cached_all=False, pad=3):
     most = max(1, max((h + BS - 1) // BS for h in held))
     nb = sum((h + BS - 1) // BS for h in held) + 3
     perm = torch.randperm(nb, generator=g)
+    if kind == "block":
+        st.update(ks=torch.exp(torch.randn((nb, Hkv), generator=g)) * 0.02, vs=torch.exp(torch.randn((nb, Hkv), generator=g)) * 0.03)
     if kind == "tensor":
         st.update(ks=0.02, vs=0.03)
+    if kind in ("tensor", "block"):
         kc, vc = (torch.randint(0, 127, (nb, BS, Hkv, D), generator=g, dtype=torch.uint8) + 128 *
                   torch.randint(0, 2, (nb, BS, Hkv, D), generator=g, dtype=torch.uint8) for _ in "kv")
         # (magnitudes up to 448: as normal values at these scales would not be larger than 4)
@@ -83,7 +89,12 @@ def cached(st, r, n):
     out = []
     for c, s in (("kc", "ks"), ("vc", "vs")):
         x = st[c][torch.where(ok, page, 0), j % BS]
-        x = x.view(E4M3).float().double() * float(torch.tensor(st[s], dtype=torch.float32)) if st["kind"] == "tensor" else x.double()
+        if st["kind"] == "tensor":
+            x = x.view(E4M3).float().double() * float(torch.tensor(st[s], dtype=torch.float32))
+        elif st["kind"] == "block":
+            x = x.view(E4M3).float().double() * st[s][torch.where(ok, page, 0)].double()[:, :, None]
+        else:
+            x = x.double()
         x[~ok] = 0
         out.append(torch.nan_to_num(x))
     return out
@@ -117,7 +128,19 @@ def reference(st, decode=False):
             o, A = p @ vh, p @ vh.abs()
             e = 2.0 ** -16 * mag + 2.0 ** -20 * (1 + z.abs())
             sumv = 0.0
-            if st["kind"] == "tensor":
+            if st["kind"] in ("tensor", "block") and decode:
+                e = e + 2.0 ** -21 * scale * q.abs().max() * kh.abs().sum(-1).max()
+                codes = vh.abs() / (st["vs"] if st["kind"] == "tensor" else torch.ones(()))
+                if st["kind"] == "block":
+                    j = torch.arange(c + n)
+                    page = st["table"][r].long()[j // BS]
+                    vs = st["vs"][torch.where(page < st["vs"].shape[0], page, 0), h // G].double()
+                    codes = vh.abs() / vs[:, None]
+                    top = vs[(s + torch.log(vs)).argmax(-1)][:, None]
+                else:
+                    top = st["vs"]
+                sumv = 2.0 ** -22 * top * (seen.double() @ codes)
+            elif st["kind"] == "tensor":
                 e = e + 2.0 ** -25 * scale * (kh.abs().sum(-1).max() + q.abs().sum(-1))
                 sumv = 2.0 ** -25 * (seen.double() @ vh.abs())
             rows = slice(row, row + n)
@@ -139,8 +162,8 @@ def call(st, which, **more):
     out = torch.full_like(g["q"], 7.0)
     lse = torch.full(g["q"].shape[:2], 7.0, dtype=torch.float32, device="cuda")
     kw = dict(window=st["window"], sinks=st["sinks"], out=out, lse=lse, **more)
-    if st["kind"] == "tensor":
-        kw.update(k_scale=st["ks"], v_scale=st["vs"])
+    if st["kind"] in ("tensor", "block"):
+        kw.update(k_scale=g["ks"], v_scale=g["vs"])
     max_len, max_new = max(1, int(st["lens"].max())), max(1, max(n for _, n in st["reqs"]))
     if which == "decode":
         pkv.paged_decode_attn(g["q"], g["kc"], g["vc"], g["table"], g["lens"], max_len, cu_q=g["cu"], **kw)
@@ -194,8 +217,9 @@ def test_refusals():
     scaled = _lib.PkvCache(fake, fake, 10, 16, 2, 128, 16 * 2 * 128, _lib.KV_FP8_E4M3_BLOCK, 1.0, 1.0, fake, fake)
     fp8_64 = _lib.PkvCache(fake, fake, 10, 16, 2, 64, 16 * 2 * 64, _lib.KV_FP8_E4M3, 1.0, 1.0)
     block32 = _lib.PkvCache(fake, fake, 10, 32, 2, 128, 32 * 2 * 128)
-    for cache in (scaled, fp8_64, block32):
+    for cache in (fp8_64, block32):
         assert decode(5, 0, cache) == 2 and extend(5, 0, cache) == 2
+    assert decode(5, 0, scaled) == 3 and extend(5, 0, scaled) == 2
     # the binding's arguments
     with pytest.raises(binding.PkvError):
         binding._window(None, 4)
@@ -215,14 +239,15 @@ LENS = [0, 1, 2, 15, 16, 17, 31, 33, 100, 127, 129, 260, 300]
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("window,sinks", [(1, 0), (2, 1), (16, 0), (17, 16), (64, 4), (100, 17), (128, 130), (260, 0), (5000, 3)])
-@pytest.mark.parametrize("kind,D,Hq,Hkv", [("bf16", 64, 8, 2), ("bf16", 128, 16, 1), ("tensor", 128, 6, 3), ("bf16", 128, 5, 5)])
+@pytest.mark.parametrize("kind,D,Hq,Hkv", [("bf16", 64, 8, 2), ("bf16", 128, 16, 1), ("tensor", 128, 6, 3), ("bf16", 128, 5, 5),
+                                           ("tensor", 128, 32, 2), ("block", 128, 16, 2), ("block", 128, 16, 1)])
 def test_decode(kind, D, Hq, Hkv, window, sinks):
     st = make([(n - 1, 1) if n else (-1, 1) for n in LENS], Hq, Hkv, D, kind, window, sinks, 3, cached_all=True)
     check(call(st, "decode"), reference(st, decode=True), st["T"])
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind,D,Hq,Hkv", [("bf16", 128, 64, 8), ("tensor", 128, 64, 8), ("bf16", 64, 16, 4)])
+@pytest.mark.parametrize("kind,D,Hq,Hkv", [("bf16", 128, 64, 8), ("tensor", 128, 64, 8), ("bf16", 64, 16, 4), ("block", 128, 32, 8)])
 @pytest.mark.parametrize("lens,window,sinks", [([9000], 4096, 64), ([5000, 40, 7001], 3001, 5), ([700] * 40, 500, 0)])
 def test_decode_cut_sequences(kind, D, Hq, Hkv, lens, window, sinks):
     """Few long windows: their blocks are cut into shares and merged."""
@@ -406,6 +431,10 @@ def test_refused_by_the_binding():
     st = on_gpu(make([(60, 1)], 4, 2, 128, "tensor", 40, 0, 3, cached_all=True, pad=0))
     s = torch.ones((st["kc"].shape[0], 2), device="cuda")
     a = (st["q"], st["kc"], st["vc"], st["table"], st["lens"], 64)
-    for kw in (dict(window=0), dict(window=-1), dict(window=4, sinks=-1), dict(sinks=3), dict(window=4, k_scale=s, v_scale=s)):
+    for kw in (dict(window=0), dict(window=-1), dict(window=4, sinks=-1), dict(sinks=3)):
         with pytest.raises(pkv.PkvError):
             pkv.paged_decode_attn(*a, **kw)
+    with pytest.raises(pkv.PkvError):  # extend over block scales has no window
+        cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        pkv.extend_attn(st["q"], st["k_new"], st["v_new"], cu, st["lens"], st["kc"], st["vc"], st["table"], 1, 64, window=4,
+                        k_scale=s, v_scale=s)
