@@ -231,13 +231,16 @@ pkv_status pkv_kv_append(const void* q, int64_t q_stride, const void* key, int64
  * The pages have no counterpart; models that norm their queries and keys head by head take it
  * in the place of kv_append. Each query head x of a token becomes
  *   x / sqrt(sum_d x_d^2 / head_dim + eps) * q_weight   (keys alike with k_weight; values are
- * left as they are) in fp32, every operation rounded by itself (the root's inverse is off by at
- * most two units in the last place), and is not rounded further before the rotation. Everything
- * else is as in kv_append: what is turned, stored, returned and scaled is the normed row.
+ * left as they are), in fp32 and not rounded further before the rotation (the row's factor is
+ * multiplied in last, its root's inverse off by at most two units in the last place; a normed and
+ * turned element is off by less than 2^-18 of its pair's magnitudes before it is rounded to what
+ * is stored). Everything else is as in kv_append: what is stored, returned and scaled is the
+ * normed row.
  * norm: q_weight, k_weight device [head_dim], 16-byte aligned, one of them NULL for a side that
  * has no norm (both NULL: PKV_ERR_INVALID_ARG); bf16, or fp32 when weight_f32 != 0; eps > 0 and
  * finite. head_dim: a power of two of at most 512, no latent cache (others PKV_ERR_UNSUPPORTED).
- * Elements whose squares sum up beyond fp32 give zeros (of magnitudes up to 2^59 none do).
+ * Magnitudes up to 2^59 keep their squares' sum, and their products with weights up to 2^60,
+ * within fp32; beyond, a row may become zeros, infinite or NaN.
  * ------------------------------------------------------------------------------------- */
 typedef struct {
   const void* q_weight;

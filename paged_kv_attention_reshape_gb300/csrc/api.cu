@@ -396,6 +396,7 @@ static pkv_status run_append(const void* q, int64_t q_stride, const void* key, i
     p.q_norm = norm->q_weight;
     p.k_norm = norm->k_weight;
     p.norm_eps = norm->eps;
+    p.norm_inv_d = 1.f / static_cast<float>(D);
     p.norm_f32 = norm->weight_f32;
   }
   int launches = 0;

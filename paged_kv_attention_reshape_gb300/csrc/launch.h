@@ -140,7 +140,7 @@ struct AppendParams {
   float* v_scales;
   const void* q_norm;      // [D] weights of the heads' norms (NULL: that side has none)
   const void* k_norm;
-  float norm_eps;
+  float norm_eps, norm_inv_d;  // 1 / D
   int32_t norm_f32;        // the weights are fp32 (else bf16)
   int32_t run_tokens;      // block scales: tokens whose runs one CTA appends (set by the launcher)
   uint32_t run_groups;     // block scales: groups of tokens whose runs a CTA appends (set by the launcher)
