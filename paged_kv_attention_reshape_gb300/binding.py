@@ -444,6 +444,26 @@ def _window(window, sinks):
     return min(int(window), 2**31 - 1), min(int(sinks), 2**31 - 1)
 
 
+def _window_args(q, heads, dim, rows, index, out, lse, kv=()):
+    """Checks the tensors of a windowed call: on the current device, of the shapes the kernels read and write.
+    index: (tensor, name, least entries); kv: (tensor, name) rows of keys and values [rows, heads, dim]."""
+    dev = torch.cuda.current_device()
+    if q.get_device() != dev:
+        raise PkvError("q must be on the current device")
+    if q.shape[2] != dim or not q.is_contiguous():
+        raise PkvError(f"q must be contiguous [T, Hq, {dim}]")
+    for t, name in kv:
+        if t.get_device() != dev or t.shape != (rows, heads, dim) or not t.is_contiguous():
+            raise PkvError(f"{name} must be contiguous [{rows}, {heads}, {dim}] on the current device")
+    for t, name, least in index:
+        if t is not None and (t.get_device() != dev or t.dtype is not torch.int32 or t.numel() < least or not t.is_contiguous()):
+            raise PkvError(f"{name} must be at least {least} contiguous int32 entries on the current device")
+    if out.shape != q.shape or out.dtype is not torch.bfloat16 or out.get_device() != dev or not out.is_contiguous():
+        raise PkvError("out must be contiguous bf16 like q")
+    if lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
+        raise PkvError("lse must be contiguous fp32 [T, Hq]")
+
+
 def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, cu_q=None,
                       reqs: Optional[Reqs] = None, scale=None, out=None, lse=None, workspace=None,
                       stream=None, k_scale=1.0, v_scale=1.0, window=None, sinks=0):
@@ -470,6 +490,10 @@ def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, 
     win = _window(window, sinks)
     workspace = _scratch(need, workspace, q.device, other)
     if win is not None:
+        _window_args(q, 0, cache.head_dim, 0, ((block_tables, "block_tables", 0), (seq_lens, "seq_lens", reqs.batch_reqs),
+                                               (cu_q, "cu_q", reqs.batch_reqs + 1)), out, lse)
+        if k_cache.get_device() != q.get_device() or block_tables.dim() != 2 or block_tables.shape[0] < reqs.batch_reqs:
+            raise PkvError("the cache must be on q's device, and block_tables [requests, max_blocks]")
         _check(lib.pkv_window_decode_attn(_ptr(q), cache, _ptr(block_tables), block_tables.shape[1],
                                           _ptr(seq_lens), _ptr(cu_q), reqs.c(), Hq, max_seq_len, *win,
                                           _scale(scale, D), _ptr(out), _ptr(lse), _ptr(workspace),
@@ -564,6 +588,11 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
         lse = _empty((T, Hq), torch.float32, q.device, other)
     win = _window(window, sinks)
     if win is not None:
+        _window_args(q, cache.num_kv_heads, cache.head_dim, T,
+                     ((block_tables, "block_tables", 0), (seq_lens, "seq_lens", reqs.batch_reqs),
+                      (cu_q, "cu_q", reqs.batch_reqs + 1)), out, lse, ((k_new, "k_new"), (v_new, "v_new")))
+        if k_cache.get_device() != q.get_device() or block_tables.dim() != 2 or block_tables.shape[0] < reqs.batch_reqs:
+            raise PkvError("the cache must be on q's device, and block_tables [requests, max_blocks]")
         _check(lib.pkv_window_extend_attn(_ptr(q), _ptr(k_new), _ptr(v_new), T, _ptr(cu_q), _ptr(seq_lens), cache,
                                           _ptr(block_tables), block_tables.shape[1], reqs.c(), Hq, max_q_len,
                                           max_seq_len, *win, _scale(scale, D), _ptr(out), _ptr(lse),
@@ -611,6 +640,7 @@ def varlen_prefill_attn(q, k, v, cu_seqlens, max_seqlen, reqs: Optional[Reqs] = 
         lse = _empty((T, Hq), torch.float32, q.device, other)
     win = _window(window, sinks)
     if win is not None:
+        _window_args(q, Hkv, D, T, ((cu_seqlens, "cu_seqlens", reqs.batch_reqs + 1),), out, lse, ((k, "k"), (v, "v")))
         _check(lib.pkv_window_prefill_attn(_ptr(q), _ptr(k), _ptr(v), T, _ptr(cu_seqlens), reqs.c(), Hq, Hkv, D,
                                            max_seqlen, *win, _scale(scale, D), _ptr(out), _ptr(lse),
                                            _stream(stream)), "varlen_prefill_attn")

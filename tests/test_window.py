@@ -438,3 +438,71 @@ def test_refused_by_the_binding():
         cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
         pkv.extend_attn(st["q"], st["k_new"], st["v_new"], cu, st["lens"], st["kc"], st["vc"], st["table"], 1, 64, window=4,
                         k_scale=s, v_scale=s)
+
+
+@pytest.mark.gpu
+def test_tensors_of_other_shapes_are_refused():
+    import paged_kv_attention_reshape_gb300 as pkv
+    st = on_gpu(make([(60, 3), (40, 2)], 4, 2, 128, "bf16", 40, 0, 3, pad=0))
+    a = dict(q=st["q"], k=st["k_new"], v=st["v_new"], cu=st["cu"], lens=st["lens"], table=st["table"])
+
+    def extend(out=None, lse=None, **x):
+        t = {**a, **x}
+        pkv.extend_attn(t["q"], t["k"], t["v"], t["cu"], t["lens"], st["kc"], st["vc"], t["table"], 3, 64, window=9, out=out, lse=lse)
+
+    def decode(out=None, lse=None, **x):
+        t = {**a, **x}
+        pkv.paged_decode_attn(t["q"][:2], st["kc"], st["vc"], t["table"], t["lens"], 64, window=9, out=out, lse=lse)
+
+    def prefill(out=None, lse=None, **x):
+        t = {**a, **x}
+        pkv.varlen_prefill_attn(t["q"], t["k"], t["v"], t["cu"], 3, window=9, out=out, lse=lse)
+
+    bad = dict(q=st["q"][:, :, :64].contiguous(), k=st["k_new"][:3], v=st["v_new"][:, :1], cu=st["cu"][:2], lens=st["lens"].long(),
+               table=st["table"][:1])
+    for f, names in ((extend, bad), (decode, ("q", "lens", "table")), (prefill, ("k", "v"))):
+        f()
+        for n in names:
+            with pytest.raises(pkv.PkvError):
+                f(**{n: bad[n]})
+        for o in (dict(out=torch.empty((1, 4, 128), dtype=torch.bfloat16, device="cuda")), dict(lse=torch.empty((9, 4), device="cuda"))):
+            with pytest.raises(pkv.PkvError):
+                f(**o)
+    assert pkv.device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "tensor"])
+def test_keys_and_values_in_one_allocation(kind):
+    """[num_blocks, 2, ...]: K and V blocks alternate, and the pool's pages lie two blocks apart."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    for which, mix in (("decode", [(300, 1), (17, 1)]), ("extend", [(300, 40), (17, 3)])):
+        st = make(mix, 8, 2, 128, kind, 150, 9, 41, cached_all=which == "decode")
+        want = call(st, which)
+        both = torch.stack([st["kc"], st["vc"]], 1)
+        st["kc"], st["vc"] = both[:, 0], both[:, 1]
+        g = both.cuda()
+        one = dict(st, kc=g[:, 0], vc=g[:, 1])
+        got = call(one, which)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """Extends and decodes on two streams beside one another, each with what is its own: the bits of calls alone."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    cases = [make([(700, 90), (30, 300), (0, 400)], 16, 2, 128, "bf16", 200, 9, s, pad=0) for s in (51, 52)]
+    want = [call(c, "extend") for c in cases]
+    g = [on_gpu(c) for c in cases]
+    outs = [[torch.empty_like(x["q"]) for _ in range(20)] for x in g]
+    streams = [torch.cuda.Stream() for _ in g]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for x, o, s in zip(g, outs, streams):
+            with torch.cuda.stream(s):
+                pkv.extend_attn(x["q"], x["k_new"], x["v_new"], x["cu"], x["lens"], x["kc"], x["vc"], x["table"], 400, 800,
+                                window=200, sinks=9, out=o[i])
+    torch.cuda.synchronize()
+    assert pkv.device_errors() == 0
+    for o, w in zip(outs, want):
+        assert all(torch.equal(x.cpu(), w[0]) for x in o)
