@@ -451,8 +451,15 @@ pkv_status pkv_varlen_prefill_attn(const void* q, const void* k, const void* v, 
  *   - a value that is not finite in a key that some row sees may reach the rows of the same
  *     request and KV head that do not see it, for extend and prefill. Keys that no row sees
  *     touch nothing, whatever they hold.
- * The decode takes the workspace of paged_decode_attn; extend and prefill need none.
+ * The decode takes the workspace of paged_decode_attn; prefill needs none. The extend over an FP8
+ * cache may be given one (16-byte aligned; NULL: none), rewritten by the call: the keys and values that
+ * requests of many new tokens see are then converted there once, as far as it reaches, instead of
+ * by every SM that reads them.
+ * pkv_window_extend_workspace_size is what such a call can use (at most 1 GiB; 0: nothing).
  * ------------------------------------------------------------------------------------- */
+size_t pkv_window_extend_workspace_size(int64_t num_tokens, int32_t max_reqs, int32_t max_q_len, int32_t max_seq_len,
+                                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t kv_dtype,
+                                        int32_t window, int32_t sinks);
 pkv_status pkv_window_decode_attn(const void* q, pkv_cache cache, const int32_t* block_tables,
                                   int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_q,
                                   pkv_reqs reqs, int32_t num_q_heads, int32_t max_seq_len, int32_t window,
@@ -462,7 +469,8 @@ pkv_status pkv_window_extend_attn(const void* q, const void* k_new, const void* 
                                   const int32_t* cu_q, const int32_t* seq_lens, pkv_cache cache,
                                   const int32_t* block_tables, int32_t max_blocks, pkv_reqs reqs,
                                   int32_t num_q_heads, int32_t max_q_len, int32_t max_seq_len, int32_t window,
-                                  int32_t sinks, float scale, void* out, float* lse, pkv_stream_t stream);
+                                  int32_t sinks, float scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, pkv_stream_t stream);
 pkv_status pkv_window_prefill_attn(const void* q, const void* k, const void* v, int64_t num_tokens,
                                    const int32_t* cu_seqlens, pkv_reqs reqs, int32_t num_q_heads,
                                    int32_t num_kv_heads, int32_t head_dim, int32_t max_seqlen, int32_t window,

@@ -61,7 +61,8 @@ SIGNATURES = [
                               P, P, P, sz, P]),
     ("pkv_varlen_prefill_attn", i32, [P, P, P, i64, P, PkvReqs, i32, i32, i32, i32, f32, P, P, P]),
     ("pkv_window_decode_attn", i32, [P, PkvCache, P, i32, P, P, PkvReqs, i32, i32, i32, i32, f32, P, P, P, sz, P]),
-    ("pkv_window_extend_attn", i32, [P, P, P, i64, P, P, PkvCache, P, i32, PkvReqs, i32, i32, i32, i32, i32, f32, P, P, P]),
+    ("pkv_window_extend_attn", i32, [P, P, P, i64, P, P, PkvCache, P, i32, PkvReqs, i32, i32, i32, i32, i32, f32, P, P, P, sz, P]),
+    ("pkv_window_extend_workspace_size", sz, [i64, i32, i32, i32, i32, i32, i32, i32, i32, i32]),
     ("pkv_window_prefill_attn", i32, [P, P, P, i64, P, PkvReqs, i32, i32, i32, i32, i32, i32, f32, P, P, P]),
     ("pkv_kv_block_pack", i32, [PkvCache, P, i32, P, P]),
     ("pkv_kv_block_unpack", i32, [P, P, i32, PkvCache, P]),

@@ -569,8 +569,9 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
     partial results of contexts that are cut (allocated here when not given).
 
     With a window each row sees the last `window` keys up to its own and the first `sinks` keys (a
-    bf16 cache, or an FP8 one with per-tensor scales at head_dim 128; no workspace); table entries of
-    blocks that no row sees are not read."""
+    bf16 cache, or an FP8 one with per-tensor scales at head_dim 128); table entries of blocks that no row sees
+    are not read. Over FP8 the workspace holds what requests of many new tokens see, converted once (allocated
+    here when not given)."""
     lib = _lib.load()
     for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
         _need(t, torch.bfloat16, n)
@@ -593,10 +594,13 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
                       (cu_q, "cu_q", reqs.batch_reqs + 1)), out, lse, ((k_new, "k_new"), (v_new, "v_new")))
         if k_cache.get_device() != q.get_device() or block_tables.dim() != 2 or block_tables.shape[0] < reqs.batch_reqs:
             raise PkvError("the cache must be on q's device, and block_tables [requests, max_blocks]")
+        need = window_extend_workspace_size(T, reqs.max_reqs, max_q_len, max_seq_len, Hq, cache.num_kv_heads, D, *win,
+                                            kv_dtype=cache.kv_dtype) if cache.kv_dtype == _lib.KV_FP8_E4M3 else 0
+        workspace = _scratch(need, workspace, q.device, other)
         _check(lib.pkv_window_extend_attn(_ptr(q), _ptr(k_new), _ptr(v_new), T, _ptr(cu_q), _ptr(seq_lens), cache,
                                           _ptr(block_tables), block_tables.shape[1], reqs.c(), Hq, max_q_len,
                                           max_seq_len, *win, _scale(scale, D), _ptr(out), _ptr(lse),
-                                          _stream(stream)), "extend_attn")
+                                          _ptr(workspace) if need else None, need, _stream(stream)), "extend_attn")
         return out, lse
     need = 0
     if cache.kv_dtype == _lib.KV_FP8_E4M3:
@@ -614,6 +618,12 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
 
 def extend_block_workspace_size(max_q_len, max_seq_len, num_q_heads, num_kv_heads) -> int:
     return int(_lib.load().pkv_extend_block_workspace_size(max_q_len, max_seq_len, num_q_heads, num_kv_heads))
+
+
+def window_extend_workspace_size(num_tokens, max_reqs, max_q_len, max_seq_len, num_q_heads, num_kv_heads, head_dim, window,
+                                 sinks=0, kv_dtype=_lib.KV_FP8_E4M3) -> int:
+    return int(_lib.load().pkv_window_extend_workspace_size(num_tokens, max_reqs, max_q_len, max_seq_len, num_q_heads,
+                                                            num_kv_heads, head_dim, kv_dtype, window, sinks))
 
 
 def extend_fp8_workspace_size(max_reqs, batch_reqs, max_seq_len, max_blocks, num_kv_heads, head_dim) -> int:

@@ -792,6 +792,10 @@ pkv_status pkv_mla_decode_attn(const void* q, pkv_cache cache, const int32_t* bl
 
 size_t pkv_extend_workspace_size(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
 
+// The windowed extend's pool over codes: fp16 K and V of 16 tokens a block, at most 1 GiB.
+static size_t window_pool_block_bytes(int32_t Hkv, int32_t D) { return static_cast<size_t>(2) * 16 * Hkv * D * 2; }
+static int64_t window_pool_limit(int32_t Hkv, int32_t D) { return (int64_t(1) << 30) / static_cast<int64_t>(window_pool_block_bytes(Hkv, D)); }
+
 // Extend (cache != NULL) and prefill (cache == NULL) share the checks and the kernel.
 // ctx_kind: the cache is bf16 (kAttnCtxBf16), a bf16 pool holding the E4M3 values of an FP8
 // cache (kAttnCtxPool), or the FP8 cache itself, read as codes (kAttnCtxFp8, head_dim 128).
@@ -803,7 +807,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
                                 int32_t D, int32_t max_q_len, int32_t max_seq_len, float scale,
                                 void* out, float* lse, pkv_stream_t stream, int ctx_kind = kAttnCtxBf16,
                                 float ctx_k_scale = 1.f, float ctx_v_scale = 1.f, void* workspace = nullptr,
-                                int32_t window = 0, int32_t sinks = 0) {
+                                int32_t window = 0, int32_t sinks = 0, size_t workspace_bytes = 0) {
   pkv_status st = check_reqs(reqs);
   if (st != PKV_OK) return st;
   if (cache != nullptr && (st = check_cache(*cache, true, true)) != PKV_OK) return st;
@@ -851,7 +855,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
   p.sinks = sinks;
   p.k_scales = cache ? cache->k_scales : nullptr;
   p.v_scales = cache ? cache->v_scales : nullptr;
-  CUtensorMap tq, tk, tv, tck, tcv, tqf, tk16, tv16;
+  CUtensorMap tq, tk, tv, tck, tcv, tqf, tk16, tv16, pool[4];
   std::memset(&tck, 0, sizeof tck);
   std::memset(&tcv, 0, sizeof tcv);
   const bool windowed = window > 0, packed = ctx_kind == kAttnCtxBlock;
@@ -869,6 +873,27 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
     as_block.stride_block = num_tokens * Hkv * D;
     as_block.kv_dtype = PKV_KV_BF16;
     if (!encode_cache(&tk16, k, as_block, 16) || !encode_cache(&tv16, v, as_block, 16)) return PKV_ERR_CUDA;
+    if (ctx_kind == kAttnCtxFp8 && workspace != nullptr) {
+      const int64_t need = attn_window_pool_blocks(num_tokens, reqs.max_reqs, max_q_len, max_seq_len, Hq, Hkv, window, sinks);
+      p.pool_blocks = static_cast<int32_t>(
+          std::min(std::min(need, window_pool_limit(Hkv, D)), static_cast<int64_t>(workspace_bytes / window_pool_block_bytes(Hkv, D))));
+    }
+    if (p.pool_blocks > 0) {
+      if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+      const int64_t rows = static_cast<int64_t>(p.pool_blocks) * 16;
+      p.pool_k = workspace;
+      p.pool_v = static_cast<uint8_t*>(workspace) + rows * Hkv * D * 2;
+      p.k_codes = static_cast<const uint8_t*>(cache->k);
+      p.v_codes = static_cast<const uint8_t*>(cache->v);
+      p.stride_block = cache->stride_block;
+      p.k_new = static_cast<const __nv_bfloat16*>(k);
+      p.v_new = static_cast<const __nv_bfloat16*>(v);
+      as_block.block_size = static_cast<int32_t>(rows);
+      as_block.stride_block = rows * Hkv * D;
+      if (!encode_cache(&pool[0], p.pool_k, as_block, 16) || !encode_cache(&pool[1], p.pool_v, as_block, 16) ||
+          !encode_rows(&pool[2], p.pool_k, rows, Hkv, D, 128) || !encode_rows(&pool[3], p.pool_v, rows, Hkv, D, 128))
+        return PKV_ERR_CUDA;
+    }
   }
   if (cache != nullptr &&
       (!encode_cache(&tck, cache->k, *cache) || !encode_cache(&tcv, cache->v, *cache)))
@@ -878,7 +903,7 @@ static pkv_status run_attention(const void* q, const void* k, const void* v, int
     p.set_offset = off;
     p.sched_slot = next_sched_slot(reinterpret_cast<cudaStream_t>(stream));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    st = cuda_status(windowed ? launch_attn_window(p, tq, tk16, tv16, tk, tv, tck, tcv, D, ctx_kind == kAttnCtxFp8, s, &launches)
+    st = cuda_status(windowed ? launch_attn_window(p, tq, tk16, tv16, tk, tv, tck, tcv, pool, D, ctx_kind == kAttnCtxFp8, s, &launches)
                      : packed ? launch_attn_scaled(p, tq, tk, tv, tck, tcv, workspace, s, &launches)
                               : launch_attention(p, tq, tk, tv, tck, tcv, tqf, D, cache != nullptr ? ctx_kind : kAttnCtxBf16,
                                                  s, &launches));
@@ -1013,18 +1038,29 @@ pkv_status pkv_varlen_prefill_attn(const void* q, const void* k, const void* v, 
                        lse, stream);
 }
 
+size_t pkv_window_extend_workspace_size(int64_t num_tokens, int32_t max_reqs, int32_t max_q_len, int32_t max_seq_len,
+                                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t kv_dtype,
+                                        int32_t window, int32_t sinks) {
+  if (num_tokens <= 0 || max_reqs <= 0 || max_q_len <= 0 || max_seq_len <= 0 || head_dim != 128 || kv_dtype != PKV_KV_FP8_E4M3 ||
+      !group_ok(num_q_heads, num_kv_heads) || !window_ok(window, sinks))
+    return 0;
+  const int64_t blocks = attn_window_pool_blocks(num_tokens, max_reqs, max_q_len, max_seq_len, num_q_heads, num_kv_heads, window, sinks);
+  return static_cast<size_t>(std::min(blocks, window_pool_limit(num_kv_heads, head_dim))) * window_pool_block_bytes(num_kv_heads, head_dim);
+}
+
 pkv_status pkv_window_extend_attn(const void* q, const void* k_new, const void* v_new, int64_t num_tokens,
                                   const int32_t* cu_q, const int32_t* seq_lens, pkv_cache cache,
                                   const int32_t* block_tables, int32_t max_blocks, pkv_reqs reqs,
                                   int32_t num_q_heads, int32_t max_q_len, int32_t max_seq_len, int32_t window,
-                                  int32_t sinks, float scale, void* out, float* lse, pkv_stream_t stream) {
+                                  int32_t sinks, float scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, pkv_stream_t stream) {
   if (!window_ok(window, sinks)) return PKV_ERR_INVALID_ARG;
   const bool fp8 = cache.kv_dtype == PKV_KV_FP8_E4M3;
   if (cache.kv_dtype == PKV_KV_FP8_E4M3_BLOCK) return PKV_ERR_UNSUPPORTED;
   return run_attention(q, k_new, v_new, num_tokens, cu_q, seq_lens, &cache, block_tables, max_blocks, reqs, num_q_heads,
                        cache.num_kv_heads, cache.head_dim, max_q_len, max_seq_len, scale, out, lse, stream,
-                       fp8 ? kAttnCtxFp8 : kAttnCtxBf16, fp8 ? cache.k_scale : 1.f, fp8 ? cache.v_scale : 1.f, nullptr,
-                       window, sinks);
+                       fp8 ? kAttnCtxFp8 : kAttnCtxBf16, fp8 ? cache.k_scale : 1.f, fp8 ? cache.v_scale : 1.f, workspace,
+                       window, sinks, workspace_bytes);
 }
 
 pkv_status pkv_window_prefill_attn(const void* q, const void* k, const void* v, int64_t num_tokens,

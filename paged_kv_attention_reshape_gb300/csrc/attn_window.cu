@@ -36,6 +36,7 @@
 // first half of its S.
 #include <math_constants.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -47,11 +48,15 @@ namespace pkv {
 
 namespace {
 
-// FP8: the cache holds E4M3 codes. They land as such, converter warps turn them, Q and the new rows into fp16 in
-// shared memory (every E4M3 value is an fp16 number; new values are divided by the value scale), and the products
-// run on fp16.
-template <int D, bool FP8>
+// What the kernel reads. kWnBf16: a bf16 cache (or none) and the new rows. Over a cache of E4M3 codes the products run
+// on fp16 (every E4M3 value is an fp16 number; new values are divided by the value scale). kWnCodes: the codes and
+// the new rows land as they are, and converter warps turn them and Q into fp16 in shared memory. kWnPool: fp16 rows that
+// the kWnCodes launch before has converted, once for all items that read them (wn_fill); the softmax warps convert Q.
+enum { kWnBf16, kWnCodes, kWnPool };
+
+template <int D, int KIND>
 struct WnCfg {
+  static constexpr bool FP8 = KIND == kWnCodes, F16 = KIND != kWnBf16;
   static constexpr int BN = 128, CHUNKS = BN / 16;        // keys of a tile
   static constexpr int HALVES = D / 64;
   static constexpr int Q_HALF = 128 * 128;                // 128 rows x 128 bytes
@@ -66,8 +71,8 @@ struct WnCfg {
   // launched at 168 registers a thread (FP8: 96); the softmax warps take some of the others'
   static constexpr int REGS_LAUNCH = FP8 ? 96 : 168, REGS_SOFTMAX = FP8 ? 144 : 208, REGS_OTHER = FP8 ? 64 : 80;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "register split");
-  // How far (in powers of two) scores may pass a row's m before it follows them: far in bf16; P <= 2^8 in fp16.
-  static constexpr float LAZY = FP8 ? 8.f : 20.f;
+  // How far (in powers of two) scores may pass a row's m before it follows them: far in bf16; P <= 2^15 in fp16.
+  static constexpr float LAZY = F16 ? 15.f : 20.f;
   static constexpr int ITEM_RING = 4;                     // claimed items published to the other roles
   static constexpr int ITEM_READERS = 8 + 2 + (FP8 ? 2 * NCONV : 1);
   static constexpr int RING_OFF = 2 * Q_BYTES;
@@ -91,8 +96,8 @@ struct WnBars {
   uint64_t rows[4];       // the two warps that share a split item's 32 rows
   uint64_t drained;       // the products in flight when a role gave up
 };
-template <int D, bool FP8>
-constexpr int wn_smem() { return 1024 + WnCfg<D, FP8>::BAR_OFF + static_cast<int>(sizeof(WnBars)); }
+template <int D, int KIND>
+constexpr int wn_smem() { return 1024 + WnCfg<D, KIND>::BAR_OFF + static_cast<int>(sizeof(WnBars)); }
 
 __device__ __forceinline__ constexpr uint32_t wn_scol(int slot) { return slot * 128u; }
 __device__ __forceinline__ constexpr uint32_t wn_ocol(int slot) { return 256u + slot * 128u; }
@@ -127,8 +132,9 @@ __device__ __forceinline__ int wn_cost(const AttnParams& p, const int4& q) {
   return static_cast<int>(min(static_cast<int64_t>(q.z) + q.w, static_cast<int64_t>(p.window) + p.sinks));
 }
 
-// Item idx of a request {request id, first query row, q_len, cached tokens}.
-__device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, int idx) {
+// Item idx of a request {request id, first query row, q_len, cached tokens}, or one half of its tokens (half 0 or 1; -1:
+// all). A second half without tokens is the first one again: another CTA, which had nothing else to do, writes the same.
+__device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, int idx, int half) {
   WnItem it;
   it.r = q.x;
   it.row0 = q.y;
@@ -136,7 +142,8 @@ __device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, in
   const int span = 256 / p.G, tile = idx / p.Hkv;
   it.kh = idx - tile * p.Hkv;
   it.tok0 = span * (wn_count(q, p.G) - 1 - tile);  // later (heavier) rows of a request first
-  it.ntok = min(span, q.z - it.tok0);
+  if (half == 1 && q.z - it.tok0 > span / 2) it.tok0 += span / 2;
+  it.ntok = min(half < 0 ? span : span / 2, q.z - it.tok0);
   it.split = it.ntok * p.G <= 128;
   const int P0 = it.C + it.tok0, P1 = it.last();
   it.cb = (it.C + 15) / 16;
@@ -155,6 +162,70 @@ __device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, in
   it.vt = (it.C & 15) == 0 ? -1 : it.cb - 1 < it.head ? it.cb - 1 : it.cb - 1 - it.gap;
   if (it.vt < it.head && it.cb - 1 >= it.head) it.vt = -1;  // (it lies in the gap)
   return it;
+}
+
+// ---- the pool (kWnPool) --------------------------------------------------------------------------------
+// The pool holds, request after request, the chunks of 16 keys that some row of the request sees: the `hb` blocks of
+// sinks, the cached blocks from the first row's window on, the new tokens. Chunk u of a request lies at its first
+// block + u, less `gap` from hb on. A request belongs to it when it has kPoolRows rows a KV head and the pool has room.
+constexpr int kPoolRows = 1024;
+struct WnPooled {
+  int cb, hb, gap;
+  __device__ WnPooled(const AttnParams& p, int C) {
+    const int low = max(C - p.window + 1, 0);
+    cb = (C + 15) / 16;
+    hb = (min(p.sinks, C) + 15) / 16;
+    gap = max((low < C ? low / 16 : cb) - hb, 0);
+  }
+  __device__ int at(int u) const { return u < hb ? u : u - gap; }
+};
+// Blocks of the pool for a request {request id, first query row, q_len, cached tokens}; 0: it is too short.
+__device__ __forceinline__ int wn_pool_need(const AttnParams& p, const int4& q) {
+  if (static_cast<int64_t>(q.z) * p.G < kPoolRows || q.z > p.num_tokens) return 0;
+  const WnPooled w(p, q.w);
+  return min(w.cb - w.gap + (q.z + 15) / 16, p.pool_blocks + 1);  // (the sum over a launch's requests stays in range)
+}
+// Where request i of the launch begins in the pool (the requests before it, those without room included), or -1.
+__device__ __forceinline__ int wn_pool_base(const AttnParams& p, const int* need, int i) {
+  int base = 0;
+#pragma unroll 8
+  for (int j = 0; j < i; ++j) base += need[j];
+  return need[i] > 0 && base + need[i] <= p.pool_blocks ? base : -1;
+}
+
+// Request i of this launch's chunk of the set: {request id, first query row, q_len, cached tokens}.
+__device__ __forceinline__ int4 wn_request(const AttnParams& p, int begin, int i) {
+  const int r = p.order ? p.order[begin + i] : begin + i;
+  if (r < 0 || r >= p.batch_reqs) {
+    if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_REQS);
+    return make_int4(0, 0, 0, 0);
+  }
+  const int q_len = max(0, p.cu_q[r + 1] - p.cu_q[r]);
+  int c = 0;
+  if (p.seq_lens != nullptr) {
+    c = max(0, p.seq_lens[r] - q_len);
+    if (c > static_cast<int64_t>(p.max_blocks) * 16) {
+      if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_LEN);
+      c = p.max_blocks * 16;
+    }
+  }
+  return make_int4(r, p.cu_q[r], q_len, c);
+}
+// This launch's chunk of the request set: its first position, and its requests.
+__device__ __forceinline__ int wn_set(const AttnParams& p, int& n) {
+  int begin = 0;
+  n = p.max_reqs;
+  if (p.bounds != nullptr) {
+    begin = p.bounds[p.cls];
+    n = p.bounds[p.cls + 1] - begin;
+    if (n > p.max_reqs) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_REQS);
+      n = p.max_reqs;
+    }
+    n = max(n, 0);
+  }
+  n = max(0, min(n - p.set_offset, kAttnSetChunk));
+  return begin + p.set_offset;
 }
 
 // Counters of claimed items and of finished CTAs, in the launch's slot (launch.h); its last CTA to finish sets
@@ -250,14 +321,57 @@ __device__ __forceinline__ void wn_zero_row(uint32_t tile, int R) {
   for (int c = 0; c < HALVES * 8; ++c) st_shared_v4(tile + (c / 8) * 16384u + R * 128 + (c % 8) * 16, make_uint4(0, 0, 0, 0));
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
+// One warp: an eighth of pool block b, chunk x of request q: four tokens' rows of K (part 0 .. 3) or of V, a cached block's
+// codes or new tokens, 16 bytes a lane at a time.
+__device__ __forceinline__ void wn_fill(const AttnParams& p, int b, int x, int part, const int4& q, int lane) {
+  const WnPooled w(p, q.w);
+  const int cached = w.cb - w.gap, row = p.Hkv * 128, t0 = 4 * (part & 3);  // (row: elements of a token)
+  const bool of_v = part >= 4;
+  uint4* const out =
+      reinterpret_cast<uint4*>(static_cast<__half*>(of_v ? p.pool_v : p.pool_k) + (static_cast<int64_t>(b) * 16 + t0) * row);
+  if (x < cached) {
+    int src = p.block_tables[static_cast<int64_t>(q.x) * p.max_blocks + (x < w.hb ? x : x + w.gap)];
+    if (src < 0 || src >= p.num_blocks) {
+      if (lane == 0) flag_error(p.err, PKV_DEVERR_BLOCK);
+      src = 0;
+    }
+    const uint4* const in = reinterpret_cast<const uint4*>((of_v ? p.v_codes : p.k_codes) + src * p.stride_block + t0 * row);
+#pragma unroll 4
+    for (int e = lane; e < row / 4; e += 32) {  // (a power of two heads or not, each takes 32 pieces)
+      const uint4 c = in[e];
+      out[2 * e] = make_uint4(e4m3x2_to_f16x2(static_cast<uint16_t>(c.x)), e4m3x2_to_f16x2(static_cast<uint16_t>(c.x >> 16)),
+                              e4m3x2_to_f16x2(static_cast<uint16_t>(c.y)), e4m3x2_to_f16x2(static_cast<uint16_t>(c.y >> 16)));
+      out[2 * e + 1] = make_uint4(e4m3x2_to_f16x2(static_cast<uint16_t>(c.z)), e4m3x2_to_f16x2(static_cast<uint16_t>(c.z >> 16)),
+                                  e4m3x2_to_f16x2(static_cast<uint16_t>(c.w)), e4m3x2_to_f16x2(static_cast<uint16_t>(c.w >> 16)));
+    }
+    return;
+  }
+  // (rows behind the request's last stay as they were: no row sees them)
+  const int tok = 16 * (x - cached) + t0;
+  const int64_t first = static_cast<int64_t>(q.y) + tok;
+  const int tokens = static_cast<int>(max(min(static_cast<int64_t>(min(4, q.z - tok)), p.num_tokens - first), int64_t(0)));
+  const uint4* const in = reinterpret_cast<const uint4*>((of_v ? p.v_new : p.k_new) + first * row);
+  const float f = of_v ? 1.f / p.ctx_v_scale : 1.f;
+#pragma unroll 4
+  for (int e = lane; e < tokens * (row / 8); e += 32) {
+    const uint4 v = in[e];
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t y[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = pack_f16(__uint_as_float(u[c] << 16) * f, __uint_as_float(u[c] & 0xFFFF0000u) * f);
+    out[e] = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(WnCfg<D, KIND>::THREADS, 1)
     attn_window_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kt,
                        const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ CUtensorMap tm_ck,
                        const __grid_constant__ CUtensorMap tm_cv) {
-  static_assert(!FP8 || D == 128, "a code row is one 128-byte box");
-  using C = WnCfg<D, FP8>;
+  using C = WnCfg<D, KIND>;
+  constexpr bool FP8 = C::FP8, F16 = C::F16, POOL = KIND == kWnPool;
+  static_assert(!F16 || D == 128, "a code row is one 128-byte box");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;                  // [slot][half][128][128 B]
@@ -271,24 +385,16 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_scan[C::MAXR / 32];
+  // (kWnCodes: the requests of the pool, in memory that the epilogues use later)
+  int4* const fill_req = reinterpret_cast<int4*>(smem + C::STAGE_OFF);
+  int2* const fill_at = reinterpret_cast<int2*>(fill_req + C::MAXR);
 
   pdl_wait();
   pdl_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  // this launch's chunk of the request set
-  int begin = 0, n = p.max_reqs;
-  if (p.bounds != nullptr) {
-    begin = p.bounds[p.cls];
-    n = p.bounds[p.cls + 1] - begin;
-    if (n > p.max_reqs) {
-      if (blockIdx.x == 0 && tid == 0) flag_error(p.err, PKV_DEVERR_REQS);
-      n = p.max_reqs;
-    }
-    n = max(n, 0);
-  }
-  begin += p.set_offset;
-  n = max(0, min(n - p.set_offset, C::MAXR));
+  int n;
+  const int begin = wn_set(p, n);
 
   if (tid == 0) {
     mbar_init(&bar.q_full, 1);
@@ -311,7 +417,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
       mbar_init(&bar.item_full[i], 1);
       mbar_init(&bar.item_empty[i], C::ITEM_READERS);
     }
-    if (FP8) mbar_init(&bar.q_ready, C::NCONV);
+    if (F16) mbar_init(&bar.q_ready, POOL ? 8 : C::NCONV);
     mbar_init(&bar.o_both, 1);
     mbar_init(&bar.drained, 1);
     s_abort = 0;
@@ -320,26 +426,37 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
   if (warp == C::W_MMA) tc::tmem_alloc(&s_tmem, 512);
 
   // the set's requests
-  if (tid < n) {
-    const int i = tid;
-    const int r = p.order ? p.order[begin + i] : begin + i;
-    int4 q = make_int4(0, 0, 0, 0);
-    if (r >= 0 && r < p.batch_reqs) {
-      const int q_len = max(0, p.cu_q[r + 1] - p.cu_q[r]);
-      int c = 0;
-      if (p.seq_lens != nullptr) {
-        c = max(0, p.seq_lens[r] - q_len);
-        if (c > static_cast<int64_t>(p.max_blocks) * 16) {
-          if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_LEN);
-          c = p.max_blocks * 16;
-        }
+  if (F16 && p.pool_blocks > 0) {
+    // those of the pool for kWnPool, the others for kWnCodes
+    const int4 q = tid < n ? wn_request(p, begin, tid) : make_int4(0, 0, 0, 0);
+    if (tid < n) s_perm[tid] = wn_pool_need(p, q);
+    __syncthreads();
+    if (tid < n) {
+      const int base = wn_pool_base(p, s_perm, tid);
+      s_req[tid] = make_int4(POOL ? base : q.x, q.y, (base >= 0) == POOL ? q.z : 0, q.w);
+      s_start[tid] = wn_cost(p, q);
+      if constexpr (FP8) {
+        fill_req[tid] = q;
+        fill_at[tid] = make_int2(base, base >= 0 ? s_perm[tid] : 0);
       }
-      q = make_int4(r, p.cu_q[r], q_len, c);
-    } else if (blockIdx.x == 0) {
-      flag_error(p.err, PKV_DEVERR_REQS);
     }
-    s_req[i] = q;
-    s_start[i] = wn_cost(p, q);
+    if constexpr (FP8) {
+      // the pool's blocks, dealt over the CTAs, before the items that stay with the codes
+      __syncthreads();
+      for (int i = 0; i < n; ++i) {
+        const int2 at = fill_at[i];
+        if (at.y == 0) continue;
+        // eighths of blocks to warps, the next request's from where this one's end
+        const int warps = static_cast<int>(gridDim.x) * (C::THREADS / 32), me = static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * warp;
+        const int first = static_cast<int>(static_cast<int64_t>(at.x) * 8 % warps);
+        for (int e = me >= first ? me - first : me - first + warps; e < 8 * at.y; e += warps)
+          wn_fill(p, at.x + (e >> 3), e >> 3, e & 7, fill_req[i], lane);
+      }
+    }
+  } else if (tid < n) {
+    const int4 q = wn_request(p, begin, tid);
+    s_req[tid] = q;
+    s_start[tid] = wn_cost(p, q);
   }
   static_assert(C::MAXR <= C::THREADS, "a thread a request");
   __syncthreads();
@@ -378,7 +495,11 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
-  const int W = s_start[C::MAXR];
+  // When the last of few rounds of items would leave half the CTAs idle, its items are halved, into those of 128 rows that deal
+  // their key tiles to both slots: 256 tokens of 64 and 8 heads under 4096 97 us without, 68 with; 2048 tokens 356 and 315.
+  const int all = s_start[C::MAXR], rest = all % static_cast<int>(gridDim.x);
+  const bool few = all <= 4 * static_cast<int>(gridDim.x);
+  const int halved = few && 2 * rest <= static_cast<int>(gridDim.x) ? rest : 0, W = all + halved;
 
   // The k-th item (null: no more, or a wait gave up). A reader frees it when it is through.
   auto take = [&](uint32_t k) -> const WnItem* {
@@ -399,6 +520,18 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
     const uint32_t lane_at = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int shift = __ffs(p.G) - 1;  // G is a power of two
     uint32_t sc = 0, oc = 0, bc = 0, rc = 0;  // phases: S of this slot, o_final, o_both, rows
+    // kWnPool: the k-th item's Q to fp16, before the epilogue of the item before, so that its first S runs beside that
+    auto convert_q = [&](uint32_t k) {
+      const WnItem* taken = take(k);
+      if (taken == nullptr) return;
+      const bool split = taken->split;
+      if (!wn_wait(&bar.q_full, k & 1, &s_abort, p.err)) return;
+      if (slot == 0 || !split) wn_conv_row(smem_u32(sQ) + slot * C::Q_BYTES, t, 1.f);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.q_ready);
+    };
+    if constexpr (POOL) convert_q(0);
     for (uint32_t k = 0;; ++k) {
       const WnItem* taken = take(k);
       if (taken == nullptr) break;
@@ -415,11 +548,11 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
         tc::fence_after_sync();
         if (live) {
           const uint32_t srow = lane_at + wn_scol(slot);
-          // FP8: a score of a cached key counts in the key scale's units. A tile of both kinds is brought to those of
+          // Over codes a score of a cached key counts in the key scale's units. A tile of both kinds is brought to those of
           // the new keys.
-          const int nc = FP8 ? 128 * j < 16 * it.cached() ? 16 * it.cached() - 128 * j : 0 : 0;  // its cached columns
-          const bool both = FP8 && nc > 0 && nc < min(128, 16 * it.NV - 128 * j);
-          const float sl = FP8 && nc > 0 && !both ? p.ctx_scale_log2 : p.scale_log2;
+          const int nc = F16 ? 128 * j < 16 * it.cached() ? 16 * it.cached() - 128 * j : 0 : 0;  // its cached columns
+          const bool both = F16 && nc > 0 && nc < min(128, 16 * it.NV - 128 * j);
+          const float sl = F16 && nc > 0 && !both ? p.ctx_scale_log2 : p.scale_log2;
           if (both || !it.full(j)) {
             // What is hidden becomes -inf in tensor memory, 32 columns at a time (a warp's rows are few tokens: they see
             // most such groups whole). In registers, with the four groups' code in a row, it is fetched anew
@@ -434,7 +567,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
               tc::touch32(x);
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                if (FP8 && both && 32 * c + e < nc) x[e] = __float_as_uint(__uint_as_float(x[e]) * p.ctx_k_scale);
+                if (F16 && both && 32 * c + e < nc) x[e] = __float_as_uint(__uint_as_float(x[e]) * p.ctx_k_scale);
                 x[e] = (seen >> e) & 1u ? x[e] : 0xFF800000u;
               }
               tc::st32(srow + 32 * c, x);
@@ -508,7 +641,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
                 sm::unf2(x, x0, x1);
                 const uint64_t pp = sm::f2(ex2_approx(x0), ex2_approx(x1));
                 rs2 = sm::add2(rs2, pp);
-                pk[16 * c + e / 2] = FP8 ? sm::f16x2(pp) : sm::bf16x2(pp);
+                pk[16 * c + e / 2] = F16 ? sm::f16x2(pp) : sm::bf16x2(pp);
               }
             tc::st32(srow + 32 * h, pk);
             tc::wait_st();
@@ -525,6 +658,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
         }
       }
       if (!ok) break;
+      if constexpr (POOL) convert_q(k + 1);
       // ---- epilogue ----
       const int64_t row = static_cast<int64_t>(it.row0) + tok;
       const bool write = tok < it.tok0 + it.ntok && row < p.num_tokens;
@@ -572,7 +706,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
         ++oc;
         tc::fence_after_sync();
         if (live) {
-          const float inv = l == 0.f ? 0.f : (FP8 ? p.ctx_v_scale : 1.f) / l;
+          const float inv = l == 0.f ? 0.f : (F16 ? p.ctx_v_scale : 1.f) / l;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {  // (unrolled, its code is fetched anew for every item: 3500 clocks)
             uint32_t o[32];
@@ -600,7 +734,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
         const float2 a = mrg[t], b = mrg[128 + t];
         const float mm = fmaxf(a.x, b.x);
         const float w0 = a.y == 0.f ? 0.f : ex2_approx(a.x - mm), w1 = b.y == 0.f ? 0.f : ex2_approx(b.x - mm);
-        const float sum = a.y * w0 + b.y * w1, inv = sum == 0.f ? 0.f : (FP8 ? p.ctx_v_scale : 1.f) / sum;
+        const float sum = a.y * w0 + b.y * w1, inv = sum == 0.f ? 0.f : (F16 ? p.ctx_v_scale : 1.f) / sum;
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           const int col = slot * (D / 2) + c * 32;
@@ -634,6 +768,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
       const int v = C::CHUNKS * j + lane;
       if (lane < C::CHUNKS && v < it.NV) {
         const int u = it.chunk(v);
+        if (POOL) return ~(16 * (it.r + WnPooled(p, it.C).at(u)));
         paged = u < it.cb;
         at = paged ? p.block_tables[static_cast<int64_t>(it.r) * p.max_blocks + u] : ~(it.row0 + 16 * (u - it.cb));
       }
@@ -697,27 +832,28 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_kt);
-        if (p.seq_lens != nullptr) tma_prefetch_desc(&tm_ck);
+        if (!POOL && p.seq_lens != nullptr) tma_prefetch_desc(&tm_ck);
       }
       uint32_t kc = 0, qn = 0;
       bool ok = true;
       int odd = 0;
+      int w = blockIdx.x;
       // item w of the launch (NV 0: there is none)
       WnItem it;
-      auto make = [&](int w) {
+      auto make = [&]() {
         it.NV = 0;
         if (w >= W) return;
-        int lo = 0, hi = n - 1;  // the last rank whose prefix is at most w
+        const int x = w < all ? w : w - halved;
+        int lo = 0, hi = n - 1;  // the last rank whose prefix is at most x
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (s_start[mid] <= w) lo = mid; else hi = mid - 1;
+          if (s_start[mid] <= x) lo = mid; else hi = mid - 1;
         }
-        it = wn_item(p, s_req[s_perm[lo]], w - s_start[lo]);
+        it = wn_item(p, s_req[s_perm[lo]], x - s_start[lo], x < all - halved ? -1 : w >= all);
       };
       // A CTA begins with the item of its own number; the next one is claimed as soon as an item begins and looked
       // up before its last tile, so that neither round trip to memory holds the loads up.
-      int w = blockIdx.x;
-      make(w);
+      make();
       int next = look_up(it, 0);
       for (uint32_t k = 0; ok; ++k) {
         const uint32_t e = k % C::ITEM_RING;
@@ -741,7 +877,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
           auto peek = [&]() {
             if (j + 1 == nt) {
               w = __shfl_sync(0xffffffffu, claimed, 0);
-              make(w);
+              make();
             }
             next = look_up(it, j + 1 < nt ? j + 1 : 0);
           };
@@ -773,7 +909,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
       if (lane == 0) {
         tma_prefetch_desc(&tm_v);
         tma_prefetch_desc(&tm_vt);
-        if (p.seq_lens != nullptr) tma_prefetch_desc(&tm_cv);
+        if (!POOL && p.seq_lens != nullptr) tma_prefetch_desc(&tm_cv);
       }
       uint32_t vc = 0;
       bool ok = true;
@@ -799,8 +935,8 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
     } else if (warp == C::W_MMA) {
       // ======================= MMA issuer =======================
       if (tc::elect()) {
-        constexpr uint32_t kQk = FP8 ? tc::idesc_f16(128, 0, 0, 0) : tc::idesc_bf16(128, 0, 0, 0),
-                           kPv = FP8 ? tc::idesc_f16(128, D, 0, 1) : tc::idesc_bf16(128, D, 0, 1);
+        constexpr uint32_t kQk = F16 ? tc::idesc_f16(128, 0, 0, 0) : tc::idesc_bf16(128, 0, 0, 0),
+                           kPv = F16 ? tc::idesc_f16(128, D, 0, 1) : tc::idesc_bf16(128, D, 0, 1);
         uint64_t* const k_in = FP8 ? bar.k_ready : bar.k_full;  // K that products may read
         // Shared-memory descriptors (tc::smem_desc) as their low words: the address in 16 bytes and the leading
         // offset; the high word is the same for all.
@@ -857,7 +993,7 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
           if (NV == 0) break;
           const int nt = (NV + C::CHUNKS - 1) / C::CHUNKS;
           auto chunks = [&](int j) { return min(C::CHUNKS, NV - C::CHUNKS * j); };
-          if (!wait(FP8 ? &bar.q_ready : &bar.q_full, k & 1)) { ok = false; break; }
+          if (!wait(F16 ? &bar.q_ready : &bar.q_full, k & 1)) { ok = false; break; }
           if (!split) {
             // P V of tile t - 1 and S of tile t, slot by slot (one place in the code for each, so that it stays in
             // the instruction cache beside the other roles'). K and V are looked for while products run that were issued
@@ -1026,27 +1162,53 @@ __global__ void __launch_bounds__(WnCfg<D, FP8>::THREADS, 1)
   }
 }
 
-template <int D, bool FP8>
+template <int D, int KIND>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv,
                    cudaStream_t stream) {
-  constexpr int kSlot = FP8 ? kAttrWinAttn128Fp8 : D == 64 ? kAttrWinAttn64 : kAttrWinAttn128;
+  constexpr int kSlot = KIND == kWnCodes  ? kAttrWinAttn128Fp8
+                        : KIND == kWnPool ? kAttrWinAttn128Pool
+                        : D == 64         ? kAttrWinAttn64
+                                          : kAttrWinAttn128;
   const cudaError_t e =
-      set_smem_attr_once(reinterpret_cast<const void*>(&attn_window_kernel<D, FP8>), wn_smem<D, FP8>(), kSlot);
+      set_smem_attr_once(reinterpret_cast<const void*>(&attn_window_kernel<D, KIND>), wn_smem<D, KIND>(), kSlot);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_window_kernel<D, FP8>, dim3(num_sms()), dim3(WnCfg<D, FP8>::THREADS), wn_smem<D, FP8>(), stream, p, tq,
+  return launch_pdl(attn_window_kernel<D, KIND>, dim3(num_sms()), dim3(WnCfg<D, KIND>::THREADS), wn_smem<D, KIND>(), stream, p, tq,
                     tk, tv, tkt, tvt, tck, tcv);
 }
 
 }  // namespace
 
+// Converting ahead costs a launch (9 us on a GB300), 0.11 ns a key and KV head and, in items of few tiles, their first and last
+// tiles, which overlap less; it saves 5.5 ns a key tile of an item. Without and with it, us, 64 query and 8 KV heads: 2048
+// tokens under 4096 315 and 230, 512 97 and 77, 128 63 and 56; 8 x 512 under 128 86 and 103, 512 137 and 145, 1024 200 and
+// 190; 8 x 256 under 1024 116 and 117, 2048 187 and 170; 8 x 128 under 1024 66 and 77, 4096 185 and 177; 4 x 1024 of 8 and 8
+// heads under 1024 46 and 62; 8 x 512 of 16 and 1 69 and 64.
+int64_t attn_window_pool_blocks(int64_t num_tokens, int32_t max_reqs, int32_t max_q_len, int32_t max_seq_len, int Hq, int Hkv,
+                                int32_t window, int32_t sinks) {
+  const int G = Hq / Hkv;
+  if (static_cast<int64_t>(max_q_len) * G < kPoolRows) return 0;
+  const int64_t reqs = std::min<int64_t>(std::min<int64_t>(max_reqs, kAttnSetChunk), num_tokens * G / kPoolRows);
+  const int64_t keys = std::min<int64_t>(max_seq_len, static_cast<int64_t>(window) + sinks);
+  const int64_t items = num_tokens * Hq / 256, tiles = (keys + 256 / G) / 128;
+  if (items * (tiles - 3) < 1640 + (reqs * keys + num_tokens) * Hkv / 50) return 0;
+  const int64_t all = (static_cast<int64_t>(max_seq_len) + 15) / 16;
+  const int64_t seen = (static_cast<int64_t>(sinks) + 15) / 16 + (static_cast<int64_t>(window) + 15) / 16 + 1;
+  return reqs * (std::min(all, seen) + 1) + num_tokens / 16;
+}
+
 cudaError_t launch_attn_window(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, int D,
-                               bool fp8, cudaStream_t stream, int* launches) {
+                               const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv,
+                               const CUtensorMap* pool, int D, bool fp8, cudaStream_t stream, int* launches) {
   *launches += 1;
-  if (fp8) return launch<128, true>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream);
-  return D == 64 ? launch<64, false>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream)
-                 : launch<128, false>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream);
+  if (fp8) {
+    if (p.pool_blocks > 0) *launches += 1;
+    const cudaError_t e = launch<128, kWnCodes>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream);
+    if (e != cudaSuccess || p.pool_blocks == 0) return e;
+    return launch<128, kWnPool>(p, tq, pool[0], pool[1], pool[2], pool[3], tck, tcv, stream);
+  }
+  return D == 64 ? launch<64, kWnBf16>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream)
+                 : launch<128, kWnBf16>(p, tq, tk, tv, tkt, tvt, tck, tcv, stream);
 }
 
 }  // namespace pkv

@@ -90,6 +90,16 @@ struct AttnParams {
   const float* v_scales;
   int32_t sched_slot;    // this launch's work-item counter slot (< kAttnSchedSlots); -1: none
   int32_t window, sinks;  // windowed attention: see DecodeParams (window 0: every key up to the row's own)
+  // windowed extend over codes: a pool of fp16 rows [pool_blocks][16][Hkv][D] of K and of V (0 blocks: none), and
+  // what it is filled from
+  void* pool_k;
+  void* pool_v;
+  int32_t pool_blocks;
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  int64_t stride_block;  // bytes between consecutive cache blocks
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
 };
 
 // Extend over an FP8 cache: the set's context blocks gathered into a bf16 pool (exact E4M3
@@ -212,6 +222,7 @@ enum AttrSlot {
   kAttrWinAttn64,
   kAttrWinAttn128,
   kAttrWinAttn128Fp8,
+  kAttrWinAttn128Pool,
   kAttrCount
 };
 
@@ -273,10 +284,13 @@ cudaError_t launch_attn_scaled(const AttnParams& p, const CUtensorMap& tq, const
                                const CUtensorMap& tck, const CUtensorMap& tcv, void* workspace, cudaStream_t stream, int* launches);
 // Windowed extend and prefill (p.window >= 1): tm_q as for launch_attn_scaled, tm_k and tm_v over the packed
 // new keys and values as (64, D/64 * Hkv, T, 1) in boxes of 16 rows, tkt and tvt as for launch_attention. fp8: the cache
-// holds E4M3 codes (head_dim 128).
+// holds E4M3 codes (head_dim 128); pool: maps over p.pool_k and p.pool_v like tm_k, tm_v, tkt and tvt, when p has one.
 cudaError_t launch_attn_window(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv, int D, bool fp8,
-                               cudaStream_t stream, int* launches);
+                               const CUtensorMap& tkt, const CUtensorMap& tvt, const CUtensorMap& tck, const CUtensorMap& tcv,
+                               const CUtensorMap* pool, int D, bool fp8, cudaStream_t stream, int* launches);
+// Blocks of a pool that holds what a windowed extend over codes converts ahead (0: nothing).
+int64_t attn_window_pool_blocks(int64_t num_tokens, int32_t max_reqs, int32_t max_q_len, int32_t max_seq_len, int Hq, int Hkv,
+                                int32_t window, int32_t sinks);
 size_t attn_scaled_workspace(int32_t max_q_len, int32_t max_seq_len, int G);
 
 }  // namespace pkv

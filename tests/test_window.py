@@ -203,7 +203,7 @@ def test_refusals():
 
     def extend(window, sinks, cache=c, Hq=4):
         return lib.pkv_window_extend_attn(fake, fake, fake, 8, fake, fake, cache, fake, 4, reqs, Hq, 8, 64, window, sinks, 1.0, fake,
-                                          None, None)
+                                          None, None, 0, None)
 
     def prefill(window, sinks, D=128, Hq=4):
         return lib.pkv_window_prefill_attn(fake, fake, fake, 8, fake, reqs, Hq, 2, D, 8, window, sinks, 1.0, fake, None, None)
@@ -291,6 +291,44 @@ MIXES = {
 def test_extend(mix, kind, D, Hq, Hkv, window, sinks):
     st = make(MIXES[mix], Hq, Hkv, D, kind, window, sinks, 11)
     check(call(st, "extend"), reference(st), st["T"])
+
+
+def extend_with(st, workspace, nbytes):
+    """A windowed extend over codes through the C call, with that much of a workspace."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    from paged_kv_attention_reshape_gb300 import binding
+    g = on_gpu(st)
+    out, lse = torch.full_like(g["q"], 7.0), torch.full(g["q"].shape[:2], 7.0, device="cuda")
+    p, R = (lambda t: t.data_ptr()), len(st["reqs"])
+    cache = binding.make_cache(g["kc"], g["vc"], st["ks"], st["vs"])
+    rc = pkv.load().pkv_window_extend_attn(
+        p(g["q"]), p(g["k_new"]), p(g["v_new"]), g["q"].shape[0], p(g["cu"]), p(g["lens"]), cache, p(g["table"]), g["table"].shape[1],
+        pkv.Reqs(R, R).c(), st["Hq"], max(n for _, n in st["reqs"]), int(st["lens"].max()), st["window"], st["sinks"],
+        1.0 / math.sqrt(st["D"]), p(out), p(lse), workspace.data_ptr() if workspace is not None else None, nbytes,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and pkv.device_errors() == 0
+    return out.cpu(), lse.cpu()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [(1800, 0), (1750, 130), (2000, 1000), (1700, 40), (100000, 0), (1, 2400)])
+@pytest.mark.parametrize("Hq,Hkv,reqs", [(32, 2, [(0, 64), (100, 63), (33, 730), (2500, 1), (2016, 300), (0, 0), (1700, 80), (5, 600)]),
+                                         (32, 4, [(2311, 1999)]), (48, 3, [(1000, 700), (31, 3), (0, 127), (2400, 600)])])
+def test_extend_converted_ahead(Hq, Hkv, reqs, window, sinks):
+    """Requests of many new tokens from rows that were converted once, the others beside them: with room for all of them, for a
+    part and for none, whatever the workspace held."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    st = make(reqs, Hq, Hkv, 128, "tensor", window, sinks, 17)
+    need = pkv.window_extend_workspace_size(st["q"].shape[0], len(reqs), max(n for _, n in reqs), int(st["lens"].max()), Hq, Hkv, 128,
+                                            window, sinks)
+    assert need > 0 and need % (2 * 16 * Hkv * 128 * 2) == 0
+    ref = reference(st)
+    check(extend_with(st, None, 0), ref, st["T"])
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for n in (need, need // 2, 5):
+        ws.fill_(0xFF)  # NaN
+        check(extend_with(st, ws, min(n, need)), ref, st["T"])
+    check(call(st, "extend"), ref, st["T"])
 
 
 @pytest.mark.gpu
