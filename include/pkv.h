@@ -14,7 +14,7 @@
  *     comment says "host". The library allocates no device memory and keeps no state
  *     between calls other than one per-device error word (pkv_device_errors), the handoff
  *     handles the caller creates (pkv_handoff_create) and, per device, work-item counter slots
- *     of the extend/prefill kernel and of the extend kernel of block-scaled caches. A launch
+ *     of the extend/prefill kernel and of those of block-scaled caches and of windows. A launch
  *     issued directly takes the next of 4096 slots and leaves it at zero; it shares its slot only
  *     with the launch 4096 extend/prefill launches later, so at most 4095 other such launches
  *     may be in flight at once on one device. A launch captured into a graph takes a slot that

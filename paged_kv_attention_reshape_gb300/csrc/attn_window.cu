@@ -5,8 +5,8 @@
 // Mathematics: with s_j = log2(e) scale (q . k_j) over the keys that a row sees and m any number of their size,
 // P_j = 2^(s_j - m):  O = sum P_j v_j,  l = sum P_j,  out = O / l,  lse = (m + log2 l) ln 2. m is the max of the
 // scores when the row first meets one, and follows them only when they pass it by more than LAZY: P and O
-// keep the precision of their types whatever the power of two in front, P <= 2^20 leaves values up to 2^100
-// room, and O is rescaled in nearly no tile.
+// keep the precision of their types whatever the power of two in front, P <= 2^20 (fp16: 2^15) leaves values up to
+// 2^100 room, and O is rescaled in nearly no tile.
 //
 // Work items. The rows of a request for one KV head are its (token, query head of the group) pairs, tokens
 // outermost (a box of Q is G heads x 128 / G tokens), and an item is 256 of them: two tiles of 128, one a
@@ -22,18 +22,31 @@
 // zeroed (P = 0 there must not meet what is not finite).
 //
 // A slot's chain is S = Q K^T (520 clocks a tile), softmax, O += P V (520), and the tensor core serves the other slot
-// meanwhile, so a softmax has some 1000 clocks: a whole row in registers, read once, and P handed over in two
-// halves. What the products wait for is issued by single threads (a barrier that is complete costs a warp 110 clocks, and
-// copies issued by eight lanes 1030 a tile instead of 540).
+// meanwhile, so a softmax has some 1000 clocks: a whole row in registers, read once (two threads a row, four warps more: no
+// faster, both warps of a row's quarter share a scheduler), and P handed over in two halves. What the products wait for is issued
+// by single threads (a barrier that is complete costs a warp 110 clocks, and copies issued by eight lanes 1030 a tile instead
+// of 540).
 //
-// Roles (12 warps, one CTA per SM, persistent):
+// Roles (one CTA per SM, persistent; 12 warps, over codes 20):
 //   warps 0-3, 4-7  softmax of slot 0, 1 (thread t owns row t = TMEM lane t) and the epilogue
 //   warp 8          claims the items, loads Q and the ring of K tiles
 //   warp 9          MMA issuer, one elected thread, waits included: S = Q K^T, O += P V (P from tensor memory)
 //   warp 10         loads the ring of V tiles (a K buffer is free before the V buffer of the tile before)
-//   warp 11         zeroes value rows of tiles at an edge
-// Tensor memory (512 columns): S_0 (two buffers) | S_1 (two buffers) | O_0 | O_1; P_s (bf16 pairs) overwrites the
-// first half of its S.
+//   warp 11         zeroes value rows of tiles at an edge (over codes it has nothing to do)
+//   warps 12-15, 16-19  over codes: Q and the K tiles to fp16, the V tiles to fp16
+// Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each (D 64: half of the O columns unused); P_s (16-bit pairs)
+// overwrites the first half of its S. (Key tiles of 64 with two score buffers a slot: three prompts under 4096 1459 us.)
+//
+// What bounds it, on a GB300 with 64 query and 8 KV heads of 128 (times of back-to-back calls; the measured peaks are 6776 GB/s and
+// 1882 TFLOP/s bf16):
+//   three prompts of 4000 to 10,007 tokens under 4096   1305 us, 1530 TFLOP/s (0.81 of measured; 1203 us alone and cool): the
+//                                                       two slots' chains, and the power limit
+//   8 x 301-512 tokens over 4000-32,000 under 128       49 us for a floor of 18.5: two edge tiles an item, so each item is
+//                                                       its chain of Q, S, masks, softmax, P V, epilogue, some 12,000 clocks
+//   32 x 4 tokens over 1000-4000 under 1024             37 us, 3.7 TB/s (floor 20.6): 256 items in two rounds of 152
+//   2048 tokens over 100,000 under 4096, E4M3 cache     230-240 us (floor 151; a bf16 cache 214): of it 8 to 10 for the rows
+//                                                       converted ahead; with the codes converted by every item 315 to 329,
+//                                                       the conversions waiting for shared memory that the products read
 #include <math_constants.h>
 
 #include <algorithm>
@@ -68,10 +81,10 @@ struct WnCfg {
   static constexpr int W_K = 8, W_MMA = 9, W_V = 10, W_FIX = 11;
   static constexpr int W_CONV = 12, NCONV = FP8 ? 4 : 0;  // converter warps of Q and K, and as many of V
   static constexpr int THREADS = FP8 ? 640 : 384;
-  // launched at 168 registers a thread (FP8: 96); the softmax warps take some of the others'
+  // launched at 168 registers a thread (kWnCodes: 96); the softmax warps take some of the others'
   static constexpr int REGS_LAUNCH = FP8 ? 96 : 168, REGS_SOFTMAX = FP8 ? 144 : 208, REGS_OTHER = FP8 ? 64 : 80;
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "register split");
-  // How far (in powers of two) scores may pass a row's m before it follows them: far in bf16; P <= 2^15 in fp16.
+  // How far (in powers of two) scores may pass a row's m before it follows them: far in bf16; in fp16 P stays below 2^16.
   static constexpr float LAZY = F16 ? 15.f : 20.f;
   static constexpr int ITEM_RING = 4;                     // claimed items published to the other roles
   static constexpr int ITEM_READERS = 8 + 2 + (FP8 ? 2 * NCONV : 1);
@@ -88,7 +101,7 @@ struct WnCfg {
 struct WnBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t k_ready[4], v_ready[4], q_ready;  // converted (K and Q: FP8 only); value rows that no row sees zeroed
+  uint64_t k_ready[4], v_ready[4], q_ready;  // converted (K: kWnCodes only, Q: fp16 only); value rows that no row sees zeroed
   uint64_t s_full[2], o_final[2];
   uint64_t p_full[2][2];  // P of the first and of the second 64 columns
   uint64_t o_both;        // both slots' O of a split item
@@ -275,7 +288,7 @@ struct WnRow {
   }
 };
 
-// ---- conversions (FP8) -------------------------------------------------------------------------------
+// ---- conversions -------------------------------------------------------------------------------
 // A K or V tile is [2 halves][128 rows][128 B] (64 16-bit values of a row per half, 128-byte swizzle: 16-byte chunk q of
 // row R at R * 128 + ((q ^ (R & 7)) << 4)). A block's codes land, with the same swizzle, where their rows' second half
 // goes, so a thread converts its own code row in place: dims 0 .. 63 into the first half, then dims 64 .. 127, read
@@ -337,7 +350,7 @@ __device__ __forceinline__ void wn_fill(const AttnParams& p, int b, int x, int p
     }
     const uint4* const in = reinterpret_cast<const uint4*>((of_v ? p.v_codes : p.k_codes) + src * p.stride_block + t0 * row);
 #pragma unroll 4
-    for (int e = lane; e < row / 4; e += 32) {  // (a power of two heads or not, each takes 32 pieces)
+    for (int e = lane; e < row / 4; e += 32) {
       const uint4 c = in[e];
       out[2 * e] = make_uint4(e4m3x2_to_f16x2(static_cast<uint16_t>(c.x)), e4m3x2_to_f16x2(static_cast<uint16_t>(c.x >> 16)),
                               e4m3x2_to_f16x2(static_cast<uint16_t>(c.y)), e4m3x2_to_f16x2(static_cast<uint16_t>(c.y >> 16)));
@@ -574,7 +587,7 @@ __global__ void __launch_bounds__(WnCfg<D, KIND>::THREADS, 1)
             }
             tc::wait_st();
           }
-          // FP8: half a row at a time, the second half read twice, which leaves registers for the converters
+          // kWnCodes: half a row at a time, the second half read twice, which leaves registers for the converters
           constexpr int G = FP8 ? 2 : 4;  // groups of 32 columns held
           uint32_t v[G][32];
           auto load = [&](int c0) {

@@ -13,7 +13,8 @@
 // What bounds it: memory for long batches (each row is read and written once: 5.0 to 6.5 TB/s below),
 // the round trips of slot, row and angle for short ones (2 us for one token, 5.5 us for 256 sequences).
 // 10,000 tokens of 64 query and 8 KV heads of 128: 66 us into a bf16 cache; 84 us into a block-scaled
-// one, where the runs need their rows in registers twice, for the maximum and for the codes.
+// one, where the runs need their rows in registers twice, for the maximum and for the codes; 76 us into a bf16 cache with
+// norms of the heads (0.85 of the measured copy), whose additional work a pair of numbers shares an instruction for.
 #include <algorithm>
 
 #include "common.cuh"
@@ -34,7 +35,8 @@ constexpr int kBlockTokens = 16;  // block size of a block-scaled cache
 // and outputs beyond L2; a prompt's tokens; 64 and 8 heads, 64 and 4, 32 and 8, 8 and 2): 2048 tokens 22.7 and 27.6, 20.6
 // and 22.9, 18.8 and 22.0, 12.8 and 12.7; 2800 30.8 and 32.2, 27.7 and 27.3, 25.4 and 25.6, 16.8 and 15.2; 4096 44.6 and
 // 40.6, 40.5 and 35.7, 36.6 and 32.6, 23.8 and 19.6. (One token a sequence with 64 and 8 heads: 2800 72.8 and 78.6, 4096
-// 106 and 106.)
+// 106 and 106.) With norms, of a bf16 cache: 64 and 8 heads 256 tokens 6.2 and 6.0, 512 11.1 and 8.5, 1024 19.7 and 13.0; 32 and 8
+// 512 8.0 and 8.6, 1024 14.2 and 12.1; 8 and 2 of 64 512 5.0 and 5.1, 1024 10.2 and 7.8.
 constexpr int kManyTokens = 512, kManyTokensBlock = 2900, kManyTokensBlockFewHeads = 2048, kFewHeads = 16;
 
 __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
