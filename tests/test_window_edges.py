@@ -177,6 +177,51 @@ def test_graphs_beside_one_another():
     assert pkv.device_errors() == 0
 
 
+def test_rows_converted_ahead_in_more_requests_than_a_launch_holds():
+    """Long requests in both launches of a set, short ones between them, in a set of its own order; the launches share the pool."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    reqs = [(3500 + i, 300) if i % 50 == 7 else (i % 50, 1 + i % 3) for i in range(300)]
+    st = make(reqs, 32, 2, 128, "tensor", 4000, 30, 95)
+    assert pkv.window_extend_workspace_size(st["q"].shape[0], 300, 300, int(st["lens"].max()), 32, 2, 128, 4000, 30) > 0
+    order = torch.randperm(300, generator=torch.Generator().manual_seed(3)).to(torch.int32).cuda()
+    check(call(st, "extend", reqs=pkv.Reqs(300, 300, order=order)), reference(st), st["T"])
+
+
+def test_rows_converted_ahead_captured_on_two_streams_and_bad_pages():
+    """An extend that converts rows ahead: captured and replayed for other inputs beside a direct call on another stream, the
+    bits of calls alone; and a bad page among those that it converts sets its bit."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    mix = [(2000, 1000), (40, 1000)]
+    a, b = (make(mix, 32, 2, 128, "tensor", 1900, 20, s, pad=0) for s in (96, 97))
+    assert pkv.window_extend_workspace_size(2000, 2, 1000, 3000, 32, 2, 128, 1900, 20) > 0
+    want = [call(x, "extend") for x in (a, b)]
+    g, h = on_gpu(a), on_gpu(b)
+    bufs = [(torch.empty_like(g["q"]), torch.empty(g["q"].shape[:2], device="cuda")) for _ in "gh"]
+
+    def run(x, out, lse, **kw):
+        pkv.extend_attn(x["q"], x["k_new"], x["v_new"], x["cu"], x["lens"], x["kc"], x["vc"], x["table"], 1000, 3000, window=1900,
+                        sinks=20, k_scale=0.02, v_scale=0.03, out=out, lse=lse, **kw)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(g, *bufs[0])
+    side = torch.cuda.Stream()
+    for x, w in ((b, want[1]), (a, want[0])):
+        for k in ("q", "k_new", "v_new", "kc", "vc", "table", "lens", "cu"):
+            g[k].copy_(x[k])
+        torch.cuda.synchronize()
+        for _ in range(5):
+            graph.replay()
+            run(h, *bufs[1], stream=side)
+        torch.cuda.synchronize()
+        for (o, l), y in zip(bufs, (w, want[1])):
+            assert torch.equal(o.cpu(), y[0]) and torch.equal(l.cpu(), y[1])
+    assert pkv.device_errors() == 0
+    h["table"][0, 100] = -9
+    run(h, *bufs[1])
+    assert pkv.device_errors() == 2
+
+
 _MANY = """
 import sys, torch
 sys.path[:0] = ["tests", "."]
