@@ -444,10 +444,12 @@ def _window(window, sinks):
     return min(int(window), 2**31 - 1), min(int(sinks), 2**31 - 1)
 
 
-def _window_args(q, heads, dim, rows, index, out, lse, kv=()):
+def _window_args(q, heads, dim, rows, index, out, lse, kv=(), workspace=None):
     """Checks the tensors of a windowed call: on the current device, of the shapes the kernels read and write.
     index: (tensor, name, least entries); kv: (tensor, name) rows of keys and values [rows, heads, dim]."""
     dev = torch.cuda.current_device()
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise PkvError("the workspace must be contiguous, on the current device")
     if q.get_device() != dev:
         raise PkvError("q must be on the current device")
     if q.shape[2] != dim or not q.is_contiguous():
@@ -491,7 +493,9 @@ def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, 
     workspace = _scratch(need, workspace, q.device, other)
     if win is not None:
         _window_args(q, 0, cache.head_dim, 0, ((block_tables, "block_tables", 0), (seq_lens, "seq_lens", reqs.batch_reqs),
-                                               (cu_q, "cu_q", reqs.batch_reqs + 1)), out, lse)
+                                               (cu_q, "cu_q", reqs.batch_reqs + 1)), out, lse, (), workspace)
+        if cu_q is None and reqs.order is None and q.shape[0] < min(reqs.max_reqs, reqs.batch_reqs):
+            raise PkvError("q must have a row for each request")
         if k_cache.get_device() != q.get_device() or block_tables.dim() != 2 or block_tables.shape[0] < reqs.batch_reqs:
             raise PkvError("the cache must be on q's device, and block_tables [requests, max_blocks]")
         _check(lib.pkv_window_decode_attn(_ptr(q), cache, _ptr(block_tables), block_tables.shape[1],
@@ -591,7 +595,7 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
     if win is not None:
         _window_args(q, cache.num_kv_heads, cache.head_dim, T,
                      ((block_tables, "block_tables", 0), (seq_lens, "seq_lens", reqs.batch_reqs),
-                      (cu_q, "cu_q", reqs.batch_reqs + 1)), out, lse, ((k_new, "k_new"), (v_new, "v_new")))
+                      (cu_q, "cu_q", reqs.batch_reqs + 1)), out, lse, ((k_new, "k_new"), (v_new, "v_new")), workspace)
         if k_cache.get_device() != q.get_device() or block_tables.dim() != 2 or block_tables.shape[0] < reqs.batch_reqs:
             raise PkvError("the cache must be on q's device, and block_tables [requests, max_blocks]")
         need = window_extend_workspace_size(T, reqs.max_reqs, max_q_len, max_seq_len, Hq, cache.num_kv_heads, D, *win,

@@ -194,7 +194,7 @@ struct WnPooled {
 };
 // Blocks of the pool for a request {request id, first query row, q_len, cached tokens}; 0: it is too short.
 __device__ __forceinline__ int wn_pool_need(const AttnParams& p, const int4& q) {
-  if (static_cast<int64_t>(q.z) * p.G < kPoolRows || q.z > p.num_tokens) return 0;
+  if (q.z * p.G < kPoolRows) return 0;
   const WnPooled w(p, q.w);
   return min(w.cb - w.gap + (q.z + 15) / 16, p.pool_blocks + 1);  // (the sum over a launch's requests stays in range)
 }
@@ -213,7 +213,11 @@ __device__ __forceinline__ int4 wn_request(const AttnParams& p, int begin, int i
     if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_REQS);
     return make_int4(0, 0, 0, 0);
   }
-  const int q_len = max(0, p.cu_q[r + 1] - p.cu_q[r]);
+  const int row0 = p.cu_q[r], q_len = max(0, p.cu_q[r + 1] - row0);
+  if (row0 < 0) {
+    if (blockIdx.x == 0) flag_error(p.err, PKV_DEVERR_LEN);
+    return make_int4(0, 0, 0, 0);
+  }
   int c = 0;
   if (p.seq_lens != nullptr) {
     c = max(0, p.seq_lens[r] - q_len);
@@ -222,7 +226,8 @@ __device__ __forceinline__ int4 wn_request(const AttnParams& p, int begin, int i
       c = p.max_blocks * 16;
     }
   }
-  return make_int4(r, p.cu_q[r], q_len, c);
+  // (rows past the last token are never written, and no row before them sees their keys)
+  return make_int4(r, row0, static_cast<int>(min(static_cast<int64_t>(q_len), max(p.num_tokens - row0, int64_t(0)))), c);
 }
 // This launch's chunk of the request set: its first position, and its requests.
 __device__ __forceinline__ int wn_set(const AttnParams& p, int& n) {

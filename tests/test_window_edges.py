@@ -119,6 +119,42 @@ def test_empty_sets_and_a_request_twice():
     assert torch.equal(g["kc"].view(torch.int16), before.view(torch.int16)) and pkv.device_errors() == 0
 
 
+def test_tokens_that_are_not_there():
+    """cu_q that counts more tokens than q has rows: those that it has are as in the whole batch. Offsets below zero: flagged, and
+    nothing written."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    for kind in ("bf16", "tensor"):
+        st = make([(40, 3), (300, 200)], 16, 2, 128, kind, 60, 5, 83, pad=0)
+        ref = reference(st)
+        g = on_gpu(st)
+        kw = dict(window=60, sinks=5, **(dict(k_scale=st["ks"], v_scale=st["vs"]) if kind == "tensor" else {}))
+        for T in (203, 202, 100, 40, 3, 2):
+            out, lse = pkv.extend_attn(g["q"][:T], g["k_new"][:T], g["v_new"][:T], g["cu"], g["lens"], g["kc"], g["vc"], g["table"], 200,
+                                       500, **kw)
+            assert pkv.device_errors() == 0
+            check((out.cpu(), lse.cpu()), [x[:T] for x in ref], T)
+        cu = g["cu"].clone()
+        cu[0] = -5
+        out = torch.full_like(g["q"], 7.0)
+        pkv.extend_attn(g["q"], g["k_new"], g["v_new"], cu, g["lens"], g["kc"], g["vc"], g["table"], 200, 500, out=out, **kw)
+        assert pkv.device_errors() == 8
+        assert torch.all(out[:3] == 7.0) and torch.all((out[3:].double().cpu() - ref[0][3:]).abs() <= ref[2][3:])
+
+
+def test_workspaces_and_rows_that_are_refused():
+    import paged_kv_attention_reshape_gb300 as pkv
+    st = make([(60, 1), (40, 1)], 4, 2, 128, "bf16", 40, 0, 3, cached_all=True, pad=0)
+    g = on_gpu(st)
+    a = (g["kc"], g["vc"], g["table"], g["lens"], 64)
+    need = pkv.paged_decode_workspace_size(2, 4, 2, 128, 64)
+    for q, ws in ((g["q"], torch.empty(need, dtype=torch.uint8)), (g["q"], torch.empty((need, 2), dtype=torch.uint8, device="cuda")[:, 0]),
+                  (g["q"][:1], None)):
+        with pytest.raises(pkv.PkvError):
+            pkv.paged_decode_attn(q, *a, window=9, workspace=ws)
+    with pytest.raises(pkv.PkvError):
+        pkv.extend_attn(g["q"], g["k_new"], g["v_new"], g["cu"], g["lens"], *a[:3], 1, 64, window=9, workspace=torch.empty(5))
+
+
 def test_graphs_beside_one_another():
     """Two captured steps (an append with norms, an extend or a decode, a copy of pages), each with its own tensors, replayed
     on two streams at once beside direct calls on a third: the bits of the steps alone."""
