@@ -180,7 +180,9 @@ __device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, in
 // ---- the pool (kWnPool) --------------------------------------------------------------------------------
 // The pool holds, request after request, the chunks of 16 keys that some row of the request sees: the `hb` blocks of
 // sinks, the cached blocks from the first row's window on, the new tokens. Chunk u of a request lies at its first
-// block + u, less `gap` from hb on. A request belongs to it when it has kPoolRows rows a KV head and the pool has room.
+// block + u, less `gap` from hb on. A request belongs to it when it has kPoolRows rows a KV head and the pool has room (four
+// items read its keys; 128 tokens of 64 and 8 heads under 4096, that many: 63 us without and 56 with, 8 x 64 of 16 and 1 under
+// 1024 26 and 33).
 constexpr int kPoolRows = 1024;
 struct WnPooled {
   int cb, hb, gap;
@@ -514,7 +516,8 @@ __global__ void __launch_bounds__(WnCfg<D, KIND>::THREADS, 1)
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
   // When the last of few rounds of items would leave half the CTAs idle, its items are halved, into those of 128 rows that deal
-  // their key tiles to both slots: 256 tokens of 64 and 8 heads under 4096 97 us without, 68 with; 2048 tokens 356 and 315.
+  // their key tiles to both slots: 256 tokens of 64 and 8 heads under 4096 97 us without, 68 with; 2048 tokens 356 and 315 (with the codes
+  // converted by every item). Of more rounds it gains nothing: 8 x 301-512 tokens, 5.4 rounds, 50 and 50.
   const int all = s_start[C::MAXR], rest = all % static_cast<int>(gridDim.x);
   const bool few = all <= 4 * static_cast<int>(gridDim.x);
   const int halved = few && 2 * rest <= static_cast<int>(gridDim.x) ? rest : 0, W = all + halved;
