@@ -444,26 +444,34 @@ def _window(window, sinks):
     return min(int(window), 2**31 - 1), min(int(sinks), 2**31 - 1)
 
 
-def _window_args(q, heads, dim, rows, index, out, lse, kv=(), workspace=None):
-    """Checks the tensors of a windowed call: on the current device, of the shapes the kernels read and write.
-    index: (tensor, name, least entries); kv: (tensor, name) rows of keys and values [rows, heads, dim]."""
-    dev = torch.cuda.current_device()
+def _window_args(q, heads, dim, rows, reqs, index, out, lse, kv=(), workspace=None):
+    """Checks the tensors of a windowed call: on the current device, as large as what the kernels read and write (q, the
+    lengths, tables and new rows have passed _need). index: (tensor, name, least entries); kv: (tensor, name) rows
+    of keys and values [rows, heads, dim]."""
+    dev = q.get_device()
+    if dev != torch.cuda.current_device():
+        raise PkvError("q must be on the current device")
+    n, hq, d = q.shape
+    n *= hq
+    if d != dim:
+        raise PkvError(f"q must be [T, Hq, {dim}]")
+    if reqs.order is not None or reqs.bounds is not None:
+        index += ((reqs.order, "order", reqs.max_reqs if reqs.bounds is None else 0), (reqs.bounds, "bounds", reqs.cls + 2))
+        for t, name, _ in index[-2:]:
+            if t is not None:
+                _need(t, torch.int32, name)
+    for t, name in kv:
+        if t.get_device() != dev or t.shape != (rows, heads, dim):
+            raise PkvError(f"{name} must be [{rows}, {heads}, {dim}] on the current device")
+    for t, name, least in index:
+        if t is not None and (t.get_device() != dev or t.numel() < least):
+            raise PkvError(f"{name} must have at least {least} entries, on the current device")
+    if out.numel() != n * d or out.dtype is not torch.bfloat16 or out.get_device() != dev or not out.is_contiguous():
+        raise PkvError("out must be contiguous bf16 like q")
+    if lse.numel() != n or lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
+        raise PkvError("lse must be contiguous fp32 [T, Hq]")
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise PkvError("the workspace must be contiguous, on the current device")
-    if q.get_device() != dev:
-        raise PkvError("q must be on the current device")
-    if q.shape[2] != dim or not q.is_contiguous():
-        raise PkvError(f"q must be contiguous [T, Hq, {dim}]")
-    for t, name in kv:
-        if t.get_device() != dev or t.shape != (rows, heads, dim) or not t.is_contiguous():
-            raise PkvError(f"{name} must be contiguous [{rows}, {heads}, {dim}] on the current device")
-    for t, name, least in index:
-        if t is not None and (t.get_device() != dev or t.dtype is not torch.int32 or t.numel() < least or not t.is_contiguous()):
-            raise PkvError(f"{name} must be at least {least} contiguous int32 entries on the current device")
-    if out.shape != q.shape or out.dtype is not torch.bfloat16 or out.get_device() != dev or not out.is_contiguous():
-        raise PkvError("out must be contiguous bf16 like q")
-    if lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
-        raise PkvError("lse must be contiguous fp32 [T, Hq]")
 
 
 def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, cu_q=None,
@@ -492,13 +500,15 @@ def paged_decode_attn(q, k_cache, v_cache, block_tables, seq_lens, max_seq_len, 
     win = _window(window, sinks)
     workspace = _scratch(need, workspace, q.device, other)
     if win is not None:
-        _window_args(q, 0, cache.head_dim, 0, ((block_tables, "block_tables", 0), (seq_lens, "seq_lens", reqs.batch_reqs),
-                                               (cu_q, "cu_q", reqs.batch_reqs + 1)), out, lse, (), workspace)
-        if cu_q is None and reqs.order is None and q.shape[0] < min(reqs.max_reqs, reqs.batch_reqs):
+        batch, width = reqs.batch_reqs, block_tables.shape[1]
+        index = ((block_tables, "block_tables", batch * width), (seq_lens, "seq_lens", batch), (k_cache, "the cache", 0))
+        if cu_q is not None:
+            _need(cu_q, torch.int32, "cu_q")
+            index += ((cu_q, "cu_q", batch + 1),)
+        elif reqs.order is None and T < min(reqs.max_reqs, batch):
             raise PkvError("q must have a row for each request")
-        if k_cache.get_device() != q.get_device() or block_tables.dim() != 2 or block_tables.shape[0] < reqs.batch_reqs:
-            raise PkvError("the cache must be on q's device, and block_tables [requests, max_blocks]")
-        _check(lib.pkv_window_decode_attn(_ptr(q), cache, _ptr(block_tables), block_tables.shape[1],
+        _window_args(q, 0, cache.head_dim, 0, reqs, index, out, lse, (), workspace)
+        _check(lib.pkv_window_decode_attn(_ptr(q), cache, _ptr(block_tables), width,
                                           _ptr(seq_lens), _ptr(cu_q), reqs.c(), Hq, max_seq_len, *win,
                                           _scale(scale, D), _ptr(out), _ptr(lse), _ptr(workspace),
                                           need, _stream(stream)), "paged_decode_attn")
@@ -593,11 +603,10 @@ def extend_attn(q, k_new, v_new, cu_q, seq_lens, k_cache, v_cache, block_tables,
         lse = _empty((T, Hq), torch.float32, q.device, other)
     win = _window(window, sinks)
     if win is not None:
-        _window_args(q, cache.num_kv_heads, cache.head_dim, T,
-                     ((block_tables, "block_tables", 0), (seq_lens, "seq_lens", reqs.batch_reqs),
-                      (cu_q, "cu_q", reqs.batch_reqs + 1)), out, lse, ((k_new, "k_new"), (v_new, "v_new")), workspace)
-        if k_cache.get_device() != q.get_device() or block_tables.dim() != 2 or block_tables.shape[0] < reqs.batch_reqs:
-            raise PkvError("the cache must be on q's device, and block_tables [requests, max_blocks]")
+        batch = reqs.batch_reqs
+        _window_args(q, cache.num_kv_heads, cache.head_dim, T, reqs,
+                     ((block_tables, "block_tables", batch * block_tables.shape[1]), (seq_lens, "seq_lens", batch),
+                      (cu_q, "cu_q", batch + 1), (k_cache, "the cache", 0)), out, lse, ((k_new, "k_new"), (v_new, "v_new")), workspace)
         need = window_extend_workspace_size(T, reqs.max_reqs, max_q_len, max_seq_len, Hq, cache.num_kv_heads, D, *win,
                                             kv_dtype=cache.kv_dtype) if cache.kv_dtype == _lib.KV_FP8_E4M3 else 0
         workspace = _scratch(need, workspace, q.device, other)
@@ -654,7 +663,7 @@ def varlen_prefill_attn(q, k, v, cu_seqlens, max_seqlen, reqs: Optional[Reqs] = 
         lse = _empty((T, Hq), torch.float32, q.device, other)
     win = _window(window, sinks)
     if win is not None:
-        _window_args(q, Hkv, D, T, ((cu_seqlens, "cu_seqlens", reqs.batch_reqs + 1),), out, lse, ((k, "k"), (v, "v")))
+        _window_args(q, Hkv, D, T, reqs, ((cu_seqlens, "cu_seqlens", reqs.batch_reqs + 1),), out, lse, ((k, "k"), (v, "v")))
         _check(lib.pkv_window_prefill_attn(_ptr(q), _ptr(k), _ptr(v), T, _ptr(cu_seqlens), reqs.c(), Hq, Hkv, D,
                                            max_seqlen, *win, _scale(scale, D), _ptr(out), _ptr(lse),
                                            _stream(stream)), "varlen_prefill_attn")

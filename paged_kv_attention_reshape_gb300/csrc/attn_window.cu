@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(WnCfg<D, KIND>::THREADS, 1)
         const int2 at = fill_at[i];
         if (at.y == 0) continue;
         // eighths of blocks to warps, the next request's from where this one's end
-        const int warps = static_cast<int>(gridDim.x) * (C::THREADS / 32), me = static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * warp;
+        const int warps = static_cast<int>(gridDim.x) * (C::THREADS / 32);
+        const int me = static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * warp;
         const int first = static_cast<int>(static_cast<int64_t>(at.x) * 8 % warps);
         for (int e = me >= first ? me - first : me - first + warps; e < 8 * at.y; e += warps)
           wn_fill(p, at.x + (e >> 3), e >> 3, e & 7, fill_req[i], lane);
@@ -516,8 +517,8 @@ __global__ void __launch_bounds__(WnCfg<D, KIND>::THREADS, 1)
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
   // When the last of few rounds of items would leave half the CTAs idle, its items are halved, into those of 128 rows that deal
-  // their key tiles to both slots: 256 tokens of 64 and 8 heads under 4096 97 us without, 68 with; 2048 tokens 356 and 315 (with the codes
-  // converted by every item). Of more rounds it gains nothing: 8 x 301-512 tokens, 5.4 rounds, 50 and 50.
+  // their key tiles to both slots: 256 tokens of 64 and 8 heads under 4096 97 us without, 68 with; 2048 tokens 356 and 315
+  // (with the codes converted by every item). Of more rounds it gains nothing: 8 x 301-512 tokens, 5.4 rounds, 50 and 50.
   const int all = s_start[C::MAXR], rest = all % static_cast<int>(gridDim.x);
   const bool few = all <= 4 * static_cast<int>(gridDim.x);
   const int halved = few && 2 * rest <= static_cast<int>(gridDim.x) ? rest : 0, W = all + halved;

@@ -151,6 +151,13 @@ def test_workspaces_and_rows_that_are_refused():
                   (g["q"][:1], None)):
         with pytest.raises(pkv.PkvError):
             pkv.paged_decode_attn(q, *a, window=9, workspace=ws)
+    order = torch.tensor([1, 0], dtype=torch.int32)
+    for reqs in (pkv.Reqs(2, 2, order=order), pkv.Reqs(2, 2, order=order.cuda().long()), pkv.Reqs(3, 2, order=order.cuda()),
+                 pkv.Reqs(2, 2, order=order.cuda(), bounds=order.cuda(), cls=1)):
+        with pytest.raises(pkv.PkvError):
+            pkv.paged_decode_attn(g["q"], *a, window=9, reqs=reqs)
+        with pytest.raises(pkv.PkvError):
+            pkv.varlen_prefill_attn(g["q"], g["k_new"], g["v_new"], g["cu"], 1, window=9, reqs=reqs)
     with pytest.raises(pkv.PkvError):
         pkv.extend_attn(g["q"], g["k_new"], g["v_new"], g["cu"], g["lens"], *a[:3], 1, 64, window=9, workspace=torch.empty(5))
 
