@@ -44,7 +44,7 @@
 //   8 x 301-512 tokens over 4000-32,000 under 128       49 us for a floor of 18.5: two edge tiles an item, so each item is
 //                                                       its chain of Q, S, masks, softmax, P V, epilogue, some 12,000 clocks
 //   32 x 4 tokens over 1000-4000 under 1024             37 us, 3.7 TB/s (floor 20.6): 256 items in two rounds of 152
-//   2048 tokens over 100,000 under 4096, E4M3 cache     230-240 us (floor 151; a bf16 cache 214): of it 8 to 16 for the rows
+//   2048 tokens over 100,000 under 4096, E4M3 cache     232 us (floor 151; a bf16 cache 214): of it 8 to 16 for the rows
 //                                                       converted ahead; with the codes converted by every item 315 to 329,
 //                                                       the conversions waiting for shared memory that the products read
 #include <math_constants.h>
@@ -900,6 +900,14 @@ __global__ void __launch_bounds__(WnCfg<D, KIND>::THREADS, 1)
             if (j + 1 == nt) {
               w = __shfl_sync(0xffffffffu, claimed, 0);
               make();
+              // kWnPool: its Q is on the way to L2 before the buffer is free, since converting it comes before its first S (236
+              // and 232 us on 2048 tokens under 4096; over bf16 8 x 301-512 tokens take 49.5 and 50.6)
+              if (POOL && it.NV > 0 && tc::elect())
+                for (int s = 0; s < (it.split ? 1 : 2); ++s)
+#pragma unroll
+                  for (int hf = 0; hf < C::HALVES; ++hf)
+                    tma_prefetch_l2_4d(&tm_q, 0, hf, it.kh * p.G, it.row0 + it.tok0 + s * (128 / p.G));
+              __syncwarp();
             }
             next = look_up(it, j + 1 < nt ? j + 1 : 0);
           };
