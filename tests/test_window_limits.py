@@ -1,0 +1,57 @@
+"""Windowed calls at the ends of what their numbers may be: windows and sinks up to 2^31 - 1, beside caches whose last block is
+partly filled. The reference and its tolerances are those of test_window.py."""
+import math
+
+import pytest
+import torch
+
+from test_window import call, check, extend_with, make, on_gpu, reference
+
+MOST = 2 ** 31 - 1
+# cached lengths that end inside a block, and new tokens that cross a group of 32 walk columns
+PARTLY = [(1, 20), (17, 3), (22, 70), (2001, 45), (15, 300), (31, 1), (0, 33), (16, 40)]
+ENDS = [(MOST, 0), (1 << 40, 0), (MOST, 5), (MOST - 7, 0), (MOST - 15, 18), (MOST - 16, 0), (MOST - 40, 0), (MOST, MOST), (9, MOST),
+        (1, 1 << 40)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", ENDS)
+@pytest.mark.parametrize("kind,D,Hq,Hkv", [("bf16", 64, 8, 2), ("bf16", 128, 16, 1), ("bf16", 128, 2, 2), ("tensor", 128, 16, 2)])
+def test_extend_under_the_widest_windows(kind, D, Hq, Hkv, window, sinks):
+    st = make(PARTLY, Hq, Hkv, D, kind, window, sinks, 91)
+    check(call(st, "extend"), reference(st), st["T"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [e for e in ENDS if max(e) <= MOST])
+def test_extend_converted_ahead_under_the_widest_windows(window, sinks):
+    """A request of the rows that were converted once, beside short ones that are read as codes."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    st = make([(2001, 700), (17, 600), (1, 20), (22, 70)], 48, 3, 128, "tensor", window, sinks, 92)
+    need = pkv.window_extend_workspace_size(st["q"].shape[0], 4, 700, int(st["lens"].max()), 48, 3, 128, window, sinks)
+    assert need > 0
+    ref = reference(st)
+    check(extend_with(st, torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda"), need), ref, st["T"])
+    check(extend_with(st, None, 0), ref, st["T"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", ENDS)
+def test_prefill_and_decode_under_the_widest_windows(window, sinks):
+    st = make([(0, n) for n in (1, 17, 300, 45)], 16, 2, 128, "none", window, sinks, 93)
+    check(call(st, "prefill"), reference(st), st["T"])
+    for kind in ("bf16", "tensor", "block"):
+        st = make([(c, 1) for c in (0, 1, 16, 22, 2001)], 16, 2, 128, kind, window, sinks, 94, cached_all=True)
+        check(call(st, "decode"), reference(st, decode=True), st["T"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,D", [("bf16", 64), ("bf16", 128), ("tensor", 128)])
+def test_the_widest_window_is_the_widest_but_one(kind, D):
+    """Windows that no row reaches the end of are alike to the bit, whatever their number."""
+    st = make(PARTLY, 16, 2, D, kind, 100000, 0, 95)
+    want = call(st, "extend")
+    for window in (MOST, MOST - 9, 1 << 40):
+        st["window"] = window
+        got = call(st, "extend")
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
