@@ -6,7 +6,9 @@
 // P_j = 2^(s_j - m):  O = sum P_j v_j,  l = sum P_j,  out = O / l,  lse = (m + log2 l) ln 2. m is the max of the
 // scores when the row first meets one, and follows them only when they pass it by more than LAZY: P and O
 // keep the precision of their types whatever the power of two in front, P <= 2^20 (fp16: 2^15) leaves values up to
-// 2^100 room, and O is rescaled in nearly no tile.
+// 2^100 room, and O is rescaled in nearly no tile. In fp16, whose smallest number is 2^-24, m is RAISE below that max: a row's
+// largest P is 2^8 at least, and terms down to 2^-33 of it count (with 2^-25, what thousands of keys have in common was
+// lost from O, not from l).
 //
 // Work items. The rows of a request for one KV head are its (token, query head of the group) pairs, tokens
 // outermost (a box of Q is G heads x 128 / G tokens), and an item is 256 of them: two tiles of 128, one a
@@ -86,6 +88,8 @@ struct WnCfg {
   static_assert(256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * REGS_LAUNCH, "register split");
   // How far (in powers of two) scores may pass a row's m before it follows them: far in bf16; in fp16 P stays below 2^16.
   static constexpr float LAZY = F16 ? 15.f : 20.f;
+  // and how far below the scores that it follows m is put: fp16 keeps 11 bits of a P from 2^-14 on, and loses one below 2^-25.
+  static constexpr float RAISE = F16 ? 8.f : 0.f;
   static constexpr int ITEM_RING = 4;                     // claimed items published to the other roles
   static constexpr int ITEM_READERS = 8 + 2 + (FP8 ? 2 * NCONV : 1);
   static constexpr int RING_OFF = 2 * Q_BYTES;
@@ -627,8 +631,9 @@ __global__ void __launch_bounds__(WnCfg<D, KIND>::THREADS, 1)
           if (__any_sync(0xffffffffu, mx > m + C::LAZY)) {  // (m may be -inf)
             float alpha = 1.f;
             if (mx > m + C::LAZY) {
-              alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mx);
-              m = mx;
+              const float to = mx - C::RAISE;
+              alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - to);
+              m = to;
             }
             l *= alpha;
             if (j > first) {

@@ -55,3 +55,41 @@ def test_the_widest_window_is_the_widest_but_one(kind, D):
         st["window"] = window
         got = call(st, "extend")
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ahead", [False, True])
+@pytest.mark.parametrize("reqs,Hq,Hkv", [([(2400, 600)], 48, 3), ([(3001, 700), (2990, 5)], 32, 2)])
+def test_small_terms_add_up(reqs, Hq, Hkv, ahead):
+    """Over an 8-bit cache P is fp16, with steps of 2^-24 below 2^-14. One key 2^26 times the others' weight, with value 0, and
+    thousands of others: out is theirs alone. The row's largest P is 2^8 at least, so each p is off by 2^-33 at most from the steps:
+    2^-33 sum |v| in the place of the 2^-25 sum |v| that test_window.py allows."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    st = make(reqs, Hq, Hkv, 128, "tensor", 5000, 0, 96)
+    for n in ("q", "k_new", "v_new"):
+        st[n][:st["T"]] = 0
+    st["q"][:st["T"], :, 0] = 10240.0  # times 0.02 / sqrt(128): 18.1, or 2^26.1
+    st["v_new"][:st["T"]] = 0.03
+    held = st["kc"] != 0x7F  # (NaN: tokens that no row sees)
+    st["kc"][held] = 0x00
+    st["vc"][held] = 0x38  # 1.0
+    for r in range(len(reqs)):
+        page = int(st["table"][r, 0])
+        st["kc"][page, 0, :, 0] = 0x38
+        st["vc"][page, 0] = 0x00
+    if ahead:
+        need = pkv.window_extend_workspace_size(st["q"].shape[0], len(reqs), max(n for _, n in reqs), int(st["lens"].max()), Hq, Hkv,
+                                                128, 5000)
+        assert need > 0
+        got = extend_with(st, torch.empty(need, dtype=torch.uint8, device="cuda"), need)
+    else:
+        got = extend_with(st, None, 0)
+    o, z, tol, ltol = reference(st)
+    row = 0
+    code, new = float(torch.tensor(st["vs"])), float(st["v_new"][0, 0, 0])
+    for c, n in reqs:
+        sumv = (c - 1) * code + new * torch.arange(1, n + 1, dtype=torch.float64)[:, None, None]
+        tol[row:row + n] -= (2.0 ** -25 - 2.0 ** -33) * sumv
+        row += n
+    assert (tol[:st["T"]] > 0).all() and (tol < 0.05 * o)[:st["T"]].all()
+    check(got, (o, z, tol, ltol), st["T"])
