@@ -36,7 +36,7 @@ constexpr int kBlockTokens = 16;  // block size of a block-scaled cache
 // and 22.9, 18.8 and 22.0, 12.8 and 12.7; 2800 30.8 and 32.2, 27.7 and 27.3, 25.4 and 25.6, 16.8 and 15.2; 4096 44.6 and
 // 40.6, 40.5 and 35.7, 36.6 and 32.6, 23.8 and 19.6. (One token a sequence with 64 and 8 heads: 2800 72.8 and 78.6, 4096
 // 106 and 106.) With norms, of a bf16 cache: 64 and 8 heads 256 tokens 6.2 and 6.0, 512 11.1 and 8.5, 1024 19.7 and 13.0; 32 and 8
-// 512 8.0 and 8.6, 1024 14.2 and 12.1; 8 and 2 of 64 512 5.0 and 5.1, 1024 10.2 and 7.8.
+// 512 8.0 and 6.5, 1024 14.2 and 9.8; 8 and 2 of 64 512 5.0 and 3.7, 1024 10.2 and 6.1.
 constexpr int kManyTokens = 512, kManyTokensBlock = 2900, kManyTokensBlockFewHeads = 2048, kFewHeads = 16;
 
 __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
@@ -463,8 +463,12 @@ __host__ __device__ __forceinline__ int64_t row_bytes(const AppendParams& p) {
   return 2ll * p.D * (p.Hq + (KIND == PKV_KV_FP8_E4M3_BLOCK ? 0 : p.Hkv * (p.v != nullptr ? 2 : 1)));
 }
 
+// CTAs of the kernel an SM holds at most: by their registers, 72 a thread, and 96 with norms.
+template <bool NORM>
+constexpr int kStreamPerSm = NORM ? 2 : 3;
+
 template <int KIND, uint32_t S, bool NORM>
-__global__ void __launch_bounds__(kThreads + 32, NORM ? 2 : 3) kv_append_stream_kernel(AppendParams p) {
+__global__ void __launch_bounds__(kThreads + 32, kStreamPerSm<NORM>) kv_append_stream_kernel(AppendParams p) {
   extern __shared__ __align__(128) uint8_t sm_rows[];
   __shared__ uint64_t full[S], done[S];
   __shared__ int64_t s_slot[S];  // -1: a token that is skipped
@@ -629,14 +633,16 @@ __global__ void __launch_bounds__(kThreads) kv_append_runs_kernel(AppendParams p
 
 }  // namespace
 
-// Rows through shared memory, if two CTAs of S stages fit an SM (three at most do, by their registers).
+// Rows through shared memory, if two CTAs of S stages fit an SM. The CTAs divide the tokens among them, so there are no more than
+// run at once (kStreamPerSm): 10,000 tokens with norms of 32 and 8 heads of 128 into a bf16 cache 58 us (three CTAs an SM in the
+// grid, of which two run: 75), of 64 and 8 into one with tensor scales 96 (123).
 // More CTAs with fewer stages where codes are made or little is stored beside q, more stages where the
 // copies are all there is: 10,000 tokens of 64 query and 8 KV heads of 128 into a bf16 cache 73.7 us
 // with 3 stages and 69.5 with 4 (66 since an elected thread issues); into a block-scaled one 84.5 and 86.
 template <int KIND, bool NORM>
 static bool launch_stream(const AppendParams& p, cudaStream_t stream, cudaError_t* e) {
   constexpr uint32_t S = KIND == PKV_KV_BF16 ? 4 : 3;
-  constexpr int64_t kRoom = 222 * 1024, kPerSm = 3;
+  constexpr int64_t kRoom = 222 * 1024, kPerSm = kStreamPerSm<NORM>;
   const int64_t bytes = (row_bytes<KIND>(p) + p.rot * 4) * S, taken = bytes + 1280;  // with the static and reserved bytes
   if (2 * taken > kRoom) return false;
   *e = set_smem_attr_once(reinterpret_cast<const void*>(&kv_append_stream_kernel<KIND, S, NORM>), static_cast<int>(kRoom / 2),
