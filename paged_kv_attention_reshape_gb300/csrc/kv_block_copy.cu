@@ -24,11 +24,12 @@ __global__ void __launch_bounds__(kThreads) kv_block_copy_kernel(const __grid_co
   const int64_t i = blockIdx.x;
   const int layer = blockIdx.y / p.parts, part = blockIdx.y % p.parts;
   const int64_t s = p.src[i], d = p.dst[i];
-  if (s < 0 || d < 0 || s == d) return;  // a padding pair, or nothing to do
+  if (s < 0 || d < 0) return;  // a padding pair
   if (s >= p.num_blocks || d >= p.num_blocks) {
     if (threadIdx.x == 0 && blockIdx.y == 0) flag_error(p.err, PKV_DEVERR_BLOCK);
     return;
   }
+  if (s == d) return;  // nothing to do
   uint8_t* base = static_cast<uint8_t*>(part ? p.layer[layer].v : p.layer[layer].k);
   const uint4* in = reinterpret_cast<const uint4*>(base + s * p.stride_bytes);
   uint4* out = reinterpret_cast<uint4*>(base + d * p.stride_bytes);

@@ -144,6 +144,16 @@ def test_bad_ids_are_flagged():
 
 
 @pytest.mark.gpu
+def test_a_bad_id_onto_itself_is_flagged():
+    import paged_kv_attention_reshape_gb300 as pkv
+    for bad in (6, 2 ** 31 - 1):
+        verify(pools(1, 6, (16, 2, 128), "bf16", 5), [0, bad, -1], [3, bad, bad])
+        assert pkv.device_errors() == 2
+    verify(pools(1, 6, (16, 2, 128), "bf16", 5), [5, -1, 6], [5, 6, -1])  # the last block onto itself, and padding
+    assert pkv.device_errors() == 0
+
+
+@pytest.mark.gpu
 def test_captured_and_on_another_stream():
     import paged_kv_attention_reshape_gb300 as pkv
     made = pools(3, 20, (16, 4, 128), "block", 8)
