@@ -436,12 +436,13 @@ def paged_decode_workspace_size(max_reqs, Hq, Hkv, D, max_seq_len) -> int:
 
 
 def _window(window, sinks):
-    """The (window, sinks) of a windowed call as integers, or None for a call without a window."""
+    """The (window, sinks) of a windowed call as 32-bit integers (no row is further away than that; below zero they stay
+    refused), or None for a call without a window."""
     if window is None:
         if sinks:
             raise PkvError("sinks belong to a window")
         return None
-    return min(int(window), 2**31 - 1), min(int(sinks), 2**31 - 1)
+    return tuple(max(-1, min(int(x), 2**31 - 1)) for x in (window, sinks))
 
 
 def _window_args(q, heads, dim, rows, reqs, index, out, lse, kv=(), workspace=None):
@@ -636,7 +637,7 @@ def extend_block_workspace_size(max_q_len, max_seq_len, num_q_heads, num_kv_head
 def window_extend_workspace_size(num_tokens, max_reqs, max_q_len, max_seq_len, num_q_heads, num_kv_heads, head_dim, window,
                                  sinks=0, kv_dtype=_lib.KV_FP8_E4M3) -> int:
     return int(_lib.load().pkv_window_extend_workspace_size(num_tokens, max_reqs, max_q_len, max_seq_len, num_q_heads,
-                                                            num_kv_heads, head_dim, kv_dtype, window, sinks))
+                                                            num_kv_heads, head_dim, kv_dtype, *_window(window, sinks)))
 
 
 def extend_fp8_workspace_size(max_reqs, batch_reqs, max_seq_len, max_blocks, num_kv_heads, head_dim) -> int:

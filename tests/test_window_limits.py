@@ -14,6 +14,20 @@ ENDS = [(MOST, 0), (1 << 40, 0), (MOST, 5), (MOST - 7, 0), (MOST - 15, 18), (MOS
         (1, 1 << 40)]
 
 
+def test_numbers_beyond_32_bits():
+    """Larger windows and sinks are the largest there are; numbers far below zero stay below it (none may wrap around)."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    from paged_kv_attention_reshape_gb300 import binding
+    assert binding._window(1 << 40, (1 << 32) + 5) == (MOST, MOST) and binding._window(MOST, 0) == (MOST, 0)
+    for x in (5 - (1 << 32), -(1 << 40), -1):
+        window, sinks = binding._window(x, x)
+        assert -2 ** 31 <= window < 1 and -2 ** 31 <= sinks < 0
+    size = lambda window, sinks: pkv.window_extend_workspace_size(2048, 1, 2048, 100000, 64, 8, 128, window, sinks)
+    assert size(1 << 40, 0) == size(MOST, 0) > 0 and size((1 << 32) + 1, 4) == size(MOST, 4) > 0
+    assert size(4096, 1 << 40) == size(4096, MOST) > 0
+    assert size(5 - (1 << 32), 0) == 0 and size(4096, 4 - (1 << 32)) == 0
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("window,sinks", ENDS)
 @pytest.mark.parametrize("kind,D,Hq,Hkv", [("bf16", 64, 8, 2), ("bf16", 128, 16, 1), ("bf16", 128, 2, 2), ("tensor", 128, 16, 2)])
