@@ -451,6 +451,8 @@ pkv_status pkv_varlen_prefill_attn(const void* q, const void* k, const void* v, 
  *   - a value that is not finite in a key that some row sees may reach the rows of the same
  *     request and KV head that do not see it, for extend and prefill. Keys that no row sees
  *     touch nothing, whatever they hold.
+ *   - extend and prefill sum up to 2^20 times a value over the keys that a row sees: values of up
+ *     to 2^108 over their number (2^96 for 4096 keys) stay finite, larger ones may become infinite.
  * The decode takes the workspace of paged_decode_attn; prefill needs none. The extend over an FP8
  * cache may be given one (16-byte aligned; NULL: none), rewritten by the call: the keys and values that
  * requests of many new tokens see are then converted there once, as far as it reaches, instead of

@@ -5,8 +5,8 @@
 // Mathematics: with s_j = log2(e) scale (q . k_j) over the keys that a row sees and m any number of their size,
 // P_j = 2^(s_j - m):  O = sum P_j v_j,  l = sum P_j,  out = O / l,  lse = (m + log2 l) ln 2. m is the max of the
 // scores when the row first meets one, and follows them only when they pass it by more than LAZY: P and O
-// keep the precision of their types whatever the power of two in front, P <= 2^20 (fp16: 2^15) leaves values up to
-// 2^100 room, and O is rescaled in nearly no tile. In fp16, whose smallest number is 2^-24, m is RAISE below that max: a row's
+// keep the precision of their types whatever the power of two in front, and O is rescaled in nearly no tile. P <= 2^20, so
+// the keys that a row sees times their largest value may come to 2^108 (over codes P <= 2^15 and values are fp16). In fp16, whose smallest number is 2^-24, m is RAISE below that max: a row's
 // largest P is 2^8 at least, and terms down to 2^-33 of it count (with 2^-25, what thousands of keys have in common was
 // lost from O, not from l).
 //

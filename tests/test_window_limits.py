@@ -107,3 +107,29 @@ def test_small_terms_add_up(reqs, Hq, Hkv, ahead):
         row += n
     assert (tol[:st["T"]] > 0).all() and (tol < 0.05 * o)[:st["T"]].all()
     check(got, (o, z, tol, ltol), st["T"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which,D", [("extend", 128), ("extend", 64), ("prefill", 128)])
+def test_the_largest_values(which, D):
+    """Scores that rise by nearly 2^20 after the first key tile, which a row's m does not follow, over values of 2^108 by the
+    number of keys: 2^99 for up to 400 of them."""
+    mix = [(0, 400)] if which == "prefill" else [(300, 100), (0, 390)]
+    st = make(mix, 16, 2, D, "none" if which == "prefill" else "bf16", 1000, 0, 97)
+    T = st["T"]
+    st["q"][:T] = 0
+    st["q"][:T, :, 0] = 19.9 * math.sqrt(D) / math.log2(math.e)
+    assert float(st["q"][0, 0, 0]) / math.sqrt(D) * math.log2(math.e) < 20
+    st["k_new"][:T] = 0
+    st["v_new"][:T] = 2.0 ** 99
+    row = 0
+    for r, (c, n) in enumerate(mix):
+        at = torch.arange(c, c + n)
+        st["k_new"][row:row + n, :, 0] = (at >= 128).to(torch.bfloat16)[:, None]
+        for j in range(c):
+            page = st["table"][r, j // 16]
+            st["kc"][page, j % 16] = 0
+            st["kc"][page, j % 16, :, 0] = float(j >= 128)
+            st["vc"][page, j % 16] = 2.0 ** 99
+        row += n
+    check(call(st, which), reference(st), T)
