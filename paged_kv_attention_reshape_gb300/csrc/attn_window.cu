@@ -287,7 +287,7 @@ struct WnRow {
   int sinks, from, end, hole0, hole1;
   __device__ WnRow(const AttnParams& p, const WnItem& it, int i) {  // the row at position i >= C
     // (a window's start before the first key is the first key: `from` minus a column stays within 32 bits)
-    const int C = it.C, cols = 16 * it.cb, gap = 16 * it.gap, low = i >= p.window ? i - p.window + 1 : 0;
+    const int C = it.C, cols = 16 * it.cb, gap = 16 * it.gap, low = max(i - p.window + 1, 0);
     sinks = p.sinks <= C ? p.sinks : min(p.sinks, i + 1) - C + cols;
     from = (low < C ? low : low - C + cols) - gap;
     end = i - C + cols - gap + 1;
