@@ -184,10 +184,12 @@ __device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, in
 // ---- the pool (kWnPool) --------------------------------------------------------------------------------
 // The pool holds, request after request, the chunks of 16 keys that some row of the request sees: the `hb` blocks of
 // sinks, the cached blocks from the first row's window on, the new tokens. Chunk u of a request lies at its first
-// block + u, less `gap` from hb on. A request belongs to it when it has kPoolRows rows a KV head and the pool has room (four
-// items read its keys; 128 tokens of 64 and 8 heads under 4096, that many: 63 us without and 56 with, 8 x 64 of 16 and 1 under
-// 1024 26 and 33).
-constexpr int kPoolRows = 1024;
+// block + u, less `gap` from hb on. A request belongs to it when it has kPoolRows rows a KV head, an item of them, and the pool
+// has room: beside long requests, shorter ones left to the codes are a launch of few items before the others' (2048 tokens of
+// 64 and 8 heads under 4096 beside 8 requests of 32 tokens: 281 us, 297 from 512 rows on; 1024 under 2048 beside 4 of 32: 102 and
+// 121). A call has a pool only with a request of kPoolLong rows (8 x 64 tokens of 64 and 8 heads under 4096, 512 rows each, 101
+// us without and 121 with; 8 x 128 193 and 173).
+constexpr int kPoolRows = 256, kPoolLong = 1024;
 struct WnPooled {
   int cb, hb, gap;
   __device__ WnPooled(const AttnParams& p, int C) {
@@ -1215,22 +1217,27 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap
 
 }  // namespace
 
-// Converting ahead costs a launch (9 us on a GB300), 0.11 ns a key and KV head and, in items of few tiles, their first and last
-// tiles, which overlap less; it saves 5.5 ns a key tile of an item. Without and with it, us, 64 query and 8 KV heads: 2048
-// tokens under 4096 315 and 230, 512 97 and 77, 128 63 and 56; 8 x 512 under 128 86 and 103, 512 137 and 145, 1024 200 and
-// 190; 8 x 256 under 1024 116 and 117, 2048 187 and 170; 8 x 128 under 1024 66 and 77, 4096 185 and 177; 4 x 1024 of 8 and 8
-// heads under 1024 46 and 62; 8 x 512 of 16 and 1 69 and 64.
+// Converting ahead saves the items some 1 us a key tile, on the CTA that has most of them, and costs 3 us a round of items (their
+// first and last tiles overlap less), 7 us for a launch and 0.15 ns a key and KV head converted. In halves of rounds (the last of few
+// rounds may be halved, as in the kernel) and 256ths of a microsecond, fitted to pairs of times; of 69 the rule takes the slower side
+// in seven, for 2 to 8 %. Without and with it, us, 64 query and 8 KV heads if no others are named: 2048 tokens under 4096 314 and
+// 230, 512 98 and 74, 128 59 and 58; 8 x 512 under 128 84 and 105, 512 135 and 143, 768 165 and 164, 1024 198 and 187; 8 x 256
+// under 1024 112 and 116, 2048 185 and 169; 8 x 128 under 1024 66 and 74, 2048 105 and 111, 4096 187 and 174; 1024 under 1024 63
+// and 62, 512 37 and 42; 4 x 1024 of 8 and 8 heads under 1024 45 and 64; 8 x 512 of 16 and 1 68 and 62, 8 x 128 27 and 34.
+// Converted, and slower: 2 x 2048 of 8 and 8 under 4096 103 and 107; 2048 under 1024 104 and 106, beside 8 x 64 134 and 144,
+// beside 8 x 128 152 and 160.
 int64_t attn_window_pool_blocks(int64_t num_tokens, int32_t max_reqs, int32_t max_q_len, int32_t max_seq_len, int Hq, int Hkv,
                                 int32_t window, int32_t sinks) {
-  const int G = Hq / Hkv;
-  if (static_cast<int64_t>(max_q_len) * G < kPoolRows) return 0;
-  const int64_t reqs = std::min<int64_t>(std::min<int64_t>(max_reqs, kAttnSetChunk), num_tokens * G / kPoolRows);
+  const int G = Hq / Hkv, sms = num_sms();
+  if (static_cast<int64_t>(max_q_len) * G < kPoolLong) return 0;
+  const int64_t most = std::min<int64_t>(max_reqs, kAttnSetChunk), reqs = std::min(most, num_tokens * G / kPoolLong);
   const int64_t keys = std::min<int64_t>(max_seq_len, static_cast<int64_t>(window) + sinks);
-  const int64_t items = num_tokens * Hq / 256, tiles = (keys + 256 / G) / 128;
-  if (items * (tiles - 3) < 1640 + (reqs * keys + num_tokens) * Hkv / 50) return 0;
+  const int64_t items = (num_tokens * Hq + 255) / 256, rest = items % sms;
+  const int64_t halves = 2 * (items / sms) + (rest == 0 ? 0 : items <= 4 * sms && 2 * rest <= sms ? 1 : 2);
+  if (halves * (keys + 256 / G - 384) < 1800 + (reqs * keys + num_tokens) * Hkv / 24) return 0;
   const int64_t all = (static_cast<int64_t>(max_seq_len) + 15) / 16;
   const int64_t seen = (static_cast<int64_t>(sinks) + 15) / 16 + (static_cast<int64_t>(window) + 15) / 16 + 1;
-  return reqs * (std::min(all, seen) + 1) + num_tokens / 16;
+  return std::min(most, num_tokens * G / kPoolRows) * (std::min(all, seen) + 1) + num_tokens / 16;
 }
 
 cudaError_t launch_attn_window(const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,

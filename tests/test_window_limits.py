@@ -133,3 +133,19 @@ def test_the_largest_values(which, D):
             st["vc"][page, j % 16] = 2.0 ** 99
         row += n
     check(call(st, which), reference(st), T)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv", [(48, 3), (64, 8)])
+def test_requests_of_an_item_of_rows(Hq, Hkv):
+    """Requests of one row less than an item of 256 rows a KV head, of an item, of one more: the former are read as codes."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    t = 256 * Hkv // Hq
+    reqs = [(300, t - 1), (2400, 900), (300, t), (317, t + 1), (5, t), (0, t), (40, 1)]
+    st = make(reqs, Hq, Hkv, 128, "tensor", 3000, 5, 98)
+    need = pkv.window_extend_workspace_size(st["q"].shape[0], len(reqs), 900, 3300, Hq, Hkv, 128, 3000, 5)
+    assert need > 0
+    ref = reference(st)
+    for n in (need, need // 3):
+        check(extend_with(st, torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda"), n), ref, st["T"])
+    check(extend_with(st, None, 0), ref, st["T"])
