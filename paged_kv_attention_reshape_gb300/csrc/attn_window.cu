@@ -150,7 +150,9 @@ __device__ __forceinline__ int wn_cost(const AttnParams& p, const int4& q) {
 }
 
 // Item idx of a request {request id, first query row, q_len, cached tokens}, or one half of its tokens (half 0 or 1; -1:
-// all). A second half without tokens is the first one again: another CTA, which had nothing else to do, writes the same.
+// all). A second half without tokens is the first one again: another CTA, which had nothing else to do, writes the same bits. It
+// does because an item's tiles go to the slots in a fixed order (tile j of a split item to slot j % 2), each slot adds them up in
+// that order, and the merge takes slot 0 first: were tiles dealt as they arrive, this half's stores would have to be left out.
 __device__ __forceinline__ WnItem wn_item(const AttnParams& p, const int4& q, int idx, int half) {
   WnItem it;
   it.r = q.x;
