@@ -36,8 +36,12 @@ constexpr int kBlockTokens = 16;  // block size of a block-scaled cache
 // and 22.9, 18.8 and 22.0, 12.8 and 12.7; 2800 30.8 and 32.2, 27.7 and 27.3, 25.4 and 25.6, 16.8 and 15.2; 4096 44.6 and
 // 40.6, 40.5 and 35.7, 36.6 and 32.6, 23.8 and 19.6. (One token a sequence with 64 and 8 heads: 2800 72.8 and 78.6, 4096
 // 106 and 106.) With norms, of a bf16 cache: 64 and 8 heads 256 tokens 6.2 and 6.0, 512 11.1 and 8.5, 1024 19.7 and 13.0; 32 and 8
-// 512 8.0 and 6.5, 1024 14.2 and 9.8; 8 and 2 of 64 512 5.0 and 3.7, 1024 10.2 and 6.1.
+// 512 8.0 and 6.5, 1024 14.2 and 9.8; 8 and 2 of 64 512 5.0 and 3.7, 1024 10.2 and 6.1; of one with tensor scales 64 and 8 256 6.3 and
+// 6.4, 512 11.3 and 9.6, 32 and 8 256 4.6 and 5.1, 512 8.2 and 7.2. Beside a block-scaled cache the norms' registers bring the
+// crossing forward: 64 and 8, 32 and 8, 8 and 2 2048 tokens 29.6 and 30.3, 23.2 and 24.2, 17.1 and 15.3; 2800 40.0 and 37.2, 31.2
+// and 29.2, 22.7 and 18.9; 8 and 2 1024 11.6 and 13.5.
 constexpr int kManyTokens = 512, kManyTokensBlock = 2900, kManyTokensBlockFewHeads = 2048, kFewHeads = 16;
+constexpr int kManyTokensBlockNorm = 2300, kManyTokensBlockFewHeadsNorm = 1500;
 
 __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -655,15 +659,17 @@ static bool launch_stream(const AppendParams& p, cudaStream_t stream, cudaError_
 }
 
 // Tokens from which launch_rows sends them through shared memory.
+template <bool NORM>
 static int many_tokens(const AppendParams& p, int kind) {
   if (kind != PKV_KV_FP8_E4M3_BLOCK) return kManyTokens;
+  if (NORM) return p.Hq > kFewHeads ? kManyTokensBlockNorm : kManyTokensBlockFewHeadsNorm;
   return p.Hq > kFewHeads ? kManyTokensBlock : kManyTokensBlockFewHeads;
 }
 
 template <int KIND, bool NORM>
 static cudaError_t launch_rows(const AppendParams& p, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  if (p.num_tokens >= many_tokens(p, KIND) && launch_stream<KIND, NORM>(p, stream, &e)) return e;
+  if (p.num_tokens >= many_tokens<NORM>(p, KIND) && launch_stream<KIND, NORM>(p, stream, &e)) return e;
   return launch_pdl(kv_append_kernel<KIND, 1, 2, false, NORM>, dim3(static_cast<unsigned>(p.num_tokens)), dim3(kThreads), 0,
                     stream, p);
 }
@@ -678,7 +684,7 @@ static cudaError_t launch_append(const AppendParams& in, int kind, cudaStream_t 
   // 11.1, 9.7, 9.1; 4096 49, 39, 37; of one token a sequence 256 8.1, 18.5, 62; 1024 26, 25, 85; 4096 112, 105, 120.
   p.run_tokens = p.num_tokens <= 1024 ? 1 : (p.num_tokens <= 4096 ? 4 : kBlockTokens);
   p.run_groups = static_cast<uint32_t>((p.num_tokens + p.run_tokens - 1) / p.run_tokens);
-  if (p.Hq > 0 && p.num_tokens < many_tokens(p, kind))
+  if (p.Hq > 0 && p.num_tokens < many_tokens<NORM>(p, kind))
     return launch_pdl(kv_append_kernel<PKV_KV_FP8_E4M3_BLOCK, 1, 2, true, NORM>,
                       dim3(static_cast<unsigned>(p.run_groups + p.num_tokens)), dim3(kThreads), 0, stream, p);
   cudaError_t e = launch_pdl(kv_append_runs_kernel<NORM>, dim3(p.run_groups), dim3(kThreads), 0, stream, p);

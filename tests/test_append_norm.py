@@ -177,6 +177,12 @@ def test_long_batches(kind, T, Hq, Hkv, w32):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,T", [(16, 1499), (16, 1500), (17, 1500), (17, 2299), (17, 2300)])
+def test_both_sides_of_where_rows_beside_block_scales_change(Hq, T):
+    verify(make("block", T, Hq, 1, 128, 128, 0, False, False, T + Hq, skipped=(0, 7, T - 1)))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "tensor", "block"])
 @pytest.mark.parametrize("sides", ["q", "k"])
 @pytest.mark.parametrize("T", [20, 800])
