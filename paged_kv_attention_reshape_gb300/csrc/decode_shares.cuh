@@ -295,10 +295,28 @@ __host__ __device__ constexpr int merge_levels(int shares) {
   return L;
 }
 
+// What the children of a node weigh in it, from their LSEs (-inf for a child that is not there). Returns the node's LSE.
+// Whoever merges a node, from registers or from memory, takes these weights and adds the children up in their order with
+// fused products, so that the node's bits do not depend on which child came last.
+__device__ __forceinline__ float merge_weights(const float (&l)[kFan], float (&w)[kFan]) {
+  float M = -CUDART_INF_F, W = 0.f;
+#pragma unroll
+  for (int m = 0; m < kFan; ++m) M = fmaxf(M, l[m]);
+#pragma unroll
+  for (int m = 0; m < kFan; ++m) {
+    w[m] = l[m] == -CUDART_INF_F ? 0.f : __expf(__fsub_rn(l[m], M));
+    W = __fadd_rn(W, w[m]);
+  }
+  const float inv = W > 0.f ? __fdiv_rn(1.f, W) : 0.f;
+#pragma unroll
+  for (int m = 0; m < kFan; ++m) w[m] = __fmul_rn(w[m], inv);
+  return W > 0.f ? __fadd_rn(M, __logf(W)) : -CUDART_INF_F;
+}
+
 // A normalised partial in registers, in the MMA accumulator layout: o[i][2h + c] is row
 // r0 + 8h (r0 = lane / 4), column i*8 + 2*(lane%4) + c, and lse[h] the row's LSE.
-// Fold the children of node (L, a) other than `self` (its index among them) into the
-// registers, which hold child `self`; the registers then hold node (L, a).
+// Merge the children of node (L, a) with the registers, which hold child `self`, one of the first two (a later one would
+// need the sum of those before it in registers of its own); the registers then hold node (L, a), in the bits of merge_node.
 template <int D>
 __device__ __forceinline__ void fold_siblings(const DecodeParams& p, const Cut& s, int L, int a, int k, int self,
                                               int kh, float (&o)[D / 8][4], float (&lse)[2], int lane) {
@@ -307,32 +325,40 @@ __device__ __forceinline__ void fold_siblings(const DecodeParams& p, const Cut& 
   for (int h = 0; h < 2; ++h) {
     const int gg = r0 + 8 * h;
     if (gg >= G) continue;
-    float M = lse[h], W = lse[h] == -CUDART_INF_F ? 0.f : 1.f;
-    for (int m = 0; m < k; ++m) {
-      if (m == self) continue;
-      const float* src = node_part<D>(p, s, L - 1, a * kFan + m, kh, gg);
-      const float l = __ldcg(src + D);
-      float2 v[D / 8];
+    float l[kFan], w[kFan];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) v[i] = __ldcg(reinterpret_cast<const float2*>(src + i * 8 + col));
-      if (l == -CUDART_INF_F) continue;
-      const float m_new = fmaxf(M, l);
-      const float al = __expf(M - m_new), w = __expf(l - m_new);
-      W = W * al + w;
-      M = m_new;
+    for (int m = 0; m < kFan; ++m)
+      l[m] = m == self ? lse[h] : m < k ? __ldcg(node_part<D>(p, s, L - 1, a * kFan + m, kh, gg) + D) : -CUDART_INF_F;
+    lse[h] = merge_weights(l, w);
+    // child 0's product is rounded, the others are added to it
+    if (self == 0) {
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        o[i][2 * h] = o[i][2 * h] * al + w * v[i].x;
-        o[i][2 * h + 1] = o[i][2 * h + 1] * al + w * v[i].y;
+        o[i][2 * h] = __fmul_rn(w[0], o[i][2 * h]);
+        o[i][2 * h + 1] = __fmul_rn(w[0], o[i][2 * h + 1]);
       }
     }
-    const float inv = W > 0.f ? 1.f / W : 0.f;
+#pragma unroll 1
+    for (int m = self == 0 ? 1 : 0; m < k; m += m == 0 ? 2 : 1) {
+      const float* src = node_part<D>(p, s, L - 1, a * kFan + m, kh, gg) + col;
+      const float wm = m == 0 ? w[0] : m == 1 ? w[1] : m == 2 ? w[2] : w[3];
+      float2 v[D / 8];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      o[i][2 * h] *= inv;
-      o[i][2 * h + 1] *= inv;
+      for (int i = 0; i < D / 8; ++i) v[i] = __ldcg(reinterpret_cast<const float2*>(src + i * 8));
+      if (m == 0) {  // (the registers hold child 1)
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][2 * h] = fmaf(w[1], o[i][2 * h], __fmul_rn(wm, v[i].x));
+          o[i][2 * h + 1] = fmaf(w[1], o[i][2 * h + 1], __fmul_rn(wm, v[i].y));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][2 * h] = fmaf(wm, v[i].x, o[i][2 * h]);
+          o[i][2 * h + 1] = fmaf(wm, v[i].y, o[i][2 * h + 1]);
+        }
+      }
     }
-    lse[h] = W > 0.f ? M + __logf(W) : -CUDART_INF_F;
   }
 }
 
@@ -390,7 +416,7 @@ __device__ __forceinline__ void store_regs(const DecodeParams& p, const Cut& s, 
 // Merge the k <= 4 children of node (L, a), all in the workspace, into out/lse (the root) or
 // into the node's partial. One warp: lane g < G turns head g's LSEs into weights; then, four
 // heads at a time, every lane loads its elements l*PER .. l*PER+PER-1 of all children before
-// folding them, so each group costs one round trip to L2 (the partials were written by other
+// adding them up, so each group costs one round trip to L2 (the partials were written by other
 // SMs and are read from L2).
 template <int D, int UPG, int OUT_DIM, bool VPERM = false>
 __device__ __forceinline__ void merge_node(const DecodeParams& p, const Cut& s, int L, int a, int k, bool root,
@@ -398,25 +424,13 @@ __device__ __forceinline__ void merge_node(const DecodeParams& p, const Cut& s, 
   constexpr int PER = D / 32;
   constexpr int HB = 4;  // heads per group of loads
   const int G = p.G;
-  float M = -CUDART_INF_F, W = 0.f, w[kFan];
+  float node_lse = -CUDART_INF_F, w[kFan] = {};
   if (lane < G) {
     float l[kFan];
 #pragma unroll
-    for (int m = 0; m < kFan; ++m) {
+    for (int m = 0; m < kFan; ++m)
       l[m] = m < k ? __ldcg(node_part<D>(p, s, L - 1, a * kFan + m, kh, lane) + D) : -CUDART_INF_F;
-      M = fmaxf(M, l[m]);
-    }
-#pragma unroll
-    for (int m = 0; m < kFan; ++m) {
-      w[m] = l[m] == -CUDART_INF_F ? 0.f : __expf(l[m] - M);
-      W += w[m];
-    }
-    const float inv = W > 0.f ? 1.f / W : 0.f;
-#pragma unroll
-    for (int m = 0; m < kFan; ++m) w[m] *= inv;
-  } else {
-#pragma unroll
-    for (int m = 0; m < kFan; ++m) w[m] = 0.f;
+    node_lse = merge_weights(l, w);
   }
   for (int g0 = 0; g0 < G; g0 += HB) {
     float v[HB][kFan][PER];
@@ -446,11 +460,10 @@ __device__ __forceinline__ void merge_node(const DecodeParams& p, const Cut& s, 
       for (int m = 0; m < kFan; ++m) {
         const float wm = __shfl_sync(0xffffffffu, w[m], gg & 31);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] += wm * v[hb][m][e];
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(wm, v[hb][m][e], acc[e]);
       }
-      const float Mg = __shfl_sync(0xffffffffu, M, gg & 31), Wg = __shfl_sync(0xffffffffu, W, gg & 31);
+      const float lse = __shfl_sync(0xffffffffu, node_lse, gg & 31);
       if (gg >= G) continue;
-      const float lse = Wg > 0.f ? Mg + __logf(Wg) : -CUDART_INF_F;
       if (root) {
         __nv_bfloat16* dst = p.out + out_offset<D, UPG, OUT_DIM>(p, s.row, kh, gg);
         if constexpr (VPERM) {
@@ -500,36 +513,41 @@ struct CutMerger {
   }
 
   // A cut piece is done: its normalised partial is in (o, lse). Climb while all siblings are
-  // in (folding them into the registers); at the root write out/lse, else store the registers
-  // as the node's partial and owe an arrival on the parent. `check` = look at the counters
-  // first (worth a round trip only when no block of the share follows to hide it).
+  // in (merging them in the registers, or, where it is the third or fourth child, from memory at the end); at the root write
+  // out/lse, else store the registers as the node's partial and owe an arrival on the parent. `check` = look at the
+  // counters first (worth a round trip only when no block of the share follows to hide it).
   __device__ void piece_done(const DecodeParams& p, const Cut& s, int piece, int kh, float (&o)[D / 8][4],
                              float (&lse)[2], bool check, int lane) {
     int L = 1, ai = piece;  // the registers hold node (L - 1, ai)
     for (;;) {
-      const int a = ai / kFan, k = s.children(L, a);
+      const int a = ai / kFan, k = s.children(L, a), self = ai - a * kFan;
       if (k > 1) {
         unsigned long long* ctr = node_ctr(p, s, L, a, kh);
         unsigned long long cur = 0;
         if (lane == 0) cur = atomicAdd(ctr, 0ull);
         const int prior = check ? __shfl_sync(0xffffffffu, static_cast<int>(arrivals_of(cur, p.epoch, k)), 0) : 0;
-        if (prior != k - 1) {
+        const bool last = prior == k - 1;
+        if (last && lane == 0) clear_counter(ctr);
+        if (!last || self > 1) {
           store_regs<D>(p, s, L - 1, ai, kh, o, lse, lane);
           if (lane == 0) {
-            st->pend_ctr = ctr;
-            st->pend_cur = cur;
-            st->pend_s = s;
-            st->pend_L = L;
-            st->pend_a = a;
-            st->pend_k = k;
+            if (last) {
+              owe(p, s, L, a);
+            } else {
+              st->pend_ctr = ctr;
+              st->pend_cur = cur;
+              st->pend_s = s;
+              st->pend_L = L;
+              st->pend_a = a;
+              st->pend_k = k;
+            }
           }
           __syncwarp();
-          pend = true;
+          pend = !last;
           return;
         }
         __threadfence();
-        if (lane == 0) clear_counter(ctr);
-        fold_siblings<D>(p, s, L, a, k, ai - a * kFan, kh, o, lse, lane);
+        fold_siblings<D>(p, s, L, a, k, self, kh, o, lse, lane);
         check = true;  // the siblings were in: the next level is likely complete too
       }
       if (s.nodes(L) == 1) {
@@ -538,6 +556,19 @@ struct CutMerger {
       }
       ai = a;
       ++L;
+    }
+  }
+
+  // (lane 0) The node is this warp's to merge when its share is done.
+  __device__ void owe(const DecodeParams& p, const Cut& s, int L, int a) {
+    const int d = st->due;
+    if (d < 2) {
+      st->due_s[d] = s;
+      st->due_L[d] = L;
+      st->due_a[d] = a;
+      st->due = d + 1;
+    } else {
+      flag_error(p.err, PKV_DEVERR_REQS);  // cannot happen: a share stores at most two partials
     }
   }
 
@@ -550,15 +581,7 @@ struct CutMerger {
       const int k = st->pend_k;
       if (arrive_counter(st->pend_ctr, p.epoch, k, st->pend_cur, p.err) == k) {
         clear_counter(st->pend_ctr);
-        const int d = st->due;
-        if (d < 2) {
-          st->due_s[d] = st->pend_s;
-          st->due_L[d] = st->pend_L;
-          st->due_a[d] = st->pend_a;
-          st->due = d + 1;
-        } else {
-          flag_error(p.err, PKV_DEVERR_REQS);  // cannot happen: a share stores at most two partials
-        }
+        owe(p, st->pend_s, st->pend_L, st->pend_a);
       }
     }
     __syncwarp();
