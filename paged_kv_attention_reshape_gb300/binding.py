@@ -442,7 +442,7 @@ def _window(window, sinks):
         if sinks:
             raise PkvError("sinks belong to a window")
         return None
-    return tuple(max(-1, min(int(x), 2**31 - 1)) for x in (window, sinks))
+    return max(-1, min(int(window), 2**31 - 1)), max(-1, min(int(sinks), 2**31 - 1))
 
 
 def _window_args(q, heads, dim, rows, reqs, index, out, lse, kv=(), workspace=None):
