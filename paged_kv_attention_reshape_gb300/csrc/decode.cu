@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8>::MAXW * 32) __maxnreg__((Dec
     float inv[2], lse[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      inv[h] = l_run[h] > 0.f ? p.v_scale / l_run[h] : 0.f;  // the value scale of an FP8 cache folds in
-      lse[h] = l_run[h] > 0.f ? (m_run[h] + __log2f(l_run[h])) * 0.69314718055994531f : -CUDART_INF_F;
+      inv[h] = l_run[h] == 0.f ? 0.f : p.v_scale / l_run[h];  // the value scale of an FP8 cache folds in
+      lse[h] = l_run[h] == 0.f ? -CUDART_INF_F : (m_run[h] + __log2f(l_run[h])) * 0.69314718055994531f;  // (NaN stays NaN)
     }
     if (whole) {
 #pragma unroll

@@ -307,10 +307,10 @@ __device__ __forceinline__ float merge_weights(const float (&l)[kFan], float (&w
     w[m] = l[m] == -CUDART_INF_F ? 0.f : __expf(__fsub_rn(l[m], M));
     W = __fadd_rn(W, w[m]);
   }
-  const float inv = W > 0.f ? __fdiv_rn(1.f, W) : 0.f;
+  const float inv = W == 0.f ? 0.f : __fdiv_rn(1.f, W);  // (a child that is no number makes the node none)
 #pragma unroll
   for (int m = 0; m < kFan; ++m) w[m] = __fmul_rn(w[m], inv);
-  return W > 0.f ? __fadd_rn(M, __logf(W)) : -CUDART_INF_F;
+  return W == 0.f ? -CUDART_INF_F : __fadd_rn(M, __logf(W));
 }
 
 // A normalised partial in registers, in the MMA accumulator layout: o[i][2h + c] is row

@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(MlaCfg::THREADS, 2) mla_decode_kernel(const De
       float inv[2], lse[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        inv[h] = l_run[h] > 0.f ? 1.f / l_run[h] : 0.f;
-        lse[h] = l_run[h] > 0.f ? (m_run[h] + __log2f(l_run[h])) * 0.69314718055994531f : -CUDART_INF_F;
+        inv[h] = l_run[h] == 0.f ? 0.f : 1.f / l_run[h];
+        lse[h] = l_run[h] == 0.f ? -CUDART_INF_F : (m_run[h] + __log2f(l_run[h])) * 0.69314718055994531f;  // (NaN stays NaN)
       }
       if (whole) {
 #pragma unroll

@@ -49,3 +49,27 @@ def test_the_same_bits_whatever_ends_first(lens, Hq, Hkv, D, kind, kw):
         differ += (x != o).sum() + (y != z).sum()
     torch.cuda.synchronize()
     assert int(differ) == 0 and pkv.device_errors() == 0
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,kind", [([8000] * 5, 16, 2, 128, "bf16"), ([8000] * 5, 8, 2, 64, "bf16"), ([40, 90], 16, 2, 128, "bf16"),
+                                                ([9000, 500], 16, 2, 128, "tensor"), ([3000] * 4, 16, 1, 576, "latent"), ([50], 16, 1, 576, "latent")])
+def test_a_key_that_is_no_number(lens, Hq, Hkv, D, kind):
+    """It makes out and lse of its request and KV head none, in whichever piece of the sequence it lies, and of no other."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    q, kc, vc, table, n, most = state(lens, Hq, Hkv, D, kind, 8)
+    if kind == "latent":
+        call = lambda: pkv.mla_decode_attn(q, kc, table, n, most, 0.05)
+    else:
+        kw = dict(k_scale=0.5, v_scale=0.25) if kind == "tensor" else {}
+        call = lambda: pkv.paged_decode_attn(q, kc, vc, table, n, most, **kw)
+    want = call()
+    G = Hq // Hkv
+    for at in (0, lens[0] // 2, lens[0] - 1):
+        page = int(table[0, at // 16])
+        was = kc[page, at % 16, Hkv - 1, 3].clone()
+        kc[page, at % 16, Hkv - 1, 3] = 0x7F if kind == "tensor" else float("nan")
+        o, z = call()
+        kc[page, at % 16, Hkv - 1, 3] = was
+        assert torch.isnan(o[0, Hq - G:]).all() and torch.isnan(z[0, Hq - G:]).all()
+        assert torch.equal(o[1:], want[0][1:]) and torch.equal(z[1:], want[1][1:]) and torch.equal(o[0, :Hq - G], want[0][0, :Hq - G])
+    assert pkv.device_errors() == 0

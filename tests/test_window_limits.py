@@ -149,3 +149,48 @@ def test_requests_of_an_item_of_rows(Hq, Hkv):
     for n in (need, need // 3):
         check(extend_with(st, torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda"), n), ref, st["T"])
     check(extend_with(st, None, 0), ref, st["T"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", ["key", "value"])
+@pytest.mark.parametrize("kind,D,Hq,Hkv", [("bf16", 64, 8, 2), ("bf16", 128, 32, 2), ("tensor", 128, 16, 2), ("block", 128, 16, 2)])
+@pytest.mark.parametrize("lens", [[40, 200, 33], [9000, 40, 9000]])
+def test_decode_over_what_is_no_number(lens, kind, D, Hq, Hkv, which):
+    """A key that the token sees and that is no number makes its KV head's rows of that request none, out and lse; a value makes its
+    column of out one, and nothing else. Sequences of one piece, and cut ones."""
+    st = make([(n - 1, 1) for n in lens], Hq, Hkv, D, kind, 5000, 3, 99, cached_all=True)
+    ref = reference(st, decode=True)
+    at = lens[0] - 30  # a key in the window
+    page = int(st["table"][0, at // 16])
+    (st["kc"] if which == "key" else st["vc"])[page, at % 16, 1, 5] = 0x7F if kind in ("tensor", "block") else math.nan
+    out, lse = call(st, "decode")
+    G = Hq // Hkv
+    if which == "key":
+        assert torch.isnan(out[0, G:]).all() and torch.isnan(lse[0, G:]).all()
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[0, G:] = True
+        lse[0, G:] = ref[1][0, G:].float()
+    else:
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[0, G:, 5] = True
+        assert torch.isnan(out[hit]).all()
+    assert not torch.isnan(out[~hit]).any()
+    out = torch.where(hit, torch.cat([ref[0], torch.full_like(out[len(lens):], 7.0).double()]).to(out.dtype), out)
+    check((out, lse), ref, st["T"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,D", [("none", 64), ("bf16", 128), ("tensor", 128)])
+@pytest.mark.parametrize("n", [20, 200])
+def test_new_keys_that_are_no_number(n, kind, D):
+    """Extend and prefill: the rows that see such a key are none (others of the request may be), other KV heads and requests are as
+    without it."""
+    c = 0 if kind == "none" else 70
+    st = make([(c, n), (0, 33)], 16, 2, D, kind, 100, 3, 100)
+    ref = reference(st)
+    st["k_new"][n // 2, 1, 7] = math.nan
+    out, lse = call(st, "prefill" if kind == "none" else "extend")
+    see = [i for i in range(n) if i >= n // 2 and i - n // 2 < 100]
+    assert torch.isnan(out[see, 8:]).all() and torch.isnan(lse[see, 8:]).all()
+    out[:n, 8:], lse[:n, 8:] = ref[0][:n, 8:].to(out.dtype), ref[1][:n, 8:].float()
+    check((out, lse), ref, st["T"])
