@@ -41,13 +41,14 @@
 //
 // What bounds it, on a GB300 with 64 query and 8 KV heads of 128 (times of back-to-back calls; the measured peaks are 6776 GB/s and
 // 1882 TFLOP/s bf16):
-//   three prompts of 4000 to 10,007 tokens under 4096   1305 us, 1530 TFLOP/s (0.81 of measured; 1203 us alone and cool): the
-//                                                       two slots' chains, and the power limit
+//   three prompts of 4000 to 10,007 tokens under 4096   1305 to 1380 us from box to box, 1450 to 1530 TFLOP/s (0.77 to 0.81 of
+//                                                       measured; 1203 us alone and cool): the two slots' chains, and the
+//                                                       power limit
 //   8 x 301-512 tokens over 4000-32,000 under 128       49 us for a floor of 18.5: two edge tiles an item, so each item is
 //                                                       its chain of Q, S, masks, softmax, P V, epilogue, some 12,000 clocks
 //   32 x 4 tokens over 1000-4000 under 1024             37 us, 3.7 TB/s (floor 20.6): 256 items in two rounds of 152
 //   2048 tokens over 100,000 under 4096, E4M3 cache     232 us (floor 151; a bf16 cache 214): of it 8 to 16 for the rows
-//                                                       converted ahead; with the codes converted by every item 315 to 329,
+//                                                       converted ahead; with the codes converted by every item 314 to 329,
 //                                                       the conversions waiting for shared memory that the products read
 #include <math_constants.h>
 

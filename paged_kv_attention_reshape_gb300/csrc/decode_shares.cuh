@@ -516,6 +516,8 @@ struct CutMerger {
   // in (merging them in the registers, or, where it is the third or fourth child, from memory at the end); at the root write
   // out/lse, else store the registers as the node's partial and owe an arrival on the parent. `check` = look at the
   // counters first (worth a round trip only when no block of the share follows to hide it).
+  // (256 sequences of 2000-3000 under a window of 1024, 16 heads a KV head: 101 us; with every merge from memory 104.7; with the
+  // third and fourth child in registers too, 60 registers more.)
   __device__ void piece_done(const DecodeParams& p, const Cut& s, int piece, int kh, float (&o)[D / 8][4],
                              float (&lse)[2], bool check, int lane) {
     int L = 1, ai = piece;  // the registers hold node (L - 1, ai)
