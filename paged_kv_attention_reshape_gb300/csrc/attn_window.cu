@@ -41,7 +41,7 @@
 //
 // What bounds it, on a GB300 with 64 query and 8 KV heads of 128 (times of back-to-back calls; the measured peaks are 6776 GB/s and
 // 1882 TFLOP/s bf16):
-//   three prompts of 4000 to 10,007 tokens under 4096   1305 to 1380 us from box to box, 1450 to 1530 TFLOP/s (0.77 to 0.81 of
+//   three prompts of 4000 to 10,007 tokens under 4096   1305 to 1380 us from GPU to GPU, 1450 to 1530 TFLOP/s (0.77 to 0.81 of
 //                                                       measured; 1203 us alone and cool): the two slots' chains, and the
 //                                                       power limit
 //   8 x 301-512 tokens over 4000-32,000 under 128       49 us for a floor of 18.5: two edge tiles an item, so each item is
