@@ -194,3 +194,19 @@ def test_new_keys_that_are_no_number(n, kind, D):
     assert torch.isnan(out[see, 8:]).all() and torch.isnan(lse[see, 8:]).all()
     out[:n, 8:], lse[:n, 8:] = ref[0][:n, 8:].to(out.dtype), ref[1][:n, 8:].float()
     check((out, lse), ref, st["T"])
+
+
+@pytest.mark.gpu
+def test_converted_ahead_from_one_allocation_in_a_set_of_its_own():
+    """Rows converted once from a pool whose K and V blocks alternate, for requests named by the device, one of them twice."""
+    import paged_kv_attention_reshape_gb300 as pkv
+    reqs = [(2001, 700), (17, 600), (1, 20), (300, 16), (900, 1)]
+    st = make(reqs, 48, 3, 128, "tensor", 1900, 9, 101)
+    T = st["q"].shape[0]
+    assert pkv.window_extend_workspace_size(T, 6, 700, int(st["lens"].max()), 48, 3, 128, 1900, 9) > 0
+    g = torch.stack([st["kc"], st["vc"]], 1).cuda()
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ref = reference(st)
+    check(call(dict(st, kc=g[:, 0], vc=g[:, 1]), "extend", reqs=pkv.Reqs(6, 5, order=i32(3, 1, 0, 4, 1, 2))), ref, st["T"])
+    check(call(dict(st, kc=g[:, 0], vc=g[:, 1]), "extend", reqs=pkv.Reqs(6, 5, order=i32(4, 0, 3, 2, 1, 9), bounds=i32(0, 0, 5, 5), cls=1)),
+          ref, st["T"])
